@@ -45,6 +45,14 @@ class MoeLayer(ctypes.Structure):
                 ("sh_down_q", ctypes.c_void_p), ("sh_down_s", ctypes.c_void_p)]
 
 
+class Routing(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("n_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_rank", ctypes.c_int32),
+                ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+_i32, _i64, _ptr_t, _size = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
+
 EXPORTS = {
     "clover_moe_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(Dims), ctypes.c_int32]),
     "clover_moe_block_step": (ctypes.c_int, [ctypes.POINTER(Dims), ctypes.POINTER(MoeLayer), ctypes.c_void_p,
@@ -86,6 +94,18 @@ EXPORTS = {
     "clover_profile_expert_events": (ctypes.c_int32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32]),
     "clover_last_error": (ctypes.c_int32, [ctypes.c_char_p, ctypes.c_size_t]),
     "clover_version": (ctypes.c_int32, []),
+    "clover_route_workspace_bytes": (_size, [ctypes.POINTER(Routing), _i32]),
+    "clover_route": (ctypes.c_int, [ctypes.POINTER(Routing), _ptr_t, _i32, _i64, _ptr_t, _i32, _ptr_t, _ptr_t, _ptr_t,
+                                    _ptr_t, _ptr_t, _ptr_t, _size, _ptr_t]),
+    "clover_fp4_scale_bytes": (_size, [_i32, _i32, _i32, _i32]),
+    "clover_fp4_grouped_scale_bytes": (_size, [_i32, _i32, _i32, _i32]),
+    "clover_quantize_fp4": (ctypes.c_int, [_i32, _ptr_t, _i32, _i64, _i32, _i32, _i32, _i32, _ptr_t, _ptr_t, _ptr_t]),
+    "clover_quantize_fp4_rows": (ctypes.c_int, [_i32, _ptr_t, _i32, _i64, _i32, _i32, _i32, _ptr_t, _i32, _i32,
+                                                _ptr_t, _i32, _ptr_t, _ptr_t, _ptr_t]),
+    "clover_dequantize_fp4": (ctypes.c_int, [_i32, _ptr_t, _ptr_t, _i32, _i32, _i32, _i32, _ptr_t, _i32, _ptr_t,
+                                             _ptr_t]),
+    "clover_moe_combine": (ctypes.c_int, [_ptr_t, _i32, _ptr_t, _ptr_t, _ptr_t, _ptr_t, _ptr_t, _i32, _i32, _i32,
+                                          _ptr_t]),
 }
 
 _lib = None
@@ -320,3 +340,213 @@ def denoise_block(m: Model, ctx, tokens, masked, logit_scale=None, threshold: fl
 
 def workspace_status(ws: torch.Tensor, stream=None):
     _check(lib().clover_workspace_status(_ptr(ws), ws.numel(), _stream(stream)))
+
+
+# ------------------------------------------- routed experts as separate calls
+#
+# Tensors are checked here (type, shape, layout, one device: the current one);
+# values and limits are checked by the library. A refused argument raises
+# CloverError with the library's codes.
+
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+FP4_NV = 0
+FP4_MX = 1
+_SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _refuse(msg: str):
+    raise CloverError(ERR_INVALID_ARG, msg)
+
+
+def _tensor(name: str, t, dtype, shape, device) -> int:
+    """The pointer of a contiguous tensor of this type and shape on `device`."""
+    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+        _refuse(f"{name}: need contiguous {dtype} {shape} on {device}, "
+                f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _rows_of(name: str, t):
+    """(pointer, type code, row stride in elements) of a 2-D fp32 or bf16 tensor with contiguous rows on the
+    current device."""
+    if t.dim() != 2 or t.dtype not in _TYPES or (t.shape[1] > 1 and t.stride(1) != 1):
+        _refuse(f"{name}: need a 2-D fp32 or bf16 tensor with contiguous rows, got {t.dtype} {tuple(t.shape)}, "
+                f"strides {t.stride()}")
+    _on_current(name, t)
+    return t.data_ptr(), _TYPES[t.dtype], (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1]))
+
+
+def _on_current(name: str, t):
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        _refuse(f"{name} is on {t.device}, not on the current CUDA device")
+
+
+def _raw_stream(stream, device) -> int:
+    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+
+def make_routing(n_experts: int, top_k: int, score: str = "softmax", n_groups: int = 1, top_groups: int | None = None,
+                 group_rank: int = 1, renormalise: bool = True, scale: float = 1.0) -> Routing:
+    """The selection rule of `route`. top_groups defaults to every group."""
+    if score not in _SCORES:
+        _refuse(f"score {score!r} is neither 'softmax' nor 'sigmoid'")
+    return Routing(n_experts, top_k, _SCORES[score], n_groups, n_groups if top_groups is None else top_groups,
+                   group_rank, int(bool(renormalise)), scale)
+
+
+def route_workspace_bytes(r: Routing, max_tokens: int) -> int:
+    return lib().clover_route_workspace_bytes(r, max_tokens)
+
+
+def route(r: Routing, logits, bias=None, grouping: bool = True, ws=None, out=None, stream=None) -> dict:
+    """Expert selection from router logits [M][E] (fp32 or bf16, rows may be strided) -> idx int32 [M][K], w fp32
+    [M][K] and, with grouping, offsets int32 [E + 1], rows int32 [M * K], pos int32 [M][K]. `out` (a dict this
+    function returned before, for the same shape) is reused."""
+    M, K, E = logits.shape[0], r.top_k, r.n_experts
+    dev = logits.device
+    p_logits, kind, ld = _rows_of("logits", logits)
+    if logits.shape[1] != E:
+        _refuse(f"logits have {logits.shape[1]} columns for {E} experts")
+    p_bias = None if bias is None else _tensor("bias", bias, torch.float32, (E,), dev)
+    if ws is None:
+        ws = workspace(route_workspace_bytes(r, M), dev)
+    i32 = torch.int32
+    if out is None:
+        out = {"idx": torch.empty((M, K), dtype=i32, device=dev),
+               "w": torch.empty((M, K), dtype=torch.float32, device=dev)}
+        if grouping:
+            out["offsets"] = torch.empty(E + 1, dtype=i32, device=dev)
+            out["rows"] = torch.empty(M * K, dtype=i32, device=dev)
+            out["pos"] = torch.empty((M, K), dtype=i32, device=dev)
+    p_group = (None, None, None)
+    if grouping:
+        p_group = (_tensor("offsets", out["offsets"], i32, (E + 1,), dev), _tensor("rows", out["rows"], i32, (M * K,), dev),
+                   _tensor("pos", out["pos"], i32, (M, K), dev))
+    _check(lib().clover_route(r, p_logits, kind, ld, p_bias, M, _tensor("idx", out["idx"], i32, (M, K), dev),
+                              _tensor("w", out["w"], torch.float32, (M, K), dev), *p_group, ws.data_ptr(), ws.numel(),
+                              _raw_stream(stream, dev)))
+    return out
+
+
+class Fp4:
+    """Matrices in a microscaled 4-bit format: codes uint8 [..][rows][cols / 2], scale tiles uint8 (1-D), and the
+    power of two the values are scaled by. With offsets (int32 [groups + 1]) the rows of one matrix form groups."""
+
+    __slots__ = ("fmt", "codes", "scales", "scale_exp", "offsets")
+
+    def __init__(self, fmt: int, codes, scales, scale_exp: int = 0, offsets=None):
+        self.fmt, self.codes, self.scales, self.scale_exp, self.offsets = fmt, codes, scales, scale_exp, offsets
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[-2]
+
+    @property
+    def cols(self) -> int:
+        return 2 * self.codes.shape[-1]
+
+    @property
+    def mats(self) -> int:
+        return self.codes.shape[0] if self.codes.dim() == 3 else 1
+
+    def _ptrs(self, name: str):
+        """Checks the parts against one another; the pointers of codes, scales and offsets."""
+        c = self.codes
+        _on_current(name, c)
+        if c.dtype != torch.uint8 or c.dim() not in (2, 3) or not c.is_contiguous():
+            _refuse(f"{name}.codes: need contiguous uint8 [rows][cols / 2] or [mats][rows][cols / 2], got {c.dtype} "
+                    f"{tuple(c.shape)}")
+        need = fp4_scale_bytes(self.fmt, self.mats, self.rows, self.cols,
+                               None if self.offsets is None else self.offsets.shape[0] - 1)
+        p_off = None
+        if self.offsets is not None:
+            if c.dim() != 2:
+                _refuse(f"{name}: rows in groups form one matrix")
+            p_off = _tensor(f"{name}.offsets", self.offsets, torch.int32, (self.offsets.shape[0],), c.device)
+        s = self.scales
+        if s.dtype != torch.uint8 or s.device != c.device or not s.is_contiguous() or s.numel() < need:
+            _refuse(f"{name}.scales: need {need} contiguous uint8 on {c.device}, got {s.dtype} {tuple(s.shape)} on "
+                    f"{s.device}")
+        return c.data_ptr(), s.data_ptr(), p_off
+
+
+def fp4_scale_bytes(fmt: int, n_mats: int, rows: int, cols: int, n_groups: int | None = None) -> int:
+    """Bytes of the scale tiles of n_mats matrices, or of `rows` rows in n_groups groups."""
+    if n_groups is None:
+        n = lib().clover_fp4_scale_bytes(fmt, n_mats, rows, cols)
+        ok = n > 0 or n_mats == 0 or rows == 0
+    else:
+        n = lib().clover_fp4_grouped_scale_bytes(fmt, rows, n_groups, cols)
+        ok = n > 0
+    if not ok:
+        raise CloverError(ERR_UNSUPPORTED_SHAPE, last_error())
+    return n
+
+
+def quantize_fp4(x, fmt: int = FP4_NV, scale_exp: int = 0, offsets=None, src_rows=None, src_div: int = 1, out=None,
+                 stream=None) -> Fp4:
+    """fp32 or bf16 matrices [rows][cols] or [mats][rows][cols] -> Fp4. With offsets (int32 [groups + 1]) the rows form
+    groups: row i comes from x row src_rows[i] // src_div (src_rows int32, default i), as `route` lists them. `out` (an
+    Fp4 this function returned before, for the same shapes) is reused."""
+    grouped = offsets is not None
+    if x.dim() == 3 and (grouped or not x.is_contiguous()):
+        _refuse("x: matrices must be contiguous, and grouped rows one matrix")
+    flat = x.view(-1, x.shape[-1]) if x.dim() == 3 else x
+    p_x, kind, ldx = _rows_of("x", flat)
+    dev, cols = x.device, x.shape[-1]
+    if not grouped and src_rows is not None:
+        _refuse("src_rows without offsets")
+    n_groups = offsets.shape[0] - 1 if grouped else None
+    n_mats, rows = (x.shape[0], x.shape[1]) if x.dim() == 3 else (1, x.shape[0] if src_rows is None else src_rows.shape[0])
+    if out is None:
+        scales = torch.empty(fp4_scale_bytes(fmt, n_mats, rows, cols, n_groups), dtype=torch.uint8, device=dev)
+        codes = torch.empty(x.shape[:-2] + (rows, cols // 2), dtype=torch.uint8, device=dev)
+        out = Fp4(fmt, codes, scales, scale_exp, offsets)
+    elif out.fmt != fmt or tuple(out.codes.shape) != x.shape[:-2] + (rows, cols // 2):
+        _refuse(f"out holds {tuple(out.codes.shape)} of format {out.fmt}")
+    else:
+        out.scale_exp, out.offsets = scale_exp, offsets
+    p_codes, p_scales, p_off = out._ptrs("out")
+    if out.codes.device != dev:
+        _refuse(f"out is on {out.codes.device}, x on {dev}")
+    L, st = lib(), _raw_stream(stream, dev)
+    if grouped:
+        p_src = None if src_rows is None else _tensor("src_rows", src_rows, torch.int32, (rows,), dev)
+        _check(L.clover_quantize_fp4_rows(fmt, p_x, kind, ldx, x.shape[0], cols, scale_exp, p_src, src_div, rows, p_off,
+                                          n_groups, p_codes, p_scales, st))
+    else:
+        _check(L.clover_quantize_fp4(fmt, p_x, kind, ldx, n_mats, rows, cols, scale_exp, p_codes, p_scales, st))
+    return out
+
+
+def dequantize_fp4(q: Fp4, out=None, stream=None):
+    """The bf16 matrices the codes stand for (rows behind the last group left as they were)."""
+    p_codes, p_scales, p_off = q._ptrs("q")
+    dev, shape = q.codes.device, tuple(q.codes.shape[:-1]) + (q.cols,)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    p_out = _tensor("out", out, torch.bfloat16, shape, dev)
+    _check(lib().clover_dequantize_fp4(q.fmt, p_codes, p_scales, q.mats, q.rows, q.cols, q.scale_exp, p_off,
+                                       0 if p_off is None else q.offsets.shape[0] - 1, p_out, _raw_stream(stream, dev)))
+    return out
+
+
+def moe_combine(y, pos, w, x=None, shared=None, out=None, stream=None):
+    """x + sum_k w[:, k] * y[pos[:, k]] + shared, fp32 [M][H]: y bf16 [rows][H], pos int32 and w fp32 [M][K] as `route`
+    gives them, x fp32 and shared bf16 [M][H] or None. out may be x itself."""
+    if y.dim() != 2 or pos.dim() != 2:
+        _refuse(f"y and pos must be matrices, got {tuple(y.shape)} and {tuple(pos.shape)}")
+    _on_current("y", y)
+    (M, K), (n, H), dev = pos.shape, y.shape, y.device
+    if out is None:
+        out = torch.empty((M, H), dtype=torch.float32, device=dev)
+    p_shared = None if shared is None else _tensor("shared", shared, torch.bfloat16, (M, H), dev)
+    p_x = None if x is None else _tensor("x", x, torch.float32, (M, H), dev)
+    _check(lib().clover_moe_combine(_tensor("y", y, torch.bfloat16, (n, H), dev), n,
+                                    _tensor("pos", pos, torch.int32, (M, K), dev),
+                                    _tensor("w", w, torch.float32, (M, K), dev), p_shared, p_x,
+                                    _tensor("out", out, torch.float32, (M, H), dev), M, K, H,
+                                    _raw_stream(stream, dev)))
+    return out

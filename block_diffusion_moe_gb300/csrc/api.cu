@@ -884,6 +884,8 @@ namespace clover {
 // clover_last_error().
 int set_last_error(int code, const char* msg) { return fail(code, "%s", msg); }
 
+int check_workspace(void* workspace, size_t have, size_t need) { return check_ws(workspace, have, need); }
+
 // clover_lmhead_unmask with one option: clear_ctrl zeroes the workspace's
 // control words on the stream (after every argument check, so a rejected
 // call enqueues nothing) for scratch memory whose previous contents are not

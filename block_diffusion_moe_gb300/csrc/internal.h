@@ -13,6 +13,9 @@ namespace clover {
 // returns code.
 int set_last_error(int code, const char* msg);
 
+// Checks a caller's workspace: not NULL, 256-byte aligned, at least `need` bytes.
+int check_workspace(void* workspace, size_t have, size_t need);
+
 // The host-side argument checks of clover_lmhead_unmask that do not involve
 // the workspace (no CUDA call).
 int lmhead_unmask_check(const clover_dims* dims, const uint16_t* head_w, const float* x, float threshold,

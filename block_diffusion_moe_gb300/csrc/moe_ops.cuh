@@ -1,0 +1,82 @@
+// Argument blocks and launch wrappers of the routed-expert operations
+// (clover_route, clover_quantize_fp4, clover_fp4_product,
+// clover_moe_combine), shared by their host side and their kernels.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace clover {
+
+constexpr int kRouteOpMaxExperts = 512;
+constexpr int kRouteOpMaxTopK = 32;
+// Tokens one CTA of the selection kernel takes, at most: one bit each in an
+// expert's 64-bit token mask.
+constexpr int kRouteOpCtaTokens = 64;
+
+struct RouteOpArgs {
+  const void* logits;  // fp32 or bf16 [M], row t at element t * ld
+  const float* bias;   // [E] or null
+  int64_t ld;
+  int bf16_logits;
+  int M, E, K;
+  int softmax, n_groups, top_groups, group_rank, renormalise;
+  float scale;
+  int32_t* idx;      // [M][K]
+  float* w;          // [M][K]
+  int32_t* offsets;  // [E + 1], null: no grouping
+  int32_t* rows;     // [M * K]
+  int32_t* pos;      // [M][K]
+  int32_t* hist;     // [E][n_ctas] (workspace)
+  int32_t* totals;   // [E] (workspace)
+  int cta_tokens;    // tokens per CTA, a multiple of 8, at most kRouteOpCtaTokens
+  int n_ctas;
+};
+
+// CTAs and tokens per CTA of the selection kernel for M >= 1 tokens.
+inline void route_op_shape(int M, int* cta_tokens, int* n_ctas) {
+  // 8 tokens (one per warp) until that fills a few hundred CTAs, then more
+  int t = 8;
+  while (t < kRouteOpCtaTokens && (M + t - 1) / t > 304) t *= 2;
+  *cta_tokens = t;
+  *n_ctas = (M + t - 1) / t;
+}
+
+cudaError_t launch_route_op(const RouteOpArgs& a, cudaStream_t s);
+
+struct CombineOpArgs {
+  const __nv_bfloat16* y;       // [n_rows][H]
+  const int32_t* pos;           // [M][K]
+  const float* w;               // [M][K]
+  const __nv_bfloat16* shared;  // [M][H] or null
+  const float* x;               // [M][H] or null
+  float* out;                   // [M][H]
+  int n_rows, M, K, H;
+};
+
+cudaError_t launch_combine_op(const CombineOpArgs& a, cudaStream_t s);
+
+struct Fp4QuantArgs {
+  const void* x;            // fp32 or bf16 rows of cols, row i at element i * ldx
+  int64_t ldx;
+  int bf16_x;
+  int64_t n_rows;           // rows of codes (n_mats * mat_rows, or the grouped rows)
+  int mat_rows;             // rows per matrix (offsets == null)
+  int cols;
+  float mul;                // 2^-scale_exp (quantise), 2^scale_exp (dequantise)
+  const int32_t* src_rows;  // grouped: source row of row i is src_rows[i] / src_div (null: i)
+  int src_div;
+  int n_src;
+  const int32_t* offsets;   // [n_groups + 1] or null
+  int n_groups;
+  uint8_t* codes;           // [n_rows][cols / 2]
+  uint8_t* scales;          // tiles
+  __nv_bfloat16* out;       // dequantise: [n_rows][cols]
+};
+
+cudaError_t launch_quantize_fp4(const Fp4QuantArgs& a, bool mx, cudaStream_t s);
+cudaError_t launch_dequantize_fp4(const Fp4QuantArgs& a, bool mx, cudaStream_t s);
+
+}  // namespace clover

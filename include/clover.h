@@ -291,6 +291,134 @@ int clover_lmhead_unmask_static(const clover_dims* dims, const uint16_t* head_w,
  * (The pages have no counterpart.) */
 int clover_lmhead_unmask_static_status(clover_stream_t stream);
 
+/* ---- Routed experts as separate operations ------------------------------
+ * The steps of a routed-expert sublayer for callers whose layer differs from
+ * clover_moe_block_step's (another score function, expert groups, longer
+ * inputs, hardware 4-bit experts): route -> quantize (gathering the rows into
+ * expert order) -> product with SwiGLU -> quantize -> product -> combine.
+ * The conventions at the top of this file hold, with these differences: the
+ * limits on shapes are the ones stated per call, a call with no rows
+ * (M == 0 or n_rows == 0) is valid and needs no data pointers, and none of
+ * the calls changes its inputs. */
+
+/* Score functions of clover_route. */
+#define CLOVER_SCORE_SOFTMAX 0
+#define CLOVER_SCORE_SIGMOID 1
+
+/* Types of an input that may come in more than one. */
+#define CLOVER_TYPE_F32 0
+#define CLOVER_TYPE_BF16 1
+
+/* Selection rule of clover_route. 1 <= n_experts <= 512; 1 <= top_k <=
+ * min(32, n_experts); 1 <= n_groups <= 32, dividing n_experts; 1 <= top_groups
+ * <= n_groups; group_rank 1 or 2; scale finite. */
+typedef struct {
+    int32_t n_experts;   /* E */
+    int32_t top_k;       /* K */
+    int32_t score;       /* CLOVER_SCORE_*                                     */
+    int32_t n_groups;    /* experts form n_groups runs of E / n_groups ids     */
+    int32_t top_groups;  /* groups that stay selectable (n_groups = all)       */
+    int32_t group_rank;  /* a group ranks by the sum of its 1 or 2 best experts */
+    int32_t renormalise; /* nonzero: a token's weights are divided by their sum */
+    float scale;         /* factor of every weight                             */
+} clover_routing;
+
+/* Bytes of workspace clover_route needs for up to max_tokens tokens. Returns
+ * 0 for an unsupported rule or max_tokens < 0. Host-only. */
+size_t clover_route_workspace_bytes(const clover_routing* routing, int32_t max_tokens);
+
+/* Expert selection from given router logits, M tokens x E experts.
+ *   s = softmax(the token's logits) or 1 / (1 + e^-logit)
+ *   key = logit without a bias (s grows with it), s + bias with one
+ * A NaN logit counts as -inf, one above the largest finite fp32 as that
+ * value. An expert is live for a token unless its logit is -inf or its bias
+ * is NaN or -inf. With n_groups >
+ * 1 the top_groups groups of the largest rank stay (rank 1: the group's
+ * largest key; rank 2: the sum of its up to two largest s + bias; a group
+ * without a live expert is last; ties to the lower group). The top_k live
+ * experts of the largest keys in the groups that stay are selected, in
+ * descending order (ties to the lower id); their weights are s, divided by
+ * their sum if renormalise is set, times scale. A token with fewer than
+ * top_k such experts (a padding row has none) gets index -1 and weight 0 in
+ * the places left over. Comparisons are exact: keys closer than fp32 can
+ * tell apart are compared in fp64.
+ * logits: logits_type [M] rows of E, row t at element t * ld (ld >= E),
+ * aligned to its element size. bias: fp32 [E] or NULL; it takes part in the
+ * selection only. topk_idx int32 [M][K], topk_w fp32 [M][K]: out.
+ * Grouping (offsets, rows and pos all set, or all NULL): offsets int32
+ * [E + 1], rows int32 [M * K], pos int32 [M][K]. The selected slots t * K + k
+ * are listed in rows by expert, then token; expert e's are rows[offsets[e]]
+ * .. rows[offsets[e + 1] - 1]. pos[t][k] is the place of slot (t, k) in rows,
+ * or -1. Places of rows from offsets[E] on are left as they were.
+ * M * top_k <= 2^30. Every result is independent of the launch shape. */
+int clover_route(const clover_routing* routing, const void* logits, int32_t logits_type, int64_t ld,
+                 const float* bias, int32_t M, int32_t* topk_idx, float* topk_w, int32_t* offsets,
+                 int32_t* rows, int32_t* pos, void* workspace, size_t workspace_bytes,
+                 clover_stream_t stream);
+
+/* Microscaled 4-bit formats (the tensor cores' own): e2m1 values 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6 and a sign bit, with one scale per block of consecutive
+ * columns: */
+#define CLOVER_FP4_NV 0 /* blocks of 16, scale e4m3                    */
+#define CLOVER_FP4_MX 1 /* blocks of 32, scale e8m0 (a power of two)   */
+
+/* Bytes of the scales of n_mats matrices [rows][cols], each in tiles of 128
+ * rows x 4 blocks (512 bytes): tile (mat, rows / 128, blocks / 4) in row-major
+ * order, the scale of row r, block b of a tile at byte (r % 32) * 16 +
+ * (r / 32) * 4 + b. Rows and blocks are padded to whole tiles. Returns 0 for
+ * arguments that clover_quantize_fp4 refuses or a size past 2^62. Host-only. */
+size_t clover_fp4_scale_bytes(int32_t format, int32_t n_mats, int32_t rows, int32_t cols);
+
+/* The same for n_rows rows in n_groups consecutive groups: group g (rows
+ * offsets[g] .. offsets[g + 1] - 1) begins at row tile offsets[g] / 128 + g,
+ * so n_rows / 128 + n_groups row tiles are enough for any offsets. */
+size_t clover_fp4_grouped_scale_bytes(int32_t format, int32_t n_rows, int32_t n_groups, int32_t cols);
+
+/* Quantises n_mats matrices x [rows][cols] (x_type fp32 or bf16; row i of the
+ * n_mats * rows rows at element i * ldx, ldx >= cols; rows 16-byte aligned;
+ * cols % 64 == 0, 64 <= cols <= 2^20) to codes [n_mats][rows][cols / 2] (the
+ * even column in the low nibble) and scales. With y = x 2^-scale_exp (fp32,
+ * |scale_exp| <= 64) and amax the largest |y| of a block, the block's scale is
+ *   NV: s = e4m3(amax / 6), round to nearest even, at most 448
+ *   MX: s = 2^(floor(log2 amax) - 2), exponent at least -127 (amax = 0: -127)
+ * and each code is the e2m1 value nearest to y / s (ties to the even code, at
+ * most 6; 0 where s = 0); it stands for code * s * 2^scale_exp. A block that
+ * holds a NaN or an infinity gets the scale NaN and codes 0. Scale bytes of
+ * padding are not written. codes and scales 16-byte aligned. */
+int clover_quantize_fp4(int32_t format, const void* x, int32_t x_type, int64_t ldx, int32_t n_mats,
+                        int32_t rows, int32_t cols, int32_t scale_exp, uint8_t* codes, uint8_t* scales,
+                        clover_stream_t stream);
+
+/* The same for n_rows rows in groups (offsets int32 [n_groups + 1] on the
+ * device, ascending from 0; 1 <= n_groups <= 512), such as the rows of
+ * clover_route: row i is quantised from x row src_rows[i] / src_div (NULL: i),
+ * 0 <= that < n_src. Rows from offsets[n_groups] on are left as they were.
+ * Offsets outside [0, n_rows] count as the nearer end; a row whose source
+ * lies outside [0, n_src) gets codes and scales of zeros. */
+int clover_quantize_fp4_rows(int32_t format, const void* x, int32_t x_type, int64_t ldx, int32_t n_src,
+                             int32_t cols, int32_t scale_exp, const int32_t* src_rows, int32_t src_div,
+                             int32_t n_rows, const int32_t* offsets, int32_t n_groups, uint8_t* codes,
+                             uint8_t* scales, clover_stream_t stream);
+
+/* What the codes stand for, code * s * 2^scale_exp rounded to bf16 (exact
+ * unless it leaves bf16's range): out bf16 [n_mats][rows][cols]; with offsets
+ * (NULL: matrices) rows in n_groups groups, n_mats = 1, rows from
+ * offsets[n_groups] on left as they were. */
+int clover_dequantize_fp4(int32_t format, const uint8_t* codes, const uint8_t* scales, int32_t n_mats,
+                          int32_t rows, int32_t cols, int32_t scale_exp, const int32_t* offsets,
+                          int32_t n_groups, uint16_t* out, clover_stream_t stream);
+
+/* Weighted sum of expert rows, and what a sublayer adds to it:
+ *   x_out[t] = x[t] + sum_k w[t][k] * y[pos[t][k]] + shared[t]
+ * y: bf16 [n_rows][H]; pos int32 and w fp32 [M][K] as clover_route gives
+ * them: a slot whose place lies outside [0, n_rows) adds nothing, whatever its
+ * weight. shared: bf16 [M][H] or NULL. x: fp32 [M][H] or NULL (zeros); x_out
+ * fp32 [M][H] may equal x, other overlap is not allowed. H % 8 == 0,
+ * 1 <= K <= 32. The sum is in fp32: x, then the slots in order, then shared. */
+int clover_moe_combine(const uint16_t* y, int32_t n_rows, const int32_t* pos, const float* w,
+                       const uint16_t* shared, const float* x, float* x_out, int32_t M, int32_t K, int32_t H,
+                       clover_stream_t stream);
+
 /* Library version as major*10000 + minor*100 + patch. */
 int32_t clover_version(void);
 

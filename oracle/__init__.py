@@ -1,2 +1,3 @@
-"""CPU oracle (test infrastructure only; see clover_oracle.py)."""
+"""CPU oracle (test infrastructure only; see clover_oracle.py and moe_ops.py)."""
 from .clover_oracle import *  # noqa: F401,F403
+from . import moe_ops  # noqa: F401

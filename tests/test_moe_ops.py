@@ -1,0 +1,223 @@
+"""The routed-expert operations on the host: what the library refuses before
+it enqueues anything (no call here reaches a GPU), its size queries, and pins
+of the oracle the GPU tests compare with."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from block_diffusion_moe_gb300 import build as B
+from block_diffusion_moe_gb300 import clover as C
+from oracle import moe_ops as R
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return C.lib()
+
+
+def _routing(**kw):
+    base = dict(n_experts=256, top_k=8, score="softmax", n_groups=8, top_groups=4, group_rank=2)
+    base.update(kw)
+    return C.make_routing(**base)
+
+
+ROUTE = dict(logits=0x10000, type=0, ld=256, bias=0x20000, M=32, idx=0x30000, w=0x40000, offsets=0x50000, rows=0x60000,
+             pos=0x70000, ws=0x100000, nbytes=1 << 24, stream=None)
+
+
+def _route(lib, r, **kw):
+    a = dict(ROUTE, **kw)
+    return lib.clover_route(r, *a.values())
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n_experts=0), C.ERR_UNSUPPORTED_SHAPE), (dict(n_experts=513, n_groups=1, top_groups=1), C.ERR_UNSUPPORTED_SHAPE),
+    (dict(top_k=0), C.ERR_UNSUPPORTED_SHAPE), (dict(top_k=33), C.ERR_UNSUPPORTED_SHAPE),
+    (dict(n_experts=4, n_groups=1, top_groups=1, top_k=5), C.ERR_UNSUPPORTED_SHAPE),
+    (dict(n_groups=7), C.ERR_UNSUPPORTED_SHAPE), (dict(n_groups=64, top_groups=4), C.ERR_UNSUPPORTED_SHAPE),
+    (dict(n_groups=0), C.ERR_UNSUPPORTED_SHAPE), (dict(top_groups=9), C.ERR_INVALID_ARG),
+    (dict(top_groups=0), C.ERR_INVALID_ARG), (dict(group_rank=3), C.ERR_INVALID_ARG),
+    (dict(scale=float("nan")), C.ERR_INVALID_ARG), (dict(scale=float("inf")), C.ERR_INVALID_ARG),
+])
+def test_route_rules_refused(lib, kw, code):
+    r = _routing(**kw)
+    assert _route(lib, r) == code
+    assert C.last_error()
+    assert lib.clover_route_workspace_bytes(r, 32) == 0
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(logits=None), C.ERR_INVALID_ARG), (dict(idx=None), C.ERR_INVALID_ARG), (dict(w=None), C.ERR_INVALID_ARG),
+    (dict(type=2), C.ERR_INVALID_ARG), (dict(ld=255), C.ERR_INVALID_ARG), (dict(logits=0x10002), C.ERR_INVALID_ARG),
+    (dict(type=1, logits=0x10001), C.ERR_INVALID_ARG), (dict(rows=None), C.ERR_INVALID_ARG),
+    (dict(offsets=None), C.ERR_INVALID_ARG), (dict(pos=0x70002), C.ERR_INVALID_ARG), (dict(M=-1), C.ERR_UNSUPPORTED_SHAPE),
+    (dict(M=1 << 28), C.ERR_UNSUPPORTED_SHAPE), (dict(ws=None), C.ERR_INVALID_ARG), (dict(ws=0x100010), C.ERR_INVALID_ARG),
+    (dict(nbytes=1000), C.ERR_WORKSPACE_TOO_SMALL),
+])
+def test_route_arguments_refused(lib, kw, code):
+    assert _route(lib, _routing(), **kw) == code
+    assert C.last_error()
+
+
+def test_route_workspace_covers_fewer_tokens(lib):
+    """A workspace for max_tokens serves every call of fewer tokens."""
+    r = _routing()
+    sizes = [lib.clover_route_workspace_bytes(r, m) for m in range(0, 40000, 37)]
+    assert sizes[0] > 0 and all(a <= b for a, b in zip(sizes, sizes[1:]))
+    assert lib.clover_route_workspace_bytes(r, -1) == 0
+    assert lib.clover_route_workspace_bytes(r, 1 << 28) == 0
+
+
+def test_score_name_refused():
+    with pytest.raises(C.CloverError):
+        C.make_routing(8, 2, score="relu")
+
+
+QUANT = dict(fmt=0, x=0x10000, type=1, ldx=256, mats=2, rows=10, cols=256, exp=0, codes=0x20000, scales=0x30000, stream=None)
+ROWS = dict(fmt=0, x=0x10000, type=1, ldx=256, n_src=10, cols=256, exp=0, src=0x40000, div=8, n_rows=10, offsets=0x50000,
+            groups=4, codes=0x20000, scales=0x30000, stream=None)
+DEQ = dict(fmt=0, codes=0x20000, scales=0x30000, mats=1, rows=10, cols=256, exp=0, offsets=0x50000, groups=4, out=0x60000,
+           stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(fmt=2), C.ERR_INVALID_ARG), (dict(cols=96), C.ERR_UNSUPPORTED_SHAPE), (dict(cols=0), C.ERR_UNSUPPORTED_SHAPE),
+    (dict(cols=(1 << 20) + 64), C.ERR_UNSUPPORTED_SHAPE), (dict(exp=65), C.ERR_INVALID_ARG), (dict(exp=-65), C.ERR_INVALID_ARG),
+    (dict(codes=None), C.ERR_INVALID_ARG), (dict(scales=0x30008), C.ERR_INVALID_ARG),
+])
+def test_fp4_arguments_refused(lib, kw, code):
+    for f, base in ((lib.clover_quantize_fp4, QUANT), (lib.clover_quantize_fp4_rows, ROWS), (lib.clover_dequantize_fp4, DEQ)):
+        assert f(*dict(base, **kw).values()) == code, f
+        assert C.last_error()
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x=None), C.ERR_INVALID_ARG), (dict(x=0x10008), C.ERR_INVALID_ARG), (dict(type=2), C.ERR_INVALID_ARG),
+    (dict(ldx=255), C.ERR_INVALID_ARG), (dict(ldx=257), C.ERR_INVALID_ARG),
+])
+def test_fp4_input_refused(lib, kw, code):
+    for f, base in ((lib.clover_quantize_fp4, QUANT), (lib.clover_quantize_fp4_rows, ROWS)):
+        assert f(*dict(base, **kw).values()) == code, f
+
+
+def test_fp4_groups_refused(lib):
+    for f, base in ((lib.clover_quantize_fp4_rows, ROWS), (lib.clover_dequantize_fp4, DEQ)):
+        assert f(*dict(base, groups=0).values()) == C.ERR_UNSUPPORTED_SHAPE
+        assert f(*dict(base, groups=513).values()) == C.ERR_UNSUPPORTED_SHAPE
+        assert f(*dict(base, offsets=0x50002).values()) == C.ERR_INVALID_ARG
+    f = lib.clover_quantize_fp4_rows
+    assert f(*dict(ROWS, offsets=None).values()) == C.ERR_INVALID_ARG
+    assert f(*dict(ROWS, src=0x40002).values()) == C.ERR_INVALID_ARG
+    assert f(*dict(ROWS, div=0).values()) == C.ERR_INVALID_ARG
+    assert f(*dict(ROWS, n_src=-1).values()) == C.ERR_INVALID_ARG
+    assert f(*dict(ROWS, n_rows=-1).values()) == C.ERR_UNSUPPORTED_SHAPE
+    assert lib.clover_dequantize_fp4(*dict(DEQ, mats=2).values()) == C.ERR_INVALID_ARG
+    assert lib.clover_dequantize_fp4(*dict(DEQ, out=None).values()) == C.ERR_INVALID_ARG
+    assert lib.clover_quantize_fp4(*dict(QUANT, mats=1 << 20, rows=1 << 12).values()) == C.ERR_UNSUPPORTED_SHAPE
+    assert lib.clover_quantize_fp4(*dict(QUANT, rows=-1).values()) == C.ERR_INVALID_ARG
+    # nothing to do: no data pointers needed
+    assert f(*dict(ROWS, n_rows=0, x=None, codes=None, offsets=None).values()) == C.OK
+    assert lib.clover_quantize_fp4(*dict(QUANT, rows=0, x=None).values()) == C.OK
+    assert lib.clover_dequantize_fp4(*dict(DEQ, rows=0, out=None).values()) == C.OK
+
+
+def test_fp4_scale_bytes(lib):
+    f, g = lib.clover_fp4_scale_bytes, lib.clover_fp4_grouped_scale_bytes
+    assert f(0, 3, 129, 64) == 3 * 2 * 1 * 512
+    assert f(0, 1, 128, 2048) == 32 * 512
+    assert f(1, 1, 128, 2048) == 16 * 512
+    assert f(1, 1, 1, 64) == 512
+    assert f(0, 1, 0, 64) == 0 and f(0, 1, 1, 65) == 0 and f(5, 1, 1, 64) == 0
+    assert g(0, 256, 7, 64) == (2 + 7) * 512
+    assert g(1, 1000, 1, 192) == (7 + 1) * 2 * 512
+    assert g(0, 1, 0, 64) == 0
+
+
+COMBINE = dict(y=0x10000, n_rows=256, pos=0x20000, w=0x30000, shared=None, x=0x40000, out=0x80000, M=32, K=8, H=256,
+               stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(y=None), C.ERR_INVALID_ARG), (dict(pos=None), C.ERR_INVALID_ARG), (dict(w=None), C.ERR_INVALID_ARG),
+    (dict(out=None), C.ERR_INVALID_ARG), (dict(y=0x10008), C.ERR_INVALID_ARG), (dict(shared=0x50008), C.ERR_INVALID_ARG),
+    (dict(K=0), C.ERR_UNSUPPORTED_SHAPE), (dict(K=33), C.ERR_UNSUPPORTED_SHAPE), (dict(H=12), C.ERR_UNSUPPORTED_SHAPE),
+    (dict(H=0), C.ERR_UNSUPPORTED_SHAPE), (dict(M=-1), C.ERR_INVALID_ARG), (dict(n_rows=-1), C.ERR_INVALID_ARG),
+    (dict(M=1 << 28), C.ERR_UNSUPPORTED_SHAPE), (dict(out=0x40010), C.ERR_INVALID_ARG),
+])
+def test_combine_arguments_refused(lib, kw, code):
+    assert lib.clover_moe_combine(*dict(COMBINE, **kw).values()) == code
+    assert C.last_error()
+
+
+def test_combine_nothing_to_do(lib):
+    assert lib.clover_moe_combine(*dict(COMBINE, M=0, y=None, pos=None, w=None, out=None).values()) == C.OK
+
+
+def test_wrappers_refuse_host_tensors(lib):
+    r = C.make_routing(8, 2)
+    with pytest.raises((C.CloverError, RuntimeError, AssertionError)):
+        C.route(r, torch.zeros(4, 8))
+
+
+# ----------------------------------------------------------------- oracle pins
+
+
+def test_e4m3_and_e2m1_tables():
+    f8 = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(R.E4M3, f8)
+    assert np.isnan(R.e4m3_value(0x7F)) and R.e4m3_value(0x80 | 0x38) == -1.0
+    # ties go to the even code, everything past 6 to 6
+    for v, want in ((0.25, 0), (0.75, 2), (1.25, 2), (1.75, 4), (2.5, 4), (3.5, 6), (5.0, 6), (0.26, 1), (4.9, 6), (1e9, 7)):
+        assert R.nearest(R.E2M1, v) == want, v
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_oracle_round_trip(fmt):
+    """Values that the format holds come back; a block's error is at most half of the widest step below its maximum."""
+    rng = np.random.default_rng(1)
+    codes = rng.integers(0, 16, size=(5, 64)).astype(np.uint8)
+    codes[:, ::16] = 7  # every block's largest value is 6
+    if fmt == "nv":
+        sb = rng.integers(40, 80, size=(5, 4)).astype(np.uint8)
+    else:
+        sb = rng.integers(100, 140, size=(5, 2)).astype(np.uint8)
+    x = R.dequantize(codes, sb, fmt)
+    c2, s2 = R.quantize(x, fmt)
+    assert np.array_equal(s2, sb) and np.array_equal(c2, codes)
+    x = rng.normal(size=(4, 128)).astype(np.float32)
+    d = R.dequantize(*R.quantize(x, fmt), fmt)
+    block = 16 if fmt == "nv" else 32
+    amax = np.abs(x).reshape(4, -1, block).max(-1).repeat(block, 1).reshape(4, 128)
+    # widest step 2 (between 4 and 6) times the scale: NV s <= amax / 6 * (1 + 1/16), saturation costs amax - 6 s <=
+    # amax / 17; MX s <= amax / 4, saturation costs less than 2 s
+    assert np.all(np.abs(d - x) <= (amax / 6 * 17 / 16 if fmt == "nv" else amax / 2))
+
+
+def test_oracle_scale_places_are_a_permutation():
+    seen = {R.scale_place(r, b) for r in range(256) for b in range(8)}
+    assert len(seen) == 256 * 8
+    assert R.scale_place(33, 2) == (0, 0, 16 + 4 + 2)
+    off = [0, 0, 130, 131, 131, 400]
+    rows = [R.grouped_scale_row(i, off) for i in range(400)]
+    assert len(set(rows)) == 400 and max(rows) < (400 // 128 + 5) * 128
+
+
+def test_oracle_route_by_hand():
+    z = np.array([[0.0, 2.0, 1.0, -np.inf], [-np.inf] * 4, [np.nan, 1.0, 1.0, 0.0]])
+    r = R.route(z, 2)
+    assert r["idx"].tolist() == [[1, 2], [-1, -1], [1, 2]]
+    e = np.exp(-1.0)
+    assert np.allclose(r["w"][0], [1 / (1 + e), e / (1 + e)]) and r["w"][1].tolist() == [0, 0]
+    assert r["offsets"].tolist() == [0, 0, 2, 4, 4] and r["rows"].tolist() == [0, 4, 1, 5]
+    assert r["pos"].tolist() == [[0, 2], [-1, -1], [1, 3]]
+    # the bias moves the choice, not the weight; groups of two, one kept by its two best
+    z = np.array([[3.0, -3.0, 1.0, 1.0]])
+    r = R.route(z, 1, score="sigmoid", bias=np.array([0, 0, 0, 1.0]), renormalise=False, scale=2.0)
+    assert r["idx"].tolist() == [[3]] and np.allclose(r["w"], 2 / (1 + np.exp(-1.0)))
+    r = R.route(z, 2, score="sigmoid", n_groups=2, top_groups=1, group_rank=2)
+    assert r["idx"].tolist() == [[2, 3]]
+    r = R.route(z, 2, score="sigmoid", n_groups=2, top_groups=1, group_rank=1)
+    assert r["idx"].tolist() == [[0, 1]]
