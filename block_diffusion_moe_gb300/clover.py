@@ -104,6 +104,9 @@ EXPORTS = {
                                                 _ptr_t, _i32, _ptr_t, _ptr_t, _ptr_t]),
     "clover_dequantize_fp4": (ctypes.c_int, [_i32, _ptr_t, _ptr_t, _i32, _i32, _i32, _i32, _ptr_t, _i32, _ptr_t,
                                              _ptr_t]),
+    "clover_fp4_product_workspace_bytes": (_size, []),
+    "clover_fp4_product": (ctypes.c_int, [_i32, _ptr_t, _ptr_t, _i32, _ptr_t, _ptr_t, _ptr_t, _i32, _i32, _i32,
+                                          ctypes.c_float, _ptr_t, _i32, _ptr_t, _ptr_t, _size, _ptr_t]),
     "clover_moe_combine": (ctypes.c_int, [_ptr_t, _i32, _ptr_t, _ptr_t, _ptr_t, _ptr_t, _ptr_t, _i32, _i32, _i32,
                                           _ptr_t]),
 }
@@ -530,6 +533,40 @@ def dequantize_fp4(q: Fp4, out=None, stream=None):
     p_out = _tensor("out", out, torch.bfloat16, shape, dev)
     _check(lib().clover_dequantize_fp4(q.fmt, p_codes, p_scales, q.mats, q.rows, q.cols, q.scale_exp, p_off,
                                        0 if p_off is None else q.offsets.shape[0] - 1, p_out, _raw_stream(stream, dev)))
+    return out
+
+
+def fp4_product_workspace_bytes() -> int:
+    return lib().clover_fp4_product_workspace_bytes()
+
+
+def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_alpha=None, ws=None, out=None,
+                stream=None):
+    """Rows of `a` times the matrix of their group (a.offsets; without offsets one group of all rows): bf16
+    [rows][N], or with swiglu silu(gate) * up, [rows][N / 2]. b holds one [N][cols] matrix per group, or with swiglu two
+    of N / 2 rows (gate, up). The result is scaled by alpha, group_alpha (fp32 [groups]) and both operands' scale_exp;
+    rows behind the last group are left as they were."""
+    pa_codes, pa_scales, p_off = a._ptrs("a")
+    pb_codes, pb_scales, b_off = b._ptrs("b")
+    dev, per = a.codes.device, 2 if swiglu else 1
+    if a.codes.dim() != 2 or b_off is not None:
+        _refuse("a must be one matrix, and only its rows may form groups")
+    if a.fmt != b.fmt or a.cols != b.cols or b.codes.device != dev:
+        _refuse(f"a (format {a.fmt}, {a.cols} columns, {dev}) does not match b (format {b.fmt}, {b.cols} columns, "
+                f"{b.codes.device})")
+    groups = 1 if p_off is None else a.offsets.shape[0] - 1
+    if b.mats != groups * per:
+        _refuse(f"b holds {b.mats} matrices for {groups} groups, {per} each")
+    rows, width = a.rows, b.rows
+    if ws is None:
+        ws = workspace(fp4_product_workspace_bytes(), dev)
+    if out is None:
+        out = torch.empty((rows, width), dtype=torch.bfloat16, device=dev)
+    p_alpha = None if group_alpha is None else _tensor("group_alpha", group_alpha, torch.float32, (groups,), dev)
+    _check(lib().clover_fp4_product(a.fmt, pa_codes, pa_scales, rows, pb_codes, pb_scales, p_off, groups, width * per,
+                                    a.cols, alpha * 2.0 ** (a.scale_exp + b.scale_exp), p_alpha, int(swiglu),
+                                    _tensor("out", out, torch.bfloat16, (rows, width), dev), ws.data_ptr(), ws.numel(),
+                                    _raw_stream(stream, dev)))
     return out
 
 

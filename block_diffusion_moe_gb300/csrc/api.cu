@@ -884,6 +884,24 @@ namespace clover {
 // clover_last_error().
 int set_last_error(int code, const char* msg) { return fail(code, "%s", msg); }
 
+int encode_code_boxes(void* tensor_map, const void* base, uint64_t n, uint64_t rows, uint64_t row_bytes,
+                      uint32_t box_rows, const char* what) {
+  int rc;
+  if ((rc = get_encoder())) return rc;
+  const cuuint64_t dims[3] = {row_bytes, rows, n};
+  const cuuint64_t strides[2] = {row_bytes, rows * row_bytes};
+  const cuuint32_t box[3] = {128, box_rows, 1};
+  return encode_nd(static_cast<CUtensorMap*>(tensor_map), CU_TENSOR_MAP_DATA_TYPE_UINT8, base, n == 0 ? 2 : 3, dims,
+                   strides, box, CU_TENSOR_MAP_SWIZZLE_128B, what);
+}
+
+int device_sms(int* sms) {
+  DevInfo di;
+  const int rc = device_info(&di);
+  *sms = di.sms;
+  return rc;
+}
+
 int check_workspace(void* workspace, size_t have, size_t need) { return check_ws(workspace, have, need); }
 
 // clover_lmhead_unmask with one option: clear_ctrl zeroes the workspace's

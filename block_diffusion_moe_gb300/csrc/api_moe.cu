@@ -34,8 +34,10 @@ int launched(cudaError_t e, const char* where) {
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-constexpr int kMaxGroups = 512;
-constexpr int kMaxSlots = 1 << 30;
+constexpr int kMaxGroups = kFp4MaxGroups;
+// Slots or rows of a call: 2^29 keeps every count of row tiles in 31 bits, even
+// over offsets that do not ascend.
+constexpr int kMaxSlots = 1 << 29;
 constexpr size_t kCtrlBytes = 256;  // the status word that clover_workspace_status reads
 
 int check_routing(const clover_routing* r) {
@@ -91,7 +93,7 @@ int check_input(const void* x, int32_t x_type, int64_t ldx, int32_t cols) {
 }
 
 int check_groups(int32_t n_rows, int32_t n_groups) {
-  if (n_rows < 0 || n_rows > kMaxSlots) return fail(CLOVER_ERR_UNSUPPORTED_SHAPE, "n_rows=%d outside [0, 2^30]", n_rows);
+  if (n_rows < 0 || n_rows > kMaxSlots) return fail(CLOVER_ERR_UNSUPPORTED_SHAPE, "n_rows=%d outside [0, 2^29]", n_rows);
   if (n_groups < 1 || n_groups > kMaxGroups)
     return fail(CLOVER_ERR_UNSUPPORTED_SHAPE, "n_groups=%d outside [1, %d]", n_groups, kMaxGroups);
   return CLOVER_OK;
@@ -100,7 +102,7 @@ int check_groups(int32_t n_rows, int32_t n_groups) {
 int check_matrices(int32_t n_mats, int32_t rows) {
   if (n_mats < 0 || rows < 0) return fail(CLOVER_ERR_INVALID_ARG, "n_mats=%d rows=%d: negative", n_mats, rows);
   if (static_cast<int64_t>(n_mats) * rows > kMaxSlots)
-    return fail(CLOVER_ERR_UNSUPPORTED_SHAPE, "n_mats=%d rows=%d: more than 2^30 rows", n_mats, rows);
+    return fail(CLOVER_ERR_UNSUPPORTED_SHAPE, "n_mats=%d rows=%d: more than 2^29 rows", n_mats, rows);
   return CLOVER_OK;
 }
 
@@ -123,7 +125,7 @@ extern "C" {
 size_t clover_route_workspace_bytes(const clover_routing* routing, int32_t max_tokens) {
   if (check_routing(routing)) return 0;
   if (max_tokens < 0 || static_cast<int64_t>(max_tokens) * routing->top_k > kMaxSlots) {
-    fail(CLOVER_ERR_UNSUPPORTED_SHAPE, "max_tokens=%d: negative, or more than 2^30 slots", max_tokens);
+    fail(CLOVER_ERR_UNSUPPORTED_SHAPE, "max_tokens=%d: negative, or more than 2^29 slots", max_tokens);
     return 0;
   }
   return route_bytes(*routing, max_tokens);
@@ -136,7 +138,7 @@ int clover_route(const clover_routing* routing, const void* logits, int32_t logi
   if ((rc = check_routing(routing))) return rc;
   const clover_routing& r = *routing;
   if (M < 0 || static_cast<int64_t>(M) * r.top_k > kMaxSlots)
-    return fail(CLOVER_ERR_UNSUPPORTED_SHAPE, "M=%d: negative, or more than 2^30 slots", M);
+    return fail(CLOVER_ERR_UNSUPPORTED_SHAPE, "M=%d: negative, or more than 2^29 slots", M);
   if (logits_type != CLOVER_TYPE_F32 && logits_type != CLOVER_TYPE_BF16)
     return fail(CLOVER_ERR_INVALID_ARG, "logits_type=%d is neither fp32 nor bf16", logits_type);
   const bool grouping = offsets != nullptr;
@@ -273,6 +275,50 @@ int clover_dequantize_fp4(int32_t format, const uint8_t* codes, const uint8_t* s
   a.out = reinterpret_cast<__nv_bfloat16*>(out);
   return launched(launch_dequantize_fp4(a, format == CLOVER_FP4_MX, reinterpret_cast<cudaStream_t>(stream)),
                   "launch dequantize fp4");
+}
+
+size_t clover_fp4_product_workspace_bytes(void) { return kCtrlBytes; }
+
+int clover_fp4_product(int32_t format, const uint8_t* a_codes, const uint8_t* a_scales, int32_t n_rows,
+                       const uint8_t* b_codes, const uint8_t* b_scales, const int32_t* offsets, int32_t n_groups,
+                       int32_t N, int32_t K, float alpha, const float* group_alpha, int32_t epilogue, uint16_t* y,
+                       void* workspace, size_t workspace_bytes, clover_stream_t stream) {
+  int rc;
+  if ((rc = check_fp4(format, K)) || (rc = check_groups(n_rows, n_groups))) return rc;
+  if (epilogue != CLOVER_FP4_PLAIN && epilogue != CLOVER_FP4_SWIGLU)
+    return fail(CLOVER_ERR_INVALID_ARG, "epilogue=%d is neither plain nor SwiGLU", epilogue);
+  const bool swiglu = epilogue == CLOVER_FP4_SWIGLU;
+  if (N < 1 || N > (1 << 24) || (swiglu && N % 2 != 0))
+    return fail(CLOVER_ERR_UNSUPPORTED_SHAPE, "N=%d: must be 1 to 2^24, even with SwiGLU", N);
+  if (offsets == nullptr && n_groups != 1)
+    return fail(CLOVER_ERR_INVALID_ARG, "offsets is NULL with n_groups=%d", n_groups);
+  if ((rc = check_workspace(workspace, workspace_bytes, kCtrlBytes))) return rc;
+  if (n_rows == 0) return CLOVER_OK;
+  if ((rc = check_codes(a_codes, a_scales)) || (rc = check_codes(b_codes, b_scales))) return rc;
+  if (y == nullptr || !aligned(y, 16)) return fail(CLOVER_ERR_INVALID_ARG, "y is NULL or not 16-byte aligned");
+  if (!aligned(offsets, 4) || !aligned(group_alpha, 4))
+    return fail(CLOVER_ERR_INVALID_ARG, "offsets/group_alpha not 4-byte aligned");
+  int sms = 0;
+  if ((rc = device_sms(&sms))) return rc;
+  Fp4ProductArgs a;
+  memset(&a, 0, sizeof(a));
+  a.b_rows = swiglu ? N / 2 : N;
+  if ((rc = encode_code_boxes(&a.tm_a, a_codes, 0, n_rows, K / 2, 32, "rows' codes"))) return rc;
+  if ((rc = encode_code_boxes(&a.tm_b, b_codes, static_cast<uint64_t>(n_groups) * (swiglu ? 2 : 1), a.b_rows, K / 2, 128,
+                              "matrices' codes")))
+    return rc;
+  a.a_scales = a_scales;
+  a.b_scales = b_scales;
+  a.offsets = offsets;
+  a.group_alpha = group_alpha;
+  a.alpha = alpha;
+  a.n_rows = n_rows;
+  a.n_groups = n_groups;
+  a.K = K;
+  a.y = reinterpret_cast<__nv_bfloat16*>(y);
+  a.err = static_cast<int*>(workspace);
+  return launched(launch_fp4_product(a, format == CLOVER_FP4_MX, swiglu, sms, reinterpret_cast<cudaStream_t>(stream)),
+                  "launch fp4 product");
 }
 
 int clover_moe_combine(const uint16_t* y, int32_t n_rows, const int32_t* pos, const float* w, const uint16_t* shared,

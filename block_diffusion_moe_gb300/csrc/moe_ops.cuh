@@ -79,4 +79,25 @@ struct Fp4QuantArgs {
 cudaError_t launch_quantize_fp4(const Fp4QuantArgs& a, bool mx, cudaStream_t s);
 cudaError_t launch_dequantize_fp4(const Fp4QuantArgs& a, bool mx, cudaStream_t s);
 
+constexpr int kFp4MaxGroups = 512;
+
+// Grouped product of 4-bit rows (csrc/product.cu).
+struct Fp4ProductArgs {
+  CUtensorMap tm_a;          // codes [n_rows][K / 2], boxes of 128 bytes x 32 rows
+  CUtensorMap tm_b;          // codes [mats][rows of a matrix][K / 2], boxes of 128 bytes x 128 rows x 1
+  const uint8_t* a_scales;   // tiles of 128 rows
+  const uint8_t* b_scales;
+  const int32_t* offsets;    // [n_groups + 1] or null (one group of all rows)
+  const float* group_alpha;  // [n_groups] or null
+  float alpha;
+  int n_rows, n_groups;
+  int b_rows;                // rows of one B matrix: N, or N / 2 with SwiGLU
+  int K;
+  __nv_bfloat16* y;          // [n_rows][b_rows]
+  int* err;
+};
+
+size_t fp4_product_smem_bytes();
+cudaError_t launch_fp4_product(const Fp4ProductArgs& a, bool mx, bool swiglu, int grid, cudaStream_t s);
+
 }  // namespace clover

@@ -1,0 +1,345 @@
+// Grouped product of rows and matrices in the microscaled 4-bit formats
+// (clover_fp4_product): y = alpha_g A_i . B_g^T, optionally SwiGLU, on the
+// block-scaled tensor-core instruction (tcgen05.mma kind::mxf4nvf4).
+//
+// One persistent CTA per SM. A tile is 128 rows of one group x 256 rows of its
+// matrix (SwiGLU: 128 gate rows and their 128 up rows, so that one thread
+// holds both factors). Roles: warp 0 streams codes (TMA, 128-byte swizzle)
+// and scale tiles (bulk copies) through a ring of stages of 256 K elements,
+// warp 1 copies each stage's scales to tensor memory and issues its four
+// MMAs, warps 4-7 drain the accumulator (one TMEM lane quarter each).
+#include <math.h>
+
+#include "fp4.cuh"
+#include "launch.cuh"
+#include "moe_ops.cuh"
+#include "routing.cuh"
+#include "sm100.cuh"
+
+namespace clover {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTileM = 128;          // rows of A per tile
+constexpr int kTileN = 256;          // rows of B per tile
+constexpr int kStageK = 256;         // K elements per stage: 128 bytes of codes per row
+constexpr int kStages = 4;
+constexpr int kABytes = kTileM * kStageK / 2;
+constexpr int kBBytes = kTileN * kStageK / 2;
+// Scale tiles of a stage: 4 chunks of 64 K elements (NV), 2 of 128 (MX)
+constexpr int kMaxChunks = 4;
+constexpr int kSfABytes = kMaxChunks * 512;
+constexpr int kSfBBytes = 2 * kMaxChunks * 512;
+constexpr int kStageBytes = kABytes + kBBytes + kSfABytes + kSfBBytes;
+
+// Tensor memory: the accumulators of consecutive tiles are columns 0-255 and
+// 192-447: 512 columns do not hold two of 256 and the scales, so they share
+// columns 192-255, which the epilogue drains first.
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kAcc1 = 192;
+constexpr uint32_t kTmemSfA = 448;
+constexpr uint32_t kTmemSfB = kTmemSfA + 4 * kMaxChunks;
+static_assert(kTmemSfB + 8 * kMaxChunks <= kTmemCols, "scales must fit behind the accumulators");
+
+struct Shared {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t acc_full;    // a tile's accumulator is complete
+  uint64_t acc_shared;  // the columns it shares with the next one are drained
+  uint64_t drain;
+  uint32_t tmem;
+  uint32_t abort;
+  int scan[17];
+  int off[kFp4MaxGroups];      // first row of each group
+  int cnt[kFp4MaxGroups];      // its rows
+  int mt[kFp4MaxGroups + 1];   // row tiles of the groups before it
+};
+
+__device__ __forceinline__ void give_up(const Fp4ProductArgs& p, Shared* sh) {
+  atomicOr(p.err, kErrMbarTimeout);
+  *reinterpret_cast<volatile uint32_t*>(&sh->abort) = 1u;
+}
+
+// Tile t, group by group, a group's row tiles in turn, the column tiles of a
+// row tile next to one another.
+struct Tile {
+  int g;
+  int row0, rows;    // first row of A, rows of it that belong to the group
+  int64_t sf_tile;   // scale tile of those rows
+  int n0;            // first row of the B matrix (SwiGLU: of either half)
+};
+
+__device__ __forceinline__ Tile tile_at(const Fp4ProductArgs& p, const Shared& sh, int64_t t, int n_tiles, int step) {
+  const int m = static_cast<int>(t / n_tiles);
+  int lo = 0, hi = p.n_groups;  // the last group with mt[g] <= m
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sh.mt[mid] <= m)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  Tile r;
+  r.g = lo;
+  const int i = m - sh.mt[lo];
+  r.row0 = sh.off[lo] + i * kTileM;
+  r.rows = min(kTileM, sh.cnt[lo] - i * kTileM);
+  r.sf_tile = sh.off[lo] / 128 + static_cast<int64_t>(lo) + i;
+  r.n0 = static_cast<int>(t - static_cast<int64_t>(m) * n_tiles) * step;
+  return r;
+}
+
+template <bool kMx, bool kSwiglu>
+__device__ void producer(const Fp4ProductArgs& p, Shared* sh, uint8_t* ring, int64_t n_all, int n_tiles) {
+  volatile uint32_t* abort = &sh->abort;
+  constexpr int kChunk = kMx ? 128 : 64;  // K elements per scale tile
+  const uint64_t pol = l2_policy_evict_last();  // row tiles share B tiles, column tiles share A tiles
+  const int nk = (p.K + kStageK - 1) / kStageK;
+  const int chunks = (p.K + kChunk - 1) / kChunk;
+  const int b_tiles = (p.b_rows + 127) / 128;
+  int st = 0;
+  uint32_t ph = 0, issued = 0, parity_bits = 0;
+  bool ok = true;
+  for (int64_t t = blockIdx.x; t < n_all && ok; t += gridDim.x) {
+    const Tile tl = tile_at(p, *sh, t, n_tiles, kSwiglu ? 128 : 256);
+    const int boxes = (tl.rows + 31) / 32;
+    // the two halves of the B tile: gate and up rows, or consecutive rows
+    // (the second may lie past the matrix: its columns are never stored)
+    const int halves = (kSwiglu || tl.n0 + 128 < p.b_rows) ? 2 : 1;
+    for (int k = 0; k < nk; ++k) {
+      if (!mbar_wait(&sh->empty[st], ph ^ 1u, abort)) {
+        give_up(p, sh);
+        ok = false;
+        break;
+      }
+      const int c0 = k * (kStageK / kChunk);
+      const int nc = min(kStageK / kChunk, chunks - c0);
+      uint64_t* bar = &sh->full[st];
+      const uint32_t base = smem_u32(ring + static_cast<size_t>(st) * kStageBytes);
+      mbar_arrive_expect_tx(bar, boxes * 4096 + halves * (kBBytes / 2) + (1 + halves) * nc * 512);
+      for (int b = 0; b < boxes; ++b) tma_load_2d(base + b * 4096, &p.tm_a, bar, k * 128, tl.row0 + b * 32, pol);
+      const uint32_t sfa = base + kABytes + kBBytes, sfb = sfa + kSfABytes;
+      bulk_load(sfa, p.a_scales + (tl.sf_tile * chunks + c0) * 512, nc * 512, bar);
+      for (int h = 0; h < halves; ++h) {
+        const int mat = kSwiglu ? 2 * tl.g + h : tl.g;
+        const int row = kSwiglu ? tl.n0 : tl.n0 + h * 128;
+        tma_load_3d(base + kABytes + h * (kBBytes / 2), &p.tm_b, bar, k * 128, row, mat, pol);
+        bulk_load(sfb + h * kMaxChunks * 512,
+                  p.b_scales + ((static_cast<int64_t>(mat) * b_tiles + row / 128) * chunks + c0) * 512, nc * 512, bar);
+      }
+      issued |= 1u << st;
+      parity_bits = (parity_bits & ~(1u << st)) | (ph << st);
+      if (++st == kStages) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+  }
+  if (*abort) {  // the copies in flight must land before the CTA leaves
+    for (int i = 0; i < kStages; ++i)
+      if (issued & (1u << i)) mbar_wait_for(&sh->full[i], (parity_bits >> i) & 1u, 200000000ull);
+  }
+}
+
+template <bool kMx>
+__device__ void mma_issuer(const Fp4ProductArgs& p, Shared* sh, uint8_t* ring, int64_t n_all) {
+  volatile uint32_t* abort = &sh->abort;
+  const uint32_t tmem = sh->tmem;
+  constexpr int kChunk = kMx ? 128 : 64;
+  const int nk = (p.K + kStageK - 1) / kStageK;
+  int st = 0, it = 0;
+  uint32_t ph = 0;
+  bool ok = true;
+  for (int64_t t = blockIdx.x; t < n_all && ok; t += gridDim.x, ++it) {
+    // the columns shared with the previous tile's accumulator are free once
+    // that one's epilogue has drained them, and it drained the tile before
+    // that first
+    if (it > 0 && !mbar_wait(&sh->acc_shared, (it - 1) & 1, abort)) {
+      give_up(p, sh);
+      break;
+    }
+    tc_fence_after();
+    const uint32_t d = tmem + (it & 1 ? kAcc1 : 0u);
+    for (int k = 0; k < nk; ++k) {
+      if (!mbar_wait(&sh->full[st], ph, abort)) {
+        give_up(p, sh);
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t base = smem_u32(ring + static_cast<size_t>(st) * kStageBytes);
+      const uint32_t sfa = base + kABytes + kBBytes, sfb = sfa + kSfABytes;
+      const int steps = min(kStageK / 64, p.K / 64 - k * (kStageK / 64));
+      const int nc = kMx ? (steps + 1) / 2 : steps;
+      for (int c = 0; c < nc; ++c) {
+        tmem_copy_scales(tmem + kTmemSfA + c * 4, sfa + c * 512);
+        tmem_copy_scales(tmem + kTmemSfB + c * 8, sfb + c * 512);
+        tmem_copy_scales(tmem + kTmemSfB + c * 8 + 4, sfb + (kMaxChunks + c) * 512);
+      }
+      const uint64_t ad = umma_desc_sw128(base), bd = umma_desc_sw128(base + kABytes);
+      for (int s = 0; s < steps; ++s) {
+        const int c = s * 64 / kChunk;
+        umma_fp4<kMx>(d, ad + 2 * s, bd + 2 * s, umma_idesc_fp4(kTileM, kTileN, kMx, kMx ? (s & 1) * 2 : 0),
+                      tmem + kTmemSfA + c * 4, tmem + kTmemSfB + c * 8, (k | s) != 0 ? 1u : 0u);
+      }
+      umma_commit(&sh->empty[st]);
+      if (++st == kStages) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+    if (ok) umma_commit(&sh->acc_full);
+  }
+  umma_commit(&sh->drain);
+  mbar_wait_for(&sh->drain, 0, 200000000ull);
+}
+
+// Stores 32 consecutive bf16 of one row, columns c0 .. c0 + 31 of `width`.
+__device__ __forceinline__ void store32(__nv_bfloat16* row, int c0, int width, bool vec, const float (&v)[32]) {
+  if (vec && c0 + 32 <= width) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+        o[i] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      *reinterpret_cast<uint4*>(row + c0 + 8 * j) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (c0 + j < width) row[c0 + j] = __float2bfloat16_rn(v[j]);
+  }
+}
+
+template <bool kSwiglu>
+__device__ void epilogue(const Fp4ProductArgs& p, Shared* sh, int64_t n_all, int n_tiles) {
+  volatile uint32_t* abort = &sh->abort;
+  const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const bool vec = p.b_rows % 8 == 0;  // rows of y 16-byte aligned
+  int it = 0;
+  for (int64_t t = blockIdx.x; t < n_all; t += gridDim.x, ++it) {
+    const Tile tl = tile_at(p, *sh, t, n_tiles, kSwiglu ? 128 : 256);
+    int good = 1;
+    if (lane == 0 && !mbar_wait(&sh->acc_full, it & 1, abort)) {
+      give_up(p, sh);
+      good = 0;
+    }
+    if (!__shfl_sync(0xffffffffu, good, 0)) return;
+    tc_fence_after();
+    const bool odd = it & 1;
+    const uint32_t acc = sh->tmem + (static_cast<uint32_t>(q * 32) << 16) + (odd ? kAcc1 : 0u);
+    const int r = q * 32 + lane;
+    const bool on = r < tl.rows;
+    const float alpha = p.alpha * (p.group_alpha != nullptr ? p.group_alpha[tl.g] : 1.f);
+    __nv_bfloat16* row = p.y + static_cast<int64_t>(tl.row0 + r) * p.b_rows;
+    // chunks of 32 columns; the two that hold the shared columns come first
+    // (the last two of the even accumulator, the first two of the odd one)
+    constexpr int kChunks = kSwiglu ? 4 : 8;
+    for (int i = 0; i < kChunks; ++i) {
+      const int c = odd ? i : (i + kChunks - 2) % kChunks;
+      float v[32];
+      tmem_ld32(acc + c * 32, v);
+      if (kSwiglu) {
+        float u[32];
+        tmem_ld32(acc + 128 + c * 32, u);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float g = v[j] * alpha;
+          v[j] = __fdividef(g, 1.f + __expf(fminf(-g, 80.f))) * (u[j] * alpha);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] *= alpha;
+      }
+      if (i == 1) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->acc_shared);
+      }
+      if (on) store32(row, tl.n0 + c * 32, p.b_rows, vec, v);
+    }
+  }
+}
+
+}  // namespace
+
+template <bool kMx, bool kSwiglu>
+__global__ void __launch_bounds__(kThreads, 1) k_fp4_product(const __grid_constant__ Fp4ProductArgs p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  Shared* sh = reinterpret_cast<Shared*>(ring + static_cast<size_t>(kStages) * kStageBytes);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&p.tm_a);
+    tma_prefetch_desc(&p.tm_b);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], 1);
+    }
+    mbar_init(&sh->acc_full, 1);
+    mbar_init(&sh->acc_shared, 4);
+    mbar_init(&sh->drain, 1);
+    sh->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh->tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_trigger();
+  // the groups' rows and row tiles, two groups per thread
+  int tiles[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int g = 2 * threadIdx.x + j;
+    tiles[j] = 0;
+    if (g < p.n_groups) {
+      const int lo = p.offsets != nullptr ? group_offset(p.offsets, g, p.n_rows) : 0;
+      const int hi = p.offsets != nullptr ? group_offset(p.offsets, g + 1, p.n_rows) : p.n_rows;
+      sh->off[g] = lo;
+      sh->cnt[g] = max(hi - lo, 0);
+      tiles[j] = (sh->cnt[g] + kTileM - 1) / kTileM;
+    }
+  }
+  int m_tiles;
+  const int before = block_excl_scan(tiles[0] + tiles[1], sh->scan, &m_tiles);
+  if (2 * threadIdx.x <= p.n_groups) sh->mt[2 * threadIdx.x] = before;
+  if (2 * threadIdx.x + 1 <= p.n_groups) sh->mt[2 * threadIdx.x + 1] = before + tiles[0];
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const int step = kSwiglu ? 128 : 256;
+  const int n_tiles = (p.b_rows + step - 1) / step;
+  const int64_t n_all = static_cast<int64_t>(m_tiles) * n_tiles;
+  if (warp == 0) {
+    if ((threadIdx.x & 31) == 0) producer<kMx, kSwiglu>(p, sh, ring, n_all, n_tiles);
+  } else if (warp == 1) {
+    if ((threadIdx.x & 31) == 0) mma_issuer<kMx>(p, sh, ring, n_all);
+  } else if (warp >= 4) {
+    epilogue<kSwiglu>(p, sh, n_all, n_tiles);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(sh->tmem, kTmemCols);
+  }
+}
+
+size_t fp4_product_smem_bytes() { return 1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(Shared); }
+
+cudaError_t launch_fp4_product(const Fp4ProductArgs& a, bool mx, bool swiglu, int grid, cudaStream_t s) {
+  void (*k)(const Fp4ProductArgs) = mx ? (swiglu ? k_fp4_product<true, true> : k_fp4_product<true, false>)
+                                       : (swiglu ? k_fp4_product<false, true> : k_fp4_product<false, false>);
+  const size_t smem = fp4_product_smem_bytes();
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_kernel(k, dim3(grid), dim3(kThreads), smem, s, true, a);
+}
+
+}  // namespace clover

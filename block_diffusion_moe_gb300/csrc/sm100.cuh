@@ -245,6 +245,53 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, u
       : "memory");
 }
 
+// Instruction descriptor of the block-scaled 4-bit product: e2m1 A and B,
+// fp32 accumulator, both operands K-major, shape M x N x 64. scale_mx: e8m0
+// scales (two per row and 64 K), else e4m3 (four). sf_id: which byte of the
+// 32-bit scale column holds the first scale (0, or 2 for the second pair).
+__host__ __device__ constexpr uint32_t umma_idesc_fp4(int M, int N, bool scale_mx, int sf_id) {
+  return (static_cast<uint32_t>(sf_id) << 4)        // B scale byte
+         | (1u << 7)                                // A format: e2m1
+         | (1u << 10)                               // B format: e2m1
+         | (static_cast<uint32_t>(N >> 3) << 17)    // N / 8
+         | ((scale_mx ? 1u : 0u) << 23)             // scale type: e8m0 or e4m3
+         | (static_cast<uint32_t>(M >> 4) << 24)    // M / 16
+         | (static_cast<uint32_t>(sf_id) << 29);    // A scale byte
+}
+
+// D[tmem] (+)= (A[smem] scaled by sfa[tmem]) * (B[smem] scaled by
+// sfb[tmem])^T over 64 K elements, issued by one thread.
+template <bool kMx>
+__device__ __forceinline__ void umma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if (kMx) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  }
+}
+
+// Copies a 512-byte scale tile (32 rows of 16 bytes) from shared memory to 4
+// TMEM columns of lanes 0-31, repeated in the other three lane quarters.
+// Ordered with this thread's earlier and later tcgen05.mma.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);  // start address
+  d |= static_cast<uint64_t>(128 >> 4) << 32;            // stride byte offset: 8 rows x 16 B
+  d |= static_cast<uint64_t>(1) << 46;                   // descriptor version, no swizzle
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
 // Stores 32 consecutive 32-bit TMEM columns of this warp's 32 lanes (thread i
 // writes lane base+i); tmem_wait_st waits for this thread's stores.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {

@@ -299,7 +299,8 @@ int clover_lmhead_unmask_static_status(clover_stream_t stream);
  * The conventions at the top of this file hold, with these differences: the
  * limits on shapes are the ones stated per call, a call with no rows
  * (M == 0 or n_rows == 0) is valid and needs no data pointers, and none of
- * the calls changes its inputs. */
+ * the calls changes its inputs. Rows, and a token's K slots, count up to 2^29
+ * in any one call. */
 
 /* Score functions of clover_route. */
 #define CLOVER_SCORE_SOFTMAX 0
@@ -350,7 +351,7 @@ size_t clover_route_workspace_bytes(const clover_routing* routing, int32_t max_t
  * are listed in rows by expert, then token; expert e's are rows[offsets[e]]
  * .. rows[offsets[e + 1] - 1]. pos[t][k] is the place of slot (t, k) in rows,
  * or -1. Places of rows from offsets[E] on are left as they were.
- * M * top_k <= 2^30. Every result is independent of the launch shape. */
+ * M * top_k <= 2^29. Every result is independent of the launch shape. */
 int clover_route(const clover_routing* routing, const void* logits, int32_t logits_type, int64_t ld,
                  const float* bias, int32_t M, int32_t* topk_idx, float* topk_w, int32_t* offsets,
                  int32_t* rows, int32_t* pos, void* workspace, size_t workspace_bytes,
@@ -407,6 +408,36 @@ int clover_quantize_fp4_rows(int32_t format, const void* x, int32_t x_type, int6
 int clover_dequantize_fp4(int32_t format, const uint8_t* codes, const uint8_t* scales, int32_t n_mats,
                           int32_t rows, int32_t cols, int32_t scale_exp, const int32_t* offsets,
                           int32_t n_groups, uint16_t* out, clover_stream_t stream);
+
+/* Epilogues of clover_fp4_product. */
+#define CLOVER_FP4_PLAIN 0
+#define CLOVER_FP4_SWIGLU 1
+
+/* Bytes of workspace clover_fp4_product needs (its status word; calls that
+ * may run at the same time may share it). Host-only. */
+size_t clover_fp4_product_workspace_bytes(void);
+
+/* Products of rows with the matrix of their group, both in a microscaled
+ * 4-bit format, on the tensor cores (fp32 accumulation):
+ *   z_i = alpha * group_alpha[g] * (A_i . B_g^T) for row i of group g
+ *   CLOVER_FP4_PLAIN:  y_i = bf16(z_i)                         [N]
+ *   CLOVER_FP4_SWIGLU: y_i = bf16(silu(z_i[0..N/2)) * z_i[N/2..N))  [N / 2]
+ * a_codes [n_rows][K / 2] with a_scales as clover_quantize_fp4_rows writes
+ * them for offsets (int32 [n_groups + 1], device). offsets NULL: all rows
+ * form one group, the layout clover_quantize_fp4 gives one matrix too.
+ * b_codes [n_groups][N][K / 2]; b_scales as clover_quantize_fp4 writes them
+ * for n_groups matrices of N rows, or, with SwiGLU, for 2 n_groups matrices
+ * of N / 2 rows (each group's gate rows, then its up rows: the codes lie the
+ * same way). group_alpha: fp32 [n_groups] or NULL. y: bf16, 16-byte aligned;
+ * rows outside every group are left as they were. K % 64 == 0, 64 <= K <=
+ * 2^20; 1 <= N <= 2^24 (even with SwiGLU); offsets outside [0, n_rows] count
+ * as the nearer end. A NaN scale makes its row's (or its column's) results
+ * NaN. Results do not depend on the other rows of the call. */
+int clover_fp4_product(int32_t format, const uint8_t* a_codes, const uint8_t* a_scales, int32_t n_rows,
+                       const uint8_t* b_codes, const uint8_t* b_scales, const int32_t* offsets,
+                       int32_t n_groups, int32_t N, int32_t K, float alpha, const float* group_alpha,
+                       int32_t epilogue, uint16_t* y, void* workspace, size_t workspace_bytes,
+                       clover_stream_t stream);
 
 /* Weighted sum of expert rows, and what a sublayer adds to it:
  *   x_out[t] = x[t] + sum_k w[t][k] * y[pos[t][k]] + shared[t]

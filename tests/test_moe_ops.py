@@ -221,3 +221,29 @@ def test_oracle_route_by_hand():
     assert r["idx"].tolist() == [[2, 3]]
     r = R.route(z, 2, score="sigmoid", n_groups=2, top_groups=1, group_rank=1)
     assert r["idx"].tolist() == [[0, 1]]
+
+
+PRODUCT = dict(fmt=0, a=0x10000, sa=0x20000, n_rows=10, b=0x30000, sb=0x40000, offsets=0x50000, groups=4, N=64, K=256,
+               alpha=1.0, group_alpha=None, epilogue=0, y=0x60000, ws=0x100000, nbytes=256, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(fmt=2), C.ERR_INVALID_ARG), (dict(K=96), C.ERR_UNSUPPORTED_SHAPE), (dict(K=0), C.ERR_UNSUPPORTED_SHAPE),
+    (dict(N=0), C.ERR_UNSUPPORTED_SHAPE), (dict(N=63, epilogue=1), C.ERR_UNSUPPORTED_SHAPE),
+    (dict(N=(1 << 24) + 1), C.ERR_UNSUPPORTED_SHAPE), (dict(epilogue=2), C.ERR_INVALID_ARG),
+    (dict(groups=0), C.ERR_UNSUPPORTED_SHAPE), (dict(groups=513), C.ERR_UNSUPPORTED_SHAPE),
+    (dict(n_rows=-1), C.ERR_UNSUPPORTED_SHAPE), (dict(n_rows=(1 << 29) + 1), C.ERR_UNSUPPORTED_SHAPE),
+    (dict(offsets=None), C.ERR_INVALID_ARG), (dict(offsets=0x50002), C.ERR_INVALID_ARG),
+    (dict(a=None), C.ERR_INVALID_ARG), (dict(sa=0x20008), C.ERR_INVALID_ARG), (dict(b=0x30004), C.ERR_INVALID_ARG),
+    (dict(sb=None), C.ERR_INVALID_ARG), (dict(y=None), C.ERR_INVALID_ARG), (dict(y=0x60008), C.ERR_INVALID_ARG),
+    (dict(group_alpha=0x70001), C.ERR_INVALID_ARG), (dict(ws=None), C.ERR_INVALID_ARG),
+    (dict(ws=0x100010), C.ERR_INVALID_ARG), (dict(nbytes=255), C.ERR_WORKSPACE_TOO_SMALL),
+])
+def test_product_arguments_refused(lib, kw, code):
+    assert lib.clover_fp4_product(*dict(PRODUCT, **kw).values()) == code
+    assert C.last_error()
+
+
+def test_product_nothing_to_do(lib):
+    assert lib.clover_fp4_product_workspace_bytes() == 256
+    assert lib.clover_fp4_product(*dict(PRODUCT, n_rows=0, a=None, b=None, y=None).values()) == C.OK
