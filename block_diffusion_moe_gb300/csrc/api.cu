@@ -884,15 +884,17 @@ namespace clover {
 // clover_last_error().
 int set_last_error(int code, const char* msg) { return fail(code, "%s", msg); }
 
-int encode_code_boxes(void* tensor_map, const void* base, uint64_t n, uint64_t rows, uint64_t row_bytes,
-                      uint32_t box_rows, const char* what) {
+int encode_byte_boxes(void* tensor_map, const void* base, uint64_t n, uint64_t rows, uint64_t row_bytes,
+                      uint32_t box_bytes, uint32_t box_rows, uint32_t box_n, bool codes, const char* what) {
   int rc;
   if ((rc = get_encoder())) return rc;
-  const cuuint64_t dims[3] = {row_bytes, rows, n};
+  const uint32_t size = codes ? 1 : 8;
+  const cuuint64_t dims[3] = {row_bytes / size, rows, n};
   const cuuint64_t strides[2] = {row_bytes, rows * row_bytes};
-  const cuuint32_t box[3] = {128, box_rows, 1};
-  return encode_nd(static_cast<CUtensorMap*>(tensor_map), CU_TENSOR_MAP_DATA_TYPE_UINT8, base, n == 0 ? 2 : 3, dims,
-                   strides, box, CU_TENSOR_MAP_SWIZZLE_128B, what);
+  const cuuint32_t box[3] = {box_bytes / size, box_rows, box_n};
+  return encode_nd(static_cast<CUtensorMap*>(tensor_map),
+                   codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT64, base, n == 0 ? 2 : 3, dims,
+                   strides, box, codes ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, what);
 }
 
 int device_sms(int* sms) {

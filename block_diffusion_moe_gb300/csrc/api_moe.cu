@@ -303,12 +303,17 @@ int clover_fp4_product(int32_t format, const uint8_t* a_codes, const uint8_t* a_
   Fp4ProductArgs a;
   memset(&a, 0, sizeof(a));
   a.b_rows = swiglu ? N / 2 : N;
-  if ((rc = encode_code_boxes(&a.tm_a, a_codes, 0, n_rows, K / 2, 32, "rows' codes"))) return rc;
-  if ((rc = encode_code_boxes(&a.tm_b, b_codes, static_cast<uint64_t>(n_groups) * (swiglu ? 2 : 1), a.b_rows, K / 2, 128,
-                              "matrices' codes")))
+  const uint64_t mats = static_cast<uint64_t>(n_groups) * (swiglu ? 2 : 1);
+  const uint32_t box_rows = swiglu ? 128 : 256, box_mats = swiglu ? 2 : 1;
+  if ((rc = encode_byte_boxes(&a.tm_a, a_codes, 0, n_rows, K / 2, 128, 128, 1, true, "rows' codes")) ||
+      (rc = encode_byte_boxes(&a.tm_a32, a_codes, 0, n_rows, K / 2, 128, 32, 1, true, "rows' codes")) ||
+      (rc = encode_byte_boxes(&a.tm_b, b_codes, mats, a.b_rows, K / 2, 128, box_rows, box_mats, true,
+                              "matrices' codes")) ||
+      (rc = encode_byte_boxes(&a.tm_b_sf, b_scales, mats, (a.b_rows + 127) / 128, scale_tile_bytes(format, K),
+                              256 / (4 * fp4_block(format)) * 512, box_rows / 128, box_mats, false,
+                              "matrices' scales")))
     return rc;
   a.a_scales = a_scales;
-  a.b_scales = b_scales;
   a.offsets = offsets;
   a.group_alpha = group_alpha;
   a.alpha = alpha;

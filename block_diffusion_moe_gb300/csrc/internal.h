@@ -16,11 +16,12 @@ int set_last_error(int code, const char* msg);
 // Checks a caller's workspace: not NULL, 256-byte aligned, at least `need` bytes.
 int check_workspace(void* workspace, size_t have, size_t need);
 
-// Encodes the TMA view of a matrix stack of bytes [n][rows][row_bytes] (rows
-// contiguous): boxes of 128 bytes x box_rows x 1 with 128-byte swizzle, zeros
-// outside. A rank-2 view (no stack) where n is 0.
-int encode_code_boxes(void* tensor_map, const void* base, uint64_t n, uint64_t rows, uint64_t row_bytes,
-                      uint32_t box_rows, const char* what);
+// Encodes the TMA view of stacked rows of bytes [n][rows][row_bytes]
+// (contiguous; rank 2 where n is 0): boxes of box_bytes x box_rows x box_n,
+// zeros outside. Codes: 128-byte boxes in the 128-byte swizzle. Scale tiles:
+// 8-byte elements, no swizzle.
+int encode_byte_boxes(void* tensor_map, const void* base, uint64_t n, uint64_t rows, uint64_t row_bytes,
+                      uint32_t box_bytes, uint32_t box_rows, uint32_t box_n, bool codes, const char* what);
 
 // Number of SMs of the current device.
 int device_sms(int* sms);

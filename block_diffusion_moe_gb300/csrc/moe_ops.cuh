@@ -83,10 +83,11 @@ constexpr int kFp4MaxGroups = 512;
 
 // Grouped product of 4-bit rows (csrc/product.cu).
 struct Fp4ProductArgs {
-  CUtensorMap tm_a;          // codes [n_rows][K / 2], boxes of 128 bytes x 32 rows
-  CUtensorMap tm_b;          // codes [mats][rows of a matrix][K / 2], boxes of 128 bytes x 128 rows x 1
+  CUtensorMap tm_a;          // codes [n_rows][K / 2], boxes of 128 bytes x 128 rows
+  CUtensorMap tm_a32;        // the same in boxes of 32 rows
+  CUtensorMap tm_b;          // codes [mats][b_rows][K / 2], boxes of 128 bytes x 256 rows x 1 (SwiGLU: 128 x 2)
+  CUtensorMap tm_b_sf;       // scale tiles [mats][b_rows / 128][..], boxes of a stage's tiles x 2 x 1 (SwiGLU: 1 x 2)
   const uint8_t* a_scales;   // tiles of 128 rows
-  const uint8_t* b_scales;
   const int32_t* offsets;    // [n_groups + 1] or null (one group of all rows)
   const float* group_alpha;  // [n_groups] or null
   float alpha;

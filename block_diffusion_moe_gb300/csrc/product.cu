@@ -89,44 +89,59 @@ __device__ __forceinline__ Tile tile_at(const Fp4ProductArgs& p, const Shared& s
   return r;
 }
 
+// The whole warp waits, so that its control flow stays uniform (the elected
+// lane's instructions need the warp converged). False: give up.
+__device__ __forceinline__ bool warp_wait(const Fp4ProductArgs& p, Shared* sh, uint64_t* bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, mbar_wait(bar, parity, &sh->abort))) return true;
+  if (elect_one()) give_up(p, sh);
+  __syncwarp();
+  return false;
+}
+
+// Run by the whole warp; one elected lane issues. The rate of an SM's copies
+// follows their number more than their size, so a stage of a full tile is four:
+// A codes, A scales, both halves of B's codes, both halves of B's scales.
 template <bool kMx, bool kSwiglu>
 __device__ void producer(const Fp4ProductArgs& p, Shared* sh, uint8_t* ring, int64_t n_all, int n_tiles) {
-  volatile uint32_t* abort = &sh->abort;
-  constexpr int kChunk = kMx ? 128 : 64;  // K elements per scale tile
+  constexpr int kChunk = kMx ? 128 : 64;       // K elements per scale tile
+  constexpr int kChunks = kStageK / kChunk;    // scale tiles of a stage
   const uint64_t pol = l2_policy_evict_last();  // row tiles share B tiles, column tiles share A tiles
+  const uint32_t ring0 = smem_u32(ring);
   const int nk = (p.K + kStageK - 1) / kStageK;
   const int chunks = (p.K + kChunk - 1) / kChunk;
-  const int b_tiles = (p.b_rows + 127) / 128;
   int st = 0;
   uint32_t ph = 0, issued = 0, parity_bits = 0;
   bool ok = true;
   for (int64_t t = blockIdx.x; t < n_all && ok; t += gridDim.x) {
     const Tile tl = tile_at(p, *sh, t, n_tiles, kSwiglu ? 128 : 256);
-    const int boxes = (tl.rows + 31) / 32;
-    // the two halves of the B tile: gate and up rows, or consecutive rows
-    // (the second may lie past the matrix: its columns are never stored)
-    const int halves = (kSwiglu || tl.n0 + 128 < p.b_rows) ? 2 : 1;
+    // a tile with few rows copies only the 32-row boxes that hold some; what
+    // the others leave in shared memory reaches only accumulator rows that
+    // nobody stores
+    const int boxes = tl.rows > 96 ? 0 : (tl.rows + 31) / 32;
+    const uint32_t a_bytes = boxes == 0 ? kABytes : boxes * 4096;
+    const uint8_t* a_sf = p.a_scales + tl.sf_tile * chunks * 512;
+    // SwiGLU: rows n0 .. n0 + 127 of the group's gate and up matrices; else
+    // rows n0 .. n0 + 255 of its matrix. Past the matrix: zeros.
+    const int mat = kSwiglu ? 2 * tl.g : tl.g;
     for (int k = 0; k < nk; ++k) {
-      if (!mbar_wait(&sh->empty[st], ph ^ 1u, abort)) {
-        give_up(p, sh);
+      if (!warp_wait(p, sh, &sh->empty[st], ph ^ 1u)) {
         ok = false;
         break;
       }
-      const int c0 = k * (kStageK / kChunk);
-      const int nc = min(kStageK / kChunk, chunks - c0);
-      uint64_t* bar = &sh->full[st];
-      const uint32_t base = smem_u32(ring + static_cast<size_t>(st) * kStageBytes);
-      mbar_arrive_expect_tx(bar, boxes * 4096 + halves * (kBBytes / 2) + (1 + halves) * nc * 512);
-      for (int b = 0; b < boxes; ++b) tma_load_2d(base + b * 4096, &p.tm_a, bar, k * 128, tl.row0 + b * 32, pol);
-      const uint32_t sfa = base + kABytes + kBBytes, sfb = sfa + kSfABytes;
-      bulk_load(sfa, p.a_scales + (tl.sf_tile * chunks + c0) * 512, nc * 512, bar);
-      for (int h = 0; h < halves; ++h) {
-        const int mat = kSwiglu ? 2 * tl.g + h : tl.g;
-        const int row = kSwiglu ? tl.n0 : tl.n0 + h * 128;
-        tma_load_3d(base + kABytes + h * (kBBytes / 2), &p.tm_b, bar, k * 128, row, mat, pol);
-        bulk_load(sfb + h * kMaxChunks * 512,
-                  p.b_scales + ((static_cast<int64_t>(mat) * b_tiles + row / 128) * chunks + c0) * 512, nc * 512, bar);
+      if (elect_one()) {
+        const int nc = min(kChunks, chunks - k * kChunks);
+        uint64_t* bar = &sh->full[st];
+        const uint32_t base = ring0 + static_cast<uint32_t>(st) * kStageBytes;
+        mbar_arrive_expect_tx(bar, a_bytes + kBBytes + nc * 512 + 2 * kChunks * 512);
+        if (boxes == 0)
+          tma_load_2d(base, &p.tm_a, bar, k * 128, tl.row0, pol);
+        else
+          for (int b = 0; b < boxes; ++b) tma_load_2d(base + b * 4096, &p.tm_a32, bar, k * 128, tl.row0 + b * 32, pol);
+        tma_load_3d(base + kABytes, &p.tm_b, bar, k * 128, tl.n0, mat, pol);
+        bulk_load(base + kABytes + kBBytes, a_sf + static_cast<int64_t>(k) * kChunks * 512, nc * 512, bar);
+        tma_load_3d(base + kABytes + kBBytes + kSfABytes, &p.tm_b_sf, bar, k * kChunks * 64, tl.n0 / 128, mat, pol);
       }
+      __syncwarp();
       issued |= 1u << st;
       parity_bits = (parity_bits & ~(1u << st)) | (ph << st);
       if (++st == kStages) {
@@ -135,18 +150,40 @@ __device__ void producer(const Fp4ProductArgs& p, Shared* sh, uint8_t* ring, int
       }
     }
   }
-  if (*abort) {  // the copies in flight must land before the CTA leaves
+  if (*reinterpret_cast<volatile uint32_t*>(&sh->abort)) {  // the copies in flight must land before the CTA leaves
     for (int i = 0; i < kStages; ++i)
       if (issued & (1u << i)) mbar_wait_for(&sh->full[i], (parity_bits >> i) & 1u, 200000000ull);
   }
 }
 
+// One stage: its scale tiles to tensor memory, then its MMAs (kSteps of 64 K
+// elements), issued by the calling thread.
+template <bool kMx, int kSteps>
+__device__ __forceinline__ void issue_stage(uint32_t base, uint32_t tmem, uint32_t d, uint32_t accumulate) {
+  constexpr int kPerTile = kMx ? 2 : 1;  // MMAs per scale tile
+  const uint32_t sfa = base + kABytes + kBBytes, sfb = sfa + kSfABytes;
+#pragma unroll
+  for (int c = 0; c < (kSteps + kPerTile - 1) / kPerTile; ++c) {
+    tmem_copy_scales(tmem + kTmemSfA + c * 4, sfa + c * 512);
+    tmem_copy_scales(tmem + kTmemSfB + c * 8, sfb + c * 512);
+    tmem_copy_scales(tmem + kTmemSfB + c * 8 + 4, sfb + (kStageK / (64 * kPerTile) + c) * 512);
+  }
+  const uint64_t ad = umma_desc_sw128(base), bd = umma_desc_sw128(base + kABytes);
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int c = s / kPerTile;
+    umma_fp4<kMx>(d, ad + 2 * s, bd + 2 * s, umma_idesc_fp4(kTileM, kTileN, kMx, kMx ? (s & 1) * 2 : 0),
+                  tmem + kTmemSfA + c * 4, tmem + kTmemSfB + c * 8, s == 0 ? accumulate : 1u);
+  }
+}
+
+// Run by the whole warp with uniform control flow; one elected lane issues.
 template <bool kMx>
 __device__ void mma_issuer(const Fp4ProductArgs& p, Shared* sh, uint8_t* ring, int64_t n_all) {
-  volatile uint32_t* abort = &sh->abort;
   const uint32_t tmem = sh->tmem;
-  constexpr int kChunk = kMx ? 128 : 64;
+  const uint32_t ring0 = smem_u32(ring);
   const int nk = (p.K + kStageK - 1) / kStageK;
+  const int last = (p.K - (nk - 1) * kStageK) / 64;  // MMAs of the last stage, 1 to 4
   int st = 0, it = 0;
   uint32_t ph = 0;
   bool ok = true;
@@ -154,43 +191,39 @@ __device__ void mma_issuer(const Fp4ProductArgs& p, Shared* sh, uint8_t* ring, i
     // the columns shared with the previous tile's accumulator are free once
     // that one's epilogue has drained them, and it drained the tile before
     // that first
-    if (it > 0 && !mbar_wait(&sh->acc_shared, (it - 1) & 1, abort)) {
-      give_up(p, sh);
-      break;
-    }
+    if (it > 0 && !warp_wait(p, sh, &sh->acc_shared, (it - 1) & 1)) break;
     tc_fence_after();
     const uint32_t d = tmem + (it & 1 ? kAcc1 : 0u);
     for (int k = 0; k < nk; ++k) {
-      if (!mbar_wait(&sh->full[st], ph, abort)) {
-        give_up(p, sh);
+      if (!warp_wait(p, sh, &sh->full[st], ph)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t base = smem_u32(ring + static_cast<size_t>(st) * kStageBytes);
-      const uint32_t sfa = base + kABytes + kBBytes, sfb = sfa + kSfABytes;
-      const int steps = min(kStageK / 64, p.K / 64 - k * (kStageK / 64));
-      const int nc = kMx ? (steps + 1) / 2 : steps;
-      for (int c = 0; c < nc; ++c) {
-        tmem_copy_scales(tmem + kTmemSfA + c * 4, sfa + c * 512);
-        tmem_copy_scales(tmem + kTmemSfB + c * 8, sfb + c * 512);
-        tmem_copy_scales(tmem + kTmemSfB + c * 8 + 4, sfb + (kMaxChunks + c) * 512);
+      const uint32_t base = ring0 + static_cast<uint32_t>(st) * kStageBytes;
+      const uint32_t acc = k != 0 ? 1u : 0u;
+      if (elect_one()) {
+        if (k + 1 < nk || last == 4) {
+          issue_stage<kMx, 4>(base, tmem, d, acc);
+        } else if (last == 3) {
+          issue_stage<kMx, 3>(base, tmem, d, acc);
+        } else if (last == 2) {
+          issue_stage<kMx, 2>(base, tmem, d, acc);
+        } else {
+          issue_stage<kMx, 1>(base, tmem, d, acc);
+        }
+        umma_commit(&sh->empty[st]);
+        if (k + 1 == nk) umma_commit(&sh->acc_full);
       }
-      const uint64_t ad = umma_desc_sw128(base), bd = umma_desc_sw128(base + kABytes);
-      for (int s = 0; s < steps; ++s) {
-        const int c = s * 64 / kChunk;
-        umma_fp4<kMx>(d, ad + 2 * s, bd + 2 * s, umma_idesc_fp4(kTileM, kTileN, kMx, kMx ? (s & 1) * 2 : 0),
-                      tmem + kTmemSfA + c * 4, tmem + kTmemSfB + c * 8, (k | s) != 0 ? 1u : 0u);
-      }
-      umma_commit(&sh->empty[st]);
+      __syncwarp();
       if (++st == kStages) {
         st = 0;
         ph ^= 1u;
       }
     }
-    if (ok) umma_commit(&sh->acc_full);
   }
-  umma_commit(&sh->drain);
+  if (elect_one()) umma_commit(&sh->drain);
+  __syncwarp();
   mbar_wait_for(&sh->drain, 0, 200000000ull);
 }
 
@@ -216,18 +249,12 @@ __device__ __forceinline__ void store32(__nv_bfloat16* row, int c0, int width, b
 
 template <bool kSwiglu>
 __device__ void epilogue(const Fp4ProductArgs& p, Shared* sh, int64_t n_all, int n_tiles) {
-  volatile uint32_t* abort = &sh->abort;
   const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const bool vec = p.b_rows % 8 == 0;  // rows of y 16-byte aligned
   int it = 0;
   for (int64_t t = blockIdx.x; t < n_all; t += gridDim.x, ++it) {
     const Tile tl = tile_at(p, *sh, t, n_tiles, kSwiglu ? 128 : 256);
-    int good = 1;
-    if (lane == 0 && !mbar_wait(&sh->acc_full, it & 1, abort)) {
-      give_up(p, sh);
-      good = 0;
-    }
-    if (!__shfl_sync(0xffffffffu, good, 0)) return;
+    if (!warp_wait(p, sh, &sh->acc_full, it & 1)) return;
     tc_fence_after();
     const bool odd = it & 1;
     const uint32_t acc = sh->tmem + (static_cast<uint32_t>(q * 32) << 16) + (odd ? kAcc1 : 0u);
@@ -274,7 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_product(const __grid_consta
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&p.tm_a);
+    tma_prefetch_desc(&p.tm_a32);
     tma_prefetch_desc(&p.tm_b);
+    tma_prefetch_desc(&p.tm_b_sf);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sh->full[i], 1);
       mbar_init(&sh->empty[i], 1);
@@ -316,9 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_product(const __grid_consta
   const int n_tiles = (p.b_rows + step - 1) / step;
   const int64_t n_all = static_cast<int64_t>(m_tiles) * n_tiles;
   if (warp == 0) {
-    if ((threadIdx.x & 31) == 0) producer<kMx, kSwiglu>(p, sh, ring, n_all, n_tiles);
+    producer<kMx, kSwiglu>(p, sh, ring, n_all, n_tiles);
   } else if (warp == 1) {
-    if ((threadIdx.x & 31) == 0) mma_issuer<kMx>(p, sh, ring, n_all);
+    mma_issuer<kMx>(p, sh, ring, n_all);
   } else if (warp >= 4) {
     epilogue<kSwiglu>(p, sh, n_all, n_tiles);
   }
