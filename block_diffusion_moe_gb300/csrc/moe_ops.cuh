@@ -33,6 +33,8 @@ struct RouteOpArgs {
   int32_t* totals;   // [E] (workspace)
   int cta_tokens;    // tokens per CTA, a multiple of 8, at most kRouteOpCtaTokens
   int n_ctas;
+  int vec;          // set by the launch: whole vectors of logits per lane
+  int group_lanes;  // set by the launch: lanes that hold one expert group, or 0
 };
 
 // CTAs and tokens per CTA of the selection kernel for M >= 1 tokens.

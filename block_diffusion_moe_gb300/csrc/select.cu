@@ -13,151 +13,294 @@ namespace {
 
 constexpr int kThreads = 256;  // 8 warps, one token each at a time
 constexpr int kWarps = kThreads / 32;
+constexpr uint32_t kAll = 0xffffffffu;
+// Largest K + 1 that is selected by counting (select_token): beyond it the
+// keys above the bound no longer fit 32 lanes as a rule.
+constexpr int kCountedMax = 17;
+constexpr int kListBytes = 384;  // a warp's list of 32 keys and ids, and their order
 
-__device__ __forceinline__ float load_logit(const RouteOpArgs& a, int64_t row, int e) {
-  float v = a.bf16_logits
-                ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[row + e])
-                : static_cast<const float*>(a.logits)[row + e];
-  // +inf counts as the largest finite value, -0 as 0; NaN stays NaN
-  return (v > 3.402823466e+38f ? 3.402823466e+38f : v) + 0.0f;
+__device__ __forceinline__ float clean_logit(float v) {
+  // +inf counts as the largest finite value, NaN as -inf, -0 as 0
+  return fmaxf(fminf(v, 3.402823466e+38f), -INFINITY) + 0.0f;
 }
 
-// The token's logits, expert lane + 32 i in slot i; -inf for NaN and past E.
+__device__ __forceinline__ float load_logit(const RouteOpArgs& a, int64_t row, int e) {
+  const float v = a.bf16_logits ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[row + e])
+                                : static_cast<const float*>(a.logits)[row + e];
+  return v != v ? -INFINITY : clean_logit(v);
+}
+
+// The token's logits: expert lane * VPL + i in slot i (so that a lower lane
+// holds lower ids), -inf past E. One vector per lane where the rows allow it
+// (a.vec: E % VPL == 0 and every lane's part aligned to its size or 16 bytes).
 template <int VPL>
 __device__ __forceinline__ void load_row(const RouteOpArgs& a, int64_t row, int lane, float (&x)[VPL]) {
+  const int e0 = lane * VPL;
+  if (a.vec) {
+    uint32_t wd[VPL];  // the lane's part
+    const int words = a.bf16_logits ? VPL / 2 : VPL;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 32 * i;
-    const float v = e < a.E ? load_logit(a, row, e) : -INFINITY;
-    x[i] = v > -INFINITY ? v : -INFINITY;
+    for (int i = 0; i < VPL; ++i) wd[i] = a.bf16_logits ? 0xFF80FF80u : 0xFF800000u;  // -inf
+    if (e0 < a.E) {
+      const uint8_t* p = static_cast<const uint8_t*>(a.logits) + (row + e0) * (a.bf16_logits ? 2 : 4);
+      if (VPL >= 4 && words >= 4) {
+#pragma unroll
+        for (int v = 0; v < VPL / 4; ++v)
+          if (4 * v < words) {
+            const uint4 u = *reinterpret_cast<const uint4*>(p + 16 * v);
+            wd[4 * v] = u.x, wd[4 * v + 1] = u.y, wd[4 * v + 2] = u.z, wd[4 * v + 3] = u.w;
+          }
+      } else if (words == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        wd[0] = u.x, wd[1] = u.y;
+      } else {
+        wd[0] = *reinterpret_cast<const uint32_t*>(p);
+      }
+    }
+    if (a.bf16_logits) {
+#pragma unroll
+      for (int i = VPL - 1; i >= 0; --i)
+        x[i] = __uint_as_float(i % 2 == 0 ? wd[i / 2] << 16 : wd[i / 2] & 0xFFFF0000u);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) x[i] = __uint_as_float(wd[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) x[i] = x[i] != x[i] ? -INFINITY : clean_logit(x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) x[i] = e0 + i < a.E ? load_logit(a, row, e0 + i) : -INFINITY;
   }
 }
 
-__device__ __forceinline__ double warp_max_d(double v) {
+// This lane's biases (0 without any, and past E).
+template <int VPL>
+__device__ __forceinline__ void load_bias(const RouteOpArgs& a, int lane, float (&b)[VPL]) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int i = 0; i < VPL; ++i) b[i] = (a.bias != nullptr && lane * VPL + i < a.E) ? a.bias[lane * VPL + i] : 0.f;
+}
+
+// Warp-wide maximum of any floats but NaN, by one reduction over keys whose
+// signed order is the floats' order.
+__device__ __forceinline__ float warp_max_fast(float v) {
+  const int b = __float_as_int(v);
+  const int m = __reduce_max_sync(kAll, b ^ ((b >> 31) & 0x7fffffff));
+  return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
+}
+__device__ __forceinline__ double warp_max_fast(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(kAll, v, o));
   return v;
 }
-__device__ __forceinline__ double warp_sum_d(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-__device__ __forceinline__ float warp_max_t(float v) { return warp_max_f(v); }
-__device__ __forceinline__ double warp_max_t(double v) { return warp_max_d(v); }
 __device__ __forceinline__ float warp_sum_t(float v) { return warp_sum_f(v); }
-__device__ __forceinline__ double warp_sum_t(double v) { return warp_sum_d(v); }
+__device__ __forceinline__ double warp_sum_t(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
 __device__ __forceinline__ float exp_t(float v) { return expf(v); }
 __device__ __forceinline__ double exp_t(double v) { return exp(v); }
+__device__ __forceinline__ float sigmoid_t(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+__device__ __forceinline__ double sigmoid_t(double v) { return 1.0 / (1.0 + exp(-v)); }
 
-// One token's selection by one warp, in T. Expert lane + 32 i sits in slot i;
-// x holds the logits, -inf where the expert is not live. Lane k < K returns
-// the k-th selected expert (-1: none left).
+// (b1, b2): the two largest of a set, kept up to date with v
+template <typename T>
+__device__ __forceinline__ void two_best(T& b1, T& b2, T v) {
+  b2 = fmax(b2, fmin(b1, v));
+  b1 = fmax(b1, v);
+}
+
+// One token's selection by one warp, in T: lane k < K returns the k-th
+// selected expert (-1: none left). x holds the logits, -inf where the expert
+// is not live. smem: the warp's scratch.
 //
 // In float, *unsure is set where the order could be another one in exact
 // arithmetic: two keys (or the ranks on either side of the group border)
-// closer than twice the largest error a key can have. A score's error is
-// below 2^-19 of the largest score (exp and quotient a few roundings each, the
-// softmax's sum up to 21), the sum with the bias adds half a unit of the key.
-// Logits used as keys are exact. The caller then repeats the token in double, whose order is the
-// definition's.
+// closer than the errors they can have. A score's error is below 2^-19 of the
+// largest score (softmax: exp and quotient a few roundings each, the sum up to
+// 21; sigmoid: the fast exp's error grows with -logit, a multiple of 2^-22 of
+// it, which s * -logit bounds by that of the largest score), the sum with the
+// bias adds half a unit of the key. Logits used as keys are exact. The caller
+// then repeats the token in double, whose order is the definition's.
+//
+// The K largest of E by counting rather than by K rounds over all of them:
+// the (K + 1)-th largest of the 32 lanes' maxima is a lower bound of the
+// (K + 1)-th largest key, the few keys at or above it (usually K + 1 to K + 4)
+// are listed in shared memory, one per lane, and each lane counts how many come
+// before its own. Where more than 32 qualify (ties; large K), K rounds.
 template <int VPL, typename T>
-__device__ __forceinline__ int select_token(const RouteOpArgs& a, const float (&x)[VPL], T* s_keys, int lane,
-                                            bool* unsure) {
+__device__ __forceinline__ int select_token(const RouteOpArgs& a, int64_t row, const float (&x)[VPL],
+                                            const float (&bias)[VPL], double* smem, int lane, bool* unsure) {
   constexpr bool kExact = sizeof(T) == 8;
   const T ninf = -static_cast<T>(INFINITY);
   const bool need_scores = a.bias != nullptr || (a.n_groups > 1 && a.group_rank == 2);
-  T key[VPL];   // what experts are ordered by
-  T total[VPL]; // score + bias, what group ranks sum
-  T err = 0;    // bound on the error of a key or half a rank
+  T key[VPL];    // what experts are ordered by
+  T total[VPL];  // score + bias, what group ranks sum
+  T err = 0;     // bound on the error of a key or half a rank
   if (need_scores) {
-    T m = ninf;
-    if (a.softmax) {
+    float xm = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) m = fmax(m, static_cast<T>(x[i]));
-      m = warp_max_t(m);
+    for (int i = 0; i < VPL; ++i) xm = fmaxf(xm, x[i]);
+    xm = warp_max_fast(xm);
+    T s_max;
+    if (a.softmax) {
       T sum = 0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        total[i] = x[i] > -INFINITY ? exp_t(static_cast<T>(x[i]) - m) : static_cast<T>(0);
+        total[i] = x[i] > -INFINITY ? exp_t(static_cast<T>(x[i]) - static_cast<T>(xm)) : static_cast<T>(0);
         sum += total[i];
       }
       sum = warp_sum_t(sum);
       const T inv = static_cast<T>(1) / sum;  // sum >= 1 where any expert is live
 #pragma unroll
       for (int i = 0; i < VPL; ++i) total[i] = kExact ? total[i] / sum : total[i] * inv;
+      s_max = inv;
     } else {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        total[i] = static_cast<T>(1) / (static_cast<T>(1) + exp_t(-static_cast<T>(x[i])));
+      for (int i = 0; i < VPL; ++i) total[i] = sigmoid_t(static_cast<T>(x[i]));
+      s_max = sigmoid_t(static_cast<T>(xm)) * (1 + static_cast<T>(fmaxf(-xm, 0.f)) * static_cast<T>(0.25));
     }
-    T s_max = 0, k_max = 0;
+    T k_max = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 32 * i;
-      const bool on = x[i] > -INFINITY;
-      if (!kExact && on) s_max = fmax(s_max, total[i]);
-      const float b = (a.bias != nullptr && e < a.E) ? a.bias[e] : 0.f;
-      const bool live = on && b > -INFINITY;  // false for NaN too
-      total[i] = live ? total[i] + static_cast<T>(b) : ninf;
+      const bool live = x[i] > -INFINITY && bias[i] > -INFINITY;  // false for NaN too
+      total[i] = live ? total[i] + static_cast<T>(bias[i]) : ninf;
       if (!kExact && live) k_max = fmax(k_max, fabs(total[i]));
     }
-    if (!kExact) err = warp_max_t(s_max) * static_cast<T>(1.9e-6) + warp_max_t(k_max) * static_cast<T>(1.2e-7) + static_cast<T>(1e-37);
+    if (!kExact)
+      err = s_max * static_cast<T>(1.9e-6) + warp_max_fast(k_max) * static_cast<T>(1.2e-7) + static_cast<T>(1e-37);
   }
 #pragma unroll
   for (int i = 0; i < VPL; ++i) key[i] = a.bias != nullptr ? total[i] : static_cast<T>(x[i]);
   bool doubt = false;
 
   if (a.n_groups > 1) {
-    // keys in shared memory, one lane per group
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (lane + 32 * i < a.E) s_keys[lane + 32 * i] = a.group_rank == 2 ? total[i] : key[i];
-    __syncwarp();
     const int size = a.E / a.n_groups;
     T b1 = ninf, b2 = ninf;
-    if (lane < a.n_groups) {
-      int j = lane % size;  // each lane starts elsewhere in its group: other banks
-      for (int n = 0; n < size; ++n) {
-        const T v = s_keys[lane * size + j];
-        if (v > b1) {
-          b2 = b1;
-          b1 = v;
-        } else if (v > b2) {
-          b2 = v;
-        }
-        if (++j == size) j = 0;
+    int g, step;  // this lane's group; lanes from one group to the next
+    bool first;   // one lane per group speaks for it
+    if (a.group_lanes > 0) {
+      // a group is VPL slots of a power of two of neighbouring lanes
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) two_best(b1, b2, a.group_rank == 2 ? total[i] : key[i]);
+      for (int o = 1; o < a.group_lanes; o <<= 1) {
+        const T c1 = __shfl_xor_sync(kAll, b1, o), c2 = __shfl_xor_sync(kAll, b2, o);
+        two_best(b1, b2, c1);
+        b2 = fmax(b2, c2);
       }
+      step = a.group_lanes;
+      g = lane / step;
+      first = lane % step == 0 && g < a.n_groups;
+    } else {
+      // any other size: keys in shared memory, lane g scans group g
+      T* s_keys = reinterpret_cast<T*>(smem);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (lane * VPL + i < a.E) s_keys[lane * VPL + i] = a.group_rank == 2 ? total[i] : key[i];
+      __syncwarp();
+      step = 1;
+      g = lane;
+      first = lane < a.n_groups;
+      if (first)
+        for (int n = 0; n < size; ++n) two_best(b1, b2, s_keys[lane * size + n]);
+      __syncwarp();
     }
-    __syncwarp();
     const T rank = (a.group_rank == 2 && b2 > ninf) ? b1 + b2 : b1;
     int before = 0;
-    for (int g = 0; g < a.n_groups; ++g) {
-      const T r = __shfl_sync(0xffffffffu, rank, g);
-      before += (r > rank || (r == rank && g < lane)) ? 1 : 0;
+    for (int j = 0; j < a.n_groups; ++j) {
+      const T r = __shfl_sync(kAll, rank, j * step);
+      before += (r > rank || (r == rank && j < g)) ? 1 : 0;
     }
-    const bool stays = lane < a.n_groups && before < a.top_groups;
-    const uint32_t mask = __ballot_sync(0xffffffffu, stays);
+    const bool stays = before < a.top_groups;
+    const uint32_t mask = __ballot_sync(kAll, first && stays);  // bit g * step
     if (!kExact && err > 0) {
-      const T low = -warp_max_t(stays ? -rank : ninf);
-      const T high = warp_max_t(lane < a.n_groups && !stays ? rank : ninf);
+      const T low = -warp_max_fast(first && stays ? -rank : ninf);
+      const T high = warp_max_fast(first && !stays ? rank : ninf);
       doubt = high > ninf && !(low - high > (a.group_rank == 2 ? 4 : 2) * err);
     }
+    if (a.group_lanes > 0) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 32 * i;
-      if (e < a.E && ((mask >> (e / size)) & 1u) == 0) key[i] = ninf;
+      for (int i = 0; i < VPL; ++i) key[i] = stays ? key[i] : ninf;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const int e = lane * VPL + i;
+        if (e < a.E && ((mask >> (e / size)) & 1u) == 0) key[i] = ninf;
+      }
     }
   }
 
-  // K rounds: the largest key, the lowest id holding it; one more round in
-  // float to see the key that just missed
+  // one more than K in float, to see the key that just missed
   const bool check = !kExact && a.bias != nullptr;
-  const int rounds = check ? a.K + 1 : a.K;
+  const int want = check ? a.K + 1 : a.K;
+  T best = key[0];
+#pragma unroll
+  for (int i = 1; i < VPL; ++i) best = fmax(best, key[i]);
   int mine = -1;
-  T last = 0, last_x = 0, last_b = 0;
-  for (int k = 0; k < rounds; ++k) {
-    T best = ninf;
+  if (!kExact && want <= kCountedMax) {
+    T m = best, bound = ninf;
+    for (int left = want; left > 0;) {
+      bound = warp_max_fast(m);
+      if (!(bound > ninf)) break;
+      const bool top = m == bound;
+      left -= __popc(__ballot_sync(kAll, top));
+      if (top) m = ninf;
+    }
+    int n = 0;
+    uint64_t* list = reinterpret_cast<uint64_t*>(smem);  // [32]: (id, key bits)
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const bool in = key[i] >= bound && key[i] > ninf;
+      const uint32_t votes = __ballot_sync(kAll, in);
+      if (votes == 0) continue;
+      const int at = n + __popc(votes & ((1u << lane) - 1u));
+      if (in && at < 32)
+        list[at] = (static_cast<uint64_t>(lane * VPL + i) << 32) | __float_as_uint(static_cast<float>(key[i]));
+      n += __popc(votes);
+    }
+    if (n <= 32) {
+      __syncwarp();
+      const uint64_t own = lane < n ? list[lane] : 0;
+      const float k0 = lane < n ? __uint_as_float(static_cast<uint32_t>(own)) : -INFINITY;
+      const int id = static_cast<int>(own >> 32);
+      int before = 0;
+      float next = -INFINITY;  // the largest key that comes after this one
+      int next_id = 0;
+      for (int j = 0; j < n; ++j) {
+        const uint64_t o = list[j];
+        const float kj = __uint_as_float(static_cast<uint32_t>(o));
+        const int ij = static_cast<int>(o >> 32);
+        const bool earlier = kj > k0 || (kj == k0 && ij < id);
+        before += earlier ? 1 : 0;
+        if (check && !earlier && j != lane && (kj > next || (kj == next && ij < next_id))) {
+          next = kj;
+          next_id = ij;
+        }
+      }
+      __syncwarp();
+      if (lane < n && check && before < a.K && next > -INFINITY && !(k0 - next > 2 * static_cast<float>(err))) {
+        // the same logit and bias give the same key: a real tie, by id
+        doubt |= !(load_logit(a, row, id) == load_logit(a, row, next_id) && a.bias[id] == a.bias[next_id]);
+      }
+      if (!kExact) *unsure = __any_sync(kAll, doubt);
+      // expert of rank r to lane r
+      int32_t* order = reinterpret_cast<int32_t*>(smem) + 64;
+      order[lane] = -1;
+      __syncwarp();
+      if (lane < n && before < a.K) order[before] = id;
+      __syncwarp();
+      mine = order[lane];
+      __syncwarp();
+      return mine;
+    }
+    __syncwarp();
+  }
+
+  // K rounds: the largest key, the lowest lane (so the lowest id) holding it
+  float last = 0.f;
+  int last_id = -1;
+  for (int k = 0; k < want; ++k) {
+    best = ninf;
     int at = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
@@ -165,28 +308,21 @@ __device__ __forceinline__ int select_token(const RouteOpArgs& a, const float (&
         best = key[i];
         at = i;
       }
-    const T top = warp_max_t(best);
+    const T top = warp_max_fast(best);
     if (!(top > ninf)) break;  // uniform: no live expert left
-    const int id = (best == top) ? lane + 32 * at : 0x7fffffff;
-    const int win = __reduce_min_sync(0xffffffffu, id);
+    const int from = __ffs(__ballot_sync(kAll, best == top)) - 1;
+    const int id = __shfl_sync(kAll, lane * VPL + at, from);
     if (check) {
-      float wx = 0.f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (i == win / 32) wx = x[i];
-      wx = __shfl_sync(0xffffffffu, wx, win & 31);
-      const float wb = a.bias[win];
-      // the same logit and bias give the same key: a real tie, by id
-      if (k > 0 && !(last - top > 2 * err) && !(wx == last_x && wb == last_b)) doubt = true;
-      last = top;
-      last_x = wx;
-      last_b = wb;
+      if (k > 0 && !(last - static_cast<float>(top) > 2 * static_cast<float>(err)))
+        doubt |= !(load_logit(a, row, id) == load_logit(a, row, last_id) && a.bias[id] == a.bias[last_id]);
+      last = static_cast<float>(top);
+      last_id = id;
     }
-    if (k < a.K && lane == k) mine = win;
-    if ((win & 31) == lane) {
+    if (k < a.K && lane == k) mine = id;
+    if (lane == from) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (i == win / 32) key[i] = ninf;
+        if (i == at) key[i] = ninf;
     }
   }
   if (!kExact) *unsure = doubt;
@@ -194,10 +330,11 @@ __device__ __forceinline__ int select_token(const RouteOpArgs& a, const float (&
 }
 
 template <int VPL>
-__device__ __noinline__ int select_token_exact(const RouteOpArgs& a, int64_t row, double* s_keys, int lane) {
-  float x[VPL];
+__device__ __noinline__ int select_token_exact(const RouteOpArgs& a, int64_t row, double* smem, int lane) {
+  float x[VPL], bias[VPL];
   load_row<VPL>(a, row, lane, x);
-  return select_token<VPL, double>(a, x, s_keys, lane, nullptr);
+  load_bias<VPL>(a, lane, bias);
+  return select_token<VPL, double>(a, row, x, bias, smem, lane, nullptr);
 }
 
 // Weight of the expert lane k holds (id < 0: 0), among the selected ones.
@@ -214,7 +351,7 @@ __device__ __forceinline__ float token_weight(const RouteOpArgs& a, const float 
 #pragma unroll
       for (int i = 0; i < VPL; ++i) m = fmaxf(m, x[i]);
     }
-    m = warp_max_f(m);
+    m = warp_max_fast(m);
     num = on ? expf(z - m) : 0.f;
     if (!a.renormalise) {
       e = 0.f;
@@ -226,11 +363,17 @@ __device__ __forceinline__ float token_weight(const RouteOpArgs& a, const float 
     }
   } else {
     const float t = fminf(z, 0.f);
-    const float shift = a.renormalise ? warp_max_f(on ? t : -INFINITY) : 0.f;
+    const float shift = a.renormalise ? warp_max_fast(on ? t : -INFINITY) : 0.f;
     num = on ? expf(t - shift) / (1.f + expf(-fabsf(z))) : 0.f;
     e = a.renormalise ? warp_sum_f(num) : 1.f;
   }
   return on ? num / e * a.scale : 0.f;
+}
+
+// A warp's scratch: the list of the largest keys, or every key in double.
+__host__ __device__ __forceinline__ size_t select_scratch(const RouteOpArgs& a) {
+  const size_t keys = a.n_groups > 1 ? static_cast<size_t>(a.E) * 8 : 0;
+  return keys > kListBytes ? keys : kListBytes;
 }
 
 // The places of this CTA's selected slots: an expert's slots are ordered by
@@ -271,10 +414,10 @@ __device__ __forceinline__ void scan_counts(const int* s_cnt, int* s_first, int*
 // are to be grouped, each CTA also leaves its counts per expert; a call that
 // one CTA takes groups them itself.
 template <int VPL>
-__global__ void __launch_bounds__(kThreads) k_select(const RouteOpArgs a) {
+__global__ void __launch_bounds__(kThreads, VPL <= 8 ? 4 : 2) k_select(const RouteOpArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
-  double* s_keys = reinterpret_cast<double*>(raw);  // [kWarps][E], only with groups
-  uint32_t* s_mask = reinterpret_cast<uint32_t*>(s_keys + (a.n_groups > 1 ? kWarps * a.E : 0));  // [E][2]
+  const size_t scratch = select_scratch(a);
+  uint32_t* s_mask = reinterpret_cast<uint32_t*>(raw + kWarps * scratch);  // [E][2]
   int* s_cnt = reinterpret_cast<int*>(s_mask + 2 * a.E);                                          // [E]
   int* s_first = s_cnt + a.E;                                                                     // [E + 1]
   __shared__ int s_tmp[17];
@@ -288,13 +431,15 @@ __global__ void __launch_bounds__(kThreads) k_select(const RouteOpArgs a) {
   }
   pdl_wait();
   pdl_trigger();
-  double* keys = s_keys + static_cast<size_t>(warp) * a.E;
+  double* keys = reinterpret_cast<double*>(raw + warp * scratch);
+  float bias[VPL];
+  load_bias<VPL>(a, lane, bias);
   for (int t = warp; t < nt; t += kWarps) {
     const int64_t row = static_cast<int64_t>(t0 + t) * a.ld;
     float x[VPL];
     load_row<VPL>(a, row, lane, x);
     bool unsure = false;
-    int id = select_token<VPL, float>(a, x, reinterpret_cast<float*>(keys), lane, &unsure);
+    int id = select_token<VPL, float>(a, row, x, bias, keys, lane, &unsure);
     if (unsure) id = select_token_exact<VPL>(a, row, keys, lane);
     const float w = token_weight<VPL>(a, x, row, id);
     if (lane < a.K) {
@@ -373,12 +518,18 @@ __global__ void __launch_bounds__(kThreads) k_place(const RouteOpArgs a) {
   place_slots(a, s_mask, s_first, t0, nt);
 }
 
-cudaError_t launch_route_op(const RouteOpArgs& a, cudaStream_t s) {
+cudaError_t launch_route_op(const RouteOpArgs& args, cudaStream_t s) {
+  RouteOpArgs a = args;
   const size_t tail = static_cast<size_t>(4 * a.E + 1) * 4;
-  const size_t smem = (a.n_groups > 1 ? static_cast<size_t>(kWarps) * a.E * 8 : 0) + tail;
-  void (*k)(const RouteOpArgs) = a.E <= 64 ? k_select<2> : a.E <= 128 ? k_select<4> : a.E <= 256 ? k_select<8>
-                                                                                                  : k_select<16>;
-  cudaError_t e = launch_kernel(k, dim3(a.n_ctas), dim3(kThreads), smem, s, true, a);
+  const size_t smem = kWarps * select_scratch(a) + tail;
+  const int vpl = a.E <= 64 ? 2 : a.E <= 128 ? 4 : a.E <= 256 ? 8 : 16;
+  void (*k)(const RouteOpArgs) = vpl == 2 ? k_select<2> : vpl == 4 ? k_select<4> : vpl == 8 ? k_select<8> : k_select<16>;
+  const int size = a.bf16_logits ? 2 : 4;
+  const int part = vpl * size < 16 ? vpl * size : 16;
+  a.vec = a.E % vpl == 0 && reinterpret_cast<uintptr_t>(a.logits) % part == 0 && a.ld * size % part == 0;
+  const int lanes = a.E / a.n_groups / vpl;  // per group, where that is whole and a power of two
+  a.group_lanes = (a.E / a.n_groups % vpl == 0 && (lanes & (lanes - 1)) == 0) ? lanes : 0;
+  cudaError_t e = launch_kernel<RouteOpArgs>(k, dim3(a.n_ctas), dim3(kThreads), smem, s, true, a);
   if (e != cudaSuccess || a.offsets == nullptr || a.n_ctas == 1) return e;
   e = launch_kernel<RouteOpArgs>(k_scan_hist, dim3((a.E + kWarps - 1) / kWarps), dim3(kThreads), 0, s, true, a);
   if (e != cudaSuccess) return e;
