@@ -17,17 +17,15 @@ constexpr uint32_t kAll = 0xffffffffu;
 // Largest K + 1 that is selected by counting (select_token): beyond it the
 // keys above the bound no longer fit 32 lanes as a rule.
 constexpr int kCountedMax = 17;
-constexpr int kListBytes = 384;  // a warp's list of 32 keys and ids, and their order
+constexpr int kListBytes = 256;  // a warp's list of 32 keys and ids
 
-__device__ __forceinline__ float clean_logit(float v) {
-  // +inf counts as the largest finite value, NaN as -inf, -0 as 0
-  return fmaxf(fminf(v, 3.402823466e+38f), -INFINITY) + 0.0f;
-}
+// +inf counts as the largest finite value, NaN as -inf.
+__device__ __forceinline__ float clean_logit(float v) { return v == v ? fminf(v, 3.402823466e+38f) : -INFINITY; }
 
 __device__ __forceinline__ float load_logit(const RouteOpArgs& a, int64_t row, int e) {
   const float v = a.bf16_logits ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[row + e])
                                 : static_cast<const float*>(a.logits)[row + e];
-  return v != v ? -INFINITY : clean_logit(v);
+  return clean_logit(v);
 }
 
 // The token's logits: expert lane * VPL + i in slot i (so that a lower lane
@@ -66,28 +64,36 @@ __device__ __forceinline__ void load_row(const RouteOpArgs& a, int64_t row, int 
       for (int i = 0; i < VPL; ++i) x[i] = __uint_as_float(wd[i]);
     }
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) x[i] = x[i] != x[i] ? -INFINITY : clean_logit(x[i]);
+    for (int i = 0; i < VPL; ++i) x[i] = clean_logit(x[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) x[i] = e0 + i < a.E ? load_logit(a, row, e0 + i) : -INFINITY;
   }
 }
 
-// This lane's biases (0 without any, and past E).
+// This lane's biases: 0 without any and past E, -inf for NaN. Returns the
+// largest magnitude in the warp (-inf, which makes an expert dead, aside).
 template <int VPL>
-__device__ __forceinline__ void load_bias(const RouteOpArgs& a, int lane, float (&b)[VPL]) {
+__device__ __forceinline__ float load_bias(const RouteOpArgs& a, int lane, float (&b)[VPL]) {
+  float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) b[i] = (a.bias != nullptr && lane * VPL + i < a.E) ? a.bias[lane * VPL + i] : 0.f;
+  for (int i = 0; i < VPL; ++i) {
+    b[i] = (a.bias != nullptr && lane * VPL + i < a.E) ? a.bias[lane * VPL + i] : 0.f;
+    if (!(b[i] > -INFINITY)) b[i] = -INFINITY;
+    if (b[i] > -INFINITY) m = fmaxf(m, fabsf(b[i]));
+  }
+  return warp_max_f(m);
 }
 
-// Warp-wide maximum of any floats but NaN, by one reduction over keys whose
-// signed order is the floats' order.
-__device__ __forceinline__ float warp_max_fast(float v) {
+// Keys whose signed order is the order of the floats (with +0 above -0).
+__device__ __forceinline__ int order_int(float v) {
   const int b = __float_as_int(v);
-  const int m = __reduce_max_sync(kAll, b ^ ((b >> 31) & 0x7fffffff));
-  return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
+  return b ^ ((b >> 31) & 0x7fffffff);
 }
-__device__ __forceinline__ double warp_max_fast(double v) {
+__device__ __forceinline__ float order_float(int m) { return __int_as_float(m ^ ((m >> 31) & 0x7fffffff)); }
+
+__device__ __forceinline__ float warp_max_t(float v) { return order_float(__reduce_max_sync(kAll, order_int(v))); }
+__device__ __forceinline__ double warp_max_t(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(kAll, v, o));
   return v;
@@ -110,197 +116,139 @@ __device__ __forceinline__ void two_best(T& b1, T& b2, T v) {
   b1 = fmax(b1, v);
 }
 
-// One token's selection by one warp, in T: lane k < K returns the k-th
-// selected expert (-1: none left). x holds the logits, -inf where the expert
-// is not live. smem: the warp's scratch.
+// What experts are ordered by, in T: -inf for a dead expert and for one in a
+// group that does not stay. x: the logits, -inf where dead. False where the
+// token has no live expert (every lane alike).
 //
-// In float, *unsure is set where the order could be another one in exact
-// arithmetic: two keys (or the ranks on either side of the group border)
-// closer than the errors they can have. A score's error is below 2^-19 of the
-// largest score (softmax: exp and quotient a few roundings each, the sum up to
-// 21; sigmoid: the fast exp's error grows with -logit, a multiple of 2^-22 of
-// it, which s * -logit bounds by that of the largest score), the sum with the
-// bias adds half a unit of the key. Logits used as keys are exact. The caller
-// then repeats the token in double, whose order is the definition's.
-//
-// The K largest of E by counting rather than by K rounds over all of them:
-// the (K + 1)-th largest of the 32 lanes' maxima is a lower bound of the
-// (K + 1)-th largest key, the few keys at or above it (usually K + 1 to K + 4)
-// are listed in shared memory, one per lane, and each lane counts how many come
-// before its own. Where more than 32 qualify (ties; large K), K rounds.
+// In float, *err bounds the error of a key, and *doubt is set in some lane
+// where two groups' ranks are closer than the errors they can have. A score's
+// error is below 2^-19 of the largest score (softmax: exp and quotient a few
+// roundings each, the sum up to 21; sigmoid: the fast exp's error grows with
+// -logit, a multiple of 2^-22 of it, which s * -logit bounds by that of the
+// largest score), the sum with the bias adds half a unit of the key. Logits
+// used as keys are exact.
 template <int VPL, typename T>
-__device__ __forceinline__ int select_token(const RouteOpArgs& a, int64_t row, const float (&x)[VPL],
-                                            const float (&bias)[VPL], double* smem, int lane, bool* unsure) {
+__device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float (&x)[VPL], const float (&bias)[VPL],
+                                           float bias_max, double* smem, int lane, T (&key)[VPL], T* err, bool* doubt) {
   constexpr bool kExact = sizeof(T) == 8;
   const T ninf = -static_cast<T>(INFINITY);
-  const bool need_scores = a.bias != nullptr || (a.n_groups > 1 && a.group_rank == 2);
-  T key[VPL];    // what experts are ordered by
-  T total[VPL];  // score + bias, what group ranks sum
-  T err = 0;     // bound on the error of a key or half a rank
-  if (need_scores) {
-    float xm = -INFINITY;
+  *err = 0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) xm = fmaxf(xm, x[i]);
-    xm = warp_max_fast(xm);
+  for (int i = 0; i < VPL; ++i) key[i] = static_cast<T>(x[i]);
+  const bool sums = a.n_groups > 1 && a.group_rank == 2;  // ranks are sums of scores
+  if (a.bias != nullptr || sums) {
+    float xm = x[0], xl = x[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) xm = fmaxf(xm, x[i]), xl = fminf(xl, x[i]);
+    xm = warp_max_t(xm);
+    if (xm == -INFINITY) return false;
     T s_max;
     if (a.softmax) {
       T sum = 0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        total[i] = x[i] > -INFINITY ? exp_t(static_cast<T>(x[i]) - static_cast<T>(xm)) : static_cast<T>(0);
-        sum += total[i];
+        key[i] = exp_t(static_cast<T>(x[i]) - static_cast<T>(xm));
+        sum += key[i];
       }
-      sum = warp_sum_t(sum);
-      const T inv = static_cast<T>(1) / sum;  // sum >= 1 where any expert is live
+      sum = warp_sum_t(sum);  // at least 1
+      s_max = static_cast<T>(1) / sum;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) total[i] = kExact ? total[i] / sum : total[i] * inv;
-      s_max = inv;
+      for (int i = 0; i < VPL; ++i) key[i] = kExact ? key[i] / sum : key[i] * s_max;
     } else {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) total[i] = sigmoid_t(static_cast<T>(x[i]));
+      for (int i = 0; i < VPL; ++i) key[i] = sigmoid_t(static_cast<T>(x[i]));
       s_max = sigmoid_t(static_cast<T>(xm)) * (1 + static_cast<T>(fmaxf(-xm, 0.f)) * static_cast<T>(0.25));
     }
-    T k_max = 0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const bool live = x[i] > -INFINITY && bias[i] > -INFINITY;  // false for NaN too
-      total[i] = live ? total[i] + static_cast<T>(bias[i]) : ninf;
-      if (!kExact && live) k_max = fmax(k_max, fabs(total[i]));
+    for (int i = 0; i < VPL; ++i) key[i] += static_cast<T>(bias[i]);
+    if (__any_sync(kAll, xl == -INFINITY)) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = x[i] > -INFINITY ? key[i] : ninf;
     }
     if (!kExact)
-      err = s_max * static_cast<T>(1.9e-6) + warp_max_fast(k_max) * static_cast<T>(1.2e-7) + static_cast<T>(1e-37);
+      *err = s_max * static_cast<T>(1.9e-6) + (s_max + bias_max) * static_cast<T>(1.2e-7) + static_cast<T>(1e-37);
   }
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) key[i] = a.bias != nullptr ? total[i] : static_cast<T>(x[i]);
-  bool doubt = false;
+  if (a.n_groups == 1) return true;
 
-  if (a.n_groups > 1) {
-    const int size = a.E / a.n_groups;
-    T b1 = ninf, b2 = ninf;
-    int g, step;  // this lane's group; lanes from one group to the next
-    bool first;   // one lane per group speaks for it
-    if (a.group_lanes > 0) {
-      // a group is VPL slots of a power of two of neighbouring lanes
+  // Group ranks. Without a bias experts go by their logits, whatever the
+  // groups go by.
+  const int size = a.E / a.n_groups;
+  T b1 = ninf, b2 = ninf;
+  int g, step;  // this lane's group, and the lanes from one group to the next
+  if (a.group_lanes > 0) {
+    // a group is all slots of a power of two of neighbouring lanes
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) two_best(b1, b2, a.group_rank == 2 ? total[i] : key[i]);
-      for (int o = 1; o < a.group_lanes; o <<= 1) {
-        const T c1 = __shfl_xor_sync(kAll, b1, o), c2 = __shfl_xor_sync(kAll, b2, o);
-        two_best(b1, b2, c1);
-        b2 = fmax(b2, c2);
-      }
-      step = a.group_lanes;
-      g = lane / step;
-      first = lane % step == 0 && g < a.n_groups;
-    } else {
-      // any other size: keys in shared memory, lane g scans group g
-      T* s_keys = reinterpret_cast<T*>(smem);
+    for (int i = 0; i < VPL; ++i) two_best(b1, b2, key[i]);
+    for (int o = 1; o < a.group_lanes; o <<= 1) {
+      const T c1 = __shfl_xor_sync(kAll, b1, o), c2 = __shfl_xor_sync(kAll, b2, o);
+      two_best(b1, b2, c1);
+      b2 = fmax(b2, c2);
+    }
+    step = a.group_lanes;
+    g = lane / step;
+  } else {
+    // any other size: keys in shared memory, lane g scans group g
+    T* s_keys = reinterpret_cast<T*>(smem);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (lane * VPL + i < a.E) s_keys[lane * VPL + i] = a.group_rank == 2 ? total[i] : key[i];
-      __syncwarp();
-      step = 1;
-      g = lane;
-      first = lane < a.n_groups;
-      if (first)
-        for (int n = 0; n < size; ++n) two_best(b1, b2, s_keys[lane * size + n]);
-      __syncwarp();
-    }
-    const T rank = (a.group_rank == 2 && b2 > ninf) ? b1 + b2 : b1;
-    int before = 0;
-    for (int j = 0; j < a.n_groups; ++j) {
-      const T r = __shfl_sync(kAll, rank, j * step);
-      before += (r > rank || (r == rank && j < g)) ? 1 : 0;
-    }
-    const bool stays = before < a.top_groups;
-    const uint32_t mask = __ballot_sync(kAll, first && stays);  // bit g * step
-    if (!kExact && err > 0) {
-      const T low = -warp_max_fast(first && stays ? -rank : ninf);
-      const T high = warp_max_fast(first && !stays ? rank : ninf);
-      doubt = high > ninf && !(low - high > (a.group_rank == 2 ? 4 : 2) * err);
-    }
-    if (a.group_lanes > 0) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = stays ? key[i] : ninf;
-    } else {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = lane * VPL + i;
-        if (e < a.E && ((mask >> (e / size)) & 1u) == 0) key[i] = ninf;
-      }
-    }
-  }
-
-  // one more than K in float, to see the key that just missed
-  const bool check = !kExact && a.bias != nullptr;
-  const int want = check ? a.K + 1 : a.K;
-  T best = key[0];
-#pragma unroll
-  for (int i = 1; i < VPL; ++i) best = fmax(best, key[i]);
-  int mine = -1;
-  if (!kExact && want <= kCountedMax) {
-    T m = best, bound = ninf;
-    for (int left = want; left > 0;) {
-      bound = warp_max_fast(m);
-      if (!(bound > ninf)) break;
-      const bool top = m == bound;
-      left -= __popc(__ballot_sync(kAll, top));
-      if (top) m = ninf;
-    }
-    int n = 0;
-    uint64_t* list = reinterpret_cast<uint64_t*>(smem);  // [32]: (id, key bits)
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const bool in = key[i] >= bound && key[i] > ninf;
-      const uint32_t votes = __ballot_sync(kAll, in);
-      if (votes == 0) continue;
-      const int at = n + __popc(votes & ((1u << lane) - 1u));
-      if (in && at < 32)
-        list[at] = (static_cast<uint64_t>(lane * VPL + i) << 32) | __float_as_uint(static_cast<float>(key[i]));
-      n += __popc(votes);
-    }
-    if (n <= 32) {
-      __syncwarp();
-      const uint64_t own = lane < n ? list[lane] : 0;
-      const float k0 = lane < n ? __uint_as_float(static_cast<uint32_t>(own)) : -INFINITY;
-      const int id = static_cast<int>(own >> 32);
-      int before = 0;
-      float next = -INFINITY;  // the largest key that comes after this one
-      int next_id = 0;
-      for (int j = 0; j < n; ++j) {
-        const uint64_t o = list[j];
-        const float kj = __uint_as_float(static_cast<uint32_t>(o));
-        const int ij = static_cast<int>(o >> 32);
-        const bool earlier = kj > k0 || (kj == k0 && ij < id);
-        before += earlier ? 1 : 0;
-        if (check && !earlier && j != lane && (kj > next || (kj == next && ij < next_id))) {
-          next = kj;
-          next_id = ij;
-        }
-      }
-      __syncwarp();
-      if (lane < n && check && before < a.K && next > -INFINITY && !(k0 - next > 2 * static_cast<float>(err))) {
-        // the same logit and bias give the same key: a real tie, by id
-        doubt |= !(load_logit(a, row, id) == load_logit(a, row, next_id) && a.bias[id] == a.bias[next_id]);
-      }
-      if (!kExact) *unsure = __any_sync(kAll, doubt);
-      // expert of rank r to lane r
-      int32_t* order = reinterpret_cast<int32_t*>(smem) + 64;
-      order[lane] = -1;
-      __syncwarp();
-      if (lane < n && before < a.K) order[before] = id;
-      __syncwarp();
-      mine = order[lane];
-      __syncwarp();
-      return mine;
-    }
+    for (int i = 0; i < VPL; ++i)
+      if (lane * VPL + i < a.E) s_keys[lane * VPL + i] = key[i];
+    __syncwarp();
+    step = 1;
+    g = lane;
+    if (g < a.n_groups)
+      for (int n = 0; n < size; ++n) two_best(b1, b2, s_keys[g * size + n]);
     __syncwarp();
   }
+  const T rank = (a.group_rank == 2 && b2 > ninf) ? b1 + b2 : b1;
+  // the groups before this one; a group's lanes share the comparisons
+  const T tol = *err * (a.group_rank == 2 ? 4 : 2);
+  int before = 0;
+  for (int j0 = 0; j0 < a.n_groups; j0 += step) {
+    const int j = j0 + lane % step;
+    const T r = __shfl_sync(kAll, rank, (j * step) & 31);
+    const bool other = j < a.n_groups && j != g;
+    before += (other && (r > rank || (r == rank && j < g))) ? 1 : 0;
+    if (!kExact && other && g < a.n_groups && tol > 0 && (r > ninf || rank > ninf) && !(fabs(r - rank) > tol)) *doubt = true;
+  }
+  for (int o = 1; o < step; o <<= 1) before += __shfl_xor_sync(kAll, before, o);
+  if (a.bias == nullptr) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = static_cast<T>(x[i]);
+    *err = 0;
+  }
+  if (a.group_lanes > 0) {
+    if (before >= a.top_groups) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = ninf;
+    }
+  } else {
+    const uint32_t mask = __ballot_sync(kAll, before < a.top_groups);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = lane * VPL + i;
+      if (e < a.E && ((mask >> (e / size)) & 1u) == 0) key[i] = ninf;
+    }
+  }
+  return true;
+}
 
-  // K rounds: the largest key, the lowest lane (so the lowest id) holding it
-  float last = 0.f;
-  int last_id = -1;
+// Whether two experts' keys, closer than their errors, are a true tie: the
+// same logit and the same bias.
+__device__ __forceinline__ bool same_key(const RouteOpArgs& a, int64_t row, int e, int f) {
+  return load_logit(a, row, e) == load_logit(a, row, f) && (a.bias == nullptr || a.bias[e] == a.bias[f]);
+}
+
+// The first `want` experts by descending key, ties to the lower id: lane k
+// returns the k-th (-1: none left). Each round takes the largest key and the
+// lowest lane, so the lowest id, that holds it.
+template <int VPL, typename T>
+__device__ __forceinline__ int pick_by_rounds(const RouteOpArgs& a, int64_t row, T (&key)[VPL], int want, T err,
+                                              int lane, bool* doubt) {
+  const T ninf = -static_cast<T>(INFINITY);
+  int mine = -1, last_id = -1;
+  T last = 0;
   for (int k = 0; k < want; ++k) {
-    best = ninf;
+    T best = ninf;
     int at = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
@@ -308,66 +256,152 @@ __device__ __forceinline__ int select_token(const RouteOpArgs& a, int64_t row, c
         best = key[i];
         at = i;
       }
-    const T top = warp_max_fast(best);
+    const T top = warp_max_t(best);
     if (!(top > ninf)) break;  // uniform: no live expert left
     const int from = __ffs(__ballot_sync(kAll, best == top)) - 1;
     const int id = __shfl_sync(kAll, lane * VPL + at, from);
-    if (check) {
-      if (k > 0 && !(last - static_cast<float>(top) > 2 * static_cast<float>(err)))
-        doubt |= !(load_logit(a, row, id) == load_logit(a, row, last_id) && a.bias[id] == a.bias[last_id]);
-      last = static_cast<float>(top);
-      last_id = id;
-    }
-    if (k < a.K && lane == k) mine = id;
+    if (k > 0 && err > 0 && !(last - top > 2 * err) && !same_key(a, row, last_id, id)) *doubt = true;
+    last = top;
+    last_id = id;
+    if (lane == k) mine = id;
     if (lane == from) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
         if (i == at) key[i] = ninf;
     }
   }
-  if (!kExact) *unsure = doubt;
   return mine;
 }
 
+// The same by counting: the want-th largest of the 32 lanes' maxima is a lower
+// bound of the want-th largest key; the few keys at or above it (as a rule
+// want to want + 4) are listed in shared memory, one per lane, and each lane
+// counts how many come before its own. False where more than 32 qualify.
+template <int VPL>
+__device__ __forceinline__ bool pick_by_count(const RouteOpArgs& a, int64_t row, const float (&key)[VPL], int want,
+                                              float err, double* smem, int lane, int* mine, bool* doubt) {
+  float best = key[0];
+#pragma unroll
+  for (int i = 1; i < VPL; ++i) best = fmaxf(best, key[i]);
+  // (equal maxima leave together, which can only lower the bound)
+  constexpr int kNone = static_cast<int>(0x80000000u);
+  int m = order_int(best), bound_int = kNone;
+  for (int k = 0; k < want; ++k) {
+    bound_int = __reduce_max_sync(kAll, m);
+    m = m == bound_int ? kNone : m;
+  }
+  // at least the lowest finite float: dead experts are not listed
+  const float bound = fmaxf(order_float(bound_int == kNone ? order_int(-INFINITY) : bound_int), -3.402823466e+38f);
+  int c = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) c += key[i] >= bound ? 1 : 0;
+  // places by lane: the sum of the lower lanes' counts, bit by bit
+  const uint32_t lower = (1u << lane) - 1u;
+  int at = 0, n = 0;
+#pragma unroll
+  for (int bit = 0; (1 << bit) <= VPL; ++bit) {
+    const uint32_t v = __ballot_sync(kAll, (c >> bit) & 1);
+    at += __popc(v & lower) << bit;
+    n += __popc(v) << bit;
+  }
+  if (n > 32) return false;
+  uint2* list = reinterpret_cast<uint2*>(smem);  // [32]
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (key[i] >= bound) list[at++] = make_uint2(__float_as_uint(key[i]), lane * VPL + i);
+  __syncwarp();
+  // (key, lower id first) as one unsigned number; 0 for no entry
+  uint64_t own = 0;
+  if (lane < n) {
+    const uint2 u = list[lane];
+    const float k0 = __uint_as_float(u.x) + 0.0f;  // -0 ties with 0
+    own = (static_cast<uint64_t>(static_cast<uint32_t>(order_int(k0)) ^ 0x80000000u) << 32) | (0xffffu - u.y);
+  }
+  uint64_t* sorted = reinterpret_cast<uint64_t*>(smem);
+  __syncwarp();
+  sorted[lane] = own;
+  __syncwarp();
+  int before = 0;
+  for (int j = 0; j < n; j += 2) {
+    const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(sorted + j);
+    before += (o.x > own ? 1 : 0) + (o.y > own ? 1 : 0);
+  }
+  __syncwarp();
+  if (lane >= n) before = lane;  // entries of 0 stay behind
+  sorted[before] = own;
+  __syncwarp();
+  own = sorted[lane];
+  __syncwarp();
+  const int id = own != 0 ? static_cast<int>(0xffffu - static_cast<uint32_t>(own & 0xffffu)) : -1;
+  *mine = lane < want ? id : -1;
+  if (err > 0) {
+    const float k0 = order_float(static_cast<int>(static_cast<uint32_t>(own >> 32) ^ 0x80000000u));
+    const float next = __shfl_down_sync(kAll, k0, 1);
+    const int next_id = __shfl_down_sync(kAll, id, 1);
+    if (lane + 1 < min(n, want) && !(k0 - next > 2 * err) && !same_key(a, row, id, next_id)) *doubt = true;
+  }
+  return true;
+}
+
+// One token's selection by one warp: lane k < K returns the k-th selected
+// expert (-1: none left). Worked out in float; where some comparison is closer
+// than the errors allow (*doubt in any lane), again in double, whose order is
+// the definition's.
 template <int VPL>
 __device__ __noinline__ int select_token_exact(const RouteOpArgs& a, int64_t row, double* smem, int lane) {
   float x[VPL], bias[VPL];
   load_row<VPL>(a, row, lane, x);
   load_bias<VPL>(a, lane, bias);
-  return select_token<VPL, double>(a, row, x, bias, smem, lane, nullptr);
+  double key[VPL], err;
+  bool doubt = false;
+  if (!token_keys<VPL, double>(a, x, bias, 0.f, smem, lane, key, &err, &doubt)) return -1;
+  return pick_by_rounds<VPL, double>(a, row, key, a.K, 0.0, lane, &doubt);
 }
 
-// Weight of the expert lane k holds (id < 0: 0), among the selected ones.
-// Shifted by the largest exponent, so that renormalised weights keep their
-// ratio where every score is below the smallest float.
+template <int VPL>
+__device__ __forceinline__ int select_token(const RouteOpArgs& a, int64_t row, const float (&x)[VPL],
+                                            const float (&bias)[VPL], float bias_max, double* smem, int lane) {
+  float key[VPL], err;
+  bool doubt = false;
+  if (!token_keys<VPL, float>(a, x, bias, bias_max, smem, lane, key, &err, &doubt)) return -1;
+  // with inexact keys one more than K, to see the key that just missed
+  const int want = err > 0 ? a.K + 1 : a.K;
+  int mine;
+  if (want > kCountedMax || !pick_by_count<VPL>(a, row, key, want, err, smem, lane, &mine, &doubt))
+    mine = pick_by_rounds<VPL, float>(a, row, key, want, err, lane, &doubt);
+  if (__any_sync(kAll, doubt)) mine = select_token_exact<VPL>(a, row, smem, lane);
+  return lane < a.K ? mine : -1;
+}
+
+// Weight of the expert lane k holds (id < 0: 0), among the selected ones. Sums
+// are shifted by the largest exponent where that matters, so that renormalised
+// weights keep their ratio where every score is below the smallest float.
 template <int VPL>
 __device__ __forceinline__ float token_weight(const RouteOpArgs& a, const float (&x)[VPL], int64_t row, int id) {
   const bool on = id >= 0;
   const float z = on ? load_logit(a, row, id) : -INFINITY;
-  float num, e;
+  float num, sum = 1.f;
   if (a.softmax) {
     float m = z;
     if (!a.renormalise) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) m = fmaxf(m, x[i]);
     }
-    m = warp_max_fast(m);
+    m = warp_max_t(m);
     num = on ? expf(z - m) : 0.f;
     if (!a.renormalise) {
-      e = 0.f;
+      sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) e += x[i] > -INFINITY ? expf(x[i] - m) : 0.f;
-      e = warp_sum_f(e);
-    } else {
-      e = warp_sum_f(num);
+      for (int i = 0; i < VPL; ++i) sum += x[i] > -INFINITY ? expf(x[i] - m) : 0.f;
+      sum = warp_sum_f(sum);
     }
   } else {
-    const float t = fminf(z, 0.f);
-    const float shift = a.renormalise ? warp_max_fast(on ? t : -INFINITY) : 0.f;
-    num = on ? expf(t - shift) / (1.f + expf(-fabsf(z))) : 0.f;
-    e = a.renormalise ? warp_sum_f(num) : 1.f;
+    float t = fminf(z, 0.f);
+    if (a.renormalise && __any_sync(kAll, on && t < -60.f)) t -= warp_max_t(on ? t : -INFINITY);
+    num = on ? __fdividef(expf(t), 1.f + expf(-fabsf(z))) : 0.f;
   }
-  return on ? num / e * a.scale : 0.f;
+  if (a.renormalise) sum = warp_sum_f(num);
+  return on ? __fdividef(num, sum) * a.scale : 0.f;
 }
 
 // A warp's scratch: the list of the largest keys, or every key in double.
@@ -433,14 +467,12 @@ __global__ void __launch_bounds__(kThreads, VPL <= 8 ? 4 : 2) k_select(const Rou
   pdl_trigger();
   double* keys = reinterpret_cast<double*>(raw + warp * scratch);
   float bias[VPL];
-  load_bias<VPL>(a, lane, bias);
+  const float bias_max = load_bias<VPL>(a, lane, bias);
   for (int t = warp; t < nt; t += kWarps) {
     const int64_t row = static_cast<int64_t>(t0 + t) * a.ld;
     float x[VPL];
     load_row<VPL>(a, row, lane, x);
-    bool unsure = false;
-    int id = select_token<VPL, float>(a, row, x, bias, keys, lane, &unsure);
-    if (unsure) id = select_token_exact<VPL>(a, row, keys, lane);
+    const int id = select_token<VPL>(a, row, x, bias, bias_max, keys, lane);
     const float w = token_weight<VPL>(a, x, row, id);
     if (lane < a.K) {
       const int64_t o = static_cast<int64_t>(t0 + t) * a.K + lane;
