@@ -365,8 +365,8 @@ def _refuse(msg: str):
 
 def _tensor(name: str, t, dtype, shape, device) -> int:
     """The pointer of a contiguous tensor of this type and shape on `device`."""
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
-        _refuse(f"{name}: need contiguous {dtype} {shape} on {device}, "
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _refuse(f"{name}: need contiguous {dtype} {tuple(shape)} on {device}, "
                 f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
     return t.data_ptr()
 
@@ -374,20 +374,24 @@ def _tensor(name: str, t, dtype, shape, device) -> int:
 def _rows_of(name: str, t):
     """(pointer, type code, row stride in elements) of a 2-D fp32 or bf16 tensor with contiguous rows on the
     current device."""
-    if t.dim() != 2 or t.dtype not in _TYPES or (t.shape[1] > 1 and t.stride(1) != 1):
+    kind = _TYPES.get(t.dtype)
+    strides = t.stride()
+    if len(strides) != 2 or kind is None or (strides[1] != 1 and t.shape[1] > 1):
         _refuse(f"{name}: need a 2-D fp32 or bf16 tensor with contiguous rows, got {t.dtype} {tuple(t.shape)}, "
-                f"strides {t.stride()}")
-    _on_current(name, t)
-    return t.data_ptr(), _TYPES[t.dtype], (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1]))
+                f"strides {strides}")
+    _on_current(name, t.device)
+    rows, cols = t.shape
+    return t.data_ptr(), kind, (strides[0] if rows > 1 else max(strides[0], cols))
 
 
-def _on_current(name: str, t):
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        _refuse(f"{name} is on {t.device}, not on the current CUDA device")
+def _on_current(name: str, device):
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        _refuse(f"{name} is on {device}, not on the current CUDA device")
 
 
 def _raw_stream(stream, device) -> int:
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    # (the stream object costs more than the launch it is for)
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def make_routing(n_experts: int, top_k: int, score: str = "softmax", n_groups: int = 1, top_groups: int | None = None,
@@ -407,15 +411,15 @@ def route(r: Routing, logits, bias=None, grouping: bool = True, ws=None, out=Non
     """Expert selection from router logits [M][E] (fp32 or bf16, rows may be strided) -> idx int32 [M][K], w fp32
     [M][K] and, with grouping, offsets int32 [E + 1], rows int32 [M * K], pos int32 [M][K]. `out` (a dict this
     function returned before, for the same shape) is reused."""
-    M, K, E = logits.shape[0], r.top_k, r.n_experts
-    dev = logits.device
     p_logits, kind, ld = _rows_of("logits", logits)
-    if logits.shape[1] != E:
-        _refuse(f"logits have {logits.shape[1]} columns for {E} experts")
+    (M, cols), dev = logits.shape, logits.device
+    K, E = r.top_k, r.n_experts
+    if cols != E:
+        _refuse(f"logits have {cols} columns for {E} experts")
+    i32 = torch.int32
     p_bias = None if bias is None else _tensor("bias", bias, torch.float32, (E,), dev)
     if ws is None:
         ws = workspace(route_workspace_bytes(r, M), dev)
-    i32 = torch.int32
     if out is None:
         out = {"idx": torch.empty((M, K), dtype=i32, device=dev),
                "w": torch.empty((M, K), dtype=torch.float32, device=dev)}
@@ -423,67 +427,72 @@ def route(r: Routing, logits, bias=None, grouping: bool = True, ws=None, out=Non
             out["offsets"] = torch.empty(E + 1, dtype=i32, device=dev)
             out["rows"] = torch.empty(M * K, dtype=i32, device=dev)
             out["pos"] = torch.empty((M, K), dtype=i32, device=dev)
-    p_group = (None, None, None)
+    p_off = p_rows = p_pos = None
     if grouping:
-        p_group = (_tensor("offsets", out["offsets"], i32, (E + 1,), dev), _tensor("rows", out["rows"], i32, (M * K,), dev),
-                   _tensor("pos", out["pos"], i32, (M, K), dev))
+        p_off = _tensor("offsets", out["offsets"], i32, (E + 1,), dev)
+        p_rows = _tensor("rows", out["rows"], i32, (M * K,), dev)
+        p_pos = _tensor("pos", out["pos"], i32, (M, K), dev)
     _check(lib().clover_route(r, p_logits, kind, ld, p_bias, M, _tensor("idx", out["idx"], i32, (M, K), dev),
-                              _tensor("w", out["w"], torch.float32, (M, K), dev), *p_group, ws.data_ptr(), ws.numel(),
-                              _raw_stream(stream, dev)))
+                              _tensor("w", out["w"], torch.float32, (M, K), dev), p_off, p_rows, p_pos, ws.data_ptr(),
+                              ws.numel(), _raw_stream(stream, dev)))
     return out
 
 
 class Fp4:
-    """Matrices in a microscaled 4-bit format: codes uint8 [..][rows][cols / 2], scale tiles uint8 (1-D), and the
-    power of two the values are scaled by. With offsets (int32 [groups + 1]) the rows of one matrix form groups."""
+    """Matrices in a microscaled 4-bit format: codes uint8 [rows][cols / 2] or [mats][rows][cols / 2], scale tiles
+    uint8 (1-D), and the power of two the values are scaled by. With offsets (int32 [groups + 1]) the rows of one
+    matrix form groups. The parts are checked against one another here, once."""
 
-    __slots__ = ("fmt", "codes", "scales", "scale_exp", "offsets")
+    __slots__ = ("fmt", "codes", "scales", "scale_exp", "_offsets", "device", "mats", "rows", "cols")
 
     def __init__(self, fmt: int, codes, scales, scale_exp: int = 0, offsets=None):
-        self.fmt, self.codes, self.scales, self.scale_exp, self.offsets = fmt, codes, scales, scale_exp, offsets
+        if codes.dtype != torch.uint8 or codes.dim() not in (2, 3) or not codes.is_contiguous():
+            _refuse(f"codes: need contiguous uint8 [rows][cols / 2] or [mats][rows][cols / 2], got {codes.dtype} "
+                    f"{tuple(codes.shape)}")
+        if scales.dtype != torch.uint8 or scales.device != codes.device or not scales.is_contiguous():
+            _refuse(f"scales: need contiguous uint8 on {codes.device}, got {scales.dtype} {tuple(scales.shape)} on "
+                    f"{scales.device}")
+        self.fmt, self.codes, self.scales, self.scale_exp = fmt, codes, scales, scale_exp
+        self.device = codes.device
+        self.mats = codes.shape[0] if codes.dim() == 3 else 1
+        self.rows, self.cols = codes.shape[-2], 2 * codes.shape[-1]
+        self.offsets = offsets
+
+    @classmethod
+    def _made(cls, fmt, codes, scales, scale_exp, offsets, device, mats, rows, cols):
+        """Parts this module has just made to fit."""
+        q = object.__new__(cls)
+        q.fmt, q.codes, q.scales, q.scale_exp, q._offsets = fmt, codes, scales, scale_exp, offsets
+        q.device, q.mats, q.rows, q.cols = device, mats, rows, cols
+        return q
 
     @property
-    def rows(self) -> int:
-        return self.codes.shape[-2]
+    def offsets(self):
+        return self._offsets
 
-    @property
-    def cols(self) -> int:
-        return 2 * self.codes.shape[-1]
-
-    @property
-    def mats(self) -> int:
-        return self.codes.shape[0] if self.codes.dim() == 3 else 1
-
-    def _ptrs(self, name: str):
-        """Checks the parts against one another; the pointers of codes, scales and offsets."""
-        c = self.codes
-        _on_current(name, c)
-        if c.dtype != torch.uint8 or c.dim() not in (2, 3) or not c.is_contiguous():
-            _refuse(f"{name}.codes: need contiguous uint8 [rows][cols / 2] or [mats][rows][cols / 2], got {c.dtype} "
-                    f"{tuple(c.shape)}")
+    @offsets.setter
+    def offsets(self, offsets):
+        if offsets is not None:
+            if self.codes.dim() != 2:
+                _refuse("rows in groups form one matrix")
+            if offsets.dim() != 1 or offsets.dtype != torch.int32 or offsets.device != self.device \
+                    or not offsets.is_contiguous():
+                _refuse(f"offsets: need contiguous int32 [groups + 1] on {self.device}, got {offsets.dtype} "
+                        f"{tuple(offsets.shape)} on {offsets.device}")
         need = fp4_scale_bytes(self.fmt, self.mats, self.rows, self.cols,
-                               None if self.offsets is None else self.offsets.shape[0] - 1)
-        p_off = None
-        if self.offsets is not None:
-            if c.dim() != 2:
-                _refuse(f"{name}: rows in groups form one matrix")
-            p_off = _tensor(f"{name}.offsets", self.offsets, torch.int32, (self.offsets.shape[0],), c.device)
-        s = self.scales
-        if s.dtype != torch.uint8 or s.device != c.device or not s.is_contiguous() or s.numel() < need:
-            _refuse(f"{name}.scales: need {need} contiguous uint8 on {c.device}, got {s.dtype} {tuple(s.shape)} on "
-                    f"{s.device}")
-        return c.data_ptr(), s.data_ptr(), p_off
+                               None if offsets is None else offsets.shape[0] - 1)
+        if self.scales.numel() < need:
+            _refuse(f"scales: {self.scales.numel()} bytes, need {need}")
+        self._offsets = offsets
 
 
 def fp4_scale_bytes(fmt: int, n_mats: int, rows: int, cols: int, n_groups: int | None = None) -> int:
     """Bytes of the scale tiles of n_mats matrices, or of `rows` rows in n_groups groups."""
     if n_groups is None:
         n = lib().clover_fp4_scale_bytes(fmt, n_mats, rows, cols)
-        ok = n > 0 or n_mats == 0 or rows == 0
     else:
         n = lib().clover_fp4_grouped_scale_bytes(fmt, rows, n_groups, cols)
-        ok = n > 0
-    if not ok:
+    if n == 0 and (n_groups is not None or (n_mats != 0 and rows != 0)):
         raise CloverError(ERR_UNSUPPORTED_SHAPE, last_error())
     return n
 
@@ -493,46 +502,59 @@ def quantize_fp4(x, fmt: int = FP4_NV, scale_exp: int = 0, offsets=None, src_row
     """fp32 or bf16 matrices [rows][cols] or [mats][rows][cols] -> Fp4. With offsets (int32 [groups + 1]) the rows form
     groups: row i comes from x row src_rows[i] // src_div (src_rows int32, default i), as `route` lists them. `out` (an
     Fp4 this function returned before, for the same shapes) is reused."""
-    grouped = offsets is not None
-    if x.dim() == 3 and (grouped or not x.is_contiguous()):
-        _refuse("x: matrices must be contiguous, and grouped rows one matrix")
-    flat = x.view(-1, x.shape[-1]) if x.dim() == 3 else x
-    p_x, kind, ldx = _rows_of("x", flat)
-    dev, cols = x.device, x.shape[-1]
-    if not grouped and src_rows is not None:
-        _refuse("src_rows without offsets")
-    n_groups = offsets.shape[0] - 1 if grouped else None
-    n_mats, rows = (x.shape[0], x.shape[1]) if x.dim() == 3 else (1, x.shape[0] if src_rows is None else src_rows.shape[0])
-    if out is None:
-        scales = torch.empty(fp4_scale_bytes(fmt, n_mats, rows, cols, n_groups), dtype=torch.uint8, device=dev)
-        codes = torch.empty(x.shape[:-2] + (rows, cols // 2), dtype=torch.uint8, device=dev)
-        out = Fp4(fmt, codes, scales, scale_exp, offsets)
-    elif out.fmt != fmt or tuple(out.codes.shape) != x.shape[:-2] + (rows, cols // 2):
-        _refuse(f"out holds {tuple(out.codes.shape)} of format {out.fmt}")
+    shape, grouped = x.shape, offsets is not None
+    if len(shape) == 3:
+        if grouped or not x.is_contiguous():
+            _refuse("x: matrices must be contiguous, and grouped rows one matrix")
+        p_x, kind, ldx = _rows_of("x", x.view(-1, shape[-1]))
     else:
-        out.scale_exp, out.offsets = scale_exp, offsets
-    p_codes, p_scales, p_off = out._ptrs("out")
-    if out.codes.device != dev:
-        _refuse(f"out is on {out.codes.device}, x on {dev}")
-    L, st = lib(), _raw_stream(stream, dev)
+        p_x, kind, ldx = _rows_of("x", x)
+    dev, cols = x.device, shape[-1]
+    if src_rows is not None:
+        if not grouped:
+            _refuse("src_rows without offsets")
+        rows = src_rows.shape[0]
+        p_src = _tensor("src_rows", src_rows, torch.int32, (rows,), dev)
+    else:
+        rows, p_src = shape[-2], None
+    codes_shape = shape[:-2] + (rows, cols // 2)
+    n_groups = p_off = None
     if grouped:
-        p_src = None if src_rows is None else _tensor("src_rows", src_rows, torch.int32, (rows,), dev)
-        _check(L.clover_quantize_fp4_rows(fmt, p_x, kind, ldx, x.shape[0], cols, scale_exp, p_src, src_div, rows, p_off,
-                                          n_groups, p_codes, p_scales, st))
+        n_groups = offsets.shape[0] - 1
+        p_off = _tensor("offsets", offsets, torch.int32, (n_groups + 1,), dev)
+    if out is None:
+        mats = shape[0] if len(shape) == 3 else 1
+        n = fp4_scale_bytes(fmt, mats, rows, cols, n_groups)
+        out = Fp4._made(fmt, torch.empty(codes_shape, dtype=torch.uint8, device=dev),
+                        torch.empty(n, dtype=torch.uint8, device=dev), scale_exp, offsets, dev, mats, rows, cols)
+    elif out.fmt != fmt or out.codes.shape != codes_shape or out.device != dev:
+        _refuse(f"out holds {tuple(out.codes.shape)} of format {out.fmt} on {out.device}")
     else:
-        _check(L.clover_quantize_fp4(fmt, p_x, kind, ldx, n_mats, rows, cols, scale_exp, p_codes, p_scales, st))
+        out.offsets, out.scale_exp = offsets, scale_exp
+    if grouped:
+        rc = lib().clover_quantize_fp4_rows(fmt, p_x, kind, ldx, shape[0], cols, scale_exp, p_src, src_div, rows,
+                                            p_off, n_groups, out.codes.data_ptr(), out.scales.data_ptr(),
+                                            _raw_stream(stream, dev))
+    else:
+        rc = lib().clover_quantize_fp4(fmt, p_x, kind, ldx, out.mats, rows, cols, scale_exp, out.codes.data_ptr(),
+                                       out.scales.data_ptr(), _raw_stream(stream, dev))
+    _check(rc)
     return out
 
 
 def dequantize_fp4(q: Fp4, out=None, stream=None):
     """The bf16 matrices the codes stand for (rows behind the last group left as they were)."""
-    p_codes, p_scales, p_off = q._ptrs("q")
-    dev, shape = q.codes.device, tuple(q.codes.shape[:-1]) + (q.cols,)
+    dev, off = q.device, q.offsets
+    _on_current("q", dev)
+    shape = q.codes.shape[:-1] + (q.cols,)
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    p_out = _tensor("out", out, torch.bfloat16, shape, dev)
-    _check(lib().clover_dequantize_fp4(q.fmt, p_codes, p_scales, q.mats, q.rows, q.cols, q.scale_exp, p_off,
-                                       0 if p_off is None else q.offsets.shape[0] - 1, p_out, _raw_stream(stream, dev)))
+        p_out = out.data_ptr()
+    else:
+        p_out = _tensor("out", out, torch.bfloat16, shape, dev)
+    _check(lib().clover_dequantize_fp4(q.fmt, q.codes.data_ptr(), q.scales.data_ptr(), q.mats, q.rows, q.cols,
+                                       q.scale_exp, None if off is None else off.data_ptr(),
+                                       0 if off is None else off.shape[0] - 1, p_out, _raw_stream(stream, dev)))
     return out
 
 
@@ -546,27 +568,29 @@ def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_
     [rows][N], or with swiglu silu(gate) * up, [rows][N / 2]. b holds one [N][cols] matrix per group, or with swiglu two
     of N / 2 rows (gate, up). The result is scaled by alpha, group_alpha (fp32 [groups]) and both operands' scale_exp;
     rows behind the last group are left as they were."""
-    pa_codes, pa_scales, p_off = a._ptrs("a")
-    pb_codes, pb_scales, b_off = b._ptrs("b")
-    dev, per = a.codes.device, 2 if swiglu else 1
-    if a.codes.dim() != 2 or b_off is not None:
+    dev, off, per = a.device, a.offsets, 2 if swiglu else 1
+    _on_current("a", dev)
+    if a.codes.dim() != 2 or b.offsets is not None:
         _refuse("a must be one matrix, and only its rows may form groups")
-    if a.fmt != b.fmt or a.cols != b.cols or b.codes.device != dev:
+    if a.fmt != b.fmt or a.cols != b.cols or b.device != dev:
         _refuse(f"a (format {a.fmt}, {a.cols} columns, {dev}) does not match b (format {b.fmt}, {b.cols} columns, "
-                f"{b.codes.device})")
-    groups = 1 if p_off is None else a.offsets.shape[0] - 1
+                f"{b.device})")
+    rows, width = a.rows, b.rows
+    groups = 1 if off is None else off.shape[0] - 1
     if b.mats != groups * per:
         _refuse(f"b holds {b.mats} matrices for {groups} groups, {per} each")
-    rows, width = a.rows, b.rows
     if ws is None:
         ws = workspace(fp4_product_workspace_bytes(), dev)
     if out is None:
         out = torch.empty((rows, width), dtype=torch.bfloat16, device=dev)
+        p_out = out.data_ptr()
+    else:
+        p_out = _tensor("out", out, torch.bfloat16, (rows, width), dev)
     p_alpha = None if group_alpha is None else _tensor("group_alpha", group_alpha, torch.float32, (groups,), dev)
-    _check(lib().clover_fp4_product(a.fmt, pa_codes, pa_scales, rows, pb_codes, pb_scales, p_off, groups, width * per,
-                                    a.cols, alpha * 2.0 ** (a.scale_exp + b.scale_exp), p_alpha, int(swiglu),
-                                    _tensor("out", out, torch.bfloat16, (rows, width), dev), ws.data_ptr(), ws.numel(),
-                                    _raw_stream(stream, dev)))
+    _check(lib().clover_fp4_product(a.fmt, a.codes.data_ptr(), a.scales.data_ptr(), rows, b.codes.data_ptr(),
+                                    b.scales.data_ptr(), None if off is None else off.data_ptr(), groups, width * per,
+                                    a.cols, alpha * 2.0 ** (a.scale_exp + b.scale_exp), p_alpha, int(swiglu), p_out,
+                                    ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)))
     return out
 
 
@@ -575,15 +599,18 @@ def moe_combine(y, pos, w, x=None, shared=None, out=None, stream=None):
     gives them, x fp32 and shared bf16 [M][H] or None. out may be x itself."""
     if y.dim() != 2 or pos.dim() != 2:
         _refuse(f"y and pos must be matrices, got {tuple(y.shape)} and {tuple(pos.shape)}")
-    _on_current("y", y)
-    (M, K), (n, H), dev = pos.shape, y.shape, y.device
+    slots, (n, H), dev = pos.shape, y.shape, y.device
+    M, K = slots
+    _on_current("y", dev)
+    f32, bf16 = torch.float32, torch.bfloat16
     if out is None:
-        out = torch.empty((M, H), dtype=torch.float32, device=dev)
-    p_shared = None if shared is None else _tensor("shared", shared, torch.bfloat16, (M, H), dev)
-    p_x = None if x is None else _tensor("x", x, torch.float32, (M, H), dev)
-    _check(lib().clover_moe_combine(_tensor("y", y, torch.bfloat16, (n, H), dev), n,
-                                    _tensor("pos", pos, torch.int32, (M, K), dev),
-                                    _tensor("w", w, torch.float32, (M, K), dev), p_shared, p_x,
-                                    _tensor("out", out, torch.float32, (M, H), dev), M, K, H,
+        out = torch.empty((M, H), dtype=f32, device=dev)
+        p_out = out.data_ptr()
+    else:
+        p_out = _tensor("out", out, f32, (M, H), dev)
+    p_shared = None if shared is None else _tensor("shared", shared, bf16, (M, H), dev)
+    p_x = None if x is None else _tensor("x", x, f32, (M, H), dev)
+    _check(lib().clover_moe_combine(_tensor("y", y, bf16, (n, H), dev), n, _tensor("pos", pos, torch.int32, slots, dev),
+                                    _tensor("w", w, f32, slots, dev), p_shared, p_x, p_out, M, K, H,
                                     _raw_stream(stream, dev)))
     return out
