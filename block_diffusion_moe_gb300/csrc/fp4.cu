@@ -19,19 +19,49 @@ namespace {
 constexpr int kThreads = 256;  // 8 warps, one row each
 constexpr int kWarps = kThreads / 32;
 
-// Two values to two e2m1 codes (nearest, ties to the even code, at most 6),
-// `lo` in the low nibble.
-__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
+// Eight values to e2m1 codes (nearest, ties to the even code, at most 6), the
+// first in the lowest nibble.
+__device__ __forceinline__ uint32_t e2m1_word(const float (&v)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
 
-// The two e2m1 codes of a byte as two halves.
+// The two e2m1 codes of a byte as floats.
 __device__ __forceinline__ float2 e2m1_values(uint32_t byte) {
   uint32_t h;
   asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(byte));
   return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
+// 32 bytes per lane: one access where the address allows it (a whole sector per
+// lane; two of 16 bytes touch every sector twice).
+__device__ __forceinline__ void load32b(const void* p, bool wide, uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+  } else {
+    const uint4 u = static_cast<const uint4*>(p)[0], v = static_cast<const uint4*>(p)[1];
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w, w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
+  }
+}
+__device__ __forceinline__ void store32b(void* p, bool wide, const uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "l"(p)
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 // The row of the scale tiles that belongs to row i, by one warp. False for a
@@ -54,17 +84,6 @@ __device__ __forceinline__ bool scale_row(const Fp4QuantArgs& a, int64_t i, int 
   return true;
 }
 
-template <bool kBf16>
-struct Src;
-template <>
-struct Src<true> {
-  using T = __nv_bfloat16;
-};
-template <>
-struct Src<false> {
-  using T = float;
-};
-
 }  // namespace
 
 // One warp per row, one lane per block of columns: a block's values stay in
@@ -75,11 +94,23 @@ struct Src<false> {
 // input: the correctly rounded quotient lies on the same side of every border
 // (or on it) as the exact one, as border * s has 7 significant bits. NV with
 // bf16 input: a quotient that is not on a border is at least 2^-9 of it away,
-// so y * (1 / s), which is off by at most 2^-23, is rounded to a multiple of
-// 2^-14 (the borders are multiples of 2^-2): a tie becomes exactly a tie.
+// far more than x * (1 / s) is off; on a border, with 1 / s rounded up and the
+// product cut off, the product is the border itself (for each of the 8
+// significands a scale can have and each border). The same holds for amax / 6
+// and the midpoints between scales.
 template <bool kMx, bool kBf16>
 __global__ void __launch_bounds__(kThreads) k_quantize_fp4(const Fp4QuantArgs a) {
   constexpr int kBlock = kMx ? 32 : 16;
+  constexpr int kWords = kBlock * (kBf16 ? 2 : 4) / 4;  // of a block's input
+  // NV, bf16: 2^-scale_exp / s, rounded up, for each scale byte (0 for none)
+  __shared__ float s_inv[128];
+  if (!kMx && kBf16) {
+    if (threadIdx.x < 128) {
+      const float s = e4m3_to_float(threadIdx.x);
+      s_inv[threadIdx.x] = s > 0.f ? __frcp_ru(s) * a.mul : 0.f;
+    }
+    __syncthreads();
+  }
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
@@ -92,78 +123,63 @@ __global__ void __launch_bounds__(kThreads) k_quantize_fp4(const Fp4QuantArgs a)
     if (a.src_rows != nullptr) src = a.src_rows[i] < 0 ? -1 : a.src_rows[i] / a.src_div;
     if (src >= a.n_src) src = -1;
   }
-  const typename Src<kBf16>::T* row = static_cast<const typename Src<kBf16>::T*>(a.x) + src * a.ldx;
+  const uint8_t* row = static_cast<const uint8_t*>(a.x) + src * a.ldx * (kBf16 ? 2 : 4);
   const int nb = a.cols / kBlock, ct = (nb + 3) / 4;
   uint8_t* tile = a.scales + (sr / 128) * ct * 512 + (sr % 32) * 16 + (sr % 128) / 32 * 4;
   uint8_t* codes = a.codes + i * (a.cols / 2);
+  const bool wide = a.wide, unit = a.mul == 1.f;
+#pragma unroll 2
   for (int b = lane; b < nb; b += 32) {
-    float y[kBlock];
-    uint32_t top = 0;  // largest |x| as bits: NaN above infinity above every number
-    if (src < 0) {
+    uint32_t in[kWords];
+    if (src >= 0) {
 #pragma unroll
-      for (int j = 0; j < kBlock; ++j) y[j] = 0.f;
-    } else if (kBf16) {
-      const uint4* p = reinterpret_cast<const uint4*>(row + b * kBlock);
-#pragma unroll
-      for (int v = 0; v < kBlock / 8; ++v) {
-        const uint4 u = p[v];
-        const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          y[8 * v + 2 * j] = __uint_as_float(wd[j] << 16);
-          y[8 * v + 2 * j + 1] = __uint_as_float(wd[j] & 0xFFFF0000u);
-        }
-      }
+      for (int v = 0; v < kWords / 8; ++v)
+        load32b(row + b * (kWords * 4) + v * 32, wide, *reinterpret_cast<uint32_t(*)[8]>(&in[8 * v]));
     } else {
-      const float4* p = reinterpret_cast<const float4*>(row + b * kBlock);
 #pragma unroll
-      for (int v = 0; v < kBlock / 4; ++v) {
-        const float4 u = p[v];
-        y[4 * v] = u.x, y[4 * v + 1] = u.y, y[4 * v + 2] = u.z, y[4 * v + 3] = u.w;
-      }
+      for (int v = 0; v < kWords; ++v) in[v] = 0;
     }
+    // largest |x| as bits: NaN above infinity above every number
+    uint32_t top = 0;
 #pragma unroll
-    for (int j = 0; j < kBlock; ++j) {
-      y[j] *= a.mul;
-      top = max(top, __float_as_uint(y[j]) & 0x7FFFFFFFu);
-    }
-    const bool finite = top < 0x7F800000u;
-    const float amax = __uint_as_float(top);
+    for (int v = 0; v < kWords; ++v)
+      top = kBf16 ? __vmaxu2(top, in[v] & 0x7FFF7FFFu) : max(top, in[v] & 0x7FFFFFFFu);
+    if (kBf16) top = max(top << 16, top & 0xFFFF0000u);
+    const float amax = __uint_as_float(top) * a.mul;
+    const bool finite = __float_as_uint(amax) < 0x7F800000u;
     uint32_t sb;
-    float s, inv;
+    float s = 0.f, inv = 0.f;
     if (kMx) {
-      const int e = max(static_cast<int>(top >> 23) - 129, -127);  // floor(log2 amax) - 2 (subnormals: -127)
+      // floor(log2 amax) - 2; subnormals: -127
+      const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 129, -127);
       sb = finite ? static_cast<uint32_t>(e + 127) : 0xFFu;
       inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      s = 0.f;
     } else {
-      sb = finite ? __nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.0f), __NV_SATFINITE, __NV_E4M3) : 0x7Fu;
-      s = e4m3_to_float(sb);
-      inv = s > 0.f ? __frcp_rn(s) : 0.f;
+      const float sixth = kBf16 ? __fmul_rz(amax, 0x1.555556p-3f) : __fdiv_rn(amax, 6.0f);
+      sb = finite ? __nv_cvt_float_to_fp8(sixth, __NV_SATFINITE, __NV_E4M3) : 0x7Fu;
+      if (kBf16)
+        inv = s_inv[sb & 127u];
+      else
+        s = e4m3_to_float(sb);
     }
+    const bool coded = finite && (kMx || sb != 0);
     uint32_t words[kBlock / 8];
 #pragma unroll
     for (int wd = 0; wd < kBlock / 8; ++wd) {
-      uint32_t word = 0;
+      float q[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float q[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float v = y[8 * wd + 2 * j + h];
-          if (kMx) {
-            q[h] = v * inv;
-          } else if (kBf16) {
-            // |v| first: the sum below would lose the sign of a small one
-            const float m = __fadd_rn(__fmaf_rn(fabsf(v), inv, 768.0f), -768.0f);
-            q[h] = copysignf(m, v);
-          } else {
-            q[h] = inv > 0.f ? __fdiv_rn(v, s) : 0.f;
-          }
-        }
-        word |= e2m1_pair(q[0], q[1]) << (8 * j);
+      for (int j = 0; j < 8; ++j) {
+        const int k = 8 * wd + j;
+        const float v = kBf16 ? __uint_as_float(k % 2 == 0 ? in[k / 2] << 16 : in[k / 2] & 0xFFFF0000u)
+                              : __uint_as_float(in[k]);
+        if (kMx)
+          q[j] = unit ? v * inv : v * a.mul * inv;
+        else if (kBf16)
+          q[j] = __fmul_rz(v, inv);
+        else
+          q[j] = s > 0.f ? __fdiv_rn(v * a.mul, s) : 0.f;
       }
-      words[wd] = (finite && (kMx || inv > 0.f)) ? word : 0u;
+      words[wd] = coded ? e2m1_word(q) : 0u;
     }
     if (kMx)
       *reinterpret_cast<uint4*>(codes + b * 16) = make_uint4(words[0], words[1], words[kMx ? 2 : 0], words[kMx ? 3 : 1]);
@@ -186,6 +202,7 @@ __global__ void __launch_bounds__(kThreads) k_dequantize_fp4(const Fp4QuantArgs 
   const int ct = ((kMx ? a.cols / 32 : a.cols / 16) + 3) / 4;
   const uint8_t* tile = a.scales + (sr / 128) * ct * 512 + (sr % 32) * 16 + (sr % 128) / 32 * 4;
   const uint8_t* codes = a.codes + i * (a.cols / 2);
+#pragma unroll 2
   for (int c = lane; c < a.cols / 16; c += 32) {
     const int b = kMx ? c / 2 : c;
     const uint32_t sb = tile[(b / 4) * 512 + b % 4];
@@ -198,9 +215,7 @@ __global__ void __launch_bounds__(kThreads) k_dequantize_fp4(const Fp4QuantArgs 
       const __nv_bfloat162 p = __floats2bfloat162_rn(v.x * s * a.mul, v.y * s * a.mul);
       o[j] = *reinterpret_cast<const uint32_t*>(&p);
     }
-    uint4* dst = reinterpret_cast<uint4*>(a.out + i * a.cols + c * 16);
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    store32b(a.out + i * a.cols + c * 16, a.wide, o);
   }
 }
 
@@ -208,13 +223,17 @@ namespace {
 dim3 row_grid(const Fp4QuantArgs& a) { return dim3(static_cast<unsigned>((a.n_rows + kWarps - 1) / kWarps)); }
 }  // namespace
 
-cudaError_t launch_quantize_fp4(const Fp4QuantArgs& a, bool mx, cudaStream_t s) {
+cudaError_t launch_quantize_fp4(const Fp4QuantArgs& args, bool mx, cudaStream_t s) {
+  Fp4QuantArgs a = args;
+  a.wide = reinterpret_cast<uintptr_t>(a.x) % 32 == 0 && a.ldx * (a.bf16_x ? 2 : 4) % 32 == 0;
   void (*k)(const Fp4QuantArgs) = mx ? (a.bf16_x ? k_quantize_fp4<true, true> : k_quantize_fp4<true, false>)
                                      : (a.bf16_x ? k_quantize_fp4<false, true> : k_quantize_fp4<false, false>);
   return launch_kernel(k, row_grid(a), dim3(kThreads), 0, s, true, a);
 }
 
-cudaError_t launch_dequantize_fp4(const Fp4QuantArgs& a, bool mx, cudaStream_t s) {
+cudaError_t launch_dequantize_fp4(const Fp4QuantArgs& args, bool mx, cudaStream_t s) {
+  Fp4QuantArgs a = args;
+  a.wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
   void (*k)(const Fp4QuantArgs) = mx ? k_dequantize_fp4<true> : k_dequantize_fp4<false>;
   return launch_kernel(k, row_grid(a), dim3(kThreads), 0, s, true, a);
 }

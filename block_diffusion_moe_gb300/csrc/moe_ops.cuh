@@ -34,7 +34,8 @@ struct RouteOpArgs {
   int cta_tokens;    // tokens per CTA, a multiple of 8, at most kRouteOpCtaTokens
   int n_ctas;
   int vec;          // set by the launch: whole vectors of logits per lane
-  int group_lanes;  // set by the launch: lanes that hold one expert group, or 0
+  int group_size;   // set by the launch: experts per group
+  int group_shift;  // set by the launch: log2 of the lanes that hold one group, or -1
 };
 
 // CTAs and tokens per CTA of the selection kernel for M >= 1 tokens.
@@ -76,6 +77,7 @@ struct Fp4QuantArgs {
   uint8_t* codes;           // [n_rows][cols / 2]
   uint8_t* scales;          // tiles
   __nv_bfloat16* out;       // dequantise: [n_rows][cols]
+  int wide;                 // set by the launch: 32-byte accesses to x (out) are aligned
 };
 
 cudaError_t launch_quantize_fp4(const Fp4QuantArgs& a, bool mx, cudaStream_t s);

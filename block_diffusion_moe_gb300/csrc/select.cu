@@ -17,6 +17,7 @@ constexpr uint32_t kAll = 0xffffffffu;
 // Largest K + 1 that is selected by counting (select_token): beyond it the
 // keys above the bound no longer fit 32 lanes as a rule.
 constexpr int kCountedMax = 17;
+constexpr int kNoGroup = 64;  // rank of a lane that holds no group
 constexpr int kListBytes = 256;  // a warp's list of 32 keys and ids
 
 // +inf counts as the largest finite value, NaN as -inf.
@@ -92,144 +93,250 @@ __device__ __forceinline__ int order_int(float v) {
 }
 __device__ __forceinline__ float order_float(int m) { return __int_as_float(m ^ ((m >> 31) & 0x7fffffff)); }
 
-__device__ __forceinline__ float warp_max_t(float v) { return order_float(__reduce_max_sync(kAll, order_int(v))); }
-__device__ __forceinline__ double warp_max_t(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(kAll, v, o));
-  return v;
+__device__ __forceinline__ float warp_max_fast(float v) { return order_float(__reduce_max_sync(kAll, order_int(v))); }
+
+// The same for doubles (-0 first made 0, so that the two tie).
+__device__ __forceinline__ int64_t order_int64(double v) {
+  const int64_t b = __double_as_longlong(v + 0.0);
+  return b ^ ((b >> 63) & 0x7fffffffffffffffLL);
 }
-__device__ __forceinline__ float warp_sum_t(float v) { return warp_sum_f(v); }
-__device__ __forceinline__ double warp_sum_t(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  return v;
+__device__ __forceinline__ double order_double(int64_t m) {
+  return __longlong_as_double(m ^ ((m >> 63) & 0x7fffffffffffffffLL));
 }
-__device__ __forceinline__ float exp_t(float v) { return expf(v); }
-__device__ __forceinline__ double exp_t(double v) { return exp(v); }
-__device__ __forceinline__ float sigmoid_t(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
-__device__ __forceinline__ double sigmoid_t(double v) { return 1.0 / (1.0 + exp(-v)); }
+
+__device__ __forceinline__ float fast_sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
 // (b1, b2): the two largest of a set, kept up to date with v
-template <typename T>
-__device__ __forceinline__ void two_best(T& b1, T& b2, T v) {
-  b2 = fmax(b2, fmin(b1, v));
-  b1 = fmax(b1, v);
+__device__ __forceinline__ void two_best(float& b1, float& b2, float v) {
+  b2 = fmaxf(b2, fminf(b1, v));
+  b1 = fmaxf(b1, v);
 }
 
-// What experts are ordered by, in T: -inf for a dead expert and for one in a
-// group that does not stay. x: the logits, -inf where dead. False where the
-// token has no live expert (every lane alike).
+// What experts are ordered by: -inf for a dead expert and for one in a group
+// that does not stay. x: the logits, -inf where dead. False where the token has
+// no live expert (every lane alike).
 //
-// In float, *err bounds the error of a key, and *doubt is set in some lane
-// where two groups' ranks are closer than the errors they can have. A score's
-// error is below 2^-19 of the largest score (softmax: exp and quotient a few
-// roundings each, the sum up to 21; sigmoid: the fast exp's error grows with
-// -logit, a multiple of 2^-22 of it, which s * -logit bounds by that of the
-// largest score), the sum with the bias adds half a unit of the key. Logits
-// used as keys are exact.
-template <int VPL, typename T>
+// *err bounds the error of a key, and *doubt is set (in every lane) where the
+// ranks on either side of the group border are closer than the errors they can
+// have. A score's error is below 2^-19 of the largest score (softmax: exp and
+// quotient a few roundings each, the sum up to 21; sigmoid: the fast exp's
+// error grows with -logit, a multiple of 2^-22 of it, which s * -logit bounds
+// by that of the largest score), the sum with the bias adds half a unit of the
+// key. Logits used as keys are exact.
+template <int VPL>
 __device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float (&x)[VPL], const float (&bias)[VPL],
-                                           float bias_max, double* smem, int lane, T (&key)[VPL], T* err, bool* doubt) {
-  constexpr bool kExact = sizeof(T) == 8;
-  const T ninf = -static_cast<T>(INFINITY);
-  *err = 0;
+                                           float bias_max, float* smem, int lane, float (&key)[VPL], float* err,
+                                           bool* doubt) {
+  *err = 0.f;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) key[i] = static_cast<T>(x[i]);
+  for (int i = 0; i < VPL; ++i) key[i] = x[i];
   const bool sums = a.n_groups > 1 && a.group_rank == 2;  // ranks are sums of scores
   if (a.bias != nullptr || sums) {
     float xm = x[0], xl = x[0];
 #pragma unroll
     for (int i = 1; i < VPL; ++i) xm = fmaxf(xm, x[i]), xl = fminf(xl, x[i]);
-    xm = warp_max_t(xm);
+    xm = warp_max_fast(xm);
     if (xm == -INFINITY) return false;
-    T s_max;
+    float s_max;
     if (a.softmax) {
-      T sum = 0;
+      float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        key[i] = exp_t(static_cast<T>(x[i]) - static_cast<T>(xm));
+        key[i] = expf(x[i] - xm);
         sum += key[i];
       }
-      sum = warp_sum_t(sum);  // at least 1
-      s_max = static_cast<T>(1) / sum;
+      s_max = 1.f / warp_sum_f(sum);  // the sum is at least 1
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = kExact ? key[i] / sum : key[i] * s_max;
+      for (int i = 0; i < VPL; ++i) key[i] *= s_max;
     } else {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = sigmoid_t(static_cast<T>(x[i]));
-      s_max = sigmoid_t(static_cast<T>(xm)) * (1 + static_cast<T>(fmaxf(-xm, 0.f)) * static_cast<T>(0.25));
+      for (int i = 0; i < VPL; ++i) key[i] = fast_sigmoid(x[i]);
+      s_max = fast_sigmoid(xm) * (1.f + fmaxf(-xm, 0.f) * 0.25f);
     }
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] += static_cast<T>(bias[i]);
+    for (int i = 0; i < VPL; ++i) key[i] += bias[i];
     if (__any_sync(kAll, xl == -INFINITY)) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = x[i] > -INFINITY ? key[i] : ninf;
+      for (int i = 0; i < VPL; ++i) key[i] = x[i] > -INFINITY ? key[i] : -INFINITY;
     }
-    if (!kExact)
-      *err = s_max * static_cast<T>(1.9e-6) + (s_max + bias_max) * static_cast<T>(1.2e-7) + static_cast<T>(1e-37);
+    *err = s_max * 1.9e-6f + (s_max + bias_max) * 1.2e-7f + 1e-37f;
   }
   if (a.n_groups == 1) return true;
 
   // Group ranks. Without a bias experts go by their logits, whatever the
   // groups go by.
-  const int size = a.E / a.n_groups;
-  T b1 = ninf, b2 = ninf;
-  int g, step;  // this lane's group, and the lanes from one group to the next
-  if (a.group_lanes > 0) {
+  float b1 = -INFINITY, b2 = -INFINITY;
+  int g = lane, shift = 0;  // this lane's group; groups lie 2^shift lanes apart
+  if (a.group_shift >= 0) {
     // a group is all slots of a power of two of neighbouring lanes
 #pragma unroll
     for (int i = 0; i < VPL; ++i) two_best(b1, b2, key[i]);
-    for (int o = 1; o < a.group_lanes; o <<= 1) {
-      const T c1 = __shfl_xor_sync(kAll, b1, o), c2 = __shfl_xor_sync(kAll, b2, o);
+    shift = a.group_shift;
+    g = lane >> shift;
+    for (int o = 1; o < (1 << shift); o <<= 1) {
+      const float c1 = __shfl_xor_sync(kAll, b1, o), c2 = __shfl_xor_sync(kAll, b2, o);
       two_best(b1, b2, c1);
-      b2 = fmax(b2, c2);
+      b2 = fmaxf(b2, c2);
     }
-    step = a.group_lanes;
-    g = lane / step;
   } else {
     // any other size: keys in shared memory, lane g scans group g
-    T* s_keys = reinterpret_cast<T*>(smem);
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (lane * VPL + i < a.E) s_keys[lane * VPL + i] = key[i];
+      if (lane * VPL + i < a.E) smem[lane * VPL + i] = key[i];
     __syncwarp();
-    step = 1;
-    g = lane;
     if (g < a.n_groups)
-      for (int n = 0; n < size; ++n) two_best(b1, b2, s_keys[g * size + n]);
+      for (int n = 0; n < a.group_size; ++n) two_best(b1, b2, smem[g * a.group_size + n]);
     __syncwarp();
   }
-  const T rank = (a.group_rank == 2 && b2 > ninf) ? b1 + b2 : b1;
+  const float rank = (a.group_rank == 2 && b2 > -INFINITY) ? b1 + b2 : b1;
   // the groups before this one; a group's lanes share the comparisons
-  const T tol = *err * (a.group_rank == 2 ? 4 : 2);
+  const int step = 1 << shift;
   int before = 0;
   for (int j0 = 0; j0 < a.n_groups; j0 += step) {
-    const int j = j0 + lane % step;
-    const T r = __shfl_sync(kAll, rank, (j * step) & 31);
-    const bool other = j < a.n_groups && j != g;
-    before += (other && (r > rank || (r == rank && j < g))) ? 1 : 0;
-    if (!kExact && other && g < a.n_groups && tol > 0 && (r > ninf || rank > ninf) && !(fabs(r - rank) > tol)) *doubt = true;
+    const int j = j0 + (lane & (step - 1));
+    const float r = __shfl_sync(kAll, rank, (j << shift) & 31);
+    before += (j < a.n_groups && (r > rank || (r == rank && j < g))) ? 1 : 0;
   }
   for (int o = 1; o < step; o <<= 1) before += __shfl_xor_sync(kAll, before, o);
+  if (g >= a.n_groups) before = kNoGroup;
+  if (*err > 0.f) {
+    // the last group that stays and the first that does not
+    const float in = __shfl_sync(kAll, rank, __ffs(__ballot_sync(kAll, before == a.top_groups - 1)) - 1);
+    const float out = __shfl_sync(kAll, rank, __ffs(__ballot_sync(kAll, before == a.top_groups)) - 1);
+    *doubt = out > -INFINITY && !(in - out > (a.group_rank == 2 ? 4.f : 2.f) * *err);
+  }
   if (a.bias == nullptr) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = static_cast<T>(x[i]);
-    *err = 0;
+    for (int i = 0; i < VPL; ++i) key[i] = x[i];
+    *err = 0.f;
   }
-  if (a.group_lanes > 0) {
+  if (a.group_shift >= 0) {
     if (before >= a.top_groups) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = ninf;
+      for (int i = 0; i < VPL; ++i) key[i] = -INFINITY;
     }
   } else {
     const uint32_t mask = __ballot_sync(kAll, before < a.top_groups);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = lane * VPL + i;
-      if (e < a.E && ((mask >> (e / size)) & 1u) == 0) key[i] = ninf;
+      if (e < a.E && ((mask >> (e / a.group_size)) & 1u) == 0) key[i] = -INFINITY;
     }
   }
   return true;
+}
+
+// ---- The order in exact arithmetic: in double, as the definition has it. Rare
+// (a few tokens in a thousand), so written for little code, not for speed.
+
+struct SoftmaxSum {
+  double max, sum;
+};
+
+__device__ __noinline__ SoftmaxSum softmax_sum(const RouteOpArgs& a, int64_t row, int lane) {
+  float m = -INFINITY;
+  for (int e = lane; e < a.E; e += 32) m = fmaxf(m, load_logit(a, row, e));
+  SoftmaxSum r;
+  r.max = warp_max_f(m);
+  r.sum = 0;
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 32) {
+    const float z = load_logit(a, row, e);
+    if (z > -INFINITY) r.sum += exp(static_cast<double>(z) - r.max);
+  }
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) r.sum += __shfl_xor_sync(kAll, r.sum, o);
+  return r;
+}
+
+// Score + bias of expert e, -inf where dead.
+__device__ __noinline__ double exact_total(const RouteOpArgs& a, int64_t row, int e, SoftmaxSum s) {
+  const float z = load_logit(a, row, e);
+  const float b = a.bias != nullptr ? a.bias[e] : 0.f;
+  if (!(z > -INFINITY && b > -INFINITY)) return -static_cast<double>(INFINITY);
+  const double t = exp(a.softmax ? static_cast<double>(z) - s.max : -static_cast<double>(z));
+  return (a.softmax ? t / s.sum : 1.0 / (1.0 + t)) + static_cast<double>(b);
+}
+
+// Lane k < n holds candidate id; returns the candidate of rank k by exact key,
+// the lower id first on ties.
+__device__ __noinline__ int rank_exact(const RouteOpArgs& a, int64_t row, int id, int n, int lane, int64_t* smem) {
+  SoftmaxSum s = {0, 1};
+  if (a.softmax) s = softmax_sum(a, row, lane);
+  const int64_t own = lane < n ? order_int64(exact_total(a, row, id, s)) : INT64_MIN;
+  smem[lane] = own;
+  __syncwarp();
+  int before = 0;
+  for (int j = 0; j < n; ++j) {
+    const int64_t o = smem[j];
+    const int f = __shfl_sync(kAll, id, j);
+    before += (o > own || (o == own && f < id)) ? 1 : 0;
+  }
+  __syncwarp();
+  int32_t* order = reinterpret_cast<int32_t*>(smem);
+  if (lane < n) order[before] = id;
+  __syncwarp();
+  const int r = lane < n ? order[lane] : -1;
+  __syncwarp();
+  return r;
+}
+
+// The whole selection: lane k < K returns the k-th expert (-1: none left).
+// smem: E numbers.
+__device__ __noinline__ int select_exact(const RouteOpArgs& a, int64_t row, int lane, int64_t* smem) {
+  const int64_t ninf = order_int64(-static_cast<double>(INFINITY));
+  SoftmaxSum s = {0, 1};
+  if (a.softmax) s = softmax_sum(a, row, lane);
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 32) smem[e] = order_int64(exact_total(a, row, e, s));
+  __syncwarp();
+  uint32_t mask = kAll;
+  if (a.n_groups > 1) {
+    int64_t b1 = ninf, b2 = ninf;
+    if (lane < a.n_groups)
+#pragma unroll 1
+      for (int n = 0; n < a.group_size; ++n) {
+        const int64_t v = smem[lane * a.group_size + n];
+        b2 = max(b2, min(b1, v));
+        b1 = max(b1, v);
+      }
+    const int64_t rank = (a.group_rank == 2 && b2 > ninf) ? order_int64(order_double(b1) + order_double(b2)) : b1;
+    int before = 0;
+#pragma unroll 1
+    for (int j = 0; j < a.n_groups; ++j) {
+      const int64_t r = __shfl_sync(kAll, rank, j);
+      before += (r > rank || (r == rank && j < lane)) ? 1 : 0;
+    }
+    mask = __ballot_sync(kAll, before < a.top_groups);
+    __syncwarp();
+  }
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 32) {
+    if (a.bias == nullptr) smem[e] = order_int64(static_cast<double>(load_logit(a, row, e)));
+    if (a.n_groups > 1 && ((mask >> (e / a.group_size)) & 1u) == 0) smem[e] = ninf;
+  }
+  __syncwarp();
+  int mine = -1;
+#pragma unroll 1
+  for (int k = 0; k < a.K; ++k) {
+    int64_t best = ninf;
+    int at = 0x7fffffff;
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 32)
+      if (smem[e] > best) {
+        best = smem[e];
+        at = e;
+      }
+    int64_t top = best;
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) top = max(top, static_cast<int64_t>(__shfl_xor_sync(kAll, top, o)));
+    if (top == ninf) break;  // uniform: no live expert left
+    const int id = __reduce_min_sync(kAll, best == top ? at : 0x7fffffff);
+    if (lane == k) mine = id;
+    if (lane == (id & 31)) smem[id] = ninf;
+    __syncwarp();
+  }
+  return mine;
 }
 
 // Whether two experts' keys, closer than their errors, are a true tie: the
@@ -240,15 +347,15 @@ __device__ __forceinline__ bool same_key(const RouteOpArgs& a, int64_t row, int 
 
 // The first `want` experts by descending key, ties to the lower id: lane k
 // returns the k-th (-1: none left). Each round takes the largest key and the
-// lowest lane, so the lowest id, that holds it.
-template <int VPL, typename T>
-__device__ __forceinline__ int pick_by_rounds(const RouteOpArgs& a, int64_t row, T (&key)[VPL], int want, T err,
+// lowest lane, so the lowest id, that holds it. *doubt is set where two
+// successive keys are closer than their errors.
+template <int VPL>
+__device__ __forceinline__ int pick_by_rounds(const RouteOpArgs& a, int64_t row, float (&key)[VPL], int want, float err,
                                               int lane, bool* doubt) {
-  const T ninf = -static_cast<T>(INFINITY);
   int mine = -1, last_id = -1;
-  T last = 0;
+  float last = 0.f;
   for (int k = 0; k < want; ++k) {
-    T best = ninf;
+    float best = -INFINITY;
     int at = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
@@ -256,18 +363,18 @@ __device__ __forceinline__ int pick_by_rounds(const RouteOpArgs& a, int64_t row,
         best = key[i];
         at = i;
       }
-    const T top = warp_max_t(best);
-    if (!(top > ninf)) break;  // uniform: no live expert left
+    const float top = warp_max_fast(best);
+    if (!(top > -INFINITY)) break;  // uniform: no live expert left
     const int from = __ffs(__ballot_sync(kAll, best == top)) - 1;
     const int id = __shfl_sync(kAll, lane * VPL + at, from);
-    if (k > 0 && err > 0 && !(last - top > 2 * err) && !same_key(a, row, last_id, id)) *doubt = true;
+    if (k > 0 && err > 0.f && !(last - top > 2.f * err) && !same_key(a, row, last_id, id)) *doubt = true;
     last = top;
     last_id = id;
     if (lane == k) mine = id;
     if (lane == from) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (i == at) key[i] = ninf;
+        if (i == at) key[i] = -INFINITY;
     }
   }
   return mine;
@@ -276,10 +383,13 @@ __device__ __forceinline__ int pick_by_rounds(const RouteOpArgs& a, int64_t row,
 // The same by counting: the want-th largest of the 32 lanes' maxima is a lower
 // bound of the want-th largest key; the few keys at or above it (as a rule
 // want to want + 4) are listed in shared memory, one per lane, and each lane
-// counts how many come before its own. False where more than 32 qualify.
+// counts how many come before its own. With inexact keys the bound is lowered
+// by twice their error, so that the list holds the first want - 1 of the exact
+// order too; where two successive ones are in doubt the list is ranked again
+// by exact keys. False where more than 32 keys qualify.
 template <int VPL>
 __device__ __forceinline__ bool pick_by_count(const RouteOpArgs& a, int64_t row, const float (&key)[VPL], int want,
-                                              float err, double* smem, int lane, int* mine, bool* doubt) {
+                                              float err, int64_t* smem, int lane, int* mine) {
   float best = key[0];
 #pragma unroll
   for (int i = 1; i < VPL; ++i) best = fmaxf(best, key[i]);
@@ -291,7 +401,8 @@ __device__ __forceinline__ bool pick_by_count(const RouteOpArgs& a, int64_t row,
     m = m == bound_int ? kNone : m;
   }
   // at least the lowest finite float: dead experts are not listed
-  const float bound = fmaxf(order_float(bound_int == kNone ? order_int(-INFINITY) : bound_int), -3.402823466e+38f);
+  float bound = bound_int == kNone ? -INFINITY : order_float(bound_int);
+  bound = fmaxf(bound - 2.f * err, -3.402823466e+38f);
   int c = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) c += key[i] >= bound ? 1 : 0;
@@ -332,44 +443,33 @@ __device__ __forceinline__ bool pick_by_count(const RouteOpArgs& a, int64_t row,
   __syncwarp();
   own = sorted[lane];
   __syncwarp();
-  const int id = own != 0 ? static_cast<int>(0xffffu - static_cast<uint32_t>(own & 0xffffu)) : -1;
-  *mine = lane < want ? id : -1;
-  if (err > 0) {
+  int id = own != 0 ? static_cast<int>(0xffffu - static_cast<uint32_t>(own & 0xffffu)) : -1;
+  if (err > 0.f) {
     const float k0 = order_float(static_cast<int>(static_cast<uint32_t>(own >> 32) ^ 0x80000000u));
     const float next = __shfl_down_sync(kAll, k0, 1);
     const int next_id = __shfl_down_sync(kAll, id, 1);
-    if (lane + 1 < min(n, want) && !(k0 - next > 2 * err) && !same_key(a, row, id, next_id)) *doubt = true;
+    const bool doubt = lane + 1 < min(n, want) && !(k0 - next > 2.f * err) && !same_key(a, row, id, next_id);
+    if (__any_sync(kAll, doubt)) id = rank_exact(a, row, id, n, lane, smem);
   }
+  *mine = id;
   return true;
 }
 
 // One token's selection by one warp: lane k < K returns the k-th selected
 // expert (-1: none left). Worked out in float; where some comparison is closer
-// than the errors allow (*doubt in any lane), again in double, whose order is
-// the definition's.
-template <int VPL>
-__device__ __noinline__ int select_token_exact(const RouteOpArgs& a, int64_t row, double* smem, int lane) {
-  float x[VPL], bias[VPL];
-  load_row<VPL>(a, row, lane, x);
-  load_bias<VPL>(a, lane, bias);
-  double key[VPL], err;
-  bool doubt = false;
-  if (!token_keys<VPL, double>(a, x, bias, 0.f, smem, lane, key, &err, &doubt)) return -1;
-  return pick_by_rounds<VPL, double>(a, row, key, a.K, 0.0, lane, &doubt);
-}
-
+// than the errors allow, again in double, whose order is the definition's.
 template <int VPL>
 __device__ __forceinline__ int select_token(const RouteOpArgs& a, int64_t row, const float (&x)[VPL],
-                                            const float (&bias)[VPL], float bias_max, double* smem, int lane) {
+                                            const float (&bias)[VPL], float bias_max, int64_t* smem, int lane) {
   float key[VPL], err;
   bool doubt = false;
-  if (!token_keys<VPL, float>(a, x, bias, bias_max, smem, lane, key, &err, &doubt)) return -1;
+  if (!token_keys<VPL>(a, x, bias, bias_max, reinterpret_cast<float*>(smem), lane, key, &err, &doubt)) return -1;
   // with inexact keys one more than K, to see the key that just missed
-  const int want = err > 0 ? a.K + 1 : a.K;
-  int mine;
-  if (want > kCountedMax || !pick_by_count<VPL>(a, row, key, want, err, smem, lane, &mine, &doubt))
-    mine = pick_by_rounds<VPL, float>(a, row, key, want, err, lane, &doubt);
-  if (__any_sync(kAll, doubt)) mine = select_token_exact<VPL>(a, row, smem, lane);
+  const int want = err > 0.f ? a.K + 1 : a.K;
+  int mine = -1;
+  if (!doubt && (want > kCountedMax || !pick_by_count<VPL>(a, row, key, want, err, smem, lane, &mine)))
+    mine = pick_by_rounds<VPL>(a, row, key, want, err, lane, &doubt);
+  if (doubt) mine = select_exact(a, row, lane, smem);
   return lane < a.K ? mine : -1;
 }
 
@@ -387,7 +487,7 @@ __device__ __forceinline__ float token_weight(const RouteOpArgs& a, const float 
 #pragma unroll
       for (int i = 0; i < VPL; ++i) m = fmaxf(m, x[i]);
     }
-    m = warp_max_t(m);
+    m = warp_max_fast(m);
     num = on ? expf(z - m) : 0.f;
     if (!a.renormalise) {
       sum = 0.f;
@@ -397,16 +497,17 @@ __device__ __forceinline__ float token_weight(const RouteOpArgs& a, const float 
     }
   } else {
     float t = fminf(z, 0.f);
-    if (a.renormalise && __any_sync(kAll, on && t < -60.f)) t -= warp_max_t(on ? t : -INFINITY);
+    if (a.renormalise && __any_sync(kAll, on && t < -60.f)) t -= warp_max_fast(on ? t : -INFINITY);
     num = on ? __fdividef(expf(t), 1.f + expf(-fabsf(z))) : 0.f;
   }
   if (a.renormalise) sum = warp_sum_f(num);
   return on ? __fdividef(num, sum) * a.scale : 0.f;
 }
 
-// A warp's scratch: the list of the largest keys, or every key in double.
+// A warp's scratch: the list of the largest keys, or every key in double where
+// keys can be inexact.
 __host__ __device__ __forceinline__ size_t select_scratch(const RouteOpArgs& a) {
-  const size_t keys = a.n_groups > 1 ? static_cast<size_t>(a.E) * 8 : 0;
+  const size_t keys = (a.n_groups > 1 || a.bias != nullptr) ? static_cast<size_t>(a.E + 1) / 2 * 16 : 0;
   return keys > kListBytes ? keys : kListBytes;
 }
 
@@ -465,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, VPL <= 8 ? 4 : 2) k_select(const Rou
   }
   pdl_wait();
   pdl_trigger();
-  double* keys = reinterpret_cast<double*>(raw + warp * scratch);
+  int64_t* keys = reinterpret_cast<int64_t*>(raw + warp * scratch);
   float bias[VPL];
   const float bias_max = load_bias<VPL>(a, lane, bias);
   for (int t = warp; t < nt; t += kWarps) {
@@ -559,8 +660,10 @@ cudaError_t launch_route_op(const RouteOpArgs& args, cudaStream_t s) {
   const int size = a.bf16_logits ? 2 : 4;
   const int part = vpl * size < 16 ? vpl * size : 16;
   a.vec = a.E % vpl == 0 && reinterpret_cast<uintptr_t>(a.logits) % part == 0 && a.ld * size % part == 0;
-  const int lanes = a.E / a.n_groups / vpl;  // per group, where that is whole and a power of two
-  a.group_lanes = (a.E / a.n_groups % vpl == 0 && (lanes & (lanes - 1)) == 0) ? lanes : 0;
+  a.group_size = a.E / a.n_groups;
+  a.group_shift = -1;
+  for (int b = 0; b <= 5; ++b)
+    if (a.group_size == vpl << b) a.group_shift = b;
   cudaError_t e = launch_kernel<RouteOpArgs>(k, dim3(a.n_ctas), dim3(kThreads), smem, s, true, a);
   if (e != cudaSuccess || a.offsets == nullptr || a.n_ctas == 1) return e;
   e = launch_kernel<RouteOpArgs>(k_scan_hist, dim3((a.E + kWarps - 1) / kWarps), dim3(kThreads), 0, s, true, a);
