@@ -73,12 +73,11 @@ __device__ __forceinline__ bool scale_row(const Fp4QuantArgs& a, int64_t i, int 
     return true;
   }
   // group of row i: the number of groups that end at or before it
-  const int n = static_cast<int>(a.n_rows);
   int below = 0;
-  for (int g = lane; g < a.n_groups; g += 32) below += group_offset(a.offsets, g + 1, n) <= i ? 1 : 0;
-  const int g = warp_sum_i(below);
+  for (int g = lane; g < a.n_groups; g += 32) below += a.offsets[g + 1] <= i ? 1 : 0;
+  const int g = __reduce_add_sync(0xffffffffu, below);
   if (g >= a.n_groups) return false;
-  const int off = group_offset(a.offsets, g, n);
+  const int off = group_offset(a.offsets, g, static_cast<int>(a.n_rows));
   if (off > i) return false;  // offsets that do not ascend
   *r = (off / 128 + static_cast<int64_t>(g)) * 128 + (i - off);
   return true;
@@ -98,7 +97,8 @@ __device__ __forceinline__ bool scale_row(const Fp4QuantArgs& a, int64_t i, int 
 // product cut off, the product is the border itself (for each of the 8
 // significands a scale can have and each border). The same holds for amax / 6
 // and the midpoints between scales.
-template <bool kMx, bool kBf16>
+// kUnit: scale_exp is 0.
+template <bool kMx, bool kBf16, bool kUnit>
 __global__ void __launch_bounds__(kThreads) k_quantize_fp4(const Fp4QuantArgs a) {
   constexpr int kBlock = kMx ? 32 : 16;
   constexpr int kWords = kBlock * (kBf16 ? 2 : 4) / 4;  // of a block's input
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) k_quantize_fp4(const Fp4QuantArgs a)
   const int nb = a.cols / kBlock, ct = (nb + 3) / 4;
   uint8_t* tile = a.scales + (sr / 128) * ct * 512 + (sr % 32) * 16 + (sr % 128) / 32 * 4;
   uint8_t* codes = a.codes + i * (a.cols / 2);
-  const bool wide = a.wide, unit = a.mul == 1.f;
+  const bool wide = a.wide;
 #pragma unroll 2
   for (int b = lane; b < nb; b += 32) {
     uint32_t in[kWords];
@@ -173,11 +173,11 @@ __global__ void __launch_bounds__(kThreads) k_quantize_fp4(const Fp4QuantArgs a)
         const float v = kBf16 ? __uint_as_float(k % 2 == 0 ? in[k / 2] << 16 : in[k / 2] & 0xFFFF0000u)
                               : __uint_as_float(in[k]);
         if (kMx)
-          q[j] = unit ? v * inv : v * a.mul * inv;
+          q[j] = kUnit ? v * inv : v * a.mul * inv;
         else if (kBf16)
           q[j] = __fmul_rz(v, inv);
         else
-          q[j] = s > 0.f ? __fdiv_rn(v * a.mul, s) : 0.f;
+          q[j] = s > 0.f ? __fdiv_rn(kUnit ? v : v * a.mul, s) : 0.f;
       }
       words[wd] = coded ? e2m1_word(q) : 0u;
     }
@@ -226,8 +226,13 @@ dim3 row_grid(const Fp4QuantArgs& a) { return dim3(static_cast<unsigned>((a.n_ro
 cudaError_t launch_quantize_fp4(const Fp4QuantArgs& args, bool mx, cudaStream_t s) {
   Fp4QuantArgs a = args;
   a.wide = reinterpret_cast<uintptr_t>(a.x) % 32 == 0 && a.ldx * (a.bf16_x ? 2 : 4) % 32 == 0;
-  void (*k)(const Fp4QuantArgs) = mx ? (a.bf16_x ? k_quantize_fp4<true, true> : k_quantize_fp4<true, false>)
-                                     : (a.bf16_x ? k_quantize_fp4<false, true> : k_quantize_fp4<false, false>);
+  void (*k)(const Fp4QuantArgs);
+  if (a.mul == 1.f)
+    k = mx ? (a.bf16_x ? k_quantize_fp4<true, true, true> : k_quantize_fp4<true, false, true>)
+           : (a.bf16_x ? k_quantize_fp4<false, true, true> : k_quantize_fp4<false, false, true>);
+  else
+    k = mx ? (a.bf16_x ? k_quantize_fp4<true, true, false> : k_quantize_fp4<true, false, false>)
+           : (a.bf16_x ? k_quantize_fp4<false, true, false> : k_quantize_fp4<false, false, false>);
   return launch_kernel(k, row_grid(a), dim3(kThreads), 0, s, true, a);
 }
 
