@@ -11,6 +11,7 @@
 #include "../../include/clover.h"
 #include "internal.h"
 #include "moe_ops.cuh"
+#include "plan.h"
 
 using namespace clover;
 
@@ -305,15 +306,18 @@ int clover_fp4_product(int32_t format, const uint8_t* a_codes, const uint8_t* a_
   a.b_rows = swiglu ? N / 2 : N;
   const uint64_t mats = static_cast<uint64_t>(n_groups) * (swiglu ? 2 : 1);
   const uint32_t box_rows = swiglu ? 128 : 256, box_mats = swiglu ? 2 : 1;
+  const bool pair = plan::fp4_pairs(n_rows, n_groups);
+  const uint64_t a_tiles = offsets != nullptr ? static_cast<uint64_t>(n_rows) / 128 + n_groups : (n_rows + 127) / 128;
+  const uint32_t sf_bytes = 256 / (4 * fp4_block(format)) * 512;  // of a stage of 256 K elements
   if ((rc = encode_byte_boxes(&a.tm_a, a_codes, 0, n_rows, K / 2, 128, 128, 1, true, "rows' codes")) ||
       (rc = encode_byte_boxes(&a.tm_a32, a_codes, 0, n_rows, K / 2, 128, 32, 1, true, "rows' codes")) ||
-      (rc = encode_byte_boxes(&a.tm_b, b_codes, mats, a.b_rows, K / 2, 128, box_rows, box_mats, true,
-                              "matrices' codes")) ||
-      (rc = encode_byte_boxes(&a.tm_b_sf, b_scales, mats, (a.b_rows + 127) / 128, scale_tile_bytes(format, K),
-                              256 / (4 * fp4_block(format)) * 512, box_rows / 128, box_mats, false,
-                              "matrices' scales")))
+      (rc = encode_byte_boxes(&a.tm_a_sf, a_scales, 0, a_tiles, scale_tile_bytes(format, K), sf_bytes, 1, 1, false,
+                              "rows' scales")) ||
+      (rc = encode_byte_boxes(&a.tm_b, b_codes, mats, a.b_rows, K / 2, 128, pair ? 128 : box_rows, pair ? 1 : box_mats,
+                              true, "matrices' codes")) ||
+      (rc = encode_byte_boxes(&a.tm_b_sf, b_scales, mats, (a.b_rows + 127) / 128, scale_tile_bytes(format, K), sf_bytes,
+                              box_rows / 128, box_mats, false, "matrices' scales")))
     return rc;
-  a.a_scales = a_scales;
   a.offsets = offsets;
   a.group_alpha = group_alpha;
   a.alpha = alpha;
@@ -322,7 +326,7 @@ int clover_fp4_product(int32_t format, const uint8_t* a_codes, const uint8_t* a_
   a.K = K;
   a.y = reinterpret_cast<__nv_bfloat16*>(y);
   a.err = static_cast<int*>(workspace);
-  return launched(launch_fp4_product(a, format == CLOVER_FP4_MX, swiglu, sms, reinterpret_cast<cudaStream_t>(stream)),
+  return launched(launch_fp4_product(a, format == CLOVER_FP4_MX, swiglu, pair, sms, reinterpret_cast<cudaStream_t>(stream)),
                   "launch fp4 product");
 }
 

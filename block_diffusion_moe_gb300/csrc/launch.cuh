@@ -1,6 +1,7 @@
 // Kernel launch helper: cudaLaunchKernelEx with optional programmatic
 // dependent launch (the kernel may start while its predecessor drains and
-// must call griddepcontrol.wait before touching the predecessor's output).
+// must call griddepcontrol.wait before touching the predecessor's output) and
+// optional clusters of neighbouring CTAs.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -9,17 +10,26 @@ namespace clover {
 
 template <typename Arg>
 cudaError_t launch_kernel(void (*kernel)(Arg), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                          bool pdl, const Arg& arg) {
+                          bool pdl, const Arg& arg, unsigned cluster = 1) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = pdl ? attr : nullptr;
-  cfg.numAttrs = pdl ? 1 : 0;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = n > 0 ? attr : nullptr;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, arg);
 }
 

@@ -89,9 +89,10 @@ constexpr int kFp4MaxGroups = 512;
 struct Fp4ProductArgs {
   CUtensorMap tm_a;          // codes [n_rows][K / 2], boxes of 128 bytes x 128 rows
   CUtensorMap tm_a32;        // the same in boxes of 32 rows
-  CUtensorMap tm_b;          // codes [mats][b_rows][K / 2], boxes of 128 bytes x 256 rows x 1 (SwiGLU: 128 x 2)
+  CUtensorMap tm_a_sf;       // scale tiles [row tiles][..], boxes of a stage's tiles x 1
+  CUtensorMap tm_b;          // codes [mats][b_rows][K / 2], boxes of 128 bytes x 256 rows x 1 (SwiGLU: 128 x 2;
+                             // CTA pairs: 128 x 1)
   CUtensorMap tm_b_sf;       // scale tiles [mats][b_rows / 128][..], boxes of a stage's tiles x 2 x 1 (SwiGLU: 1 x 2)
-  const uint8_t* a_scales;   // tiles of 128 rows
   const int32_t* offsets;    // [n_groups + 1] or null (one group of all rows)
   const float* group_alpha;  // [n_groups] or null
   float alpha;
@@ -102,7 +103,6 @@ struct Fp4ProductArgs {
   int* err;
 };
 
-size_t fp4_product_smem_bytes();
-cudaError_t launch_fp4_product(const Fp4ProductArgs& a, bool mx, bool swiglu, int grid, cudaStream_t s);
+cudaError_t launch_fp4_product(const Fp4ProductArgs& a, bool mx, bool swiglu, bool pair, int sms, cudaStream_t s);
 
 }  // namespace clover

@@ -2,12 +2,17 @@
 // (clover_fp4_product): y = alpha_g A_i . B_g^T, optionally SwiGLU, on the
 // block-scaled tensor-core instruction (tcgen05.mma kind::mxf4nvf4).
 //
-// One persistent CTA per SM. A tile is 128 rows of one group x 256 rows of its
+// Persistent, one CTA per SM. A tile is 128 rows of one group x 256 rows of its
 // matrix (SwiGLU: 128 gate rows and their 128 up rows, so that one thread
 // holds both factors). Roles: warp 0 streams codes (TMA, 128-byte swizzle)
-// and scale tiles (bulk copies) through a ring of stages of 256 K elements,
-// warp 1 copies each stage's scales to tensor memory and issues its four
-// MMAs, warps 4-7 drain the accumulator (one TMEM lane quarter each).
+// and scale tiles through a ring of stages of 256 K elements, warp 1 copies each
+// stage's scales to tensor memory and issues its four MMAs, warps 4-7 drain the
+// accumulator (one TMEM lane quarter each).
+//
+// Where groups are long, pairs of CTAs take tiles of 256 x 256 (kPair): each
+// CTA holds its 128 rows of A and half of B, and the pair's MMA reads both
+// halves, so an SM takes in 38 KB per stage instead of 54. The single form's
+// rate is that of the SM's L2 port (64 bytes a cycle), not the tensor core's.
 #include <math.h>
 
 #include "fp4.cuh"
@@ -24,14 +29,23 @@ constexpr int kThreads = 256;
 constexpr int kTileM = 128;          // rows of A per tile
 constexpr int kTileN = 256;          // rows of B per tile
 constexpr int kStageK = 256;         // K elements per stage: 128 bytes of codes per row
-constexpr int kStages = 4;
 constexpr int kABytes = kTileM * kStageK / 2;
-constexpr int kBBytes = kTileN * kStageK / 2;
 // Scale tiles of a stage: 4 chunks of 64 K elements (NV), 2 of 128 (MX)
 constexpr int kMaxChunks = 4;
 constexpr int kSfABytes = kMaxChunks * 512;
 constexpr int kSfBBytes = 2 * kMaxChunks * 512;
-constexpr int kStageBytes = kABytes + kBBytes + kSfABytes + kSfBBytes;
+constexpr int kMaxStages = 5;
+
+// A stage of one CTA: A codes, B codes (a pair's CTA: half of them), A's
+// scales, all of B's scales.
+template <bool kPair>
+struct Stage {
+  static constexpr int kBBytes = (kPair ? kTileN / 2 : kTileN) * kStageK / 2;
+  static constexpr int kSfA = kABytes + kBBytes;
+  static constexpr int kSfB = kSfA + kSfABytes;
+  static constexpr int kBytes = kSfB + kSfBBytes;
+  static constexpr int kCount = kPair ? 5 : 4;
+};
 
 // Tensor memory: the accumulators of consecutive tiles are columns 0-255 and
 // 192-447: 512 columns do not hold two of 256 and the scales, so they share
@@ -43,7 +57,7 @@ constexpr uint32_t kTmemSfB = kTmemSfA + 4 * kMaxChunks;
 static_assert(kTmemSfB + 8 * kMaxChunks <= kTmemCols, "scales must fit behind the accumulators");
 
 struct Shared {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t acc_full;    // a tile's accumulator is complete
   uint64_t acc_shared;  // the columns it shares with the next one are drained
   uint64_t drain;
@@ -61,7 +75,8 @@ __device__ __forceinline__ void give_up(const Fp4ProductArgs& p, Shared* sh) {
 }
 
 // Tile t, group by group, a group's row tiles in turn, the column tiles of a
-// row tile next to one another.
+// row tile next to one another. A pair's row tile is 256 rows, rank's half of
+// it the rows here (none, or fewer than none, where the group ends before).
 struct Tile {
   int g;
   int row0, rows;    // first row of A, rows of it that belong to the group
@@ -69,7 +84,9 @@ struct Tile {
   int n0;            // first row of the B matrix (SwiGLU: of either half)
 };
 
-__device__ __forceinline__ Tile tile_at(const Fp4ProductArgs& p, const Shared& sh, int64_t t, int n_tiles, int step) {
+template <bool kPair>
+__device__ __forceinline__ Tile tile_at(const Fp4ProductArgs& p, const Shared& sh, int64_t t, int n_tiles, int step,
+                                        int rank) {
   const int m = static_cast<int>(t / n_tiles);
   int lo = 0, hi = p.n_groups;  // the last group with mt[g] <= m
   while (hi - lo > 1) {
@@ -81,12 +98,22 @@ __device__ __forceinline__ Tile tile_at(const Fp4ProductArgs& p, const Shared& s
   }
   Tile r;
   r.g = lo;
-  const int i = m - sh.mt[lo];
+  const int i = kPair ? 2 * (m - sh.mt[lo]) + rank : m - sh.mt[lo];
   r.row0 = sh.off[lo] + i * kTileM;
   r.rows = min(kTileM, sh.cnt[lo] - i * kTileM);
   r.sf_tile = sh.off[lo] / 128 + static_cast<int64_t>(lo) + i;
   r.n0 = static_cast<int>(t - static_cast<int64_t>(m) * n_tiles) * step;
   return r;
+}
+
+// First tile of this CTA (or pair) and the distance to its next one.
+template <bool kPair>
+__device__ __forceinline__ int64_t first_tile() {
+  return kPair ? blockIdx.x / 2 : blockIdx.x;
+}
+template <bool kPair>
+__device__ __forceinline__ int64_t tile_step() {
+  return kPair ? gridDim.x / 2 : gridDim.x;
 }
 
 // The whole warp waits, so that its control flow stays uniform (the elected
@@ -101,25 +128,24 @@ __device__ __forceinline__ bool warp_wait(const Fp4ProductArgs& p, Shared* sh, u
 // Run by the whole warp; one elected lane issues. The rate of an SM's copies
 // follows their number more than their size, so a stage of a full tile is four:
 // A codes, A scales, both halves of B's codes, both halves of B's scales.
-template <bool kMx, bool kSwiglu>
-__device__ void producer(const Fp4ProductArgs& p, Shared* sh, uint8_t* ring, int64_t n_all, int n_tiles) {
+template <bool kMx, bool kSwiglu, bool kPair>
+__device__ void producer(const Fp4ProductArgs& p, Shared* sh, uint8_t* ring, int64_t n_all, int n_tiles, int rank) {
+  using St = Stage<kPair>;
   constexpr int kChunk = kMx ? 128 : 64;       // K elements per scale tile
   constexpr int kChunks = kStageK / kChunk;    // scale tiles of a stage
   const uint64_t pol = l2_policy_evict_last();  // row tiles share B tiles, column tiles share A tiles
   const uint32_t ring0 = smem_u32(ring);
   const int nk = (p.K + kStageK - 1) / kStageK;
-  const int chunks = (p.K + kChunk - 1) / kChunk;
   int st = 0;
   uint32_t ph = 0, issued = 0, parity_bits = 0;
   bool ok = true;
-  for (int64_t t = blockIdx.x; t < n_all && ok; t += gridDim.x) {
-    const Tile tl = tile_at(p, *sh, t, n_tiles, kSwiglu ? 128 : 256);
+  for (int64_t t = first_tile<kPair>(); t < n_all && ok; t += tile_step<kPair>()) {
+    const Tile tl = tile_at<kPair>(p, *sh, t, n_tiles, kSwiglu ? 128 : 256, rank);
     // a tile with few rows copies only the 32-row boxes that hold some; what
     // the others leave in shared memory reaches only accumulator rows that
     // nobody stores
-    const int boxes = tl.rows > 96 ? 0 : (tl.rows + 31) / 32;
+    const int boxes = kPair || tl.rows > 96 ? 0 : (tl.rows + 31) / 32;
     const uint32_t a_bytes = boxes == 0 ? kABytes : boxes * 4096;
-    const uint8_t* a_sf = p.a_scales + tl.sf_tile * chunks * 512;
     // SwiGLU: rows n0 .. n0 + 127 of the group's gate and up matrices; else
     // rows n0 .. n0 + 255 of its matrix. Past the matrix: zeros.
     const int mat = kSwiglu ? 2 * tl.g : tl.g;
@@ -129,57 +155,86 @@ __device__ void producer(const Fp4ProductArgs& p, Shared* sh, uint8_t* ring, int
         break;
       }
       if (elect_one()) {
-        const int nc = min(kChunks, chunks - k * kChunks);
         uint64_t* bar = &sh->full[st];
-        const uint32_t base = ring0 + static_cast<uint32_t>(st) * kStageBytes;
-        mbar_arrive_expect_tx(bar, a_bytes + kBBytes + nc * 512 + 2 * kChunks * 512);
-        if (boxes == 0)
-          tma_load_2d(base, &p.tm_a, bar, k * 128, tl.row0, pol);
-        else
-          for (int b = 0; b < boxes; ++b) tma_load_2d(base + b * 4096, &p.tm_a32, bar, k * 128, tl.row0 + b * 32, pol);
-        tma_load_3d(base + kABytes, &p.tm_b, bar, k * 128, tl.n0, mat, pol);
-        bulk_load(base + kABytes + kBBytes, a_sf + static_cast<int64_t>(k) * kChunks * 512, nc * 512, bar);
-        tma_load_3d(base + kABytes + kBBytes + kSfABytes, &p.tm_b_sf, bar, k * kChunks * 64, tl.n0 / 128, mat, pol);
+        const uint32_t base = ring0 + static_cast<uint32_t>(st) * St::kBytes;
+        const uint32_t bytes = a_bytes + St::kBBytes + 3 * kChunks * 512;
+        const int sf = k * kChunks * 64, sf_row = static_cast<int>(tl.sf_tile);
+        if (kPair) {
+          // both CTAs' copies complete on rank 0's barrier, which alone waits
+          // for them (the whole boxes: what lies past the group or the tensor
+          // does no harm)
+          if (rank == 0) mbar_arrive_expect_tx(bar, 2 * bytes);
+          const uint32_t bar0 = cluster_map(smem_u32(bar), 0);
+          tma_load_2d_pair(base, &p.tm_a, bar0, k * 128, tl.row0, pol);
+          tma_load_3d_pair(base + kABytes, &p.tm_b, bar0, k * 128, kSwiglu ? tl.n0 : tl.n0 + rank * 128,
+                           kSwiglu ? mat + rank : mat, pol);
+          tma_load_2d_pair(base + St::kSfA, &p.tm_a_sf, bar0, sf, sf_row, pol);
+          tma_load_3d_pair(base + St::kSfB, &p.tm_b_sf, bar0, sf, tl.n0 / 128, mat, pol);
+        } else {
+          mbar_arrive_expect_tx(bar, bytes);
+          if (boxes == 0)
+            tma_load_2d(base, &p.tm_a, bar, k * 128, tl.row0, pol);
+          else
+            for (int b = 0; b < boxes; ++b)
+              tma_load_2d(base + b * 4096, &p.tm_a32, bar, k * 128, tl.row0 + b * 32, pol);
+          tma_load_3d(base + kABytes, &p.tm_b, bar, k * 128, tl.n0, mat, pol);
+          tma_load_2d(base + St::kSfA, &p.tm_a_sf, bar, sf, sf_row, pol);
+          tma_load_3d(base + St::kSfB, &p.tm_b_sf, bar, sf, tl.n0 / 128, mat, pol);
+        }
       }
       __syncwarp();
       issued |= 1u << st;
       parity_bits = (parity_bits & ~(1u << st)) | (ph << st);
-      if (++st == kStages) {
+      if (++st == St::kCount) {
         st = 0;
         ph ^= 1u;
       }
     }
   }
-  if (*reinterpret_cast<volatile uint32_t*>(&sh->abort)) {  // the copies in flight must land before the CTA leaves
-    for (int i = 0; i < kStages; ++i)
+  // the copies in flight must land before the CTA leaves (a pair's rank 1 sees
+  // that through the cluster barrier behind rank 0's wait)
+  if (*reinterpret_cast<volatile uint32_t*>(&sh->abort) && rank == 0) {
+    for (int i = 0; i < St::kCount; ++i)
       if (issued & (1u << i)) mbar_wait_for(&sh->full[i], (parity_bits >> i) & 1u, 200000000ull);
   }
 }
 
 // One stage: its scale tiles to tensor memory, then its MMAs (kSteps of 64 K
 // elements), issued by the calling thread.
-template <bool kMx, int kSteps>
+template <bool kMx, bool kPair, int kSteps>
 __device__ __forceinline__ void issue_stage(uint32_t base, uint32_t tmem, uint32_t d, uint32_t accumulate) {
+  using St = Stage<kPair>;
   constexpr int kPerTile = kMx ? 2 : 1;  // MMAs per scale tile
-  const uint32_t sfa = base + kABytes + kBBytes, sfb = sfa + kSfABytes;
+  const uint32_t sfa = base + St::kSfA, sfb = base + St::kSfB;
 #pragma unroll
   for (int c = 0; c < (kSteps + kPerTile - 1) / kPerTile; ++c) {
-    tmem_copy_scales(tmem + kTmemSfA + c * 4, sfa + c * 512);
-    tmem_copy_scales(tmem + kTmemSfB + c * 8, sfb + c * 512);
-    tmem_copy_scales(tmem + kTmemSfB + c * 8 + 4, sfb + (kStageK / (64 * kPerTile) + c) * 512);
+    tmem_copy_scales<kPair>(tmem + kTmemSfA + c * 4, sfa + c * 512);
+    tmem_copy_scales<kPair>(tmem + kTmemSfB + c * 8, sfb + c * 512);
+    tmem_copy_scales<kPair>(tmem + kTmemSfB + c * 8 + 4, sfb + (kStageK / (64 * kPerTile) + c) * 512);
   }
   const uint64_t ad = umma_desc_sw128(base), bd = umma_desc_sw128(base + kABytes);
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     const int c = s / kPerTile;
-    umma_fp4<kMx>(d, ad + 2 * s, bd + 2 * s, umma_idesc_fp4(kTileM, kTileN, kMx, kMx ? (s & 1) * 2 : 0),
-                  tmem + kTmemSfA + c * 4, tmem + kTmemSfB + c * 8, s == 0 ? accumulate : 1u);
+    umma_fp4<kMx, kPair>(d, ad + 2 * s, bd + 2 * s,
+                         umma_idesc_fp4(kPair ? 2 * kTileM : kTileM, kTileN, kMx, kMx ? (s & 1) * 2 : 0),
+                         tmem + kTmemSfA + c * 4, tmem + kTmemSfB + c * 8, s == 0 ? accumulate : 1u);
   }
 }
 
-// Run by the whole warp with uniform control flow; one elected lane issues.
-template <bool kMx>
+template <bool kPair>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if (kPair)
+    umma_commit_pair(bar);
+  else
+    umma_commit(bar);
+}
+
+// Run by the whole warp (of a pair: rank 0's) with uniform control flow; one
+// elected lane issues.
+template <bool kMx, bool kPair>
 __device__ void mma_issuer(const Fp4ProductArgs& p, Shared* sh, uint8_t* ring, int64_t n_all) {
+  using St = Stage<kPair>;
   const uint32_t tmem = sh->tmem;
   const uint32_t ring0 = smem_u32(ring);
   const int nk = (p.K + kStageK - 1) / kStageK;
@@ -187,11 +242,14 @@ __device__ void mma_issuer(const Fp4ProductArgs& p, Shared* sh, uint8_t* ring, i
   int st = 0, it = 0;
   uint32_t ph = 0;
   bool ok = true;
-  for (int64_t t = blockIdx.x; t < n_all && ok; t += gridDim.x, ++it) {
+  for (int64_t t = first_tile<kPair>(); t < n_all && ok; t += tile_step<kPair>(), ++it) {
     // the columns shared with the previous tile's accumulator are free once
     // that one's epilogue has drained them, and it drained the tile before
     // that first
-    if (it > 0 && !warp_wait(p, sh, &sh->acc_shared, (it - 1) & 1)) break;
+    if (it > 0) {
+      if (!warp_wait(p, sh, &sh->acc_shared, (it - 1) & 1)) break;
+      if (kPair) asm volatile("fence.acq_rel.cluster;" ::: "memory");  // half of the arrivals came from rank 1
+    }
     tc_fence_after();
     const uint32_t d = tmem + (it & 1 ? kAcc1 : 0u);
     for (int k = 0; k < nk; ++k) {
@@ -200,29 +258,34 @@ __device__ void mma_issuer(const Fp4ProductArgs& p, Shared* sh, uint8_t* ring, i
         break;
       }
       tc_fence_after();
-      const uint32_t base = ring0 + static_cast<uint32_t>(st) * kStageBytes;
+      const uint32_t base = ring0 + static_cast<uint32_t>(st) * St::kBytes;
       const uint32_t acc = k != 0 ? 1u : 0u;
       if (elect_one()) {
         if (k + 1 < nk || last == 4) {
-          issue_stage<kMx, 4>(base, tmem, d, acc);
+          issue_stage<kMx, kPair, 4>(base, tmem, d, acc);
         } else if (last == 3) {
-          issue_stage<kMx, 3>(base, tmem, d, acc);
+          issue_stage<kMx, kPair, 3>(base, tmem, d, acc);
         } else if (last == 2) {
-          issue_stage<kMx, 2>(base, tmem, d, acc);
+          issue_stage<kMx, kPair, 2>(base, tmem, d, acc);
         } else {
-          issue_stage<kMx, 1>(base, tmem, d, acc);
+          issue_stage<kMx, kPair, 1>(base, tmem, d, acc);
         }
-        umma_commit(&sh->empty[st]);
-        if (k + 1 == nk) umma_commit(&sh->acc_full);
+        commit<kPair>(&sh->empty[st]);
+        if (k + 1 == nk) commit<kPair>(&sh->acc_full);
       }
       __syncwarp();
-      if (++st == kStages) {
+      if (++st == St::kCount) {
         st = 0;
         ph ^= 1u;
       }
     }
   }
-  if (elect_one()) umma_commit(&sh->drain);
+  if (elect_one()) {
+    if (kPair)
+      umma_commit_own_pair(&sh->drain);
+    else
+      umma_commit(&sh->drain);
+  }
   __syncwarp();
   mbar_wait_for(&sh->drain, 0, 200000000ull);
 }
@@ -247,13 +310,13 @@ __device__ __forceinline__ void store32(__nv_bfloat16* row, int c0, int width, b
   }
 }
 
-template <bool kSwiglu>
-__device__ void epilogue(const Fp4ProductArgs& p, Shared* sh, int64_t n_all, int n_tiles) {
+template <bool kSwiglu, bool kPair>
+__device__ void epilogue(const Fp4ProductArgs& p, Shared* sh, int64_t n_all, int n_tiles, int rank) {
   const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const bool vec = p.b_rows % 8 == 0;  // rows of y 16-byte aligned
   int it = 0;
-  for (int64_t t = blockIdx.x; t < n_all; t += gridDim.x, ++it) {
-    const Tile tl = tile_at(p, *sh, t, n_tiles, kSwiglu ? 128 : 256);
+  for (int64_t t = first_tile<kPair>(); t < n_all; t += tile_step<kPair>(), ++it) {
+    const Tile tl = tile_at<kPair>(p, *sh, t, n_tiles, kSwiglu ? 128 : 256, rank);
     if (!warp_wait(p, sh, &sh->acc_full, it & 1)) return;
     tc_fence_after();
     const bool odd = it & 1;
@@ -284,7 +347,12 @@ __device__ void epilogue(const Fp4ProductArgs& p, Shared* sh, int64_t n_all, int
       if (i == 1) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->acc_shared);
+        if (lane == 0) {
+          if (kPair)
+            mbar_arrive_cluster(cluster_map(smem_u32(&sh->acc_shared), 0));
+          else
+            mbar_arrive(&sh->acc_shared);
+        }
       }
       if (on) store32(row, tl.n0 + c * 32, p.b_rows, vec, v);
     }
@@ -293,30 +361,37 @@ __device__ void epilogue(const Fp4ProductArgs& p, Shared* sh, int64_t n_all, int
 
 }  // namespace
 
-template <bool kMx, bool kSwiglu>
+template <bool kMx, bool kSwiglu, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1) k_fp4_product(const __grid_constant__ Fp4ProductArgs p) {
+  using St = Stage<kPair>;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  Shared* sh = reinterpret_cast<Shared*>(ring + static_cast<size_t>(kStages) * kStageBytes);
+  Shared* sh = reinterpret_cast<Shared*>(ring + static_cast<size_t>(St::kCount) * St::kBytes);
   const int warp = threadIdx.x >> 5;
+  const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&p.tm_a);
-    tma_prefetch_desc(&p.tm_a32);
+    tma_prefetch_desc(&p.tm_a_sf);
     tma_prefetch_desc(&p.tm_b);
     tma_prefetch_desc(&p.tm_b_sf);
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < St::kCount; ++i) {
       mbar_init(&sh->full[i], 1);
       mbar_init(&sh->empty[i], 1);
     }
     mbar_init(&sh->acc_full, 1);
-    mbar_init(&sh->acc_shared, 4);
+    mbar_init(&sh->acc_shared, kPair ? 8 : 4);
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(&sh->tmem, kTmemCols);
-    tmem_relinquish();
+    if (kPair) {
+      tmem_alloc_pair(&sh->tmem, kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&sh->tmem, kTmemCols);
+      tmem_relinquish();
+    }
   }
   pdl_wait();
   pdl_trigger();
@@ -331,7 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_product(const __grid_consta
       const int hi = p.offsets != nullptr ? group_offset(p.offsets, g + 1, p.n_rows) : p.n_rows;
       sh->off[g] = lo;
       sh->cnt[g] = max(hi - lo, 0);
-      tiles[j] = (sh->cnt[g] + kTileM - 1) / kTileM;
+      constexpr int kRows = kPair ? 2 * kTileM : kTileM;
+      tiles[j] = (sh->cnt[g] + kRows - 1) / kRows;
     }
   }
   int m_tiles;
@@ -339,36 +415,53 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_product(const __grid_consta
   if (2 * threadIdx.x <= p.n_groups) sh->mt[2 * threadIdx.x] = before;
   if (2 * threadIdx.x + 1 <= p.n_groups) sh->mt[2 * threadIdx.x + 1] = before + tiles[0];
   tc_fence_before();
-  __syncthreads();
+  if (kPair)
+    cluster_sync();  // both CTAs' barriers are set up
+  else
+    __syncthreads();
   tc_fence_after();
   const int step = kSwiglu ? 128 : 256;
   const int n_tiles = (p.b_rows + step - 1) / step;
   const int64_t n_all = static_cast<int64_t>(m_tiles) * n_tiles;
   if (warp == 0) {
-    producer<kMx, kSwiglu>(p, sh, ring, n_all, n_tiles);
+    producer<kMx, kSwiglu, kPair>(p, sh, ring, n_all, n_tiles, rank);
   } else if (warp == 1) {
-    mma_issuer<kMx>(p, sh, ring, n_all);
+    if (rank == 0) mma_issuer<kMx, kPair>(p, sh, ring, n_all);
   } else if (warp >= 4) {
-    epilogue<kSwiglu>(p, sh, n_all, n_tiles);
+    epilogue<kSwiglu, kPair>(p, sh, n_all, n_tiles, rank);
   }
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  if (kPair)
+    cluster_sync();  // neither CTA's memory goes away under the other's work
+  else
+    __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(sh->tmem, kTmemCols);
+    if (kPair)
+      tmem_dealloc_pair(sh->tmem, kTmemCols);
+    else
+      tmem_dealloc(sh->tmem, kTmemCols);
   }
 }
 
-size_t fp4_product_smem_bytes() { return 1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(Shared); }
+namespace {
 
-cudaError_t launch_fp4_product(const Fp4ProductArgs& a, bool mx, bool swiglu, int grid, cudaStream_t s) {
-  void (*k)(const Fp4ProductArgs) = mx ? (swiglu ? k_fp4_product<true, true> : k_fp4_product<true, false>)
-                                       : (swiglu ? k_fp4_product<false, true> : k_fp4_product<false, false>);
-  const size_t smem = fp4_product_smem_bytes();
+template <bool kPair>
+cudaError_t launch(const Fp4ProductArgs& a, bool mx, bool swiglu, int grid, cudaStream_t s) {
+  void (*k)(const Fp4ProductArgs) =
+      mx ? (swiglu ? k_fp4_product<true, true, kPair> : k_fp4_product<true, false, kPair>)
+         : (swiglu ? k_fp4_product<false, true, kPair> : k_fp4_product<false, false, kPair>);
+  const size_t smem = 1024 + static_cast<size_t>(Stage<kPair>::kCount) * Stage<kPair>::kBytes + sizeof(Shared);
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_kernel(k, dim3(grid), dim3(kThreads), smem, s, true, a);
+  return launch_kernel(k, dim3(grid), dim3(kThreads), smem, s, true, a, kPair ? 2 : 1);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_product(const Fp4ProductArgs& a, bool mx, bool swiglu, bool pair, int sms, cudaStream_t s) {
+  return pair ? launch<true>(a, mx, swiglu, sms / 2 * 2, s) : launch<false>(a, mx, swiglu, sms, s);
 }
 
 }  // namespace clover

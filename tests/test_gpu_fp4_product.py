@@ -104,6 +104,15 @@ def test_groups(counts, swiglu, fmt):
     _check(a, b, off, swiglu=swiglu)
 
 
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("counts,N,K", [([256], 256, 256), ([512], 512, 64), ([300], 130, 320), ([1000, 0, 3], 520, 448),
+                                        ([0, 513, 385, 1], 256, 192), ([700] * 40, 600, 320), ([129, 640], 96, 2048)])
+def test_long_groups(counts, N, K, swiglu, fmt):
+    """256 rows per group and more: tiles of 256 rows on two CTAs, with and without rows in the second half."""
+    _check(*_operands(counts, N, K, fmt, swiglu, sum(counts), extra_rows=1), swiglu=swiglu)
+
+
 def test_scale_exponents_and_alpha():
     for swiglu in (False, True):
         a, b, off = _operands([40, 0, 90], 128, 256, "nv", swiglu, 3, scale_exp=-9)
