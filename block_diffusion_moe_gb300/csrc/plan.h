@@ -33,7 +33,7 @@ inline int persistent_grid(int sms, int resident_per_sm) {
 
 // Whether a grouped 4-bit product runs on pairs of CTAs (tiles of 256 rows)
 // rather than single ones (128).
-inline bool fp4_pairs(int rows, int groups) { return rows / groups >= 256; }
+inline bool fp4_pairs(int rows, int groups) { return rows / groups >= 1024; }
 
 }  // namespace plan
 }  // namespace clover

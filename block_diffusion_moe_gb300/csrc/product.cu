@@ -6,8 +6,9 @@
 // matrix (SwiGLU: 128 gate rows and their 128 up rows, so that one thread
 // holds both factors). Roles: warp 0 streams codes (TMA, 128-byte swizzle)
 // and scale tiles through a ring of stages of 256 K elements, warp 1 copies each
-// stage's scales to tensor memory and issues its four MMAs, warps 4-7 drain the
-// accumulator (one TMEM lane quarter each).
+// stage's scales to tensor memory and issues its four MMAs, warps 4-11 drain the
+// accumulator (two per TMEM lane quarter, each every other chunk of 32 columns:
+// with one the SwiGLU epilogue of a tile took longer than its MMAs).
 //
 // Where groups are long, pairs of CTAs take tiles of 256 x 256 (kPair): each
 // CTA holds its 128 rows of A and half of B, and the pair's MMA reads both
@@ -25,7 +26,8 @@ namespace clover {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;        // 12 warps
+constexpr int kEpilogueWarps = 8;
 constexpr int kTileM = 128;          // rows of A per tile
 constexpr int kTileN = 256;          // rows of B per tile
 constexpr int kStageK = 256;         // K elements per stage: 128 bytes of codes per row
@@ -84,18 +86,20 @@ struct Tile {
   int n0;            // first row of the B matrix (SwiGLU: of either half)
 };
 
+// Called by a whole warp.
 template <bool kPair>
 __device__ __forceinline__ Tile tile_at(const Fp4ProductArgs& p, const Shared& sh, int64_t t, int n_tiles, int step,
                                         int rank) {
-  const int m = static_cast<int>(t / n_tiles);
-  int lo = 0, hi = p.n_groups;  // the last group with mt[g] <= m
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (sh.mt[mid] <= m)
-      lo = mid;
-    else
-      hi = mid;
-  }
+  const int m = t <= 0x7fffffff ? static_cast<int>(static_cast<uint32_t>(t) / static_cast<uint32_t>(n_tiles))
+                                : static_cast<int>(t / n_tiles);
+  // the last group with mt[g] <= m: among every per-th group, then among the
+  // per from there
+  const int lane = threadIdx.x & 31;
+  const int per = (p.n_groups + 31) / 32;
+  const int a = lane * per;
+  int lo = (31 - __clz(__ballot_sync(0xffffffffu, a < p.n_groups && sh.mt[a] <= m))) * per;
+  const int b = lo + lane;
+  lo += 31 - __clz(__ballot_sync(0xffffffffu, lane < per && b < p.n_groups && sh.mt[b] <= m));
   Tile r;
   r.g = lo;
   const int i = kPair ? 2 * (m - sh.mt[lo]) + rank : m - sh.mt[lo];
@@ -313,6 +317,7 @@ __device__ __forceinline__ void store32(__nv_bfloat16* row, int c0, int width, b
 template <bool kSwiglu, bool kPair>
 __device__ void epilogue(const Fp4ProductArgs& p, Shared* sh, int64_t n_all, int n_tiles, int rank) {
   const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int half = (threadIdx.x >> 7) & 1;  // which of the quarter's two warps
   const bool vec = p.b_rows % 8 == 0;  // rows of y 16-byte aligned
   int it = 0;
   for (int64_t t = first_tile<kPair>(); t < n_all; t += tile_step<kPair>(), ++it) {
@@ -328,23 +333,12 @@ __device__ void epilogue(const Fp4ProductArgs& p, Shared* sh, int64_t n_all, int
     // chunks of 32 columns; the two that hold the shared columns come first
     // (the last two of the even accumulator, the first two of the odd one)
     constexpr int kChunks = kSwiglu ? 4 : 8;
-    for (int i = 0; i < kChunks; ++i) {
+    for (int i = half; i < kChunks; i += 2) {
       const int c = odd ? i : (i + kChunks - 2) % kChunks;
-      float v[32];
+      float v[32], u[kSwiglu ? 32 : 1];
       tmem_ld32(acc + c * 32, v);
-      if (kSwiglu) {
-        float u[32];
-        tmem_ld32(acc + 128 + c * 32, u);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float g = v[j] * alpha;
-          v[j] = __fdividef(g, 1.f + __expf(fminf(-g, 80.f))) * (u[j] * alpha);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] *= alpha;
-      }
-      if (i == 1) {
+      if constexpr (kSwiglu) tmem_ld32(acc + 128 + c * 32, u);
+      if (i == half) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -353,6 +347,11 @@ __device__ void epilogue(const Fp4ProductArgs& p, Shared* sh, int64_t n_all, int
           else
             mbar_arrive(&sh->acc_shared);
         }
+      }
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        v[j] *= alpha;
+        if constexpr (kSwiglu) v[j] = __fdividef(v[j], 1.f + __expf(fminf(-v[j], 80.f))) * (u[j] * alpha);
       }
       if (on) store32(row, tl.n0 + c * 32, p.b_rows, vec, v);
     }
@@ -379,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_product(const __grid_consta
       mbar_init(&sh->empty[i], 1);
     }
     mbar_init(&sh->acc_full, 1);
-    mbar_init(&sh->acc_shared, kPair ? 8 : 4);
+    mbar_init(&sh->acc_shared, kPair ? 2 * kEpilogueWarps : kEpilogueWarps);
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
     fence_mbar_init();
@@ -396,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_product(const __grid_consta
   pdl_wait();
   pdl_trigger();
   // the groups' rows and row tiles, two groups per thread
+  static_assert(2 * kThreads > kFp4MaxGroups, "every group needs a thread");
   int tiles[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
