@@ -11,7 +11,6 @@
 #include "../../include/clover.h"
 #include "internal.h"
 #include "moe_ops.cuh"
-#include "plan.h"
 
 using namespace clover;
 
@@ -182,7 +181,9 @@ int clover_route(const clover_routing* routing, const void* logits, int32_t logi
   a.offsets = offsets;
   a.rows = rows;
   a.pos = pos;
-  route_op_shape(M, &a.cta_tokens, &a.n_ctas);
+  a.shape = plan::route_shape(M);
+  a.n_ctas = a.shape.ctas;
+  a.cta_tokens = a.shape.cta_tokens;
   a.totals = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kCtrlBytes);
   a.hist = a.totals + a.E;
   return launched(launch_route_op(a, s), "launch route");
@@ -306,7 +307,7 @@ int clover_fp4_product(int32_t format, const uint8_t* a_codes, const uint8_t* a_
   a.b_rows = swiglu ? N / 2 : N;
   const uint64_t mats = static_cast<uint64_t>(n_groups) * (swiglu ? 2 : 1);
   const uint32_t box_rows = swiglu ? 128 : 256, box_mats = swiglu ? 2 : 1;
-  const bool pair = plan::fp4_pairs(n_rows, n_groups);
+  const bool pair = plan::fp4_pairs(n_rows, n_groups, K, swiglu);
   const uint64_t a_tiles = offsets != nullptr ? static_cast<uint64_t>(n_rows) / 128 + n_groups : (n_rows + 127) / 128;
   const uint32_t sf_bytes = 256 / (4 * fp4_block(format)) * 512;  // of a stage of 256 K elements
   if ((rc = encode_byte_boxes(&a.tm_a, a_codes, 0, n_rows, K / 2, 128, 128, 1, true, "rows' codes")) ||

@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "plan.h"
+
 namespace clover {
 
 constexpr int kRouteOpMaxExperts = 512;
@@ -29,23 +31,15 @@ struct RouteOpArgs {
   int32_t* offsets;  // [E + 1], null: no grouping
   int32_t* rows;     // [M * K]
   int32_t* pos;      // [M][K]
-  int32_t* hist;     // [E][n_ctas] (workspace)
+  int32_t* hist;     // [E][n_ctas] counts per expert and CTA (workspace)
   int32_t* totals;   // [E] (workspace)
-  int cta_tokens;    // tokens per CTA, a multiple of 8, at most kRouteOpCtaTokens
-  int n_ctas;
+  plan::RouteShape shape;
+  int n_ctas;        // shape.ctas
+  int cta_tokens;    // shape.cta_tokens, at most kRouteOpCtaTokens
   int vec;          // set by the launch: whole vectors of logits per lane
   int group_size;   // set by the launch: experts per group
   int group_shift;  // set by the launch: log2 of the lanes that hold one group, or -1
 };
-
-// CTAs and tokens per CTA of the selection kernel for M >= 1 tokens.
-inline void route_op_shape(int M, int* cta_tokens, int* n_ctas) {
-  // 8 tokens (one per warp) until that fills a few hundred CTAs, then more
-  int t = 8;
-  while (t < kRouteOpCtaTokens && (M + t - 1) / t > 304) t *= 2;
-  *cta_tokens = t;
-  *n_ctas = (M + t - 1) / t;
-}
 
 cudaError_t launch_route_op(const RouteOpArgs& a, cudaStream_t s);
 

@@ -32,8 +32,46 @@ inline int persistent_grid(int sms, int resident_per_sm) {
 }
 
 // Whether a grouped 4-bit product runs on pairs of CTAs (tiles of 256 rows)
-// rather than single ones (128).
-inline bool fp4_pairs(int rows, int groups) { return rows / groups >= 1024; }
+// rather than single ones (128). A pair takes in fewer bytes per product, but
+// waits longer between tiles and fills its tiles worse: it needs long groups
+// and a long K (single -> pair on one box: 8,192^3 195 -> 178 us, SwiGLU with N =
+// K = 8,192 186 -> 161, with K = 4,096 104 -> 99; but plain with K = 4,096 111 ->
+// 114, with K = 2,048 74 -> 83, and 64 groups of about 256 rows 150 -> 174).
+inline bool fp4_pairs(int rows, int groups, int k, bool swiglu) {
+  return rows / groups >= 1024 && k >= (swiglu ? 4096 : 8192);
+}
+
+// Expert routing: CTAs of 8 warps, one token per warp and round. Up to 64
+// tokens one cluster of up to 8 CTAs selects and groups in one launch (64 tokens
+// on one box: 5.3 us, as three launches 7.0). Beyond, the tokens spread over
+// more CTAs, which leave their counts per expert; a second launch scans them and
+// a third places the slots. (Without the second, each CTA of the third adding
+// up all counts itself: 257 tokens 11.2 instead of 10.0 us, 1,024 19.8 instead
+// of 9.6.)
+constexpr int kRouteWarps = 8;
+constexpr int kRouteClusterTokens = 64;
+constexpr int kRoutePlaceTokens = 64;
+
+struct RouteShape {
+  int cta_tokens;  // tokens per CTA
+  int ctas;
+  bool cluster;    // all of them one cluster
+};
+
+inline RouteShape route_shape(int tokens) {
+  RouteShape s;
+  s.cta_tokens = kRouteWarps;
+  s.cluster = tokens <= kRouteClusterTokens;
+  if (s.cluster) {
+    s.ctas = 1;
+    while (s.ctas * s.cta_tokens < tokens) s.ctas *= 2;
+  } else {
+    // one token per warp until that fills two CTAs per SM, then up to 64 per CTA
+    while (s.cta_tokens < 64 && (tokens + s.cta_tokens - 1) / s.cta_tokens > 304) s.cta_tokens *= 2;
+    s.ctas = (tokens + s.cta_tokens - 1) / s.cta_tokens;
+  }
+  return s;
+}
 
 }  // namespace plan
 }  // namespace clover

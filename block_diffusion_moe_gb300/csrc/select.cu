@@ -11,8 +11,9 @@ namespace clover {
 
 namespace {
 
-constexpr int kThreads = 256;  // 8 warps, one token each at a time
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = plan::kRouteWarps;  // one token each at a time
+constexpr int kThreads = kWarps * 32;
+constexpr int kPerThread = kRouteOpMaxExperts / kThreads;  // experts a thread counts for, at most
 constexpr uint32_t kAll = 0xffffffffu;
 // Largest K + 1 that is selected by counting (select_token): beyond it the
 // keys above the bound no longer fit 32 lanes as a rule.
@@ -118,11 +119,13 @@ __device__ __forceinline__ void two_best(float& b1, float& b2, float v) {
 //
 // *err bounds the error of a key, and *doubt is set (in every lane) where the
 // ranks on either side of the group border are closer than the errors they can
-// have. A score's error is below 2^-19 of the largest score (softmax: exp and
-// quotient a few roundings each, the sum up to 21; sigmoid: the fast exp's
-// error grows with -logit, a multiple of 2^-22 of it, which s * -logit bounds
-// by that of the largest score), the sum with the bias adds half a unit of the
-// key. Logits used as keys are exact.
+// have. With m the largest score: a softmax score is off by less than 2^-19 m
+// (exp and quotient a few roundings each, the sum up to 21). A sigmoid: by its
+// documented bound __expf is off by (2 + 1.18 |x|) 2^-23 of the value, which
+// changes s by (1 - s) s of that; s (1 - s) |x| is below 0.23, and below m |x of
+// m| where all logits are low, so with the quotient's 2^-22 less than
+// (2^-20 + 2^-22 max(-x of m, 0)) m. The sum with the bias adds half a unit of
+// the key. Logits used as keys are exact.
 template <int VPL>
 __device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float (&x)[VPL], const float (&bias)[VPL],
                                            float bias_max, float* smem, int lane, float (&key)[VPL], float* err,
@@ -146,12 +149,14 @@ __device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float (&x
         sum += key[i];
       }
       s_max = 1.f / warp_sum_f(sum);  // the sum is at least 1
+      *err = s_max * 0x1p-19f;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) key[i] *= s_max;
     } else {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) key[i] = fast_sigmoid(x[i]);
-      s_max = fast_sigmoid(xm) * (1.f + fmaxf(-xm, 0.f) * 0.25f);
+      s_max = fast_sigmoid(xm);
+      *err = s_max * (0x1p-20f + 0x1p-22f * fmaxf(-xm, 0.f));
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) key[i] += bias[i];
@@ -159,7 +164,7 @@ __device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float (&x
 #pragma unroll
       for (int i = 0; i < VPL; ++i) key[i] = x[i] > -INFINITY ? key[i] : -INFINITY;
     }
-    *err = s_max * 1.9e-6f + (s_max + bias_max) * 1.2e-7f + 1e-37f;
+    *err += (s_max + bias_max) * 0x1p-23f + 1e-37f;
   }
   if (a.n_groups == 1) return true;
 
@@ -227,7 +232,8 @@ __device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float (&x
 }
 
 // ---- The order in exact arithmetic: in double, as the definition has it. Rare
-// (a few tokens in a thousand), so written for little code, not for speed.
+// (about one token in a thousand), so compact; what counts is the delay of that
+// token, so the exponentials run four at a time.
 
 struct SoftmaxSum {
   double max, sum;
@@ -240,9 +246,14 @@ __device__ __noinline__ SoftmaxSum softmax_sum(const RouteOpArgs& a, int64_t row
   r.max = warp_max_f(m);
   r.sum = 0;
 #pragma unroll 1
-  for (int e = lane; e < a.E; e += 32) {
-    const float z = load_logit(a, row, e);
-    if (z > -INFINITY) r.sum += exp(static_cast<double>(z) - r.max);
+  for (int e0 = lane; e0 < a.E; e0 += 128) {
+    double t[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float z = e0 + 32 * j < a.E ? load_logit(a, row, e0 + 32 * j) : -INFINITY;
+      t[j] = exp(static_cast<double>(z) - r.max);
+    }
+    r.sum += (t[0] + t[1]) + (t[2] + t[3]);
   }
 #pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) r.sum += __shfl_xor_sync(kAll, r.sum, o);
@@ -250,7 +261,7 @@ __device__ __noinline__ SoftmaxSum softmax_sum(const RouteOpArgs& a, int64_t row
 }
 
 // Score + bias of expert e, -inf where dead.
-__device__ __noinline__ double exact_total(const RouteOpArgs& a, int64_t row, int e, SoftmaxSum s) {
+__device__ __forceinline__ double exact_total(const RouteOpArgs& a, int64_t row, int e, SoftmaxSum s) {
   const float z = load_logit(a, row, e);
   const float b = a.bias != nullptr ? a.bias[e] : 0.f;
   if (!(z > -INFINITY && b > -INFINITY)) return -static_cast<double>(INFINITY);
@@ -288,7 +299,14 @@ __device__ __noinline__ int select_exact(const RouteOpArgs& a, int64_t row, int 
   SoftmaxSum s = {0, 1};
   if (a.softmax) s = softmax_sum(a, row, lane);
 #pragma unroll 1
-  for (int e = lane; e < a.E; e += 32) smem[e] = order_int64(exact_total(a, row, e, s));
+  for (int e0 = lane; e0 < a.E; e0 += 128) {
+    int64_t t[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[j] = order_int64(exact_total(a, row, min(e0 + 32 * j, a.E - 1), s));
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (e0 + 32 * j < a.E) smem[e0 + 32 * j] = t[j];
+  }
   __syncwarp();
   uint32_t mask = kAll;
   if (a.n_groups > 1) {
@@ -517,7 +535,7 @@ __host__ __device__ __forceinline__ size_t select_scratch(const RouteOpArgs& a) 
 __device__ __forceinline__ void place_slots(const RouteOpArgs& a, const uint32_t* s_mask, const int* s_first, int t0,
                                             int nt) {
   const int64_t base = static_cast<int64_t>(t0) * a.K;
-  for (int i = threadIdx.x; i < nt * a.K; i += kThreads) {
+  for (int i = threadIdx.x; i < nt * a.K; i += blockDim.x) {
     const int t = i / a.K;
     const int e = a.idx[base + i];
     int p = -1;
@@ -530,35 +548,49 @@ __device__ __forceinline__ void place_slots(const RouteOpArgs& a, const uint32_t
   }
 }
 
-// Exclusive scan of s_cnt[E] (E <= 2 kThreads) into s_first, the total in
-// s_first[E].
+// Exclusive scan of s_cnt[E] into s_first, the total in s_first[E], by the
+// whole CTA. s_tmp: a word per warp.
 __device__ __forceinline__ void scan_counts(const int* s_cnt, int* s_first, int* s_tmp, int E) {
-  const int e = 2 * threadIdx.x;
-  const int c0 = e < E ? s_cnt[e] : 0, c1 = e + 1 < E ? s_cnt[e + 1] : 0;
-  int total;
-  const int x = block_excl_scan(c0 + c1, s_tmp, &total);
-  if (e < E) s_first[e] = x;
-  if (e + 1 < E) s_first[e + 1] = x + c0;
-  if (threadIdx.x == 0) s_first[E] = total;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  int carry = 0;
+  for (int e0 = 0; e0 < E; e0 += blockDim.x) {
+    const int e = e0 + threadIdx.x;
+    const int v = e < E ? s_cnt[e] : 0;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(kAll, incl, o);
+      if (lane >= o) incl += n;
+    }
+    if (lane == 31) s_tmp[warp] = incl;
+    __syncthreads();
+    const int w = lane < warps ? s_tmp[lane] : 0;
+    const int before = __reduce_add_sync(kAll, lane < warp ? w : 0);
+    if (e < E) s_first[e] = carry + before + incl - v;
+    carry += __reduce_add_sync(kAll, w);
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) s_first[E] = carry;
   __syncthreads();
 }
 
 }  // namespace
 
 // Selection: one warp per token, cta_tokens tokens per CTA. Where the slots
-// are to be grouped, each CTA also leaves its counts per expert; a call that
-// one CTA takes groups them itself.
+// are to be grouped, a call that one cluster takes groups them too (each CTA
+// reads the others' counts in their shared memory); otherwise each CTA leaves
+// its counts per expert to the kernels below.
 template <int VPL>
 __global__ void __launch_bounds__(kThreads, VPL <= 8 ? 4 : 2) k_select(const RouteOpArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
   const size_t scratch = select_scratch(a);
   uint32_t* s_mask = reinterpret_cast<uint32_t*>(raw + kWarps * scratch);  // [E][2]
-  int* s_cnt = reinterpret_cast<int*>(s_mask + 2 * a.E);                                          // [E]
-  int* s_first = s_cnt + a.E;                                                                     // [E + 1]
-  __shared__ int s_tmp[17];
+  int* s_cnt = reinterpret_cast<int*>(s_mask + 2 * a.E);                      // [E]
+  int* s_first = s_cnt + a.E;                                                 // [E + 1]
+  __shared__ int s_tmp[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t0 = blockIdx.x * a.cta_tokens;
-  const int nt = min(a.cta_tokens, a.M - t0);
+  const int nt = min(a.cta_tokens, a.M - t0);  // below 1 in a cluster's last CTAs
   const bool grouping = a.offsets != nullptr;
   if (grouping) {
     for (int e = threadIdx.x; e < 2 * a.E; e += kThreads) s_mask[e] = 0;
@@ -586,15 +618,43 @@ __global__ void __launch_bounds__(kThreads, VPL <= 8 ? 4 : 2) k_select(const Rou
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += kThreads) {
     const int c = __popc(s_mask[2 * e]) + __popc(s_mask[2 * e + 1]);
-    if (a.n_ctas == 1)
+    if (a.shape.cluster)
       s_cnt[e] = c;
     else
       a.hist[static_cast<int64_t>(e) * a.n_ctas + blockIdx.x] = c;
   }
-  if (a.n_ctas > 1) return;
+  if (!a.shape.cluster) return;
+  const int ctas = a.n_ctas, rank = blockIdx.x;
+  int before[kPerThread];  // the expert's slots in earlier CTAs
+  if (ctas > 1) {
+    cluster_sync();  // every CTA's counts are there
+    int total[kPerThread];
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      const int e = threadIdx.x + j * kThreads;
+      before[j] = total[j] = 0;
+      for (int r = 0; e < a.E && r < ctas; ++r) {
+        const int v = cluster_load(cluster_map(smem_u32(&s_cnt[e]), r));
+        total[j] += v;
+        before[j] += r < rank ? v : 0;
+      }
+    }
+    cluster_sync();  // and read, so they may become the totals
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j)
+      if (threadIdx.x + j * kThreads < a.E) s_cnt[threadIdx.x + j * kThreads] = total[j];
+  }
   __syncthreads();
   scan_counts(s_cnt, s_first, s_tmp, a.E);
-  for (int e = threadIdx.x; e <= a.E; e += kThreads) a.offsets[e] = s_first[e];
+  if (rank == 0)
+    for (int e = threadIdx.x; e <= a.E; e += kThreads) a.offsets[e] = s_first[e];
+  if (ctas > 1) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j)
+      if (threadIdx.x + j * kThreads < a.E) s_first[threadIdx.x + j * kThreads] += before[j];
+    __syncthreads();
+  }
   place_slots(a, s_mask, s_first, t0, nt);
 }
 
@@ -621,32 +681,43 @@ __global__ void __launch_bounds__(kThreads) k_scan_hist(const RouteOpArgs a) {
   if (lane == 0) a.totals[e] = run;
 }
 
-// Each CTA takes the tokens it had in k_select and places their slots.
+// Places the slots of kRoutePlaceTokens tokens per CTA, from the scanned counts.
 __global__ void __launch_bounds__(kThreads) k_place(const RouteOpArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
   uint32_t* s_mask = reinterpret_cast<uint32_t*>(raw);
   int* s_cnt = reinterpret_cast<int*>(s_mask + 2 * a.E);
   int* s_first = s_cnt + a.E;
-  __shared__ int s_tmp[17];
-  const int t0 = blockIdx.x * a.cta_tokens;
-  const int nt = min(a.cta_tokens, a.M - t0);
+  __shared__ int s_tmp[kWarps];
+  const int t0 = blockIdx.x * plan::kRoutePlaceTokens;
+  const int nt = min(plan::kRoutePlaceTokens, a.M - t0);
   for (int e = threadIdx.x; e < 2 * a.E; e += kThreads) s_mask[e] = 0;
   __syncthreads();
   pdl_wait();
   pdl_trigger();
   const int64_t base = static_cast<int64_t>(t0) * a.K;
+  const int mine = t0 / a.cta_tokens;  // the first of k_select's CTAs that had these tokens
+  int before[kPerThread];
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    const int e = threadIdx.x + j * kThreads;
+    before[j] = 0;
+    if (e < a.E) {
+      before[j] = a.hist[static_cast<int64_t>(e) * a.n_ctas + mine];
+      s_cnt[e] = a.totals[e];
+    }
+  }
   for (int i = threadIdx.x; i < nt * a.K; i += kThreads) {
     const int t = i / a.K, e = a.idx[base + i];
     if (e >= 0) atomicOr(&s_mask[2 * e + (t >> 5)], 1u << (t & 31));
   }
-  for (int e = threadIdx.x; e < a.E; e += kThreads) s_cnt[e] = a.totals[e];
   __syncthreads();
   scan_counts(s_cnt, s_first, s_tmp, a.E);
   if (blockIdx.x == 0)
     for (int e = threadIdx.x; e <= a.E; e += kThreads) a.offsets[e] = s_first[e];
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += kThreads)
-    s_first[e] += a.hist[static_cast<int64_t>(e) * a.n_ctas + blockIdx.x];
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j)
+    if (threadIdx.x + j * kThreads < a.E) s_first[threadIdx.x + j * kThreads] += before[j];
   __syncthreads();
   place_slots(a, s_mask, s_first, t0, nt);
 }
@@ -664,11 +735,13 @@ cudaError_t launch_route_op(const RouteOpArgs& args, cudaStream_t s) {
   a.group_shift = -1;
   for (int b = 0; b <= 5; ++b)
     if (a.group_size == vpl << b) a.group_shift = b;
-  cudaError_t e = launch_kernel<RouteOpArgs>(k, dim3(a.n_ctas), dim3(kThreads), smem, s, true, a);
-  if (e != cudaSuccess || a.offsets == nullptr || a.n_ctas == 1) return e;
+  cudaError_t e =
+      launch_kernel<RouteOpArgs>(k, dim3(a.n_ctas), dim3(kThreads), smem, s, true, a, a.shape.cluster ? a.n_ctas : 1);
+  if (e != cudaSuccess || a.offsets == nullptr || a.shape.cluster) return e;
   e = launch_kernel<RouteOpArgs>(k_scan_hist, dim3((a.E + kWarps - 1) / kWarps), dim3(kThreads), 0, s, true, a);
   if (e != cudaSuccess) return e;
-  return launch_kernel<RouteOpArgs>(k_place, dim3(a.n_ctas), dim3(kThreads), tail, s, true, a);
+  const dim3 grid((a.M + plan::kRoutePlaceTokens - 1) / plan::kRoutePlaceTokens);
+  return launch_kernel<RouteOpArgs>(k_place, grid, dim3(kThreads), tail, s, true, a);
 }
 
 // ---------------------------------------------------------------- combine

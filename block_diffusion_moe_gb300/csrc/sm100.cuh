@@ -314,9 +314,9 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// ------------------------------------------------------------ CTA pairs
+// --------------------------------------------------- clusters, CTA pairs
 //
-// Two CTAs of a cluster (ranks 0 and 1) work on one tcgen05.mma: each holds
+// A pair: two CTAs of a cluster (ranks 0 and 1) work on one tcgen05.mma: each holds
 // half of A's rows and half of B's in its shared memory, and its half of the
 // accumulator's rows in its tensor memory. Rank 0 issues.
 
@@ -326,7 +326,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// Every thread of every CTA of the cluster (the warps converged).
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -335,6 +337,13 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
+}
+
+// A word of another CTA's shared memory (a cluster_map address).
+__device__ __forceinline__ int cluster_load(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 // Arrives on a barrier of another CTA of the cluster (a cluster_map address).

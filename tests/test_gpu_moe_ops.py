@@ -47,7 +47,7 @@ def _check_route(logits, r_kw, bias=None, out=None, ws=None):
 
 SHAPES = [  # M, E, K
     (1, 256, 8), (1, 1, 1), (2, 7, 7), (3, 32, 32), (9, 60, 6), (64, 64, 2), (65, 65, 3), (130, 128, 1), (257, 256, 8),
-    (70, 384, 10), (33, 512, 32),
+    (70, 384, 10), (33, 512, 32), (16, 256, 8), (256, 512, 4), (512, 256, 8), (513, 256, 8),
 ]
 
 

@@ -247,3 +247,35 @@ def test_product_arguments_refused(lib, kw, code):
 def test_product_nothing_to_do(lib):
     assert lib.clover_fp4_product_workspace_bytes() == 256
     assert lib.clover_fp4_product(*dict(PRODUCT, n_rows=0, a=None, b=None, y=None).values()) == C.OK
+
+
+PLAN = r"""
+#include <cstdio>
+#include "plan.h"
+using namespace clover::plan;
+int main() {
+  for (int t = 1; t <= 200000; t += t < 2000 ? 1 : 997) {
+    const RouteShape s = route_shape(t);
+    printf("%d %d %d %d\n", t, s.cta_tokens, s.ctas, s.cluster ? 1 : 0);
+  }
+  return 0;
+}
+"""
+
+
+def test_route_shapes(tmp_path):
+    """Every token has a place, a CTA's tokens fit its 64-bit masks and divide the
+    placing launch's 64, a cluster is of at most 8 CTAs."""
+    import os
+    import shutil
+    import subprocess
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no host C++ compiler")
+    (tmp_path / "p.cpp").write_text(PLAN)
+    subprocess.run([cxx, "-std=c++17", "-I", B.CSRC, str(tmp_path / "p.cpp"), "-o", str(tmp_path / "p")], check=True)
+    out = subprocess.run([str(tmp_path / "p")], check=True, capture_output=True, text=True, cwd=os.fspath(tmp_path)).stdout
+    for line in out.splitlines():
+        tokens, per, ctas, cluster = map(int, line.split())
+        assert per * ctas >= tokens and per <= 64 and per % 8 == 0 and 64 % per == 0, line
+        assert ctas in (1, 2, 4, 8) if cluster else (ctas - 1) * per < tokens, line
