@@ -113,122 +113,30 @@ __device__ __forceinline__ void two_best(float& b1, float& b2, float v) {
   b1 = fmaxf(b1, v);
 }
 
-// What experts are ordered by: -inf for a dead expert and for one in a group
-// that does not stay. x: the logits, -inf where dead. False where the token has
-// no live expert (every lane alike).
-//
-// *err bounds the error of a key, and *doubt is set (in every lane) where the
-// ranks on either side of the group border are closer than the errors they can
-// have. With m the largest score: a softmax score is off by less than 2^-19 m
-// (exp and quotient a few roundings each, the sum up to 21). A sigmoid: by its
-// documented bound __expf is off by (2 + 1.18 |x|) 2^-23 of the value, which
-// changes s by (1 - s) s of that; s (1 - s) |x| is below 0.23, and below m |x of
-// m| where all logits are low, so with the quotient's 2^-22 less than
-// (2^-20 + 2^-22 max(-x of m, 0)) m. The sum with the bias adds half a unit of
-// the key. Logits used as keys are exact.
+// Lists this warp's keys at or above the lane's bound (and above -inf) in shared
+// memory, lower lanes first: (key, id). Returns their number; a number above 32
+// and no list where they do not fit.
 template <int VPL>
-__device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float (&x)[VPL], const float (&bias)[VPL],
-                                           float bias_max, float* smem, int lane, float (&key)[VPL], float* err,
-                                           bool* doubt) {
-  *err = 0.f;
+__device__ __forceinline__ int list_above(const float (&key)[VPL], float bound, uint2* list, int lane) {
+  bound = fmaxf(bound, -3.402823466e+38f);
+  int c = 0;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) key[i] = x[i];
-  const bool sums = a.n_groups > 1 && a.group_rank == 2;  // ranks are sums of scores
-  if (a.bias != nullptr || sums) {
-    float xm = x[0], xl = x[0];
+  for (int i = 0; i < VPL; ++i) c += key[i] >= bound ? 1 : 0;
+  // places by lane: the sum of the lower lanes' counts, bit by bit
+  const uint32_t lower = (1u << lane) - 1u;
+  int at = 0, n = 0;
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) xm = fmaxf(xm, x[i]), xl = fminf(xl, x[i]);
-    xm = warp_max_fast(xm);
-    if (xm == -INFINITY) return false;
-    float s_max;
-    if (a.softmax) {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        key[i] = expf(x[i] - xm);
-        sum += key[i];
-      }
-      s_max = 1.f / warp_sum_f(sum);  // the sum is at least 1
-      *err = s_max * 0x1p-19f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] *= s_max;
-    } else {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = fast_sigmoid(x[i]);
-      s_max = fast_sigmoid(xm);
-      *err = s_max * (0x1p-20f + 0x1p-22f * fmaxf(-xm, 0.f));
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] += bias[i];
-    if (__any_sync(kAll, xl == -INFINITY)) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = x[i] > -INFINITY ? key[i] : -INFINITY;
-    }
-    *err += (s_max + bias_max) * 0x1p-23f + 1e-37f;
+  for (int bit = 0; (1 << bit) <= VPL; ++bit) {
+    const uint32_t v = __ballot_sync(kAll, (c >> bit) & 1);
+    at += __popc(v & lower) << bit;
+    n += __popc(v) << bit;
   }
-  if (a.n_groups == 1) return true;
-
-  // Group ranks. Without a bias experts go by their logits, whatever the
-  // groups go by.
-  float b1 = -INFINITY, b2 = -INFINITY;
-  int g = lane, shift = 0;  // this lane's group; groups lie 2^shift lanes apart
-  if (a.group_shift >= 0) {
-    // a group is all slots of a power of two of neighbouring lanes
+  if (n > 32) return n;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) two_best(b1, b2, key[i]);
-    shift = a.group_shift;
-    g = lane >> shift;
-    for (int o = 1; o < (1 << shift); o <<= 1) {
-      const float c1 = __shfl_xor_sync(kAll, b1, o), c2 = __shfl_xor_sync(kAll, b2, o);
-      two_best(b1, b2, c1);
-      b2 = fmaxf(b2, c2);
-    }
-  } else {
-    // any other size: keys in shared memory, lane g scans group g
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (lane * VPL + i < a.E) smem[lane * VPL + i] = key[i];
-    __syncwarp();
-    if (g < a.n_groups)
-      for (int n = 0; n < a.group_size; ++n) two_best(b1, b2, smem[g * a.group_size + n]);
-    __syncwarp();
-  }
-  const float rank = (a.group_rank == 2 && b2 > -INFINITY) ? b1 + b2 : b1;
-  // the groups before this one; a group's lanes share the comparisons
-  const int step = 1 << shift;
-  int before = 0;
-  for (int j0 = 0; j0 < a.n_groups; j0 += step) {
-    const int j = j0 + (lane & (step - 1));
-    const float r = __shfl_sync(kAll, rank, (j << shift) & 31);
-    before += (j < a.n_groups && (r > rank || (r == rank && j < g))) ? 1 : 0;
-  }
-  for (int o = 1; o < step; o <<= 1) before += __shfl_xor_sync(kAll, before, o);
-  if (g >= a.n_groups) before = kNoGroup;
-  if (*err > 0.f) {
-    // the last group that stays and the first that does not
-    const float in = __shfl_sync(kAll, rank, __ffs(__ballot_sync(kAll, before == a.top_groups - 1)) - 1);
-    const float out = __shfl_sync(kAll, rank, __ffs(__ballot_sync(kAll, before == a.top_groups)) - 1);
-    *doubt = out > -INFINITY && !(in - out > (a.group_rank == 2 ? 4.f : 2.f) * *err);
-  }
-  if (a.bias == nullptr) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = x[i];
-    *err = 0.f;
-  }
-  if (a.group_shift >= 0) {
-    if (before >= a.top_groups) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = -INFINITY;
-    }
-  } else {
-    const uint32_t mask = __ballot_sync(kAll, before < a.top_groups);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane * VPL + i;
-      if (e < a.E && ((mask >> (e / a.group_size)) & 1u) == 0) key[i] = -INFINITY;
-    }
-  }
-  return true;
+  for (int i = 0; i < VPL; ++i)
+    if (key[i] >= bound) list[at++] = make_uint2(__float_as_uint(key[i]), lane * VPL + i);
+  __syncwarp();
+  return n;
 }
 
 // ---- The order in exact arithmetic: in double, as the definition has it. Rare
@@ -357,6 +265,164 @@ __device__ __noinline__ int select_exact(const RouteOpArgs& a, int64_t row, int 
   return mine;
 }
 
+// Groups before this lane's, by exact ranks: lane k < n holds one of the
+// candidates (the experts that can be among the one or two best of their
+// group). g: this lane's group.
+__device__ __noinline__ int rank_groups_exact(const RouteOpArgs& a, int64_t row, int id, int n, int g, int lane,
+                                              int64_t* smem) {
+  const int64_t ninf = order_int64(-static_cast<double>(INFINITY));
+  SoftmaxSum s = {0, 1};
+  if (a.softmax) s = softmax_sum(a, row, lane);
+  if (lane < n) smem[lane] = order_int64(exact_total(a, row, id, s));
+  __syncwarp();
+  int64_t b1 = ninf, b2 = ninf;  // of group `lane`
+  for (int j = 0; j < n; ++j) {
+    const int64_t v = __shfl_sync(kAll, id, j) / a.group_size == lane ? smem[j] : ninf;
+    b2 = max(b2, min(b1, v));
+    b1 = max(b1, v);
+  }
+  __syncwarp();
+  const int64_t rank = (a.group_rank == 2 && b2 > ninf) ? order_int64(order_double(b1) + order_double(b2)) : b1;
+  const int64_t mine = __shfl_sync(kAll, rank, g & 31);
+  int before = 0;
+  for (int j = 0; j < a.n_groups; ++j) {
+    const int64_t r = __shfl_sync(kAll, rank, j);
+    before += (r > mine || (r == mine && j < g)) ? 1 : 0;
+  }
+  return before;
+}
+
+// What experts are ordered by: -inf for a dead expert and for one in a group
+// that does not stay. x: the logits, -inf where dead. False where the token has
+// no live expert (every lane alike).
+//
+// *err bounds the error of a key, and *doubt is set (in every lane) where the
+// ranks on either side of the group border are closer than the errors they can
+// have and are not settled here. With m the largest score: a softmax score is off by less than 2^-19 m
+// (exp and quotient a few roundings each, the sum up to 21). A sigmoid: by its
+// documented bound __expf is off by (2 + 1.18 |x|) 2^-23 of the value, which
+// changes s by (1 - s) s of that; s (1 - s) |x| is below 0.23, and below m |x of
+// m| where all logits are low, so with the quotient's 2^-22 less than
+// (2^-20 + 2^-22 max(-x of m, 0)) m. The sum with the bias adds half a unit of
+// the key. Logits used as keys are exact.
+template <int VPL>
+__device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float (&x)[VPL], const float (&bias)[VPL],
+                                           float bias_max, int64_t row, int64_t* smem, int lane, float (&key)[VPL],
+                                           float* err, bool* doubt) {
+  *err = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) key[i] = x[i];
+  const bool sums = a.n_groups > 1 && a.group_rank == 2;  // ranks are sums of scores
+  if (a.bias != nullptr || sums) {
+    float xm = x[0], xl = x[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) xm = fmaxf(xm, x[i]), xl = fminf(xl, x[i]);
+    xm = warp_max_fast(xm);
+    if (xm == -INFINITY) return false;
+    float s_max;
+    if (a.softmax) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        key[i] = expf(x[i] - xm);
+        sum += key[i];
+      }
+      s_max = 1.f / warp_sum_f(sum);  // the sum is at least 1
+      *err = s_max * 0x1p-19f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] *= s_max;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = fast_sigmoid(x[i]);
+      s_max = fast_sigmoid(xm);
+      *err = s_max * (0x1p-20f + 0x1p-22f * fmaxf(-xm, 0.f));
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] += bias[i];
+    if (__any_sync(kAll, xl == -INFINITY)) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = x[i] > -INFINITY ? key[i] : -INFINITY;
+    }
+    *err += (s_max + bias_max) * 0x1p-23f + 1e-37f;
+  }
+  if (a.n_groups == 1) return true;
+
+  // Group ranks. Without a bias experts go by their logits, whatever the
+  // groups go by.
+  float b1 = -INFINITY, b2 = -INFINITY;
+  int g = lane, shift = 0;  // this lane's group; groups lie 2^shift lanes apart
+  if (a.group_shift >= 0) {
+    // a group is all slots of a power of two of neighbouring lanes
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) two_best(b1, b2, key[i]);
+    shift = a.group_shift;
+    g = lane >> shift;
+    for (int o = 1; o < (1 << shift); o <<= 1) {
+      const float c1 = __shfl_xor_sync(kAll, b1, o), c2 = __shfl_xor_sync(kAll, b2, o);
+      two_best(b1, b2, c1);
+      b2 = fmaxf(b2, c2);
+    }
+  } else {
+    // any other size: keys in shared memory, lane g scans group g
+    float* s_keys = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (lane * VPL + i < a.E) s_keys[lane * VPL + i] = key[i];
+    __syncwarp();
+    if (g < a.n_groups)
+      for (int n = 0; n < a.group_size; ++n) two_best(b1, b2, s_keys[g * a.group_size + n]);
+    __syncwarp();
+  }
+  const float rank = (a.group_rank == 2 && b2 > -INFINITY) ? b1 + b2 : b1;
+  // the groups before this one; a group's lanes share the comparisons
+  const int step = 1 << shift;
+  int before = 0;
+  for (int j0 = 0; j0 < a.n_groups; j0 += step) {
+    const int j = j0 + (lane & (step - 1));
+    const float r = __shfl_sync(kAll, rank, (j << shift) & 31);
+    before += (j < a.n_groups && (r > rank || (r == rank && j < g))) ? 1 : 0;
+  }
+  for (int o = 1; o < step; o <<= 1) before += __shfl_xor_sync(kAll, before, o);
+  if (g >= a.n_groups) before = kNoGroup;
+  if (*err > 0.f) {
+    // the last group that stays and the first that does not
+    const float in = __shfl_sync(kAll, rank, __ffs(__ballot_sync(kAll, before == a.top_groups - 1)) - 1);
+    const float out = __shfl_sync(kAll, rank, __ffs(__ballot_sync(kAll, before == a.top_groups)) - 1);
+    *doubt = out > -INFINITY && !(in - out > (a.group_rank == 2 ? 4.f : 2.f) * *err);
+    if (*doubt && a.group_shift >= 0) {
+      // the ranks again, from the exact scores of the few that can matter
+      uint2* list = reinterpret_cast<uint2*>(smem);
+      const int n = list_above<VPL>(key, (a.group_rank == 2 ? b2 : b1) - 2.f * *err, list, lane);
+      if (n <= 32) {
+        const int id = lane < n ? static_cast<int>(list[lane].y) : 0;
+        __syncwarp();
+        before = rank_groups_exact(a, row, id, n, g, lane, smem);
+        if (g >= a.n_groups) before = kNoGroup;
+        *doubt = false;
+      }
+    }
+  }
+  if (a.bias == nullptr) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = x[i];
+    *err = 0.f;
+  }
+  if (a.group_shift >= 0) {
+    if (before >= a.top_groups) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = -INFINITY;
+    }
+  } else {
+    const uint32_t mask = __ballot_sync(kAll, before < a.top_groups);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = lane * VPL + i;
+      if (e < a.E && ((mask >> (e / a.group_size)) & 1u) == 0) key[i] = -INFINITY;
+    }
+  }
+  return true;
+}
+
 // Whether two experts' keys, closer than their errors, are a true tie: the
 // same logit and the same bias.
 __device__ __forceinline__ bool same_key(const RouteOpArgs& a, int64_t row, int e, int f) {
@@ -418,27 +484,10 @@ __device__ __forceinline__ bool pick_by_count(const RouteOpArgs& a, int64_t row,
     bound_int = __reduce_max_sync(kAll, m);
     m = m == bound_int ? kNone : m;
   }
-  // at least the lowest finite float: dead experts are not listed
-  float bound = bound_int == kNone ? -INFINITY : order_float(bound_int);
-  bound = fmaxf(bound - 2.f * err, -3.402823466e+38f);
-  int c = 0;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) c += key[i] >= bound ? 1 : 0;
-  // places by lane: the sum of the lower lanes' counts, bit by bit
-  const uint32_t lower = (1u << lane) - 1u;
-  int at = 0, n = 0;
-#pragma unroll
-  for (int bit = 0; (1 << bit) <= VPL; ++bit) {
-    const uint32_t v = __ballot_sync(kAll, (c >> bit) & 1);
-    at += __popc(v & lower) << bit;
-    n += __popc(v) << bit;
-  }
-  if (n > 32) return false;
+  const float bound = bound_int == kNone ? -INFINITY : order_float(bound_int);
   uint2* list = reinterpret_cast<uint2*>(smem);  // [32]
-#pragma unroll
-  for (int i = 0; i < VPL; ++i)
-    if (key[i] >= bound) list[at++] = make_uint2(__float_as_uint(key[i]), lane * VPL + i);
-  __syncwarp();
+  const int n = list_above<VPL>(key, bound - 2.f * err, list, lane);
+  if (n > 32) return false;
   // (key, lower id first) as one unsigned number; 0 for no entry
   uint64_t own = 0;
   if (lane < n) {
@@ -481,7 +530,7 @@ __device__ __forceinline__ int select_token(const RouteOpArgs& a, int64_t row, c
                                             const float (&bias)[VPL], float bias_max, int64_t* smem, int lane) {
   float key[VPL], err;
   bool doubt = false;
-  if (!token_keys<VPL>(a, x, bias, bias_max, reinterpret_cast<float*>(smem), lane, key, &err, &doubt)) return -1;
+  if (!token_keys<VPL>(a, x, bias, bias_max, row, smem, lane, key, &err, &doubt)) return -1;
   // with inexact keys one more than K, to see the key that just missed
   const int want = err > 0.f ? a.K + 1 : a.K;
   int mine = -1;
