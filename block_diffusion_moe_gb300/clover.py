@@ -356,42 +356,46 @@ SCORE_SIGMOID = 1
 FP4_NV = 0
 FP4_MX = 1
 _SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
-_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+_F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
+_TYPES = {_F32: 0, _BF16: 1}
+# (calls of a few microseconds: the device and stream objects of torch.cuda cost as much as the launch)
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _refuse(msg: str):
     raise CloverError(ERR_INVALID_ARG, msg)
 
 
-def _tensor(name: str, t, dtype, shape, device) -> int:
-    """The pointer of a contiguous tensor of this type and shape on `device`."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        _refuse(f"{name}: need contiguous {dtype} {tuple(shape)} on {device}, "
+def _tensor(name: str, t, dtype, shape, dev: int) -> int:
+    """The pointer of a contiguous tensor of this type and shape on CUDA device `dev`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(f"{name}: need contiguous {dtype} {tuple(shape)} on cuda:{dev}, "
                 f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
     return t.data_ptr()
 
 
+def _on_current(name: str, t) -> int:
+    """The index of the current CUDA device, which holds t."""
+    dev = t.get_device()  # -1 on the host
+    if dev < 0 or dev != _current_device():
+        _refuse(f"{name} is on {t.device}, not on the current CUDA device")
+    return dev
+
+
 def _rows_of(name: str, t):
-    """(pointer, type code, row stride in elements) of a 2-D fp32 or bf16 tensor with contiguous rows on the
+    """(device, pointer, type code, row stride in elements) of a 2-D fp32 or bf16 tensor with contiguous rows on the
     current device."""
-    kind = _TYPES.get(t.dtype)
-    strides = t.stride()
+    dev, kind, strides = _on_current(name, t), _TYPES.get(t.dtype), t.stride()
     if len(strides) != 2 or kind is None or (strides[1] != 1 and t.shape[1] > 1):
         _refuse(f"{name}: need a 2-D fp32 or bf16 tensor with contiguous rows, got {t.dtype} {tuple(t.shape)}, "
                 f"strides {strides}")
-    _on_current(name, t.device)
     rows, cols = t.shape
-    return t.data_ptr(), kind, (strides[0] if rows > 1 else max(strides[0], cols))
+    return dev, t.data_ptr(), kind, (strides[0] if rows > 1 else max(strides[0], cols))
 
 
-def _on_current(name: str, device):
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        _refuse(f"{name} is on {device}, not on the current CUDA device")
-
-
-def _raw_stream(stream, device) -> int:
-    # (the stream object costs more than the launch it is for)
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+def _raw_stream(stream, dev: int) -> int:
+    return _current_stream(dev) if stream is None else stream.cuda_stream
 
 
 def make_routing(n_experts: int, top_k: int, score: str = "softmax", n_groups: int = 1, top_groups: int | None = None,
@@ -411,30 +415,32 @@ def route(r: Routing, logits, bias=None, grouping: bool = True, ws=None, out=Non
     """Expert selection from router logits [M][E] (fp32 or bf16, rows may be strided) -> idx int32 [M][K], w fp32
     [M][K] and, with grouping, offsets int32 [E + 1], rows int32 [M * K], pos int32 [M][K]. `out` (a dict this
     function returned before, for the same shape) is reused."""
-    p_logits, kind, ld = _rows_of("logits", logits)
-    (M, cols), dev = logits.shape, logits.device
+    dev, p_logits, kind, ld = _rows_of("logits", logits)
+    M, cols = logits.shape
     K, E = r.top_k, r.n_experts
     if cols != E:
         _refuse(f"logits have {cols} columns for {E} experts")
-    i32 = torch.int32
-    p_bias = None if bias is None else _tensor("bias", bias, torch.float32, (E,), dev)
+    slots = (M, K)
+    p_bias = None if bias is None else _tensor("bias", bias, _F32, (E,), dev)
     if ws is None:
-        ws = workspace(route_workspace_bytes(r, M), dev)
+        ws = workspace(route_workspace_bytes(r, M), logits.device)
     if out is None:
-        out = {"idx": torch.empty((M, K), dtype=i32, device=dev),
-               "w": torch.empty((M, K), dtype=torch.float32, device=dev)}
+        device = logits.device
+        out = {"idx": torch.empty(slots, dtype=_I32, device=device), "w": torch.empty(slots, dtype=_F32, device=device)}
         if grouping:
-            out["offsets"] = torch.empty(E + 1, dtype=i32, device=dev)
-            out["rows"] = torch.empty(M * K, dtype=i32, device=dev)
-            out["pos"] = torch.empty((M, K), dtype=i32, device=dev)
+            out["offsets"] = torch.empty(E + 1, dtype=_I32, device=device)
+            out["rows"] = torch.empty(M * K, dtype=_I32, device=device)
+            out["pos"] = torch.empty(slots, dtype=_I32, device=device)
     p_off = p_rows = p_pos = None
     if grouping:
-        p_off = _tensor("offsets", out["offsets"], i32, (E + 1,), dev)
-        p_rows = _tensor("rows", out["rows"], i32, (M * K,), dev)
-        p_pos = _tensor("pos", out["pos"], i32, (M, K), dev)
-    _check(lib().clover_route(r, p_logits, kind, ld, p_bias, M, _tensor("idx", out["idx"], i32, (M, K), dev),
-                              _tensor("w", out["w"], torch.float32, (M, K), dev), p_off, p_rows, p_pos, ws.data_ptr(),
-                              ws.numel(), _raw_stream(stream, dev)))
+        p_off = _tensor("offsets", out["offsets"], _I32, (E + 1,), dev)
+        p_rows = _tensor("rows", out["rows"], _I32, (M * K,), dev)
+        p_pos = _tensor("pos", out["pos"], _I32, slots, dev)
+    rc = lib().clover_route(r, p_logits, kind, ld, p_bias, M, _tensor("idx", out["idx"], _I32, slots, dev),
+                            _tensor("w", out["w"], _F32, slots, dev), p_off, p_rows, p_pos, ws.data_ptr(), ws.numel(),
+                            _raw_stream(stream, dev))
+    if rc != OK:
+        _check(rc)
     return out
 
 
@@ -443,10 +449,10 @@ class Fp4:
     uint8 (1-D), and the power of two the values are scaled by. With offsets (int32 [groups + 1]) the rows of one
     matrix form groups. The parts are checked against one another here, once."""
 
-    __slots__ = ("fmt", "codes", "scales", "scale_exp", "_offsets", "device", "mats", "rows", "cols")
+    __slots__ = ("fmt", "codes", "scales", "scale_exp", "_offsets", "device", "mats", "rows", "cols", "groups")
 
     def __init__(self, fmt: int, codes, scales, scale_exp: int = 0, offsets=None):
-        if codes.dtype != torch.uint8 or codes.dim() not in (2, 3) or not codes.is_contiguous():
+        if codes.dtype != _U8 or codes.dim() not in (2, 3) or not codes.is_contiguous():
             _refuse(f"codes: need contiguous uint8 [rows][cols / 2] or [mats][rows][cols / 2], got {codes.dtype} "
                     f"{tuple(codes.shape)}")
         if scales.dtype != torch.uint8 or scales.device != codes.device or not scales.is_contiguous():
@@ -464,6 +470,7 @@ class Fp4:
         q = object.__new__(cls)
         q.fmt, q.codes, q.scales, q.scale_exp, q._offsets = fmt, codes, scales, scale_exp, offsets
         q.device, q.mats, q.rows, q.cols = device, mats, rows, cols
+        q.groups = 0 if offsets is None else offsets.shape[0] - 1
         return q
 
     @property
@@ -484,6 +491,7 @@ class Fp4:
         if self.scales.numel() < need:
             _refuse(f"scales: {self.scales.numel()} bytes, need {need}")
         self._offsets = offsets
+        self.groups = 0 if offsets is None else offsets.shape[0] - 1
 
 
 def fp4_scale_bytes(fmt: int, n_mats: int, rows: int, cols: int, n_groups: int | None = None) -> int:
@@ -506,55 +514,55 @@ def quantize_fp4(x, fmt: int = FP4_NV, scale_exp: int = 0, offsets=None, src_row
     if len(shape) == 3:
         if grouped or not x.is_contiguous():
             _refuse("x: matrices must be contiguous, and grouped rows one matrix")
-        p_x, kind, ldx = _rows_of("x", x.view(-1, shape[-1]))
+        dev, p_x, kind, ldx = _rows_of("x", x.view(-1, shape[-1]))
     else:
-        p_x, kind, ldx = _rows_of("x", x)
-    dev, cols = x.device, shape[-1]
+        dev, p_x, kind, ldx = _rows_of("x", x)
+    cols, rows, p_src = shape[-1], shape[-2], None
     if src_rows is not None:
         if not grouped:
             _refuse("src_rows without offsets")
         rows = src_rows.shape[0]
-        p_src = _tensor("src_rows", src_rows, torch.int32, (rows,), dev)
-    else:
-        rows, p_src = shape[-2], None
+        p_src = _tensor("src_rows", src_rows, _I32, (rows,), dev)
     codes_shape = shape[:-2] + (rows, cols // 2)
     n_groups = p_off = None
     if grouped:
         n_groups = offsets.shape[0] - 1
-        p_off = _tensor("offsets", offsets, torch.int32, (n_groups + 1,), dev)
+        p_off = _tensor("offsets", offsets, _I32, (n_groups + 1,), dev)
     if out is None:
-        mats = shape[0] if len(shape) == 3 else 1
+        mats, device = shape[0] if len(shape) == 3 else 1, x.device
         n = fp4_scale_bytes(fmt, mats, rows, cols, n_groups)
-        out = Fp4._made(fmt, torch.empty(codes_shape, dtype=torch.uint8, device=dev),
-                        torch.empty(n, dtype=torch.uint8, device=dev), scale_exp, offsets, dev, mats, rows, cols)
-    elif out.fmt != fmt or out.codes.shape != codes_shape or out.device != dev:
+        out = Fp4._made(fmt, torch.empty(codes_shape, dtype=_U8, device=device),
+                        torch.empty(n, dtype=_U8, device=device), scale_exp, offsets, device, mats, rows, cols)
+    elif out.fmt != fmt or out.codes.shape != codes_shape or out.device != x.device:
         _refuse(f"out holds {tuple(out.codes.shape)} of format {out.fmt} on {out.device}")
     else:
         out.offsets, out.scale_exp = offsets, scale_exp
     if grouped:
-        rc = lib().clover_quantize_fp4_rows(fmt, p_x, kind, ldx, shape[0], cols, scale_exp, p_src, src_div, rows,
-                                            p_off, n_groups, out.codes.data_ptr(), out.scales.data_ptr(),
+        rc = lib().clover_quantize_fp4_rows(fmt, p_x, kind, ldx, shape[0], cols, scale_exp, p_src, src_div, rows, p_off,
+                                            n_groups, out.codes.data_ptr(), out.scales.data_ptr(),
                                             _raw_stream(stream, dev))
     else:
         rc = lib().clover_quantize_fp4(fmt, p_x, kind, ldx, out.mats, rows, cols, scale_exp, out.codes.data_ptr(),
                                        out.scales.data_ptr(), _raw_stream(stream, dev))
-    _check(rc)
+    if rc != OK:
+        _check(rc)
     return out
 
 
 def dequantize_fp4(q: Fp4, out=None, stream=None):
     """The bf16 matrices the codes stand for (rows behind the last group left as they were)."""
-    dev, off = q.device, q.offsets
-    _on_current("q", dev)
-    shape = q.codes.shape[:-1] + (q.cols,)
+    codes, off = q.codes, q._offsets
+    dev = _on_current("q", codes)
+    shape = codes.shape[:-1] + (q.cols,)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
         p_out = out.data_ptr()
     else:
-        p_out = _tensor("out", out, torch.bfloat16, shape, dev)
-    _check(lib().clover_dequantize_fp4(q.fmt, q.codes.data_ptr(), q.scales.data_ptr(), q.mats, q.rows, q.cols,
-                                       q.scale_exp, None if off is None else off.data_ptr(),
-                                       0 if off is None else off.shape[0] - 1, p_out, _raw_stream(stream, dev)))
+        p_out = _tensor("out", out, _BF16, shape, dev)
+    rc = lib().clover_dequantize_fp4(q.fmt, codes.data_ptr(), q.scales.data_ptr(), q.mats, q.rows, q.cols, q.scale_exp,
+                                     None if off is None else off.data_ptr(), q.groups, p_out, _raw_stream(stream, dev))
+    if rc != OK:
+        _check(rc)
     return out
 
 
@@ -568,29 +576,31 @@ def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_
     [rows][N], or with swiglu silu(gate) * up, [rows][N / 2]. b holds one [N][cols] matrix per group, or with swiglu two
     of N / 2 rows (gate, up). The result is scaled by alpha, group_alpha (fp32 [groups]) and both operands' scale_exp;
     rows behind the last group are left as they were."""
-    dev, off, per = a.device, a.offsets, 2 if swiglu else 1
-    _on_current("a", dev)
-    if a.codes.dim() != 2 or b.offsets is not None:
+    codes, off, per = a.codes, a._offsets, 2 if swiglu else 1
+    dev = _on_current("a", codes)
+    if codes.dim() != 2 or b._offsets is not None:
         _refuse("a must be one matrix, and only its rows may form groups")
-    if a.fmt != b.fmt or a.cols != b.cols or b.device != dev:
-        _refuse(f"a (format {a.fmt}, {a.cols} columns, {dev}) does not match b (format {b.fmt}, {b.cols} columns, "
+    if a.fmt != b.fmt or a.cols != b.cols or b.device != a.device:
+        _refuse(f"a (format {a.fmt}, {a.cols} columns, {a.device}) does not match b (format {b.fmt}, {b.cols} columns, "
                 f"{b.device})")
     rows, width = a.rows, b.rows
-    groups = 1 if off is None else off.shape[0] - 1
+    groups = 1 if off is None else a.groups
     if b.mats != groups * per:
         _refuse(f"b holds {b.mats} matrices for {groups} groups, {per} each")
     if ws is None:
-        ws = workspace(fp4_product_workspace_bytes(), dev)
+        ws = workspace(fp4_product_workspace_bytes(), a.device)
     if out is None:
-        out = torch.empty((rows, width), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((rows, width), dtype=_BF16, device=a.device)
         p_out = out.data_ptr()
     else:
-        p_out = _tensor("out", out, torch.bfloat16, (rows, width), dev)
-    p_alpha = None if group_alpha is None else _tensor("group_alpha", group_alpha, torch.float32, (groups,), dev)
-    _check(lib().clover_fp4_product(a.fmt, a.codes.data_ptr(), a.scales.data_ptr(), rows, b.codes.data_ptr(),
-                                    b.scales.data_ptr(), None if off is None else off.data_ptr(), groups, width * per,
-                                    a.cols, alpha * 2.0 ** (a.scale_exp + b.scale_exp), p_alpha, int(swiglu), p_out,
-                                    ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)))
+        p_out = _tensor("out", out, _BF16, (rows, width), dev)
+    p_alpha = None if group_alpha is None else _tensor("group_alpha", group_alpha, _F32, (groups,), dev)
+    rc = lib().clover_fp4_product(a.fmt, codes.data_ptr(), a.scales.data_ptr(), rows, b.codes.data_ptr(),
+                                  b.scales.data_ptr(), None if off is None else off.data_ptr(), groups, width * per,
+                                  a.cols, alpha * 2.0 ** (a.scale_exp + b.scale_exp), p_alpha, int(swiglu), p_out,
+                                  ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+    if rc != OK:
+        _check(rc)
     return out
 
 
@@ -599,18 +609,20 @@ def moe_combine(y, pos, w, x=None, shared=None, out=None, stream=None):
     gives them, x fp32 and shared bf16 [M][H] or None. out may be x itself."""
     if y.dim() != 2 or pos.dim() != 2:
         _refuse(f"y and pos must be matrices, got {tuple(y.shape)} and {tuple(pos.shape)}")
-    slots, (n, H), dev = pos.shape, y.shape, y.device
-    M, K = slots
-    _on_current("y", dev)
-    f32, bf16 = torch.float32, torch.bfloat16
+    dev = _on_current("y", y)
+    slots, y_shape = pos.shape, y.shape
+    (M, K), (n, H) = slots, y_shape
+    full = (M, H)
     if out is None:
-        out = torch.empty((M, H), dtype=f32, device=dev)
+        out = torch.empty(full, dtype=_F32, device=y.device)
         p_out = out.data_ptr()
     else:
-        p_out = _tensor("out", out, f32, (M, H), dev)
-    p_shared = None if shared is None else _tensor("shared", shared, bf16, (M, H), dev)
-    p_x = None if x is None else _tensor("x", x, f32, (M, H), dev)
-    _check(lib().clover_moe_combine(_tensor("y", y, bf16, (n, H), dev), n, _tensor("pos", pos, torch.int32, slots, dev),
-                                    _tensor("w", w, f32, slots, dev), p_shared, p_x, p_out, M, K, H,
-                                    _raw_stream(stream, dev)))
+        p_out = _tensor("out", out, _F32, full, dev)
+    rc = lib().clover_moe_combine(_tensor("y", y, _BF16, y_shape, dev), n, _tensor("pos", pos, _I32, slots, dev),
+                                  _tensor("w", w, _F32, slots, dev),
+                                  None if shared is None else _tensor("shared", shared, _BF16, full, dev),
+                                  None if x is None else _tensor("x", x, _F32, full, dev), p_out, M, K, H,
+                                  _raw_stream(stream, dev))
+    if rc != OK:
+        _check(rc)
     return out
