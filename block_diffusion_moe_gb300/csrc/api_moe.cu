@@ -58,14 +58,8 @@ int check_routing(const clover_routing* r) {
   return CLOVER_OK;
 }
 
-// Most CTAs any call of at most M tokens uses (more tokens may take fewer,
-// larger ones).
-int64_t max_route_ctas(int64_t M) {
-  return std::min<int64_t>((M + 7) / 8, std::max<int64_t>(304, (M + kRouteOpCtaTokens - 1) / kRouteOpCtaTokens));
-}
-
 size_t route_bytes(const clover_routing& r, int32_t M) {
-  return kCtrlBytes + static_cast<size_t>(r.n_experts) * (max_route_ctas(M) + 1) * 4;
+  return kCtrlBytes + static_cast<size_t>(r.n_experts) * (static_cast<size_t>(plan::route_max_ctas(M)) + 1) * 4;
 }
 
 int fp4_block(int32_t format) { return format == CLOVER_FP4_MX ? 32 : 16; }
@@ -184,6 +178,9 @@ int clover_route(const clover_routing* routing, const void* logits, int32_t logi
   a.shape = plan::route_shape(M);
   a.n_ctas = a.shape.ctas;
   a.cta_tokens = a.shape.cta_tokens;
+  if (!a.shape.cluster && a.n_ctas > plan::route_max_ctas(M))
+    return fail(CLOVER_ERR_INVALID_ARG, "M=%d: launch of %d CTAs, the workspace holds %d", M, a.n_ctas,
+                plan::route_max_ctas(M));
   a.totals = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kCtrlBytes);
   a.hist = a.totals + a.E;
   return launched(launch_route_op(a, s), "launch route");

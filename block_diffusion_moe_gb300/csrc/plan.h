@@ -58,6 +58,17 @@ struct RouteShape {
   bool cluster;    // all of them one cluster
 };
 
+// Tokens per CTA grow to kRouteCtaTokens once the CTAs reach kRouteFullCtas.
+constexpr int kRouteCtaTokens = 64;
+constexpr int kRouteFullCtas = 304;
+
+// Most CTAs any call of at most this many tokens uses: what a workspace holds.
+inline int route_max_ctas(int tokens) {
+  const int most = (tokens + kRouteWarps - 1) / kRouteWarps;
+  const int full = (tokens + kRouteCtaTokens - 1) / kRouteCtaTokens;
+  return full > kRouteFullCtas ? full : (most < kRouteFullCtas ? most : kRouteFullCtas);
+}
+
 inline RouteShape route_shape(int tokens) {
   RouteShape s;
   s.cta_tokens = kRouteWarps;
@@ -67,7 +78,8 @@ inline RouteShape route_shape(int tokens) {
     while (s.ctas * s.cta_tokens < tokens) s.ctas *= 2;
   } else {
     // one token per warp until that fills two CTAs per SM, then up to 64 per CTA
-    while (s.cta_tokens < 64 && (tokens + s.cta_tokens - 1) / s.cta_tokens > 304) s.cta_tokens *= 2;
+    while (s.cta_tokens < kRouteCtaTokens && (tokens + s.cta_tokens - 1) / s.cta_tokens > kRouteFullCtas)
+      s.cta_tokens *= 2;
     s.ctas = (tokens + s.cta_tokens - 1) / s.cta_tokens;
   }
   return s;

@@ -73,17 +73,19 @@ __device__ __forceinline__ void load_row(const RouteOpArgs& a, int64_t row, int 
   }
 }
 
-// This lane's biases: 0 without any and past E, -inf for NaN. Returns the
-// largest magnitude in the warp (-inf, which makes an expert dead, aside).
+// The biases in shared memory, by the whole CTA: 0 without any and past E, -inf
+// for NaN. Returns the largest magnitude (-inf, which makes an expert dead,
+// aside).
 template <int VPL>
-__device__ __forceinline__ float load_bias(const RouteOpArgs& a, int lane, float (&b)[VPL]) {
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    b[i] = (a.bias != nullptr && lane * VPL + i < a.E) ? a.bias[lane * VPL + i] : 0.f;
-    if (!(b[i] > -INFINITY)) b[i] = -INFINITY;
-    if (b[i] > -INFINITY) m = fmaxf(m, fabsf(b[i]));
+__device__ __forceinline__ float load_bias(const RouteOpArgs& a, float* s_bias) {
+  for (int e = threadIdx.x; e < 32 * VPL; e += kThreads) {
+    const float b = (a.bias != nullptr && e < a.E) ? a.bias[e] : 0.f;
+    s_bias[e] = b > -INFINITY ? b : -INFINITY;
   }
+  __syncthreads();
+  float m = 0.f;
+  for (int e = threadIdx.x & 31; e < 32 * VPL; e += 32)
+    if (s_bias[e] > -INFINITY) m = fmaxf(m, fabsf(s_bias[e]));
   return warp_max_f(m);
 }
 
@@ -292,9 +294,9 @@ __device__ __noinline__ int rank_groups_exact(const RouteOpArgs& a, int64_t row,
   return before;
 }
 
-// What experts are ordered by: -inf for a dead expert and for one in a group
-// that does not stay. x: the logits, -inf where dead. False where the token has
-// no live expert (every lane alike).
+// Turns the token's logits in key (-inf where dead) into what experts are
+// ordered by: -inf for a dead expert and for one in a group that does not stay.
+// False where the token has no live expert (every lane alike).
 //
 // *err bounds the error of a key, and *doubt is set (in every lane) where the
 // ranks on either side of the group border are closer than the errors they can
@@ -306,25 +308,27 @@ __device__ __noinline__ int rank_groups_exact(const RouteOpArgs& a, int64_t row,
 // (2^-20 + 2^-22 max(-x of m, 0)) m. The sum with the bias adds half a unit of
 // the key. Logits used as keys are exact.
 template <int VPL>
-__device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float (&x)[VPL], const float (&bias)[VPL],
-                                           float bias_max, int64_t row, int64_t* smem, int lane, float (&key)[VPL],
-                                           float* err, bool* doubt) {
+__device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float* bias, float bias_max, int64_t row,
+                                           int64_t* smem, int lane, float (&key)[VPL], float* err, bool* doubt) {
   *err = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) key[i] = x[i];
   const bool sums = a.n_groups > 1 && a.group_rank == 2;  // ranks are sums of scores
   if (a.bias != nullptr || sums) {
-    float xm = x[0], xl = x[0];
+    float xm = key[0], xl = key[0];
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) xm = fmaxf(xm, x[i]), xl = fminf(xl, x[i]);
+    for (int i = 1; i < VPL; ++i) xm = fmaxf(xm, key[i]), xl = fminf(xl, key[i]);
     xm = warp_max_fast(xm);
     if (xm == -INFINITY) return false;
+    uint32_t dead = 0;  // bit i: slot i holds no live expert
+    if (__any_sync(kAll, xl == -INFINITY)) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) dead |= (key[i] > -INFINITY ? 0u : 1u) << i;
+    }
     float s_max;
     if (a.softmax) {
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        key[i] = expf(x[i] - xm);
+        key[i] = expf(key[i] - xm);
         sum += key[i];
       }
       s_max = 1.f / warp_sum_f(sum);  // the sum is at least 1
@@ -333,15 +337,17 @@ __device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float (&x
       for (int i = 0; i < VPL; ++i) key[i] *= s_max;
     } else {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = fast_sigmoid(x[i]);
+      for (int i = 0; i < VPL; ++i) key[i] = fast_sigmoid(key[i]);
       s_max = fast_sigmoid(xm);
       *err = s_max * (0x1p-20f + 0x1p-22f * fmaxf(-xm, 0.f));
     }
+    if (a.bias != nullptr) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] += bias[i];
-    if (__any_sync(kAll, xl == -INFINITY)) {
+      for (int i = 0; i < VPL; ++i) key[i] += bias[lane * VPL + i];
+    }
+    if (__any_sync(kAll, dead != 0)) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = x[i] > -INFINITY ? key[i] : -INFINITY;
+      for (int i = 0; i < VPL; ++i) key[i] = (dead >> i) & 1u ? -INFINITY : key[i];
     }
     *err += (s_max + bias_max) * 0x1p-23f + 1e-37f;
   }
@@ -402,9 +408,8 @@ __device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float (&x
       }
     }
   }
-  if (a.bias == nullptr) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = x[i];
+  if (a.bias == nullptr && sums) {
+    load_row<VPL>(a, row, lane, key);
     *err = 0.f;
   }
   if (a.group_shift >= 0) {
@@ -526,11 +531,12 @@ __device__ __forceinline__ bool pick_by_count(const RouteOpArgs& a, int64_t row,
 // expert (-1: none left). Worked out in float; where some comparison is closer
 // than the errors allow, again in double, whose order is the definition's.
 template <int VPL>
-__device__ __forceinline__ int select_token(const RouteOpArgs& a, int64_t row, const float (&x)[VPL],
-                                            const float (&bias)[VPL], float bias_max, int64_t* smem, int lane) {
+__device__ __forceinline__ int select_token(const RouteOpArgs& a, int64_t row, const float* bias, float bias_max,
+                                            int64_t* smem, int lane) {
   float key[VPL], err;
   bool doubt = false;
-  if (!token_keys<VPL>(a, x, bias, bias_max, row, smem, lane, key, &err, &doubt)) return -1;
+  load_row<VPL>(a, row, lane, key);
+  if (!token_keys<VPL>(a, bias, bias_max, row, smem, lane, key, &err, &doubt)) return -1;
   // with inexact keys one more than K, to see the key that just missed
   const int want = err > 0.f ? a.K + 1 : a.K;
   int mine = -1;
@@ -544,24 +550,25 @@ __device__ __forceinline__ int select_token(const RouteOpArgs& a, int64_t row, c
 // are shifted by the largest exponent where that matters, so that renormalised
 // weights keep their ratio where every score is below the smallest float.
 template <int VPL>
-__device__ __forceinline__ float token_weight(const RouteOpArgs& a, const float (&x)[VPL], int64_t row, int id) {
+__device__ __forceinline__ float token_weight(const RouteOpArgs& a, int64_t row, int id, int lane) {
   const bool on = id >= 0;
   const float z = on ? load_logit(a, row, id) : -INFINITY;
   float num, sum = 1.f;
-  if (a.softmax) {
-    float m = z;
-    if (!a.renormalise) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) m = fmaxf(m, x[i]);
-    }
-    m = warp_max_fast(m);
+  if (a.softmax && a.renormalise) {
+    const float m = warp_max_fast(z);
     num = on ? expf(z - m) : 0.f;
-    if (!a.renormalise) {
-      sum = 0.f;
+  } else if (a.softmax) {
+    float x[VPL];
+    load_row<VPL>(a, row, lane, x);
+    float m = x[0];
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) sum += x[i] > -INFINITY ? expf(x[i] - m) : 0.f;
-      sum = warp_sum_f(sum);
-    }
+    for (int i = 1; i < VPL; ++i) m = fmaxf(m, x[i]);
+    m = warp_max_fast(m);
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) sum += x[i] > -INFINITY ? expf(x[i] - m) : 0.f;
+    sum = warp_sum_f(sum);
+    num = on ? expf(z - m) : 0.f;
   } else {
     float t = fminf(z, 0.f);
     if (a.renormalise && __any_sync(kAll, on && t < -60.f)) t -= warp_max_fast(on ? t : -INFINITY);
@@ -648,14 +655,12 @@ __global__ void __launch_bounds__(kThreads, VPL <= 8 ? 4 : 2) k_select(const Rou
   pdl_wait();
   pdl_trigger();
   int64_t* keys = reinterpret_cast<int64_t*>(raw + warp * scratch);
-  float bias[VPL];
-  const float bias_max = load_bias<VPL>(a, lane, bias);
+  __shared__ __align__(16) float s_bias[32 * VPL];
+  const float bias_max = load_bias<VPL>(a, s_bias);
   for (int t = warp; t < nt; t += kWarps) {
     const int64_t row = static_cast<int64_t>(t0 + t) * a.ld;
-    float x[VPL];
-    load_row<VPL>(a, row, lane, x);
-    const int id = select_token<VPL>(a, row, x, bias, bias_max, keys, lane);
-    const float w = token_weight<VPL>(a, x, row, id);
+    const int id = select_token<VPL>(a, row, s_bias, bias_max, keys, lane);
+    const float w = token_weight<VPL>(a, row, id, lane);
     if (lane < a.K) {
       const int64_t o = static_cast<int64_t>(t0 + t) * a.K + lane;
       a.idx[o] = id;

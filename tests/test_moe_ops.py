@@ -256,7 +256,7 @@ using namespace clover::plan;
 int main() {
   for (int t = 1; t <= 200000; t += t < 2000 ? 1 : 997) {
     const RouteShape s = route_shape(t);
-    printf("%d %d %d %d\n", t, s.cta_tokens, s.ctas, s.cluster ? 1 : 0);
+    printf("%d %d %d %d %d\n", t, s.cta_tokens, s.ctas, s.cluster ? 1 : 0, route_max_ctas(t));
   }
   return 0;
 }
@@ -275,7 +275,12 @@ def test_route_shapes(tmp_path):
     (tmp_path / "p.cpp").write_text(PLAN)
     subprocess.run([cxx, "-std=c++17", "-I", B.CSRC, str(tmp_path / "p.cpp"), "-o", str(tmp_path / "p")], check=True)
     out = subprocess.run([str(tmp_path / "p")], check=True, capture_output=True, text=True, cwd=os.fspath(tmp_path)).stdout
+    held = 0
     for line in out.splitlines():
-        tokens, per, ctas, cluster = map(int, line.split())
+        tokens, per, ctas, cluster, most = map(int, line.split())
         assert per * ctas >= tokens and per <= 64 and per % 8 == 0 and 64 % per == 0, line
         assert ctas in (1, 2, 4, 8) if cluster else (ctas - 1) * per < tokens, line
+        # a workspace holds the counts of every call of its tokens or fewer
+        assert cluster or ctas <= most, line
+        assert most >= held, line
+        held = most
