@@ -65,20 +65,19 @@ __device__ __forceinline__ void store32b(void* p, bool wide, const uint32_t (&w)
 }
 
 // The row of the scale tiles that belongs to row i, by one warp. False for a
-// grouped row behind the last group.
+// grouped row in no group: behind the last one, or in none by offsets that do
+// not ascend.
 __device__ __forceinline__ bool scale_row(const Fp4QuantArgs& a, int64_t i, int lane, int64_t* r) {
   if (a.offsets == nullptr) {
     const int64_t m = i / a.mat_rows;
     *r = m * ((a.mat_rows + 127) / 128 * 128) + (i - m * a.mat_rows);
     return true;
   }
-  // group of row i: the number of groups that end at or before it
-  int below = 0;
-  for (int g = lane; g < a.n_groups; g += 32) below += a.offsets[g + 1] <= i ? 1 : 0;
-  const int g = __reduce_add_sync(0xffffffffu, below);
-  if (g >= a.n_groups) return false;
-  const int off = group_offset(a.offsets, g, static_cast<int>(a.n_rows));
-  if (off > i) return false;  // offsets that do not ascend
+  const int row = static_cast<int>(i);
+  const int g = warp_search(a.n_groups, row, [&](int j) { return a.offsets[j]; });
+  const int n = static_cast<int>(a.n_rows);
+  const int off = group_offset(a.offsets, g, n);
+  if (off > row || row >= group_offset(a.offsets, g + 1, n)) return false;
   *r = (off / 128 + static_cast<int64_t>(g)) * 128 + (i - off);
   return true;
 }
@@ -120,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) k_quantize_fp4(const Fp4QuantArgs a)
   if (!scale_row(a, i, lane, &sr)) return;
   int64_t src = i;
   if (a.offsets != nullptr) {
-    if (a.src_rows != nullptr) src = a.src_rows[i] < 0 ? -1 : a.src_rows[i] / a.src_div;
+    if (a.src_rows != nullptr) src = a.src_rows[i] < 0 ? -1 : (a.src_shift >= 0 ? a.src_rows[i] >> a.src_shift : a.src_rows[i] / a.src_div);
     if (src >= a.n_src) src = -1;
   }
   const uint8_t* row = static_cast<const uint8_t*>(a.x) + src * a.ldx * (kBf16 ? 2 : 4);
@@ -225,6 +224,9 @@ dim3 row_grid(const Fp4QuantArgs& a) { return dim3(static_cast<unsigned>((a.n_ro
 
 cudaError_t launch_quantize_fp4(const Fp4QuantArgs& args, bool mx, cudaStream_t s) {
   Fp4QuantArgs a = args;
+  a.src_shift = -1;
+  for (int b = 0; b < 31; ++b)
+    if (a.src_div == 1 << b) a.src_shift = b;
   a.wide = reinterpret_cast<uintptr_t>(a.x) % 32 == 0 && a.ldx * (a.bf16_x ? 2 : 4) % 32 == 0;
   void (*k)(const Fp4QuantArgs);
   if (a.mul == 1.f)

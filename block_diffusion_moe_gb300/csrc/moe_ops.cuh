@@ -66,6 +66,7 @@ struct Fp4QuantArgs {
   float mul;                // 2^-scale_exp (quantise), 2^scale_exp (dequantise)
   const int32_t* src_rows;  // grouped: source row of row i is src_rows[i] / src_div (null: i)
   int src_div;
+  int src_shift;            // set by the launch: log2 of src_div, or -1
   int n_src;
   const int32_t* offsets;   // [n_groups + 1] or null
   int n_groups;

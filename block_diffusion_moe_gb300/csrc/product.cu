@@ -92,14 +92,7 @@ __device__ __forceinline__ Tile tile_at(const Fp4ProductArgs& p, const Shared& s
                                         int rank) {
   const int m = t <= 0x7fffffff ? static_cast<int>(static_cast<uint32_t>(t) / static_cast<uint32_t>(n_tiles))
                                 : static_cast<int>(t / n_tiles);
-  // the last group with mt[g] <= m: among every per-th group, then among the
-  // per from there
-  const int lane = threadIdx.x & 31;
-  const int per = (p.n_groups + 31) / 32;
-  const int a = lane * per;
-  int lo = (31 - __clz(__ballot_sync(0xffffffffu, a < p.n_groups && sh.mt[a] <= m))) * per;
-  const int b = lo + lane;
-  lo += 31 - __clz(__ballot_sync(0xffffffffu, lane < per && b < p.n_groups && sh.mt[b] <= m));
+  const int lo = warp_search(p.n_groups, m, [&](int g) { return sh.mt[g]; });
   Tile r;
   r.g = lo;
   const int i = kPair ? 2 * (m - sh.mt[lo]) + rank : m - sh.mt[lo];
