@@ -719,18 +719,28 @@ __global__ void __launch_bounds__(kThreads) k_scan_hist(const RouteOpArgs a) {
   const int e = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (e >= a.E) return;
   int32_t* h = a.hist + static_cast<int64_t>(e) * a.n_ctas;
+  constexpr int kAhead = 16;  // counts a lane loads before the first is added
   int run = 0;
-  for (int c0 = 0; c0 < a.n_ctas; c0 += 32) {
-    const int c = c0 + lane;
-    const int v = c < a.n_ctas ? h[c] : 0;
-    int incl = v;
+  for (int c0 = 0; c0 < a.n_ctas; c0 += 32 * kAhead) {
+    int v[kAhead];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += n;
+    for (int j = 0; j < kAhead; ++j) {
+      const int c = c0 + 32 * j + lane;
+      v[j] = c < a.n_ctas ? h[c] : 0;
     }
-    if (c < a.n_ctas) h[c] = run + incl - v;
-    run += __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int c = c0 + 32 * j + lane;
+      if (c0 + 32 * j >= a.n_ctas) break;
+      int incl = v[j];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += n;
+      }
+      if (c < a.n_ctas) h[c] = run + incl - v[j];
+      run += __shfl_sync(kAll, incl, 31);
+    }
   }
   if (lane == 0) a.totals[e] = run;
 }
