@@ -17,7 +17,7 @@ constexpr int kRouteOpMaxTopK = 32;
 // Tokens one CTA of the selection kernel takes, at most: one bit each in an
 // expert's 64-bit token mask.
 constexpr int kRouteOpCtaTokens = plan::kRouteCtaTokens;
-static_assert(kRouteOpCtaTokens <= 64 && kRouteOpCtaTokens <= plan::kRoutePlaceTokens, "64-bit token masks");
+static_assert(kRouteOpCtaTokens <= 64, "64-bit token masks");
 
 struct RouteOpArgs {
   const void* logits;  // fp32 or bf16 [M], row t at element t * ld

@@ -50,17 +50,18 @@ inline bool fp4_pairs(int rows, int groups, int k, bool swiglu) {
 // of 9.6.)
 constexpr int kRouteWarps = 8;
 constexpr int kRouteClusterTokens = 64;
-constexpr int kRoutePlaceTokens = 64;
+constexpr int kRouteCtaTokens = 64;  // at most: one bit each in an expert's token mask
+// CTAs that fill the machine (4 on each of 152 SMs). The tokens are spread over
+// that many as evenly as 64 per CTA allow: with fewer and larger ones some SMs
+// hold four and others none, as a launch fills what the one before it frees
+// (32,768 tokens in 512 CTAs of 64: 50 us, in 607 of 54: 45 us).
+constexpr int kRouteFullCtas = 608;
 
 struct RouteShape {
   int cta_tokens;  // tokens per CTA
   int ctas;
   bool cluster;    // all of them one cluster
 };
-
-// Tokens per CTA grow to kRouteCtaTokens once the CTAs reach kRouteFullCtas.
-constexpr int kRouteCtaTokens = 64;
-constexpr int kRouteFullCtas = 304;
 
 // Most CTAs any call of at most this many tokens uses: what a workspace holds.
 inline int route_max_ctas(int tokens) {
@@ -77,9 +78,8 @@ inline RouteShape route_shape(int tokens) {
     s.ctas = 1;
     while (s.ctas * s.cta_tokens < tokens) s.ctas *= 2;
   } else {
-    // one token per warp until that fills two CTAs per SM, then up to 64 per CTA
-    while (s.cta_tokens < kRouteCtaTokens && (tokens + s.cta_tokens - 1) / s.cta_tokens > kRouteFullCtas)
-      s.cta_tokens *= 2;
+    const int even = (tokens + kRouteFullCtas - 1) / kRouteFullCtas;
+    if (even > s.cta_tokens) s.cta_tokens = even < kRouteCtaTokens ? even : kRouteCtaTokens;
     s.ctas = (tokens + s.cta_tokens - 1) / s.cta_tokens;
   }
   return s;

@@ -745,28 +745,28 @@ __global__ void __launch_bounds__(kThreads) k_scan_hist(const RouteOpArgs a) {
   if (lane == 0) a.totals[e] = run;
 }
 
-// Places the slots of kRoutePlaceTokens tokens per CTA, from the scanned counts.
+// Places the slots of the tokens that this CTA had in k_select, from the
+// scanned counts.
 __global__ void __launch_bounds__(kThreads) k_place(const RouteOpArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
   uint32_t* s_mask = reinterpret_cast<uint32_t*>(raw);
   int* s_cnt = reinterpret_cast<int*>(s_mask + 2 * a.E);
   int* s_first = s_cnt + a.E;
   __shared__ int s_tmp[kWarps];
-  const int t0 = blockIdx.x * plan::kRoutePlaceTokens;
-  const int nt = min(plan::kRoutePlaceTokens, a.M - t0);
+  const int t0 = blockIdx.x * a.cta_tokens;
+  const int nt = min(a.cta_tokens, a.M - t0);
   for (int e = threadIdx.x; e < 2 * a.E; e += kThreads) s_mask[e] = 0;
   __syncthreads();
   pdl_wait();
   pdl_trigger();
   const int64_t base = static_cast<int64_t>(t0) * a.K;
-  const int mine = t0 / a.cta_tokens;  // the first of k_select's CTAs that had these tokens
   int before[kPerThread];
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
     const int e = threadIdx.x + j * kThreads;
     before[j] = 0;
     if (e < a.E) {
-      before[j] = a.hist[static_cast<int64_t>(e) * a.n_ctas + mine];
+      before[j] = a.hist[static_cast<int64_t>(e) * a.n_ctas + blockIdx.x];
       s_cnt[e] = a.totals[e];
     }
   }
@@ -804,8 +804,7 @@ cudaError_t launch_route_op(const RouteOpArgs& args, cudaStream_t s) {
   if (e != cudaSuccess || a.offsets == nullptr || a.shape.cluster) return e;
   e = launch_kernel<RouteOpArgs>(k_scan_hist, dim3((a.E + kWarps - 1) / kWarps), dim3(kThreads), 0, s, true, a);
   if (e != cudaSuccess) return e;
-  const dim3 grid((a.M + plan::kRoutePlaceTokens - 1) / plan::kRoutePlaceTokens);
-  return launch_kernel<RouteOpArgs>(k_place, grid, dim3(kThreads), tail, s, true, a);
+  return launch_kernel<RouteOpArgs>(k_place, dim3(a.n_ctas), dim3(kThreads), tail, s, true, a);
 }
 
 // ---------------------------------------------------------------- combine

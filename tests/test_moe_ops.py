@@ -264,8 +264,8 @@ int main() {
 
 
 def test_route_shapes(tmp_path):
-    """Every token has a place, a CTA's tokens fit its 64-bit masks and divide the
-    placing launch's 64, a cluster is of at most 8 CTAs."""
+    """Every token has a place, a CTA's tokens fit its 64-bit masks, a cluster is of at
+    most 8 CTAs, a workspace holds every launch."""
     import os
     import shutil
     import subprocess
@@ -278,7 +278,7 @@ def test_route_shapes(tmp_path):
     held = 0
     for line in out.splitlines():
         tokens, per, ctas, cluster, most = map(int, line.split())
-        assert per * ctas >= tokens and per <= 64 and per % 8 == 0 and 64 % per == 0, line
+        assert per * ctas >= tokens and per <= 64, line
         assert ctas in (1, 2, 4, 8) if cluster else (ctas - 1) * per < tokens, line
         # a workspace holds the counts of every call of its tokens or fewer
         assert cluster or ctas <= most, line
