@@ -391,6 +391,8 @@ def _rows_of(name: str, t):
         _refuse(f"{name}: need a 2-D fp32 or bf16 tensor with contiguous rows, got {t.dtype} {tuple(t.shape)}, "
                 f"strides {strides}")
     rows, cols = t.shape
+    if rows > 1 << 29 or cols > 1 << 29:  # (past 32 bits a count would wrap on its way to the library)
+        raise CloverError(ERR_UNSUPPORTED_SHAPE, f"{name}: {tuple(t.shape)} is past 2^29 rows or columns")
     return dev, t.data_ptr(), kind, (strides[0] if rows > 1 else max(strides[0], cols))
 
 
@@ -403,8 +405,10 @@ def make_routing(n_experts: int, top_k: int, score: str = "softmax", n_groups: i
     """The selection rule of `route`. top_groups defaults to every group."""
     if score not in _SCORES:
         _refuse(f"score {score!r} is neither 'softmax' nor 'sigmoid'")
-    return Routing(n_experts, top_k, _SCORES[score], n_groups, n_groups if top_groups is None else top_groups,
-                   group_rank, int(bool(renormalise)), scale)
+    top_groups = n_groups if top_groups is None else top_groups
+    if any(not -(1 << 31) <= v < 1 << 31 for v in (n_experts, top_k, n_groups, top_groups, group_rank)):
+        _refuse("a count past 32 bits")
+    return Routing(n_experts, top_k, _SCORES[score], n_groups, top_groups, group_rank, int(bool(renormalise)), scale)
 
 
 def route_workspace_bytes(r: Routing, max_tokens: int) -> int:
@@ -447,9 +451,10 @@ def route(r: Routing, logits, bias=None, grouping: bool = True, ws=None, out=Non
 class Fp4:
     """Matrices in a microscaled 4-bit format: codes uint8 [rows][cols / 2] or [mats][rows][cols / 2], scale tiles
     uint8 (1-D), and the power of two the values are scaled by. With offsets (int32 [groups + 1]) the rows of one
-    matrix form groups. The parts are checked against one another here, once."""
+    matrix form groups. The parts are checked against one another here, once, and cannot be replaced but for offsets
+    and scale_exp."""
 
-    __slots__ = ("fmt", "codes", "scales", "scale_exp", "_offsets", "device", "mats", "rows", "cols", "groups")
+    __slots__ = ("fmt", "_codes", "_scales", "scale_exp", "_offsets", "device", "mats", "rows", "cols", "groups")
 
     def __init__(self, fmt: int, codes, scales, scale_exp: int = 0, offsets=None):
         if codes.dtype != _U8 or codes.dim() not in (2, 3) or not codes.is_contiguous():
@@ -458,7 +463,7 @@ class Fp4:
         if scales.dtype != torch.uint8 or scales.device != codes.device or not scales.is_contiguous():
             _refuse(f"scales: need contiguous uint8 on {codes.device}, got {scales.dtype} {tuple(scales.shape)} on "
                     f"{scales.device}")
-        self.fmt, self.codes, self.scales, self.scale_exp = fmt, codes, scales, scale_exp
+        self.fmt, self._codes, self._scales, self.scale_exp = fmt, codes, scales, scale_exp
         self.device = codes.device
         self.mats = codes.shape[0] if codes.dim() == 3 else 1
         self.rows, self.cols = codes.shape[-2], 2 * codes.shape[-1]
@@ -468,10 +473,18 @@ class Fp4:
     def _made(cls, fmt, codes, scales, scale_exp, offsets, device, mats, rows, cols):
         """Parts this module has just made to fit."""
         q = object.__new__(cls)
-        q.fmt, q.codes, q.scales, q.scale_exp, q._offsets = fmt, codes, scales, scale_exp, offsets
+        q.fmt, q._codes, q._scales, q.scale_exp, q._offsets = fmt, codes, scales, scale_exp, offsets
         q.device, q.mats, q.rows, q.cols = device, mats, rows, cols
         q.groups = 0 if offsets is None else offsets.shape[0] - 1
         return q
+
+    @property
+    def codes(self):
+        return self._codes
+
+    @property
+    def scales(self):
+        return self._scales
 
     @property
     def offsets(self):
@@ -480,7 +493,7 @@ class Fp4:
     @offsets.setter
     def offsets(self, offsets):
         if offsets is not None:
-            if self.codes.dim() != 2:
+            if self._codes.dim() != 2:
                 _refuse("rows in groups form one matrix")
             if offsets.dim() != 1 or offsets.dtype != torch.int32 or offsets.device != self.device \
                     or not offsets.is_contiguous():
@@ -488,8 +501,8 @@ class Fp4:
                         f"{tuple(offsets.shape)} on {offsets.device}")
         need = fp4_scale_bytes(self.fmt, self.mats, self.rows, self.cols,
                                None if offsets is None else offsets.shape[0] - 1)
-        if self.scales.numel() < need:
-            _refuse(f"scales: {self.scales.numel()} bytes, need {need}")
+        if self._scales.numel() < need:
+            _refuse(f"scales: {self._scales.numel()} bytes, need {need}")
         self._offsets = offsets
         self.groups = 0 if offsets is None else offsets.shape[0] - 1
 
@@ -514,10 +527,12 @@ def quantize_fp4(x, fmt: int = FP4_NV, scale_exp: int = 0, offsets=None, src_row
     if len(shape) == 3:
         if grouped or not x.is_contiguous():
             _refuse("x: matrices must be contiguous, and grouped rows one matrix")
-        dev, p_x, kind, ldx = _rows_of("x", x.view(-1, shape[-1]))
+        dev, p_x, kind, ldx = _rows_of("x", x.flatten(0, 1))
     else:
         dev, p_x, kind, ldx = _rows_of("x", x)
     cols, rows, p_src = shape[-1], shape[-2], None
+    if not (-64 <= scale_exp <= 64 and 1 <= src_div < 1 << 31):
+        _refuse(f"scale_exp={scale_exp} outside [-64, 64], or src_div={src_div} below 1 or past 32 bits")
     if src_rows is not None:
         if not grouped:
             _refuse("src_rows without offsets")
@@ -533,17 +548,17 @@ def quantize_fp4(x, fmt: int = FP4_NV, scale_exp: int = 0, offsets=None, src_row
         n = fp4_scale_bytes(fmt, mats, rows, cols, n_groups)
         out = Fp4._made(fmt, torch.empty(codes_shape, dtype=_U8, device=device),
                         torch.empty(n, dtype=_U8, device=device), scale_exp, offsets, device, mats, rows, cols)
-    elif out.fmt != fmt or out.codes.shape != codes_shape or out.device != x.device:
+    elif out.fmt != fmt or out._codes.shape != codes_shape or out.device != x.device:
         _refuse(f"out holds {tuple(out.codes.shape)} of format {out.fmt} on {out.device}")
     else:
         out.offsets, out.scale_exp = offsets, scale_exp
     if grouped:
         rc = lib().clover_quantize_fp4_rows(fmt, p_x, kind, ldx, shape[0], cols, scale_exp, p_src, src_div, rows, p_off,
-                                            n_groups, out.codes.data_ptr(), out.scales.data_ptr(),
+                                            n_groups, out._codes.data_ptr(), out._scales.data_ptr(),
                                             _raw_stream(stream, dev))
     else:
-        rc = lib().clover_quantize_fp4(fmt, p_x, kind, ldx, out.mats, rows, cols, scale_exp, out.codes.data_ptr(),
-                                       out.scales.data_ptr(), _raw_stream(stream, dev))
+        rc = lib().clover_quantize_fp4(fmt, p_x, kind, ldx, out.mats, rows, cols, scale_exp, out._codes.data_ptr(),
+                                       out._scales.data_ptr(), _raw_stream(stream, dev))
     if rc != OK:
         _check(rc)
     return out
@@ -551,7 +566,7 @@ def quantize_fp4(x, fmt: int = FP4_NV, scale_exp: int = 0, offsets=None, src_row
 
 def dequantize_fp4(q: Fp4, out=None, stream=None):
     """The bf16 matrices the codes stand for (rows behind the last group left as they were)."""
-    codes, off = q.codes, q._offsets
+    codes, off = q._codes, q._offsets
     dev = _on_current("q", codes)
     shape = codes.shape[:-1] + (q.cols,)
     if out is None:
@@ -559,7 +574,7 @@ def dequantize_fp4(q: Fp4, out=None, stream=None):
         p_out = out.data_ptr()
     else:
         p_out = _tensor("out", out, _BF16, shape, dev)
-    rc = lib().clover_dequantize_fp4(q.fmt, codes.data_ptr(), q.scales.data_ptr(), q.mats, q.rows, q.cols, q.scale_exp,
+    rc = lib().clover_dequantize_fp4(q.fmt, codes.data_ptr(), q._scales.data_ptr(), q.mats, q.rows, q.cols, q.scale_exp,
                                      None if off is None else off.data_ptr(), q.groups, p_out, _raw_stream(stream, dev))
     if rc != OK:
         _check(rc)
@@ -576,7 +591,7 @@ def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_
     [rows][N], or with swiglu silu(gate) * up, [rows][N / 2]. b holds one [N][cols] matrix per group, or with swiglu two
     of N / 2 rows (gate, up). The result is scaled by alpha, group_alpha (fp32 [groups]) and both operands' scale_exp;
     rows behind the last group are left as they were."""
-    codes, off, per = a.codes, a._offsets, 2 if swiglu else 1
+    codes, off, per = a._codes, a._offsets, 2 if swiglu else 1
     dev = _on_current("a", codes)
     if codes.dim() != 2 or b._offsets is not None:
         _refuse("a must be one matrix, and only its rows may form groups")
@@ -595,8 +610,8 @@ def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_
     else:
         p_out = _tensor("out", out, _BF16, (rows, width), dev)
     p_alpha = None if group_alpha is None else _tensor("group_alpha", group_alpha, _F32, (groups,), dev)
-    rc = lib().clover_fp4_product(a.fmt, codes.data_ptr(), a.scales.data_ptr(), rows, b.codes.data_ptr(),
-                                  b.scales.data_ptr(), None if off is None else off.data_ptr(), groups, width * per,
+    rc = lib().clover_fp4_product(a.fmt, codes.data_ptr(), a._scales.data_ptr(), rows, b._codes.data_ptr(),
+                                  b._scales.data_ptr(), None if off is None else off.data_ptr(), groups, width * per,
                                   a.cols, alpha * 2.0 ** (a.scale_exp + b.scale_exp), p_alpha, int(swiglu), p_out,
                                   ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
     if rc != OK:
@@ -607,8 +622,8 @@ def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_
 def moe_combine(y, pos, w, x=None, shared=None, out=None, stream=None):
     """x + sum_k w[:, k] * y[pos[:, k]] + shared, fp32 [M][H]: y bf16 [rows][H], pos int32 and w fp32 [M][K] as `route`
     gives them, x fp32 and shared bf16 [M][H] or None. out may be x itself."""
-    if y.dim() != 2 or pos.dim() != 2:
-        _refuse(f"y and pos must be matrices, got {tuple(y.shape)} and {tuple(pos.shape)}")
+    if y.dim() != 2 or pos.dim() != 2 or max(y.shape + pos.shape) > 1 << 29:
+        _refuse(f"y and pos must be matrices of at most 2^29 rows, got {tuple(y.shape)} and {tuple(pos.shape)}")
     dev = _on_current("y", y)
     slots, y_shape = pos.shape, y.shape
     (M, K), (n, H) = slots, y_shape

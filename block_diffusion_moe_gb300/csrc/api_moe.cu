@@ -289,6 +289,7 @@ int clover_fp4_product(int32_t format, const uint8_t* a_codes, const uint8_t* a_
   const bool swiglu = epilogue == CLOVER_FP4_SWIGLU;
   if (N < 1 || N > (1 << 24) || (swiglu && N % 2 != 0))
     return fail(CLOVER_ERR_UNSUPPORTED_SHAPE, "N=%d: must be 1 to 2^24, even with SwiGLU", N);
+  if (!isfinite(alpha)) return fail(CLOVER_ERR_INVALID_ARG, "alpha is not finite");
   if (offsets == nullptr && n_groups != 1)
     return fail(CLOVER_ERR_INVALID_ARG, "offsets is NULL with n_groups=%d", n_groups);
   if ((rc = check_workspace(workspace, workspace_bytes, kCtrlBytes))) return rc;

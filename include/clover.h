@@ -383,8 +383,8 @@ size_t clover_fp4_grouped_scale_bytes(int32_t format, int32_t n_rows, int32_t n_
  *   NV: s = e4m3(amax / 6), round to nearest even, at most 448
  *   MX: s = 2^(floor(log2 amax) - 2), exponent at least -127 (amax = 0: -127)
  * and each code is the e2m1 value nearest to y / s (ties to the even code, at
- * most 6; 0 where s = 0); it stands for code * s * 2^scale_exp. A block that
- * holds a NaN or an infinity gets the scale NaN and codes 0. Scale bytes of
+ * most 6; 0 where s = 0); it stands for code * s * 2^scale_exp. A block whose
+ * y hold a NaN or an infinity gets the scale NaN and codes 0. Scale bytes of
  * padding are not written. codes and scales 16-byte aligned. */
 int clover_quantize_fp4(int32_t format, const void* x, int32_t x_type, int64_t ldx, int32_t n_mats,
                         int32_t rows, int32_t cols, int32_t scale_exp, uint8_t* codes, uint8_t* scales,
@@ -419,7 +419,7 @@ size_t clover_fp4_product_workspace_bytes(void);
 
 /* Products of rows with the matrix of their group, both in a microscaled
  * 4-bit format, on the tensor cores (fp32 accumulation):
- *   z_i = alpha * group_alpha[g] * (A_i . B_g^T) for row i of group g
+ *   z_i = alpha * group_alpha[g] * (A_i . B_g^T) for row i of group g (alpha finite)
  *   CLOVER_FP4_PLAIN:  y_i = bf16(z_i)                         [N]
  *   CLOVER_FP4_SWIGLU: y_i = bf16(silu(z_i[0..N/2)) * z_i[N/2..N))  [N / 2]
  * a_codes [n_rows][K / 2] with a_scales as clover_quantize_fp4_rows writes

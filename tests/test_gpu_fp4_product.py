@@ -172,12 +172,24 @@ def test_empty_and_refused():
            lambda: C.fp4_product(a, b, swiglu=True), lambda: C.fp4_product(b, b), lambda: C.fp4_product(a, a),
            lambda: C.fp4_product(a, b, out=torch.empty(30, 64, device=DEV)),
            lambda: C.fp4_product(a, b, group_alpha=torch.ones(3, device=DEV)),
+           lambda: C.fp4_product(a, b, alpha=float("inf")), lambda: C.fp4_product(a, b, alpha=2.0 ** 128),
            lambda: C.fp4_product(a, C.Fp4(b.fmt, b.codes, b.scales[:-1])),
            lambda: C.fp4_product(a, C.Fp4(b.fmt, b.codes.cpu(), b.scales.cpu()))]
     for i, f in enumerate(bad):
         with pytest.raises(C.CloverError):
             f()
             pytest.fail(f"call {i} was accepted")
+
+
+def test_results_past_2_31_elements():
+    """Result rows that begin past 2^31 elements are those of the same rows alone."""
+    rows, N, K = 270000, 8192, 64
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn(rows, K, generator=g, device=DEV).bfloat16()
+    b = C.quantize_fp4(torch.randn(N, K, generator=g, device=DEV).bfloat16(), C.FP4_MX)
+    y = C.fp4_product(C.quantize_fp4(x, C.FP4_MX), b)
+    for part in (slice(0, 200), slice(rows - 200, rows)):
+        assert torch.equal(y[part], C.fp4_product(C.quantize_fp4(x[part].contiguous(), C.FP4_MX), b))
 
 
 def test_many_row_tiles_and_column_tiles():

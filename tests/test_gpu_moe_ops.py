@@ -114,6 +114,17 @@ def test_route_no_expert_left():
     _check_route(torch.full((200, 40), -inf, device=DEV), dict(top_k=4))
 
 
+def test_route_infinite_biases():
+    z = torch.randn(20, 96, generator=_gen(12))
+    b = 0.1 * torch.randn(96, generator=_gen(13))
+    b[5], b[60], b[7] = float("inf"), float("inf"), -float("inf")
+    for score in ("softmax", "sigmoid"):
+        _check_route(z.to(DEV), dict(top_k=4, score=score), bias=b.to(DEV))
+        _check_route(z.to(DEV), dict(top_k=4, score=score, n_groups=6, top_groups=2, group_rank=2), bias=b.to(DEV))
+        _check_route(z[:, :24].contiguous().to(DEV), dict(top_k=4, score=score, n_groups=3, top_groups=1, group_rank=1),
+                     bias=b[:24].contiguous().to(DEV))
+
+
 def test_route_keys_closer_than_fp32():
     """Keys that differ by about 1e-9: their order is that of the exact sums, which fp32 cannot tell."""
     rng = np.random.default_rng(5)
@@ -296,6 +307,25 @@ def test_quantize_strided_rows():
         assert torch.equal(a.codes, b.codes) and torch.equal(C.dequantize_fp4(a), C.dequantize_fp4(b))
 
 
+def test_quantize_and_combine_past_2_31_elements():
+    """Rows that begin past 2^31 elements and bytes are those of the same rows alone."""
+    rows, cols = 263000, 8192
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV)
+    x[:64].normal_(generator=torch.Generator(device=DEV).manual_seed(1))
+    x[64:-64] = 0
+    x[-64:].normal_(generator=torch.Generator(device=DEV).manual_seed(2))
+    q = C.quantize_fp4(x, C.FP4_NV)
+    back = C.dequantize_fp4(q)
+    for part in (slice(0, 64), slice(rows - 64, rows)):
+        assert torch.equal(back[part], C.dequantize_fp4(C.quantize_fp4(x[part], C.FP4_NV)))
+    del back, q
+    pos = torch.tensor([[rows - 1, 3], [0, rows - 2]], dtype=torch.int32, device=DEV)
+    w = torch.tensor([[1.0, 2.0], [0.5, -1.0]], device=DEV)
+    near = torch.cat([x[:4], x[-2:]])
+    small = torch.tensor([[5, 3], [0, 4]], dtype=torch.int32, device=DEV)
+    assert torch.equal(C.moe_combine(x, pos, w), C.moe_combine(near, small, w))
+
+
 # -------------------------------------------------------------------- combine
 
 
@@ -389,7 +419,9 @@ def test_wrappers_refuse():
         lambda: C.route(r, z, bias=torch.zeros(63, device=DEV)), lambda: C.route(r, z, bias=torch.zeros(64)),
         lambda: C.route(r, z, ws=torch.zeros(256, dtype=torch.uint8, device=DEV)),
         lambda: C.route(r, z, out=C.route(r, z[:4])), lambda: C.quantize_fp4(z.half()), lambda: C.quantize_fp4(z[:, :48]),
-        lambda: C.quantize_fp4(z, 7), lambda: C.quantize_fp4(z, src_rows=pos[0]), lambda: C.quantize_fp4(z.cpu()),
+        lambda: C.quantize_fp4(z, 7), lambda: C.quantize_fp4(z, scale_exp=1 << 32),
+        lambda: C.quantize_fp4(z, offsets=off, src_rows=pos[0], src_div=(1 << 32) + 1),
+        lambda: C.quantize_fp4(z, src_rows=pos[0]), lambda: C.quantize_fp4(z.cpu()),
         lambda: C.quantize_fp4(z.expand(2, 8, 64)), lambda: C.quantize_fp4(z, offsets=off.long()),
         lambda: C.quantize_fp4(z, offsets=off, src_rows=pos[0].long()), lambda: C.quantize_fp4(z, out=C.quantize_fp4(z[:4])),
         lambda: C.dequantize_fp4(C.Fp4(0, torch.zeros(8, 32, device=DEV), torch.zeros(512, dtype=torch.uint8, device=DEV))),

@@ -158,8 +158,41 @@ def test_combine_nothing_to_do(lib):
 
 def test_wrappers_refuse_host_tensors(lib):
     r = C.make_routing(8, 2)
-    with pytest.raises((C.CloverError, RuntimeError, AssertionError)):
-        C.route(r, torch.zeros(4, 8))
+    bad = [lambda: C.route(r, torch.zeros(4, 8)), lambda: C.quantize_fp4(torch.zeros(4, 64)),
+           lambda: C.moe_combine(torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(2, 2, dtype=torch.int32),
+                                 torch.zeros(2, 2))]
+    q = C.Fp4(C.FP4_NV, torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8))
+    bad += [lambda: C.dequantize_fp4(q), lambda: C.fp4_product(q, q)]
+    for f in bad:
+        with pytest.raises(C.CloverError):
+            f()
+
+
+def test_fp4_parts_are_checked_and_kept(lib):
+    codes, scales = torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8)
+    q = C.Fp4(C.FP4_NV, codes, scales)
+    assert (q.mats, q.rows, q.cols, q.groups) == (1, 4, 64, 0)
+    with pytest.raises(AttributeError):
+        q.scales = scales[:1]
+    with pytest.raises(AttributeError):
+        q.codes = codes[:1]
+    for off in (torch.zeros(3, dtype=torch.int32), torch.zeros(3), torch.zeros(1, 3, dtype=torch.int32)):
+        with pytest.raises(C.CloverError):
+            q.offsets = off  # two groups need two row tiles of scales; another type; another shape
+    q.offsets = torch.zeros(2, dtype=torch.int32)
+    assert q.groups == 1
+    for bad in (lambda: C.Fp4(C.FP4_NV, codes, scales[:511]), lambda: C.Fp4(C.FP4_NV, codes.float(), scales),
+                lambda: C.Fp4(C.FP4_NV, codes[:, ::2], scales), lambda: C.Fp4(2, codes, scales),
+                lambda: C.Fp4(C.FP4_NV, codes[None], scales, offsets=torch.zeros(2, dtype=torch.int32))):
+        with pytest.raises(C.CloverError):
+            bad()
+
+
+def test_counts_past_32_bits_refused():
+    for kw in (dict(n_experts=(1 << 32) + 8, top_k=2), dict(n_experts=8, top_k=(1 << 32) + 2),
+               dict(n_experts=8, top_k=2, n_groups=1 << 40)):
+        with pytest.raises(C.CloverError):
+            C.make_routing(**kw)
 
 
 # ----------------------------------------------------------------- oracle pins
@@ -238,6 +271,7 @@ PRODUCT = dict(fmt=0, a=0x10000, sa=0x20000, n_rows=10, b=0x30000, sb=0x40000, o
     (dict(sb=None), C.ERR_INVALID_ARG), (dict(y=None), C.ERR_INVALID_ARG), (dict(y=0x60008), C.ERR_INVALID_ARG),
     (dict(group_alpha=0x70001), C.ERR_INVALID_ARG), (dict(ws=None), C.ERR_INVALID_ARG),
     (dict(ws=0x100010), C.ERR_INVALID_ARG), (dict(nbytes=255), C.ERR_WORKSPACE_TOO_SMALL),
+    (dict(alpha=float("inf")), C.ERR_INVALID_ARG), (dict(alpha=float("nan")), C.ERR_INVALID_ARG),
 ])
 def test_product_arguments_refused(lib, kw, code):
     assert lib.clover_fp4_product(*dict(PRODUCT, **kw).values()) == code
