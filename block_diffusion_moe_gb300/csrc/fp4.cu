@@ -85,8 +85,11 @@ __device__ __forceinline__ bool scale_row(const Fp4QuantArgs& a, int64_t i, int 
 }  // namespace
 
 // One warp per row, one lane per block of columns: a block's values stay in
-// registers between its maximum and its codes, so x is read once. Bound by
-// HBM (2.56 bytes per bf16 element with NV scales).
+// registers between its maximum and its codes, so x is read once. Matrices are
+// bound by HBM (64 x 1,024 x 2,048 bf16 to NV: 52 us, 343 MB at 6.6 TB/s); rows
+// gathered eight times each, which come from L2, by the arithmetic (65,536 rows
+// of 2,048 to MX: 43 us, the ALU pipe two thirds busy). A division per element
+// instead of the products below: 62 us for the matrices.
 //
 // The codes are exact. MX: y / s is exact (s a power of two). NV with fp32
 // input: the correctly rounded quotient lies on the same side of every border
@@ -188,7 +191,8 @@ __global__ void __launch_bounds__(kThreads) k_quantize_fp4(const Fp4QuantArgs a)
   }
 }
 
-// The other way: one warp per row, one lane per 16 columns.
+// The other way: one warp per row, one lane per 16 columns. Bound by HBM (the
+// same sizes: 52 and 54 us, 6.6 TB/s).
 template <bool kMx>
 __global__ void __launch_bounds__(kThreads) k_dequantize_fp4(const Fp4QuantArgs a) {
   pdl_wait();
