@@ -396,6 +396,13 @@ def _rows_of(name: str, t):
     return dev, t.data_ptr(), kind, (strides[0] if rows > 1 else max(strides[0], cols))
 
 
+def _scratch(ws, dev: int):
+    """(pointer, bytes) of a caller's workspace."""
+    if ws.dtype is not _U8 or ws.get_device() != dev or not ws.is_contiguous():
+        _refuse(f"ws: need contiguous uint8 on cuda:{dev}, got {ws.dtype} on {ws.device}, strides {ws.stride()}")
+    return ws.data_ptr(), ws.numel()
+
+
 def _raw_stream(stream, dev: int) -> int:
     return _current_stream(dev) if stream is None else stream.cuda_stream
 
@@ -441,7 +448,7 @@ def route(r: Routing, logits, bias=None, grouping: bool = True, ws=None, out=Non
         p_rows = _tensor("rows", out["rows"], _I32, (M * K,), dev)
         p_pos = _tensor("pos", out["pos"], _I32, slots, dev)
     rc = lib().clover_route(r, p_logits, kind, ld, p_bias, M, _tensor("idx", out["idx"], _I32, slots, dev),
-                            _tensor("w", out["w"], _F32, slots, dev), p_off, p_rows, p_pos, ws.data_ptr(), ws.numel(),
+                            _tensor("w", out["w"], _F32, slots, dev), p_off, p_rows, p_pos, *_scratch(ws, dev),
                             _raw_stream(stream, dev))
     if rc != OK:
         _check(rc)
@@ -613,7 +620,7 @@ def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_
     rc = lib().clover_fp4_product(a.fmt, codes.data_ptr(), a._scales.data_ptr(), rows, b._codes.data_ptr(),
                                   b._scales.data_ptr(), None if off is None else off.data_ptr(), groups, width * per,
                                   a.cols, alpha * 2.0 ** (a.scale_exp + b.scale_exp), p_alpha, int(swiglu), p_out,
-                                  ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+                                  *_scratch(ws, dev), _raw_stream(stream, dev))
     if rc != OK:
         _check(rc)
     return out

@@ -122,7 +122,10 @@ __global__ void __launch_bounds__(kThreads) k_quantize_fp4(const Fp4QuantArgs a)
   if (!scale_row(a, i, lane, &sr)) return;
   int64_t src = i;
   if (a.offsets != nullptr) {
-    if (a.src_rows != nullptr) src = a.src_rows[i] < 0 ? -1 : (a.src_shift >= 0 ? a.src_rows[i] >> a.src_shift : a.src_rows[i] / a.src_div);
+    if (a.src_rows != nullptr) {
+      const int v = a.src_rows[i];
+      src = v < 0 ? -1 : (a.src_shift >= 0 ? v >> a.src_shift : v / a.src_div);
+    }
     if (src >= a.n_src) src = -1;
   }
   const uint8_t* row = static_cast<const uint8_t*>(a.x) + src * a.ldx * (kBf16 ? 2 : 4);

@@ -300,13 +300,13 @@ __device__ __noinline__ int rank_groups_exact(const RouteOpArgs& a, int64_t row,
 //
 // *err bounds the error of a key, and *doubt is set (in every lane) where the
 // ranks on either side of the group border are closer than the errors they can
-// have and are not settled here. With m the largest score: a softmax score is off by less than 2^-19 m
-// (exp and quotient a few roundings each, the sum up to 21). A sigmoid: by its
-// documented bound __expf is off by (2 + 1.18 |x|) 2^-23 of the value, which
-// changes s by (1 - s) s of that; s (1 - s) |x| is below 0.23, and below m |x of
-// m| where all logits are low, so with the quotient's 2^-22 less than
-// (2^-20 + 2^-22 max(-x of m, 0)) m. The sum with the bias adds half a unit of
-// the key. Logits used as keys are exact.
+// have and are not settled here. With m the largest score: a softmax score is
+// off by less than 2^-19 m (exp and quotient a few roundings each, the sum up to
+// 21). A sigmoid: by its documented bound __expf is off by (2 + 1.18 |x|) 2^-23
+// of the value, which changes s by (1 - s) s of that; s (1 - s) |x| is below
+// 0.23, and below m |x of m| where all logits are low, so with the quotient's
+// 2^-22 less than (2^-20 + 2^-22 max(-x of m, 0)) m. The sum with the bias adds
+// half a unit of the key. Logits used as keys are exact.
 template <int VPL>
 __device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float* bias, float bias_max, int64_t row,
                                            int64_t* smem, int lane, float (&key)[VPL], float* err, bool* doubt) {
@@ -798,7 +798,10 @@ cudaError_t launch_route_op(const RouteOpArgs& args, cudaStream_t s) {
   const size_t tail = static_cast<size_t>(4 * a.E + 1) * 4;
   const size_t smem = kWarps * select_scratch(a) + tail;
   const int vpl = a.E <= 64 ? 2 : a.E <= 128 ? 4 : a.E <= 256 ? 8 : 16;
-  void (*k)(const RouteOpArgs) = vpl == 2 ? k_select<2> : vpl == 4 ? k_select<4> : vpl == 8 ? k_select<8> : k_select<16>;
+  void (*k)(const RouteOpArgs) = vpl == 2   ? k_select<2>
+                                 : vpl == 4 ? k_select<4>
+                                 : vpl == 8 ? k_select<8>
+                                            : k_select<16>;
   const int size = a.bf16_logits ? 2 : 4;
   const int part = vpl * size < 16 ? vpl * size : 16;
   a.vec = a.E % vpl == 0 && reinterpret_cast<uintptr_t>(a.logits) % part == 0 && a.ld * size % part == 0;

@@ -172,6 +172,8 @@ def test_empty_and_refused():
            lambda: C.fp4_product(a, b, swiglu=True), lambda: C.fp4_product(b, b), lambda: C.fp4_product(a, a),
            lambda: C.fp4_product(a, b, out=torch.empty(30, 64, device=DEV)),
            lambda: C.fp4_product(a, b, group_alpha=torch.ones(3, device=DEV)),
+           lambda: C.fp4_product(a, b, ws=torch.zeros(256, dtype=torch.uint8)),
+           lambda: C.fp4_product(a, b, ws=torch.zeros(255, dtype=torch.uint8, device=DEV)),
            lambda: C.fp4_product(a, b, alpha=float("inf")), lambda: C.fp4_product(a, b, alpha=2.0 ** 128),
            lambda: C.fp4_product(a, C.Fp4(b.fmt, b.codes, b.scales[:-1])),
            lambda: C.fp4_product(a, C.Fp4(b.fmt, b.codes.cpu(), b.scales.cpu()))]

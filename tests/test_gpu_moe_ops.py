@@ -418,6 +418,8 @@ def test_wrappers_refuse():
         lambda: C.route(r, z.cpu()), lambda: C.route(r, z.half()), lambda: C.route(r, z[:, :32]), lambda: C.route(r, z.t()),
         lambda: C.route(r, z, bias=torch.zeros(63, device=DEV)), lambda: C.route(r, z, bias=torch.zeros(64)),
         lambda: C.route(r, z, ws=torch.zeros(256, dtype=torch.uint8, device=DEV)),
+        lambda: C.route(r, z, ws=torch.zeros(1 << 20, dtype=torch.uint8)),
+        lambda: C.route(r, z, ws=torch.zeros(1 << 20, device=DEV)),
         lambda: C.route(r, z, out=C.route(r, z[:4])), lambda: C.quantize_fp4(z.half()), lambda: C.quantize_fp4(z[:, :48]),
         lambda: C.quantize_fp4(z, 7), lambda: C.quantize_fp4(z, scale_exp=1 << 32),
         lambda: C.quantize_fp4(z, offsets=off, src_rows=pos[0], src_div=(1 << 32) + 1),
