@@ -461,37 +461,43 @@ class Fp4:
     matrix form groups. The parts are checked against one another here, once, and cannot be replaced but for offsets
     and scale_exp."""
 
-    __slots__ = ("fmt", "_codes", "_scales", "scale_exp", "_offsets", "device", "mats", "rows", "cols", "groups")
+    __slots__ = ("fmt", "scale_exp", "device", "mats", "rows", "cols", "groups", "_offsets", "_shape", "_codes",
+                 "_scales", "_at")
 
     def __init__(self, fmt: int, codes, scales, scale_exp: int = 0, offsets=None):
         if codes.dtype != _U8 or codes.dim() not in (2, 3) or not codes.is_contiguous():
             _refuse(f"codes: need contiguous uint8 [rows][cols / 2] or [mats][rows][cols / 2], got {codes.dtype} "
                     f"{tuple(codes.shape)}")
-        if scales.dtype != torch.uint8 or scales.device != codes.device or not scales.is_contiguous():
+        if scales.dtype != _U8 or scales.device != codes.device or not scales.is_contiguous():
             _refuse(f"scales: need contiguous uint8 on {codes.device}, got {scales.dtype} {tuple(scales.shape)} on "
                     f"{scales.device}")
-        self.fmt, self._codes, self._scales, self.scale_exp = fmt, codes, scales, scale_exp
-        self.device = codes.device
+        self.fmt, self.scale_exp, self.device = fmt, scale_exp, codes.device
+        self._shape, self._codes, self._scales, self._at = codes.shape, codes, scales, -1  # two tensors
         self.mats = codes.shape[0] if codes.dim() == 3 else 1
         self.rows, self.cols = codes.shape[-2], 2 * codes.shape[-1]
         self.offsets = offsets
 
     @classmethod
-    def _made(cls, fmt, codes, scales, scale_exp, offsets, device, mats, rows, cols):
-        """Parts this module has just made to fit."""
+    def _new(cls, fmt, shape, scale_bytes, scale_exp, offsets, groups, device, mats, rows, cols):
+        """Room for codes of this shape and as many scales, in one allocation: the codes, then the scales."""
         q = object.__new__(cls)
-        q.fmt, q._codes, q._scales, q.scale_exp, q._offsets = fmt, codes, scales, scale_exp, offsets
-        q.device, q.mats, q.rows, q.cols = device, mats, rows, cols
-        q.groups = 0 if offsets is None else offsets.shape[0] - 1
+        at = (mats * rows * cols // 2 + 127) & -128
+        q._codes = q._scales = torch.empty(at + scale_bytes, dtype=_U8, device=device)
+        q.fmt, q.scale_exp, q._offsets, q._shape, q._at = fmt, scale_exp, offsets, shape, at
+        q.device, q.mats, q.rows, q.cols, q.groups = device, mats, rows, cols, groups
         return q
 
     @property
     def codes(self):
-        return self._codes
+        return self._codes if self._at < 0 else self._codes[:self.mats * self.rows * self.cols // 2].view(self._shape)
 
     @property
     def scales(self):
-        return self._scales
+        return self._scales if self._at < 0 else self._scales[self._at:]
+
+    def _pointers(self):
+        p = self._codes.data_ptr()
+        return p, (self._scales.data_ptr() if self._at < 0 else p + self._at)
 
     @property
     def offsets(self):
@@ -500,18 +506,18 @@ class Fp4:
     @offsets.setter
     def offsets(self, offsets):
         if offsets is not None:
-            if self._codes.dim() != 2:
+            if len(self._shape) != 2:
                 _refuse("rows in groups form one matrix")
             if offsets.dim() != 1 or offsets.dtype != torch.int32 or offsets.device != self.device \
                     or not offsets.is_contiguous():
                 _refuse(f"offsets: need contiguous int32 [groups + 1] on {self.device}, got {offsets.dtype} "
                         f"{tuple(offsets.shape)} on {offsets.device}")
-        need = fp4_scale_bytes(self.fmt, self.mats, self.rows, self.cols,
-                               None if offsets is None else offsets.shape[0] - 1)
-        if self._scales.numel() < need:
-            _refuse(f"scales: {self._scales.numel()} bytes, need {need}")
-        self._offsets = offsets
-        self.groups = 0 if offsets is None else offsets.shape[0] - 1
+        groups = 0 if offsets is None else offsets.shape[0] - 1
+        need = fp4_scale_bytes(self.fmt, self.mats, self.rows, self.cols, None if offsets is None else groups)
+        have = self._scales.numel() - max(self._at, 0)
+        if have < need:
+            _refuse(f"scales: {have} bytes, need {need}")
+        self._offsets, self.groups = offsets, groups
 
 
 def fp4_scale_bytes(fmt: int, n_mats: int, rows: int, cols: int, n_groups: int | None = None) -> int:
@@ -553,19 +559,17 @@ def quantize_fp4(x, fmt: int = FP4_NV, scale_exp: int = 0, offsets=None, src_row
     if out is None:
         mats, device = shape[0] if len(shape) == 3 else 1, x.device
         n = fp4_scale_bytes(fmt, mats, rows, cols, n_groups)
-        out = Fp4._made(fmt, torch.empty(codes_shape, dtype=_U8, device=device),
-                        torch.empty(n, dtype=_U8, device=device), scale_exp, offsets, device, mats, rows, cols)
-    elif out.fmt != fmt or out._codes.shape != codes_shape or out.device != x.device:
-        _refuse(f"out holds {tuple(out.codes.shape)} of format {out.fmt} on {out.device}")
+        out = Fp4._new(fmt, codes_shape, n, scale_exp, offsets, n_groups or 0, device, mats, rows, cols)
+    elif out.fmt != fmt or out._shape != codes_shape or out.device != x.device:
+        _refuse(f"out holds {tuple(out._shape)} of format {out.fmt} on {out.device}")
     else:
         out.offsets, out.scale_exp = offsets, scale_exp
     if grouped:
         rc = lib().clover_quantize_fp4_rows(fmt, p_x, kind, ldx, shape[0], cols, scale_exp, p_src, src_div, rows, p_off,
-                                            n_groups, out._codes.data_ptr(), out._scales.data_ptr(),
-                                            _raw_stream(stream, dev))
+                                            n_groups, *out._pointers(), _raw_stream(stream, dev))
     else:
-        rc = lib().clover_quantize_fp4(fmt, p_x, kind, ldx, out.mats, rows, cols, scale_exp, out._codes.data_ptr(),
-                                       out._scales.data_ptr(), _raw_stream(stream, dev))
+        rc = lib().clover_quantize_fp4(fmt, p_x, kind, ldx, out.mats, rows, cols, scale_exp, *out._pointers(),
+                                       _raw_stream(stream, dev))
     if rc != OK:
         _check(rc)
     return out
@@ -573,15 +577,15 @@ def quantize_fp4(x, fmt: int = FP4_NV, scale_exp: int = 0, offsets=None, src_row
 
 def dequantize_fp4(q: Fp4, out=None, stream=None):
     """The bf16 matrices the codes stand for (rows behind the last group left as they were)."""
-    codes, off = q._codes, q._offsets
-    dev = _on_current("q", codes)
-    shape = codes.shape[:-1] + (q.cols,)
+    off = q._offsets
+    dev = _on_current("q", q._codes)
+    shape = q._shape[:-1] + (q.cols,)
     if out is None:
         out = torch.empty(shape, dtype=_BF16, device=q.device)
         p_out = out.data_ptr()
     else:
         p_out = _tensor("out", out, _BF16, shape, dev)
-    rc = lib().clover_dequantize_fp4(q.fmt, codes.data_ptr(), q._scales.data_ptr(), q.mats, q.rows, q.cols, q.scale_exp,
+    rc = lib().clover_dequantize_fp4(q.fmt, *q._pointers(), q.mats, q.rows, q.cols, q.scale_exp,
                                      None if off is None else off.data_ptr(), q.groups, p_out, _raw_stream(stream, dev))
     if rc != OK:
         _check(rc)
@@ -598,9 +602,9 @@ def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_
     [rows][N], or with swiglu silu(gate) * up, [rows][N / 2]. b holds one [N][cols] matrix per group, or with swiglu two
     of N / 2 rows (gate, up). The result is scaled by alpha, group_alpha (fp32 [groups]) and both operands' scale_exp;
     rows behind the last group are left as they were."""
-    codes, off, per = a._codes, a._offsets, 2 if swiglu else 1
-    dev = _on_current("a", codes)
-    if codes.dim() != 2 or b._offsets is not None:
+    off, per = a._offsets, 2 if swiglu else 1
+    dev = _on_current("a", a._codes)
+    if len(a._shape) != 2 or b._offsets is not None:
         _refuse("a must be one matrix, and only its rows may form groups")
     if a.fmt != b.fmt or a.cols != b.cols or b.device != a.device:
         _refuse(f"a (format {a.fmt}, {a.cols} columns, {a.device}) does not match b (format {b.fmt}, {b.cols} columns, "
@@ -617,9 +621,8 @@ def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_
     else:
         p_out = _tensor("out", out, _BF16, (rows, width), dev)
     p_alpha = None if group_alpha is None else _tensor("group_alpha", group_alpha, _F32, (groups,), dev)
-    rc = lib().clover_fp4_product(a.fmt, codes.data_ptr(), a._scales.data_ptr(), rows, b._codes.data_ptr(),
-                                  b._scales.data_ptr(), None if off is None else off.data_ptr(), groups, width * per,
-                                  a.cols, alpha * 2.0 ** (a.scale_exp + b.scale_exp), p_alpha, int(swiglu), p_out,
+    rc = lib().clover_fp4_product(a.fmt, *a._pointers(), rows, *b._pointers(), None if off is None else off.data_ptr(),
+                                  groups, width * per, a.cols, alpha * 2.0 ** (a.scale_exp + b.scale_exp), p_alpha, int(swiglu), p_out,
                                   *_scratch(ws, dev), _raw_stream(stream, dev))
     if rc != OK:
         _check(rc)

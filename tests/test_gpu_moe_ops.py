@@ -300,6 +300,20 @@ def test_quantize_rows_bad_indices():
     torch.cuda.synchronize()
 
 
+def test_quantized_parts_are_the_whole():
+    """codes and scales as tensors make the same matrix again; an empty one has its shape."""
+    x = torch.randn(3, 70, 192, generator=_gen(21)).to(DEV)
+    q = C.quantize_fp4(x, C.FP4_MX, scale_exp=-3)
+    assert q.codes.shape == (3, 70, 96) and q.scales.numel() == C.fp4_scale_bytes(C.FP4_MX, 3, 70, 192)
+    again = C.Fp4(C.FP4_MX, q.codes.clone(), q.scales.clone(), scale_exp=-3)
+    assert torch.equal(C.dequantize_fp4(again), C.dequantize_fp4(q))
+    e = C.quantize_fp4(x[:, :0].contiguous())
+    assert e.codes.shape == (3, 0, 96) and C.dequantize_fp4(e).shape == (3, 0, 192)
+    off = torch.zeros(3, dtype=torch.int32, device=DEV)
+    e = C.quantize_fp4(x[0, :0], offsets=off)
+    assert e.codes.shape == (0, 96) and e.scales.numel() == C.fp4_scale_bytes(C.FP4_NV, 1, 0, 192, 2)
+
+
 def test_quantize_strided_rows():
     x = torch.randn(40, 256, generator=_gen(1)).bfloat16().to(DEV)
     for v in (x[:, 64:192], x[::3, :128], x[5:6, 128:]):
