@@ -19,7 +19,7 @@ constexpr uint32_t kAll = 0xffffffffu;
 // keys above the bound no longer fit 32 lanes as a rule.
 constexpr int kCountedMax = 17;
 constexpr int kNoGroup = 64;  // rank of a lane that holds no group
-constexpr int kListBytes = 256;  // a warp's list of 32 keys and ids
+constexpr int kListBytes = 512;  // a warp's list of 32 keys and ids, or exact keys and scores
 
 // +inf counts as the largest finite value, NaN as -inf.
 __device__ __forceinline__ float clean_logit(float v) { return v == v ? fminf(v, 3.402823466e+38f) : -INFINITY; }
@@ -142,8 +142,9 @@ __device__ __forceinline__ int list_above(const float (&key)[VPL], float bound, 
 }
 
 // ---- The order in exact arithmetic: in double, as the definition has it. Rare
-// (about one token in a thousand), so compact; what counts is the delay of that
-// token, so the exponentials run four at a time.
+// (about one token in a thousand) and written for few registers: what these
+// functions need is taken from the loop over tokens that calls them (with four
+// exponentials at a time 32,768 tokens took 51 instead of 47 us).
 
 struct SoftmaxSum {
   double max, sum;
@@ -156,45 +157,80 @@ __device__ __noinline__ SoftmaxSum softmax_sum(const RouteOpArgs& a, int64_t row
   r.max = warp_max_f(m);
   r.sum = 0;
 #pragma unroll 1
-  for (int e0 = lane; e0 < a.E; e0 += 128) {
-    double t[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float z = e0 + 32 * j < a.E ? load_logit(a, row, e0 + 32 * j) : -INFINITY;
-      t[j] = exp(static_cast<double>(z) - r.max);
-    }
-    r.sum += (t[0] + t[1]) + (t[2] + t[3]);
-  }
+  for (int e = lane; e < a.E; e += 32) r.sum += exp(static_cast<double>(load_logit(a, row, e)) - r.max);
 #pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) r.sum += __shfl_xor_sync(kAll, r.sum, o);
   return r;
 }
 
-// Score + bias of expert e, -inf where dead.
-__device__ __forceinline__ double exact_total(const RouteOpArgs& a, int64_t row, int e, SoftmaxSum s) {
+// The same with a sum in float, off by less than 2^-19 of it.
+__device__ __noinline__ SoftmaxSum softmax_sum_near(const RouteOpArgs& a, int64_t row, int lane) {
+  float m = -INFINITY, sum = 0.f;
+  for (int e = lane; e < a.E; e += 32) m = fmaxf(m, load_logit(a, row, e));
+  m = warp_max_f(m);
+  for (int e = lane; e < a.E; e += 32) sum += expf(load_logit(a, row, e) - m);
+  SoftmaxSum r;
+  r.max = m;
+  r.sum = warp_sum_f(sum);
+  return r;
+}
+
+// Score + bias of expert e, -inf where dead; the score in *score.
+__device__ __forceinline__ double exact_total(const RouteOpArgs& a, int64_t row, int e, SoftmaxSum s,
+                                              double* score = nullptr) {
   const float z = load_logit(a, row, e);
   const float b = a.bias != nullptr ? a.bias[e] : 0.f;
   if (!(z > -INFINITY && b > -INFINITY)) return -static_cast<double>(INFINITY);
-  const double t = exp(a.softmax ? static_cast<double>(z) - s.max : -static_cast<double>(z));
-  return (a.softmax ? t / s.sum : 1.0 / (1.0 + t)) + static_cast<double>(b);
+  double t = exp(a.softmax ? static_cast<double>(z) - s.max : -static_cast<double>(z));
+  t = a.softmax ? t / s.sum : 1.0 / (1.0 + t);
+  if (score != nullptr) *score = t;
+  return t + static_cast<double>(b);
 }
 
 // Lane k < n holds candidate id; returns the candidate of rank k by exact key,
 // the lower id first on ties.
+//
+// A softmax's sum is what costs (E exponentials in double, 8 us; the candidates'
+// own take 1.5). An error of the sum moves all scores in proportion, so the
+// difference of two keys by as much of the difference of their scores: with the
+// sum in float the order stands unless two neighbours are that close, and only
+// then the sum is worked out in double.
 __device__ __noinline__ int rank_exact(const RouteOpArgs& a, int64_t row, int id, int n, int lane, int64_t* smem) {
-  SoftmaxSum s = {0, 1};
-  if (a.softmax) s = softmax_sum(a, row, lane);
-  const int64_t own = lane < n ? order_int64(exact_total(a, row, id, s)) : INT64_MIN;
-  smem[lane] = own;
-  __syncwarp();
-  int before = 0;
-  for (int j = 0; j < n; ++j) {
-    const int64_t o = smem[j];
-    const int f = __shfl_sync(kAll, id, j);
-    before += (o > own || (o == own && f < id)) ? 1 : 0;
-  }
-  __syncwarp();
+  struct Entry {
+    double key, score;
+  };
+  Entry* sorted = reinterpret_cast<Entry*>(smem);  // [32]
   int32_t* order = reinterpret_cast<int32_t*>(smem);
+  SoftmaxSum s = {0, 1};
+  if (a.softmax) s = softmax_sum_near(a, row, lane);
+  int before;
+#pragma unroll 1
+  for (bool near = a.softmax != 0;; near = false) {
+    double score = 0;
+    const double key = lane < n ? exact_total(a, row, id, s, &score) : 0.0;
+    const int64_t own = order_int64(key);
+    smem[lane] = own;
+    __syncwarp();
+    before = 0;
+    for (int j = 0; j < n; ++j) {
+      const int64_t o = smem[j];
+      const int f = __shfl_sync(kAll, id, j);
+      before += (o > own || (o == own && f < id)) ? 1 : 0;
+    }
+    __syncwarp();
+    if (!near) break;
+    if (lane < n) sorted[before] = Entry{key, score};
+    __syncwarp();
+    bool close = false;
+    if (lane + 1 < n) {
+      const Entry u = sorted[lane], v = sorted[lane + 1];
+      const double apart = fabs(u.score - v.score);
+      close = apart > 0 && !(u.key - v.key > apart * 0x1p-18 + fabs(u.key) * 0x1p-50);
+    }
+    __syncwarp();
+    if (!__any_sync(kAll, close)) break;
+    s = softmax_sum(a, row, lane);
+  }
   if (lane < n) order[before] = id;
   __syncwarp();
   const int r = lane < n ? order[lane] : -1;
@@ -209,14 +245,7 @@ __device__ __noinline__ int select_exact(const RouteOpArgs& a, int64_t row, int 
   SoftmaxSum s = {0, 1};
   if (a.softmax) s = softmax_sum(a, row, lane);
 #pragma unroll 1
-  for (int e0 = lane; e0 < a.E; e0 += 128) {
-    int64_t t[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) t[j] = order_int64(exact_total(a, row, min(e0 + 32 * j, a.E - 1), s));
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (e0 + 32 * j < a.E) smem[e0 + 32 * j] = t[j];
-  }
+  for (int e = lane; e < a.E; e += 32) smem[e] = order_int64(exact_total(a, row, e, s));
   __syncwarp();
   uint32_t mask = kAll;
   if (a.n_groups > 1) {
@@ -520,8 +549,8 @@ __device__ __forceinline__ bool pick_by_count(const RouteOpArgs& a, int64_t row,
     const float k0 = order_float(static_cast<int>(static_cast<uint32_t>(own >> 32) ^ 0x80000000u));
     const float next = __shfl_down_sync(kAll, k0, 1);
     const int next_id = __shfl_down_sync(kAll, id, 1);
-    const bool doubt = lane + 1 < min(n, want) && !(k0 - next > 2.f * err) && !same_key(a, row, id, next_id);
-    if (__any_sync(kAll, doubt)) id = rank_exact(a, row, id, n, lane, smem);
+    const bool close = lane + 1 < min(n, want) && !(k0 - next > 2.f * err) && !same_key(a, row, id, next_id);
+    if (__any_sync(kAll, close)) id = rank_exact(a, row, id, n, lane, smem);
   }
   *mine = id;
   return true;
@@ -643,7 +672,7 @@ __device__ __forceinline__ void scan_counts(const int* s_cnt, int* s_first, int*
 // reads the others' counts in their shared memory); otherwise each CTA leaves
 // its counts per expert to the kernels below.
 template <int VPL>
-__global__ void __launch_bounds__(kThreads, VPL <= 8 ? 4 : 2) k_select(const RouteOpArgs a) {
+__global__ void __launch_bounds__(kThreads, VPL <= 8 ? 4 : 2) k_select(const __grid_constant__ RouteOpArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
   const size_t scratch = select_scratch(a);
   uint32_t* s_mask = reinterpret_cast<uint32_t*>(raw + kWarps * scratch);  // [E][2]

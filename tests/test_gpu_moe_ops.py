@@ -144,6 +144,24 @@ def test_route_keys_closer_than_fp32():
     _check_route(zt, dict(top_k=8, score="sigmoid", n_groups=8, top_groups=4, group_rank=2), bias=bt)
 
 
+def test_route_softmax_keys_closer_than_fp32():
+    """Softmax scores with a bias each, aimed at one sum, the logits rounded and moved by a step: keys some 1e-9 apart,
+    among scores that differ (so that an error of the softmax's sum could turn their order) and a few that do not."""
+    rng = np.random.default_rng(8)
+    M, E = 48, 64
+    z = rng.normal(size=(M, E)).astype(np.float32)
+    z[:, 1::16] = z[:, 0::16]
+    b = np.zeros((M, E), dtype=np.float32)
+    for t in range(M):
+        p = np.exp(z[t].astype(np.float64))
+        p /= p.sum()
+        b[t] = (0.7 - p).astype(np.float32)  # off by up to 3e-8
+        b[t, 1::16] = b[t, 0::16]
+        for k in (dict(top_k=8), dict(top_k=3, n_groups=8, top_groups=2, group_rank=1),
+                  dict(top_k=8, n_groups=4, top_groups=2, group_rank=2)):
+            _check_route(torch.from_numpy(z[t:t + 1]).to(DEV), dict(k, score="softmax"), bias=torch.from_numpy(b[t]).to(DEV))
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_route_strided_rows(dtype):
     z = torch.randn(50, 101, generator=_gen(3)).to(dtype).to(DEV)
