@@ -341,8 +341,9 @@ size_t clover_route_workspace_bytes(const clover_routing* routing, int32_t max_t
  * descending order (ties to the lower id); their weights are s, divided by
  * their sum if renormalise is set, times scale. A token with fewer than
  * top_k such experts (a padding row has none) gets index -1 and weight 0 in
- * the places left over. Comparisons are exact: keys closer than fp32 can
- * tell apart are compared in fp64.
+ * the places left over. Keys and ranks closer than fp32 can tell apart are
+ * compared in fp64 (ranks that are equal but for fp64's rounding, such as the
+ * same two scores and two biases paired otherwise, may order either way).
  * logits: logits_type [M] rows of E, row t at element t * ld (ld >= E),
  * aligned to its element size. bias: fp32 [E] or NULL; it takes part in the
  * selection only. topk_idx int32 [M][K], topk_w fp32 [M][K]: out.
