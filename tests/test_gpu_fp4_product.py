@@ -109,8 +109,18 @@ def test_groups(counts, swiglu, fmt):
 @pytest.mark.parametrize("counts,N,K", [([256], 256, 256), ([512], 512, 64), ([300], 130, 320), ([1000, 0, 3], 520, 448),
                                         ([0, 513, 385, 1], 256, 192), ([700] * 40, 600, 320), ([129, 640], 96, 2048)])
 def test_long_groups(counts, N, K, swiglu, fmt):
-    """256 rows per group and more: tiles of 256 rows on two CTAs, with and without rows in the second half."""
+    """256 rows per group and more, several row tiles per group."""
     _check(*_operands(counts, N, K, fmt, swiglu, sum(counts), extra_rows=1), swiglu=swiglu)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("counts,N,K,swiglu", [([1024], 256, 8192, False), ([1100, 0, 2300], 520, 8192, False),
+                                               ([1, 2400, 1000], 130, 8192, False), ([1150], 512, 4096, True),
+                                               ([3000, 1, 129, 1000], 260, 4288, True), ([1025] * 3, 66, 4160, True)])
+def test_pairs_of_ctas(counts, N, K, swiglu, fmt):
+    """Long groups and a long K: tiles of 256 rows on two CTAs, with and without rows in the second half, and with a K
+    that ends inside a stage."""
+    _check(*_operands(counts, N, K, fmt, swiglu, sum(counts), extra_rows=2), swiglu=swiglu)
 
 
 def test_scale_exponents_and_alpha():
@@ -280,3 +290,32 @@ def test_layer_captured():
             graph.replay()
         side.synchronize()
         assert torch.equal(out, _layer(*args)[2])
+
+
+def test_streams_at_once():
+    """Products (single CTAs and pairs), routing and the framework's own layer kernel on three streams at the same time,
+    each with its own workspace: the results of one after the other."""
+    from block_diffusion_moe_gb300 import synth
+
+    a1, b1, _ = _operands([40, 0, 300, 17], 700, 512, "nv", True, 31)
+    a2, b2, _ = _operands([2100], 512, 8192, "nv", False, 32)  # long group, long K: CTA pairs
+    d = synth.TINY
+    layer, x = synth.make_layer(d, 33, 0, DEV), synth.make_x(d, 8, 34, DEV)
+    z = torch.randn(3000, 256, generator=_gen(35)).to(DEV)
+    r = C.make_routing(256, 8, score="sigmoid", n_groups=8, top_groups=4, group_rank=2)
+    bias = (0.1 * torch.randn(256, generator=_gen(36))).to(DEV)
+    ws = C.workspace(C.moe_workspace_bytes(d, 8))
+    calls = [lambda: C.fp4_product(a1, b1, swiglu=True), lambda: C.fp4_product(a2, b2),
+             lambda: C.route(r, z, bias=bias)["pos"], lambda: C.moe_block_step(d, layer, x, ws=ws, with_topk=False)[0]]
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[] for _ in calls]
+    for _ in range(10):
+        for i, (f, s) in enumerate(zip(calls, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(f())
+    torch.cuda.synchronize()
+    C.workspace_status(ws)
+    for i, w in enumerate(want):
+        assert all(torch.equal(g, w) for g in got[i]), i

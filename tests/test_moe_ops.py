@@ -288,6 +288,9 @@ PLAN = r"""
 #include "plan.h"
 using namespace clover::plan;
 int main() {
+  const int pairs[][4] = {{1024, 1, 8192, 0}, {1023, 1, 8192, 0}, {3402, 3, 8192, 0}, {1150, 1, 4096, 1}, {4132, 4, 4288, 1},
+                          {3075, 3, 4160, 1}, {8192, 1, 4096, 0}, {65536, 256, 8192, 1}};
+  for (auto& p : pairs) printf("pair %d\n", fp4_pairs(p[0], p[1], p[2], p[3] != 0) ? 1 : 0);
   for (int t = 1; t <= 200000; t += t < 2000 ? 1 : 997) {
     const RouteShape s = route_shape(t);
     printf("%d %d %d %d %d\n", t, s.cta_tokens, s.ctas, s.cluster ? 1 : 0, route_max_ctas(t));
@@ -309,8 +312,11 @@ def test_route_shapes(tmp_path):
     (tmp_path / "p.cpp").write_text(PLAN)
     subprocess.run([cxx, "-std=c++17", "-I", B.CSRC, str(tmp_path / "p.cpp"), "-o", str(tmp_path / "p")], check=True)
     out = subprocess.run([str(tmp_path / "p")], check=True, capture_output=True, text=True, cwd=os.fspath(tmp_path)).stdout
+    # the product's rule, at the shapes the tests of its two forms use
+    lines = out.splitlines()
+    assert [x.split()[1] for x in lines if x.startswith("pair")] == ["1", "0", "1", "1", "1", "1", "0", "0"]
     held = 0
-    for line in out.splitlines():
+    for line in [x for x in lines if not x.startswith("pair")]:
         tokens, per, ctas, cluster, most = map(int, line.split())
         assert per * ctas >= tokens and per <= 64, line
         assert ctas in (1, 2, 4, 8) if cluster else (ctas - 1) * per < tokens, line
