@@ -21,8 +21,9 @@ constexpr int kCountedMax = 17;
 constexpr int kNoGroup = 64;  // rank of a lane that holds no group
 constexpr int kListBytes = 512;  // a warp's list of 32 keys and ids, or exact keys and scores
 
-// +inf counts as the largest finite value, NaN as -inf.
-__device__ __forceinline__ float clean_logit(float v) { return v == v ? fminf(v, 3.402823466e+38f) : -INFINITY; }
+// +inf counts as the largest finite value, NaN as -inf (fmaxf takes the operand
+// that is a number).
+__device__ __forceinline__ float clean_logit(float v) { return fminf(fmaxf(v, -INFINITY), 3.402823466e+38f); }
 
 __device__ __forceinline__ float load_logit(const RouteOpArgs& a, int64_t row, int e) {
   const float v = a.bf16_logits ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[row + e])
@@ -107,7 +108,14 @@ __device__ __forceinline__ double order_double(int64_t m) {
   return __longlong_as_double(m ^ ((m >> 63) & 0x7fffffffffffffffLL));
 }
 
-__device__ __forceinline__ float fast_sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+// Error: see token_keys. Values below 2^-126 count as 0 (.ftz; with the steps
+// that keep them 32,768 tokens took 35.2 instead of 34.2 us).
+__device__ __forceinline__ float fast_sigmoid(float v) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
+}
 
 // (b1, b2): the two largest of a set, kept up to date with v
 __device__ __forceinline__ void two_best(float& b1, float& b2, float v) {
@@ -331,11 +339,13 @@ __device__ __noinline__ int rank_groups_exact(const RouteOpArgs& a, int64_t row,
 // ranks on either side of the group border are closer than the errors they can
 // have and are not settled here. With m the largest score: a softmax score is
 // off by less than 2^-19 m (exp and quotient a few roundings each, the sum up to
-// 21). A sigmoid: by its documented bound __expf is off by (2 + 1.18 |x|) 2^-23
-// of the value, which changes s by (1 - s) s of that; s (1 - s) |x| is below
-// 0.23, and below m |x of m| where all logits are low, so with the quotient's
-// 2^-22 less than (2^-20 + 2^-22 max(-x of m, 0)) m. The sum with the bias adds
-// half a unit of the key. Logits used as keys are exact.
+// 21). A sigmoid: exp(-x) is off by (2 + |x|) 2^-23 of its value (2^-22 by the
+// documented bound of ex2.approx, the rest by the rounding of its argument and of
+// log2 e), which changes s by (1 - s) s of that; s (1 - s) |x| is below 0.23, and
+// below m |x of m| where all logits are low, so with the 2^-22 of the sum and the
+// reciprocal less than (2^-20 + 2^-22 max(-x of m, 0)) m. The sum with the bias
+// adds half a unit of the key, and scores that count as 0 less than 1e-37. Logits
+// used as keys are exact.
 template <int VPL>
 __device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float* bias, float bias_max, int64_t row,
                                            int64_t* smem, int lane, float (&key)[VPL], float* err, bool* doubt) {
@@ -662,15 +672,17 @@ __device__ __forceinline__ void scan_counts(const int* s_cnt, int* s_first, int*
 }  // namespace
 
 // Selection: one warp per token, cta_tokens tokens per CTA. Bound by the issue
-// of a token's ~900 instructions and the latency between them (50% of issue slots
+// of a token's ~850 instructions and the latency between them (70% of issue slots
 // busy), not by its logits: 32,768 tokens x 256 experts, sigmoid with bias, 4 of 8
-// groups, 8 experts 37 us (33.6 MB at 0.9 TB/s), softmax alone 21 us; one token
+// groups, 8 experts 34 us (33.6 MB at 1 TB/s), softmax alone 20 us; one token
 // 2.6-3.6 us. A thread per token instead would leave 7 warps per SM at that size.
 // 64 registers and 4 CTAs per SM: 3 or 5 CTAs were slower (60 and 66 against 51
-// us). Where the slots
-// are to be grouped, a call that one cluster takes groups them too (each CTA
-// reads the others' counts in their shared memory); otherwise each CTA leaves
-// its counts per expert to the kernels below.
+// us). Where tokens can be in doubt, which takes several times as long, a CTA's
+// warps take its tokens in common (35.2 us; each its own eighth of them 36.4);
+// where they cannot, that costs more than it gives (softmax alone 21.4 against
+// 20.2). Where the slots are to be grouped, a call that one cluster takes groups
+// them too (each CTA reads the others' counts in their shared memory); otherwise
+// each CTA leaves its counts per expert to the kernels below.
 template <int VPL>
 __global__ void __launch_bounds__(kThreads, VPL <= 8 ? 4 : 2) k_select(const __grid_constant__ RouteOpArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
@@ -683,6 +695,9 @@ __global__ void __launch_bounds__(kThreads, VPL <= 8 ? 4 : 2) k_select(const __g
   const int t0 = blockIdx.x * a.cta_tokens;
   const int nt = min(a.cta_tokens, a.M - t0);  // below 1 in a cluster's last CTAs
   const bool grouping = a.offsets != nullptr;
+  const bool take = nt > kWarps && (a.bias != nullptr || a.n_groups > 1);
+  __shared__ int s_next;  // the next token that no warp has taken
+  if (threadIdx.x == 0) s_next = kWarps;
   if (grouping) {
     for (int e = threadIdx.x; e < 2 * a.E; e += kThreads) s_mask[e] = 0;
     __syncthreads();
@@ -692,7 +707,12 @@ __global__ void __launch_bounds__(kThreads, VPL <= 8 ? 4 : 2) k_select(const __g
   int64_t* keys = reinterpret_cast<int64_t*>(raw + warp * scratch);
   __shared__ __align__(16) float s_bias[32 * VPL];
   const float bias_max = load_bias<VPL>(a, s_bias);
-  for (int t = warp; t < nt; t += kWarps) {
+  for (int t = warp, next; t < nt; t = next) {
+    next = t + kWarps;
+    if (take) {
+      if (lane == 0) next = atomicAdd(&s_next, 1);
+      next = __shfl_sync(kAll, next, 0);
+    }
     const int64_t row = static_cast<int64_t>(t0 + t) * a.ld;
     const int id = select_token<VPL>(a, row, s_bias, bias_max, keys, lane);
     const float w = token_weight<VPL>(a, row, id, lane);
