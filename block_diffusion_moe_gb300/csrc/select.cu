@@ -768,14 +768,17 @@ __global__ void __launch_bounds__(kThreads, VPL <= 8 ? 4 : 2) k_select(const __g
 }
 
 // One warp per expert: the exclusive scan of its counts over the CTAs (607 CTAs
-// x 256 experts: with k_place 9 us, both latency).
+// x 256 experts: with k_place 8 us, both latency).
 __global__ void __launch_bounds__(kThreads) k_scan_hist(const RouteOpArgs a) {
   pdl_wait();
   pdl_trigger();
   const int e = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (e >= a.E) return;
   int32_t* h = a.hist + static_cast<int64_t>(e) * a.n_ctas;
-  constexpr int kAhead = 16;  // counts a lane loads before the first is added
+  // Counts a lane loads before the first is added (all of 640 CTAs), and how many
+  // scans of 32 run side by side (32,768 tokens: one at a time 45.4 us per call, four
+  // 44.1; 257 tokens, which have 33 CTAs, 7.9 and 8.0).
+  constexpr int kAhead = 20, kSide = 4;
   int run = 0;
   for (int c0 = 0; c0 < a.n_ctas; c0 += 32 * kAhead) {
     int v[kAhead];
@@ -785,17 +788,25 @@ __global__ void __launch_bounds__(kThreads) k_scan_hist(const RouteOpArgs a) {
       v[j] = c < a.n_ctas ? h[c] : 0;
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int c = c0 + 32 * j + lane;
-      if (c0 + 32 * j >= a.n_ctas) break;
-      int incl = v[j];
+    for (int j0 = 0; j0 < kAhead; j0 += kSide) {
+      if (c0 + 32 * j0 >= a.n_ctas) break;
+      int incl[kSide];
+#pragma unroll
+      for (int j = 0; j < kSide; ++j) incl[j] = v[j0 + j];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int n = __shfl_up_sync(kAll, incl, o);
-        if (lane >= o) incl += n;
+#pragma unroll
+        for (int j = 0; j < kSide; ++j) {
+          const int n = __shfl_up_sync(kAll, incl[j], o);
+          if (lane >= o) incl[j] += n;
+        }
       }
-      if (c < a.n_ctas) h[c] = run + incl - v[j];
-      run += __shfl_sync(kAll, incl, 31);
+#pragma unroll
+      for (int j = 0; j < kSide; ++j) {
+        const int c = c0 + 32 * (j0 + j) + lane;
+        if (c < a.n_ctas) h[c] = run + incl[j] - v[j0 + j];
+        run += __shfl_sync(kAll, incl[j], 31);
+      }
     }
   }
   if (lane == 0) a.totals[e] = run;
