@@ -672,7 +672,7 @@ __device__ __forceinline__ void scan_counts(const int* s_cnt, int* s_first, int*
 }  // namespace
 
 // Selection: one warp per token, cta_tokens tokens per CTA. Bound by the issue
-// of a token's ~850 instructions and the latency between them (70% of issue slots
+// of a token's ~900 instructions and the latency between them (70% of issue slots
 // busy), not by its logits: 32,768 tokens x 256 experts, sigmoid with bias, 4 of 8
 // groups, 8 experts 34 us (33.6 MB at 1 TB/s), softmax alone 20 us; one token
 // 2.6-3.6 us. A thread per token instead would leave 7 warps per SM at that size.
