@@ -100,6 +100,19 @@ def test_route_ties_and_signed_zeros():
         _check_route(z.to(DEV), dict(top_k=8, score=score, n_groups=8, top_groups=3, group_rank=1), bias=torch.ones(96, device=DEV))
 
 
+@pytest.mark.parametrize("low", [False, True])
+def test_route_scores_around_the_smallest_float(low):
+    """Sigmoids on both sides of 2^-126 (logits of -87.3), or all below it, in more tokens than warps."""
+    z = torch.empty(6000, 96).uniform_(-110.0 if low else -92.0, -88.0 if low else -84.0, generator=_gen(14))
+    z[::7, 3] = 0.5
+    z[1::7, ::2] = 90.0
+    for kw in (dict(n_groups=6, top_groups=2, group_rank=2), dict(n_groups=8, top_groups=4, group_rank=1)):
+        _check_route(z.to(DEV), dict(top_k=8, score="sigmoid", **kw))
+        b = torch.zeros(96)
+        b[10:20] = 1e-38
+        _check_route(z.to(DEV), dict(top_k=8, score="sigmoid", **kw), bias=b.to(DEV))
+
+
 def test_route_no_expert_left():
     inf, nan = float("inf"), float("nan")
     z = torch.tensor([[-inf] * 8, [nan] * 8, [-inf] * 7 + [1.0], [nan, 2.0] * 4, [inf] * 3 + [0.0] * 5,
