@@ -3,6 +3,11 @@
 Argument marshalling only: every step of the denoising path runs in the CUDA
 library. PyTorch supplies device memory and the current stream. There is no
 CPU or PyTorch fallback: if the library is missing, loading fails.
+
+A call with stream= behaves as inside `with torch.cuda.stream(stream)`: what it
+allocates, results included, belongs to that stream. The caller orders its
+inputs before the call, and tells the allocator (Tensor.record_stream) of a
+tensor that is dropped while a stream other than its own still uses it.
 """
 from __future__ import annotations
 
@@ -150,6 +155,15 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _as_current(stream, t):
+    """Makes `stream`, of the device that holds t, the current one for the rest of a call, so that what the call
+    allocates belongs to the stream it runs on: a block of another stream's may still be in use there, is filled there,
+    and goes back to it when the call drops it."""
+    if stream.device != t.device:
+        raise CloverError(ERR_INVALID_ARG, f"the stream is of {stream.device}, the tensors are on {t.device}")
+    return torch.cuda.stream(stream)
+
+
 def make_dims(d: synth.Dims, coreset_top_p: float = 0.0) -> Dims:
     return Dims(d.hidden, d.n_experts, d.top_k, d.d_ff, d.vocab, d.mask_id, d.rms_eps, coreset_top_p)
 
@@ -170,13 +184,16 @@ class Q4Layer:
 def quantize_q4(w, stream=None):
     """bf16 [n_mats][rows][cols] (or [rows][cols]) -> (codes uint8
     [..][rows][cols/2], scales int16 [..][cols/64][rows]) on the device."""
+    if stream is not None:
+        with _as_current(stream, w):
+            return quantize_q4(w)
     assert w.is_cuda and w.dtype == torch.bfloat16 and w.is_contiguous()
     shape = tuple(w.shape)
     w3 = w.view(1, *shape) if w.dim() == 2 else w
     n, rows, cols = w3.shape
     q = torch.empty((n, rows, cols // 2), dtype=torch.uint8, device=w.device)
     sc = torch.empty((n, cols // 64, rows), dtype=torch.int16, device=w.device)
-    _check(lib().clover_quantize_q4(_ptr(w3), n, rows, cols, _ptr(q), _ptr(sc), _stream(stream)))
+    _check(lib().clover_quantize_q4(_ptr(w3), n, rows, cols, _ptr(q), _ptr(sc), _stream()))
     if w.dim() == 2:
         return q[0], sc[0]
     return q, sc
@@ -235,6 +252,9 @@ def denoise_hidden(d: synth.Dims, ws: torch.Tensor, M: int) -> torch.Tensor:
 
 def moe_block_step(d: synth.Dims, layer: synth.Layer, x_in: torch.Tensor, x_out: torch.Tensor | None = None,
                    ws: torch.Tensor | None = None, with_topk: bool = True, stream=None, coreset_top_p: float = 0.0):
+    if stream is not None:
+        with _as_current(stream, x_in):
+            return moe_block_step(d, layer, x_in, x_out, ws, with_topk, coreset_top_p=coreset_top_p)
     M = x_in.shape[0]
     if x_out is None:
         x_out = torch.empty_like(x_in)
@@ -245,7 +265,7 @@ def moe_block_step(d: synth.Dims, layer: synth.Layer, x_in: torch.Tensor, x_out:
     dims = make_dims(d, coreset_top_p)
     lay = make_layer(layer)
     _check(lib().clover_moe_block_step(ctypes.byref(dims), ctypes.byref(lay), _ptr(x_in), _ptr(x_out), _ptr(idx),
-                                       _ptr(w), M, _ptr(ws), ws.numel(), _stream(stream)))
+                                       _ptr(w), M, _ptr(ws), ws.numel(), _stream()))
     return x_out, idx, w
 
 
@@ -254,6 +274,9 @@ def lmhead_unmask(d: synth.Dims, head_w, x, tokens, masked, logit_scale=None, th
     """Head statistics + unmask over M = x.shape[0] positions. `out` (a dict
     this function returned before, for the same M) is reused; the library
     writes every entry, including the committed count."""
+    if stream is not None:
+        with _as_current(stream, x):
+            return lmhead_unmask(d, head_w, x, tokens, masked, logit_scale, threshold, block, ws, out=out)
     M = x.shape[0]
     dev = x.device
     if ws is None:
@@ -268,7 +291,7 @@ def lmhead_unmask(d: synth.Dims, head_w, x, tokens, masked, logit_scale=None, th
     _check(lib().clover_lmhead_unmask(ctypes.byref(dims), _ptr(head_w), _ptr(x), _ptr(logit_scale), threshold, block,
                                       _ptr(tokens), _ptr(masked), _ptr(out["argmax"]), _ptr(out["max_logit"]),
                                       _ptr(out["lse"]), _ptr(out["max_prob"]), _ptr(out["n_committed"]), M,
-                                      _ptr(ws), ws.numel(), _stream(stream)))
+                                      _ptr(ws), ws.numel(), _stream()))
     return out
 
 
@@ -285,6 +308,9 @@ def lmhead_accept(d: synth.Dims, head_w, x, draft, block: int, rule: int = ACCEP
     """Verify-pass head + accept test over M = x.shape[0] rows in blocks of
     `block` rows (block - 1 drafts + the boundary row). `out` (a dict this
     function returned before, for the same M and block) is reused."""
+    if stream is not None:
+        with _as_current(stream, x):
+            return lmhead_accept(d, head_w, x, draft, block, rule, ratio, delta, logit_scale, ws, out=out)
     M = x.shape[0]
     dev = x.device
     if ws is None:
@@ -300,7 +326,7 @@ def lmhead_accept(d: synth.Dims, head_w, x, draft, block: int, rule: int = ACCEP
                                       rule, ratio, delta, block, _ptr(out["argmax"]), _ptr(out["max_logit"]),
                                       _ptr(out["lse"]), _ptr(out["max_prob"]), _ptr(out["entropy"]),
                                       _ptr(out["p_draft"]), _ptr(out["accept_len"]), _ptr(out["tokens"]), M,
-                                      _ptr(ws), ws.numel(), _stream(stream)))
+                                      _ptr(ws), ws.numel(), _stream()))
     return out
 
 
@@ -319,17 +345,23 @@ class Model:
 
 def denoise_step(m: Model, ctx, tokens, masked, logit_scale=None, threshold: float = 0.95, block: int = 32,
                  ws=None, stream=None):
+    if stream is not None:
+        with _as_current(stream, tokens):
+            return denoise_step(m, ctx, tokens, masked, logit_scale, threshold, block, ws)
     M = tokens.shape[0]
     if ws is None:
         ws = workspace(denoise_workspace_bytes(m.d, M), tokens.device)
     _check(lib().clover_denoise_step(ctypes.byref(m.c_dims), m.c_layers, len(m.layers), _ptr(m.embed), _ptr(ctx),
                                      _ptr(m.head_w), _ptr(logit_scale), threshold, block, _ptr(tokens),
-                                     _ptr(masked), M, _ptr(ws), ws.numel(), _stream(stream)))
+                                     _ptr(masked), M, _ptr(ws), ws.numel(), _stream()))
     return ws
 
 
 def denoise_block(m: Model, ctx, tokens, masked, logit_scale=None, threshold: float = 0.95, block: int = 32,
                   max_steps: int = 32, ws=None, stream=None) -> int:
+    if stream is not None:
+        with _as_current(stream, tokens):
+            return denoise_block(m, ctx, tokens, masked, logit_scale, threshold, block, max_steps, ws)
     M = tokens.shape[0]
     if ws is None:
         ws = workspace(denoise_workspace_bytes(m.d, M), tokens.device)
@@ -337,7 +369,7 @@ def denoise_block(m: Model, ctx, tokens, masked, logit_scale=None, threshold: fl
     _check(lib().clover_denoise_block(ctypes.byref(m.c_dims), m.c_layers, len(m.layers), _ptr(m.embed), _ptr(ctx),
                                       _ptr(m.head_w), _ptr(logit_scale), threshold, block, _ptr(tokens),
                                       _ptr(masked), M, max_steps, ctypes.byref(steps), _ptr(ws), ws.numel(),
-                                      _stream(stream)))
+                                      _stream()))
     return steps.value
 
 
@@ -403,10 +435,6 @@ def _scratch(ws, dev: int):
     return ws.data_ptr(), ws.numel()
 
 
-def _raw_stream(stream, dev: int) -> int:
-    return _current_stream(dev) if stream is None else stream.cuda_stream
-
-
 def make_routing(n_experts: int, top_k: int, score: str = "softmax", n_groups: int = 1, top_groups: int | None = None,
                  group_rank: int = 1, renormalise: bool = True, scale: float = 1.0) -> Routing:
     """The selection rule of `route`. top_groups defaults to every group."""
@@ -426,6 +454,9 @@ def route(r: Routing, logits, bias=None, grouping: bool = True, ws=None, out=Non
     """Expert selection from router logits [M][E] (fp32 or bf16, rows may be strided) -> idx int32 [M][K], w fp32
     [M][K] and, with grouping, offsets int32 [E + 1], rows int32 [M * K], pos int32 [M][K]. `out` (a dict this
     function returned before, for the same shape) is reused."""
+    if stream is not None:
+        with _as_current(stream, logits):
+            return route(r, logits, bias, grouping, ws, out)
     dev, p_logits, kind, ld = _rows_of("logits", logits)
     M, cols = logits.shape
     K, E = r.top_k, r.n_experts
@@ -449,7 +480,7 @@ def route(r: Routing, logits, bias=None, grouping: bool = True, ws=None, out=Non
         p_pos = _tensor("pos", out["pos"], _I32, slots, dev)
     rc = lib().clover_route(r, p_logits, kind, ld, p_bias, M, _tensor("idx", out["idx"], _I32, slots, dev),
                             _tensor("w", out["w"], _F32, slots, dev), p_off, p_rows, p_pos, *_scratch(ws, dev),
-                            _raw_stream(stream, dev))
+                            _current_stream(dev))
     if rc != OK:
         _check(rc)
     return out
@@ -536,6 +567,9 @@ def quantize_fp4(x, fmt: int = FP4_NV, scale_exp: int = 0, offsets=None, src_row
     """fp32 or bf16 matrices [rows][cols] or [mats][rows][cols] -> Fp4. With offsets (int32 [groups + 1]) the rows form
     groups: row i comes from x row src_rows[i] // src_div (src_rows int32, default i), as `route` lists them. `out` (an
     Fp4 this function returned before, for the same shapes) is reused."""
+    if stream is not None:
+        with _as_current(stream, x):
+            return quantize_fp4(x, fmt, scale_exp, offsets, src_rows, src_div, out)
     shape, grouped = x.shape, offsets is not None
     if len(shape) == 3:
         if grouped or not x.is_contiguous():
@@ -566,10 +600,10 @@ def quantize_fp4(x, fmt: int = FP4_NV, scale_exp: int = 0, offsets=None, src_row
         out.offsets, out.scale_exp = offsets, scale_exp
     if grouped:
         rc = lib().clover_quantize_fp4_rows(fmt, p_x, kind, ldx, shape[0], cols, scale_exp, p_src, src_div, rows, p_off,
-                                            n_groups, *out._pointers(), _raw_stream(stream, dev))
+                                            n_groups, *out._pointers(), _current_stream(dev))
     else:
         rc = lib().clover_quantize_fp4(fmt, p_x, kind, ldx, out.mats, rows, cols, scale_exp, *out._pointers(),
-                                       _raw_stream(stream, dev))
+                                       _current_stream(dev))
     if rc != OK:
         _check(rc)
     return out
@@ -577,6 +611,9 @@ def quantize_fp4(x, fmt: int = FP4_NV, scale_exp: int = 0, offsets=None, src_row
 
 def dequantize_fp4(q: Fp4, out=None, stream=None):
     """The bf16 matrices the codes stand for (rows behind the last group left as they were)."""
+    if stream is not None:
+        with _as_current(stream, q):
+            return dequantize_fp4(q, out)
     off = q._offsets
     dev = _on_current("q", q._codes)
     shape = q._shape[:-1] + (q.cols,)
@@ -586,7 +623,7 @@ def dequantize_fp4(q: Fp4, out=None, stream=None):
     else:
         p_out = _tensor("out", out, _BF16, shape, dev)
     rc = lib().clover_dequantize_fp4(q.fmt, *q._pointers(), q.mats, q.rows, q.cols, q.scale_exp,
-                                     None if off is None else off.data_ptr(), q.groups, p_out, _raw_stream(stream, dev))
+                                     None if off is None else off.data_ptr(), q.groups, p_out, _current_stream(dev))
     if rc != OK:
         _check(rc)
     return out
@@ -602,6 +639,9 @@ def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_
     [rows][N], or with swiglu silu(gate) * up, [rows][N / 2]. b holds one [N][cols] matrix per group, or with swiglu two
     of N / 2 rows (gate, up). The result is scaled by alpha, group_alpha (fp32 [groups]) and both operands' scale_exp;
     rows behind the last group are left as they were."""
+    if stream is not None:
+        with _as_current(stream, a):
+            return fp4_product(a, b, swiglu, alpha, group_alpha, ws, out)
     off, per = a._offsets, 2 if swiglu else 1
     dev = _on_current("a", a._codes)
     if len(a._shape) != 2 or b._offsets is not None:
@@ -623,7 +663,7 @@ def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_
     p_alpha = None if group_alpha is None else _tensor("group_alpha", group_alpha, _F32, (groups,), dev)
     rc = lib().clover_fp4_product(a.fmt, *a._pointers(), rows, *b._pointers(), None if off is None else off.data_ptr(),
                                   groups, width * per, a.cols, alpha * 2.0 ** (a.scale_exp + b.scale_exp), p_alpha, int(swiglu), p_out,
-                                  *_scratch(ws, dev), _raw_stream(stream, dev))
+                                  *_scratch(ws, dev), _current_stream(dev))
     if rc != OK:
         _check(rc)
     return out
@@ -632,6 +672,9 @@ def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_
 def moe_combine(y, pos, w, x=None, shared=None, out=None, stream=None):
     """x + sum_k w[:, k] * y[pos[:, k]] + shared, fp32 [M][H]: y bf16 [rows][H], pos int32 and w fp32 [M][K] as `route`
     gives them, x fp32 and shared bf16 [M][H] or None. out may be x itself."""
+    if stream is not None:
+        with _as_current(stream, y):
+            return moe_combine(y, pos, w, x, shared, out)
     if y.dim() != 2 or pos.dim() != 2 or max(y.shape + pos.shape) > 1 << 29:
         _refuse(f"y and pos must be matrices of at most 2^29 rows, got {tuple(y.shape)} and {tuple(pos.shape)}")
     dev = _on_current("y", y)
@@ -647,7 +690,7 @@ def moe_combine(y, pos, w, x=None, shared=None, out=None, stream=None):
                                   _tensor("w", w, _F32, slots, dev),
                                   None if shared is None else _tensor("shared", shared, _BF16, full, dev),
                                   None if x is None else _tensor("x", x, _F32, full, dev), p_out, M, K, H,
-                                  _raw_stream(stream, dev))
+                                  _current_stream(dev))
     if rc != OK:
         _check(rc)
     return out

@@ -324,3 +324,85 @@ def test_route_shapes(tmp_path):
         assert cluster or ctas <= most, line
         assert most >= held, line
         held = most
+
+
+# --------------------------------------------------- streams of the binding
+
+
+class _Calls:
+    """Stands in for the library: every launch succeeds, its stream is kept, sizes are ordinary."""
+
+    def __init__(self):
+        self.streams = []
+
+    def __getattr__(self, name):
+        def f(*args):
+            if name.endswith("_bytes"):
+                return 4096
+            self.streams.append(args[-1].value if isinstance(args[-1], ctypes.c_void_p) else args[-1])
+            return C.OK
+        return f
+
+
+def _calls_with_streams():
+    from block_diffusion_moe_gb300 import synth
+    d = synth.TINY
+    x, z, y = torch.zeros(4, 64), torch.zeros(4, 8), torch.zeros(8, 64, dtype=torch.bfloat16)
+    pos, w = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    q = C.Fp4(C.FP4_NV, torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4096, dtype=torch.uint8))
+    r = C.make_routing(8, 2)
+    return [lambda s: C.route(r, z, stream=s), lambda s: C.quantize_fp4(x, stream=s), lambda s: C.dequantize_fp4(q, stream=s),
+            lambda s: C.fp4_product(q, q, stream=s), lambda s: C.moe_combine(y, pos, w, stream=s),
+            lambda s: C.lmhead_unmask(d, y, torch.zeros(4, d.hidden), pos, pos, stream=s),
+            lambda s: C.lmhead_accept(d, y, torch.zeros(4, d.hidden), pos, 2, stream=s)]
+
+
+def test_calls_allocate_on_their_stream(monkeypatch):
+    """What a call with stream= makes (workspaces, results) is made while that stream is current, and the launch goes to
+    it: a block made under another stream is filled, reused and freed in that one's order."""
+    import contextlib
+    import types
+    fake = _Calls()
+    current, made = [111], []
+
+    @contextlib.contextmanager
+    def as_current(s):
+        current.append(s.cuda_stream)
+        yield
+        current.pop()
+
+    def spy(f):
+        def g(*a, **kw):
+            made.append(current[-1])
+            return f(*a, **kw)
+        return g
+
+    side = types.SimpleNamespace(cuda_stream=222, device=torch.device("cpu"))
+    calls = _calls_with_streams()
+    monkeypatch.setattr(C, "lib", lambda: fake)
+    monkeypatch.setattr(C, "_on_current", lambda name, t: -1)  # (host tensors stand in for the device's)
+    monkeypatch.setattr(C, "_current_stream", lambda dev: current[-1])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=current[-1]))
+    monkeypatch.setattr(torch.cuda, "stream", as_current)
+    monkeypatch.setattr(torch, "empty", spy(torch.empty))
+    monkeypatch.setattr(torch, "zeros", spy(torch.zeros))
+    for i, f in enumerate(calls):
+        for s, want in ((side, 222), (None, 111)):
+            made.clear()
+            fake.streams.clear()
+            f(s)
+            assert fake.streams == [want], (i, fake.streams)
+            if i != 5 and i != 6:
+                assert made and all(m == want for m in made), (i, made)
+            else:  # (the call's own inputs are made before it)
+                assert all(m == want for m in made[1:]), (i, made)
+        assert current == [111]
+
+
+def test_streams_of_another_device_refused():
+    import types
+    other = types.SimpleNamespace(cuda_stream=222, device=torch.device("cuda", 1))
+    B.build()
+    for f in _calls_with_streams():
+        with pytest.raises(C.CloverError):
+            f(other)
