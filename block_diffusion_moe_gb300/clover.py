@@ -110,6 +110,7 @@ EXPORTS = {
     "clover_dequantize_fp4": (ctypes.c_int, [_i32, _ptr_t, _ptr_t, _i32, _i32, _i32, _i32, _ptr_t, _i32, _ptr_t,
                                              _ptr_t]),
     "clover_fp4_product_workspace_bytes": (_size, []),
+    "clover_fp4_product_shared_workspace": (ctypes.c_int, [ctypes.POINTER(_ptr_t)]),
     "clover_fp4_product": (ctypes.c_int, [_i32, _ptr_t, _ptr_t, _i32, _ptr_t, _ptr_t, _ptr_t, _i32, _i32, _i32,
                                           ctypes.c_float, _ptr_t, _i32, _ptr_t, _ptr_t, _size, _ptr_t]),
     "clover_moe_combine": (ctypes.c_int, [_ptr_t, _i32, _ptr_t, _ptr_t, _ptr_t, _ptr_t, _ptr_t, _i32, _i32, _i32,
@@ -633,12 +634,28 @@ def fp4_product_workspace_bytes() -> int:
     return lib().clover_fp4_product_workspace_bytes()
 
 
+def _shared_workspace():
+    """(pointer, bytes) of the library's own workspace for products on the current device."""
+    p = ctypes.c_void_p()
+    rc = lib().clover_fp4_product_shared_workspace(ctypes.byref(p))
+    if rc != OK:
+        _check(rc)
+    return p.value, 256
+
+
+def fp4_product_status(stream=None):
+    """Synchronises the stream, then raises CloverError if a wait ran out in an `fp4_product` without ws on the current
+    device since the last look (rows of its result are then missing)."""
+    _check(lib().clover_workspace_status(*_shared_workspace(), _stream(stream)))
+
+
 def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_alpha=None, ws=None, out=None,
                 stream=None):
     """Rows of `a` times the matrix of their group (a.offsets; without offsets one group of all rows): bf16
     [rows][N], or with swiglu silu(gate) * up, [rows][N / 2]. b holds one [N][cols] matrix per group, or with swiglu two
     of N / 2 rows (gate, up). The result is scaled by alpha, group_alpha (fp32 [groups]) and both operands' scale_exp;
-    rows behind the last group are left as they were."""
+    rows behind the last group are left as they were. ws (fp4_product_workspace_bytes(); calls may share it) holds the status
+    that workspace_status reads; without one it is fp4_product_status that does."""
     if stream is not None:
         with _as_current(stream, a):
             return fp4_product(a, b, swiglu, alpha, group_alpha, ws, out)
@@ -653,8 +670,6 @@ def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_
     groups = 1 if off is None else a.groups
     if b.mats != groups * per:
         _refuse(f"b holds {b.mats} matrices for {groups} groups, {per} each")
-    if ws is None:
-        ws = workspace(fp4_product_workspace_bytes(), a.device)
     if out is None:
         out = torch.empty((rows, width), dtype=_BF16, device=a.device)
         p_out = out.data_ptr()
@@ -663,7 +678,7 @@ def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_
     p_alpha = None if group_alpha is None else _tensor("group_alpha", group_alpha, _F32, (groups,), dev)
     rc = lib().clover_fp4_product(a.fmt, *a._pointers(), rows, *b._pointers(), None if off is None else off.data_ptr(),
                                   groups, width * per, a.cols, alpha * 2.0 ** (a.scale_exp + b.scale_exp), p_alpha, int(swiglu), p_out,
-                                  *_scratch(ws, dev), _current_stream(dev))
+                                  *(_shared_workspace() if ws is None else _scratch(ws, dev)), _current_stream(dev))
     if rc != OK:
         _check(rc)
     return out

@@ -278,6 +278,11 @@ int clover_dequantize_fp4(int32_t format, const uint8_t* codes, const uint8_t* s
 
 size_t clover_fp4_product_workspace_bytes(void) { return kCtrlBytes; }
 
+int clover_fp4_product_shared_workspace(void** workspace) {
+  if (workspace == nullptr) return fail(CLOVER_ERR_INVALID_ARG, "workspace is NULL");
+  return launched(fp4_product_shared(workspace), "looking up the shared workspace");
+}
+
 int clover_fp4_product(int32_t format, const uint8_t* a_codes, const uint8_t* a_scales, int32_t n_rows,
                        const uint8_t* b_codes, const uint8_t* b_scales, const int32_t* offsets, int32_t n_groups,
                        int32_t N, int32_t K, float alpha, const float* group_alpha, int32_t epilogue, uint16_t* y,

@@ -99,6 +99,9 @@ struct Fp4ProductArgs {
   int* err;
 };
 
+// The product's workspace in the library (256 bytes on the current device).
+cudaError_t fp4_product_shared(void** p);
+
 cudaError_t launch_fp4_product(const Fp4ProductArgs& a, bool mx, bool swiglu, bool pair, int sms, cudaStream_t s);
 
 }  // namespace clover

@@ -470,6 +470,11 @@ cudaError_t launch(const Fp4ProductArgs& a, bool mx, bool swiglu, int grid, cuda
 
 }  // namespace
 
+// Looked up on every call: the address belongs to the current context.
+static __device__ __align__(256) uint32_t g_fp4_product_ws[64];
+
+cudaError_t fp4_product_shared(void** p) { return cudaGetSymbolAddress(p, g_fp4_product_ws); }
+
 cudaError_t launch_fp4_product(const Fp4ProductArgs& a, bool mx, bool swiglu, bool pair, int sms, cudaStream_t s) {
   return pair ? launch<true>(a, mx, swiglu, sms / 2 * 2, s) : launch<false>(a, mx, swiglu, sms, s);
 }

@@ -418,6 +418,13 @@ int clover_dequantize_fp4(int32_t format, const uint8_t* codes, const uint8_t* s
  * may run at the same time may share it). Host-only. */
 size_t clover_fp4_product_workspace_bytes(void);
 
+/* *workspace receives the device address, on the current device, of a
+ * workspace for clover_fp4_product that lives in the library: 256 bytes, zeroed
+ * when the library is loaded, that calls on any streams may share. For callers
+ * who keep none: clover_workspace_status reads and clears it, and so reports a
+ * wait that ran out in any of them. Enqueues nothing. */
+int clover_fp4_product_shared_workspace(void** workspace);
+
 /* Products of rows with the matrix of their group, both in a microscaled
  * 4-bit format, on the tensor cores (fp32 accumulation):
  *   z_i = alpha * group_alpha[g] * (A_i . B_g^T) for row i of group g (alpha finite)

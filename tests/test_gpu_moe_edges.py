@@ -59,3 +59,33 @@ def test_calls_on_a_stream_that_is_not_the_current_one():
         assert all(torch.equal(g, w) for g, w in zip(got, want))
         assert torch.equal(got_layer, want_layer)
     torch.cuda.synchronize()
+
+
+# -------------------------------------------------------------------- product
+
+
+class _Words:
+    def __init__(self, p):
+        self.__cuda_array_interface__ = dict(shape=(64,), typestr="<i4", data=(p, False), version=2)
+
+
+def test_product_without_workspace_keeps_its_status():
+    """The status of a product without ws can be read afterwards: a set word is reported once and cleared, and a product
+    uses that word (as every product does, on any stream) and leaves it alone."""
+    a = C.quantize_fp4(torch.randn(70, 64, generator=_gen(61)).to(DEV))
+    p, n = C._shared_workspace()
+    assert n == C.fp4_product_workspace_bytes() and p % 256 == 0 and C._shared_workspace() == (p, n)
+    want = C.fp4_product(a, a)
+    C.fp4_product_status()
+    word = torch.as_tensor(_Words(p), device=DEV)
+    assert word.tolist() == [0] * 64
+    word[0] = 1  # what a wait that ran out records
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert torch.equal(C.fp4_product(a, a), want)
+    C.fp4_product(a, a, stream=side)
+    with pytest.raises(C.CloverError) as e:
+        C.fp4_product_status(stream=side)
+    assert e.value.code == C.ERR_DEVICE_TIMEOUT
+    C.fp4_product_status()
+    assert word.tolist() == [0] * 64

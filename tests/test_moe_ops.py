@@ -326,6 +326,10 @@ def test_route_shapes(tmp_path):
         held = most
 
 
+def test_product_shared_workspace_arguments(lib):
+    assert lib.clover_fp4_product_shared_workspace(None) == C.ERR_INVALID_ARG
+
+
 # --------------------------------------------------- streams of the binding
 
 
@@ -339,7 +343,8 @@ class _Calls:
         def f(*args):
             if name.endswith("_bytes"):
                 return 4096
-            self.streams.append(args[-1].value if isinstance(args[-1], ctypes.c_void_p) else args[-1])
+            if not name.endswith("_shared_workspace"):
+                self.streams.append(args[-1].value if isinstance(args[-1], ctypes.c_void_p) else args[-1])
             return C.OK
         return f
 
