@@ -75,19 +75,27 @@ __device__ __forceinline__ void load_row(const RouteOpArgs& a, int64_t row, int 
 }
 
 // The biases in shared memory, by the whole CTA: 0 without any and past E, -inf
-// for NaN. Returns the largest magnitude (-inf, which makes an expert dead,
-// aside).
+// for NaN.
 template <int VPL>
-__device__ __forceinline__ float load_bias(const RouteOpArgs& a, float* s_bias) {
+__device__ __forceinline__ void load_bias(const RouteOpArgs& a, float* s_bias) {
   for (int e = threadIdx.x; e < 32 * VPL; e += kThreads) {
     const float b = (a.bias != nullptr && e < a.E) ? a.bias[e] : 0.f;
     s_bias[e] = b > -INFINITY ? b : -INFINITY;
   }
   __syncthreads();
-  float m = 0.f;
-  for (int e = threadIdx.x & 31; e < 32 * VPL; e += 32)
-    if (s_bias[e] > -INFINITY) m = fmaxf(m, fabsf(s_bias[e]));
-  return warp_max_f(m);
+}
+
+// How far below key k another has to lie for their order to be certain, where a
+// score is off by up to err: the error of both keys. The rounding of the sum with
+// the bias, half a unit of the key, comes on top of the score's (twice that here,
+// which covers the comparison's own). It goes by the key, not by the largest bias,
+// so that an expert masked by -1e9 puts no other in doubt (32,768 tokens with one
+// such expert: 490 us by the largest bias, 45 so). The lower key's unit can only
+// be the larger one where both are negative or far apart, and then by less than a
+// 2^-23rd of their distance. k -+ key_gap(k) grows with k, so where the order of
+// two keys is certain, all above the one lie above all below the other.
+__device__ __forceinline__ float key_gap(float err, float k) {
+  return fmaf(fminf(fabsf(k), 3.402823466e+38f), 0x1p-22f, 2.f * err);
 }
 
 // Keys whose signed order is the order of the floats (with +0 above -0).
@@ -335,20 +343,19 @@ __device__ __noinline__ int rank_groups_exact(const RouteOpArgs& a, int64_t row,
 // ordered by: -inf for a dead expert and for one in a group that does not stay.
 // False where the token has no live expert (every lane alike).
 //
-// *err bounds the error of a key, and *doubt is set (in every lane) where the
-// ranks on either side of the group border are closer than the errors they can
-// have and are not settled here. With m the largest score: a softmax score is
+// *err bounds the error of a score (key_gap: that of two keys), and *doubt is set
+// (in every lane) where the ranks on either side of the group border are closer
+// than the errors they can have and are not settled here. With m the largest score: a softmax score is
 // off by less than 2^-19 m (exp and quotient a few roundings each, the sum up to
 // 21). A sigmoid: exp(-x) is off by (2 + |x|) 2^-23 of its value (2^-22 by the
 // documented bound of ex2.approx, the rest by the rounding of its argument and of
 // log2 e), which changes s by (1 - s) s of that; s (1 - s) |x| is below 0.23, and
 // below m |x of m| where all logits are low, so with the 2^-22 of the sum and the
-// reciprocal less than (2^-20 + 2^-22 max(-x of m, 0)) m. The sum with the bias
-// adds half a unit of the key, and scores that count as 0 less than 1e-37. Logits
-// used as keys are exact.
+// reciprocal less than (2^-20 + 2^-22 max(-x of m, 0)) m. Scores that count as 0
+// add less than 1e-37. Logits used as keys are exact.
 template <int VPL>
-__device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float* bias, float bias_max, int64_t row,
-                                           int64_t* smem, int lane, float (&key)[VPL], float* err, bool* doubt) {
+__device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float* bias, int64_t row, int64_t* smem, int lane,
+                                           float (&key)[VPL], float* err, bool* doubt) {
   *err = 0.f;
   const bool sums = a.n_groups > 1 && a.group_rank == 2;  // ranks are sums of scores
   if (a.bias != nullptr || sums) {
@@ -388,7 +395,7 @@ __device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float* bi
 #pragma unroll
       for (int i = 0; i < VPL; ++i) key[i] = (dead >> i) & 1u ? -INFINITY : key[i];
     }
-    *err += (s_max + bias_max) * 0x1p-23f + 1e-37f;
+    *err += 1e-37f;
   }
   if (a.n_groups == 1) return true;
 
@@ -418,7 +425,8 @@ __device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float* bi
       for (int n = 0; n < a.group_size; ++n) two_best(b1, b2, s_keys[g * a.group_size + n]);
     __syncwarp();
   }
-  const float rank = (a.group_rank == 2 && b2 > -INFINITY) ? b1 + b2 : b1;
+  const bool two = a.group_rank == 2 && b2 > -INFINITY;
+  const float rank = two ? b1 + b2 : b1;
   // the groups before this one; a group's lanes share the comparisons
   const int step = 1 << shift;
   int before = 0;
@@ -430,14 +438,18 @@ __device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float* bi
   for (int o = 1; o < step; o <<= 1) before += __shfl_xor_sync(kAll, before, o);
   if (g >= a.n_groups) before = kNoGroup;
   if (*err > 0.f) {
-    // the last group that stays and the first that does not
-    const float in = __shfl_sync(kAll, rank, __ffs(__ballot_sync(kAll, before == a.top_groups - 1)) - 1);
-    const float out = __shfl_sync(kAll, rank, __ffs(__ballot_sync(kAll, before == a.top_groups)) - 1);
-    *doubt = out > -INFINITY && !(in - out > (a.group_rank == 2 ? 4.f : 2.f) * *err);
+    // the lowest that a group that stays can rank and the highest that another
+    // live one can (a sum's own rounding: the other half of the keys' units)
+    float off = 0.5f * key_gap(*err, b1);
+    if (two) off += fmaf(fminf(fabsf(rank), 3.402823466e+38f), 0x1p-24f, 0.5f * key_gap(*err, b2));
+    const float in = -warp_max_fast(before < a.top_groups ? off - rank : -INFINITY);
+    const float out = warp_max_fast(before < a.top_groups || b1 == -INFINITY ? -INFINITY : rank + off);
+    *doubt = out > -INFINITY && !(in > out);
     if (*doubt && a.group_shift >= 0) {
       // the ranks again, from the exact scores of the few that can matter
       uint2* list = reinterpret_cast<uint2*>(smem);
-      const int n = list_above<VPL>(key, (a.group_rank == 2 ? b2 : b1) - 2.f * *err, list, lane);
+      const float last = a.group_rank == 2 ? b2 : b1;
+      const int n = list_above<VPL>(key, last - key_gap(*err, last), list, lane);
       if (n <= 32) {
         const int id = lane < n ? static_cast<int>(list[lane].y) : 0;
         __syncwarp();
@@ -481,7 +493,7 @@ template <int VPL>
 __device__ __forceinline__ int pick_by_rounds(const RouteOpArgs& a, int64_t row, float (&key)[VPL], int want, float err,
                                               int lane, bool* doubt) {
   int mine = -1, last_id = -1;
-  float last = 0.f;
+  float last = 0.f, gap = 0.f;  // the last key, key_gap(last)
   for (int k = 0; k < want; ++k) {
     float best = -INFINITY;
     int at = 0;
@@ -495,8 +507,9 @@ __device__ __forceinline__ int pick_by_rounds(const RouteOpArgs& a, int64_t row,
     if (!(top > -INFINITY)) break;  // uniform: no live expert left
     const int from = __ffs(__ballot_sync(kAll, best == top)) - 1;
     const int id = __shfl_sync(kAll, lane * VPL + at, from);
-    if (k > 0 && err > 0.f && !(last - top > 2.f * err) && !same_key(a, row, last_id, id)) *doubt = true;
+    if (k > 0 && err > 0.f && !(last - top > gap) && !same_key(a, row, last_id, id)) *doubt = true;
     last = top;
+    gap = key_gap(err, top);
     last_id = id;
     if (lane == k) mine = id;
     if (lane == from) {
@@ -512,7 +525,7 @@ __device__ __forceinline__ int pick_by_rounds(const RouteOpArgs& a, int64_t row,
 // bound of the want-th largest key; the few keys at or above it (as a rule
 // want to want + 4) are listed in shared memory, one per lane, and each lane
 // counts how many come before its own. With inexact keys the bound is lowered
-// by twice their error, so that the list holds the first want - 1 of the exact
+// by twice its error, so that the list holds the first want - 1 of the exact
 // order too; where two successive ones are in doubt the list is ranked again
 // by exact keys. False where more than 32 keys qualify.
 template <int VPL>
@@ -530,7 +543,7 @@ __device__ __forceinline__ bool pick_by_count(const RouteOpArgs& a, int64_t row,
   }
   const float bound = bound_int == kNone ? -INFINITY : order_float(bound_int);
   uint2* list = reinterpret_cast<uint2*>(smem);  // [32]
-  const int n = list_above<VPL>(key, bound - 2.f * err, list, lane);
+  const int n = list_above<VPL>(key, err > 0.f ? bound - key_gap(err, bound) : bound, list, lane);
   if (n > 32) return false;
   // (key, lower id first) as one unsigned number; 0 for no entry
   uint64_t own = 0;
@@ -559,7 +572,7 @@ __device__ __forceinline__ bool pick_by_count(const RouteOpArgs& a, int64_t row,
     const float k0 = order_float(static_cast<int>(static_cast<uint32_t>(own >> 32) ^ 0x80000000u));
     const float next = __shfl_down_sync(kAll, k0, 1);
     const int next_id = __shfl_down_sync(kAll, id, 1);
-    const bool close = lane + 1 < min(n, want) && !(k0 - next > 2.f * err) && !same_key(a, row, id, next_id);
+    const bool close = lane + 1 < min(n, want) && !(k0 - next > key_gap(err, k0)) && !same_key(a, row, id, next_id);
     if (__any_sync(kAll, close)) id = rank_exact(a, row, id, n, lane, smem);
   }
   *mine = id;
@@ -570,12 +583,12 @@ __device__ __forceinline__ bool pick_by_count(const RouteOpArgs& a, int64_t row,
 // expert (-1: none left). Worked out in float; where some comparison is closer
 // than the errors allow, again in double, whose order is the definition's.
 template <int VPL>
-__device__ __forceinline__ int select_token(const RouteOpArgs& a, int64_t row, const float* bias, float bias_max,
-                                            int64_t* smem, int lane) {
+__device__ __forceinline__ int select_token(const RouteOpArgs& a, int64_t row, const float* bias, int64_t* smem,
+                                            int lane) {
   float key[VPL], err;
   bool doubt = false;
   load_row<VPL>(a, row, lane, key);
-  if (!token_keys<VPL>(a, bias, bias_max, row, smem, lane, key, &err, &doubt)) return -1;
+  if (!token_keys<VPL>(a, bias, row, smem, lane, key, &err, &doubt)) return -1;
   // with inexact keys one more than K, to see the key that just missed
   const int want = err > 0.f ? a.K + 1 : a.K;
   int mine = -1;
@@ -706,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, VPL <= 8 ? 4 : 2) k_select(const __g
   pdl_trigger();
   int64_t* keys = reinterpret_cast<int64_t*>(raw + warp * scratch);
   __shared__ __align__(16) float s_bias[32 * VPL];
-  const float bias_max = load_bias<VPL>(a, s_bias);
+  load_bias<VPL>(a, s_bias);
   for (int t = warp, next; t < nt; t = next) {
     next = t + kWarps;
     if (take) {
@@ -714,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, VPL <= 8 ? 4 : 2) k_select(const __g
       next = __shfl_sync(kAll, next, 0);
     }
     const int64_t row = static_cast<int64_t>(t0 + t) * a.ld;
-    const int id = select_token<VPL>(a, row, s_bias, bias_max, keys, lane);
+    const int id = select_token<VPL>(a, row, s_bias, keys, lane);
     const float w = token_weight<VPL>(a, row, id, lane);
     if (lane < a.K) {
       const int64_t o = static_cast<int64_t>(t0 + t) * a.K + lane;

@@ -6,8 +6,11 @@ import torch
 from block_diffusion_moe_gb300 import clover as C
 from block_diffusion_moe_gb300 import synth
 
+from .test_gpu_moe_ops import _check_route
+
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+LOWEST = torch.finfo(torch.float32).min
 
 
 def _gen(seed):
@@ -59,6 +62,59 @@ def test_calls_on_a_stream_that_is_not_the_current_one():
         assert all(torch.equal(g, w) for g, w in zip(got, want))
         assert torch.equal(got_layer, want_layer)
     torch.cuda.synchronize()
+
+
+# -------------------------------------------------------------------- routing
+
+
+@pytest.mark.parametrize("low", [-1e9, LOWEST])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_masked_by_finite_biases(score, low):
+    """Experts switched off (or forced) by a large finite bias: alone, a group of them, all but a few."""
+    z = 1.5 * torch.randn(200, 256, generator=_gen(41))
+    z[4, 30:] = -float("inf")
+    b = 0.2 * torch.randn(256, generator=_gen(42))
+    some, group, most, forced = b.clone(), b.clone(), b.clone(), b.clone()
+    some[torch.randperm(256, generator=_gen(43))[:90]] = low
+    group[32:64] = low
+    most[5:250] = low
+    forced[77], forced[100:110] = -low, low
+    for bias in (some, group, most, forced):
+        _check_route(z.to(DEV), dict(top_k=8, score=score), bias=bias.to(DEV))
+        _check_route(z.to(DEV), dict(top_k=20, score=score), bias=bias.to(DEV))
+        for rank in (1, 2):
+            kw = dict(top_k=8, score=score, n_groups=8, top_groups=3, group_rank=rank)
+            _check_route(z.to(DEV), kw, bias=bias.to(DEV))
+            _check_route(z[:, :120].contiguous().to(DEV), dict(kw, n_groups=6), bias=bias[:120].contiguous().to(DEV))
+
+
+def _route_us(z, r, bias):
+    out, ws = C.route(r, z, bias=bias), C.workspace(C.route_workspace_bytes(r, z.shape[0]))
+    best = float("inf")
+    for _ in range(8):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        a.record()
+        for _ in range(5):
+            C.route(r, z, bias=bias, ws=ws, out=out)
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 200)
+    return best
+
+
+def test_route_masks_cost_no_more_than_other_biases():
+    """An expert masked by a large finite bias does not put every token's order in doubt."""
+    z = 1.5 * torch.randn(32768, 256, generator=_gen(45)).to(DEV)
+    b = 0.1 * torch.randn(256, generator=_gen(46))
+    for kw in (dict(score="sigmoid", n_groups=8, top_groups=4, group_rank=2), dict(score="softmax")):
+        r = C.make_routing(256, 8, **kw)
+        plain = _route_us(z, r, b.to(DEV))
+        for low in (-1e9, LOWEST):
+            for at in (slice(0, 1), slice(32, 64), slice(0, 256, 3)):
+                m = b.clone()
+                m[at] = low
+                assert _route_us(z, r, m.to(DEV)) < 2 * plain, (kw, low, at)
 
 
 # -------------------------------------------------------------------- product
