@@ -426,7 +426,9 @@ __device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float* bi
     __syncwarp();
   }
   const bool two = a.group_rank == 2 && b2 > -INFINITY;
-  const float rank = two ? b1 + b2 : b1;
+  const float sum = two ? b1 + b2 : b1;
+  // below fp32's range a live group still comes before one without a live expert
+  const float rank = two ? fmaxf(sum, -3.402823466e+38f) : sum;
   // the groups before this one; a group's lanes share the comparisons
   const int step = 1 << shift;
   int before = 0;
@@ -442,7 +444,8 @@ __device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float* bi
     // live one can (a sum's own rounding: the other half of the keys' units)
     float off = 0.5f * key_gap(*err, b1);
     if (two) off += fmaf(fminf(fabsf(rank), 3.402823466e+38f), 0x1p-24f, 0.5f * key_gap(*err, b2));
-    const float in = -warp_max_fast(before < a.top_groups ? off - rank : -INFINITY);
+    // (sums outside fp32's range are bounded on one side only)
+    const float in = -warp_max_fast(before < a.top_groups ? off - fminf(sum, 3.402823466e+38f) : -INFINITY);
     const float out = warp_max_fast(before < a.top_groups || b1 == -INFINITY ? -INFINITY : rank + off);
     *doubt = out > -INFINITY && !(in > out);
     if (*doubt && a.group_shift >= 0) {

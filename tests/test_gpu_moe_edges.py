@@ -88,6 +88,24 @@ def test_route_masked_by_finite_biases(score, low):
             _check_route(z[:, :120].contiguous().to(DEV), dict(kw, n_groups=6), bias=bias[:120].contiguous().to(DEV))
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [4, 3])
+def test_route_group_ranks_outside_fp32(score, size):
+    """Two biases whose sum leaves fp32's range either way: groups go by the sum itself, and a live group comes before
+    one without an expert. (Groups of 4 lie on whole lanes, groups of 3 do not.)"""
+    z = torch.randn(30, 6 * size, generator=_gen(44))
+    z[3, :size] = -float("inf")
+    z[5] = -float("inf")
+    b = torch.empty(6 * size)
+    for g, v in enumerate((-3e38, -2e38, -float("inf"), -2.5e38, -3.2e38, 0.1)):
+        b[g * size:(g + 1) * size] = v
+    for sign in (1.0, -1.0):
+        for top in range(1, 6):
+            for k in (2, 3 * size):
+                _check_route(z.to(DEV), dict(top_k=k, score=score, n_groups=6, top_groups=top, group_rank=2),
+                             bias=(sign * b).to(DEV))
+
+
 def _route_us(z, r, bias):
     out, ws = C.route(r, z, bias=bias), C.workspace(C.route_workspace_bytes(r, z.shape[0]))
     best = float("inf")
