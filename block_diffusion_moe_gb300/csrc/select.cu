@@ -491,13 +491,16 @@ __device__ __forceinline__ bool same_key(const RouteOpArgs& a, int64_t row, int 
 // The first `want` experts by descending key, ties to the lower id: lane k
 // returns the k-th (-1: none left). Each round takes the largest key and the
 // lowest lane, so the lowest id, that holds it. *doubt is set where two
-// successive keys are closer than their errors.
+// successive keys are closer than their errors. The last pair's order has to be
+// certain: behind a true tie there the rounds go on to the first one that is
+// not, as a key further down could still belong before both.
 template <int VPL>
 __device__ __forceinline__ int pick_by_rounds(const RouteOpArgs& a, int64_t row, float (&key)[VPL], int want, float err,
                                               int lane, bool* doubt) {
   int mine = -1, last_id = -1;
   float last = 0.f, gap = 0.f;  // the last key, key_gap(last)
-  for (int k = 0; k < want; ++k) {
+  bool tied = false;            // the last pair is a true tie
+  for (int k = 0; k < want || tied; ++k) {
     float best = -INFINITY;
     int at = 0;
 #pragma unroll
@@ -510,7 +513,11 @@ __device__ __forceinline__ int pick_by_rounds(const RouteOpArgs& a, int64_t row,
     if (!(top > -INFINITY)) break;  // uniform: no live expert left
     const int from = __ffs(__ballot_sync(kAll, best == top)) - 1;
     const int id = __shfl_sync(kAll, lane * VPL + at, from);
-    if (k > 0 && err > 0.f && !(last - top > gap) && !same_key(a, row, last_id, id)) *doubt = true;
+    tied = k > 0 && err > 0.f && !(last - top > gap);
+    if (tied && !same_key(a, row, last_id, id)) {
+      *doubt = true;
+      break;
+    }
     last = top;
     gap = key_gap(err, top);
     last_id = id;
@@ -575,7 +582,11 @@ __device__ __forceinline__ bool pick_by_count(const RouteOpArgs& a, int64_t row,
     const float k0 = order_float(static_cast<int>(static_cast<uint32_t>(own >> 32) ^ 0x80000000u));
     const float next = __shfl_down_sync(kAll, k0, 1);
     const int next_id = __shfl_down_sync(kAll, id, 1);
-    const bool close = lane + 1 < min(n, want) && !(k0 - next > key_gap(err, k0)) && !same_key(a, row, id, next_id);
+    // the first certain step at the K-th key or behind it; no pair before it may
+    // be in doubt (behind true ties a key further down could belong before them)
+    const bool sure = lane + 1 >= n || k0 - next > key_gap(err, k0);
+    const int end = __ffs(__ballot_sync(kAll, sure) & (kAll << (want - 2))) - 1;
+    const bool close = lane < end && !sure && !same_key(a, row, id, next_id);
     if (__any_sync(kAll, close)) id = rank_exact(a, row, id, n, lane, smem);
   }
   *mine = id;

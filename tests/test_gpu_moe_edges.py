@@ -1,5 +1,6 @@
 """The routed-expert operations at their edges. Every call goes through the C
 ABI."""
+import numpy as np
 import pytest
 import torch
 
@@ -104,6 +105,23 @@ def test_route_group_ranks_outside_fp32(score, size):
             for k in (2, 3 * size):
                 _check_route(z.to(DEV), dict(top_k=k, score=score, n_groups=6, top_groups=top, group_rank=2),
                              bias=(sign * b).to(DEV))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("k", [1, 2, 5, 16, 20])
+def test_route_true_ties_in_front_of_closer_keys(k, score):
+    """Experts of the same logit and bias, and others so close above or below them that only fp64 tells: the tie must
+    not hide those."""
+    rng = np.random.default_rng(k)
+    for E, values, bias in ((64, 2, 0.25), (64, 3, 1e4), (250, 3, 0.25), (250, 40, 1e4), (24, 2, 0.0)):
+        z = (0.5 + 1e-6 * rng.integers(0, values, size=(60, E))).astype(np.float32)
+        z[rng.random((60, E)) < 0.5] = -3.0
+        z[3:6] = 0.5
+        b = np.where(rng.random(E) < 0.1, bias + 0.125, bias).astype(np.float32)
+        zt, bt = torch.from_numpy(z).to(DEV), torch.from_numpy(b).to(DEV)
+        _check_route(zt, dict(top_k=min(k, E), score=score), bias=bt)
+        if E != 64:
+            _check_route(zt, dict(top_k=min(k, E), score=score, n_groups=2, top_groups=1, group_rank=1), bias=bt)
 
 
 def _route_us(z, r, bias):
