@@ -213,12 +213,15 @@ __global__ void __launch_bounds__(kThreads) k_dequantize_fp4(const Fp4QuantArgs 
     const int b = kMx ? c / 2 : c;
     const uint32_t sb = tile[(b / 4) * 512 + b % 4];
     const float s = kMx ? e8m0_to_float(sb) : e4m3_to_float(sb);
+    // a 2^scale_exp below 1 first: either way both products are then exact unless
+    // the result itself leaves bf16's range (6 x 2^126 x 2^-3 does not)
+    const float f1 = a.mul < 1.f ? a.mul : s, f2 = a.mul < 1.f ? s : a.mul;
     const uint2 u = *reinterpret_cast<const uint2*>(codes + c * 8);
     uint32_t o[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float2 v = e2m1_values(((j < 4 ? u.x : u.y) >> (8 * (j & 3))) & 0xFFu);
-      const __nv_bfloat162 p = __floats2bfloat162_rn(v.x * s * a.mul, v.y * s * a.mul);
+      const __nv_bfloat162 p = __floats2bfloat162_rn(v.x * f1 * f2, v.y * f1 * f2);
       o[j] = *reinterpret_cast<const uint32_t*>(&p);
     }
     store32b(a.out + i * a.cols + c * 16, a.wide, o);

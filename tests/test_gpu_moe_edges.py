@@ -6,6 +6,7 @@ import torch
 
 from block_diffusion_moe_gb300 import clover as C
 from block_diffusion_moe_gb300 import synth
+from oracle import moe_ops as R
 
 from .test_gpu_moe_ops import _check_route
 
@@ -151,6 +152,30 @@ def test_route_masks_cost_no_more_than_other_biases():
                 m = b.clone()
                 m[at] = low
                 assert _route_us(z, r, m.to(DEV)) < 2 * plain, (kw, low, at)
+
+
+# --------------------------------------------------------------- quantisation
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_dequantize_every_scale(fmt):
+    """Every code under every scale byte, times powers of two that lead out of the scale's own range and back."""
+    n = 127 if fmt == "nv" else 256
+    block = 16 if fmt == "nv" else 32
+    codes = np.tile(np.arange(16, dtype=np.uint8), (n, 4))
+    sb = np.repeat(np.arange(n, dtype=np.uint8)[:, None], 64 // block, 1)
+    tiles = R.scale_tiles(-(-n // 128), 64 // block)
+    for r in range(n):
+        for b in range(64 // block):
+            tiles[R.scale_place(r, b)] = sb[r, b]
+    q = C.Fp4(C.FP4_NV if fmt == "nv" else C.FP4_MX, torch.from_numpy(R.pack_codes(codes)).to(DEV),
+              torch.from_numpy(tiles.reshape(-1)).to(DEV))
+    for exp in (0, -1, -3, -64, 5, 64):
+        q.scale_exp = exp
+        want = torch.from_numpy(R.dequantize(codes, sb, fmt, exp)).bfloat16()
+        got = C.dequantize_fp4(q).cpu()
+        ok = (got == want) | (got.isnan() & want.isnan())
+        assert bool(ok.all()), (exp, [int(r) for r in torch.nonzero(~ok.all(1)).flatten()][:5])
 
 
 # -------------------------------------------------------------------- product
