@@ -323,6 +323,13 @@ __device__ __forceinline__ void store32(__nv_bfloat16* row, int c0, int width, b
   }
 }
 
+// z / (1 + e^-z), below zero as z e^z / (1 + e^z): e^-z would leave fp32's range
+// where the result is still an ordinary number.
+__device__ __forceinline__ float silu(float z) {
+  const float e = __expf(-fabsf(z));
+  return __fdividef(z < 0.f ? z * e : z, 1.f + e);
+}
+
 template <bool kSwiglu, bool kPair>
 __device__ void epilogue(const Fp4ProductArgs& p, Shared* sh, int64_t n_all, int n_tiles, int rank) {
   const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
@@ -360,7 +367,7 @@ __device__ void epilogue(const Fp4ProductArgs& p, Shared* sh, int64_t n_all, int
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         v[j] *= alpha;
-        if constexpr (kSwiglu) v[j] = __fdividef(v[j], 1.f + __expf(fminf(-v[j], 80.f))) * (u[j] * alpha);
+        if constexpr (kSwiglu) v[j] = silu(v[j]) * (u[j] * alpha);
       }
       if (on) store32(row, tl.n0 + c * 32, p.b_rows, vec, v);
     }

@@ -206,3 +206,29 @@ def test_product_without_workspace_keeps_its_status():
     assert e.value.code == C.ERR_DEVICE_TIMEOUT
     C.fp4_product_status()
     assert word.tolist() == [0] * 64
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_swiglu_of_gates_far_below_zero(fmt):
+    """silu falls to 0 for gates far below zero, whatever they are multiplied with. Rows and matrices have one element
+    each, so that the products are exact."""
+    up = 1.5 * 2.0 ** 9
+    x = torch.zeros(40, 64)
+    x[:, 0] = torch.tensor([1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -1.0, -6.0]).repeat(5) * torch.exp2(torch.arange(5.0)).repeat_interleave(8)
+    w = torch.zeros(2, 8, 64)
+    w[0, :, 0] = -4.0  # gate
+    w[1, :, 0] = up
+    a, b = C.quantize_fp4(x.to(DEV), C.FP4_NV if fmt == "nv" else C.FP4_MX), C.quantize_fp4(w.to(DEV), C.FP4_NV if fmt == "nv" else C.FP4_MX)
+    av, wv = R.dequantize(*R.quantize(x.numpy(), fmt), fmt)[:, 0], R.dequantize(*R.quantize(w.view(16, 64).numpy(), fmt), fmt)[:, 0]
+    for alpha in (1.0, 0.9375, 0.92, 1e3, 1e10, 1e20, 1e30):
+        z = float(np.float32(alpha)) * np.outer(av, wv)
+        gate, u = z[:, :8], z[:, 8:]
+        with np.errstate(over="ignore", under="ignore"):
+            y = gate / (1.0 + np.exp(-gate)) * u
+            # the gate's rounding moves silu(g) by |g| u of its slope, the exponential's argument by 2 |g| u more, which
+            # changes it in proportion (below 88; further down it is 0 but for denormals); a few steps of the rest
+            rel = 2.0 ** -8 + (np.minimum(np.abs(gate), 128.0) * 4 + 16) * 2.0 ** -24
+        got = C.fp4_product(a, b, swiglu=True, alpha=alpha).double().cpu().numpy()
+        ordinary = np.abs(y) < 3e38
+        assert np.all(np.abs(got - y)[ordinary] <= (rel * np.abs(y) + 2.0 ** -126 * np.maximum(np.abs(u), 1.0))[ordinary]), alpha
+        assert np.all(np.abs(got[~ordinary]) >= 3e38)
