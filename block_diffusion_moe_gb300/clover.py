@@ -12,6 +12,7 @@ tensor that is dropped while a stream other than its own still uses it.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import torch
@@ -493,8 +494,11 @@ class Fp4:
     matrix form groups. The parts are checked against one another here, once, and cannot be replaced but for offsets
     and scale_exp."""
 
-    __slots__ = ("fmt", "scale_exp", "device", "mats", "rows", "cols", "groups", "_offsets", "_shape", "_codes",
+    __slots__ = ("scale_exp", "_fmt", "_device", "_mats", "_rows", "_cols", "_groups", "_offsets", "_shape", "_codes",
                  "_scales", "_at")
+    # (the calls below read the fields themselves)
+    fmt, device, mats, rows, cols, groups = (property(operator.attrgetter(f)) for f in (
+        "_fmt", "_device", "_mats", "_rows", "_cols", "_groups"))
 
     def __init__(self, fmt: int, codes, scales, scale_exp: int = 0, offsets=None):
         if codes.dtype != _U8 or codes.dim() not in (2, 3) or not codes.is_contiguous():
@@ -503,10 +507,10 @@ class Fp4:
         if scales.dtype != _U8 or scales.device != codes.device or not scales.is_contiguous():
             _refuse(f"scales: need contiguous uint8 on {codes.device}, got {scales.dtype} {tuple(scales.shape)} on "
                     f"{scales.device}")
-        self.fmt, self.scale_exp, self.device = fmt, scale_exp, codes.device
+        self._fmt, self.scale_exp, self._device = fmt, scale_exp, codes.device
         self._shape, self._codes, self._scales, self._at = codes.shape, codes, scales, -1  # two tensors
-        self.mats = codes.shape[0] if codes.dim() == 3 else 1
-        self.rows, self.cols = codes.shape[-2], 2 * codes.shape[-1]
+        self._mats = codes.shape[0] if codes.dim() == 3 else 1
+        self._rows, self._cols = codes.shape[-2], 2 * codes.shape[-1]
         self.offsets = offsets
 
     @classmethod
@@ -515,13 +519,13 @@ class Fp4:
         q = object.__new__(cls)
         at = (mats * rows * cols // 2 + 127) & -128
         q._codes = q._scales = torch.empty(at + scale_bytes, dtype=_U8, device=device)
-        q.fmt, q.scale_exp, q._offsets, q._shape, q._at = fmt, scale_exp, offsets, shape, at
-        q.device, q.mats, q.rows, q.cols, q.groups = device, mats, rows, cols, groups
+        q._fmt, q.scale_exp, q._offsets, q._shape, q._at = fmt, scale_exp, offsets, shape, at
+        q._device, q._mats, q._rows, q._cols, q._groups = device, mats, rows, cols, groups
         return q
 
     @property
     def codes(self):
-        return self._codes if self._at < 0 else self._codes[:self.mats * self.rows * self.cols // 2].view(self._shape)
+        return self._codes if self._at < 0 else self._codes[:self._mats * self._rows * self._cols // 2].view(self._shape)
 
     @property
     def scales(self):
@@ -540,16 +544,16 @@ class Fp4:
         if offsets is not None:
             if len(self._shape) != 2:
                 _refuse("rows in groups form one matrix")
-            if offsets.dim() != 1 or offsets.dtype != torch.int32 or offsets.device != self.device \
+            if offsets.dim() != 1 or offsets.dtype != torch.int32 or offsets.device != self._device \
                     or not offsets.is_contiguous():
-                _refuse(f"offsets: need contiguous int32 [groups + 1] on {self.device}, got {offsets.dtype} "
+                _refuse(f"offsets: need contiguous int32 [groups + 1] on {self._device}, got {offsets.dtype} "
                         f"{tuple(offsets.shape)} on {offsets.device}")
         groups = 0 if offsets is None else offsets.shape[0] - 1
-        need = fp4_scale_bytes(self.fmt, self.mats, self.rows, self.cols, None if offsets is None else groups)
+        need = fp4_scale_bytes(self._fmt, self._mats, self._rows, self._cols, None if offsets is None else groups)
         have = self._scales.numel() - max(self._at, 0)
         if have < need:
             _refuse(f"scales: {have} bytes, need {need}")
-        self._offsets, self.groups = offsets, groups
+        self._offsets, self._groups = offsets, groups
 
 
 def fp4_scale_bytes(fmt: int, n_mats: int, rows: int, cols: int, n_groups: int | None = None) -> int:
@@ -595,15 +599,15 @@ def quantize_fp4(x, fmt: int = FP4_NV, scale_exp: int = 0, offsets=None, src_row
         mats, device = shape[0] if len(shape) == 3 else 1, x.device
         n = fp4_scale_bytes(fmt, mats, rows, cols, n_groups)
         out = Fp4._new(fmt, codes_shape, n, scale_exp, offsets, n_groups or 0, device, mats, rows, cols)
-    elif out.fmt != fmt or out._shape != codes_shape or out.device != x.device:
-        _refuse(f"out holds {tuple(out._shape)} of format {out.fmt} on {out.device}")
+    elif out._fmt != fmt or out._shape != codes_shape or out._device != x.device:
+        _refuse(f"out holds {tuple(out._shape)} of format {out._fmt} on {out._device}")
     else:
         out.offsets, out.scale_exp = offsets, scale_exp
     if grouped:
         rc = lib().clover_quantize_fp4_rows(fmt, p_x, kind, ldx, shape[0], cols, scale_exp, p_src, src_div, rows, p_off,
                                             n_groups, *out._pointers(), _current_stream(dev))
     else:
-        rc = lib().clover_quantize_fp4(fmt, p_x, kind, ldx, out.mats, rows, cols, scale_exp, *out._pointers(),
+        rc = lib().clover_quantize_fp4(fmt, p_x, kind, ldx, out._mats, rows, cols, scale_exp, *out._pointers(),
                                        _current_stream(dev))
     if rc != OK:
         _check(rc)
@@ -617,14 +621,14 @@ def dequantize_fp4(q: Fp4, out=None, stream=None):
             return dequantize_fp4(q, out)
     off = q._offsets
     dev = _on_current("q", q._codes)
-    shape = q._shape[:-1] + (q.cols,)
+    shape = q._shape[:-1] + (q._cols,)
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=q.device)
+        out = torch.empty(shape, dtype=_BF16, device=q._device)
         p_out = out.data_ptr()
     else:
         p_out = _tensor("out", out, _BF16, shape, dev)
-    rc = lib().clover_dequantize_fp4(q.fmt, *q._pointers(), q.mats, q.rows, q.cols, q.scale_exp,
-                                     None if off is None else off.data_ptr(), q.groups, p_out, _current_stream(dev))
+    rc = lib().clover_dequantize_fp4(q._fmt, *q._pointers(), q._mats, q._rows, q._cols, q.scale_exp,
+                                     None if off is None else off.data_ptr(), q._groups, p_out, _current_stream(dev))
     if rc != OK:
         _check(rc)
     return out
@@ -663,21 +667,21 @@ def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_
     dev = _on_current("a", a._codes)
     if len(a._shape) != 2 or b._offsets is not None:
         _refuse("a must be one matrix, and only its rows may form groups")
-    if a.fmt != b.fmt or a.cols != b.cols or b.device != a.device:
-        _refuse(f"a (format {a.fmt}, {a.cols} columns, {a.device}) does not match b (format {b.fmt}, {b.cols} columns, "
-                f"{b.device})")
-    rows, width = a.rows, b.rows
-    groups = 1 if off is None else a.groups
-    if b.mats != groups * per:
-        _refuse(f"b holds {b.mats} matrices for {groups} groups, {per} each")
+    if a._fmt != b._fmt or a._cols != b._cols or b._device != a._device:
+        _refuse(f"a (format {a._fmt}, {a._cols} columns, {a._device}) does not match b (format {b._fmt}, {b._cols} columns, "
+                f"{b._device})")
+    rows, width = a._rows, b._rows
+    groups = 1 if off is None else a._groups
+    if b._mats != groups * per:
+        _refuse(f"b holds {b._mats} matrices for {groups} groups, {per} each")
     if out is None:
-        out = torch.empty((rows, width), dtype=_BF16, device=a.device)
+        out = torch.empty((rows, width), dtype=_BF16, device=a._device)
         p_out = out.data_ptr()
     else:
         p_out = _tensor("out", out, _BF16, (rows, width), dev)
     p_alpha = None if group_alpha is None else _tensor("group_alpha", group_alpha, _F32, (groups,), dev)
-    rc = lib().clover_fp4_product(a.fmt, *a._pointers(), rows, *b._pointers(), None if off is None else off.data_ptr(),
-                                  groups, width * per, a.cols, alpha * 2.0 ** (a.scale_exp + b.scale_exp), p_alpha, int(swiglu), p_out,
+    rc = lib().clover_fp4_product(a._fmt, *a._pointers(), rows, *b._pointers(), None if off is None else off.data_ptr(),
+                                  groups, width * per, a._cols, alpha * 2.0 ** (a.scale_exp + b.scale_exp), p_alpha, int(swiglu), p_out,
                                   *(_shared_workspace() if ws is None else _scratch(ws, dev)), _current_stream(dev))
     if rc != OK:
         _check(rc)

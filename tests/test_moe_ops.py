@@ -330,6 +330,16 @@ def test_product_shared_workspace_arguments(lib):
     assert lib.clover_fp4_product_shared_workspace(None) == C.ERR_INVALID_ARG
 
 
+def test_fp4_fields_cannot_be_set(lib):
+    """Sizes and format are what the parts were checked for: another value would reach past them."""
+    q = C.Fp4(C.FP4_MX, torch.zeros(2, 4, 32, dtype=torch.uint8), torch.zeros(1024, dtype=torch.uint8))
+    for name, value in dict(fmt=C.FP4_NV, device="cuda", mats=9, rows=400, cols=6400, groups=3).items():
+        with pytest.raises(AttributeError):
+            setattr(q, name, value)
+    assert (q.fmt, q.device, q.mats, q.rows, q.cols, q.groups) == (C.FP4_MX, torch.device("cpu"), 2, 4, 64, 0)
+    q.scale_exp = 3
+
+
 # --------------------------------------------------- streams of the binding
 
 
