@@ -401,6 +401,13 @@ def _refuse(msg: str):
     raise CloverError(ERR_INVALID_ARG, msg)
 
 
+def _counts(*values):
+    """Refuses what would wrap on its way to the library's 32-bit arguments."""
+    for v in values:
+        if not -(1 << 31) <= v < 1 << 31:
+            _refuse(f"{v}: a count past 32 bits")
+
+
 def _tensor(name: str, t, dtype, shape, dev: int) -> int:
     """The pointer of a contiguous tensor of this type and shape on CUDA device `dev`."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
@@ -443,12 +450,12 @@ def make_routing(n_experts: int, top_k: int, score: str = "softmax", n_groups: i
     if score not in _SCORES:
         _refuse(f"score {score!r} is neither 'softmax' nor 'sigmoid'")
     top_groups = n_groups if top_groups is None else top_groups
-    if any(not -(1 << 31) <= v < 1 << 31 for v in (n_experts, top_k, n_groups, top_groups, group_rank)):
-        _refuse("a count past 32 bits")
+    _counts(n_experts, top_k, n_groups, top_groups, group_rank)
     return Routing(n_experts, top_k, _SCORES[score], n_groups, top_groups, group_rank, int(bool(renormalise)), scale)
 
 
 def route_workspace_bytes(r: Routing, max_tokens: int) -> int:
+    _counts(max_tokens)
     return lib().clover_route_workspace_bytes(r, max_tokens)
 
 
@@ -558,6 +565,7 @@ class Fp4:
 
 def fp4_scale_bytes(fmt: int, n_mats: int, rows: int, cols: int, n_groups: int | None = None) -> int:
     """Bytes of the scale tiles of n_mats matrices, or of `rows` rows in n_groups groups."""
+    _counts(fmt, n_mats, rows, cols, n_groups or 0)
     if n_groups is None:
         n = lib().clover_fp4_scale_bytes(fmt, n_mats, rows, cols)
     else:
@@ -583,6 +591,7 @@ def quantize_fp4(x, fmt: int = FP4_NV, scale_exp: int = 0, offsets=None, src_row
     else:
         dev, p_x, kind, ldx = _rows_of("x", x)
     cols, rows, p_src = shape[-1], shape[-2], None
+    _counts(fmt)
     if not (-64 <= scale_exp <= 64 and 1 <= src_div < 1 << 31):
         _refuse(f"scale_exp={scale_exp} outside [-64, 64], or src_div={src_div} below 1 or past 32 bits")
     if src_rows is not None:

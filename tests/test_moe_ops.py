@@ -340,6 +340,21 @@ def test_fp4_fields_cannot_be_set(lib):
     q.scale_exp = 3
 
 
+def test_sizes_past_32_bits_refused(lib):
+    """A count that would wrap on its way to the library is refused, not taken for the wrapped one."""
+    big = (1 << 32) + 1
+    r = C.make_routing(8, 2)
+    codes = torch.zeros(1, 1, dtype=torch.uint8).expand(big, 32)  # (never contiguous, so only its shape counts)
+    for f in (lambda: C.route_workspace_bytes(r, big), lambda: C.fp4_scale_bytes(C.FP4_NV, 1, big, 64),
+              lambda: C.fp4_scale_bytes(C.FP4_NV, big, 1, 64), lambda: C.fp4_scale_bytes(C.FP4_NV, 1, 1, (1 << 32) + 64),
+              lambda: C.fp4_scale_bytes(C.FP4_NV, 1, 1, 64, big), lambda: C.fp4_scale_bytes(1 << 32, 1, 1, 64),
+              lambda: C.Fp4(C.FP4_NV, codes, torch.zeros(512, dtype=torch.uint8)),
+              lambda: C.Fp4(1 << 32, torch.zeros(1, 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8))):
+        with pytest.raises(C.CloverError):
+            f()
+    assert C.fp4_scale_bytes(C.FP4_NV, 1, 1, 64) == 512
+
+
 # --------------------------------------------------- streams of the binding
 
 
