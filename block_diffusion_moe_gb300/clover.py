@@ -548,6 +548,10 @@ class Fp4:
 
     @offsets.setter
     def offsets(self, offsets):
+        self._offsets, self._groups = offsets, self._groups_of(offsets)
+
+    def _groups_of(self, offsets):
+        """The number of groups of these offsets, checked against the scales' room."""
         if offsets is not None:
             if len(self._shape) != 2:
                 _refuse("rows in groups form one matrix")
@@ -560,7 +564,7 @@ class Fp4:
         have = self._scales.numel() - max(self._at, 0)
         if have < need:
             _refuse(f"scales: {have} bytes, need {need}")
-        self._offsets, self._groups = offsets, groups
+        return groups
 
 
 def fp4_scale_bytes(fmt: int, n_mats: int, rows: int, cols: int, n_groups: int | None = None) -> int:
@@ -611,7 +615,7 @@ def quantize_fp4(x, fmt: int = FP4_NV, scale_exp: int = 0, offsets=None, src_row
     elif out._fmt != fmt or out._shape != codes_shape or out._device != x.device:
         _refuse(f"out holds {tuple(out._shape)} of format {out._fmt} on {out._device}")
     else:
-        out.offsets, out.scale_exp = offsets, scale_exp
+        out._groups_of(offsets)
     if grouped:
         rc = lib().clover_quantize_fp4_rows(fmt, p_x, kind, ldx, shape[0], cols, scale_exp, p_src, src_div, rows, p_off,
                                             n_groups, *out._pointers(), _current_stream(dev))
@@ -620,6 +624,7 @@ def quantize_fp4(x, fmt: int = FP4_NV, scale_exp: int = 0, offsets=None, src_row
                                        _current_stream(dev))
     if rc != OK:
         _check(rc)
+    out._offsets, out._groups, out.scale_exp = offsets, n_groups or 0, scale_exp
     return out
 
 

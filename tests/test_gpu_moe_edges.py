@@ -178,6 +178,21 @@ def test_dequantize_every_scale(fmt):
         assert bool(ok.all()), (exp, [int(r) for r in torch.nonzero(~ok.all(1)).flatten()][:5])
 
 
+def test_refused_quantisation_leaves_out_as_it_was():
+    """A refused call does not give `out` the exponent and offsets that its codes were not made for."""
+    x = torch.randn(40, 72, generator=_gen(57)).to(DEV)
+    off = torch.tensor([0, 30, 40], dtype=torch.int32, device=DEV)
+    q = C.quantize_fp4(x[:, :64].contiguous(), scale_exp=-2, offsets=off)
+    want = C.dequantize_fp4(q)
+    with pytest.raises(C.CloverError):
+        C.quantize_fp4(x[:, 1:65], scale_exp=5, offsets=torch.zeros(2, dtype=torch.int32, device=DEV), out=q)  # rows not aligned
+    assert q.scale_exp == -2 and q.offsets is off and q.groups == 2
+    assert torch.equal(C.dequantize_fp4(q), want)
+    got = C.quantize_fp4(x[:, :64], scale_exp=5, offsets=off, out=q)
+    assert got is q and q.scale_exp == 5
+    assert torch.equal(C.dequantize_fp4(q), C.dequantize_fp4(C.quantize_fp4(x[:, :64], scale_exp=5)))
+
+
 # -------------------------------------------------------------------- product
 
 
