@@ -392,6 +392,8 @@ FP4_MX = 1
 _SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
 _F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
 _TYPES = {_F32: 0, _BF16: 1}
+_UNGROUPED = {"idx", "w"}
+_GROUPED = _UNGROUPED | {"offsets", "rows", "pos"}
 # (calls of a few microseconds: the device and stream objects of torch.cuda cost as much as the launch)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -414,6 +416,12 @@ def _tensor(name: str, t, dtype, shape, dev: int) -> int:
         _refuse(f"{name}: need contiguous {dtype} {tuple(shape)} on cuda:{dev}, "
                 f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
     return t.data_ptr()
+
+
+def _length(name: str, t) -> int:
+    if t.dim() != 1:
+        _refuse(f"{name}: need one dimension, got {tuple(t.shape)}")
+    return t.shape[0]
 
 
 def _on_current(name: str, t) -> int:
@@ -482,6 +490,8 @@ def route(r: Routing, logits, bias=None, grouping: bool = True, ws=None, out=Non
             out["offsets"] = torch.empty(E + 1, dtype=_I32, device=device)
             out["rows"] = torch.empty(M * K, dtype=_I32, device=device)
             out["pos"] = torch.empty(slots, dtype=_I32, device=device)
+    elif not (_GROUPED if grouping else _UNGROUPED) <= out.keys():
+        _refuse(f"out holds {sorted(out)}, not what this call returns")
     p_off = p_rows = p_pos = None
     if grouping:
         p_off = _tensor("offsets", out["offsets"], _I32, (E + 1,), dev)
@@ -601,12 +611,12 @@ def quantize_fp4(x, fmt: int = FP4_NV, scale_exp: int = 0, offsets=None, src_row
     if src_rows is not None:
         if not grouped:
             _refuse("src_rows without offsets")
-        rows = src_rows.shape[0]
+        rows = _length("src_rows", src_rows)
         p_src = _tensor("src_rows", src_rows, _I32, (rows,), dev)
     codes_shape = shape[:-2] + (rows, cols // 2)
     n_groups = p_off = None
     if grouped:
-        n_groups = offsets.shape[0] - 1
+        n_groups = _length("offsets", offsets) - 1
         p_off = _tensor("offsets", offsets, _I32, (n_groups + 1,), dev)
     if out is None:
         mats, device = shape[0] if len(shape) == 3 else 1, x.device
@@ -694,8 +704,12 @@ def fp4_product(a: Fp4, b: Fp4, swiglu: bool = False, alpha: float = 1.0, group_
     else:
         p_out = _tensor("out", out, _BF16, (rows, width), dev)
     p_alpha = None if group_alpha is None else _tensor("group_alpha", group_alpha, _F32, (groups,), dev)
+    try:
+        factor = alpha * 2.0 ** (a.scale_exp + b.scale_exp)
+    except OverflowError:
+        _refuse(f"alpha {alpha} and scale exponents {a.scale_exp}, {b.scale_exp}: past the largest number")
     rc = lib().clover_fp4_product(a._fmt, *a._pointers(), rows, *b._pointers(), None if off is None else off.data_ptr(),
-                                  groups, width * per, a._cols, alpha * 2.0 ** (a.scale_exp + b.scale_exp), p_alpha, int(swiglu), p_out,
+                                  groups, width * per, a._cols, factor, p_alpha, int(swiglu), p_out,
                                   *(_shared_workspace() if ws is None else _scratch(ws, dev)), _current_stream(dev))
     if rc != OK:
         _check(rc)

@@ -355,6 +355,22 @@ def test_sizes_past_32_bits_refused(lib):
     assert C.fp4_scale_bytes(C.FP4_NV, 1, 1, 64) == 512
 
 
+def test_malformed_arguments_are_refused(lib, monkeypatch):
+    """What the checks once met with an IndexError, KeyError or OverflowError of their own."""
+    monkeypatch.setattr(C, "_on_current", lambda name, t: -1)  # (host tensors: every call here is refused before the library's)
+    monkeypatch.setattr(C, "_current_stream", lambda dev: None)
+    r = C.make_routing(8, 2)
+    z, x, i32 = torch.zeros(4, 8), torch.zeros(4, 64), torch.zeros(4, dtype=torch.int32)
+    some = {"idx": torch.zeros(4, 2, dtype=torch.int32), "w": torch.zeros(4, 2)}
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    q = C.Fp4(C.FP4_NV, torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8), scale_exp=4000)
+    for f in (lambda: C.quantize_fp4(x, offsets=i32[0]), lambda: C.quantize_fp4(x, offsets=i32, src_rows=i32[0]),
+              lambda: C.route(r, z, ws=ws, out=some), lambda: C.route(r, z, ws=ws, out={}, grouping=False),
+              lambda: C.fp4_product(q, q, ws=ws)):
+        with pytest.raises(C.CloverError):
+            f()
+
+
 # --------------------------------------------------- streams of the binding
 
 
