@@ -8,6 +8,7 @@ from block_diffusion_moe_gb300 import clover as C
 from block_diffusion_moe_gb300 import synth
 from oracle import moe_ops as R
 
+from .test_gpu_fp4_product import _operands
 from .test_gpu_moe_ops import _check_route
 
 pytestmark = pytest.mark.gpu
@@ -154,6 +155,32 @@ def test_route_masks_cost_no_more_than_other_biases():
                 assert _route_us(z, r, m.to(DEV)) < 2 * plain, (kw, low, at)
 
 
+@pytest.mark.parametrize("M", [4864, 4865, 38912, 38913, 40960, 40961, 90000])
+def test_route_of_many_tokens(M):
+    """Where a CTA's tokens begin to grow (4,865), where the CTAs do (38,913), and more counts of an expert than a scan
+    loads at once (40,961): the slots against a stable sort."""
+    E, K = 24, 2
+    z = torch.randn(M, E, generator=_gen(M)) + torch.linspace(-1, 1, E)
+    z[torch.rand(M, generator=_gen(M + 1)) < 0.05] = -float("inf")
+    out = C.route(C.make_routing(E, K), z.to(DEV))
+    got = {k: v.cpu() for k, v in out.items()}
+    top = torch.sort(z, dim=1, descending=True, stable=True)
+    idx = torch.where(top.values[:, :K] > -float("inf"), top.indices[:, :K], -1)
+    assert torch.equal(got["idx"].long(), idx)
+    flat = idx.flatten()
+    key = torch.where(flat >= 0, flat, E)
+    order = torch.argsort(key, stable=True)
+    n = int((flat >= 0).sum())
+    pos = torch.full((M * K,), -1, dtype=torch.int64)
+    pos[order[:n]] = torch.arange(n)
+    assert torch.equal(got["rows"][:n].long(), order[:n])
+    assert torch.equal(got["pos"].long().flatten(), pos)
+    assert torch.equal(got["offsets"].long(), torch.searchsorted(key[order].contiguous(), torch.arange(E + 1)))
+    w = torch.softmax(top.values[:, :K].double(), 1)
+    # differences of logits up to 12, an exponential and a quotient: 60 u
+    assert bool(((got["w"].double() - torch.where(idx >= 0, w, 0.0)).abs() <= 60 * 2.0 ** -24).all())
+
+
 # --------------------------------------------------------------- quantisation
 
 
@@ -247,3 +274,33 @@ def test_swiglu_of_gates_far_below_zero(fmt):
         ordinary = np.abs(y) < 3e38
         assert np.all(np.abs(got - y)[ordinary] <= (rel * np.abs(y) + 2.0 ** -126 * np.maximum(np.abs(u), 1.0))[ordinary]), alpha
         assert np.all(np.abs(got[~ordinary]) >= 3e38)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("counts,N,K,swiglu", [([2100, 0, 2500], 2300, 8192, False), ([2100, 1, 2500], 2600, 4160, True),
+                                               ([1500, 3100], 5000, 8192, False)])
+def test_pairs_of_ctas_take_several_tiles(counts, N, K, swiglu, fmt):
+    """More tiles than twice the pairs of CTAs: every pair uses both accumulators, and some the first again."""
+    a, b, off = _operands(counts, N, K, fmt, swiglu, sum(counts), extra_rows=2)
+    step = 128 if swiglu else 256
+    width = N // 2 if swiglu else N
+    tiles = sum(-(-c // 256) for c in counts) * -(-width // step)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert tiles > 2 * (sms // 2)
+    ws = C.workspace(C.fp4_product_workspace_bytes())
+    out = torch.full((a.rows, width), 7.0, dtype=torch.bfloat16, device=DEV)
+    C.fp4_product(a, b, swiglu=swiglu, ws=ws, out=out)
+    C.workspace_status(ws)
+    assert out[off[-1]:].eq(7.0).all()
+    av, bv = C.dequantize_fp4(a).double(), C.dequantize_fp4(b).double().view(len(counts), -1, K)
+    for g in range(len(counts)):
+        r = slice(off[g], off[g + 1])
+        y, m = av[r] @ bv[g].T, av[r].abs() @ bv[g].abs().T * 2.0 ** -13
+        if swiglu:
+            gate, up, mg, mu = y[:, :width], y[:, width:], m[:, :width], m[:, width:]
+            s = gate / (1 + torch.exp(-gate))
+            y = s * up  # |silu'| <= 1.1; exp and the quotient 2^-20 of the value
+            m = 1.1 * mg * up.abs() + s.abs() * mu + 1.1 * mg * mu + y.abs() * 2.0 ** -20
+        tol = m + (y.abs() + m) * 2.0 ** -8 + 1e-37
+        err = (out[r].double() - y).abs()
+        assert bool((err <= tol).all()), (g, float((err / tol).max()), int((err > tol).sum()))
