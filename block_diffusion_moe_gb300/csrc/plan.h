@@ -36,7 +36,9 @@ inline int persistent_grid(int sms, int resident_per_sm) {
 // waits longer between tiles and fills its tiles worse: it needs long groups
 // and a long K (single -> pair on one box: 8,192^3 195 -> 178 us, SwiGLU with N =
 // K = 8,192 186 -> 161, with K = 4,096 104 -> 99; but plain with K = 4,096 111 ->
-// 114, with K = 2,048 74 -> 83, and 64 groups of about 256 rows 150 -> 174).
+// 114, with K = 2,048 74 -> 83, and 64 groups of about 256 rows 150 -> 174). Not
+// timed, and left to single CTAs: a plain K between 4,096 and 8,192, groups between
+// 256 and 1,024 rows. N is not asked about: 256 rows of it make a tile either way.
 inline bool fp4_pairs(int rows, int groups, int k, bool swiglu) {
   return rows / groups >= 1024 && k >= (swiglu ? 4096 : 8192);
 }
