@@ -18,12 +18,13 @@
 // What bounds it, measured: few rows per group, HBM (256 rows of 256 experts
 // 1,024 x 2,048, SwiGLU: 27.7 us, the 192 MB of the matrices that have rows at
 // 7.0 TB/s). 65,536 rows over the same experts: 87 us, 435 MB of DRAM traffic at
-// 5.0 TB/s; without its loads 72 us (timed without that part; a tile's MMAs and scale copies take 680
+// 5.0 TB/s; without its loads 72 us (a tile's MMAs and scale copies take 680
 // cycles per stage, and the next tile starts some 700 cycles late, when the
 // shared accumulator columns are drained). 8,192^3: 178 us, 6.2 PFLOP/s; without
 // the scale copies 168, without the codes' loads 162, without MMAs but one per
 // stage and the copies 146: the tensor core spends 492 of 740 cycles per stage in
-// MMAs and the 12 scale copies, which it executes in order with them, 190.
+// MMAs and the 12 scale copies, which it executes in order with them, 190. (The
+// "without" figures are of copies of this kernel with that part taken out.)
 #include <math.h>
 
 #include "fp4.cuh"

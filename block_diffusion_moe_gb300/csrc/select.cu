@@ -343,16 +343,17 @@ __device__ __noinline__ int rank_groups_exact(const RouteOpArgs& a, int64_t row,
 // ordered by: -inf for a dead expert and for one in a group that does not stay.
 // False where the token has no live expert (every lane alike).
 //
-// *err bounds the error of a score (key_gap: that of two keys), and *doubt is set
-// (in every lane) where the ranks on either side of the group border are closer
-// than the errors they can have and are not settled here. With m the largest score: a softmax score is
-// off by less than 2^-19 m (exp and quotient a few roundings each, the sum up to
-// 21). A sigmoid: exp(-x) is off by (2 + |x|) 2^-23 of its value (2^-22 by the
-// documented bound of ex2.approx, the rest by the rounding of its argument and of
-// log2 e), which changes s by (1 - s) s of that; s (1 - s) |x| is below 0.23, and
-// below m |x of m| where all logits are low, so with the 2^-22 of the sum and the
-// reciprocal less than (2^-20 + 2^-22 max(-x of m, 0)) m. Scores that count as 0
-// add less than 1e-37. Logits used as keys are exact.
+// *err bounds the error of a score (key_gap: that of two keys), and *doubt is
+// set (in every lane) where the ranks on either side of the group border are
+// closer than the errors they can have and are not settled here. With m the
+// largest score: a softmax score is off by less than 2^-19 m (exp and quotient a
+// few roundings each, the sum up to 21). A sigmoid: exp(-x) is off by (2 + |x|)
+// 2^-23 of its value (2^-22 by the documented bound of ex2.approx, the rest by
+// the rounding of its argument and of log2 e), which changes s by (1 - s) s of
+// that; s (1 - s) |x| is below 0.23, and below m |x of m| where all logits are
+// low, so with the 2^-22 of the sum and the reciprocal less than (2^-20 + 2^-22
+// max(-x of m, 0)) m. Scores that count as 0 add less than 1e-37. Logits used as
+// keys are exact.
 template <int VPL>
 __device__ __forceinline__ bool token_keys(const RouteOpArgs& a, const float* bias, int64_t row, int64_t* smem, int lane,
                                            float (&key)[VPL], float* err, bool* doubt) {
