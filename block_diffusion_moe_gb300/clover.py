@@ -57,6 +57,25 @@ class Routing(ctypes.Structure):
                 ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class KvCacheArgs(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("k_exp", ctypes.c_int32),
+                ("v_exp", ctypes.c_int32)]
+
+
+class KvSeqs(ctypes.Structure):
+    _fields_ = [("offsets", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class PromptSeqs(ctypes.Structure):
+    _fields_ = [("offsets", ctypes.c_void_p), ("k_offsets", ctypes.c_void_p), ("n_seqs", ctypes.c_int32)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
 _i32, _i64, _ptr_t, _size = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
 
 EXPORTS = {
@@ -116,6 +135,17 @@ EXPORTS = {
                                           ctypes.c_float, _ptr_t, _i32, _ptr_t, _ptr_t, _size, _ptr_t]),
     "clover_moe_combine": (ctypes.c_int, [_ptr_t, _i32, _ptr_t, _ptr_t, _ptr_t, _ptr_t, _ptr_t, _i32, _i32, _i32,
                                           _ptr_t]),
+    "clover_kv_page_bytes": (_size, [_i32, _i32, _i32]),
+    "clover_kv_write": (ctypes.c_int, [ctypes.POINTER(KvCacheArgs), ctypes.POINTER(KvSeqs), ctypes.POINTER(Rows),
+                                       ctypes.POINTER(Rows), _i32, _i32, _ptr_t]),
+    "clover_kv_read": (ctypes.c_int, [ctypes.POINTER(KvCacheArgs), ctypes.POINTER(KvSeqs), _ptr_t, _ptr_t, _i32, _ptr_t]),
+    "clover_kv_attention_workspace_bytes": (_size, [ctypes.POINTER(KvCacheArgs), _i32, _i32, _i32, _i32]),
+    "clover_kv_attention": (ctypes.c_int, [ctypes.POINTER(KvCacheArgs), ctypes.POINTER(KvSeqs), ctypes.POINTER(Rows),
+                                           _i32, _i32, ctypes.c_float, _i32, _ptr_t, _ptr_t, _ptr_t, _size, _ptr_t]),
+    "clover_prompt_attention_workspace_bytes": (_size, [_i32] * 6),
+    "clover_prompt_attention": (ctypes.c_int, [ctypes.POINTER(PromptSeqs), ctypes.POINTER(Rows), ctypes.POINTER(Rows),
+                                               ctypes.POINTER(Rows), _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _i32,
+                                               _ptr_t, _ptr_t, _ptr_t, _size, _ptr_t]),
 }
 
 _lib = None
@@ -741,3 +771,188 @@ def moe_combine(y, pos, w, x=None, shared=None, out=None, stream=None):
     if rc != OK:
         _check(rc)
     return out
+
+
+# ------------------------------------------------------------------- attention
+
+
+class KvCache:
+    """A paged 4-bit cache of keys and values: pages uint8 [pages][kv_heads][page_tokens / 16][18 * head_dim]
+    (include/clover.h has the layout), keys scaled by 2^k_exp and values by 2^v_exp. The tensor is checked here, once."""
+
+    __slots__ = ("_pages", "_args", "_device")
+    pages, device = property(operator.attrgetter("_pages")), property(operator.attrgetter("_device"))
+    n_pages, page_tokens, kv_heads, head_dim, k_exp, v_exp = (property(operator.attrgetter("_args." + f)) for f in (
+        "n_pages", "page_tokens", "kv_heads", "head_dim", "k_exp", "v_exp"))
+
+    def __init__(self, pages, k_exp: int = 0, v_exp: int = 0):
+        if pages.dtype != _U8 or pages.dim() != 4 or not pages.is_contiguous() or pages.shape[3] % 18 != 0:
+            _refuse(f"pages: need contiguous uint8 [pages][kv_heads][page_tokens / 16][18 * head_dim], got {pages.dtype} "
+                    f"{tuple(pages.shape)}, strides {pages.stride()}")
+        n, heads, sixteens, row = pages.shape
+        _counts(n, k_exp, v_exp)
+        kv_page_bytes(16 * sixteens, heads, row // 18)
+        if n < 1 or max(abs(k_exp), abs(v_exp)) > 64:
+            _refuse(f"{n} pages, k_exp={k_exp}, v_exp={v_exp}: need at least one page, exponents in [-64, 64]")
+        self._pages, self._device = pages, pages.device
+        self._args = KvCacheArgs(pages.data_ptr(), n, 16 * sixteens, heads, row // 18, k_exp, v_exp)
+
+    @classmethod
+    def empty(cls, n_pages: int, page_tokens: int, kv_heads: int, head_dim: int, k_exp: int = 0, v_exp: int = 0,
+              device="cuda"):
+        """A cache whose pages hold zeros."""
+        kv_page_bytes(page_tokens, kv_heads, head_dim)
+        return cls(torch.zeros((n_pages, kv_heads, page_tokens // 16, 18 * head_dim), dtype=_U8, device=device), k_exp, v_exp)
+
+
+def kv_page_bytes(page_tokens: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of one page."""
+    _counts(page_tokens, kv_heads, head_dim)
+    n = lib().clover_kv_page_bytes(page_tokens, kv_heads, head_dim)
+    if n == 0:
+        raise CloverError(ERR_UNSUPPORTED_SHAPE, last_error())
+    return n
+
+
+def _heads_of(name: str, t, heads, dim: int, kinds, dev: int):
+    """The library's view of rows [rows][heads][dim] of one of these types, the last dimension contiguous (heads None: any
+    number)."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or t.dtype not in kinds or shape[2] != dim or (heads is not None and shape[1] != heads) \
+            or t.get_device() != dev or strides[2] != 1:
+        _refuse(f"{name}: need {' or '.join(map(str, kinds))} [rows][{'heads' if heads is None else heads}][{dim}] on "
+                f"cuda:{dev} with a contiguous last dimension, got {t.dtype} {tuple(shape)} on {t.device}, strides {strides}")
+    if shape[0] > 1 << 29 or shape[1] > 1 << 20:
+        raise CloverError(ERR_UNSUPPORTED_SHAPE, f"{name}: {tuple(shape)} is past 2^29 rows or 2^20 heads")
+    return Rows(t.data_ptr(), strides[0], strides[1])
+
+
+def _kv_seqs(cache, offsets, lens, table, dev: int):
+    if table.dim() != 2 or table.shape[1] > 1 << 24:
+        _refuse(f"table: need [sequences][pages], got {tuple(table.shape)}")
+    n, pages = shape = table.shape
+    return KvSeqs(_tensor("offsets", offsets, _I32, (n + 1,), dev), _tensor("lens", lens, _I32, (n,), dev),
+                  _tensor("table", table, _I32, shape, dev), n, pages)
+
+
+def kv_write(cache: KvCache, k, v, offsets, lens, table, stream=None):
+    """Quantises rows of keys and values (fp32 or bf16 [rows][kv_heads][head_dim], rows and heads may be strided) into the
+    cache. Rows offsets[s] .. offsets[s + 1] - 1 (int32 [sequences + 1]) are the last positions of sequence s, whose length
+    with them is lens[s] (int32 [sequences]); table int32 [sequences][pages] lists its pages."""
+    if stream is not None:
+        with _as_current(stream, cache):
+            return kv_write(cache, k, v, offsets, lens, table)
+    dev = _on_current("cache", cache._pages)
+    heads, dim = cache._args.kv_heads, cache._args.head_dim
+    seqs, kinds = _kv_seqs(cache, offsets, lens, table, dev), (_F32, _BF16)
+    rk, rv = _heads_of("k", k, heads, dim, kinds, dev), _heads_of("v", v, heads, dim, kinds, dev)
+    if k.dtype is not v.dtype or k.shape[0] != v.shape[0]:
+        _refuse(f"k ({k.dtype} {tuple(k.shape)}) does not match v ({v.dtype} {tuple(v.shape)})")
+    rc = lib().clover_kv_write(cache._args, seqs, rk, rv, _TYPES[k.dtype], k.shape[0], _current_stream(dev))
+    if rc != OK:
+        _check(rc)
+
+
+def kv_read(cache: KvCache, offsets, lens, table, rows: int, out=None, stream=None):
+    """What the cache holds at the positions of `rows` rows (offsets, lens and table as for `kv_write`; a whole sequence
+    where it has lens[s] rows): keys and values, bf16 [rows][kv_heads][head_dim] each. Rows behind the last sequence are left
+    as they were. `out` (a pair this function returned before, for as many rows) is reused."""
+    if stream is not None:
+        with _as_current(stream, cache):
+            return kv_read(cache, offsets, lens, table, rows, out)
+    dev = _on_current("cache", cache._pages)
+    _counts(rows)
+    shape = (rows, cache._args.kv_heads, cache._args.head_dim)
+    if rows < 0:
+        _refuse(f"rows={rows} is negative")
+    seqs = _kv_seqs(cache, offsets, lens, table, dev)
+    if out is None:
+        out = tuple(torch.empty(shape, dtype=_BF16, device=cache._device) for _ in range(2))
+    rc = lib().clover_kv_read(cache._args, seqs, _tensor("out[0]", out[0], _BF16, shape, dev),
+                              _tensor("out[1]", out[1], _BF16, shape, dev), rows, _current_stream(dev))
+    if rc != OK:
+        _check(rc)
+    return out
+
+
+def kv_attention_workspace_bytes(cache: KvCache, rows: int, q_heads: int, n_seqs: int, max_pages: int) -> int:
+    """Bytes of workspace `kv_attention` needs for up to `rows` rows of n_seqs sequences with a table of max_pages."""
+    _counts(rows, q_heads, n_seqs, max_pages)
+    return lib().clover_kv_attention_workspace_bytes(cache._args, rows, q_heads, n_seqs, max_pages)
+
+
+def _attention_out(out, lse, shape, dev: int, device):
+    """(out, its pointer, lse or None, its pointer): lse False, True or a tensor to fill."""
+    if out is None:
+        out = torch.empty(shape, dtype=_BF16, device=device)
+        p_out = out.data_ptr()
+    else:
+        p_out = _tensor("out", out, _BF16, shape, dev)
+    if lse is False:
+        return out, p_out, None, None
+    if lse is True:
+        lse = torch.empty(shape[:2], dtype=_F32, device=device)
+        return out, p_out, lse, lse.data_ptr()
+    return out, p_out, lse, _tensor("lse", lse, _F32, shape[:2], dev)
+
+
+def kv_attention(q, cache: KvCache, offsets, lens, table, block: int = 1, scale: float | None = None, lse=False, ws=None,
+                 out=None, stream=None):
+    """Attention of queries (bf16 [rows][q_heads][head_dim], rows and heads may be strided) over the cache: bf16
+    [rows][q_heads][head_dim]. offsets, lens and table as for `kv_write`, which writes the rows' own keys and values first.
+    The query at position p of a sequence sees positions below (p // block + 1) * block (1: causal; 0: all of them). scale:
+    of the scores, head_dim ** -0.5 by default. With lse (True, or fp32 [rows][q_heads] to fill) the result is a pair with
+    the logarithms of the softmax's sums; a query that sees nothing has 0 and -inf."""
+    if stream is not None:
+        with _as_current(stream, cache):
+            return kv_attention(q, cache, offsets, lens, table, block, scale, lse, ws, out)
+    dev, dim = _on_current("cache", cache._pages), cache._args.head_dim
+    rq = _heads_of("q", q, None, dim, (_BF16,), dev)
+    seqs = _kv_seqs(cache, offsets, lens, table, dev)
+    shape = q.shape
+    _counts(block)
+    if ws is None:
+        ws = workspace(kv_attention_workspace_bytes(cache, shape[0], shape[1], *table.shape), q.device)
+    out, p_out, lse, p_lse = _attention_out(out, lse, shape, dev, q.device)
+    rc = lib().clover_kv_attention(cache._args, seqs, rq, shape[0], shape[1], dim ** -0.5 if scale is None else scale, block,
+                                   p_out, p_lse, *_scratch(ws, dev), _current_stream(dev))
+    if rc != OK:
+        _check(rc)
+    return out if lse is None else (out, lse)
+
+
+def prompt_attention_workspace_bytes(rows: int, keys: int, n_seqs: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace `prompt_attention` needs for up to `rows` rows and `keys` keys of n_seqs sequences."""
+    _counts(rows, keys, n_seqs, q_heads, kv_heads, head_dim)
+    return lib().clover_prompt_attention_workspace_bytes(rows, keys, n_seqs, q_heads, kv_heads, head_dim)
+
+
+def prompt_attention(q, k, v, offsets, k_offsets=None, block: int = 1, scale: float | None = None, lse=False, ws=None,
+                     out=None, stream=None):
+    """Attention over packed prompts: q bf16 [rows][q_heads][head_dim], k and v bf16 [keys][kv_heads][head_dim] (rows and
+    heads may be strided) -> bf16 [rows][q_heads][head_dim]. Rows offsets[s] .. offsets[s + 1] - 1 (int32 [sequences + 1])
+    are the last positions of sequence s, whose keys are rows k_offsets[s] .. k_offsets[s + 1] - 1 of k and v (by default
+    the same rows: every position has a query). block, scale and lse as for `kv_attention`."""
+    if stream is not None:
+        with _as_current(stream, q):
+            return prompt_attention(q, k, v, offsets, k_offsets, block, scale, lse, ws, out)
+    dev, shape = _on_current("q", q), q.shape
+    if len(shape) != 3:
+        _refuse(f"q: need [rows][heads][head_dim], got {tuple(shape)}")
+    rq = _heads_of("q", q, None, shape[2], (_BF16,), dev)
+    rk, rv = _heads_of("k", k, None, shape[2], (_BF16,), dev), _heads_of("v", v, k.shape[1], shape[2], (_BF16,), dev)
+    if k.shape[0] != v.shape[0]:
+        _refuse(f"k has {k.shape[0]} rows, v {v.shape[0]}")
+    n = _length("offsets", offsets) - 1
+    p_off = _tensor("offsets", offsets, _I32, (n + 1,), dev)
+    p_k = p_off if k_offsets is None else _tensor("k_offsets", k_offsets, _I32, (n + 1,), dev)
+    _counts(block)
+    if ws is None:
+        ws = workspace(prompt_attention_workspace_bytes(shape[0], k.shape[0], n, shape[1], k.shape[1], shape[2]), q.device)
+    out, p_out, lse, p_lse = _attention_out(out, lse, shape, dev, q.device)
+    rc = lib().clover_prompt_attention(PromptSeqs(p_off, p_k, n), rq, rk, rv, shape[0], k.shape[0], shape[1], k.shape[1],
+                                       shape[2], shape[2] ** -0.5 if scale is None else scale, block, p_out, p_lse,
+                                       *_scratch(ws, dev), _current_stream(dev))
+    if rc != OK:
+        _check(rc)
+    return out if lse is None else (out, lse)

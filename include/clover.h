@@ -458,6 +458,128 @@ int clover_moe_combine(const uint16_t* y, int32_t n_rows, const int32_t* pos, co
                        const uint16_t* shared, const float* x, float* x_out, int32_t M, int32_t K, int32_t H,
                        clover_stream_t stream);
 
+/* ---- Attention ------------------------------------------------------------
+ * Softmax attention with grouped heads (query head h reads key/value head
+ * h / (q_heads / kv_heads)), over a paged 4-bit cache or over a packed prompt.
+ * The conventions at the top of this file hold, with the limits stated here:
+ * head_dim 64 or 128; 1 <= kv_heads <= 256, 1 to 64 query heads to each; 1 to
+ * 1,024 sequences; up to 2^24 rows and positions in any one call. A call with
+ * no rows is valid and needs no data pointers. None of the calls changes its
+ * inputs.
+ *
+ * Sequences. Rows offsets[s] .. offsets[s + 1] - 1 of a call (offsets int32
+ * [n_seqs + 1] on the device, ascending from 0) belong to sequence s, whose
+ * length is len: they are its LAST positions, row offsets[s] + i position
+ * p = len - n + i of n rows. Offsets outside [0, rows] count as the nearer end.
+ * Rows from offsets[n_seqs] on belong to no sequence: nothing of them is read
+ * or written.
+ *
+ * Visibility. The query at position p sees positions below
+ *   block 0:      len                    (all of them)
+ *   block n >= 1: min(len, (p / n + 1) n)  (its own block of n and what lies
+ *                 before; 1: causal; 32: block-causal), none if p < 0
+ * With z_j = scale * q . k_j over the positions it sees (scale finite, > 0):
+ *   out = bf16(sum_j softmax(z)_j v_j),  lse = ln sum_j e^z_j
+ * A query that sees nothing, or whose z are all -inf, gets out 0 and lse -inf.
+ * Scores, softmax statistics and sums are fp32; the softmax's numerators are
+ * rounded to the products' 16-bit type. What a query does not see does not
+ * change its results, whatever it holds. */
+
+/* Strided rows of heads (bf16 unless a call says otherwise): row i, head h at
+ * element i * row_stride + h * head_stride, head_dim contiguous elements. data
+ * and the strides in bytes are multiples of 16; a stride is at least head_dim
+ * where there is more than one row (head), at most 2^36 elements. */
+typedef struct {
+    const void* data;
+    int64_t row_stride;
+    int64_t head_stride;
+} clover_rows;
+
+/* A paged cache of keys and values in the CLOVER_FP4_NV format (e2m1 codes, an
+ * e4m3 scale for 16 elements). pages: uint8
+ * [n_pages][kv_heads][page_tokens / 16][18 head_dim], 16-byte aligned: the
+ * tokens of a page in sixteens, each 16 rows of key codes (head_dim / 2 bytes,
+ * the even element in the low nibble), 16 rows of key scales (head_dim / 16
+ * bytes), and the same of the values. Keys stand for code * scale * 2^k_exp,
+ * values for code * scale * 2^v_exp. page_tokens: a multiple of 16, 16 to
+ * 65,536; 1 <= n_pages; |k_exp|, |v_exp| <= 64. */
+typedef struct {
+    uint8_t* pages;
+    int32_t n_pages;
+    int32_t page_tokens;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t k_exp;
+    int32_t v_exp;
+} clover_kv_cache;
+
+/* Sequences of a cache: offsets as above, lens int32 [n_seqs] their lengths
+ * INCLUDING the call's rows (below 0 counts as 0, past the table's
+ * max_pages * page_tokens, which may not exceed 2^24, as that), table int32
+ * [n_seqs][max_pages] the page of positions j * page_tokens and on. All on the
+ * device. A page id outside [0, n_pages) stands for no page: nothing is
+ * written to it, its positions read as zeros and no query sees them. */
+typedef struct {
+    const int32_t* offsets;
+    const int32_t* lens;
+    const int32_t* table;
+    int32_t n_seqs;
+    int32_t max_pages;
+} clover_kv_seqs;
+
+/* Bytes of one page. Returns 0 for an unsupported shape. Host-only. */
+size_t clover_kv_page_bytes(int32_t page_tokens, int32_t kv_heads, int32_t head_dim);
+
+/* Quantises rows of keys and values (type fp32 or bf16) into the cache, at the
+ * positions the rows have. Codes and scales as clover_quantize_fp4 (NV) gives
+ * them with scale_exp k_exp or v_exp; a block of 16 with a NaN or an infinity
+ * becomes NaN. Rows at negative positions are left out. Two rows of a call must
+ * not have the same place (a page listed twice). */
+int clover_kv_write(const clover_kv_cache* cache, const clover_kv_seqs* seqs, const clover_rows* k, const clover_rows* v,
+                    int32_t type, int32_t n_rows, clover_stream_t stream);
+
+/* The other way: k_out, v_out bf16 [n_rows][kv_heads][head_dim] receive what
+ * the positions of the rows stand for (exact unless it leaves bf16's range),
+ * zeros at negative positions. With n = len, a whole sequence. */
+int clover_kv_read(const clover_kv_cache* cache, const clover_kv_seqs* seqs, uint16_t* k_out, uint16_t* v_out,
+                   int32_t n_rows, clover_stream_t stream);
+
+/* Bytes of workspace clover_kv_attention needs for up to n_rows rows of n_seqs
+ * sequences with a table of max_pages (no data pointer is looked at). Returns 0
+ * for an unsupported shape. Host-only. */
+size_t clover_kv_attention_workspace_bytes(const clover_kv_cache* cache, int32_t n_rows, int32_t q_heads,
+                                           int32_t n_seqs, int32_t max_pages);
+
+/* Attention of n_rows query rows over the cache (the rows' own keys and values
+ * among it: write them first). q: bf16. out: bf16
+ * [n_rows][q_heads][head_dim], 16-byte aligned. lse: fp32 [n_rows][q_heads] or
+ * NULL. */
+int clover_kv_attention(const clover_kv_cache* cache, const clover_kv_seqs* seqs, const clover_rows* q, int32_t n_rows,
+                        int32_t q_heads, float scale, int32_t block, uint16_t* out, float* lse, void* workspace,
+                        size_t workspace_bytes, clover_stream_t stream);
+
+/* Packed prompts: query rows by offsets, keys and values by k_offsets (int32
+ * [n_seqs + 1]; a sequence's len is its number of keys; the same array as
+ * offsets where every position has a query). */
+typedef struct {
+    const int32_t* offsets;
+    const int32_t* k_offsets;
+    int32_t n_seqs;
+} clover_prompt_seqs;
+
+/* Bytes of workspace clover_prompt_attention needs for up to n_rows rows and
+ * n_keys keys of n_seqs sequences. Returns 0 for an unsupported shape.
+ * Host-only. */
+size_t clover_prompt_attention_workspace_bytes(int32_t n_rows, int32_t n_keys, int32_t n_seqs, int32_t q_heads,
+                                               int32_t kv_heads, int32_t head_dim);
+
+/* Attention of n_rows query rows over n_keys key/value rows, bf16. out and lse
+ * as in clover_kv_attention. */
+int clover_prompt_attention(const clover_prompt_seqs* seqs, const clover_rows* q, const clover_rows* k,
+                            const clover_rows* v, int32_t n_rows, int32_t n_keys, int32_t q_heads, int32_t kv_heads,
+                            int32_t head_dim, float scale, int32_t block, uint16_t* out, float* lse, void* workspace,
+                            size_t workspace_bytes, clover_stream_t stream);
+
 /* Library version as major*10000 + minor*100 + patch. */
 int32_t clover_version(void);
 
