@@ -897,6 +897,15 @@ int encode_byte_boxes(void* tensor_map, const void* base, uint64_t n, uint64_t r
                    strides, box, codes ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, what);
 }
 
+int encode_head_boxes(void* tensor_map, const void* base, uint64_t rows, uint64_t heads, uint64_t dim, uint64_t row_stride,
+                      uint64_t head_stride, uint32_t box_heads, uint32_t box_rows, const char* what) {
+  int rc;
+  if ((rc = get_encoder())) return rc;
+  const cuuint64_t dims[3] = {dim, heads, rows}, strides[2] = {head_stride, row_stride};
+  const cuuint32_t box[3] = {64, box_heads, box_rows};
+  return encode_bf16_nd(static_cast<CUtensorMap*>(tensor_map), base, 3, dims, strides, box, what);
+}
+
 int device_sms(int* sms) {
   DevInfo di;
   const int rc = device_info(&di);

@@ -1,5 +1,6 @@
 // Host side of the attention operations declared in include/clover.h: argument
 // checks, workspace layout and kernel launches.
+#include <float.h>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -142,7 +143,12 @@ void fill_cache(const clover_kv_cache& c, const clover_kv_seqs& s, int32_t n_row
   ks->n_keys = s.max_pages * c.page_tokens;
 }
 
-constexpr double kLog2E = 1.4426950408889634;
+// The factor that takes q . k to the exponent of 2: kept a positive finite number
+// where it would leave fp32's range.
+float exponent_scale(float scale, float k_mul) {
+  const double c = static_cast<double>(scale) * k_mul * 1.4426950408889634;
+  return c > FLT_MAX ? FLT_MAX : (c < FLT_TRUE_MIN ? FLT_TRUE_MIN : static_cast<float>(c));
+}
 
 size_t cached_bytes(const clover_kv_cache& c, int32_t n_rows, int32_t q_heads, int32_t n_seqs, int32_t max_pages) {
   return kCtrlBytes;
@@ -224,7 +230,7 @@ int clover_kv_attention(const clover_kv_cache* cache, const clover_kv_seqs* seqs
   a.q_heads = q_heads;
   a.group = q_heads / cache->kv_heads;
   a.block = block;
-  a.scale_log2 = static_cast<float>(scale * kLog2E * a.c.k_mul);
+  a.scale_log2 = exponent_scale(scale, a.c.k_mul);
   a.out = reinterpret_cast<__nv_bfloat16*>(out);
   a.lse = lse;
   a.err = static_cast<int*>(workspace);
@@ -268,11 +274,23 @@ int clover_prompt_attention(const clover_prompt_seqs* seqs, const clover_rows* q
   a.q_heads = q_heads;
   a.group = q_heads / kv_heads;
   a.block = block;
-  a.scale_log2 = static_cast<float>(scale * kLog2E);
+  a.scale_log2 = exponent_scale(scale, 1.f);
   a.out = reinterpret_cast<__nv_bfloat16*>(out);
   a.lse = lse;
   a.err = static_cast<int*>(workspace);
-  return launched(launch_attention_simple(a, false, reinterpret_cast<cudaStream_t>(stream)), "launch prompt attention");
+  AttendArgs t;
+  memset(&t, 0, sizeof(t));
+  t.a = a;
+  t.tokens = 128 / a.group;
+  t.n_slots = n_rows / (2 * t.tokens) + seqs->n_seqs;
+  if ((rc = encode_head_boxes(&t.tm_q, a.q.data, n_rows, q_heads, head_dim, a.q.row, a.q.head, a.group, t.tokens, "q")))
+    return rc;
+  t.tm_k = t.tm_v = t.tm_q;  // without keys nothing is loaded through them
+  if (n_keys > 0 &&
+      ((rc = encode_head_boxes(&t.tm_k, a.k.data, n_keys, kv_heads, head_dim, a.k.row, a.k.head, 1, 128, "k")) ||
+      (rc = encode_head_boxes(&t.tm_v, a.v.data, n_keys, kv_heads, head_dim, a.v.row, a.v.head, 1, 128, "v"))))
+    return rc;
+  return launched(launch_attend(t, reinterpret_cast<cudaStream_t>(stream)), "launch prompt attention");
 }
 
 }  // extern "C"

@@ -56,10 +56,25 @@ struct AttnArgs {
   float scale_log2;  // scale * log2(e) * 2^k_exp
   __nv_bfloat16* out;
   float* lse;  // or null
+  int wide_out;  // set by the launch: 32-byte stores to out are aligned
   int* err;
 };
 
 cudaError_t launch_attention_simple(const AttnArgs& a, bool cached, cudaStream_t s);
+
+// Attention on tensor-core tiles (csrc/attend.cu). A tile is 128 rows: the
+// group's query heads of `tokens` = 128 / group consecutive tokens, row
+// token * group + head.
+struct AttendArgs {
+  CUtensorMap tm_q;  // q [n_rows][q_heads][dim], boxes of 64 elements x group x tokens
+  CUtensorMap tm_k;  // k [n_keys][heads][dim], boxes of 64 elements x 1 x 128
+  CUtensorMap tm_v;
+  AttnArgs a;
+  int tokens;
+  int n_slots;       // pairs of tiles: n_rows / (2 tokens) + the number of sequences
+};
+
+cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s);
 
 // ------------------------------------------------------------ device helpers
 

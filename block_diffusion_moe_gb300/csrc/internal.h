@@ -23,6 +23,12 @@ int check_workspace(void* workspace, size_t have, size_t need);
 int encode_byte_boxes(void* tensor_map, const void* base, uint64_t n, uint64_t rows, uint64_t row_bytes,
                       uint32_t box_bytes, uint32_t box_rows, uint32_t box_n, bool codes, const char* what);
 
+// Encodes the TMA view of strided bf16 rows [rows][heads][dim] (strides in
+// bytes): boxes of 64 elements x box_heads x box_rows in the 128-byte swizzle,
+// zeros outside.
+int encode_head_boxes(void* tensor_map, const void* base, uint64_t rows, uint64_t heads, uint64_t dim, uint64_t row_stride,
+                      uint64_t head_stride, uint32_t box_heads, uint32_t box_rows, const char* what);
+
 // Number of SMs of the current device.
 int device_sms(int* sms);
 

@@ -445,6 +445,60 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Loads 32 consecutive columns without waiting; tmem_wait_ld orders the uses of
+// what was loaded behind the wait.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+template <int kArrays>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[kArrays][32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int a = 0; a < kArrays; ++a)
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[a][i]));
+}
+
+// Shared-memory matrix descriptor for an MN-major operand tile in the layout a
+// TMA load with 128-byte swizzle writes it: slabs of 64 bf16 along M/N (128-byte
+// rows, one per K), `slab_bytes` apart, groups of 8 K rows 1,024 bytes apart.
+// Advancing along K by 16 adds 2,048 bytes (128 in the encoded field).
+__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t saddr, uint32_t slab_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);     // start address
+  d |= static_cast<uint64_t>(slab_bytes >> 4) << 16;       // leading byte offset: next 64 along M/N
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;             // stride byte offset: next 8 along K
+  d |= static_cast<uint64_t>(1) << 46;                     // descriptor version
+  d |= static_cast<uint64_t>(2) << 61;                     // 128-byte swizzle
+  return d;
+}
+
+// Bit of the instruction descriptor: B is MN-major.
+constexpr uint32_t kUmmaBMnMajor = 1u << 16;
+
+// A larger or smaller share of the registers the CTA was launched with, per
+// thread, for a whole warpgroup.
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// 2^x (-inf: 0, NaN: NaN; denormal results are 0).
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // ------------------------------------------------- dependent launch / misc
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
