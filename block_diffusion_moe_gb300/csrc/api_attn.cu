@@ -150,8 +150,17 @@ float exponent_scale(float scale, float k_mul) {
   return c > FLT_MAX ? FLT_MAX : (c < FLT_TRUE_MIN ? FLT_TRUE_MIN : static_cast<float>(c));
 }
 
+// Workspace of the kernel for few rows, behind the control block: arrival
+// counters, then maxima and sums of weights, then sums, of two parts per CTA.
+constexpr size_t kFewArrived = (plan::kAttendFewCtas * 4 + 255) / 256 * 256;
+constexpr size_t kFewMl = 2 * plan::kAttendFewCtas * kFewRows * 8;
+
+size_t few_bytes(int32_t head_dim) {
+  return kFewArrived + kFewMl + static_cast<size_t>(2) * plan::kAttendFewCtas * kFewRows * head_dim * 4;
+}
+
 size_t cached_bytes(const clover_kv_cache& c, int32_t n_rows, int32_t q_heads, int32_t n_seqs, int32_t max_pages) {
-  return kCtrlBytes;
+  return kCtrlBytes + few_bytes(c.head_dim);
 }
 
 size_t prompt_bytes(int32_t n_rows, int32_t n_keys, int32_t n_seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
@@ -234,6 +243,20 @@ int clover_kv_attention(const clover_kv_cache* cache, const clover_kv_seqs* seqs
   a.out = reinterpret_cast<__nv_bfloat16*>(out);
   a.lse = lse;
   a.err = static_cast<int*>(workspace);
+  if (plan::attend_few(n_rows, a.group, seqs->n_seqs)) {
+    int sms = 0;
+    if ((rc = device_sms(&sms))) return rc;
+    AttendFewArgs f;
+    f.a = a;
+    f.tokens = kFewRows / a.group;
+    uint8_t* at = static_cast<uint8_t*>(workspace) + kCtrlBytes;
+    f.arrived = reinterpret_cast<uint32_t*>(at);
+    f.part_ml = reinterpret_cast<float2*>(at + kFewArrived);
+    f.part = reinterpret_cast<float*>(at + kFewArrived + kFewMl);
+    return launched(launch_attend_few(f, sms < plan::kAttendFewCtas ? sms : plan::kAttendFewCtas,
+                                      reinterpret_cast<cudaStream_t>(stream)),
+                    "launch kv attention");
+  }
   return launched(launch_attention_simple(a, true, reinterpret_cast<cudaStream_t>(stream)), "launch kv attention");
 }
 

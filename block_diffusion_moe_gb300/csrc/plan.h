@@ -87,5 +87,10 @@ inline RouteShape route_shape(int tokens) {
   return s;
 }
 
+// Attention over a cache: CTAs of the kernel for few rows, and whether it takes a
+// call: sequences of at most 16 rows (tokens x heads of a group) on average.
+constexpr int kAttendFewCtas = 152;
+inline bool attend_few(long long rows, int group, int seqs) { return group <= 16 && rows * group <= 16LL * seqs; }
+
 }  // namespace plan
 }  // namespace clover

@@ -117,12 +117,12 @@ def limit(p, length, block):
 
 
 def attend(q, k, v, there, block, scale):
-    """q [n][Hq][D], the last n positions of k, v [L][H][D] (fp64) -> out, lse, and per result the sum of p |v| and the
-    largest sum of |q k| scale of a visible position, which errors are measured by."""
+    """q [n][Hq][D], the last n positions of k, v [L][H][D] (fp64) -> out, lse, and what errors are measured by: per result
+    the sum of p |v|, the largest sum of |q k| scale of a visible position, and the sum of |v|."""
     n, Hq, D = q.shape
     L, H, _ = k.shape
     out, lse = np.zeros((n, Hq, D)), np.full((n, Hq), -np.inf)
-    mag, size = np.zeros((n, Hq, D)), np.zeros((n, Hq))
+    mag, size, total = np.zeros((n, Hq, D)), np.zeros((n, Hq)), np.zeros((n, Hq, D))
     for i in range(n):
         lim = limit(L - n + i, L, block)
         see = np.nonzero(there[:lim])[0]
@@ -140,13 +140,15 @@ def attend(q, k, v, there, block, scale):
                 mag[i, h] = (e / e.sum()) @ np.abs(vv)
                 lse[i, h] = m + np.log(e.sum())
                 size[i, h] = scale * (np.abs(kk) @ np.abs(q[i, h])).max()
-    return out, lse, mag, size
+                total[i, h] = np.abs(vv).sum(0)
+    return out, lse, mag, size, total
 
 
 def kv_attention(q, pages, offsets, lens, table, block, scale, k_exp=0, v_exp=0):
     """Results of every row (rows of no sequence: NaN), as `attend` gives them."""
     n, Hq, D = q.shape
-    res = [np.full((n, Hq, D), np.nan), np.full((n, Hq), np.nan), np.zeros((n, Hq, D)), np.zeros((n, Hq))]
+    res = [np.full((n, Hq, D), np.nan), np.full((n, Hq), np.nan), np.zeros((n, Hq, D)), np.zeros((n, Hq)),
+           np.zeros((n, Hq, D))]
     off = np.clip(offsets, 0, n)
     cap = table.shape[1] * 16 * pages.shape[2]
     for s in range(len(off) - 1):
@@ -159,7 +161,8 @@ def kv_attention(q, pages, offsets, lens, table, block, scale, k_exp=0, v_exp=0)
 
 def prompt_attention(q, k, v, offsets, k_offsets, block, scale):
     n, Hq, D = q.shape
-    res = [np.full((n, Hq, D), np.nan), np.full((n, Hq), np.nan), np.zeros((n, Hq, D)), np.zeros((n, Hq))]
+    res = [np.full((n, Hq, D), np.nan), np.full((n, Hq), np.nan), np.zeros((n, Hq, D)), np.zeros((n, Hq)),
+           np.zeros((n, Hq, D))]
     off, koff = np.clip(offsets, 0, n), np.clip(k_offsets, 0, len(k))
     for s in range(len(off) - 1):
         r, c = slice(off[s], off[s + 1]), slice(koff[s], koff[s + 1])

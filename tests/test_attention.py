@@ -231,11 +231,11 @@ def test_oracle_attention_by_hand():
     q = np.zeros((2, 2, 64))
     k, v = np.zeros((3, 1, 64)), np.zeros((3, 1, 64))
     v[:, 0, 0] = [1.0, 2.0, 6.0]
-    out, lse, _, _ = R.attend(q, k, v, np.ones(3, dtype=bool), 1, 1.0)
+    out, lse, *_ = R.attend(q, k, v, np.ones(3, dtype=bool), 1, 1.0)
     assert np.allclose(out[:, :, 0], [[1.5, 1.5], [3.0, 3.0]]) and np.allclose(np.exp(lse), [[2, 2], [3, 3]])
-    out, _, _, _ = R.attend(q, k, v, np.array([True, False, True]), 0, 1.0)
+    out, *_ = R.attend(q, k, v, np.array([True, False, True]), 0, 1.0)
     assert np.allclose(out[:, :, 0], 3.5)
-    out, lse, _, _ = R.attend(np.zeros((5, 2, 64)), k, v, np.ones(3, dtype=bool), 2, 1.0)
+    out, lse, *_ = R.attend(np.zeros((5, 2, 64)), k, v, np.ones(3, dtype=bool), 2, 1.0)
     assert (out[:2] == 0).all() and (lse[:2] == -np.inf).all()  # before the first position
     assert np.allclose(out[2:, 0, 0], [1.5, 1.5, 3.0])
 
