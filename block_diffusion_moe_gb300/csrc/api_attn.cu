@@ -6,6 +6,8 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "../../include/clover.h"
 #include "attn_ops.cuh"
 #include "internal.h"
@@ -150,17 +152,30 @@ float exponent_scale(float scale, float k_mul) {
   return c > FLT_MAX ? FLT_MAX : (c < FLT_TRUE_MIN ? FLT_TRUE_MIN : static_cast<float>(c));
 }
 
-// Workspace of the kernel for few rows, behind the control block: arrival
-// counters, then maxima and sums of weights, then sums, of two parts per CTA.
-constexpr size_t kFewArrived = (plan::kAttendFewCtas * 4 + 255) / 256 * 256;
-constexpr size_t kFewMl = 2 * plan::kAttendFewCtas * kFewRows * 8;
+// Workspace of the kernel for few rows, behind the control block.
+struct FewLayout {
+  size_t arrived, ml, part, bytes;
+};
 
-size_t few_bytes(int32_t head_dim) {
-  return kFewArrived + kFewMl + static_cast<size_t>(2) * plan::kAttendFewCtas * kFewRows * head_dim * 4;
+FewLayout few_layout(int32_t rows, bool alone, int32_t head_dim) {
+  const size_t pieces = plan::attend_few_pieces(rows, alone);
+  FewLayout l;
+  l.arrived = kCtrlBytes;
+  l.ml = l.arrived + (pieces * 4 + 255) / 256 * 256;
+  l.part = l.ml + 2 * pieces * kFewRows * 8;
+  l.bytes = l.part + 2 * pieces * (alone ? rows : kFewRows) * head_dim * 4;
+  return l;
 }
 
+// (for up to n_rows rows: calls of fewer may take tiles of 8 rows instead of 16)
 size_t cached_bytes(const clover_kv_cache& c, int32_t n_rows, int32_t q_heads, int32_t n_seqs, int32_t max_pages) {
-  return kCtrlBytes + few_bytes(c.head_dim);
+  const int group = q_heads / c.kv_heads;
+  const bool alone = plan::attend_few_alone(n_seqs, c.kv_heads);
+  size_t most = kCtrlBytes;
+  if (group <= 8) most = std::max(most, few_layout(8, alone, c.head_dim).bytes);
+  if (group <= 16 && plan::attend_few_rows(n_rows, group, n_seqs) == 16)
+    most = std::max(most, few_layout(16, alone, c.head_dim).bytes);
+  return most;
 }
 
 size_t prompt_bytes(int32_t n_rows, int32_t n_keys, int32_t n_seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
@@ -248,12 +263,15 @@ int clover_kv_attention(const clover_kv_cache* cache, const clover_kv_seqs* seqs
     if ((rc = device_sms(&sms))) return rc;
     AttendFewArgs f;
     f.a = a;
-    f.tokens = kFewRows / a.group;
-    uint8_t* at = static_cast<uint8_t*>(workspace) + kCtrlBytes;
-    f.arrived = reinterpret_cast<uint32_t*>(at);
-    f.part_ml = reinterpret_cast<float2*>(at + kFewArrived);
-    f.part = reinterpret_cast<float*>(at + kFewArrived + kFewMl);
-    return launched(launch_attend_few(f, sms < plan::kAttendFewCtas ? sms : plan::kAttendFewCtas,
+    const int rows = plan::attend_few_rows(n_rows, a.group, seqs->n_seqs);
+    const bool alone = plan::attend_few_alone(seqs->n_seqs, cache->kv_heads);
+    const FewLayout l = few_layout(rows, alone, cache->head_dim);
+    uint8_t* at = static_cast<uint8_t*>(workspace);
+    f.tokens = rows / a.group;
+    f.arrived = reinterpret_cast<uint32_t*>(at + l.arrived);
+    f.part_ml = reinterpret_cast<float2*>(at + l.ml);
+    f.part = reinterpret_cast<float*>(at + l.part);
+    return launched(launch_attend_few(f, sms < plan::kAttendSms ? sms : plan::kAttendSms, alone,
                                       reinterpret_cast<cudaStream_t>(stream)),
                     "launch kv attention");
   }

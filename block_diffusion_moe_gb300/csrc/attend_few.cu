@@ -1,20 +1,24 @@
 // Attention of few query rows over the paged 4-bit cache (clover_kv_attention of
 // single tokens and short runs).
 //
-// A tile is up to 16 rows: the group's query heads of one or more tokens. Each
+// A tile is up to 8 or 16 rows: the group's query heads of one or more tokens. Each
 // warp expands codes to fp16 in registers (exact: e2m1 times e4m3 has 6
 // significant bits and stays below 2^12) and multiplies with mma.sync m16n8k16,
-// whose 16 rows the few queries half fill: the tensor core is not what bounds
-// this, and no operand passes through shared memory a second time. Queries are
-// scaled to fp16 by a power of two per row (the largest element to 2^14, so that
+// keys and values on its side of 16 and queries on that of 8: the tensor core is
+// not what bounds this, and no operand passes through shared memory a second time.
+// Scores come out transposed (a lane holds keys g and g + 8 of rows 2t and 2t + 1),
+// and so do the sums; movmatrix turns the numerators between. Queries are scaled to fp16 by a power of two per row (the largest element to 2^14, so that
 // what falls below fp16's range is 2^-38 of it).
 //
-// The call's work is one line of units of 384 keys of one tile (32 for each of 12
-// warps); every CTA takes an equal piece of it, whatever the lengths are. A
-// piece that begins or ends inside a tile leaves its sums in the workspace; the
-// last CTA to finish with a tile adds them up, in the order of the keys. Each warp
-// streams its own keys through its own ring (one copy per 16 tokens, of codes and
-// scales together), on past the ends of tiles.
+// The call's work is one line of units of keys of one tile; every team of warps
+// takes an equal piece of it, whatever the lengths are. A team is one warp (units of
+// 32 keys) where there are many tiles: nothing waits for another warp. Few tiles
+// would then be in too many pieces, so a team is all warps of an SM (32 keys of a
+// unit each), whose sums meet in shared memory. A piece that begins or ends inside a
+// tile leaves its sums in the workspace; the last team to finish with a tile adds
+// them up, in the order of the keys. Each warp streams its own keys through its own
+// ring (one copy per 16 tokens, of codes and scales together), on past the ends of
+// tiles.
 #include <math.h>
 
 #include "attn_ops.cuh"
@@ -25,36 +29,37 @@ namespace clover {
 
 namespace {
 
-constexpr int kWarps = 12;
-constexpr int kThreads = kWarps * 32;
 constexpr int kWarpKeys = 32;  // of a unit: two sixteens
-constexpr int kUnit = kWarps * kWarpKeys;
+// Warps on an SM: what registers allow.
+constexpr int few_warps(int cols) { return cols == 1 ? 16 : 12; }
 // Numerators are 2^(c S - m + 11), m the row's maximum or up to 2^4 below it: at most
 // 2^15, and what fp16 cannot tell from 0 or rounds by more than half a step is
 // 2^-36 of the largest.
 constexpr float kGrowth = 4.f, kLift = 11.f;
 
-template <int kDim>
+// kCols: groups of 8 rows.
+template <int kDim, int kCols>
 struct Layout {
   static constexpr int kSixteen = 18 * kDim;  // bytes: key codes, key scales, value codes, value scales
   static constexpr int kKs = 8 * kDim, kV = 9 * kDim, kVs = 17 * kDim;
   static constexpr int kStage = 2 * kSixteen;
-  static constexpr int kStages = kDim == 128 ? 3 : 6;
-  static constexpr int kFrag = kDim / 2;  // accumulator registers of a lane
-  static constexpr int kPitch = kDim + 4;  // of a row of sums in shared memory: element d at d + d / (kDim / 4)
+  static constexpr int kStages = (kCols == 1 ? 2 : 3) * (128 / kDim);
+  static constexpr int kFrag = kCols * kDim / 4;  // accumulator registers of a lane
+  // of a row of sums in shared memory, element d at d + d / (kDim / 8): no bank twice
+  static constexpr int kPitch = kDim + 36;
 };
 
-template <int kDim>
+template <int kDim, int kCols, int kWarps, int kTeam>
 struct Shared {
-  uint8_t ring[kWarps][Layout<kDim>::kStages][Layout<kDim>::kStage];
-  float sums[kWarps / 2][Layout<kDim>::kFrag * 32];
+  uint8_t ring[kWarps][Layout<kDim, kCols>::kStages][Layout<kDim, kCols>::kStage];
+  float sums[kTeam > 1 ? kTeam / 2 : 1][kTeam > 1 ? Layout<kDim, kCols>::kFrag * 32 : 1];
   float2 ml[kWarps][kFewRows];
   float2 row_ml[kFewRows];
-  int64_t before[kFewMaxSeqs + 1];  // units of the sequences before
   int64_t scan[kWarps];
-  uint64_t full[kWarps][Layout<kDim>::kStages];
+  uint64_t full[kWarps][Layout<kDim, kCols>::kStages];
   int poison, last;
   uint32_t abort;
+  alignas(8) int64_t before[1];  // [sequences + 1] units of the sequences before
 };
 
 // Where a warp is in the line of units.
@@ -62,6 +67,7 @@ struct Cursor {
   int64_t u;
   int seq, head, tile, unit, units;
   int lim;  // positions from here on are seen by no row of the tile
+  SeqSpan sp;
 };
 
 __device__ __forceinline__ int last_seen(const AttendFewArgs& p, const SeqSpan& sp, int tile) {
@@ -70,107 +76,110 @@ __device__ __forceinline__ int last_seen(const AttendFewArgs& p, const SeqSpan& 
 }
 
 // Units of a tile: at least one, which writes the rows that see nothing.
-__device__ __forceinline__ int units_of(int lim) { return max(1, (lim + kUnit - 1) / kUnit); }
+template <int kTeam>
+__device__ __forceinline__ int units_of(int lim) {
+  return max(1, (lim + kTeam * kWarpKeys - 1) / (kTeam * kWarpKeys));
+}
 
+template <int kTeam>
 __device__ __forceinline__ int64_t units_of_seq(const AttendFewArgs& p, int i) {
   const SeqSpan sp = seq_span(p.a.s, i);
   int64_t n = 0;
-  for (int t = 0; t * p.tokens < sp.rows; ++t) n += units_of(last_seen(p, sp, t));
+  for (int t = 0; t * p.tokens < sp.rows; ++t) n += units_of<kTeam>(last_seen(p, sp, t));
   return n * p.a.c.heads;
 }
 
-template <int kDim>
-__device__ void place(const AttendFewArgs& p, const Shared<kDim>& sh, Cursor* c) {
+template <int kTeam>
+__device__ void place(const AttendFewArgs& p, const int64_t* before, Cursor* c) {
   int lo = 0, hi = p.a.s.n;
   while (hi - lo > 1) {
     const int m = (lo + hi) >> 1;
-    if (sh.before[m] <= c->u)
+    if (before[m] <= c->u)
       lo = m;
     else
       hi = m;
   }
   c->seq = lo;
-  const int64_t per_head = (sh.before[lo + 1] - sh.before[lo]) / p.a.c.heads, r = c->u - sh.before[lo];
+  const int64_t per_head = (before[lo + 1] - before[lo]) / p.a.c.heads, r = c->u - before[lo];
   c->head = static_cast<int>(r / per_head);
   int left = static_cast<int>(r - c->head * per_head);
-  const SeqSpan sp = seq_span(p.a.s, lo);
+  c->sp = seq_span(p.a.s, lo);
   for (c->tile = 0;; ++c->tile) {
-    c->lim = last_seen(p, sp, c->tile);
-    c->units = units_of(c->lim);
+    c->lim = last_seen(p, c->sp, c->tile);
+    c->units = units_of<kTeam>(c->lim);
     if (left < c->units) break;
     left -= c->units;
   }
   c->unit = left;
 }
 
-// The page of lane i's sixteen (i < 2) of the cursor's unit, -1: none.
-__device__ __forceinline__ int page_of(const AttendFewArgs& p, const Cursor& c, int pos) {
-  if (pos >= c.lim) return -1;
-  const int page = p.a.s.table[static_cast<int64_t>(c.seq) * p.a.s.max_pages + pos / p.a.c.page_tokens];
-  return page < p.a.c.n_pages ? page : -1;
-}
-
-// Four pairs of values of eight codes.
-__device__ __forceinline__ void expand(uint32_t w, uint32_t (&h)[4]) {
+// Four pairs of values of eight codes (one instruction each, whichever byte).
+__device__ __forceinline__ void expand(uint32_t w, __half2 (&h)[4]) {
+  uint32_t r[4];
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "mov.b32 {a, b, c, d}, %4;\n\t"
       "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
       "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
       "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
       "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
       : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<const __half2*>(&r[i]);
 }
 
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+// The two scale bytes of a halfword in fp16.
+__device__ __forceinline__ __half2 scales2(uint32_t bytes) {
   uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
+  asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(r) : "r"(bytes));
+  return *reinterpret_cast<const __half2*>(&r);
 }
 
-// A scale byte, twice, in fp16.
-__device__ __forceinline__ uint32_t scale2(uint32_t byte) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(r) : "r"(byte * 0x101u));
-  return r;
-}
+__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
+// An 8 x 8 matrix of 16-bit values, two of a row to a lane, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
-// The rows of a tile that a lane holds: g and g + 8.
-template <int kDim>
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) { return bits(__floats2half2_rn(a, b)); }
+
+// What a lane keeps of a tile's rows. As a factor: elements kDim / 4 * t .. of
+// rows g and g + 8, four to a step. As results: rows 2t, 2t + 1 (and 8 further).
+template <int kDim, int kCols>
 struct Rows {
-  uint32_t q[kDim / 16][4];  // elements kDim / 4 * t .. of both rows, four to a step
-  float c[2];                // exponent of 2 per unit of the rows' scores
-  int lim[2];
-  int all;                   // positions below are seen by every row
+  uint32_t q[kCols][kDim / 16][2];
+  float c[kCols][2];  // exponent of 2 per unit of the rows' scores
+  int lim[kCols][2];
+  int all;            // positions below are seen by every row
 };
 
-template <int kDim>
-__device__ __forceinline__ void load_rows(const AttendFewArgs& p, const Cursor& cu, Rows<kDim>* r) {
+template <int kDim, int kCols>
+__device__ __forceinline__ void load_rows(const AttendFewArgs& p, const Cursor& cu, Rows<kDim, kCols>* r) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const SeqSpan sp = seq_span(p.a.s, cu.seq);
+  const SeqSpan& sp = cu.sp;
   r->all = seen(sp.len - sp.rows + cu.tile * p.tokens, sp.len, p.a.block);
+  // the token (of the sequence) of a row, or -1
+  auto token = [&](int row) {
+    const int in = row / p.a.group, tok = cu.tile * p.tokens + in;
+    return in < p.tokens && tok < sp.rows ? tok : -1;
+  };
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int row = g + 8 * h, tok_in = row / p.a.group, tok = cu.tile * p.tokens + tok_in;
-    const bool mine = tok_in < p.tokens && tok < sp.rows;
-    r->lim[h] = mine ? seen(sp.len - sp.rows + tok, sp.len, p.a.block) : 0;
+  for (int h = 0; h < kCols; ++h) {
+    const int row = g + 8 * h, tok = token(row);
     float v[kDim / 4], top = 0.f;
-    if (mine) {
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.a.q.data + (sp.row0 + tok) * p.a.q.row + (cu.head * p.a.group + row - tok_in * p.a.group) * p.a.q.head +
-          t * (kDim / 2));
+    if (tok >= 0) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.a.q.data + (sp.row0 + tok) * p.a.q.row +
+                                                        (cu.head * p.a.group + row % p.a.group) * p.a.q.head + t * (kDim / 2));
 #pragma unroll
       for (int i = 0; i < kDim / 32; ++i) {
         const uint4 x = src[i];
@@ -194,168 +203,218 @@ __device__ __forceinline__ void load_rows(const AttendFewArgs& p, const Cursor& 
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     // top 2^-e in [2^14, 2^15)
     const int e = top > 0.f ? ilogbf(top) - 14 : 0;
-    r->c[h] = fminf(fmaxf(scalbnf(p.a.scale_log2, e), 1.4e-45f), 3.4028234e38f);
+    const float c = fminf(fmaxf(scalbnf(p.a.scale_log2, e), 1.4e-45f), 3.4028234e38f);
     const float f0 = scalbnf(1.f, -e / 2), f1 = scalbnf(1.f, -e - -e / 2);  // (2^-e itself may leave fp32's range)
 #pragma unroll
     for (int i = 0; i < kDim / 4; ++i) v[i] = v[i] * f0 * f1;
 #pragma unroll
     for (int i = 0; i < kDim / 16; ++i) {
-      r->q[i][h] = half2_bits(v[4 * i], v[4 * i + 1]);
-      r->q[i][2 + h] = half2_bits(v[4 * i + 2], v[4 * i + 3]);
+      r->q[h][i][0] = half2_bits(v[4 * i], v[4 * i + 1]);
+      r->q[h][i][1] = half2_bits(v[4 * i + 2], v[4 * i + 3]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      r->c[h][i] = __shfl_sync(0xffffffffu, c, 4 * (2 * t + i));
+      const int at = token(8 * h + 2 * t + i);
+      r->lim[h][i] = at >= 0 ? seen(sp.len - sp.rows + at, sp.len, p.a.block) : 0;
     }
   }
 }
 
-// Softmax state of a lane's two rows, and its share of their sums: accumulator j
-// holds columns 2t and 2t + 1 of the 8 elements j, j + kDim / 8, ...
-template <int kDim>
+// Softmax state of a lane's rows, and its share of their sums: accumulator j holds
+// elements kDim / 8 * g + 2 j (registers 0 and 1) and the next (2 and 3).
+template <int kDim, int kCols>
 struct State {
-  float o[kDim / 8][4];
-  float m[2], l[2];
+  float o[kCols][kDim / 16][4];
+  float m[kCols][2], l[kCols][2];
 };
 
 // One step of a warp: 32 keys from position pos, whose sixteens with a page are
 // `there`. Returns whether a value that some but not all rows see is NaN (it counts
 // as 0 here).
-template <int kDim, bool kMasked>
-__device__ __forceinline__ bool step(const AttendFewArgs& p, const uint8_t* stage, const Rows<kDim>& r, int pos, int any,
-                                     uint32_t there, State<kDim>* st) {
-  using L = Layout<kDim>;
-  constexpr int kWordsK = kDim / 32;  // words of codes of a lane's share of a key
+template <int kDim, int kCols, bool kMasked>
+__device__ __forceinline__ bool step(const uint8_t* stage, const Rows<kDim, kCols>& r, int pos, int any, uint32_t there,
+                                     State<kDim, kCols>* st) {
+  using L = Layout<kDim, kCols>;
+  constexpr int kWords = kDim / 32;  // words of codes of a lane's share of a key
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  float s[2][2][4];
+  float s[2][kCols][4];
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
+  for (int x = 0; x < 2; ++x)
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const uint8_t* k = stage + x * L::kSixteen;
-      const int key = 8 * n + g;
-      uint32_t w[kWordsK];
-      uint32_t sc[kWordsK];
-      if (kDim == 128) {
-        const uint4 v = *reinterpret_cast<const uint4*>(k + key * 64 + t * 16);
-        w[0] = v.x, w[1] = v.y, w[2 % kWordsK] = v.z, w[3 % kWordsK] = v.w;
-        const uint32_t b = *reinterpret_cast<const uint16_t*>(k + L::kKs + key * 8 + 2 * t);
-        sc[0] = sc[1] = scale2(b & 0xFFu);
-        sc[2 % kWordsK] = sc[3 % kWordsK] = scale2(b >> 8);
-      } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(k + key * 32 + t * 8);
-        w[0] = v.x, w[1] = v.y;
-        sc[0] = sc[1] = scale2(k[L::kKs + key * 4 + t]);
+    for (int h = 0; h < kCols; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[x][h][i] = 0.f;
+  {
+    uint32_t w[2][2][kWords];
+    __half2 sc[2][2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const uint8_t* k = stage + x * L::kSixteen;
+        const int key = 8 * n + g;
+        if constexpr (kDim == 128) {
+          const uint4 v = *reinterpret_cast<const uint4*>(k + key * 64 + t * 16);
+          w[x][n][0] = v.x, w[x][n][1] = v.y, w[x][n][2] = v.z, w[x][n][3] = v.w;
+          sc[x][n] = scales2(*reinterpret_cast<const uint16_t*>(k + L::kKs + key * 8 + 2 * t));
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(k + key * 32 + t * 8);
+          w[x][n][0] = v.x, w[x][n][1] = v.y;
+          sc[x][n] = scales2(k[L::kKs + key * 4 + t]);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[x][n][i] = 0.f;
+    for (int i = 0; i < kWords; ++i)
 #pragma unroll
-      for (int i = 0; i < kWordsK; ++i) {
-        uint32_t h[4];
-        expand(w[i], h);
-        mma(s[x][n], r.q[2 * i], mul2(h[0], sc[i]), mul2(h[1], sc[i]));
-        mma(s[x][n], r.q[2 * i + 1], mul2(h[2], sc[i]), mul2(h[3], sc[i]));
+      for (int x = 0; x < 2; ++x) {
+        __half2 h[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          expand(w[x][n][i], h[n]);
+          const __half2 f = kDim == 128 && i >= 2 ? __high2half2(sc[x][n]) : __low2half2(sc[x][n]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[n][e] = __hmul2(h[n][e], f);
+        }
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            mma(s[x][c], bits(h[0][2 * e]), bits(h[1][2 * e]), bits(h[0][2 * e + 1]), bits(h[1][2 * e + 1]),
+                r.q[c][2 * i + e][0], r.q[c][2 * i + e][1]);
       }
-    }
   }
   if (kMasked) {
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int c = 0; c < kCols; ++c)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int at = pos + 16 * x + 8 * n + 2 * t + (i & 1);
-          if (at >= r.lim[i >> 1] || !(there >> x & 1u)) s[x][n][i] = -INFINITY;
+          const int at = pos + 16 * x + g + (i >> 1) * 8;
+          if (at >= r.lim[c][i & 1] || !(there >> x & 1u)) s[x][c][i] = -INFINITY;
         }
   }
-  float top[2], base[2];
+  // each lane's own keys say whether a row's maximum may have grown; only then is
+  // it worked out
+  float top[kCols][2], lift[kCols][2];
+  bool grown = false;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float v = -INFINITY;
+  for (int c = 0; c < kCols; ++c)
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int n = 0; n < 2; ++n) v = fmaxf(v, fmaxf(s[x][n][2 * h], s[x][n][2 * h + 1]));
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-    top[h] = v * r.c[h];
-  }
-  if (__any_sync(0xffffffffu, top[0] - st->m[0] > kGrowth || top[1] - st->m[1] > kGrowth)) {
-    float f[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float up = fmaxf(st->m[h], top[h]);
-      f[h] = st->m[h] == up ? 1.f : exp2_fast(st->m[h] - up);
-      st->m[h] = up;
-      st->l[h] *= f[h];
+    for (int i = 0; i < 2; ++i) {
+      top[c][i] = fmaxf(fmaxf(s[0][c][i], s[0][c][i + 2]), fmaxf(s[1][c][i], s[1][c][i + 2])) * r.c[c][i];
+      grown |= top[c][i] - st->m[c][i] > kGrowth;
     }
+  if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-    for (int j = 0; j < kDim / 8; ++j)
+    for (int c = 0; c < kCols; ++c)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) st->o[j][i] *= f[i >> 1];
+      for (int i = 0; i < 2; ++i) {
+        float up = fmaxf(top[c][i], st->m[c][i]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
+        const float f = st->m[c][i] == up ? 1.f : exp2_fast(st->m[c][i] - up);
+        st->m[c][i] = up;
+        st->l[c][i] *= f;
+#pragma unroll
+        for (int j = 0; j < kDim / 16; ++j) st->o[c][j][i] *= f, st->o[c][j][i + 2] *= f;
+      }
   }
-  base[0] = (st->m[0] == -INFINITY ? 0.f : st->m[0]) - kLift;
-  base[1] = (st->m[1] == -INFINITY ? 0.f : st->m[1]) - kLift;
+#pragma unroll
+  for (int c = 0; c < kCols; ++c)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) lift[c][i] = kLift - (st->m[c][i] == -INFINITY ? 0.f : st->m[c][i]);
   bool poison = false;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    uint32_t a[4];
+    uint32_t b[kCols][2];
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int c = 0; c < kCols; ++c) {
+      float e[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float e0 = exp2_fast(fmaf(s[x][n][2 * h], r.c[h], -base[h]));
-        const float e1 = exp2_fast(fmaf(s[x][n][2 * h + 1], r.c[h], -base[h]));
-        st->l[h] += e0 + e1;
-        a[2 * n + h] = half2_bits(e0, e1);
+      for (int i = 0; i < 4; ++i) {
+        e[i] = exp2_fast(fmaf(s[x][c][i], r.c[c][i & 1], lift[c][i & 1]));
+        st->l[c][i & 1] += e[i];
       }
+      b[c][0] = transposed(half2_bits(e[0], e[1]));
+      b[c][1] = transposed(half2_bits(e[2], e[3]));
+    }
     const uint8_t* v = stage + x * L::kSixteen + L::kV;
     const uint8_t* vs = stage + x * L::kSixteen + L::kVs;
-    uint32_t w[4][kDim / 64], sc[4];
+    // two keys' codes side by side in a byte: the pairs that the product takes
+    uint32_t w[2][kDim / 64][2];
+    __half2 sc[2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int key = 2 * t + (k & 1) + (k >> 1) * 8;
-      uint32_t b;
-      if (kDim == 128) {
-        const uint2 c = *reinterpret_cast<const uint2*>(v + key * 64 + g * 8);
-        w[k][0] = c.x, w[k][kDim / 64 - 1] = c.y;
-        b = vs[key * 8 + g];
-      } else {
-        w[k][0] = *reinterpret_cast<const uint32_t*>(v + key * 32 + g * 4);
-        b = vs[key * 4 + g / 2];
-      }
-      if (kMasked) {
-        const int at = pos + 16 * x + key;
-        if (at >= any || !(there >> x & 1u)) b = 0;
-        if (at >= r.all && (b & 0x7Fu) == 0x7Fu) {
-          poison = true;
-          b = 0;
+    for (int k = 0; k < 2; ++k) {
+      uint32_t u[2][kDim / 64], byte[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int key = 2 * t + e + 8 * k;
+        if constexpr (kDim == 128) {
+          const uint2 x2 = *reinterpret_cast<const uint2*>(v + key * 64 + g * 8);
+          u[e][0] = x2.x, u[e][1] = x2.y;
+          byte[e] = vs[key * 8 + g];
+        } else {
+          u[e][0] = *reinterpret_cast<const uint32_t*>(v + key * 32 + g * 4);
+          byte[e] = vs[key * 4 + g / 2];
+        }
+        if (kMasked) {
+          const int at = pos + 16 * x + key;
+          if (at >= any || !(there >> x & 1u)) byte[e] = 0;
+          if (at >= r.all && (byte[e] & 0x7Fu) == 0x7Fu) {
+            poison = true;
+            byte[e] = 0;
+          }
         }
       }
-      sc[k] = scale2(b);
+      sc[k] = scales2(byte[0] + byte[1] * 256u);
+#pragma unroll
+      for (int i = 0; i < kDim / 64; ++i) {
+        w[k][i][0] = (u[0][i] & 0x0F0F0F0Fu) | (u[1][i] * 16u & 0xF0F0F0F0u);
+        w[k][i][1] = (u[0][i] >> 4 & 0x0F0F0F0Fu) | (u[1][i] & 0xF0F0F0F0u);
+      }
     }
 #pragma unroll
     for (int i = 0; i < kDim / 64; ++i) {
-      uint32_t h[4][4];
+      __half2 h[2][2][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        expand(w[k][i], h[k]);
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[k][e] = mul2(h[k][e], sc[k]);
-      }
+        for (int n = 0; n < 2; ++n) {
+          expand(w[k][i][n], h[k][n]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        mma(st->o[8 * i + 2 * e], a, __byte_perm(h[0][e], h[1][e], 0x5410), __byte_perm(h[2][e], h[3][e], 0x5410));
-        mma(st->o[8 * i + 2 * e + 1], a, __byte_perm(h[0][e], h[1][e], 0x7632), __byte_perm(h[2][e], h[3][e], 0x7632));
-      }
+          for (int e = 0; e < 4; ++e) h[k][n][e] = __hmul2(h[k][n][e], sc[k]);
+        }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+          mma(st->o[c][4 * i + e], bits(h[0][0][e]), bits(h[0][1][e]), bits(h[1][0][e]), bits(h[1][1][e]), b[c][0], b[c][1]);
     }
   }
   return poison;
 }
 
-// First unit of CTA c's piece, and the CTA whose piece holds unit u. No more CTAs
-// than units have a piece.
-__device__ __forceinline__ int64_t pieces(int64_t total) { return min(total, static_cast<int64_t>(gridDim.x)); }
-__device__ __forceinline__ int64_t piece(int64_t total, int c) { return total * c / pieces(total); }
-__device__ __forceinline__ int piece_of(int64_t total, int64_t u) {
-  return static_cast<int>(((u + 1) * pieces(total) - 1) / total);
+// The line is cut into as many pieces as there are teams (or units, if those are
+// fewer): the first unit of piece k, and the piece that holds unit u.
+struct Line {
+  int64_t total, pieces;
+  __device__ __forceinline__ int64_t first(int k) const { return total * k / pieces; }
+  __device__ __forceinline__ int piece_of(int64_t u) const { return static_cast<int>(((u + 1) * pieces - 1) / total); }
+};
+
+// Where piece k keeps its sums of the tile that begins at unit `first`: a piece has
+// two places, for a tile that began before it and for one that goes on behind it.
+__device__ __forceinline__ int place_of(const Line& line, int k, int64_t first) {
+  return 2 * k + (first > line.first(k) ? 1 : 0);
+}
+
+// Says that this team's sums of the tile of units first .. first + units - 1 are in
+// place; true for the last team of them.
+__device__ __forceinline__ bool arrive_last(const AttendFewArgs& p, int c0, int c1) {
+  __threadfence();
+  return atomicInc(p.arrived + c0, c1 - c0) == static_cast<uint32_t>(c1 - c0);
 }
 
 // A row's result from its sum, maximum and weight.
@@ -371,74 +430,83 @@ __device__ __forceinline__ void write_lse(const AttendFewArgs& p, int64_t at, fl
 // The end of a tile's keys in this CTA, by all its threads: the warps' sums
 // become one, which is the result or goes to the workspace. units u0 .. u1 - 1 of
 // the tile lie here.
-template <int kDim>
-__device__ void finish(const AttendFewArgs& p, Shared<kDim>* sh, const Cursor& c, int64_t total, int u0, int u1, State<kDim>* st) {
-  using L = Layout<kDim>;
+template <int kDim, int kCols, int kWarps>
+__device__ void finish_team(const AttendFewArgs& p, Shared<kDim, kCols, kWarps, kWarps>* sh, const Cursor& c, const Line& line,
+                            int u0, int u1, State<kDim, kCols>* st) {
+  using L = Layout<kDim, kCols>;
+  constexpr int kThreads = kWarps * 32, kUnit = kWarps * kWarpKeys;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    st->l[h] += __shfl_xor_sync(0xffffffffu, st->l[h], 1);
-    st->l[h] += __shfl_xor_sync(0xffffffffu, st->l[h], 2);
-    if (t == 0) sh->ml[warp][g + 8 * h] = make_float2(st->m[h], st->l[h]);
-  }
-  __syncthreads();
-  float f[2];
+  for (int h = 0; h < kCols; ++h)
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float m = -INFINITY, l = 0.f;
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sh->ml[w][g + 8 * h].x);
-    f[h] = st->m[h] == m ? 1.f : exp2_fast(st->m[h] - m);
-    if (warp == 0 && t == 0) {
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 v = sh->ml[w][g + 8 * h];
-        l += v.y * (v.x == m ? 1.f : exp2_fast(v.x - m));
-      }
-      sh->row_ml[g + 8 * h] = make_float2(m, l);
+    for (int i = 0; i < 2; ++i) {
+      float l = st->l[h][i];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (g == 0) sh->ml[warp][8 * h + 2 * t + i] = make_float2(st->m[h][i], l);
     }
-  }
+  __syncthreads();
 #pragma unroll
-  for (int j = 0; j < kDim / 8; ++j)
+  for (int h = 0; h < kCols; ++h)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) st->o[j][i] *= f[i >> 1];
-  // 12 warps' sums to 6, to 3, to 1: `from` warps from `to` on hand theirs over
-  constexpr int kSteps[3][2] = {{6, 6}, {3, 3}, {1, 2}};
+    for (int i = 0; i < 2; ++i) {
+      const int row = 8 * h + 2 * t + i;
+      float m = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    const int to = kSteps[k][0], from = kSteps[k][1];
-    if (warp >= to && warp < to + from)
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sh->ml[w][row].x);
+      const float f = st->m[h][i] == m ? 1.f : exp2_fast(st->m[h][i] - m);
+      if (warp == 0 && g == 0) {
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 v = sh->ml[w][row];
+          l += v.y * (v.x == m ? 1.f : exp2_fast(v.x - m));
+        }
+        sh->row_ml[row] = make_float2(m, l);
+      }
 #pragma unroll
-      for (int i = 0; i < L::kFrag; ++i) sh->sums[warp - to][i * 32 + lane] = st->o[i / 4][i % 4];
+      for (int j = 0; j < kDim / 16; ++j) st->o[h][j][i] *= f, st->o[h][j][i + 2] *= f;
+    }
+  // the warps' sums to half as many, and so on (12: 6, 3, 1): those from `to` on hand
+  // theirs over, the others add one each, in the last step the first adds all
+  float (&acc)[L::kFrag] = *reinterpret_cast<float(*)[L::kFrag]>(&st->o[0][0][0]);
+#pragma unroll
+  for (int from = kWarps; from > 1; from = from > 3 ? from / 2 : 1) {
+    const int to = from > 3 ? from / 2 : 1;
+    if (warp >= to && warp < from)
+#pragma unroll
+      for (int i = 0; i < L::kFrag; ++i) sh->sums[warp - to][i * 32 + lane] = acc[i];
     __syncthreads();
-    if (k < 2 ? warp < to : warp == 0)
-      for (int w = k < 2 ? warp : 0; w < from; w += k < 2 ? from : 1)
+    if (warp < to)
+      for (int w = warp; w < from - to; w += to)
 #pragma unroll
-        for (int i = 0; i < L::kFrag; ++i) st->o[i / 4][i % 4] += sh->sums[w][i * 32 + lane];
+        for (int i = 0; i < L::kFrag; ++i) acc[i] += sh->sums[w][i * 32 + lane];
     __syncthreads();
   }
   float* rows = sh->sums[0];
+  static_assert(8 * kCols * L::kPitch <= kWarps / 2 * L::kFrag * 32, "a tile's rows must fit");
   if (warp == 0) {
 #pragma unroll
-    for (int i = 0; i < L::kFrag; ++i) {
-      const int d = (2 * t + (i & 1)) * (kDim / 8) + i / 4;
-      rows[(g + (i & 2) * 4) * L::kPitch + d + d / (kDim / 4)] = st->o[i / 4][i % 4];
-    }
+    for (int h = 0; h < kCols; ++h)
+#pragma unroll
+      for (int j = 0; j < kDim / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int d = g * (kDim / 8) + 2 * j + (i >> 1);
+          rows[(8 * h + 2 * t + (i & 1)) * L::kPitch + d + g] = st->o[h][j][i];
+        }
   }
   __syncthreads();
-  const SeqSpan sp = seq_span(p.a.s, c.seq);
+  const SeqSpan& sp = c.sp;
   const int n_rows = min(p.tokens, sp.rows - c.tile * p.tokens) * p.a.group;
-  const bool whole = u0 == 0 && u1 == c.units;
-  const bool poison = sh->poison != 0;
-  // (a piece that begins inside a tile keeps that tile's sums in the first of
-  // the CTA's two places, one that ends inside a later tile in the second)
+  const bool whole = u0 == 0 && u1 == c.units, poison = sh->poison != 0;
   const int64_t first = c.u - c.unit;  // unit 0 of the tile
-  const int place0 = 2 * blockIdx.x + (first + u0 == piece(total, blockIdx.x) ? 0 : 1);
+  const int place0 = place_of(line, blockIdx.x, first);
   auto row_at = [&](int r) {
     const int tok = r / p.a.group;
     return (static_cast<int64_t>(sp.row0) + c.tile * p.tokens + tok) * p.a.q_heads + c.head * p.a.group + (r - tok * p.a.group);
   };
   for (int i = threadIdx.x; i < n_rows * (kDim / 4); i += kThreads) {
     const int r = i / (kDim / 4), d = i % (kDim / 4) * 4;
-    const float* s = rows + r * L::kPitch + d + d / (kDim / 4);
+    const float* s = rows + r * L::kPitch + d + d / (kDim / 8);
     float4 o = make_float4(s[0], s[1], s[2], s[3]);
     const float2 ml = sh->row_ml[r];
     if (poison) {
@@ -460,27 +528,43 @@ __device__ void finish(const AttendFewArgs& p, Shared<kDim>* sh, const Cursor& c
     }
   }
   if (!whole) {
-    const int c0 = piece_of(total, first), c1 = piece_of(total, first + c.units - 1);
+    const int c0 = line.piece_of(first), c1 = line.piece_of(first + c.units - 1);
     __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) sh->last = atomicInc(p.arrived + c0, c1 - c0) == static_cast<uint32_t>(c1 - c0);
+    if (threadIdx.x == 0) sh->last = arrive_last(p, c0, c1);
     __syncthreads();
     if (sh->last) {
       __threadfence();
-      auto place_of = [&](int k) { return 2 * k + (k == c0 && first != piece(total, k) ? 1 : 0); };
+      const int skip = place_of(line, c0, first) - 2 * c0;
       for (int i = threadIdx.x; i < n_rows * (kDim / 4); i += kThreads) {
         const int r = i / (kDim / 4), d = i % (kDim / 4) * 4;
         float m = -INFINITY, l = 0.f;
-        for (int k = c0; k <= c1; ++k) m = fmaxf(m, __ldcg(&p.part_ml[place_of(k) * kFewRows + r].x));
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = c0; k <= c1; ++k) {
-          const float2 ml = __ldcg(&p.part_ml[place_of(k) * kFewRows + r]);
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(
-              p.part + (static_cast<int64_t>(place_of(k)) * kFewRows + r) * kDim + d));
-          const float w = ml.x == m ? 1.f : exp2_fast(ml.x - m);
-          l += w * ml.y;
-          o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+        // kBatch parts at a time, so that their loads are in flight together
+        constexpr int kBatch = 8;
+        for (int k0 = c0; k0 <= c1; k0 += kBatch) {
+          float2 ml[kBatch];
+          float4 v[kBatch];
+          float top = m;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int j = min(k0 + k, c1), at = (2 * j + (j == c0 ? skip : 0)) * kFewRows + r;
+            ml[k] = __ldcg(&p.part_ml[at]);
+            v[k] = __ldcg(reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(at) * kDim + d));
+          }
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);
+          const float f = m == top ? 1.f : exp2_fast(m - top);
+          m = top;
+          l *= f;
+          o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            if (k0 + k > c1) continue;
+            const float w = ml[k].x == m ? 1.f : exp2_fast(ml[k].x - m);
+            l += w * ml[k].y;
+            o.x += w * v[k].x, o.y += w * v[k].y, o.z += w * v[k].z, o.w += w * v[k].w;
+          }
         }
         write_row(p, row_at(r), kDim, d, o, l == 0.f ? 0.f : p.a.c.v_mul / l);
         if (d == 0) write_lse(p, row_at(r), m, l);
@@ -490,13 +574,120 @@ __device__ void finish(const AttendFewArgs& p, Shared<kDim>* sh, const Cursor& c
   __syncthreads();  // the buffers are free again
 }
 
+// The same for a team of one warp, whose lanes keep their own elements throughout:
+// in the workspace a part lies as the lanes hold it.
+template <int kDim, int kCols>
+__device__ void finish_warp(const AttendFewArgs& p, const Cursor& c, const Line& line, int piece, int u0, int u1, bool poison,
+                            State<kDim, kCols>* st) {
+  constexpr int kFrag = Layout<kDim, kCols>::kFrag;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const SeqSpan& sp = c.sp;
+  const int n_rows = min(p.tokens, sp.rows - c.tile * p.tokens) * p.a.group;
+#pragma unroll
+  for (int h = 0; h < kCols; ++h)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) st->l[h][i] += __shfl_xor_sync(0xffffffffu, st->l[h][i], o);
+  if (__any_sync(0xffffffffu, poison)) {
+    const int p0 = sp.len - sp.rows, at0 = max(seen(p0 + c.tile * p.tokens, sp.len, p.a.block), u0 * kWarpKeys);
+#pragma unroll
+    for (int h = 0; h < kCols; ++h)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = 8 * h + 2 * t + i, tok = c.tile * p.tokens + row / p.a.group;
+        const int hi = row < n_rows ? min(seen(p0 + tok, sp.len, p.a.block), u1 * kWarpKeys) : 0;
+        for (int j = at0; j < hi; ++j) {
+          const uint8_t* six = kv_sixteen(p.a.c, p.a.s, c.seq, c.head, j);
+          if (six != nullptr && (six[Layout<kDim, kCols>::kVs + j % 16 * (kDim / 16) + g * (kDim / 8) / 16] & 0x7F) == 0x7F)
+#pragma unroll
+            for (int k = 0; k < kDim / 16; ++k) st->o[h][k][i] = st->o[h][k][i + 2] = NAN;
+        }
+      }
+    __syncwarp();
+  }
+  float (&acc)[kFrag] = *reinterpret_cast<float(*)[kFrag]>(&st->o[0][0][0]);
+  if (u0 != 0 || u1 != c.units) {
+    const int64_t first = c.u - c.unit;
+    const int c0 = line.piece_of(first), c1 = line.piece_of(first + c.units - 1);
+    const int mine = place_of(line, piece, first);
+    float* part = p.part + static_cast<int64_t>(mine) * (kFrag * 32) + lane;
+#pragma unroll
+    for (int i = 0; i < kFrag; ++i) __stcg(part + i * 32, acc[i]);
+    if (g == 0)
+#pragma unroll
+      for (int h = 0; h < kCols; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          __stcg(&p.part_ml[mine * kFewRows + 8 * h + 2 * t + i], make_float2(st->m[h][i], st->l[h][i]));
+    __threadfence();
+    __syncwarp();
+    int last = 0;
+    if (lane == 0) last = arrive_last(p, c0, c1);
+    if (!__shfl_sync(0xffffffffu, last, 0)) return;
+    __threadfence();
+    const int skip = place_of(line, c0, first) - 2 * c0;
+#pragma unroll
+    for (int h = 0; h < kCols; ++h)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) st->m[h][i] = -INFINITY, st->l[h][i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kFrag; ++i) acc[i] = 0.f;
+#pragma unroll 1
+    for (int k = c0; k <= c1; ++k) {
+      const int at = 2 * k + (k == c0 ? skip : 0);
+      const float* from = p.part + static_cast<int64_t>(at) * (kFrag * 32) + lane;
+      float v[kFrag];
+#pragma unroll
+      for (int i = 0; i < kFrag; ++i) v[i] = __ldcg(from + i * 32);
+#pragma unroll
+      for (int h = 0; h < kCols; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 ml = __ldcg(&p.part_ml[at * kFewRows + 8 * h + 2 * t + i]);
+          const float m = fmaxf(st->m[h][i], ml.x);
+          const float f = st->m[h][i] == m ? 1.f : exp2_fast(st->m[h][i] - m), w = ml.x == m ? 1.f : exp2_fast(ml.x - m);
+          st->m[h][i] = m;
+          st->l[h][i] = st->l[h][i] * f + ml.y * w;
+#pragma unroll
+          for (int j = 0; j < kDim / 16; ++j)
+#pragma unroll
+            for (int e = i; e < 4; e += 2) st->o[h][j][e] = st->o[h][j][e] * f + v[(h * (kDim / 16) + j) * 4 + e] * w;
+        }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < kCols; ++h)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = 8 * h + 2 * t + i;
+      if (row >= n_rows) continue;
+      const int tok = row / p.a.group;
+      const int64_t at = (static_cast<int64_t>(sp.row0) + c.tile * p.tokens + tok) * p.a.q_heads + c.head * p.a.group +
+                         (row - tok * p.a.group);
+      const float l = st->l[h][i], inv = l == 0.f ? 0.f : p.a.c.v_mul / l;
+      uint32_t w[kDim / 16];
+#pragma unroll
+      for (int j = 0; j < kDim / 16; ++j) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(st->o[h][j][i] * inv, st->o[h][j][i + 2] * inv);
+        w[j] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+      uint4* to = reinterpret_cast<uint4*>(p.a.out + at * kDim + g * (kDim / 8));
+#pragma unroll
+      for (int j = 0; j < kDim / 64; ++j) to[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+      if (g == 0) write_lse(p, at, st->m[h][i], l);
+    }
+  __syncwarp();
+}
+
 }  // namespace
 
-template <int kDim>
-__global__ void __launch_bounds__(kThreads, 1) k_attend_few(const __grid_constant__ AttendFewArgs p) {
-  using L = Layout<kDim>;
+template <int kDim, int kCols, int kWarps, int kTeam>
+__global__ void __launch_bounds__(kWarps * 32, few_warps(kCols) / kWarps) k_attend_few(const __grid_constant__ AttendFewArgs p) {
+  using L = Layout<kDim, kCols>;
+  constexpr int kThreads = kWarps * 32, kUnit = kTeam * kWarpKeys;
   extern __shared__ __align__(128) uint8_t raw[];
-  Shared<kDim>* sh = reinterpret_cast<Shared<kDim>*>(raw);
+  auto* sh = reinterpret_cast<Shared<kDim, kCols, kWarps, kTeam>*>(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x < kWarps * L::kStages) mbar_init(&sh->full[0][0] + threadIdx.x, 1);
   if (threadIdx.x == 0) {
@@ -506,14 +697,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_few(const __grid_constan
   fence_mbar_init();
   pdl_wait();
   pdl_trigger();
-  // the line of units: three sequences to a thread
-  static_assert(3 * kThreads >= kFewMaxSeqs, "every sequence needs a thread");
-  int64_t own[3], sum = 0;
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    const int i = 3 * threadIdx.x + k;
-    own[k] = i < p.a.s.n ? units_of_seq(p, i) : 0;
-    sum += own[k];
+  // the line of units: `per` neighbouring sequences to a thread
+  const int per = (p.a.s.n + kThreads - 1) / kThreads, i0 = threadIdx.x * per, i1 = min(i0 + per, p.a.s.n);
+  int64_t sum = 0;
+  for (int i = i0; i < i1; ++i) {
+    const int64_t n = units_of_seq<kTeam>(p, i);
+    sh->before[i] = n;
+    sum += n;
   }
   int64_t incl = sum;
 #pragma unroll
@@ -528,69 +718,80 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_few(const __grid_constan
     if (w < warp) at += sh->scan[w];
     total += sh->scan[w];
   }
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    const int i = 3 * threadIdx.x + k;
-    if (i < p.a.s.n) sh->before[i] = at;
-    at += own[k];
-    if (i == p.a.s.n - 1) sh->before[i + 1] = at;
+  for (int i = i0; i < i1; ++i) {
+    const int64_t n = sh->before[i];
+    sh->before[i] = at;
+    at += n;
   }
+  if (threadIdx.x == 0) sh->before[p.a.s.n] = total;
   __syncthreads();
-  if (blockIdx.x >= pieces(total)) return;
-  const int64_t u_begin = piece(total, blockIdx.x), u_end = piece(total, blockIdx.x + 1);
+  const int piece = kTeam == 1 ? blockIdx.x * kWarps + warp : blockIdx.x;
+  const Line line = {total, min(total, static_cast<int64_t>(gridDim.x) * (kWarps / kTeam))};
+  if (piece >= line.pieces) return;  // (all of the team)
+  const int64_t u_end = line.first(piece + 1);
 
-  // the ring: what is fetched next, its page looked up one step ahead
+  // the ring: f is what is fetched next, c what is worked on
   Cursor f;
-  f.u = u_begin;
-  place<kDim>(p, *sh, &f);
+  f.u = line.first(piece);
+  place<kTeam>(p, sh->before, &f);
   Cursor c = f;
-  auto pos_of = [&](const Cursor& x) { return x.unit * kUnit + warp * kWarpKeys + (lane & 1) * 16; };
-  int page = lane < 2 ? page_of(p, f, pos_of(f)) : -1;
+  // lane i looks up the i % 2-th sixteen of the warp's keys, i / 2 units on: 16 units
+  // of one tile at a time
+  int six = -1;   // its place in the pool, in sixteens
+  int ahead = 16;  // units of those that are fetched already
   uint32_t there = 0;  // two bits per stage: sixteens that have a page
-  int fs = 0;
-  uint32_t fph = 0;  // parity of each stage's last fetch
-  bool dead = false;
-  auto fetch = [&]() {
-    if (f.u >= u_end) return;
-    const uint32_t has = __ballot_sync(0xffffffffu, page >= 0) & 3u;
-    there = (there & ~(3u << (2 * fs))) | has << (2 * fs);
-    fph ^= 1u << fs;
-    uint64_t* bar = &sh->full[warp][fs];
-    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(has) * L::kSixteen);
-    __syncwarp();
-    if (page >= 0) {
-      const int pos = pos_of(f), per = p.a.c.page_tokens / 16;
-      const uint8_t* src = p.a.c.pages + ((static_cast<int64_t>(page) * p.a.c.heads + f.head) * per +
-                                          pos % p.a.c.page_tokens / 16) * L::kSixteen;
-      bulk_load(smem_u32(sh->ring[warp][fs]) + lane * L::kSixteen, src, L::kSixteen, bar);
+  int fs = 0, s = 0;
+  uint32_t fph = 0, ph = 0;  // parity of each stage's last fetch; of the stages worked on
+  bool dead = false, begin = true, poison = false;
+  State<kDim, kCols> st;
+  Rows<kDim, kCols> rows;
+  int u0 = 0;
+  for (int warm = L::kStages;;) {
+    if (f.u < u_end && !dead) {
+      if (ahead == 16) {
+        ahead = 0;
+        const int i = (f.unit + (lane >> 1)) * (kUnit / 16) + (kTeam == 1 ? 0 : warp * 2) + (lane & 1);
+        six = -1;
+        if (i * 16 < f.lim) {
+          const int of_page = p.a.c.page_tokens / 16, entry = p.per_magic != 0 ? static_cast<int>(__umulhi(i, p.per_magic)) : i;
+          const int page = p.a.s.table[static_cast<int64_t>(f.seq) * p.a.s.max_pages + entry];
+          if (page >= 0 && page < p.a.c.n_pages) six = (page * p.a.c.heads + f.head) * of_page + (i - entry * of_page);
+        }
+      }
+      const int from = __shfl_sync(0xffffffffu, six, 2 * ahead + (lane & 1));
+      const uint32_t has = __ballot_sync(0xffffffffu, from >= 0) & 3u;
+      there = (there & ~(3u << (2 * fs))) | has << (2 * fs);
+      fph ^= 1u << fs;
+      uint64_t* bar = &sh->full[warp][fs];
+      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(has) * L::kSixteen);
+      __syncwarp();
+      if (lane < 2 && from >= 0)
+        bulk_load(smem_u32(sh->ring[warp][fs]) + lane * L::kSixteen, p.a.c.pages + static_cast<int64_t>(from) * L::kSixteen,
+                  L::kSixteen, bar);
+      fs = fs + 1 == L::kStages ? 0 : fs + 1;
+      ++ahead;
+      if (++f.u < u_end && ++f.unit == f.units) {
+        place<kTeam>(p, sh->before, &f);
+        ahead = 16;
+      }
     }
-    fs = fs + 1 == L::kStages ? 0 : fs + 1;
-    if (++f.u < u_end) {
-      if (++f.unit == f.units) place<kDim>(p, *sh, &f);
-      page = lane < 2 ? page_of(p, f, pos_of(f)) : -1;
-    }
-  };
-  for (int i = 0; i < L::kStages; ++i) fetch();
-
-  State<kDim> st;
-  Rows<kDim> rows;
-  int s = 0;
-  uint32_t ph = 0;
-  int u0 = c.unit;
-  bool begin = true;
-  while (true) {
+    if (warm > 0 && --warm > 0) continue;  // fill the ring first
     if (begin) {
       begin = false;
       u0 = c.unit;
-      load_rows<kDim>(p, c, &rows);
+      poison = false;
+      load_rows<kDim, kCols>(p, c, &rows);
 #pragma unroll
-      for (int j = 0; j < kDim / 8; ++j)
+      for (int h = 0; h < kCols; ++h) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st.o[j][i] = 0.f;
-      st.m[0] = st.m[1] = -INFINITY;
-      st.l[0] = st.l[1] = 0.f;
+        for (int j = 0; j < kDim / 16; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st.o[h][j][i] = 0.f;
+        st.m[h][0] = st.m[h][1] = -INFINITY;
+        st.l[h][0] = st.l[h][1] = 0.f;
+      }
     }
-    const int pos = c.unit * kUnit + warp * kWarpKeys;
+    const int pos = c.unit * kUnit + (kTeam == 1 ? 0 : warp * kWarpKeys);
     const uint32_t has = there >> (2 * s) & 3u;
     if (!dead && !__all_sync(0xffffffffu, mbar_wait(&sh->full[warp][s], ph, &sh->abort))) {
       dead = true;
@@ -601,44 +802,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_few(const __grid_constan
     }
     if (pos < c.lim) {
       const uint8_t* stage = sh->ring[warp][s];
-      if (has == 3u && pos + kWarpKeys <= rows.all) {
-        step<kDim, false>(p, stage, rows, pos, c.lim, has, &st);
-      } else if (step<kDim, true>(p, stage, rows, pos, c.lim, has, &st)) {
-        *reinterpret_cast<volatile int*>(&sh->poison) = 1;
-      }
+      if (has == 3u && pos + kWarpKeys <= rows.all)
+        step<kDim, kCols, false>(stage, rows, pos, c.lim, has, &st);
+      else
+        poison |= step<kDim, kCols, true>(stage, rows, pos, c.lim, has, &st);
     }
     __syncwarp();
     if (++s == L::kStages) {
       s = 0;
       ph ^= 1u;
     }
-    if (!dead) fetch();
     const bool end = c.u + 1 == u_end;
     if (end || c.unit + 1 == c.units) {
-      finish<kDim>(p, sh, c, total, u0, c.unit + 1, &st);
-      if (threadIdx.x == 0) sh->poison = 0;
-      __syncthreads();
+      if constexpr (kTeam == 1) {
+        finish_warp<kDim, kCols>(p, c, line, piece, u0, c.unit + 1, poison, &st);
+      } else {
+        if (poison) *reinterpret_cast<volatile int*>(&sh->poison) = 1;
+        finish_team<kDim, kCols, kWarps>(p, sh, c, line, u0, c.unit + 1, &st);
+        if (threadIdx.x == 0) sh->poison = 0;
+        __syncthreads();
+      }
       begin = true;
     }
     if (end) break;
     ++c.u;
-    if (++c.unit == c.units) place<kDim>(p, *sh, &c);
+    if (++c.unit == c.units) place<kTeam>(p, sh->before, &c);
   }
   // (the copies in flight must land before the CTA leaves)
   if (dead)
     for (int i = 0; i < L::kStages; ++i) mbar_wait_for(&sh->full[warp][i], (fph >> i & 1u) ^ 1u, 200000000ull);
 }
 
-template <int kDim>
-static cudaError_t launch(const AttendFewArgs& a, int grid, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(k_attend_few<kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(sizeof(Shared<kDim>)));
+template <int kDim, int kCols, int kWarps, int kTeam>
+static cudaError_t launch(const AttendFewArgs& a, int sms, cudaStream_t s) {
+  void (*k)(const AttendFewArgs) = k_attend_few<kDim, kCols, kWarps, kTeam>;
+  const size_t smem = sizeof(Shared<kDim, kCols, kWarps, kTeam>) + static_cast<size_t>(a.a.s.n) * 8;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_kernel(k_attend_few<kDim>, dim3(grid), dim3(kThreads), sizeof(Shared<kDim>), s, true, a);
+  return launch_kernel(k, dim3(sms * (few_warps(kCols) / kWarps)), dim3(kWarps * 32), smem, s, true, a);
 }
 
-cudaError_t launch_attend_few(const AttendFewArgs& a, int grid, cudaStream_t s) {
-  return a.a.c.dim == 64 ? launch<64>(a, grid, s) : launch<128>(a, grid, s);
+template <int kDim>
+static cudaError_t launch(const AttendFewArgs& a, int sms, bool alone, cudaStream_t s) {
+  if (a.tokens * a.a.group <= 8) return alone ? launch<kDim, 1, 4, 1>(a, sms, s) : launch<kDim, 1, 16, 16>(a, sms, s);
+  return alone ? launch<kDim, 2, 4, 1>(a, sms, s) : launch<kDim, 2, 12, 12>(a, sms, s);
+}
+
+cudaError_t launch_attend_few(const AttendFewArgs& args, int sms, bool alone, cudaStream_t s) {
+  AttendFewArgs a = args;
+  const unsigned per = a.a.c.page_tokens / 16;
+  a.per_magic = per == 1 ? 0u : static_cast<unsigned>(((1ull << 32) + per - 1) / per);
+  return a.a.c.dim == 64 ? launch<64>(a, sms, alone, s) : launch<128>(a, sms, alone, s);
 }
 
 }  // namespace clover

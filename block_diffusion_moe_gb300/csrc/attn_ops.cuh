@@ -76,20 +76,21 @@ struct AttendArgs {
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s);
 
-// Attention of few query rows over a cache (csrc/attend_few.cu): tiles of at
-// most 16 rows, the group's query heads of `tokens` = 16 / group tokens.
+// Attention of few query rows over a cache (csrc/attend_few.cu): tiles of at most
+// 8 or 16 rows, the group's query heads of `tokens` tokens.
 constexpr int kFewRows = 16;
-constexpr int kFewMaxSeqs = 1024;
 
 struct AttendFewArgs {
   AttnArgs a;
   int tokens;
-  float* part;     // [2 grid][16][dim] sums of parts of a tile's keys (workspace)
-  float2* part_ml;  // [2 grid][16] their maxima and sums of weights
-  uint32_t* arrived;  // [grid], zero between calls
+  float* part;        // [2 pieces][16 (8)][dim] sums of parts of a tile's keys (workspace)
+  float2* part_ml;    // [2 pieces][16] their maxima and sums of weights
+  uint32_t* arrived;  // [pieces], zero between calls
+  uint32_t per_magic;  // set by the launch: 2^32 / sixteens of a page, rounded up (0: one)
 };
 
-cudaError_t launch_attend_few(const AttendFewArgs& a, int grid, cudaStream_t s);
+// alone: a piece of the work to each warp, else to an SM.
+cudaError_t launch_attend_few(const AttendFewArgs& a, int sms, bool alone, cudaStream_t s);
 
 // ------------------------------------------------------------ device helpers
 

@@ -89,8 +89,15 @@ inline RouteShape route_shape(int tokens) {
 
 // Attention over a cache: CTAs of the kernel for few rows, and whether it takes a
 // call: sequences of at most 16 rows (tokens x heads of a group) on average.
-constexpr int kAttendFewCtas = 152;
+constexpr int kAttendSms = 152;
 inline bool attend_few(long long rows, int group, int seqs) { return group <= 16 && rows * group <= 16LL * seqs; }
+// Rows of its tiles, at most: 8 where the group has no more heads and the call
+// about one token for each sequence.
+inline int attend_few_rows(long long rows, int group, int seqs) { return group <= 8 && rows * group <= 8LL * seqs ? 8 : 16; }
+// Whether each warp takes a piece of the work for itself (16, or with tiles of 16
+// rows 12, on an SM), or each SM: with many tiles.
+inline bool attend_few_alone(int seqs, int heads) { return static_cast<long long>(seqs) * heads >= 2 * kAttendSms; }
+inline int attend_few_pieces(int rows, bool alone) { return kAttendSms * (alone ? (rows == 8 ? 16 : 12) : 1); }
 
 }  // namespace plan
 }  // namespace clover
