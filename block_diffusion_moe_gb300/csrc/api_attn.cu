@@ -167,6 +167,22 @@ FewLayout few_layout(int32_t rows, bool alone, int32_t head_dim) {
   return l;
 }
 
+// Workspace of the kernel on tiles, where a call may be cut.
+size_t tile_bytes(int32_t head_dim) {
+  return kCtrlBytes + static_cast<size_t>(plan::kAttendMaxPieces) * 256 * (8 + head_dim * 4);
+}
+
+// Fills in what the kernel on tiles needs besides a.
+int fill_tiles(AttendArgs* t, int32_t n_rows, int32_t n_seqs, int32_t head_dim, void* workspace) {
+  const AttnArgs& a = t->a;
+  t->tokens = 128 / a.group;
+  t->n_slots = n_rows / (2 * t->tokens) + n_seqs;
+  t->may_cut = plan::attend_may_cut(n_rows, a.group, a.c.heads);
+  t->part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + kCtrlBytes);
+  t->part = reinterpret_cast<float*>(t->part_ml + plan::kAttendMaxPieces * 256);
+  return encode_head_boxes(&t->tm_q, a.q.data, n_rows, a.q_heads, head_dim, a.q.row, a.q.head, a.group, t->tokens, "q");
+}
+
 // (for up to n_rows rows: calls of fewer may take tiles of 8 rows instead of 16)
 size_t cached_bytes(const clover_kv_cache& c, int32_t n_rows, int32_t q_heads, int32_t n_seqs, int32_t max_pages) {
   const int group = q_heads / c.kv_heads;
@@ -175,12 +191,11 @@ size_t cached_bytes(const clover_kv_cache& c, int32_t n_rows, int32_t q_heads, i
   if (group <= 8) most = std::max(most, few_layout(8, alone, c.head_dim).bytes);
   if (group <= 16 && plan::attend_few_rows(n_rows, group, n_seqs) == 16)
     most = std::max(most, few_layout(16, alone, c.head_dim).bytes);
+  if (!plan::attend_few(n_rows, group, n_seqs)) most = std::max(most, tile_bytes(c.head_dim));
   return most;
 }
 
-size_t prompt_bytes(int32_t n_rows, int32_t n_keys, int32_t n_seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
-  return kCtrlBytes;
-}
+size_t prompt_bytes(int32_t head_dim) { return tile_bytes(head_dim); }
 
 }  // namespace
 
@@ -275,13 +290,20 @@ int clover_kv_attention(const clover_kv_cache* cache, const clover_kv_seqs* seqs
                                       reinterpret_cast<cudaStream_t>(stream)),
                     "launch kv attention");
   }
-  return launched(launch_attention_simple(a, true, reinterpret_cast<cudaStream_t>(stream)), "launch kv attention");
+  int sms = 0;
+  if ((rc = device_sms(&sms))) return rc;
+  AttendArgs t;
+  memset(&t, 0, sizeof(t));
+  t.a = a;
+  if ((rc = fill_tiles(&t, n_rows, seqs->n_seqs, cache->head_dim, workspace))) return rc;
+  return launched(launch_attend(t, true, std::min(sms, plan::kAttendSms), reinterpret_cast<cudaStream_t>(stream)),
+                  "launch kv attention");
 }
 
 size_t clover_prompt_attention_workspace_bytes(int32_t n_rows, int32_t n_keys, int32_t n_seqs, int32_t q_heads,
                                                int32_t kv_heads, int32_t head_dim) {
   if (check_prompt(n_rows, n_keys, n_seqs, q_heads, kv_heads, head_dim)) return 0;
-  return prompt_bytes(n_rows, n_keys, n_seqs, q_heads, kv_heads, head_dim);
+  return prompt_bytes(head_dim);
 }
 
 int clover_prompt_attention(const clover_prompt_seqs* seqs, const clover_rows* q, const clover_rows* k,
@@ -292,7 +314,7 @@ int clover_prompt_attention(const clover_prompt_seqs* seqs, const clover_rows* q
   if (seqs == nullptr) return fail(CLOVER_ERR_INVALID_ARG, "seqs is NULL");
   if ((rc = check_prompt(n_rows, n_keys, seqs->n_seqs, q_heads, kv_heads, head_dim)) || (rc = check_rule(scale, block)) ||
       (rc = check_workspace(workspace, workspace_bytes,
-                            prompt_bytes(n_rows, n_keys, seqs->n_seqs, q_heads, kv_heads, head_dim))))
+                            prompt_bytes(head_dim))))
     return rc;
   if (n_rows == 0) return CLOVER_OK;
   AttnArgs a;
@@ -322,16 +344,16 @@ int clover_prompt_attention(const clover_prompt_seqs* seqs, const clover_rows* q
   AttendArgs t;
   memset(&t, 0, sizeof(t));
   t.a = a;
-  t.tokens = 128 / a.group;
-  t.n_slots = n_rows / (2 * t.tokens) + seqs->n_seqs;
-  if ((rc = encode_head_boxes(&t.tm_q, a.q.data, n_rows, q_heads, head_dim, a.q.row, a.q.head, a.group, t.tokens, "q")))
-    return rc;
+  if ((rc = fill_tiles(&t, n_rows, seqs->n_seqs, head_dim, workspace))) return rc;
   t.tm_k = t.tm_v = t.tm_q;  // without keys nothing is loaded through them
   if (n_keys > 0 &&
       ((rc = encode_head_boxes(&t.tm_k, a.k.data, n_keys, kv_heads, head_dim, a.k.row, a.k.head, 1, 128, "k")) ||
       (rc = encode_head_boxes(&t.tm_v, a.v.data, n_keys, kv_heads, head_dim, a.v.row, a.v.head, 1, 128, "v"))))
     return rc;
-  return launched(launch_attend(t, reinterpret_cast<cudaStream_t>(stream)), "launch prompt attention");
+  int sms = 0;
+  if ((rc = device_sms(&sms))) return rc;
+  return launched(launch_attend(t, false, std::min(sms, plan::kAttendSms), reinterpret_cast<cudaStream_t>(stream)),
+                  "launch prompt attention");
 }
 
 }  // extern "C"

@@ -1,17 +1,25 @@
-// Attention on tensor-core tiles (clover_prompt_attention).
+// Attention on tensor-core tiles: clover_prompt_attention, and
+// clover_kv_attention where a sequence has more than a few rows.
 //
-// One CTA takes two tiles of 128 query rows (the group's heads of consecutive
-// tokens of one sequence) over the keys they see, 128 at a time:
+// An item is two tiles of 128 query rows (the group's heads of consecutive tokens
+// of one sequence) over the keys they see, 128 at a time:
 //   S = Q K^T          tcgen05.mma, both operands from shared memory
 //   P = 2^(c S - m)    one thread per row: m a running maximum, l the sum of P
 //   O = O + P V        tcgen05.mma, P (16 bits) from tensor memory
 // and in the end O / l. m moves only where the row's maximum has grown by more
-// than 2^8 (O and l are scaled then); until then P is at most 2^8, which costs no
-// precision: numerators and sums are floating point.
+// than a limit (O and l are scaled then): numerators and sums are floating point,
+// so a P above 1 costs no precision.
 //
-// Roles: warps 0-3 and 4-7 the softmax of tile 0 and 1, warp 8 loads (TMA), warp
-// 9 issues the MMAs, warp 10 looks after the values no row may see. While one
-// tile's softmax runs, the tensor core works for the other.
+// Roles: warps 0-3 and 4-7 the softmax of tile 0 and 1, warp 8 loads, warp 9
+// issues the MMAs. While one tile's softmax runs, the tensor core works for the
+// other. Prompt: keys and values come as they are (TMA), and warp 10 looks after the
+// values that not every row may see. Cache: warp 8 copies pages' codes and scales,
+// and warps 12-15 expand them to fp16 tiles (exact), which takes a third of the
+// time of the MMAs that read them; queries become fp16 too, each row scaled by a
+// power of two so that its largest element is about 2^14.
+//
+// CTAs are persistent, one per SM. Where a call has fewer items than SMs, an item's
+// keys are cut into pieces, whose sums a second kernel joins.
 #include <math.h>
 
 #include "attn_ops.cuh"
@@ -22,52 +30,67 @@ namespace clover {
 
 namespace {
 
-constexpr int kThreads = 384;
 constexpr int kKeys = 128;  // keys per step
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;  // of tile t: + 128 t
-constexpr float kGrowth = 8.f;
+constexpr int kWholeItems = plan::kAttendSms;  // calls of as many items cut none
+constexpr int kMinSteps = 4;                   // of a piece
 
-template <int kDim>
+template <int kDim, bool kCached>
 struct Layout {
+  static constexpr int kThreads = kCached ? 512 : 384;
   static constexpr int kTileBytes = 128 * kDim * 2;  // of Q, of K, of V
   static constexpr int kSlab = 128 * 128;            // 64 elements of 128 rows
-  static constexpr int kStages = kDim == 128 ? 5 : 10;
+  static constexpr int kStages = (kCached ? 3 : 5) * (128 / kDim);
+  static constexpr int kSixteen = 18 * kDim;  // bytes of 16 tokens in the cache
+  static constexpr int kKs = 8 * kDim, kV = 9 * kDim, kVs = 17 * kDim;
+  static constexpr int kRawBytes = 8 * kSixteen;
+  static constexpr int kRaw = kCached ? 3 * (128 / kDim) : 0;  // steps' codes and scales
+  // Cache: numerators are 2^(c S - m + 11), m up to 2^4 behind: at most 2^15, and what
+  // fp16 rounds by more than half a step, or to 0, is 2^-36 of the largest.
+  static constexpr float kGrowth = kCached ? 4.f : 8.f, kLift = kCached ? 11.f : 0.f;
+  // the numerators lie where scores were that are in registers by then
+  static constexpr uint32_t kP = kCached ? 64 : 0;
 };
 
 struct Shared {
-  uint64_t q_full[2], full[10], empty[10];
-  uint64_t v_ok[10];  // a stage's values have been looked after
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], q_empty[2], q_ready[2];  // ready: converted (cache)
+  uint64_t full[10], empty[10];
+  uint64_t v_ok[10];  // a stage's values have been looked after (prompt)
+  uint64_t raw_full[6], raw_empty[6];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint64_t drain;
   uint32_t tmem, abort;
-  int poison;
+  int poison[16];  // of item k: [k % 16]
+  uint32_t there[16];  // of step k: sixteens that have a page (cache)
+  int sums[2][16];
 };
 
 // What a CTA works on.
 struct Item {
   SeqSpan sp;
-  int head;       // key/value head
+  int seq, head;
   int tok0;       // first token of tile 0 in the sequence; tile t: + t * tokens
   int n[2];       // steps of each tile
   int all, any;   // positions below `all` are seen by every row, none from `any` on
+  int j0, j1;     // the steps of this piece
+  int part, parts;
+  __device__ __forceinline__ int steps(int t) const { return max(min(j1, n[t]) - j0, 0); }
+  __device__ __forceinline__ int steps() const { return max(steps(0), steps(1)); }
+};
+
+// How a call is cut: every item whole, its slots counted from the offsets alone; or
+// in pieces of at most `chunk` steps.
+struct Cut {
+  int chunk;   // 0: whole
+  int pieces;  // (whole: slots, some of them empty)
 };
 
 __device__ __forceinline__ int seen_by(const AttendArgs& p, const SeqSpan& sp, int tok) {
   return seen(sp.len - sp.rows + tok, sp.len, p.a.block);
 }
 
-// Called by a whole warp. False: nothing to do.
-__device__ __forceinline__ bool item_of(const AttendArgs& p, Item* it) {
-  // the last tiles of a sequence see the most: they begin first
-  const int idx = gridDim.x - 1 - blockIdx.x;
-  const int slot = idx / p.a.c.heads, pair = 2 * p.tokens;
-  it->head = idx - slot * p.a.c.heads;
-  const int n = p.a.s.n_rows;
-  const int s = warp_search(p.a.s.n, slot, [&](int i) { return group_offset(p.a.s.offsets, i, n) / pair + i; });
-  it->sp = seq_span(p.a.s, s);
-  it->tok0 = (slot - (it->sp.row0 / pair + s)) * pair;
-  if (it->tok0 < 0 || it->tok0 >= it->sp.rows) return false;
+__device__ __forceinline__ void fill_item(const AttendArgs& p, Item* it) {
   it->any = 0;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -77,8 +100,129 @@ __device__ __forceinline__ bool item_of(const AttendArgs& p, Item* it) {
     it->any = max(it->any, lim);
   }
   it->all = seen_by(p, it->sp, it->tok0);
-  return true;
+  it->j0 = 0;
+  it->j1 = max(it->n[0], it->n[1]);
+  it->part = 0;
+  it->parts = 1;
 }
+
+// Pieces of an item of this many steps.
+__device__ __forceinline__ int pieces_of(int steps, int chunk) { return max(1, (steps + chunk - 1) / chunk); }
+
+__device__ __forceinline__ int steps_of_tile(const AttendArgs& p, const SeqSpan& sp, int tile) {
+  const int last = min((tile + 1) * 2 * p.tokens, sp.rows) - 1;
+  return (seen_by(p, sp, last) + kKeys - 1) / kKeys;
+}
+
+// Piece k, by a whole warp. False: an empty slot.
+__device__ bool locate(const AttendArgs& p, const Cut& cut, int k, Item* it) {
+  const int pair = 2 * p.tokens, n = p.a.s.n_rows;
+  if (cut.chunk == 0) {
+    // the last tiles of a sequence see the most: they come first
+    const int idx = cut.pieces - 1 - k, slot = idx / p.a.c.heads;
+    it->head = idx - slot * p.a.c.heads;
+    const int s = warp_search(p.a.s.n, slot, [&](int i) { return group_offset(p.a.s.offsets, i, n) / pair + i; });
+    it->seq = s;
+    it->sp = seq_span(p.a.s, s);
+    it->tok0 = (slot - (it->sp.row0 / pair + s)) * pair;
+    if (it->tok0 < 0 || it->tok0 >= it->sp.rows) return false;
+    fill_item(p, it);
+    return true;
+  }
+  const int lane = threadIdx.x & 31;
+  for (int s0 = 0; s0 < p.a.s.n; s0 += 32) {
+    int own = 0;
+    if (s0 + lane < p.a.s.n) {
+      const SeqSpan sp = seq_span(p.a.s, s0 + lane);
+      for (int t = 0; t * pair < sp.rows; ++t) own += pieces_of(steps_of_tile(p, sp, t), cut.chunk);
+      own *= p.a.c.heads;
+    }
+    int upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const int all = __shfl_sync(0xffffffffu, upto, 31);
+    if (k >= all) {
+      k -= all;
+      continue;
+    }
+    const int l = __ffs(__ballot_sync(0xffffffffu, upto > k)) - 1;
+    const int per_head = __shfl_sync(0xffffffffu, own, l) / p.a.c.heads;
+    k -= __shfl_sync(0xffffffffu, upto - own, l);
+    it->seq = s0 + l;
+    it->sp = seq_span(p.a.s, it->seq);
+    it->head = k / per_head;
+    k -= it->head * per_head;
+    for (int t = 0;; ++t) {
+      const int steps = steps_of_tile(p, it->sp, t), parts = pieces_of(steps, cut.chunk);
+      if (k < parts) {
+        it->tok0 = t * pair;
+        fill_item(p, it);
+        it->part = k;
+        it->parts = parts;
+        it->j0 = static_cast<int>(static_cast<int64_t>(steps) * k / parts);
+        it->j1 = static_cast<int>(static_cast<int64_t>(steps) * (k + 1) / parts);
+        return true;
+      }
+      k -= parts;
+    }
+  }
+  return false;
+}
+
+// Sum over the CTA's threads.
+__device__ __forceinline__ int cta_sum(int v, int* scratch) {
+  v = warp_sum_i(v);
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int all = 0;
+  for (int w = 0; w < blockDim.x / 32; ++w) all += scratch[w];
+  return all;
+}
+
+// How the call is cut, by all threads of a CTA; the same in every CTA. With `items`
+// of them and target > items pieces wanted, pieces of total / (target - items)
+// steps are at most `target`.
+__device__ Cut cut_call(const AttendArgs& p, int (&sums)[2][16]) {
+  const Cut whole = {0, p.n_slots * p.a.c.heads};
+  if (!p.may_cut) return whole;
+  const int pair = 2 * p.tokens;
+  int items = 0;
+  uint32_t own = 0;  // steps (what overflows belongs to too many items)
+  for (int i = threadIdx.x; i < p.a.s.n; i += blockDim.x) {
+    const SeqSpan sp = seq_span(p.a.s, i);
+    const int tiles = (sp.rows + pair - 1) / pair;
+    items += min(tiles, kWholeItems) * p.a.c.heads;
+    if (tiles < kWholeItems)
+      for (int t = 0; t < tiles; ++t) own += steps_of_tile(p, sp, t) * p.a.c.heads;
+  }
+  items = cta_sum(items, sums[0]);
+  if (items >= kWholeItems) return whole;
+  const int steps = cta_sum(static_cast<int>(own), sums[1]);
+  const int target = 2 * items <= kWholeItems ? kWholeItems : 2 * kWholeItems;
+  Cut cut;
+  cut.chunk = max(kMinSteps, (steps + target - items - 1) / (target - items));
+  int pieces = 0;
+  for (int i = threadIdx.x; i < p.a.s.n; i += blockDim.x) {
+    const SeqSpan sp = seq_span(p.a.s, i);
+    for (int t = 0; t * pair < sp.rows; ++t) pieces += pieces_of(steps_of_tile(p, sp, t), cut.chunk) * p.a.c.heads;
+  }
+  cut.pieces = cta_sum(pieces, sums[0]);  // (all have read it: there was a barrier between)
+  return cut;
+}
+
+// This CTA's pieces in turn: forth and back over the CTAs, so that no CTA always
+// has the longest.
+struct Turn {
+  int i = 0;
+  __device__ __forceinline__ int next() {
+    const int b = blockIdx.x, g = gridDim.x, k = i * g + (i & 1 ? g - 1 - b : b);
+    ++i;
+    return k;
+  }
+};
 
 __device__ __forceinline__ bool warp_wait(const AttendArgs& p, Shared* sh, uint64_t* bar, uint32_t parity) {
   if (__all_sync(0xffffffffu, mbar_wait(bar, parity, &sh->abort))) return true;
@@ -90,74 +234,125 @@ __device__ __forceinline__ bool warp_wait(const AttendArgs& p, Shared* sh, uint6
   return false;
 }
 
-// The ring's stages hold K of step 0, V of step 0, K of step 1, ...
-template <int kDim>
+// A ring's stages in turn. K and V ring: K of step 0, V of step 0, K of step 1, ...
+template <int kStages>
 struct Ring {
   int st = 0;
   uint32_t ph = 0;
   __device__ __forceinline__ void next(int by = 1) {
     st += by;
-    if (st >= Layout<kDim>::kStages) {
-      st -= Layout<kDim>::kStages;
+    if (st >= kStages) {
+      st -= kStages;
       ph ^= 1u;
     }
   }
 };
 
-template <int kDim>
-__device__ void load_role(const AttendArgs& p, Shared* sh, const Item& it, uint32_t q, uint32_t ring) {
-  using L = Layout<kDim>;
+// Copies of barriers that may be in flight when a role gives up.
+struct Flight {
+  uint32_t issued = 0, parity = 0;
+  __device__ __forceinline__ void add(int st, uint32_t ph) {
+    issued |= 1u << st;
+    parity = (parity & ~(1u << st)) | (ph << st);
+  }
+  __device__ __forceinline__ void land(uint64_t* bars) {
+    for (int i = 0; i < 32; ++i)
+      if (issued >> i & 1u) mbar_wait_for(&bars[i], parity >> i & 1u, 200000000ull);
+  }
+};
+
+template <int kDim, bool kCached>
+__device__ void load_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint32_t q, uint32_t ring, uint32_t raw) {
+  using L = Layout<kDim, kCached>;
+  const int lane = threadIdx.x & 31;
   const uint64_t keep = l2_policy_evict_last();
-  const int steps = max(it.n[0], it.n[1]);
-  if (elect_one()) {
+  Ring<kCached ? L::kRaw : L::kStages> r;
+  Flight flight, q_flight;
+  uint32_t q_count[2] = {0, 0};
+  int k_step = 0;  // steps so far, of all items
+  bool ok = true;
+  Turn turn;
+  Item it;
+  for (int k; ok && (k = turn.next()) < cut.pieces;) {
+    if (!locate(p, cut, k, &it)) continue;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if (it.n[t] == 0) continue;
-      mbar_arrive_expect_tx(&sh->q_full[t], kDim / 64 * p.a.group * p.tokens * 128);
+      if (!ok || it.steps(t) == 0) continue;
+      if (!(ok = warp_wait(p, sh, &sh->q_empty[t], (q_count[t] & 1) ^ 1u))) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&sh->q_full[t], kDim / 64 * p.a.group * p.tokens * 128);
 #pragma unroll
-      for (int d = 0; d < kDim / 64; ++d)
-        tma_load_3d(q + t * L::kTileBytes + d * L::kSlab, &p.tm_q, &sh->q_full[t], d * 64, it.head * p.a.group,
-                    it.sp.row0 + it.tok0 + t * p.tokens, keep);
+        for (int d = 0; d < kDim / 64; ++d)
+          tma_load_3d(q + t * L::kTileBytes + d * L::kSlab, &p.tm_q, &sh->q_full[t], d * 64, it.head * p.a.group,
+                      it.sp.row0 + it.tok0 + t * p.tokens, keep);
+      }
+      __syncwarp();
+      q_flight.add(t, q_count[t] & 1);
+      ++q_count[t];
     }
-  }
-  __syncwarp();
-  Ring<kDim> r;
-  uint32_t issued = 0, parity = 0;
-  for (int i = 0; i < 2 * steps; ++i) {
-    if (!warp_wait(p, sh, &sh->empty[r.st], r.ph ^ 1u)) break;
-    if (elect_one()) {
-      mbar_arrive_expect_tx(&sh->full[r.st], L::kTileBytes);
+    const int steps = it.steps();
+    if constexpr (!kCached) {
+      for (int i = 0; i < 2 * steps && ok; ++i, r.next()) {
+        if (!(ok = warp_wait(p, sh, &sh->empty[r.st], r.ph ^ 1u))) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sh->full[r.st], L::kTileBytes);
 #pragma unroll
-      for (int d = 0; d < kDim / 64; ++d)
-        tma_load_3d(ring + r.st * L::kTileBytes + d * L::kSlab, i & 1 ? &p.tm_v : &p.tm_k, &sh->full[r.st], d * 64, it.head,
-                    it.sp.key0 + (i >> 1) * kKeys, keep);
+          for (int d = 0; d < kDim / 64; ++d)
+            tma_load_3d(ring + r.st * L::kTileBytes + d * L::kSlab, i & 1 ? &p.tm_v : &p.tm_k, &sh->full[r.st], d * 64, it.head,
+                        it.sp.key0 + (it.j0 + (i >> 1)) * kKeys, keep);
+        }
+        __syncwarp();
+        flight.add(r.st, r.ph);
+      }
+    } else {
+      // lane i looks up the sixteen i % 8 of step i / 8 on, four steps at a time
+      const int per = p.a.c.page_tokens / 16;
+      int from = -1;
+      for (int i = 0; i < steps && ok; ++i, r.next(), ++k_step) {
+        if ((i & 3) == 0) {
+          const int x = (it.j0 + i) * 8 + lane;
+          from = -1;
+          if (x * 16 < it.any && i + (lane >> 3) < steps) {
+            const int entry = p.per_magic != 0 ? static_cast<int>(__umulhi(x, p.per_magic)) : x;
+            const int page = p.a.s.table[static_cast<int64_t>(it.seq) * p.a.s.max_pages + entry];
+            if (page >= 0 && page < p.a.c.n_pages) from = (page * p.a.c.heads + it.head) * per + (x - entry * per);
+          }
+        }
+        const int at = __shfl_sync(0xffffffffu, from, (i & 3) * 8 + (lane & 7));
+        const uint32_t has = __ballot_sync(0xffffffffu, at >= 0) & 0xFFu;
+        if (!(ok = warp_wait(p, sh, &sh->raw_empty[r.st], r.ph ^ 1u))) break;
+        if (lane == 0) {
+          *reinterpret_cast<volatile uint32_t*>(&sh->there[k_step & 15]) = has;
+          mbar_arrive_expect_tx(&sh->raw_full[r.st], __popc(has) * L::kSixteen);
+        }
+        __syncwarp();
+        if (lane < 8 && at >= 0)
+          bulk_load(raw + r.st * L::kRawBytes + lane * L::kSixteen, p.a.c.pages + static_cast<int64_t>(at) * L::kSixteen,
+                    L::kSixteen, &sh->raw_full[r.st]);
+        __syncwarp();
+        flight.add(r.st, r.ph);
+      }
     }
-    __syncwarp();
-    issued |= 1u << r.st;
-    parity = (parity & ~(1u << r.st)) | (r.ph << r.st);
-    r.next();
   }
   // the copies in flight must land before the CTA leaves
   if (*reinterpret_cast<volatile uint32_t*>(&sh->abort)) {
-    for (int i = 0; i < L::kStages; ++i)
-      if (issued & (1u << i)) mbar_wait_for(&sh->full[i], (parity >> i) & 1u, 200000000ull);
-    for (int t = 0; t < 2; ++t)
-      if (it.n[t] > 0) mbar_wait_for(&sh->q_full[t], 0, 200000000ull);
+    flight.land(kCached ? sh->raw_full : sh->full);
+    q_flight.land(sh->q_full);
   }
 }
 
-template <int kDim>
-__device__ void mma_role(const AttendArgs& p, Shared* sh, const Item& it, uint32_t q, uint32_t ring) {
-  using L = Layout<kDim>;
-  constexpr uint32_t kIdS = umma_idesc_bf16(128, kKeys), kIdO = umma_idesc_bf16(128, kDim) | kUmmaBMnMajor;
+template <int kDim, bool kCached>
+__device__ void mma_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint32_t q, uint32_t ring) {
+  using L = Layout<kDim, kCached>;
+  constexpr uint32_t kIdS = kCached ? umma_idesc_f16(128, kKeys) : umma_idesc_bf16(128, kKeys);
+  constexpr uint32_t kIdO = (kCached ? umma_idesc_f16(128, kDim) : umma_idesc_bf16(128, kDim)) | kUmmaBMnMajor;
   const uint32_t tmem = sh->tmem;
-  const int steps = max(it.n[0], it.n[1]);
-  const int first_masked = it.all / kKeys;  // steps from here on wait for the values to be looked after
-  Ring<kDim> rk, rv;
-  rv.next();
-  uint32_t v_parity = 0;
-  // tile t's scores of step j; the ring's rk holds its keys
-  auto scores = [&](int t) {
+  Ring<L::kStages> rk, rv;
+  uint32_t v_parity = 0, q_count[2] = {0, 0}, p_count[2] = {0, 0};
+  Turn turn;
+  Item it;
+  // tile t's scores of a step; the ring's rk holds its keys
+  auto scores = [&](int t, bool last) {
     if (elect_one()) {
       const uint64_t a = umma_desc_sw128(q + t * L::kTileBytes), b = umma_desc_sw128(ring + rk.st * L::kTileBytes);
 #pragma unroll
@@ -166,16 +361,17 @@ __device__ void mma_role(const AttendArgs& p, Shared* sh, const Item& it, uint32
         umma_bf16(tmem + kTmemS + t * 128, a + o, b + o, kIdS, s > 0);
       }
       umma_commit(&sh->s_full[t]);
+      if (last) umma_commit(&sh->q_empty[t]);
     }
     __syncwarp();
   };
-  auto sums = [&](int t, int j) {
+  auto sums = [&](int t, bool first, bool last) {
     if (elect_one()) {
       const uint64_t b = umma_desc_sw128_mn(ring + rv.st * L::kTileBytes, L::kSlab);
 #pragma unroll
       for (int s = 0; s < kKeys / 16; ++s)
-        umma_bf16_ta(tmem + kTmemO + t * 128, tmem + kTmemS + t * 128 + s * 8, b + s * 128, kIdO, j > 0 || s > 0);
-      if (j + 1 == it.n[t]) umma_commit(&sh->o_full[t]);
+        umma_bf16_ta(tmem + kTmemO + t * 128, tmem + kTmemS + t * 128 + L::kP + s * 8, b + s * 128, kIdO, !first || s > 0);
+      if (last) umma_commit(&sh->o_full[t]);
     }
     __syncwarp();
   };
@@ -184,36 +380,48 @@ __device__ void mma_role(const AttendArgs& p, Shared* sh, const Item& it, uint32
     __syncwarp();
   };
   bool ok = true;
-  for (int t = 0; t < 2 && ok; ++t)
-    if (it.n[t] > 0) ok = warp_wait(p, sh, &sh->q_full[t], 0);
-  if (ok) ok = warp_wait(p, sh, &sh->full[rk.st], rk.ph);
-  if (ok) {
+  for (int k; ok && (k = turn.next()) < cut.pieces;) {
+    if (!locate(p, cut, k, &it)) continue;
+    const int steps = it.steps();
+    if (steps == 0) continue;
+    const int first_masked = it.all / kKeys - it.j0;  // steps from here on wait for the values to be looked after
+    const int n[2] = {it.steps(0), it.steps(1)};
+    rv = rk;
+    rv.next();
+    for (int t = 0; t < 2 && ok; ++t)
+      if (n[t] > 0) ok = warp_wait(p, sh, kCached ? &sh->q_ready[t] : &sh->q_full[t], q_count[t] & 1);
+    if (ok) ok = warp_wait(p, sh, &sh->full[rk.st], rk.ph);
+    if (!ok) break;
     tc_fence_after();
     for (int t = 0; t < 2; ++t)
-      if (it.n[t] > 0) scores(t);
+      if (n[t] > 0) scores(t, n[t] == 1);
     release(rk.st);
-  }
-  for (int j = 0; j < steps && ok; ++j) {
-    rk.next(2);
-    const bool more = j + 1 < steps;
-    ok = warp_wait(p, sh, &sh->full[rv.st], rv.ph);
-    if (ok && j >= first_masked) {
-      ok = warp_wait(p, sh, &sh->v_ok[rv.st], (v_parity >> rv.st) & 1u);
-      v_parity ^= 1u << rv.st;
-    }
-    if (ok && more) ok = warp_wait(p, sh, &sh->full[rk.st], rk.ph);
-    for (int t = 0; t < 2 && ok; ++t) {
-      if (j >= it.n[t]) continue;
-      ok = warp_wait(p, sh, &sh->p_full[t], j & 1);
+    for (int j = 0; j < steps && ok; ++j) {
+      rk.next(2);
+      const bool more = j + 1 < steps;
+      ok = warp_wait(p, sh, &sh->full[rv.st], rv.ph);
+      if (!kCached && ok && j >= first_masked) {
+        ok = warp_wait(p, sh, &sh->v_ok[rv.st], (v_parity >> rv.st) & 1u);
+        v_parity ^= 1u << rv.st;
+      }
+      if (ok && more) ok = warp_wait(p, sh, &sh->full[rk.st], rk.ph);
+      for (int t = 0; t < 2 && ok; ++t) {
+        if (j >= n[t]) continue;
+        // the sums of the item before are read
+        if (j == 0) ok = warp_wait(p, sh, &sh->o_empty[t], (q_count[t] & 1) ^ 1u);
+        if (ok) ok = warp_wait(p, sh, &sh->p_full[t], p_count[t] & 1);
+        if (!ok) break;
+        ++p_count[t];
+        tc_fence_after();
+        sums(t, j == 0, j + 1 == n[t]);
+        if (j + 1 < n[t]) scores(t, j + 2 == n[t]);
+      }
       if (!ok) break;
-      tc_fence_after();
-      sums(t, j);
-      if (j + 1 < it.n[t]) scores(t);
+      release(rv.st);
+      if (more) release(rk.st);
+      rv.next(2);
     }
-    if (!ok) break;
-    release(rv.st);
-    if (more) release(rk.st);
-    rv.next(2);
+    for (int t = 0; t < 2; ++t) q_count[t] += n[t] > 0;
   }
   if (elect_one()) umma_commit(&sh->drain);
   __syncwarp();
@@ -225,203 +433,417 @@ __device__ void mma_role(const AttendArgs& p, Shared* sh, const Item& it, uint32
 // infinities and NaN among the others, which the end of the softmax role adds
 // to the rows that do see them.
 template <int kDim>
-__device__ void guard_role(const AttendArgs& p, Shared* sh, const Item& it, uint8_t* ring) {
-  using L = Layout<kDim>;
-  const int lane = threadIdx.x & 31, steps = max(it.n[0], it.n[1]);
-  Ring<kDim> r;
-  // every stage in turn, keys and whole steps too: who leaves one out can take a
-  // later phase of its barrier for the one it waits for
-  for (int i = 0; i < 2 * steps; ++i, r.next()) {
-    if (!warp_wait(p, sh, &sh->full[r.st], r.ph)) return;
-    const int j = i >> 1;
-    if (i % 2 == 0 || (j + 1) * kKeys <= it.all) {
-      if (lane == 0) mbar_arrive(&sh->empty[r.st]);
-      continue;
-    }
-    uint8_t* v = ring + r.st * L::kTileBytes;
-    const int lo = max(it.all - j * kKeys, 0), hi = min(it.any - j * kKeys, kKeys);
-    constexpr int kPer = kDim / 8;  // 16-byte pieces of a row
-    uint32_t top = 0;
-    const int n = (hi - lo) * kPer;
-#pragma unroll 4
-    for (int k = lane; k < n; k += 32) {
-      const int row = lo + k / kPer, c = k % kPer;
-      const uint4 x = *reinterpret_cast<const uint4*>(v + (c / 8) * L::kSlab + row * 128 + (c % 8) * 16);
-      top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
-    }
-    if (__any_sync(0xffffffffu, (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u)) {
-      for (int k = lane; k < (hi - lo) * kDim; k += 32) {
-        const int row = lo + k / kDim, d = k % kDim;
-        uint16_t* x = reinterpret_cast<uint16_t*>(v + (d / 64) * L::kSlab + row * 128 + ((d % 64 / 8) ^ (row & 7)) * 16) + d % 8;
-        if ((*x & 0x7F80u) == 0x7F80u) *x = 0;
-      }
-      if (lane == 0) *reinterpret_cast<volatile int*>(&sh->poison) = 1;
-    }
-    for (int k = lane; k < (kKeys - hi) * kPer; k += 32) {
-      const int row = hi + k / kPer, c = k % kPer;
-      *reinterpret_cast<uint4*>(v + (c / 8) * L::kSlab + row * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
-    }
-    fence_proxy_async_shared();
+__device__ void guard_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint8_t* ring) {
+  using L = Layout<kDim, false>;
+  const int lane = threadIdx.x & 31;
+  Ring<L::kStages> r;
+  Turn turn;
+  Item it;
+  for (int k, item = -1; (k = turn.next()) < cut.pieces;) {
+    if (!locate(p, cut, k, &it) || it.steps() == 0) continue;
+    // (items with steps are counted; of a ring of 16, eight on, or back, is out of
+    // everyone's reach)
+    ++item;
+    if (lane == 0) *reinterpret_cast<volatile int*>(&sh->poison[(item + 8) & 15]) = 0;
     __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(&sh->v_ok[r.st]);
-      mbar_arrive(&sh->empty[r.st]);
+    // every stage in turn, keys and whole steps too: who leaves one out can take a
+    // later phase of its barrier for the one it waits for
+    for (int i = 0; i < 2 * it.steps(); ++i, r.next()) {
+      if (!warp_wait(p, sh, &sh->full[r.st], r.ph)) return;
+      const int j = it.j0 + (i >> 1);
+      if (i % 2 == 0 || (j + 1) * kKeys <= it.all) {
+        if (lane == 0) mbar_arrive(&sh->empty[r.st]);
+        continue;
+      }
+      uint8_t* v = ring + r.st * L::kTileBytes;
+      const int lo = max(it.all - j * kKeys, 0), hi = min(it.any - j * kKeys, kKeys);
+      constexpr int kPer = kDim / 8;  // 16-byte pieces of a row
+      uint32_t top = 0;
+      const int n = (hi - lo) * kPer;
+#pragma unroll 4
+      for (int e = lane; e < n; e += 32) {
+        const int row = lo + e / kPer, c = e % kPer;
+        const uint4 x = *reinterpret_cast<const uint4*>(v + (c / 8) * L::kSlab + row * 128 + (c % 8) * 16);
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+      }
+      if (__any_sync(0xffffffffu, (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u)) {
+        for (int e = lane; e < (hi - lo) * kDim; e += 32) {
+          const int row = lo + e / kDim, d = e % kDim;
+          uint16_t* x = reinterpret_cast<uint16_t*>(v + (d / 64) * L::kSlab + row * 128 + ((d % 64 / 8) ^ (row & 7)) * 16) + d % 8;
+          if ((*x & 0x7F80u) == 0x7F80u) *x = 0;
+        }
+        if (lane == 0) *reinterpret_cast<volatile int*>(&sh->poison[item & 15]) = 1;
+      }
+      for (int e = lane; e < (kKeys - hi) * kPer; e += 32) {
+        const int row = hi + e / kPer, c = e % kPer;
+        *reinterpret_cast<uint4*>(v + (c / 8) * L::kSlab + row * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh->v_ok[r.st]);
+        mbar_arrive(&sh->empty[r.st]);
+      }
     }
   }
 }
 
+// One tile of 128 rows from a step's codes: 4 warps, a lane takes 16 codes (one
+// scale) of a key at a time. Neighbouring lanes take one key's codes, so that reads
+// do not meet in a bank; of the two 16-byte pieces a lane writes, the upper half of
+// a 128-element key swaps the order, so that writes do not either.
+// kValues: the bytes of positions pos + .. that are not to count are replaced.
+template <int kDim, bool kValues>
+__device__ __forceinline__ bool expand_tile(const uint8_t* raw, uint8_t* tile, int warp, uint32_t there, int all, int any, int pos) {
+  using L = Layout<kDim, true>;
+  constexpr int kPer = kDim / 16;            // lanes of a key
+  constexpr int kRows = 32 / kPer;           // keys of a warp at a time
+  const int lane = threadIdx.x & 31, c = lane % kPer, swap = kDim == 128 && c >= 4;
+  bool poison = false;
+#pragma unroll 4
+  for (int i = 0; i < 32 / kRows; ++i) {
+    const int row = warp * 32 + i * kRows + lane / kPer, in = row & 15;
+    const uint8_t* six = raw + (row >> 4) * L::kSixteen + (kValues ? L::kV : 0);
+    const uint2 w = *reinterpret_cast<const uint2*>(six + in * (kDim / 2) + c * 8);
+    uint32_t b = six[8 * kDim + in * kPer + c];
+    if (kValues) {
+      if (pos + row >= any || !(there >> (row >> 4) & 1u)) b = 0;
+      if (pos + row >= all && (b & 0x7Fu) == 0x7Fu) {
+        poison = true;
+        b = 0;
+      }
+    }
+    const __half2 s = __low2half2(scales2(b));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      __half2 v[4];
+      expand_word((h ^ swap) ? w.y : w.x, v);
+      uint4 o;
+      o.x = half2_word(__hmul2(v[0], s));
+      o.y = half2_word(__hmul2(v[1], s));
+      o.z = half2_word(__hmul2(v[2], s));
+      o.w = half2_word(__hmul2(v[3], s));
+      const int chunk = 2 * c + (h ^ swap);
+      *reinterpret_cast<uint4*>(tile + (chunk / 8) * L::kSlab + row * 128 + ((chunk & 7) ^ (row & 7)) * 16) = o;
+    }
+  }
+  return poison;
+}
+
 template <int kDim>
-__device__ void softmax_role(const AttendArgs& p, Shared* sh, const Item& it, int t) {
+__device__ void expand_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint8_t* ring, const uint8_t* raw) {
+  using L = Layout<kDim, true>;
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  Ring<L::kStages> r;
+  Ring<L::kRaw> rr;
+  int k_step = 0;
+  Turn turn;
+  Item it;
+  for (int k, item = -1; (k = turn.next()) < cut.pieces;) {
+    if (!locate(p, cut, k, &it) || it.steps() == 0) continue;
+    ++item;
+    if (warp == 0 && lane == 0) *reinterpret_cast<volatile int*>(&sh->poison[(item + 8) & 15]) = 0;
+    __syncwarp();
+    for (int i = 0; i < it.steps(); ++i, rr.next(), ++k_step) {
+      if (!warp_wait(p, sh, &sh->raw_full[rr.st], rr.ph)) return;
+      const uint32_t there = *reinterpret_cast<volatile uint32_t*>(&sh->there[k_step & 15]);
+      const uint8_t* from = raw + rr.st * L::kRawBytes;
+      const int pos = (it.j0 + i) * kKeys;
+#pragma unroll
+      for (int v = 0; v < 2; ++v, r.next()) {
+        if (!warp_wait(p, sh, &sh->empty[r.st], r.ph ^ 1u)) return;
+        uint8_t* tile = ring + r.st * L::kTileBytes;
+        if (v == 0) {
+          expand_tile<kDim, false>(from, tile, warp, there, 0, 0, 0);
+        } else if (there == 0xFFu && pos + kKeys <= it.all) {
+          expand_tile<kDim, true>(from, tile, warp, 0xFFu, 0x7fffffff, 0x7fffffff, 0);
+        } else if (__any_sync(0xffffffffu, expand_tile<kDim, true>(from, tile, warp, there, it.all, it.any, pos))) {
+          if (lane == 0) *reinterpret_cast<volatile int*>(&sh->poison[item & 15]) = 1;
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->full[r.st]);
+      }
+      if (lane == 0) mbar_arrive(&sh->raw_empty[rr.st]);
+    }
+  }
+}
+
+// The row of Q that a thread of the softmax owns to fp16, scaled by a power of two;
+// returns the factor's inverse exponent.
+template <int kDim>
+__device__ __forceinline__ int convert_row(uint8_t* q, int r) {
+  using L = Layout<kDim, true>;
+  uint32_t top = 0;  // the largest finite magnitude, as bits
+#pragma unroll 4
+  for (int c = 0; c < kDim / 8; ++c) {
+    const uint4 x = *reinterpret_cast<const uint4*>(q + (c / 8) * L::kSlab + r * 128 + (c % 8) * 16);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = w[i] << 16 & 0x7FFF0000u, hi = w[i] & 0x7FFF0000u;
+      top = max(top, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
+    }
+  }
+  const int e = top != 0 ? ilogbf(__uint_as_float(top)) - 14 : 0;
+  const float f0 = scalbnf(1.f, -e / 2), f1 = scalbnf(1.f, -e - -e / 2);  // (2^-e itself may leave fp32's range)
+#pragma unroll 4
+  for (int c = 0; c < kDim / 8; ++c) {
+    uint4* at = reinterpret_cast<uint4*>(q + (c / 8) * L::kSlab + r * 128 + (c % 8) * 16);
+    const uint4 x = *at;
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = half2_word(__floats2half2_rn(__uint_as_float(w[i] << 16) * f0 * f1, __uint_as_float(w[i] & 0xFFFF0000u) * f0 * f1));
+    *at = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  return e;
+}
+
+// Numerators of 64 scores: 32 words of pairs, and their sum.
+template <bool kHalf>
+__device__ __forceinline__ float numerators(const uint32_t (&s)[2][32], float c, float lift, uint32_t (&w)[32]) {
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const float a = exp2_fast(fmaf(__uint_as_float(s[k / 16][2 * k % 32]), c, lift));
+    const float b = exp2_fast(fmaf(__uint_as_float(s[k / 16][2 * k % 32 + 1]), c, lift));
+    sum[(2 * k) & 3] += a;
+    sum[(2 * k + 1) & 3] += b;
+    if (kHalf) {
+      w[k] = half2_word(__floats2half2_rn(a, b));
+    } else {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+      w[k] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+  }
+  return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+
+// Scores of 64 keys from key `at` of the step on that the row does not see: -inf.
+__device__ __forceinline__ void mask(uint32_t (&s)[2][32], int at, int left, uint32_t there) {
+#pragma unroll
+  for (int i = 0; i < 64; ++i)
+    if (at + i >= left || !(there >> ((at + i) / 16) & 1u)) s[i / 32][i % 32] = 0xFF800000u;
+}
+
+__device__ __forceinline__ float largest(const uint32_t (&s)[2][32]) {
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(s[i / 32][i % 32]));
+  return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+}
+
+template <int kDim, bool kCached>
+__device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, int t, uint8_t* q) {
+  using L = Layout<kDim, kCached>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x & 127;
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
   const uint32_t s_at = sh->tmem + kTmemS + t * 128 + lanes, o_at = sh->tmem + kTmemO + t * 128 + lanes;
-  const int tok_in = r / p.a.group, tok = it.tok0 + t * p.tokens + tok_in;
-  const bool mine = tok_in < p.tokens && tok < it.sp.rows;
-  const int lim = mine ? seen_by(p, it.sp, tok) : 0;
-  int whole = mine ? lim : 0x7fffffff;  // every row of the warp sees the positions below
+  const int tok_in = r / p.a.group, head_in = r - tok_in * p.a.group;
+  uint32_t s_count = 0, q_count = 0;
+  int k_step = 0;
+  Turn turn;
+  Item it;
+  for (int k, item = -1; (k = turn.next()) < cut.pieces;) {
+    if (!locate(p, cut, k, &it)) continue;
+    const int tok = it.tok0 + t * p.tokens + tok_in;
+    const bool mine = tok_in < p.tokens && tok < it.sp.rows;
+    const int lim = mine ? seen_by(p, it.sp, tok) : 0;
+    int whole = mine ? lim : 0x7fffffff;  // every row of the warp sees the positions below
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) whole = min(whole, __shfl_xor_sync(0xffffffffu, whole, o));
-  const float c = p.a.scale_log2;
-  float m = -INFINITY, l = 0.f;  // m: of c S
-  const int n = it.n[t];
-  for (int j = 0; j < n; ++j) {
-    if (!warp_wait(p, sh, &sh->s_full[t], j & 1)) return;
-    tc_fence_after();
-    uint32_t s[4][32];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) tmem_ld32_async(s_at + i * 32, s[i]);
-    tmem_wait_ld(s);
-    if ((j + 1) * kKeys > whole) {
-      const int left = lim - j * kKeys;
-#pragma unroll
-      for (int i = 0; i < 128; ++i)
-        if (i >= left) s[i / 32][i % 32] = 0xFF800000u;
+    for (int o = 16; o > 0; o >>= 1) whole = min(whole, __shfl_xor_sync(0xffffffffu, whole, o));
+    float c = p.a.scale_log2;
+    float m = -INFINITY, l = 0.f;  // m: of c S
+    const int n = it.steps(t), steps = it.steps();
+    item += steps > 0;
+    if (kCached && n > 0) {
+      if (!warp_wait(p, sh, &sh->q_full[t], q_count & 1)) return;
+      const int e = convert_row<kDim>(q + t * L::kTileBytes, r);
+      c = fminf(fmaxf(scalbnf(c, e), 1.4e-45f), 3.4028234e38f);
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->q_ready[t]);
     }
-    float top[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      top[i] = __uint_as_float(s[i][0]);
-#pragma unroll
-      for (int k = 1; k < 32; ++k) top[i] = fmaxf(top[i], __uint_as_float(s[i][k]));
-    }
-    const float m1 = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-    if (__any_sync(0xffffffffu, m1 - m > kGrowth)) {
-      const float up = fmaxf(m, m1);
-      const float f = m == up ? 1.f : exp2_fast(m - up);
-      m = up;
-      l *= f;
-      if (j > 0) {
+    for (int i = 0; i < n; ++i) {
+      if (!warp_wait(p, sh, &sh->s_full[t], s_count & 1)) return;
+      ++s_count;
+      tc_fence_after();
+      const int j = it.j0 + i, left = lim - j * kKeys;
+      const uint32_t there = kCached ? *reinterpret_cast<volatile uint32_t*>(&sh->there[(k_step + i) & 15]) : 0xFFu;
+      const bool masked = (j + 1) * kKeys > whole || (kCached && there != 0xFFu);
+      uint32_t lo[2][32], hi[2][32];
+      tmem_ld32_async(s_at, lo[0]);
+      tmem_ld32_async(s_at + 32, lo[1]);
+      if (!kCached) {
+        tmem_ld32_async(s_at + 64, hi[0]);
+        tmem_ld32_async(s_at + 96, hi[1]);
+      }
+      tmem_wait_ld(lo);
+      if (masked) mask(lo, 0, left, there);
+      float top = largest(lo);
+      if (kCached) {
+        tmem_ld32_async(s_at + 64, hi[0]);
+        tmem_ld32_async(s_at + 96, hi[1]);
+      }
+      tmem_wait_ld(hi);
+      if (masked) mask(hi, 64, left, there);
+      top = fmaxf(top, largest(hi)) * c;
+      if (__any_sync(0xffffffffu, top - m > L::kGrowth)) {
+        const float up = fmaxf(m, top);
+        const float f = m == up ? 1.f : exp2_fast(m - up);
+        m = up;
+        l *= f;
+        if (i > 0) {
 #pragma unroll 1
-        for (int i = 0; i < kDim / 32; ++i) {
-          uint32_t o[1][32];
-          tmem_ld32_async(o_at + i * 32, o[0]);
-          tmem_wait_ld(o);
+          for (int d = 0; d < kDim / 32; ++d) {
+            uint32_t o[1][32];
+            tmem_ld32_async(o_at + d * 32, o[0]);
+            tmem_wait_ld(o);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[0][k] = __float_as_uint(__uint_as_float(o[0][k]) * f);
-          tmem_st32(o_at + i * 32, o[0]);
+            for (int x = 0; x < 32; ++x) o[0][x] = __float_as_uint(__uint_as_float(o[0][x]) * f);
+            tmem_st32(o_at + d * 32, o[0]);
+          }
         }
       }
-    }
-    const float base = m == -INFINITY ? 0.f : m;
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
+      const float lift = L::kLift - (m == -INFINITY ? 0.f : m);
       uint32_t w[32];
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const int i = 64 * h + 2 * k;
-        const float a = exp2_fast(fmaf(__uint_as_float(s[i / 32][i % 32]), c, -base));
-        const float b = exp2_fast(fmaf(__uint_as_float(s[(i + 1) / 32][(i + 1) % 32]), c, -base));
-        sum[(2 * k) & 3] += a;
-        sum[(2 * k + 1) & 3] += b;
-        const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
-        w[k] = *reinterpret_cast<const uint32_t*>(&x);
+      l += numerators<kCached>(hi, c, lift, w);
+      tmem_st32(s_at + L::kP + 32, w);
+      if (kCached) {  // (registers do not hold all scores beside the roles that share them: half are read again)
+        tmem_ld32_async(s_at, lo[0]);
+        tmem_ld32_async(s_at + 32, lo[1]);
+        tmem_wait_ld(lo);
+        if (masked) mask(lo, 0, left, there);
       }
-      tmem_st32(s_at + h * 32, w);
+      l += numerators<kCached>(lo, c, lift, w);
+      tmem_st32(s_at + L::kP, w);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->p_full[t]);
     }
-    tmem_wait_st();
-    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh->p_full[t]);
-  }
-  if (n > 0 && !warp_wait(p, sh, &sh->o_full[t], 0)) return;
-  tc_fence_after();
-  const int64_t at = (static_cast<int64_t>(it.sp.row0 + tok) * p.a.q_heads + it.head * p.a.group + (r - tok_in * p.a.group));
-  const float inv = l == 0.f ? 0.f : p.a.c.v_mul / l;
-  const bool poison = *reinterpret_cast<volatile int*>(&sh->poison) != 0;
+    k_step += steps;
+    if (n > 0) {
+      if (!warp_wait(p, sh, &sh->o_full[t], q_count & 1)) return;
+      ++q_count;
+    }
+    tc_fence_after();
+    const int64_t at = static_cast<int64_t>(it.sp.row0 + tok) * p.a.q_heads + it.head * p.a.group + head_in;
+    const bool part = it.parts > 1;
+    const float f = part ? 1.f : (l == 0.f ? 0.f : p.a.c.v_mul / l);
+    const bool poison = steps > 0 && *reinterpret_cast<volatile int*>(&sh->poison[item & 15]) != 0;
+    float* to_part = p.part + ((static_cast<int64_t>(k) * 2 + t) * 128 + r) * kDim;
 #pragma unroll 1
-  for (int i = 0; i < kDim / 32; ++i) {
-    uint32_t o[1][32];
+    for (int i = 0; i < kDim / 32; ++i) {
+      uint32_t o[1][32];
+      __syncwarp();
+      if (n > 0) {
+        tmem_ld32_async(o_at + i * 32, o[0]);
+        tmem_wait_ld(o);
+      }
+#pragma unroll
+      for (int x = 0; x < 32; ++x) o[0][x] = n > 0 ? __float_as_uint(__uint_as_float(o[0][x]) * f) : 0u;
+      if (!mine) continue;
+      if (poison) {
+        for (int j = max(it.all, it.j0 * kKeys); j < min(lim, it.j1 * kKeys); ++j) {
+          if (kCached) {
+            const uint8_t* six = kv_sixteen(p.a.c, p.a.s, it.seq, it.head, j);
+#pragma unroll
+            for (int x = 0; x < 32; x += 16)
+              if (six != nullptr && (six[L::kVs + j % 16 * (kDim / 16) + (i * 32 + x) / 16] & 0x7F) == 0x7F)
+#pragma unroll
+                for (int y = 0; y < 16; ++y) o[0][x + y] = 0x7FC00000u;
+          } else {
+            const uint16_t* v = reinterpret_cast<const uint16_t*>(p.a.v.data + (it.sp.key0 + j) * p.a.v.row + it.head * p.a.v.head);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const uint32_t b = v[i * 32 + x];
+              if ((b & 0x7F80u) == 0x7F80u) o[0][x] = __float_as_uint(__uint_as_float(o[0][x]) + __uint_as_float(b << 16));
+            }
+          }
+        }
+      }
+      if (part) {
+#pragma unroll
+        for (int x = 0; x < 32; x += 8) store32b(to_part + i * 32 + x, true, *reinterpret_cast<uint32_t(*)[8]>(&o[0][x]));
+        continue;
+      }
+      uint32_t w[2][8];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(o[0][2 * x]), __uint_as_float(o[0][2 * x + 1]));
+        w[x / 8][x % 8] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+      store32b(p.a.out + at * kDim + i * 32, p.a.wide_out, w[0]);
+      store32b(p.a.out + at * kDim + i * 32 + 16, p.a.wide_out, w[1]);
+    }
     __syncwarp();
     if (n > 0) {
-      tmem_ld32_async(o_at + i * 32, o[0]);
-      tmem_wait_ld(o);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->o_empty[t]);
     }
-#pragma unroll
-    for (int k = 0; k < 32; ++k) o[0][k] = n > 0 ? __float_as_uint(__uint_as_float(o[0][k]) * inv) : 0u;
-    if (!mine) continue;
-    if (poison) {
-      for (int j = it.all; j < lim; ++j) {
-        const uint16_t* v = reinterpret_cast<const uint16_t*>(p.a.v.data + (it.sp.key0 + j) * p.a.v.row + it.head * p.a.v.head);
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const uint32_t x = v[i * 32 + k];
-          if ((x & 0x7F80u) == 0x7F80u) o[0][k] = __float_as_uint(__uint_as_float(o[0][k]) + __uint_as_float(x << 16));
-        }
-      }
+    m -= L::kLift;
+    if (part) {
+      p.part_ml[(static_cast<int64_t>(k) * 2 + t) * 128 + r] = make_float2(m, l);
+    } else if (mine && p.a.lse != nullptr) {
+      p.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
-    uint32_t w[2][8];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(o[0][2 * k]), __uint_as_float(o[0][2 * k + 1]));
-      w[k / 8][k % 8] = *reinterpret_cast<const uint32_t*>(&x);
-    }
-    store32b(p.a.out + at * kDim + i * 32, p.a.wide_out, w[0]);
-    store32b(p.a.out + at * kDim + i * 32 + 16, p.a.wide_out, w[1]);
+    __syncwarp();
   }
-  if (mine && p.a.lse != nullptr) p.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 }  // namespace
 
-template <int kDim>
-__global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ AttendArgs p) {
-  using L = Layout<kDim>;
-  extern __shared__ uint8_t raw[];
-  uint8_t* q = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+template <int kDim, bool kCached>
+__global__ void __launch_bounds__(Layout<kDim, kCached>::kThreads, 1) k_attend(const __grid_constant__ AttendArgs p) {
+  using L = Layout<kDim, kCached>;
+  extern __shared__ uint8_t smem[];
+  uint8_t* q = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u);
   uint8_t* ring = q + 2 * L::kTileBytes;
-  Shared* sh = reinterpret_cast<Shared*>(ring + L::kStages * L::kTileBytes);
+  uint8_t* raw = ring + L::kStages * L::kTileBytes;
+  Shared* sh = reinterpret_cast<Shared*>(raw + L::kRaw * L::kRawBytes);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh->q_full[t], 1);
+      mbar_init(&sh->q_empty[t], 1);
+      mbar_init(&sh->q_ready[t], 4);
       mbar_init(&sh->s_full[t], 1);
       mbar_init(&sh->p_full[t], 4);
       mbar_init(&sh->o_full[t], 1);
+      mbar_init(&sh->o_empty[t], 4);
     }
     for (int i = 0; i < L::kStages; ++i) {
-      mbar_init(&sh->full[i], 1);
-      mbar_init(&sh->empty[i], 2);  // the MMAs that read it, and the guard
+      mbar_init(&sh->full[i], kCached ? 4 : 1);   // expanding warps, or the copy
+      mbar_init(&sh->empty[i], kCached ? 1 : 2);  // the MMAs that read it, and the guard
       mbar_init(&sh->v_ok[i], 1);
+    }
+    for (int i = 0; i < L::kRaw; ++i) {
+      mbar_init(&sh->raw_full[i], 1);
+      mbar_init(&sh->raw_empty[i], 4);
     }
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
-    sh->poison = 0;
+    for (int i = 0; i < 16; ++i) sh->poison[i] = 0;
     fence_mbar_init();
   }
   if (warp == 8) {
     if (elect_one()) {
       tma_prefetch_desc(&p.tm_q);
-      tma_prefetch_desc(&p.tm_k);
-      tma_prefetch_desc(&p.tm_v);
+      if (!kCached) {
+        tma_prefetch_desc(&p.tm_k);
+        tma_prefetch_desc(&p.tm_v);
+      }
     }
     __syncwarp();
   }
   pdl_wait();
   pdl_trigger();
-  Item it;
-  if (!item_of(p, &it)) return;  // the whole CTA
+  const Cut cut = cut_call(p, sh->sums);
+  if (blockIdx.x >= cut.pieces) return;  // the whole CTA
   if (warp == 9) {
     tmem_alloc(&sh->tmem, kTmemCols);
     tmem_relinquish();
@@ -430,16 +852,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   if (warp < 8) {
-    regs_inc<216>();
-    softmax_role<kDim>(p, sh, it, warp >> 2);
+    if (!kCached) regs_inc<216>();
+    softmax_role<kDim, kCached>(p, sh, cut, warp >> 2, q);
   } else {
-    regs_dec<72>();
+    if (!kCached) regs_dec<72>();
     if (warp == 8)
-      load_role<kDim>(p, sh, it, smem_u32(q), smem_u32(ring));
-    else if (warp == 9 && max(it.n[0], it.n[1]) > 0)
-      mma_role<kDim>(p, sh, it, smem_u32(q), smem_u32(ring));
-    else if (warp == 10)
-      guard_role<kDim>(p, sh, it, ring);
+      load_role<kDim, kCached>(p, sh, cut, smem_u32(q), smem_u32(ring), smem_u32(raw));
+    else if (warp == 9)
+      mma_role<kDim, kCached>(p, sh, cut, smem_u32(q), smem_u32(ring));
+    else if (!kCached && warp == 10)
+      guard_role<kDim>(p, sh, cut, ring);
+    else if (kCached && warp >= 12)
+      expand_role<kDim>(p, sh, cut, ring, raw);
   }
   __syncwarp();
   tc_fence_before();
@@ -450,19 +874,91 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
   }
 }
 
+// The pieces' sums of cut items, joined: a CTA for each piece, which takes its share
+// of the item's rows, one warp per row.
 template <int kDim>
-static cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
-  using L = Layout<kDim>;
-  const size_t smem = 1024 + (2 + L::kStages) * static_cast<size_t>(L::kTileBytes) + sizeof(Shared);
-  const cudaError_t e = cudaFuncSetAttribute(k_attend<kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  return launch_kernel(k_attend<kDim>, dim3(static_cast<unsigned>(a.n_slots) * a.a.c.heads), dim3(kThreads), smem, s, true, a);
+__global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ AttendArgs p) {
+  __shared__ int sums[2][16];
+  pdl_wait();
+  pdl_trigger();
+  const Cut cut = cut_call(p, sums);
+  Item it;
+  if (cut.chunk == 0 || blockIdx.x >= cut.pieces || !locate(p, cut, blockIdx.x, &it) || it.parts == 1) return;
+  constexpr int kPer = kDim / 32;
+  const int lane = threadIdx.x & 31, k0 = blockIdx.x - it.part;
+  const int rows = min(2 * p.tokens, it.sp.rows - it.tok0) * p.a.group;
+  for (int i = it.part * 4 + (threadIdx.x >> 5); i < rows; i += it.parts * 4) {
+    const int tok_in = i / p.a.group, t = tok_in >= p.tokens, head_in = i - tok_in * p.a.group;
+    const int r = t * 128 + (tok_in - t * p.tokens) * p.a.group + head_in;
+    float m = -INFINITY, l = 0.f, o[kPer] = {};
+    constexpr int kBatch = 8;
+    for (int b = 0; b < it.parts; b += kBatch) {
+      float2 ml[kBatch];
+      float v[kBatch][kPer];
+      float top = m;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const int64_t at = static_cast<int64_t>(k0 + min(b + x, it.parts - 1)) * 256 + r;
+        ml[x] = __ldcg(&p.part_ml[at]);
+        if constexpr (kDim == 128) {
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part + at * kDim) + lane);
+          v[x][0] = y.x, v[x][1] = y.y, v[x][kPer - 2] = y.z, v[x][kPer - 1] = y.w;
+        } else {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(p.part + at * kDim) + lane);
+          v[x][0] = y.x, v[x][1] = y.y;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) top = fmaxf(top, ml[x].x);
+      const float f = m == top ? 1.f : exp2_fast(m - top);
+      m = top;
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] *= f;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        if (b + x >= it.parts) continue;
+        const float w = ml[x].x == m ? 1.f : exp2_fast(ml[x].x - m);
+        l += w * ml[x].y;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[e] += w * v[x][e];
+      }
+    }
+    const int64_t at = static_cast<int64_t>(it.sp.row0 + it.tok0 + tok_in) * p.a.q_heads + it.head * p.a.group + head_in;
+    const float inv = l == 0.f ? 0.f : p.a.c.v_mul / l;
+    const __nv_bfloat162 a = __floats2bfloat162_rn(o[0] * inv, o[1] * inv);
+    if constexpr (kDim == 128) {
+      const __nv_bfloat162 c = __floats2bfloat162_rn(o[kPer - 2] * inv, o[kPer - 1] * inv);
+      reinterpret_cast<uint2*>(p.a.out + at * kDim)[lane] =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
+    } else {
+      reinterpret_cast<uint32_t*>(p.a.out + at * kDim)[lane] = *reinterpret_cast<const uint32_t*>(&a);
+    }
+    if (lane == 0 && p.a.lse != nullptr) p.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  }
 }
 
-cudaError_t launch_attend(const AttendArgs& args, cudaStream_t s) {
+template <int kDim, bool kCached>
+static cudaError_t launch(const AttendArgs& a, int grid, cudaStream_t s) {
+  using L = Layout<kDim, kCached>;
+  const size_t smem = 1024 + (2 + L::kStages) * static_cast<size_t>(L::kTileBytes) + L::kRaw * L::kRawBytes + sizeof(Shared);
+  cudaError_t e = cudaFuncSetAttribute(k_attend<kDim, kCached>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  e = launch_kernel(k_attend<kDim, kCached>, dim3(grid), dim3(L::kThreads), smem, s, true, a);
+  if (e != cudaSuccess || !a.may_cut) return e;
+  return launch_kernel(k_attend_join<kDim>, dim3(plan::kAttendMaxPieces), dim3(128), 0, s, true, a);
+}
+
+cudaError_t launch_attend(const AttendArgs& args, bool cached, int sms, cudaStream_t s) {
   AttendArgs a = args;
   a.a.wide_out = reinterpret_cast<uintptr_t>(a.a.out) % 32 == 0;
-  return a.a.c.dim == 64 ? launch<64>(a, s) : launch<128>(a, s);
+  const unsigned per = a.a.c.page_tokens / 16;
+  a.per_magic = per <= 1 ? 0u : static_cast<unsigned>(((1ull << 32) + per - 1) / per);
+  const int64_t slots = static_cast<int64_t>(a.n_slots) * a.a.c.heads;
+  const int grid = a.may_cut || slots > sms ? sms : static_cast<int>(slots);
+  if (a.a.c.dim == 64) return cached ? launch<64, true>(a, grid, s) : launch<64, false>(a, grid, s);
+  return cached ? launch<128, true>(a, grid, s) : launch<128, false>(a, grid, s);
 }
 
 }  // namespace clover

@@ -113,30 +113,6 @@ __device__ void place(const AttendFewArgs& p, const int64_t* before, Cursor* c) 
   c->unit = left;
 }
 
-// Four pairs of values of eight codes (one instruction each, whichever byte).
-__device__ __forceinline__ void expand(uint32_t w, __half2 (&h)[4]) {
-  uint32_t r[4];
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "mov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-      : "r"(w));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<const __half2*>(&r[i]);
-}
-
-// The two scale bytes of a halfword in fp16.
-__device__ __forceinline__ __half2 scales2(uint32_t bytes) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(r) : "r"(bytes));
-  return *reinterpret_cast<const __half2*>(&r);
-}
-
-__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
-
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -151,7 +127,7 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t half2_bits(float a, float b) { return bits(__floats2half2_rn(a, b)); }
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) { return half2_word(__floats2half2_rn(a, b)); }
 
 // What a lane keeps of a tile's rows. As a factor: elements kDim / 4 * t .. of
 // rows g and g + 8, four to a step. As results: rows 2t, 2t + 1 (and 8 further).
@@ -271,7 +247,7 @@ __device__ __forceinline__ bool step(const uint8_t* stage, const Rows<kDim, kCol
         __half2 h[2][4];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          expand(w[x][n][i], h[n]);
+          expand_word(w[x][n][i], h[n]);
           const __half2 f = kDim == 128 && i >= 2 ? __high2half2(sc[x][n]) : __low2half2(sc[x][n]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) h[n][e] = __hmul2(h[n][e], f);
@@ -280,7 +256,7 @@ __device__ __forceinline__ bool step(const uint8_t* stage, const Rows<kDim, kCol
         for (int c = 0; c < kCols; ++c)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            mma(s[x][c], bits(h[0][2 * e]), bits(h[1][2 * e]), bits(h[0][2 * e + 1]), bits(h[1][2 * e + 1]),
+            mma(s[x][c], half2_word(h[0][2 * e]), half2_word(h[1][2 * e]), half2_word(h[0][2 * e + 1]), half2_word(h[1][2 * e + 1]),
                 r.q[c][2 * i + e][0], r.q[c][2 * i + e][1]);
       }
   }
@@ -382,7 +358,7 @@ __device__ __forceinline__ bool step(const uint8_t* stage, const Rows<kDim, kCol
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          expand(w[k][i][n], h[k][n]);
+          expand_word(w[k][i][n], h[k][n]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) h[k][n][e] = __hmul2(h[k][n][e], sc[k]);
         }
@@ -390,7 +366,7 @@ __device__ __forceinline__ bool step(const uint8_t* stage, const Rows<kDim, kCol
       for (int e = 0; e < 4; ++e)
 #pragma unroll
         for (int c = 0; c < kCols; ++c)
-          mma(st->o[c][4 * i + e], bits(h[0][0][e]), bits(h[0][1][e]), bits(h[1][0][e]), bits(h[1][1][e]), b[c][0], b[c][1]);
+          mma(st->o[c][4 * i + e], half2_word(h[0][0][e]), half2_word(h[0][1][e]), half2_word(h[1][0][e]), half2_word(h[1][1][e]), b[c][0], b[c][1]);
     }
   }
   return poison;

@@ -60,21 +60,23 @@ struct AttnArgs {
   int* err;
 };
 
-cudaError_t launch_attention_simple(const AttnArgs& a, bool cached, cudaStream_t s);
-
 // Attention on tensor-core tiles (csrc/attend.cu). A tile is 128 rows: the
 // group's query heads of `tokens` = 128 / group consecutive tokens, row
 // token * group + head.
 struct AttendArgs {
   CUtensorMap tm_q;  // q [n_rows][q_heads][dim], boxes of 64 elements x group x tokens
-  CUtensorMap tm_k;  // k [n_keys][heads][dim], boxes of 64 elements x 1 x 128
+  CUtensorMap tm_k;  // prompt: k [n_keys][heads][dim], boxes of 64 elements x 1 x 128
   CUtensorMap tm_v;
   AttnArgs a;
   int tokens;
-  int n_slots;       // pairs of tiles: n_rows / (2 tokens) + the number of sequences
+  int n_slots;         // pairs of tiles: n_rows / (2 tokens) + the number of sequences
+  int may_cut;         // few items are cut into pieces
+  float* part;         // [pieces][256][dim] sums of pieces (workspace)
+  float2* part_ml;     // [pieces][256] their maxima and sums of weights
+  uint32_t per_magic;  // set by the launch: 2^32 / sixteens of a page, rounded up (0: one)
 };
 
-cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s);
+cudaError_t launch_attend(const AttendArgs& a, bool cached, int sms, cudaStream_t s);
 
 // Attention of few query rows over a cache (csrc/attend_few.cu): tiles of at most
 // 8 or 16 rows, the group's query heads of `tokens` tokens.

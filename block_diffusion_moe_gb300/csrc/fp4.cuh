@@ -148,4 +148,28 @@ __device__ __forceinline__ uint32_t quantize_block(const uint32_t (&in)[(kMx ? 3
   return sb;
 }
 
+// Four pairs of values of eight codes (one instruction each, whichever byte).
+__device__ __forceinline__ void expand_word(uint32_t w, __half2 (&h)[4]) {
+  uint32_t r[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<const __half2*>(&r[i]);
+}
+
+// The two scale bytes of a halfword in fp16.
+__device__ __forceinline__ __half2 scales2(uint32_t bytes) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(r) : "r"(bytes));
+  return *reinterpret_cast<const __half2*>(&r);
+}
+
+__device__ __forceinline__ uint32_t half2_word(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+
 }  // namespace clover
