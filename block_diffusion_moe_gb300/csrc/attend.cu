@@ -11,10 +11,10 @@
 // so a P above 1 costs no precision.
 //
 // Roles: warps 0-3 and 4-7 the softmax of tile 0 and 1, warp 8 loads, warp 9
-// issues the MMAs. While one tile's softmax runs, the tensor core works for the
-// other. Prompt: keys and values come as they are (TMA), and warp 10 looks after the
-// values that not every row may see. Cache: warp 8 copies pages' codes and scales,
-// and warps 12-15 expand them to fp16 tiles (exact), which takes a third of the
+// issues the MMAs, warp 10 watches the ring for it. While one tile's softmax runs,
+// the tensor core works for the other. Prompt: keys and values come as they are
+// (TMA), and warp 10 looks after the values that not every row may see. Cache: warp 8
+// copies pages' codes and scales, and warps 12-15 expand them to fp16 tiles (exact), which takes a third of the
 // time of the MMAs that read them; queries become fp16 too, each row scaled by a
 // power of two so that its largest element is about 2^14.
 //
@@ -33,7 +33,7 @@ namespace {
 constexpr int kKeys = 128;  // keys per step
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;  // of tile t: + 128 t
-constexpr int kWholeItems = plan::kAttendSms;  // calls of as many items cut none
+constexpr int kWholeItems = plan::kAttendSms;  // calls of more than half as many items cut none
 constexpr int kMinSteps = 4;                   // of a piece
 
 template <int kDim, bool kCached>
@@ -56,7 +56,6 @@ struct Layout {
 struct Shared {
   uint64_t q_full[2], q_empty[2], q_ready[2];  // ready: converted (cache)
   uint64_t full[10], empty[10];
-  uint64_t v_ok[10];  // a stage's values have been looked after (prompt)
   uint64_t raw_full[6], raw_empty[6];
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint64_t drain;
@@ -115,7 +114,7 @@ __device__ __forceinline__ int steps_of_tile(const AttendArgs& p, const SeqSpan&
 }
 
 // Piece k, by a whole warp. False: an empty slot.
-__device__ bool locate(const AttendArgs& p, const Cut& cut, int k, Item* it) {
+__device__ __forceinline__ bool locate(const AttendArgs& p, const Cut& cut, int k, Item* it) {
   const int pair = 2 * p.tokens, n = p.a.s.n_rows;
   if (cut.chunk == 0) {
     // the last tiles of a sequence see the most: they come first
@@ -182,9 +181,10 @@ __device__ __forceinline__ int cta_sum(int v, int* scratch) {
   return all;
 }
 
-// How the call is cut, by all threads of a CTA; the same in every CTA. With `items`
-// of them and target > items pieces wanted, pieces of total / (target - items)
-// steps are at most `target`.
+// How the call is cut, by all threads of a CTA; the same in every CTA. Pieces of
+// steps / (SMs - items) steps are at most as many as SMs. (Of more items than half
+// the SMs, none is cut: 126 items of 98 steps in two rounds of pieces took 324 us,
+// whole 165.)
 __device__ Cut cut_call(const AttendArgs& p, int (&sums)[2][16]) {
   const Cut whole = {0, p.n_slots * p.a.c.heads};
   if (!p.may_cut) return whole;
@@ -199,11 +199,10 @@ __device__ Cut cut_call(const AttendArgs& p, int (&sums)[2][16]) {
       for (int t = 0; t < tiles; ++t) own += steps_of_tile(p, sp, t) * p.a.c.heads;
   }
   items = cta_sum(items, sums[0]);
-  if (items >= kWholeItems) return whole;
+  if (2 * items > kWholeItems) return whole;
   const int steps = cta_sum(static_cast<int>(own), sums[1]);
-  const int target = 2 * items <= kWholeItems ? kWholeItems : 2 * kWholeItems;
   Cut cut;
-  cut.chunk = max(kMinSteps, (steps + target - items - 1) / (target - items));
+  cut.chunk = max(kMinSteps, (steps + kWholeItems - items - 1) / (kWholeItems - items));
   int pieces = 0;
   for (int i = threadIdx.x; i < p.a.s.n; i += blockDim.x) {
     const SeqSpan sp = seq_span(p.a.s, i);
@@ -277,18 +276,19 @@ __device__ void load_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint3
     if (!locate(p, cut, k, &it)) continue;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if (!ok || it.steps(t) == 0) continue;
-      if (!(ok = warp_wait(p, sh, &sh->q_empty[t], (q_count[t] & 1) ^ 1u))) break;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(&sh->q_full[t], kDim / 64 * p.a.group * p.tokens * 128);
+      if (ok && it.steps(t) > 0) {
+        ok = warp_wait(p, sh, &sh->q_empty[t], (q_count[t] & 1) ^ 1u);
+        if (ok && elect_one()) {
+          mbar_arrive_expect_tx(&sh->q_full[t], kDim / 64 * p.a.group * p.tokens * 128);
 #pragma unroll
-        for (int d = 0; d < kDim / 64; ++d)
-          tma_load_3d(q + t * L::kTileBytes + d * L::kSlab, &p.tm_q, &sh->q_full[t], d * 64, it.head * p.a.group,
-                      it.sp.row0 + it.tok0 + t * p.tokens, keep);
+          for (int d = 0; d < kDim / 64; ++d)
+            tma_load_3d(q + t * L::kTileBytes + d * L::kSlab, &p.tm_q, &sh->q_full[t], d * 64, it.head * p.a.group,
+                        it.sp.row0 + it.tok0 + t * p.tokens, keep);
+        }
+        __syncwarp();
+        if (ok) q_flight.add(t, q_count[t] & 1);
+        ++q_count[t];
       }
-      __syncwarp();
-      q_flight.add(t, q_count[t] & 1);
-      ++q_count[t];
     }
     const int steps = it.steps();
     if constexpr (!kCached) {
@@ -341,88 +341,97 @@ __device__ void load_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint3
   }
 }
 
+// Run by a whole warp whose control flow is uniform: what it depends on is put in
+// uniform registers, where the MMAs' descriptors stay. (With the piece count and the
+// steps left in ordinary ones the issue of an MMA took longer than the 64 cycles
+// that the tensor core needs for it.) False: gave up.
 template <int kDim, bool kCached>
-__device__ void mma_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint32_t q, uint32_t ring) {
+__device__ __forceinline__ bool issue_all(const AttendArgs& p, Shared* sh, const Cut& cut_in, uint32_t q, uint32_t ring) {
   using L = Layout<kDim, kCached>;
   constexpr uint32_t kIdS = kCached ? umma_idesc_f16(128, kKeys) : umma_idesc_bf16(128, kKeys);
   constexpr uint32_t kIdO = (kCached ? umma_idesc_f16(128, kDim) : umma_idesc_bf16(128, kDim)) | kUmmaBMnMajor;
-  const uint32_t tmem = sh->tmem;
+  const Cut cut = {warp_uniform(cut_in.chunk), warp_uniform(cut_in.pieces)};
+  const uint32_t tmem = static_cast<uint32_t>(warp_uniform(static_cast<int>(sh->tmem)));
   Ring<L::kStages> rk, rv;
-  uint32_t v_parity = 0, q_count[2] = {0, 0}, p_count[2] = {0, 0};
+  uint32_t items0 = 0, items1 = 0, steps0 = 0, steps1 = 0;
+  // (by one lane) tile t's scores of a step, whose keys the ring's rk holds
+  auto scores = [&](int t, bool last) {
+    const uint64_t a = umma_desc_sw128(q + t * L::kTileBytes), b = umma_desc_sw128(ring + rk.st * L::kTileBytes);
+#pragma unroll
+    for (int s = 0; s < kDim / 16; ++s) {
+      const uint32_t o = (s / 4) * (L::kSlab >> 4) + (s % 4) * 2;
+      umma_bf16(tmem + kTmemS + t * 128, a + o, b + o, kIdS, s > 0);
+    }
+    umma_commit(&sh->s_full[t]);
+    if (last) umma_commit(&sh->q_empty[t]);
+  };
+  // (by one lane) its numerators times the values that rv holds
+  auto sums = [&](int t, bool first, bool last) {
+    const uint64_t b = umma_desc_sw128_mn(ring + rv.st * L::kTileBytes, L::kSlab);
+#pragma unroll
+    for (int s = 0; s < kKeys / 16; ++s)
+      umma_bf16_ta(tmem + kTmemO + t * 128, tmem + kTmemS + t * 128 + L::kP + s * 8, b + s * 128, kIdO, s > 0 ? 1u : !first);
+    if (last) umma_commit(&sh->o_full[t]);
+  };
   Turn turn;
   Item it;
-  // tile t's scores of a step; the ring's rk holds its keys
-  auto scores = [&](int t, bool last) {
-    if (elect_one()) {
-      const uint64_t a = umma_desc_sw128(q + t * L::kTileBytes), b = umma_desc_sw128(ring + rk.st * L::kTileBytes);
-#pragma unroll
-      for (int s = 0; s < kDim / 16; ++s) {
-        const uint32_t o = (s / 4) * (L::kSlab >> 4) + (s % 4) * 2;
-        umma_bf16(tmem + kTmemS + t * 128, a + o, b + o, kIdS, s > 0);
-      }
-      umma_commit(&sh->s_full[t]);
-      if (last) umma_commit(&sh->q_empty[t]);
-    }
-    __syncwarp();
-  };
-  auto sums = [&](int t, bool first, bool last) {
-    if (elect_one()) {
-      const uint64_t b = umma_desc_sw128_mn(ring + rv.st * L::kTileBytes, L::kSlab);
-#pragma unroll
-      for (int s = 0; s < kKeys / 16; ++s)
-        umma_bf16_ta(tmem + kTmemO + t * 128, tmem + kTmemS + t * 128 + L::kP + s * 8, b + s * 128, kIdO, !first || s > 0);
-      if (last) umma_commit(&sh->o_full[t]);
-    }
-    __syncwarp();
-  };
-  auto release = [&](int st) {
-    if (elect_one()) umma_commit(&sh->empty[st]);
-    __syncwarp();
-  };
-  bool ok = true;
-  for (int k; ok && (k = turn.next()) < cut.pieces;) {
-    if (!locate(p, cut, k, &it)) continue;
-    const int steps = it.steps();
+  for (int k; (k = turn.next()) < cut.pieces;) {
+    const bool there = locate(p, cut, k, &it);
+    const int n0 = warp_uniform(there ? it.steps(0) : 0), n1 = warp_uniform(there ? it.steps(1) : 0), steps = max(n0, n1);
     if (steps == 0) continue;
-    const int first_masked = it.all / kKeys - it.j0;  // steps from here on wait for the values to be looked after
-    const int n[2] = {it.steps(0), it.steps(1)};
     rv = rk;
     rv.next();
-    for (int t = 0; t < 2 && ok; ++t)
-      if (n[t] > 0) ok = warp_wait(p, sh, kCached ? &sh->q_ready[t] : &sh->q_full[t], q_count[t] & 1);
-    if (ok) ok = warp_wait(p, sh, &sh->full[rk.st], rk.ph);
-    if (!ok) break;
+    if (n0 > 0 && !warp_wait(p, sh, kCached ? &sh->q_ready[0] : &sh->q_full[0], items0 & 1)) return false;
+    if (n1 > 0 && !warp_wait(p, sh, kCached ? &sh->q_ready[1] : &sh->q_full[1], items1 & 1)) return false;
+    if (!warp_wait(p, sh, &sh->full[rk.st], rk.ph)) return false;
     tc_fence_after();
-    for (int t = 0; t < 2; ++t)
-      if (n[t] > 0) scores(t, n[t] == 1);
-    release(rk.st);
-    for (int j = 0; j < steps && ok; ++j) {
+    if (elect_one()) {
+      if (n0 > 0) scores(0, n0 == 1);
+      if (n1 > 0) scores(1, n1 == 1);
+      umma_commit(&sh->empty[rk.st]);
+    }
+    __syncwarp();
+    for (int j = 0; j < steps; ++j) {
       rk.next(2);
-      const bool more = j + 1 < steps;
-      ok = warp_wait(p, sh, &sh->full[rv.st], rv.ph);
-      if (!kCached && ok && j >= first_masked) {
-        ok = warp_wait(p, sh, &sh->v_ok[rv.st], (v_parity >> rv.st) & 1u);
-        v_parity ^= 1u << rv.st;
-      }
-      if (ok && more) ok = warp_wait(p, sh, &sh->full[rk.st], rk.ph);
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (j >= n[t]) continue;
-        // the sums of the item before are read
-        if (j == 0) ok = warp_wait(p, sh, &sh->o_empty[t], (q_count[t] & 1) ^ 1u);
-        if (ok) ok = warp_wait(p, sh, &sh->p_full[t], p_count[t] & 1);
-        if (!ok) break;
-        ++p_count[t];
+      // p_full: the numerators are in place, and the values of this step and the keys
+      // of the next one; o_empty: the sums of the item before are read
+      if (j < n0) {
+        if (j == 0 && !warp_wait(p, sh, &sh->o_empty[0], (items0 & 1) ^ 1u)) return false;
+        if (!warp_wait(p, sh, &sh->p_full[0], steps0++ & 1)) return false;
         tc_fence_after();
-        sums(t, j == 0, j + 1 == n[t]);
-        if (j + 1 < n[t]) scores(t, j + 2 == n[t]);
+        if (elect_one()) {
+          sums(0, j == 0, j + 1 == n0);
+          if (j + 1 < n0) scores(0, j + 2 == n0);
+          if (j >= n1) {
+            umma_commit(&sh->empty[rv.st]);
+            if (j + 1 < steps) umma_commit(&sh->empty[rk.st]);
+          }
+        }
+        __syncwarp();
       }
-      if (!ok) break;
-      release(rv.st);
-      if (more) release(rk.st);
+      if (j < n1) {
+        if (j == 0 && !warp_wait(p, sh, &sh->o_empty[1], (items1 & 1) ^ 1u)) return false;
+        if (!warp_wait(p, sh, &sh->p_full[1], steps1++ & 1)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          sums(1, j == 0, j + 1 == n1);
+          if (j + 1 < n1) scores(1, j + 2 == n1);
+          umma_commit(&sh->empty[rv.st]);
+          if (j + 1 < steps) umma_commit(&sh->empty[rk.st]);
+        }
+        __syncwarp();
+      }
       rv.next(2);
     }
-    for (int t = 0; t < 2; ++t) q_count[t] += n[t] > 0;
+    items0 += n0 > 0;
+    items1 += n1 > 0;
   }
+  return true;
+}
+
+template <int kDim, bool kCached>
+__device__ void mma_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint32_t q, uint32_t ring) {
+  issue_all<kDim, kCached>(p, sh, cut, q, ring);
   if (elect_one()) umma_commit(&sh->drain);
   __syncwarp();
   mbar_wait_for(&sh->drain, 0, 200000000ull);
@@ -431,12 +440,45 @@ __device__ void mma_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint32
 // Values that not every row sees: a weight of 0 does not keep an infinity or a
 // NaN out of a sum. Rows of V past every row's sight become zeros, and so do
 // infinities and NaN among the others, which the end of the softmax role adds
-// to the rows that do see them.
+// to the rows that do see them (true: there were some). Step j of an item, by a warp.
 template <int kDim>
-__device__ void guard_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint8_t* ring) {
+__device__ __forceinline__ bool look_after(const Item& it, uint8_t* v, int j) {
   using L = Layout<kDim, false>;
+  const int lane = threadIdx.x & 31, lo = max(it.all - j * kKeys, 0), hi = min(it.any - j * kKeys, kKeys);
+  constexpr int kPer = kDim / 8;  // 16-byte pieces of a row
+  uint32_t top = 0;
+#pragma unroll 4
+  for (int e = lane; e < (hi - lo) * kPer; e += 32) {
+    const int row = lo + e / kPer, c = e % kPer;
+    const uint4 x = *reinterpret_cast<const uint4*>(v + (c / 8) * L::kSlab + row * 128 + (c % 8) * 16);
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+  }
+  const bool odd = __any_sync(0xffffffffu, (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u);
+  if (odd) {
+    for (int e = lane; e < (hi - lo) * kDim; e += 32) {
+      const int row = lo + e / kDim, d = e % kDim;
+      uint16_t* x = reinterpret_cast<uint16_t*>(v + (d / 64) * L::kSlab + row * 128 + ((d % 64 / 8) ^ (row & 7)) * 16) + d % 8;
+      if ((*x & 0x7F80u) == 0x7F80u) *x = 0;
+    }
+  }
+  for (int e = lane; e < (kKeys - hi) * kPer; e += 32) {
+    const int row = hi + e / kPer, c = e % kPer;
+    *reinterpret_cast<uint4*>(v + (c / 8) * L::kSlab + row * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_shared();
+  __syncwarp();
+  return odd;
+}
+
+// Waits for the ring in place of the MMA role, which then has one barrier to wait
+// for per tile and step (with all of them it left the tensor core idle for a
+// quarter of the time), and looks after the prompt's values.
+template <int kDim, bool kCached>
+__device__ void watch_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint8_t* ring) {
+  using L = Layout<kDim, kCached>;
   const int lane = threadIdx.x & 31;
   Ring<L::kStages> r;
+  uint32_t count[2] = {0, 0};
   Turn turn;
   Item it;
   for (int k, item = -1; (k = turn.next()) < cut.pieces;) {
@@ -444,45 +486,30 @@ __device__ void guard_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint
     // (items with steps are counted; of a ring of 16, eight on, or back, is out of
     // everyone's reach)
     ++item;
-    if (lane == 0) *reinterpret_cast<volatile int*>(&sh->poison[(item + 8) & 15]) = 0;
+    if (!kCached && lane == 0) *reinterpret_cast<volatile int*>(&sh->poison[(item + 8) & 15]) = 0;
     __syncwarp();
-    // every stage in turn, keys and whole steps too: who leaves one out can take a
-    // later phase of its barrier for the one it waits for
-    for (int i = 0; i < 2 * it.steps(); ++i, r.next()) {
-      if (!warp_wait(p, sh, &sh->full[r.st], r.ph)) return;
-      const int j = it.j0 + (i >> 1);
-      if (i % 2 == 0 || (j + 1) * kKeys <= it.all) {
+    const int steps = it.steps();
+    for (int j = -1; j < steps; ++j) {
+      if (j >= 0) {  // values of step j
+        if (!warp_wait(p, sh, &sh->full[r.st], r.ph)) return;
+        if (!kCached && (it.j0 + j + 1) * kKeys > it.all && look_after<kDim>(it, ring + r.st * L::kTileBytes, it.j0 + j) && lane == 0)
+          *reinterpret_cast<volatile int*>(&sh->poison[item & 15]) = 1;
         if (lane == 0) mbar_arrive(&sh->empty[r.st]);
-        continue;
+        r.next();
       }
-      uint8_t* v = ring + r.st * L::kTileBytes;
-      const int lo = max(it.all - j * kKeys, 0), hi = min(it.any - j * kKeys, kKeys);
-      constexpr int kPer = kDim / 8;  // 16-byte pieces of a row
-      uint32_t top = 0;
-      const int n = (hi - lo) * kPer;
-#pragma unroll 4
-      for (int e = lane; e < n; e += 32) {
-        const int row = lo + e / kPer, c = e % kPer;
-        const uint4 x = *reinterpret_cast<const uint4*>(v + (c / 8) * L::kSlab + row * 128 + (c % 8) * 16);
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+      if (j + 1 < steps) {  // keys of the next one
+        if (!warp_wait(p, sh, &sh->full[r.st], r.ph)) return;
+        if (lane == 0) mbar_arrive(&sh->empty[r.st]);
+        r.next();
       }
-      if (__any_sync(0xffffffffu, (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u)) {
-        for (int e = lane; e < (hi - lo) * kDim; e += 32) {
-          const int row = lo + e / kDim, d = e % kDim;
-          uint16_t* x = reinterpret_cast<uint16_t*>(v + (d / 64) * L::kSlab + row * 128 + ((d % 64 / 8) ^ (row & 7)) * 16) + d % 8;
-          if ((*x & 0x7F80u) == 0x7F80u) *x = 0;
-        }
-        if (lane == 0) *reinterpret_cast<volatile int*>(&sh->poison[item & 15]) = 1;
-      }
-      for (int e = lane; e < (kKeys - hi) * kPer; e += 32) {
-        const int row = hi + e / kPer, c = e % kPer;
-        *reinterpret_cast<uint4*>(v + (c / 8) * L::kSlab + row * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
-      }
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sh->v_ok[r.st]);
-        mbar_arrive(&sh->empty[r.st]);
+      if (j < 0) continue;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (j >= it.steps(t)) continue;
+        // (not before the step before has been through)
+        if (!warp_wait(p, sh, &sh->p_full[t], (count[t] & 1) ^ 1u)) return;
+        ++count[t];
+        if (lane == 0) mbar_arrive(&sh->p_full[t]);
       }
     }
   }
@@ -533,7 +560,7 @@ __device__ __forceinline__ bool expand_tile(const uint8_t* raw, uint8_t* tile, i
 template <int kDim>
 __device__ void expand_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint8_t* ring, const uint8_t* raw) {
   using L = Layout<kDim, true>;
-  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int warp = (threadIdx.x >> 5) - 12, lane = threadIdx.x & 31;
   Ring<L::kStages> r;
   Ring<L::kRaw> rr;
   int k_step = 0;
@@ -601,28 +628,34 @@ __device__ __forceinline__ int convert_row(uint8_t* q, int r) {
   return e;
 }
 
-// Numerators of 64 scores: 32 words of pairs, and their sum.
+// Numerators of 64 scores to tensor memory as 32 columns of pairs; returns their sum.
 template <bool kHalf>
-__device__ __forceinline__ float numerators(const uint32_t (&s)[2][32], float c, float lift, uint32_t (&w)[32]) {
+__device__ __forceinline__ float numerators(const uint32_t (&s)[2][32], float c, float lift, uint32_t to) {
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    const float a = exp2_fast(fmaf(__uint_as_float(s[k / 16][2 * k % 32]), c, lift));
-    const float b = exp2_fast(fmaf(__uint_as_float(s[k / 16][2 * k % 32 + 1]), c, lift));
-    sum[(2 * k) & 3] += a;
-    sum[(2 * k + 1) & 3] += b;
-    if (kHalf) {
-      w[k] = half2_word(__floats2half2_rn(a, b));
-    } else {
-      const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
-      w[k] = *reinterpret_cast<const uint32_t*>(&x);
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float a = exp2_fast(fmaf(__uint_as_float(s[h][2 * k]), c, lift));
+      const float b = exp2_fast(fmaf(__uint_as_float(s[h][2 * k + 1]), c, lift));
+      sum[(2 * k) & 3] += a;
+      sum[(2 * k + 1) & 3] += b;
+      if (kHalf) {
+        w[k] = half2_word(__floats2half2_rn(a, b));
+      } else {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+        w[k] = *reinterpret_cast<const uint32_t*>(&x);
+      }
     }
+    tmem_st16(to + h * 16, w);
   }
   return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
 // Scores of 64 keys from key `at` of the step on that the row does not see: -inf.
 __device__ __forceinline__ void mask(uint32_t (&s)[2][32], int at, int left, uint32_t there) {
+  asm volatile("");  // a branch, not 64 predicated instructions in every step
 #pragma unroll
   for (int i = 0; i < 64; ++i)
     if (at + i >= left || !(there >> ((at + i) / 16) & 1u)) s[i / 32][i % 32] = 0xFF800000u;
@@ -631,8 +664,31 @@ __device__ __forceinline__ void mask(uint32_t (&s)[2][32], int at, int left, uin
 __device__ __forceinline__ float largest(const uint32_t (&s)[2][32]) {
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int i = 0; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(s[i / 32][i % 32]));
-  return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  for (int i = 0; i < 32; ++i) top[i & 3] = max3(top[i & 3], __uint_as_float(s[i / 16][2 * i % 32]), __uint_as_float(s[i / 16][2 * i % 32 + 1]));
+  return fmaxf(max3(top[0], top[1], top[2]), top[3]);
+}
+
+// What look_after (expand_tile) has taken out of V, added to elements 32 i .. of the
+// rows that see it: infinities and NaN. By a whole warp.
+template <int kDim, bool kCached>
+__device__ __noinline__ void add_odd_values(const AttendArgs& p, const Cut& cut, int k, int lim, int i, uint32_t (&o)[32]) {
+  using L = Layout<kDim, kCached>;
+  Item it;
+  locate(p, cut, k, &it);
+  for (int j = max(it.all, it.j0 * kKeys); j < min(lim, it.j1 * kKeys); ++j) {
+    if (kCached) {
+      const uint8_t* six = kv_sixteen(p.a.c, p.a.s, it.seq, it.head, j);
+      for (int x = 0; x < 32; ++x)
+        if (six != nullptr && (six[L::kVs + j % 16 * (kDim / 16) + (i * 32 + x) / 16] & 0x7F) == 0x7F) o[x] = 0x7FC00000u;
+    } else {
+      const uint16_t* v = reinterpret_cast<const uint16_t*>(p.a.v.data + (it.sp.key0 + j) * p.a.v.row + it.head * p.a.v.head);
+      for (int x = 0; x < 32; ++x) {
+        const uint32_t b = v[i * 32 + x];
+        if ((b & 0x7F80u) == 0x7F80u) o[x] = __float_as_uint(__uint_as_float(o[x]) + __uint_as_float(b << 16));
+      }
+    }
+  }
+  __syncwarp();
 }
 
 template <int kDim, bool kCached>
@@ -645,18 +701,28 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
   uint32_t s_count = 0, q_count = 0;
   int k_step = 0;
   Turn turn;
-  Item it;
   for (int k, item = -1; (k = turn.next()) < cut.pieces;) {
-    if (!locate(p, cut, k, &it)) continue;
-    const int tok = it.tok0 + t * p.tokens + tok_in;
-    const bool mine = tok_in < p.tokens && tok < it.sp.rows;
-    const int lim = mine ? seen_by(p, it.sp, tok) : 0;
-    int whole = mine ? lim : 0x7fffffff;  // every row of the warp sees the positions below
+    // what outlives this block lives in registers beside the scores
+    int lim, whole, n, steps, j0;
+    bool mine, part;
+    int64_t at;  // the row in out and lse
+    {
+      Item it;
+      if (!locate(p, cut, k, &it)) continue;
+      const int tok = it.tok0 + t * p.tokens + tok_in;
+      mine = tok_in < p.tokens && tok < it.sp.rows;
+      lim = mine ? seen_by(p, it.sp, tok) : 0;
+      n = t == 0 ? it.steps(0) : it.steps(1);
+      steps = it.steps();
+      j0 = it.j0;
+      part = it.parts > 1;
+      at = static_cast<int64_t>(it.sp.row0 + tok) * p.a.q_heads + it.head * p.a.group + head_in;
+    }
+    whole = mine ? lim : 0x7fffffff;  // every row of the warp sees the positions below
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) whole = min(whole, __shfl_xor_sync(0xffffffffu, whole, o));
     float c = p.a.scale_log2;
     float m = -INFINITY, l = 0.f;  // m: of c S
-    const int n = it.steps(t), steps = it.steps();
     item += steps > 0;
     if (kCached && n > 0) {
       if (!warp_wait(p, sh, &sh->q_full[t], q_count & 1)) return;
@@ -670,7 +736,7 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
       if (!warp_wait(p, sh, &sh->s_full[t], s_count & 1)) return;
       ++s_count;
       tc_fence_after();
-      const int j = it.j0 + i, left = lim - j * kKeys;
+      const int j = j0 + i, left = lim - j * kKeys;
       const uint32_t there = kCached ? *reinterpret_cast<volatile uint32_t*>(&sh->there[(k_step + i) & 15]) : 0xFFu;
       const bool masked = (j + 1) * kKeys > whole || (kCached && there != 0xFFu);
       uint32_t lo[2][32], hi[2][32];
@@ -708,17 +774,14 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
         }
       }
       const float lift = L::kLift - (m == -INFINITY ? 0.f : m);
-      uint32_t w[32];
-      l += numerators<kCached>(hi, c, lift, w);
-      tmem_st32(s_at + L::kP + 32, w);
+      l += numerators<kCached>(hi, c, lift, s_at + L::kP + 32);
       if (kCached) {  // (registers do not hold all scores beside the roles that share them: half are read again)
         tmem_ld32_async(s_at, lo[0]);
         tmem_ld32_async(s_at + 32, lo[1]);
         tmem_wait_ld(lo);
         if (masked) mask(lo, 0, left, there);
       }
-      l += numerators<kCached>(lo, c, lift, w);
-      tmem_st32(s_at + L::kP, w);
+      l += numerators<kCached>(lo, c, lift, s_at + L::kP);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -730,8 +793,6 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
       ++q_count;
     }
     tc_fence_after();
-    const int64_t at = static_cast<int64_t>(it.sp.row0 + tok) * p.a.q_heads + it.head * p.a.group + head_in;
-    const bool part = it.parts > 1;
     const float f = part ? 1.f : (l == 0.f ? 0.f : p.a.c.v_mul / l);
     const bool poison = steps > 0 && *reinterpret_cast<volatile int*>(&sh->poison[item & 15]) != 0;
     float* to_part = p.part + ((static_cast<int64_t>(k) * 2 + t) * 128 + r) * kDim;
@@ -745,26 +806,8 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
       }
 #pragma unroll
       for (int x = 0; x < 32; ++x) o[0][x] = n > 0 ? __float_as_uint(__uint_as_float(o[0][x]) * f) : 0u;
+      if (poison) add_odd_values<kDim, kCached>(p, cut, k, lim, i, o[0]);
       if (!mine) continue;
-      if (poison) {
-        for (int j = max(it.all, it.j0 * kKeys); j < min(lim, it.j1 * kKeys); ++j) {
-          if (kCached) {
-            const uint8_t* six = kv_sixteen(p.a.c, p.a.s, it.seq, it.head, j);
-#pragma unroll
-            for (int x = 0; x < 32; x += 16)
-              if (six != nullptr && (six[L::kVs + j % 16 * (kDim / 16) + (i * 32 + x) / 16] & 0x7F) == 0x7F)
-#pragma unroll
-                for (int y = 0; y < 16; ++y) o[0][x + y] = 0x7FC00000u;
-          } else {
-            const uint16_t* v = reinterpret_cast<const uint16_t*>(p.a.v.data + (it.sp.key0 + j) * p.a.v.row + it.head * p.a.v.head);
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const uint32_t b = v[i * 32 + x];
-              if ((b & 0x7F80u) == 0x7F80u) o[0][x] = __float_as_uint(__uint_as_float(o[0][x]) + __uint_as_float(b << 16));
-            }
-          }
-        }
-      }
       if (part) {
 #pragma unroll
         for (int x = 0; x < 32; x += 8) store32b(to_part + i * 32 + x, true, *reinterpret_cast<uint32_t(*)[8]>(&o[0][x]));
@@ -812,14 +855,13 @@ __global__ void __launch_bounds__(Layout<kDim, kCached>::kThreads, 1) k_attend(c
       mbar_init(&sh->q_empty[t], 1);
       mbar_init(&sh->q_ready[t], 4);
       mbar_init(&sh->s_full[t], 1);
-      mbar_init(&sh->p_full[t], 4);
+      mbar_init(&sh->p_full[t], 5);  // the softmax's warps, and the watch
       mbar_init(&sh->o_full[t], 1);
       mbar_init(&sh->o_empty[t], 4);
     }
     for (int i = 0; i < L::kStages; ++i) {
       mbar_init(&sh->full[i], kCached ? 4 : 1);   // expanding warps, or the copy
-      mbar_init(&sh->empty[i], kCached ? 1 : 2);  // the MMAs that read it, and the guard
-      mbar_init(&sh->v_ok[i], 1);
+      mbar_init(&sh->empty[i], 2);               // the MMAs that read it, and the watch
     }
     for (int i = 0; i < L::kRaw; ++i) {
       mbar_init(&sh->raw_full[i], 1);
@@ -852,16 +894,16 @@ __global__ void __launch_bounds__(Layout<kDim, kCached>::kThreads, 1) k_attend(c
   __syncthreads();
   tc_fence_after();
   if (warp < 8) {
-    if (!kCached) regs_inc<216>();
+    regs_inc<kCached ? 168 : 216>();
     softmax_role<kDim, kCached>(p, sh, cut, warp >> 2, q);
   } else {
-    if (!kCached) regs_dec<72>();
+    regs_dec<kCached ? 80 : 72>();
     if (warp == 8)
       load_role<kDim, kCached>(p, sh, cut, smem_u32(q), smem_u32(ring), smem_u32(raw));
     else if (warp == 9)
       mma_role<kDim, kCached>(p, sh, cut, smem_u32(q), smem_u32(ring));
-    else if (!kCached && warp == 10)
-      guard_role<kDim>(p, sh, cut, ring);
+    else if (warp == 10)
+      watch_role<kDim, kCached>(p, sh, cut, ring);
     else if (kCached && warp >= 12)
       expand_role<kDim>(p, sh, cut, ring, raw);
   }

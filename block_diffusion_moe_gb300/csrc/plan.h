@@ -99,15 +99,15 @@ inline int attend_few_rows(long long rows, int group, int seqs) { return group <
 inline bool attend_few_alone(int seqs, int heads) { return static_cast<long long>(seqs) * heads >= 2 * kAttendSms; }
 inline int attend_few_pieces(int rows, bool alone) { return kAttendSms * (alone ? (rows == 8 ? 16 : 12) : 1); }
 
-// The kernel on tensor-core tiles: items (pairs of tiles of 128 rows) that are fewer
-// than the SMs are cut into pieces; never more of them than this.
-constexpr int kAttendMaxPieces = 2 * kAttendSms;
+// The kernel on tensor-core tiles: items (pairs of tiles of 128 rows) that are at most
+// half as many as the SMs are cut into pieces, no more than SMs.
+constexpr int kAttendMaxPieces = kAttendSms;
 // Whether a call may have so few items: if even all its rows side by side make
 // fewer. (Rows of no sequence may leave fewer than counted here; those calls are not
 // cut.)
 inline bool attend_may_cut(long long rows, int group, int heads) {
   const long long pair = 2 * (128 / group);
-  return (rows + pair - 1) / pair * heads < kAttendSms;
+  return 2 * ((rows + pair - 1) / pair * heads) <= kAttendSms;
 }
 
 }  // namespace plan
