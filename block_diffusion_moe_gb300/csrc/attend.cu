@@ -33,7 +33,6 @@ namespace {
 constexpr int kKeys = 128;  // keys per step
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;  // of tile t: + 128 t
-constexpr int kWholeItems = plan::kAttendSms;  // calls of more than half as many items cut none
 constexpr int kMinSteps = 4;                   // of a piece
 
 template <int kDim, bool kCached>
@@ -53,6 +52,21 @@ struct Layout {
   static constexpr uint32_t kP = kCached ? 64 : 0;
 };
 
+constexpr int kItems = 16;  // of a CTA that are worked out at its beginning
+
+// What a CTA works on.
+struct Item {
+  SeqSpan sp;
+  int seq, head;
+  int tok0;       // first token of tile 0 in the sequence; tile t: + t * tokens
+  int n[2];       // steps of each tile
+  int all, any;   // positions below `all` are seen by every row, none from `any` on
+  int j0, j1;     // the steps of this piece
+  int part, parts;  // parts 0: nothing
+  __device__ __forceinline__ int steps(int t) const { return max(min(j1, n[t]) - j0, 0); }
+  __device__ __forceinline__ int steps() const { return max(steps(0), steps(1)); }
+};
+
 struct Shared {
   uint64_t q_full[2], q_empty[2], q_ready[2];  // ready: converted (cache)
   uint64_t full[10], empty[10];
@@ -63,19 +77,7 @@ struct Shared {
   int poison[16];  // of item k: [k % 16]
   uint32_t there[16];  // of step k: sixteens that have a page (cache)
   int sums[2][16];
-};
-
-// What a CTA works on.
-struct Item {
-  SeqSpan sp;
-  int seq, head;
-  int tok0;       // first token of tile 0 in the sequence; tile t: + t * tokens
-  int n[2];       // steps of each tile
-  int all, any;   // positions below `all` are seen by every row, none from `any` on
-  int j0, j1;     // the steps of this piece
-  int part, parts;
-  __device__ __forceinline__ int steps(int t) const { return max(min(j1, n[t]) - j0, 0); }
-  __device__ __forceinline__ int steps() const { return max(steps(0), steps(1)); }
+  Item items[kItems];  // this CTA's first
 };
 
 // How a call is cut: every item whole, its slots counted from the offsets alone; or
@@ -188,21 +190,21 @@ __device__ __forceinline__ int cta_sum(int v, int* scratch) {
 __device__ Cut cut_call(const AttendArgs& p, int (&sums)[2][16]) {
   const Cut whole = {0, p.n_slots * p.a.c.heads};
   if (!p.may_cut) return whole;
-  const int pair = 2 * p.tokens;
+  const int pair = 2 * p.tokens, ctas = gridDim.x;
   int items = 0;
   uint32_t own = 0;  // steps (what overflows belongs to too many items)
   for (int i = threadIdx.x; i < p.a.s.n; i += blockDim.x) {
     const SeqSpan sp = seq_span(p.a.s, i);
     const int tiles = (sp.rows + pair - 1) / pair;
-    items += min(tiles, kWholeItems) * p.a.c.heads;
-    if (tiles < kWholeItems)
+    items += min(tiles, ctas) * p.a.c.heads;
+    if (tiles < ctas)
       for (int t = 0; t < tiles; ++t) own += steps_of_tile(p, sp, t) * p.a.c.heads;
   }
   items = cta_sum(items, sums[0]);
-  if (2 * items > kWholeItems) return whole;
+  if (2 * items > ctas) return whole;
   const int steps = cta_sum(static_cast<int>(own), sums[1]);
   Cut cut;
-  cut.chunk = max(kMinSteps, (steps + kWholeItems - items - 1) / (kWholeItems - items));
+  cut.chunk = max(kMinSteps, (steps + ctas - items - 1) / (ctas - items));
   int pieces = 0;
   for (int i = threadIdx.x; i < p.a.s.n; i += blockDim.x) {
     const SeqSpan sp = seq_span(p.a.s, i);
@@ -212,14 +214,27 @@ __device__ Cut cut_call(const AttendArgs& p, int (&sums)[2][16]) {
   return cut;
 }
 
-// This CTA's pieces in turn: forth and back over the CTAs, so that no CTA always
-// has the longest.
-struct Turn {
-  int i = 0;
-  __device__ __forceinline__ int next() {
-    const int b = blockIdx.x, g = gridDim.x, k = i * g + (i & 1 ? g - 1 - b : b);
-    ++i;
-    return k;
+// This CTA's i-th piece: forth and back over the CTAs, so that no CTA always has the
+// longest.
+__device__ __forceinline__ int piece_at(int i) {
+  const int b = blockIdx.x, g = gridDim.x;
+  return i * g + (i & 1 ? g - 1 - b : b);
+}
+
+// A role's way through the CTA's pieces, by a whole warp.
+struct Work {
+  int i = -1;
+  // The next one that is not empty; false: there is none left.
+  __device__ __forceinline__ bool next(const AttendArgs& p, const Shared* sh, const Cut& cut, Item* it) {
+    while (piece_at(++i) < cut.pieces) {
+      if (i < kItems) {
+        *it = sh->items[i];
+        if (it->parts != 0) return true;
+      } else if (locate(p, cut, piece_at(i), it)) {
+        return true;
+      }
+    }
+    return false;
   }
 };
 
@@ -270,10 +285,9 @@ __device__ void load_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint3
   uint32_t q_count[2] = {0, 0};
   int k_step = 0;  // steps so far, of all items
   bool ok = true;
-  Turn turn;
+  Work work;
   Item it;
-  for (int k; ok && (k = turn.next()) < cut.pieces;) {
-    if (!locate(p, cut, k, &it)) continue;
+  while (ok && work.next(p, sh, cut, &it)) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       if (ok && it.steps(t) > 0) {
@@ -373,11 +387,10 @@ __device__ __forceinline__ bool issue_all(const AttendArgs& p, Shared* sh, const
       umma_bf16_ta(tmem + kTmemO + t * 128, tmem + kTmemS + t * 128 + L::kP + s * 8, b + s * 128, kIdO, s > 0 ? 1u : !first);
     if (last) umma_commit(&sh->o_full[t]);
   };
-  Turn turn;
+  Work work;
   Item it;
-  for (int k; (k = turn.next()) < cut.pieces;) {
-    const bool there = locate(p, cut, k, &it);
-    const int n0 = warp_uniform(there ? it.steps(0) : 0), n1 = warp_uniform(there ? it.steps(1) : 0), steps = max(n0, n1);
+  while (__any_sync(0xffffffffu, work.next(p, sh, cut, &it))) {
+    const int n0 = warp_uniform(it.steps(0)), n1 = warp_uniform(it.steps(1)), steps = max(n0, n1);
     if (steps == 0) continue;
     rv = rk;
     rv.next();
@@ -479,10 +492,10 @@ __device__ void watch_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint
   const int lane = threadIdx.x & 31;
   Ring<L::kStages> r;
   uint32_t count[2] = {0, 0};
-  Turn turn;
+  Work work;
   Item it;
-  for (int k, item = -1; (k = turn.next()) < cut.pieces;) {
-    if (!locate(p, cut, k, &it) || it.steps() == 0) continue;
+  for (int item = -1; work.next(p, sh, cut, &it);) {
+    if (it.steps() == 0) continue;
     // (items with steps are counted; of a ring of 16, eight on, or back, is out of
     // everyone's reach)
     ++item;
@@ -519,21 +532,34 @@ __device__ void watch_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint
 // scale) of a key at a time. Neighbouring lanes take one key's codes, so that reads
 // do not meet in a bank; of the two 16-byte pieces a lane writes, the upper half of
 // a 128-element key swaps the order, so that writes do not either.
-// kValues: the bytes of positions pos + .. that are not to count are replaced.
+// kValues: the scales of positions pos + .. that are not to count are replaced; true:
+// there were NaN among them.
 template <int kDim, bool kValues>
 __device__ __forceinline__ bool expand_tile(const uint8_t* raw, uint8_t* tile, int warp, uint32_t there, int all, int any, int pos) {
   using L = Layout<kDim, true>;
   constexpr int kPer = kDim / 16;            // lanes of a key
   constexpr int kRows = 32 / kPer;           // keys of a warp at a time
-  const int lane = threadIdx.x & 31, c = lane % kPer, swap = kDim == 128 && c >= 4;
+  const int lane = threadIdx.x & 31, c = lane % kPer, key = lane / kPer;
+  const bool swap = kDim == 128 && c >= 4;
+  // (row = warp 32 + i kRows + key; what follows from i is known when this is compiled)
+  const uint8_t* codes = raw + warp * 2 * L::kSixteen + (kValues ? L::kV : 0) + key * (kDim / 2) + c * 8;
+  const uint8_t* scales = raw + warp * 2 * L::kSixteen + (kValues ? L::kVs : L::kKs) + key * kPer + c;
+  uint8_t* to[2][2];  // first and second piece of rows whose number mod 8 is below and from 4 on (64 elements: one kind)
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int chunk = 2 * c + (h ^ static_cast<int>(swap));
+    uint8_t* at = tile + (chunk / 8) * L::kSlab + (warp * 32 + key) * 128;
+    to[h][0] = at + ((chunk & 7) ^ key) * 16;
+    to[h][1] = at + ((chunk & 7) ^ key ^ 4) * 16;
+  }
   bool poison = false;
-#pragma unroll 4
+#pragma unroll
   for (int i = 0; i < 32 / kRows; ++i) {
-    const int row = warp * 32 + i * kRows + lane / kPer, in = row & 15;
-    const uint8_t* six = raw + (row >> 4) * L::kSixteen + (kValues ? L::kV : 0);
-    const uint2 w = *reinterpret_cast<const uint2*>(six + in * (kDim / 2) + c * 8);
-    uint32_t b = six[8 * kDim + in * kPer + c];
+    const int in = i * kRows;  // of the warp's rows, less key
+    const uint2 w = *reinterpret_cast<const uint2*>(codes + (in / 16) * L::kSixteen + (in % 16) * (kDim / 2));
+    uint32_t b = scales[(in / 16) * L::kSixteen + (in % 16) * kPer];
     if (kValues) {
+      const int row = warp * 32 + in + key;
       if (pos + row >= any || !(there >> (row >> 4) & 1u)) b = 0;
       if (pos + row >= all && (b & 0x7Fu) == 0x7Fu) {
         poison = true;
@@ -544,14 +570,13 @@ __device__ __forceinline__ bool expand_tile(const uint8_t* raw, uint8_t* tile, i
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       __half2 v[4];
-      expand_word((h ^ swap) ? w.y : w.x, v);
+      expand_word((h == 1) != swap ? w.y : w.x, v);
       uint4 o;
       o.x = half2_word(__hmul2(v[0], s));
       o.y = half2_word(__hmul2(v[1], s));
       o.z = half2_word(__hmul2(v[2], s));
       o.w = half2_word(__hmul2(v[3], s));
-      const int chunk = 2 * c + (h ^ swap);
-      *reinterpret_cast<uint4*>(tile + (chunk / 8) * L::kSlab + row * 128 + ((chunk & 7) ^ (row & 7)) * 16) = o;
+      *reinterpret_cast<uint4*>(to[h][kRows == 4 ? i & 1 : 0] + in * 128) = o;
     }
   }
   return poison;
@@ -564,10 +589,10 @@ __device__ void expand_role(const AttendArgs& p, Shared* sh, const Cut& cut, uin
   Ring<L::kStages> r;
   Ring<L::kRaw> rr;
   int k_step = 0;
-  Turn turn;
+  Work work;
   Item it;
-  for (int k, item = -1; (k = turn.next()) < cut.pieces;) {
-    if (!locate(p, cut, k, &it) || it.steps() == 0) continue;
+  for (int item = -1; work.next(p, sh, cut, &it);) {
+    if (it.steps() == 0) continue;
     ++item;
     if (warp == 0 && lane == 0) *reinterpret_cast<volatile int*>(&sh->poison[(item + 8) & 15]) = 0;
     __syncwarp();
@@ -583,7 +608,7 @@ __device__ void expand_role(const AttendArgs& p, Shared* sh, const Cut& cut, uin
         if (v == 0) {
           expand_tile<kDim, false>(from, tile, warp, there, 0, 0, 0);
         } else if (there == 0xFFu && pos + kKeys <= it.all) {
-          expand_tile<kDim, true>(from, tile, warp, 0xFFu, 0x7fffffff, 0x7fffffff, 0);
+          expand_tile<kDim, false>(from + L::kV, tile, warp, there, 0, 0, 0);
         } else if (__any_sync(0xffffffffu, expand_tile<kDim, true>(from, tile, warp, there, it.all, it.any, pos))) {
           if (lane == 0) *reinterpret_cast<volatile int*>(&sh->poison[item & 15]) = 1;
         }
@@ -700,15 +725,15 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
   const int tok_in = r / p.a.group, head_in = r - tok_in * p.a.group;
   uint32_t s_count = 0, q_count = 0;
   int k_step = 0;
-  Turn turn;
-  for (int k, item = -1; (k = turn.next()) < cut.pieces;) {
+  Work work;
+  for (int item = -1;;) {
     // what outlives this block lives in registers beside the scores
     int lim, whole, n, steps, j0;
     bool mine, part;
     int64_t at;  // the row in out and lse
     {
       Item it;
-      if (!locate(p, cut, k, &it)) continue;
+      if (!work.next(p, sh, cut, &it)) break;
       const int tok = it.tok0 + t * p.tokens + tok_in;
       mine = tok_in < p.tokens && tok < it.sp.rows;
       lim = mine ? seen_by(p, it.sp, tok) : 0;
@@ -795,7 +820,9 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
     tc_fence_after();
     const float f = part ? 1.f : (l == 0.f ? 0.f : p.a.c.v_mul / l);
     const bool poison = steps > 0 && *reinterpret_cast<volatile int*>(&sh->poison[item & 15]) != 0;
-    float* to_part = p.part + ((static_cast<int64_t>(k) * 2 + t) * 128 + r) * kDim;
+    const int k = piece_at(work.i);
+    // (a piece's sums: four columns of all rows next to one another, as the lanes have them)
+    float4* to_part = reinterpret_cast<float4*>(p.part + (static_cast<int64_t>(k) * 2 + t) * 128 * kDim) + r;
 #pragma unroll 1
     for (int i = 0; i < kDim / 32; ++i) {
       uint32_t o[1][32];
@@ -810,7 +837,9 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
       if (!mine) continue;
       if (part) {
 #pragma unroll
-        for (int x = 0; x < 32; x += 8) store32b(to_part + i * 32 + x, true, *reinterpret_cast<uint32_t(*)[8]>(&o[0][x]));
+        for (int x = 0; x < 8; ++x)
+          __stcg(to_part + (i * 8 + x) * 128, make_float4(__uint_as_float(o[0][4 * x]), __uint_as_float(o[0][4 * x + 1]),
+                                                          __uint_as_float(o[0][4 * x + 2]), __uint_as_float(o[0][4 * x + 3])));
         continue;
       }
       uint32_t w[2][8];
@@ -830,7 +859,7 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
     }
     m -= L::kLift;
     if (part) {
-      p.part_ml[(static_cast<int64_t>(k) * 2 + t) * 128 + r] = make_float2(m, l);
+      __stcg(&p.part_ml[(static_cast<int64_t>(k) * 2 + t) * 128 + r], make_float2(m, l));
     } else if (mine && p.a.lse != nullptr) {
       p.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
@@ -885,6 +914,17 @@ __global__ void __launch_bounds__(Layout<kDim, kCached>::kThreads, 1) k_attend(c
   pdl_wait();
   pdl_trigger();
   const Cut cut = cut_call(p, sh->sums);
+  for (int i = warp; i < kItems && piece_at(i) < cut.pieces; i += L::kThreads / 32) {
+    Item it;
+    if (!locate(p, cut, piece_at(i), &it)) it.parts = 0;
+    if (elect_one()) {
+      sh->items[i] = it;
+      if (i == 0 && cut.chunk != 0)
+        p.joins[blockIdx.x] = {it.parts, it.part, it.head, it.sp.row0 + it.tok0, min(2 * p.tokens, it.sp.rows - it.tok0)};
+    }
+    __syncwarp();
+  }
+  if (p.may_cut && threadIdx.x == 0 && (cut.chunk == 0 || blockIdx.x >= cut.pieces)) p.joins[blockIdx.x].parts = 0;
   if (blockIdx.x >= cut.pieces) return;  // the whole CTA
   if (warp == 9) {
     tmem_alloc(&sh->tmem, kTmemCols);
@@ -916,67 +956,56 @@ __global__ void __launch_bounds__(Layout<kDim, kCached>::kThreads, 1) k_attend(c
   }
 }
 
-// The pieces' sums of cut items, joined: a CTA for each piece, which takes its share
-// of the item's rows, one warp per row.
+// The pieces' sums of cut items, joined. Each piece has kJoinCtas CTAs, which with
+// those of the item's other pieces share its outputs: a warp takes four columns of 32
+// rows, a row to a lane, and has the loads of 16 pieces in flight.
+constexpr int kJoinCtas = 4;
+
 template <int kDim>
-__global__ void __launch_bounds__(128) k_attend_join(const __grid_constant__ AttendArgs p) {
-  __shared__ int sums[2][16];
+__global__ void __launch_bounds__(256) k_attend_join(const __grid_constant__ AttendArgs p) {
   pdl_wait();
   pdl_trigger();
-  const Cut cut = cut_call(p, sums);
-  Item it;
-  if (cut.chunk == 0 || blockIdx.x >= cut.pieces || !locate(p, cut, blockIdx.x, &it) || it.parts == 1) return;
-  constexpr int kPer = kDim / 32;
-  const int lane = threadIdx.x & 31, k0 = blockIdx.x - it.part;
-  const int rows = min(2 * p.tokens, it.sp.rows - it.tok0) * p.a.group;
-  for (int i = it.part * 4 + (threadIdx.x >> 5); i < rows; i += it.parts * 4) {
-    const int tok_in = i / p.a.group, t = tok_in >= p.tokens, head_in = i - tok_in * p.a.group;
-    const int r = t * 128 + (tok_in - t * p.tokens) * p.a.group + head_in;
-    float m = -INFINITY, l = 0.f, o[kPer] = {};
-    constexpr int kBatch = 8;
+  const int k = blockIdx.x / kJoinCtas;
+  const AttendJoin it = p.joins[k];
+  if (it.parts <= 1) return;
+  const int lane = threadIdx.x & 31, k0 = k - it.part;
+  const int first = (it.part * kJoinCtas + blockIdx.x % kJoinCtas) * 8 + (threadIdx.x >> 5);
+  for (int u = first; u < 8 * (kDim / 4); u += it.parts * kJoinCtas * 8) {
+    const int r = (u & 7) * 32 + lane, t = r >> 7, tok_in = (r & 127) / p.a.group, tok = t * p.tokens + tok_in, d4 = u >> 3;
+    if (tok_in >= p.tokens || tok >= it.tokens) continue;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kBatch = 16;
     for (int b = 0; b < it.parts; b += kBatch) {
       float2 ml[kBatch];
-      float v[kBatch][kPer];
+      float4 v[kBatch];
       float top = m;
 #pragma unroll
       for (int x = 0; x < kBatch; ++x) {
-        const int64_t at = static_cast<int64_t>(k0 + min(b + x, it.parts - 1)) * 256 + r;
-        ml[x] = __ldcg(&p.part_ml[at]);
-        if constexpr (kDim == 128) {
-          const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part + at * kDim) + lane);
-          v[x][0] = y.x, v[x][1] = y.y, v[x][kPer - 2] = y.z, v[x][kPer - 1] = y.w;
-        } else {
-          const float2 y = __ldcg(reinterpret_cast<const float2*>(p.part + at * kDim) + lane);
-          v[x][0] = y.x, v[x][1] = y.y;
-        }
+        const int64_t at = k0 + min(b + x, it.parts - 1);
+        ml[x] = __ldcg(&p.part_ml[at * 256 + r]);
+        v[x] = __ldcg(reinterpret_cast<const float4*>(p.part + (at * 2 + t) * 128 * kDim) + d4 * 128 + (r & 127));
       }
 #pragma unroll
       for (int x = 0; x < kBatch; ++x) top = fmaxf(top, ml[x].x);
       const float f = m == top ? 1.f : exp2_fast(m - top);
       m = top;
       l *= f;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) o[e] *= f;
+      o.x *= f, o.y *= f, o.z *= f, o.w *= f;
 #pragma unroll
       for (int x = 0; x < kBatch; ++x) {
         if (b + x >= it.parts) continue;
         const float w = ml[x].x == m ? 1.f : exp2_fast(ml[x].x - m);
         l += w * ml[x].y;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) o[e] += w * v[x][e];
+        o.x += w * v[x].x, o.y += w * v[x].y, o.z += w * v[x].z, o.w += w * v[x].w;
       }
     }
-    const int64_t at = static_cast<int64_t>(it.sp.row0 + it.tok0 + tok_in) * p.a.q_heads + it.head * p.a.group + head_in;
+    const int64_t at = static_cast<int64_t>(it.row0 + tok) * p.a.q_heads + it.head * p.a.group + (r & 127) - tok_in * p.a.group;
     const float inv = l == 0.f ? 0.f : p.a.c.v_mul / l;
-    const __nv_bfloat162 a = __floats2bfloat162_rn(o[0] * inv, o[1] * inv);
-    if constexpr (kDim == 128) {
-      const __nv_bfloat162 c = __floats2bfloat162_rn(o[kPer - 2] * inv, o[kPer - 1] * inv);
-      reinterpret_cast<uint2*>(p.a.out + at * kDim)[lane] =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
-    } else {
-      reinterpret_cast<uint32_t*>(p.a.out + at * kDim)[lane] = *reinterpret_cast<const uint32_t*>(&a);
-    }
-    if (lane == 0 && p.a.lse != nullptr) p.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), c = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(p.a.out + at * kDim + d4 * 4) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
+    if (d4 == 0 && p.a.lse != nullptr) p.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   }
 }
 
@@ -989,7 +1018,7 @@ static cudaError_t launch(const AttendArgs& a, int grid, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_kernel(k_attend<kDim, kCached>, dim3(grid), dim3(L::kThreads), smem, s, true, a);
   if (e != cudaSuccess || !a.may_cut) return e;
-  return launch_kernel(k_attend_join<kDim>, dim3(plan::kAttendMaxPieces), dim3(128), 0, s, true, a);
+  return launch_kernel(k_attend_join<kDim>, dim3(grid * kJoinCtas), dim3(256), 0, s, true, a);
 }
 
 cudaError_t launch_attend(const AttendArgs& args, bool cached, int sms, cudaStream_t s) {

@@ -60,6 +60,12 @@ struct AttnArgs {
   int* err;
 };
 
+// A piece of a cut item: which of how many (at most one: nothing to join), and the
+// item's rows.
+struct AttendJoin {
+  int parts, part, head, row0, tokens;
+};
+
 // Attention on tensor-core tiles (csrc/attend.cu). A tile is 128 rows: the
 // group's query heads of `tokens` = 128 / group consecutive tokens, row
 // token * group + head.
@@ -71,8 +77,9 @@ struct AttendArgs {
   int tokens;
   int n_slots;         // pairs of tiles: n_rows / (2 tokens) + the number of sequences
   int may_cut;         // few items are cut into pieces
-  float* part;         // [pieces][256][dim] sums of pieces (workspace)
+  float* part;         // [pieces][2][dim / 4][128][4] sums of pieces (workspace)
   float2* part_ml;     // [pieces][256] their maxima and sums of weights
+  AttendJoin* joins;   // [pieces]
   uint32_t per_magic;  // set by the launch: 2^32 / sixteens of a page, rounded up (0: one)
 };
 
