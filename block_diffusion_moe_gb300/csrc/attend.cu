@@ -40,11 +40,11 @@ struct Layout {
   static constexpr int kThreads = kCached ? 512 : 384;
   static constexpr int kTileBytes = 128 * kDim * 2;  // of Q, of K, of V
   static constexpr int kSlab = 128 * 128;            // 64 elements of 128 rows
-  static constexpr int kStages = (kCached ? 3 : 5) * (128 / kDim);
+  static constexpr int kStages = (kCached ? 4 : 5) * (128 / kDim);
   static constexpr int kSixteen = 18 * kDim;  // bytes of 16 tokens in the cache
-  static constexpr int kKs = 8 * kDim, kV = 9 * kDim, kVs = 17 * kDim;
-  static constexpr int kRawBytes = 8 * kSixteen;
-  static constexpr int kRaw = kCached ? 3 * (128 / kDim) : 0;  // steps' codes and scales
+  static constexpr int kHalf = 9 * kDim;      // of their keys, or of their values: codes, then scales
+  static constexpr int kRawBytes = 8 * kHalf;  // a tile's
+  static constexpr int kRaw = kCached ? 3 * (128 / kDim) : 0;
   // Cache: numerators are 2^(c S - m + 11), m up to 2^4 behind: at most 2^15, and what
   // fp16 rounds by more than half a step, or to 0, is 2^-36 of the largest.
   static constexpr float kGrowth = kCached ? 4.f : 8.f, kLift = kCached ? 11.f : 0.f;
@@ -71,7 +71,7 @@ struct Shared {
   uint64_t q_full[2], q_empty[2], q_ready[2];  // ready: converted (cache)
   uint64_t full[10], empty[10];
   uint64_t raw_full[6], raw_empty[6];
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2];
   uint64_t drain;
   uint32_t tmem, abort;
   int poison[16];  // of item k: [k % 16]
@@ -319,30 +319,34 @@ __device__ void load_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint3
         flight.add(r.st, r.ph);
       }
     } else {
-      // lane i looks up the sixteen i % 8 of step i / 8 on, four steps at a time
+      // keys, then values of each step; lane i looks up the sixteen i % 8 of step i / 8 on,
+      // four steps at a time
       const int per = p.a.c.page_tokens / 16;
       int from = -1;
-      for (int i = 0; i < steps && ok; ++i, r.next(), ++k_step) {
-        if ((i & 3) == 0) {
-          const int x = (it.j0 + i) * 8 + lane;
+      uint32_t all = 0;
+      for (int i = 0; i < 2 * steps && ok; ++i, r.next()) {
+        if ((i & 7) == 0) {
+          const int x = (it.j0 + (i >> 1)) * 8 + lane;
           from = -1;
-          if (x * 16 < it.any && i + (lane >> 3) < steps) {
+          if (x * 16 < it.any && (i >> 1) + (lane >> 3) < steps) {
             const int entry = p.per_magic != 0 ? static_cast<int>(__umulhi(x, p.per_magic)) : x;
             const int page = p.a.s.table[static_cast<int64_t>(it.seq) * p.a.s.max_pages + entry];
             if (page >= 0 && page < p.a.c.n_pages) from = (page * p.a.c.heads + it.head) * per + (x - entry * per);
           }
+          all = __ballot_sync(0xffffffffu, from >= 0);
         }
-        const int at = __shfl_sync(0xffffffffu, from, (i & 3) * 8 + (lane & 7));
-        const uint32_t has = __ballot_sync(0xffffffffu, at >= 0) & 0xFFu;
+        const int at = __shfl_sync(0xffffffffu, from, (i & 6) * 4 + (lane & 7));
+        const uint32_t has = all >> ((i & 6) * 4) & 0xFFu;
         if (!(ok = warp_wait(p, sh, &sh->raw_empty[r.st], r.ph ^ 1u))) break;
         if (lane == 0) {
-          *reinterpret_cast<volatile uint32_t*>(&sh->there[k_step & 15]) = has;
-          mbar_arrive_expect_tx(&sh->raw_full[r.st], __popc(has) * L::kSixteen);
+          if ((i & 1) == 0) *reinterpret_cast<volatile uint32_t*>(&sh->there[k_step & 15]) = has;
+          mbar_arrive_expect_tx(&sh->raw_full[r.st], __popc(has) * L::kHalf);
         }
+        k_step += i & 1;
         __syncwarp();
         if (lane < 8 && at >= 0)
-          bulk_load(raw + r.st * L::kRawBytes + lane * L::kSixteen, p.a.c.pages + static_cast<int64_t>(at) * L::kSixteen,
-                    L::kSixteen, &sh->raw_full[r.st]);
+          bulk_load(raw + r.st * L::kRawBytes + lane * L::kHalf,
+                    p.a.c.pages + static_cast<int64_t>(at) * L::kSixteen + (i & 1) * L::kHalf, L::kHalf, &sh->raw_full[r.st]);
         __syncwarp();
         flight.add(r.st, r.ph);
       }
@@ -368,25 +372,31 @@ __device__ __forceinline__ bool issue_all(const AttendArgs& p, Shared* sh, const
   const uint32_t tmem = static_cast<uint32_t>(warp_uniform(static_cast<int>(sh->tmem)));
   Ring<L::kStages> rk, rv;
   uint32_t items0 = 0, items1 = 0, steps0 = 0, steps1 = 0;
-  // (by one lane) tile t's scores of a step, whose keys the ring's rk holds
-  auto scores = [&](int t, bool last) {
-    const uint64_t a = umma_desc_sw128(q + t * L::kTileBytes), b = umma_desc_sw128(ring + rk.st * L::kTileBytes);
+  // a descriptor whose address (in units of 16 bytes) is `at` further on than that of
+  // the first Q tile or stage
+  const uint64_t q_desc = umma_desc_sw128(q), k_desc = umma_desc_sw128(ring), v_desc = umma_desc_sw128_mn(ring, L::kSlab);
+  auto at = [](uint64_t desc, uint32_t by) {
+    return desc & ~0xFFFFFFFFull | static_cast<uint32_t>(desc) + by;
+  };
+  // (by one lane) tile t's scores of a step, whose keys lie in the ring at rk's stage
+  auto scores = [&](int t, uint32_t k_at, bool last) {
 #pragma unroll
     for (int s = 0; s < kDim / 16; ++s) {
       const uint32_t o = (s / 4) * (L::kSlab >> 4) + (s % 4) * 2;
-      umma_bf16(tmem + kTmemS + t * 128, a + o, b + o, kIdS, s > 0);
+      umma_bf16(tmem + kTmemS + t * 128, at(q_desc, t * (L::kTileBytes >> 4) + o), at(k_desc, k_at + o), kIdS, s > 0);
     }
     umma_commit(&sh->s_full[t]);
     if (last) umma_commit(&sh->q_empty[t]);
   };
-  // (by one lane) its numerators times the values that rv holds
-  auto sums = [&](int t, bool first, bool last) {
-    const uint64_t b = umma_desc_sw128_mn(ring + rv.st * L::kTileBytes, L::kSlab);
+  // (by one lane) half of its numerators times the values that rv holds: the upper 64
+  // keys' come first
+  auto sums = [&](int t, int h, uint32_t v_at, bool first) {
 #pragma unroll
-    for (int s = 0; s < kKeys / 16; ++s)
-      umma_bf16_ta(tmem + kTmemO + t * 128, tmem + kTmemS + t * 128 + L::kP + s * 8, b + s * 128, kIdO, s > 0 ? 1u : !first);
-    if (last) umma_commit(&sh->o_full[t]);
+    for (int s = h * 4; s < h * 4 + 4; ++s)
+      umma_bf16_ta(tmem + kTmemO + t * 128, tmem + kTmemS + t * 128 + L::kP + s * 8, at(v_desc, v_at + s * 128), kIdO,
+                   s != 4 ? 1u : !first);
   };
+  auto stage = [](int st) { return static_cast<uint32_t>(warp_uniform(st * (L::kTileBytes >> 4))); };
   Work work;
   Item it;
   while (__any_sync(0xffffffffu, work.next(p, sh, cut, &it))) {
@@ -398,23 +408,30 @@ __device__ __forceinline__ bool issue_all(const AttendArgs& p, Shared* sh, const
     if (n1 > 0 && !warp_wait(p, sh, kCached ? &sh->q_ready[1] : &sh->q_full[1], items1 & 1)) return false;
     if (!warp_wait(p, sh, &sh->full[rk.st], rk.ph)) return false;
     tc_fence_after();
+    const uint32_t k_first = stage(rk.st);
     if (elect_one()) {
-      if (n0 > 0) scores(0, n0 == 1);
-      if (n1 > 0) scores(1, n1 == 1);
+      if (n0 > 0) scores(0, k_first, n0 == 1);
+      if (n1 > 0) scores(1, k_first, n1 == 1);
       umma_commit(&sh->empty[rk.st]);
     }
     __syncwarp();
     for (int j = 0; j < steps; ++j) {
       rk.next(2);
-      // p_full: the numerators are in place, and the values of this step and the keys
-      // of the next one; o_empty: the sums of the item before are read
+      const uint32_t k_at = stage(rk.st), v_at = stage(rv.st);
+      // p_half: half the numerators are in place, and the values of this step and the
+      // keys of the next one; o_empty: the sums of the item before are read
       if (j < n0) {
         if (j == 0 && !warp_wait(p, sh, &sh->o_empty[0], (items0 & 1) ^ 1u)) return false;
+        if (!warp_wait(p, sh, &sh->p_half[0], steps0 & 1)) return false;
+        tc_fence_after();
+        if (elect_one()) sums(0, 1, v_at, j == 0);
+        __syncwarp();
         if (!warp_wait(p, sh, &sh->p_full[0], steps0++ & 1)) return false;
         tc_fence_after();
         if (elect_one()) {
-          sums(0, j == 0, j + 1 == n0);
-          if (j + 1 < n0) scores(0, j + 2 == n0);
+          sums(0, 0, v_at, false);
+          if (j + 1 == n0) umma_commit(&sh->o_full[0]);
+          if (j + 1 < n0) scores(0, k_at, j + 2 == n0);
           if (j >= n1) {
             umma_commit(&sh->empty[rv.st]);
             if (j + 1 < steps) umma_commit(&sh->empty[rk.st]);
@@ -424,11 +441,16 @@ __device__ __forceinline__ bool issue_all(const AttendArgs& p, Shared* sh, const
       }
       if (j < n1) {
         if (j == 0 && !warp_wait(p, sh, &sh->o_empty[1], (items1 & 1) ^ 1u)) return false;
+        if (!warp_wait(p, sh, &sh->p_half[1], steps1 & 1)) return false;
+        tc_fence_after();
+        if (elect_one()) sums(1, 1, v_at, j == 0);
+        __syncwarp();
         if (!warp_wait(p, sh, &sh->p_full[1], steps1++ & 1)) return false;
         tc_fence_after();
         if (elect_one()) {
-          sums(1, j == 0, j + 1 == n1);
-          if (j + 1 < n1) scores(1, j + 2 == n1);
+          sums(1, 0, v_at, false);
+          if (j + 1 == n1) umma_commit(&sh->o_full[1]);
+          if (j + 1 < n1) scores(1, k_at, j + 2 == n1);
           umma_commit(&sh->empty[rv.st]);
           if (j + 1 < steps) umma_commit(&sh->empty[rk.st]);
         }
@@ -520,21 +542,21 @@ __device__ void watch_role(const AttendArgs& p, Shared* sh, const Cut& cut, uint
       for (int t = 0; t < 2; ++t) {
         if (j >= it.steps(t)) continue;
         // (not before the step before has been through)
-        if (!warp_wait(p, sh, &sh->p_full[t], (count[t] & 1) ^ 1u)) return;
+        if (!warp_wait(p, sh, &sh->p_half[t], (count[t] & 1) ^ 1u)) return;
         ++count[t];
-        if (lane == 0) mbar_arrive(&sh->p_full[t]);
+        if (lane == 0) mbar_arrive(&sh->p_half[t]);
       }
     }
   }
 }
 
-// One tile of 128 rows from a step's codes: 4 warps, a lane takes 16 codes (one
+// A tile of 128 rows from its codes: 4 warps, 32 rows each; a lane takes 16 codes (one
 // scale) of a key at a time. Neighbouring lanes take one key's codes, so that reads
 // do not meet in a bank; of the two 16-byte pieces a lane writes, the upper half of
 // a 128-element key swaps the order, so that writes do not either.
-// kValues: the scales of positions pos + .. that are not to count are replaced; true:
+// kGuard: the scales of positions pos + .. that are not to count are replaced; true:
 // there were NaN among them.
-template <int kDim, bool kValues>
+template <int kDim, bool kGuard>
 __device__ __forceinline__ bool expand_tile(const uint8_t* raw, uint8_t* tile, int warp, uint32_t there, int all, int any, int pos) {
   using L = Layout<kDim, true>;
   constexpr int kPer = kDim / 16;            // lanes of a key
@@ -542,8 +564,8 @@ __device__ __forceinline__ bool expand_tile(const uint8_t* raw, uint8_t* tile, i
   const int lane = threadIdx.x & 31, c = lane % kPer, key = lane / kPer;
   const bool swap = kDim == 128 && c >= 4;
   // (row = warp 32 + i kRows + key; what follows from i is known when this is compiled)
-  const uint8_t* codes = raw + warp * 2 * L::kSixteen + (kValues ? L::kV : 0) + key * (kDim / 2) + c * 8;
-  const uint8_t* scales = raw + warp * 2 * L::kSixteen + (kValues ? L::kVs : L::kKs) + key * kPer + c;
+  const uint8_t* codes = raw + warp * 2 * L::kHalf + key * (kDim / 2) + c * 8;
+  const uint8_t* scales = raw + warp * 2 * L::kHalf + 8 * kDim + key * kPer + c;
   uint8_t* to[2][2];  // first and second piece of rows whose number mod 8 is below and from 4 on (64 elements: one kind)
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -556,9 +578,9 @@ __device__ __forceinline__ bool expand_tile(const uint8_t* raw, uint8_t* tile, i
 #pragma unroll
   for (int i = 0; i < 32 / kRows; ++i) {
     const int in = i * kRows;  // of the warp's rows, less key
-    const uint2 w = *reinterpret_cast<const uint2*>(codes + (in / 16) * L::kSixteen + (in % 16) * (kDim / 2));
-    uint32_t b = scales[(in / 16) * L::kSixteen + (in % 16) * kPer];
-    if (kValues) {
+    const uint2 w = *reinterpret_cast<const uint2*>(codes + (in / 16) * L::kHalf + (in % 16) * (kDim / 2));
+    uint32_t b = scales[(in / 16) * L::kHalf + (in % 16) * kPer];
+    if (kGuard) {
       const int row = warp * 32 + in + key;
       if (pos + row >= any || !(there >> (row >> 4) & 1u)) b = 0;
       if (pos + row >= all && (b & 0x7Fu) == 0x7Fu) {
@@ -596,27 +618,26 @@ __device__ void expand_role(const AttendArgs& p, Shared* sh, const Cut& cut, uin
     ++item;
     if (warp == 0 && lane == 0) *reinterpret_cast<volatile int*>(&sh->poison[(item + 8) & 15]) = 0;
     __syncwarp();
-    for (int i = 0; i < it.steps(); ++i, rr.next(), ++k_step) {
-      if (!warp_wait(p, sh, &sh->raw_full[rr.st], rr.ph)) return;
-      const uint32_t there = *reinterpret_cast<volatile uint32_t*>(&sh->there[k_step & 15]);
-      const uint8_t* from = raw + rr.st * L::kRawBytes;
+    for (int i = 0; i < it.steps(); ++i, ++k_step) {
       const int pos = (it.j0 + i) * kKeys;
 #pragma unroll
-      for (int v = 0; v < 2; ++v, r.next()) {
-        if (!warp_wait(p, sh, &sh->empty[r.st], r.ph ^ 1u)) return;
+      for (int v = 0; v < 2; ++v, r.next(), rr.next()) {
+        if (!warp_wait(p, sh, &sh->raw_full[rr.st], rr.ph) || !warp_wait(p, sh, &sh->empty[r.st], r.ph ^ 1u)) return;
+        const uint8_t* from = raw + rr.st * L::kRawBytes;
         uint8_t* tile = ring + r.st * L::kTileBytes;
-        if (v == 0) {
+        const uint32_t there = *reinterpret_cast<volatile uint32_t*>(&sh->there[k_step & 15]);
+        if (v == 0 || (there == 0xFFu && pos + kKeys <= it.all)) {
           expand_tile<kDim, false>(from, tile, warp, there, 0, 0, 0);
-        } else if (there == 0xFFu && pos + kKeys <= it.all) {
-          expand_tile<kDim, false>(from + L::kV, tile, warp, there, 0, 0, 0);
         } else if (__any_sync(0xffffffffu, expand_tile<kDim, true>(from, tile, warp, there, it.all, it.any, pos))) {
           if (lane == 0) *reinterpret_cast<volatile int*>(&sh->poison[item & 15]) = 1;
         }
         fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->full[r.st]);
+        if (lane == 0) {
+          mbar_arrive(&sh->full[r.st]);
+          mbar_arrive(&sh->raw_empty[rr.st]);
+        }
       }
-      if (lane == 0) mbar_arrive(&sh->raw_empty[rr.st]);
     }
   }
 }
@@ -656,16 +677,18 @@ __device__ __forceinline__ int convert_row(uint8_t* q, int r) {
 // Numerators of 64 scores to tensor memory as 32 columns of pairs; returns their sum.
 template <bool kHalf>
 __device__ __forceinline__ float numerators(const uint32_t (&s)[2][32], float c, float lift, uint32_t to) {
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  uint64_t sum[2] = {0, 0};
+  const uint64_t c2 = pack2(c, c), lift2 = pack2(lift, lift);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t w[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      const float a = exp2_fast(fmaf(__uint_as_float(s[h][2 * k]), c, lift));
-      const float b = exp2_fast(fmaf(__uint_as_float(s[h][2 * k + 1]), c, lift));
-      sum[(2 * k) & 3] += a;
-      sum[(2 * k + 1) & 3] += b;
+      float a, b;
+      unpack2(fma2(pack2(__uint_as_float(s[h][2 * k]), __uint_as_float(s[h][2 * k + 1])), c2, lift2), &a, &b);
+      a = exp2_fast(a);
+      b = exp2_fast(b);
+      sum[k & 1] = add2(sum[k & 1], pack2(a, b));
       if (kHalf) {
         w[k] = half2_word(__floats2half2_rn(a, b));
       } else {
@@ -675,7 +698,9 @@ __device__ __forceinline__ float numerators(const uint32_t (&s)[2][32], float c,
     }
     tmem_st16(to + h * 16, w);
   }
-  return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  float a, b;
+  unpack2(add2(sum[0], sum[1]), &a, &b);
+  return a + b;
 }
 
 // Scores of 64 keys from key `at` of the step on that the row does not see: -inf.
@@ -704,7 +729,7 @@ __device__ __noinline__ void add_odd_values(const AttendArgs& p, const Cut& cut,
     if (kCached) {
       const uint8_t* six = kv_sixteen(p.a.c, p.a.s, it.seq, it.head, j);
       for (int x = 0; x < 32; ++x)
-        if (six != nullptr && (six[L::kVs + j % 16 * (kDim / 16) + (i * 32 + x) / 16] & 0x7F) == 0x7F) o[x] = 0x7FC00000u;
+        if (six != nullptr && (six[17 * kDim + j % 16 * (kDim / 16) + (i * 32 + x) / 16] & 0x7F) == 0x7F) o[x] = 0x7FC00000u;
     } else {
       const uint16_t* v = reinterpret_cast<const uint16_t*>(p.a.v.data + (it.sp.key0 + j) * p.a.v.row + it.head * p.a.v.head);
       for (int x = 0; x < 32; ++x) {
@@ -800,6 +825,10 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
       }
       const float lift = L::kLift - (m == -INFINITY ? 0.f : m);
       l += numerators<kCached>(hi, c, lift, s_at + L::kP + 32);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->p_half[t]);
       if (kCached) {  // (registers do not hold all scores beside the roles that share them: half are read again)
         tmem_ld32_async(s_at, lo[0]);
         tmem_ld32_async(s_at + 32, lo[1]);
@@ -884,7 +913,8 @@ __global__ void __launch_bounds__(Layout<kDim, kCached>::kThreads, 1) k_attend(c
       mbar_init(&sh->q_empty[t], 1);
       mbar_init(&sh->q_ready[t], 4);
       mbar_init(&sh->s_full[t], 1);
-      mbar_init(&sh->p_full[t], 5);  // the softmax's warps, and the watch
+      mbar_init(&sh->p_half[t], 5);  // the softmax's warps, and the watch
+      mbar_init(&sh->p_full[t], 4);
       mbar_init(&sh->o_full[t], 1);
       mbar_init(&sh->o_empty[t], 4);
     }
