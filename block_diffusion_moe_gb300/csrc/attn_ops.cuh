@@ -41,7 +41,9 @@ struct KvCopyArgs {  // write: k, v -> cache; read: cache -> k_out, v_out
   AttnRows k, v;
   __nv_bfloat16* k_out;
   __nv_bfloat16* v_out;
-  int wide;  // set by the launch: 32-byte accesses to the rows are aligned
+  int wide;            // set by the launch: 32-byte accesses to the rows are aligned
+  int cta_rows;        // set by the launch: rows of a CTA
+  uint32_t row_magic;  // set by the launch: 2^32 / blocks of a row, rounded up (0: divide)
 };
 
 cudaError_t launch_kv_write(const KvCopyArgs& a, bool bf16, cudaStream_t s);
