@@ -32,7 +32,9 @@ namespace {
 
 constexpr int kKeys = 128;  // keys per step
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemS = 0, kTmemO = 256;  // of tile t: + 128 t
+// Columns of tile t's scores and sums: + 128 t. Its numerators lie where the scores
+// were, which are in registers by then.
+constexpr uint32_t kTmemS = 0, kTmemO = 256;
 constexpr int kMinSteps = 4;                   // of a piece
 
 template <int kDim, bool kCached>
@@ -48,8 +50,6 @@ struct Layout {
   // Cache: numerators are 2^(c S - m + 11), m up to 2^4 behind: at most 2^15, and what
   // fp16 rounds by more than half a step, or to 0, is 2^-36 of the largest.
   static constexpr float kGrowth = kCached ? 4.f : 8.f, kLift = kCached ? 11.f : 0.f;
-  // the numerators lie where scores were that are in registers by then
-  static constexpr uint32_t kP = kCached ? 64 : 0;
 };
 
 constexpr int kItems = 16;  // of a CTA that are worked out at its beginning
@@ -393,7 +393,7 @@ __device__ __forceinline__ bool issue_all(const AttendArgs& p, Shared* sh, const
   auto sums = [&](int t, int h, uint32_t v_at, bool first) {
 #pragma unroll
     for (int s = h * 4; s < h * 4 + 4; ++s)
-      umma_bf16_ta(tmem + kTmemO + t * 128, tmem + kTmemS + t * 128 + L::kP + s * 8, at(v_desc, v_at + s * 128), kIdO,
+      umma_bf16_ta(tmem + kTmemO + t * 128, tmem + kTmemS + t * 128 + s * 8, at(v_desc, v_at + s * 128), kIdO,
                    s != 4 ? 1u : !first);
   };
   auto stage = [](int st) { return static_cast<uint32_t>(warp_uniform(st * (L::kTileBytes >> 4))); };
@@ -792,17 +792,11 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
       uint32_t lo[2][32], hi[2][32];
       tmem_ld32_async(s_at, lo[0]);
       tmem_ld32_async(s_at + 32, lo[1]);
-      if (!kCached) {
-        tmem_ld32_async(s_at + 64, hi[0]);
-        tmem_ld32_async(s_at + 96, hi[1]);
-      }
+      tmem_ld32_async(s_at + 64, hi[0]);
+      tmem_ld32_async(s_at + 96, hi[1]);
       tmem_wait_ld(lo);
       if (masked) mask(lo, 0, left, there);
       float top = largest(lo);
-      if (kCached) {
-        tmem_ld32_async(s_at + 64, hi[0]);
-        tmem_ld32_async(s_at + 96, hi[1]);
-      }
       tmem_wait_ld(hi);
       if (masked) mask(hi, 64, left, there);
       top = fmaxf(top, largest(hi)) * c;
@@ -824,18 +818,12 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
         }
       }
       const float lift = L::kLift - (m == -INFINITY ? 0.f : m);
-      l += numerators<kCached>(hi, c, lift, s_at + L::kP + 32);
+      l += numerators<kCached>(hi, c, lift, s_at + 32);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->p_half[t]);
-      if (kCached) {  // (registers do not hold all scores beside the roles that share them: half are read again)
-        tmem_ld32_async(s_at, lo[0]);
-        tmem_ld32_async(s_at + 32, lo[1]);
-        tmem_wait_ld(lo);
-        if (masked) mask(lo, 0, left, there);
-      }
-      l += numerators<kCached>(lo, c, lift, s_at + L::kP);
+      l += numerators<kCached>(lo, c, lift, s_at);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -964,10 +952,10 @@ __global__ void __launch_bounds__(Layout<kDim, kCached>::kThreads, 1) k_attend(c
   __syncthreads();
   tc_fence_after();
   if (warp < 8) {
-    regs_inc<kCached ? 168 : 216>();
+    regs_inc<kCached ? 184 : 216>();  // (a warpgroup's share; 8 x 184 + 8 x 72 and 8 x 216 + 4 x 72 are what a CTA has)
     softmax_role<kDim, kCached>(p, sh, cut, warp >> 2, q);
   } else {
-    regs_dec<kCached ? 80 : 72>();
+    regs_dec<kCached ? 72 : 72>();
     if (warp == 8)
       load_role<kDim, kCached>(p, sh, cut, smem_u32(q), smem_u32(ring), smem_u32(raw));
     else if (warp == 9)
@@ -987,26 +975,29 @@ __global__ void __launch_bounds__(Layout<kDim, kCached>::kThreads, 1) k_attend(c
 }
 
 // The pieces' sums of cut items, joined. Each piece has kJoinCtas CTAs, which with
-// those of the item's other pieces share its outputs: a warp takes four columns of 32
-// rows, a row to a lane, and has the loads of 16 pieces in flight.
+// those of the item's other pieces share its outputs: four columns of 32 rows to two
+// warps, a row to a lane; the warps take 16 pieces each in turn, whose loads are in
+// flight together.
 constexpr int kJoinCtas = 4;
 
 template <int kDim>
 __global__ void __launch_bounds__(256) k_attend_join(const __grid_constant__ AttendArgs p) {
+  __shared__ float4 s_o[4][32];
+  __shared__ float2 s_ml[4][32];
   pdl_wait();
   pdl_trigger();
   const int k = blockIdx.x / kJoinCtas;
   const AttendJoin it = p.joins[k];
   if (it.parts <= 1) return;
-  const int lane = threadIdx.x & 31, k0 = k - it.part;
-  const int first = (it.part * kJoinCtas + blockIdx.x % kJoinCtas) * 8 + (threadIdx.x >> 5);
-  for (int u = first; u < 8 * (kDim / 4); u += it.parts * kJoinCtas * 8) {
+  const int lane = threadIdx.x & 31, k0 = k - it.part, pair = threadIdx.x >> 6, second = threadIdx.x >> 5 & 1;
+  const int first = (it.part * kJoinCtas + blockIdx.x % kJoinCtas) * 4 + pair;
+  for (int u = first; u < 8 * (kDim / 4); u += it.parts * kJoinCtas * 4) {
     const int r = (u & 7) * 32 + lane, t = r >> 7, tok_in = (r & 127) / p.a.group, tok = t * p.tokens + tok_in, d4 = u >> 3;
-    if (tok_in >= p.tokens || tok >= it.tokens) continue;
+    const bool mine = tok_in < p.tokens && tok < it.tokens;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int kBatch = 16;
-    for (int b = 0; b < it.parts; b += kBatch) {
+    for (int b = second * kBatch; b < it.parts && mine; b += 2 * kBatch) {
       float2 ml[kBatch];
       float4 v[kBatch];
       float top = m;
@@ -1030,12 +1021,26 @@ __global__ void __launch_bounds__(256) k_attend_join(const __grid_constant__ Att
         o.x += w * v[x].x, o.y += w * v[x].y, o.z += w * v[x].z, o.w += w * v[x].w;
       }
     }
-    const int64_t at = static_cast<int64_t>(it.row0 + tok) * p.a.q_heads + it.head * p.a.group + (r & 127) - tok_in * p.a.group;
-    const float inv = l == 0.f ? 0.f : p.a.c.v_mul / l;
-    const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), c = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-    *reinterpret_cast<uint2*>(p.a.out + at * kDim + d4 * 4) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
-    if (d4 == 0 && p.a.lse != nullptr) p.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    __syncwarp();
+    if (second) {
+      s_o[pair][lane] = o;
+      s_ml[pair][lane] = make_float2(m, l);
+    }
+    named_bar_sync(1 + pair, 64);
+    if (!second && mine) {
+      const float2 other = s_ml[pair][lane];
+      const float4 v = s_o[pair][lane];
+      const float top = fmaxf(m, other.x), f = m == top ? 1.f : exp2_fast(m - top), w = other.x == top ? 1.f : exp2_fast(other.x - top);
+      l = l * f + other.y * w;
+      o = make_float4(o.x * f + v.x * w, o.y * f + v.y * w, o.z * f + v.z * w, o.w * f + v.w * w);
+      const int64_t at = static_cast<int64_t>(it.row0 + tok) * p.a.q_heads + it.head * p.a.group + (r & 127) - tok_in * p.a.group;
+      const float inv = l == 0.f ? 0.f : p.a.c.v_mul / l;
+      const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), c = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+      *reinterpret_cast<uint2*>(p.a.out + at * kDim + d4 * 4) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
+      if (d4 == 0 && p.a.lse != nullptr) p.a.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+    }
+    named_bar_sync(1 + pair, 64);
   }
 }
 
