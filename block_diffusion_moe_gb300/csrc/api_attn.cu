@@ -152,27 +152,32 @@ float exponent_scale(float scale, float k_mul) {
   return c > FLT_MAX ? FLT_MAX : (c < FLT_TRUE_MIN ? FLT_TRUE_MIN : static_cast<float>(c));
 }
 
-// Workspace of the kernel for few rows, behind the control block.
+// A workspace: the control block, arrival counters that are zero between calls, and
+// behind them what needs no value before a call. The counters have this place in a
+// workspace of either kernel, whichever was the last to use it.
+constexpr size_t kArrived = kCtrlBytes;
+constexpr size_t kFreeBytes = kArrived + (plan::attend_few_pieces(8, true) * 4 + 255) / 256 * 256;
+
+// The kernel for few rows.
 struct FewLayout {
-  size_t arrived, ml, part, bytes;
+  size_t ml, part, bytes;
 };
 
 FewLayout few_layout(int32_t rows, bool alone, int32_t head_dim) {
   const size_t pieces = plan::attend_few_pieces(rows, alone);
   FewLayout l;
-  l.arrived = kCtrlBytes;
-  l.ml = l.arrived + (pieces * 4 + 255) / 256 * 256;
+  l.ml = kFreeBytes;
   l.part = l.ml + 2 * pieces * kFewRows * 8;
   l.bytes = l.part + 2 * pieces * (alone ? rows : kFewRows) * head_dim * 4;
   return l;
 }
 
-// Workspace of the kernel on tiles, where a call may be cut: what the pieces are, their
-// maxima and sums of weights, their sums.
+// The kernel on tiles, where a call may be cut: what the pieces are, their maxima and
+// sums of weights, their sums.
 constexpr size_t kJoinBytes = (plan::kAttendMaxPieces * sizeof(AttendJoin) + 255) / 256 * 256;
 
 size_t tile_bytes(int32_t head_dim) {
-  return kCtrlBytes + kJoinBytes + static_cast<size_t>(plan::kAttendMaxPieces) * 256 * (8 + head_dim * 4);
+  return kFreeBytes + kJoinBytes + static_cast<size_t>(plan::kAttendMaxPieces) * 256 * (8 + head_dim * 4);
 }
 
 // Fills in what the kernel on tiles needs besides a.
@@ -181,8 +186,8 @@ int fill_tiles(AttendArgs* t, int32_t n_rows, int32_t n_seqs, int32_t head_dim, 
   t->tokens = 128 / a.group;
   t->n_slots = n_rows / (2 * t->tokens) + n_seqs;
   t->may_cut = plan::attend_may_cut(n_rows, a.group, a.c.heads);
-  t->joins = reinterpret_cast<AttendJoin*>(static_cast<uint8_t*>(workspace) + kCtrlBytes);
-  t->part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + kCtrlBytes + kJoinBytes);
+  t->joins = reinterpret_cast<AttendJoin*>(static_cast<uint8_t*>(workspace) + kFreeBytes);
+  t->part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + kFreeBytes + kJoinBytes);
   t->part = reinterpret_cast<float*>(t->part_ml + plan::kAttendMaxPieces * 256);
   return encode_head_boxes(&t->tm_q, a.q.data, n_rows, a.q_heads, head_dim, a.q.row, a.q.head, a.group, t->tokens, "q");
 }
@@ -191,7 +196,7 @@ int fill_tiles(AttendArgs* t, int32_t n_rows, int32_t n_seqs, int32_t head_dim, 
 size_t cached_bytes(const clover_kv_cache& c, int32_t n_rows, int32_t q_heads, int32_t n_seqs, int32_t max_pages) {
   const int group = q_heads / c.kv_heads;
   const bool alone = plan::attend_few_alone(n_seqs, c.kv_heads);
-  size_t most = kCtrlBytes;
+  size_t most = kFreeBytes;
   if (group <= 8) most = std::max(most, few_layout(8, alone, c.head_dim).bytes);
   if (group <= 16 && plan::attend_few_rows(n_rows, group, n_seqs) == 16)
     most = std::max(most, few_layout(16, alone, c.head_dim).bytes);
@@ -287,7 +292,7 @@ int clover_kv_attention(const clover_kv_cache* cache, const clover_kv_seqs* seqs
     const FewLayout l = few_layout(rows, alone, cache->head_dim);
     uint8_t* at = static_cast<uint8_t*>(workspace);
     f.tokens = rows / a.group;
-    f.arrived = reinterpret_cast<uint32_t*>(at + l.arrived);
+    f.arrived = reinterpret_cast<uint32_t*>(at + kArrived);
     f.part_ml = reinterpret_cast<float2*>(at + l.ml);
     f.part = reinterpret_cast<float*>(at + l.part);
     return launched(launch_attend_few(f, sms < plan::kAttendSms ? sms : plan::kAttendSms, alone,

@@ -97,7 +97,7 @@ inline int attend_few_rows(long long rows, int group, int seqs) { return group <
 // Whether each warp takes a piece of the work for itself (16, or with tiles of 16
 // rows 12, on an SM), or each SM: with many tiles.
 inline bool attend_few_alone(int seqs, int heads) { return static_cast<long long>(seqs) * heads >= 2 * kAttendSms; }
-inline int attend_few_pieces(int rows, bool alone) { return kAttendSms * (alone ? (rows == 8 ? 16 : 12) : 1); }
+constexpr int attend_few_pieces(int rows, bool alone) { return kAttendSms * (alone ? (rows == 8 ? 16 : 12) : 1); }
 
 // The kernel on tensor-core tiles: items (pairs of tiles of 128 rows) that are at most
 // half as many as the SMs are cut into pieces, no more than SMs.

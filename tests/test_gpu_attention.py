@@ -484,6 +484,54 @@ def test_captured_and_replayed():
             C.workspace_status(r[4])
 
 
+def test_one_workspace_for_calls_of_all_sizes():
+    """Single tokens, blocks and prompts in turn through the same workspace."""
+    cases = [Case([1], [5000], 32, 2, 128, seed=40), Case([32], [3000], 32, 2, 128, seed=41),
+             Case([1] * 200, list(range(1, 201)), 16, 2, 128, seed=42), Case([2] * 90, list(range(2, 182, 2)), 16, 2, 128, seed=43)]
+    calls = [(c.q(16).to(DEV), c.cache(), *c.args()) for c in cases]
+    nbytes = max(C.kv_attention_workspace_bytes(a[1], a[0].shape[0], 16, *a[4].shape) for a in calls)
+    k = torch.randn(32, 2, 128, device=DEV).bfloat16()
+    nbytes = max(nbytes, C.prompt_attention_workspace_bytes(32, 32, 1, 16, 2, 128))
+    ws = C.workspace(nbytes)
+    want = [C.kv_attention(*a) for a in calls] + [C.prompt_attention(calls[1][0], k, k, calls[1][2])]
+    for _ in range(3):
+        for i in (0, 1, 2, 4, 0, 3, 1, 1, 0, 2):
+            if i < 4:
+                got = C.kv_attention(*calls[i], ws=ws)
+            else:
+                got = C.prompt_attention(calls[1][0], k, k, calls[1][2], ws=ws)
+            assert torch.equal(got, want[i]), i
+    C.workspace_status(ws)
+
+
+@pytest.mark.parametrize("new,group", [(1, 8), (40, 8)])
+def test_cached_queries_that_are_not_numbers(new, group):
+    """A NaN or an infinity in a query stays in its row."""
+    c = Case([new, 1], [200, 60], 16, 1, 64, seed=44)
+    q = c.q(group)
+    q[0, 1, 3], q[-1, 0, 5] = float("nan"), float("nan")
+    want = R.kv_attention(q.double().numpy(), c.pages, c.off, c.lens, c.table, 1, 0.125)
+    out, lse = C.kv_attention(q.to(DEV), c.cache(), *c.args(), lse=True)
+    _close(out, want, c.rows, lse, cached=True)
+    assert torch.isnan(out[0, 1]).all() and torch.isfinite(out[0, 0]).all()
+
+
+def test_no_pages_and_no_keys():
+    """A table of no pages, keys and values without rows: every query sees nothing."""
+    c = Case([3, 1], [3, 1], 16, 2, 64, seed=45)
+    q = c.q(8).to(DEV)
+    table = torch.zeros((2, 0), dtype=torch.int32, device=DEV)
+    off, lens, _ = c.args()
+    for rows in (4, 1):
+        out, lse = C.kv_attention(q[:rows], c.cache(), off, lens, table, lse=True)
+        assert not out.any() and (lse == -torch.inf).all()
+    k, v = C.kv_read(c.cache(), off, lens, table, 4)
+    assert not k.any() and not v.any()
+    none = torch.zeros((0, 2, 64), dtype=torch.bfloat16, device=DEV)
+    out, lse = C.prompt_attention(q, none, none, off, torch.zeros(3, dtype=torch.int32, device=DEV), lse=True)
+    assert not out.any() and (lse == -torch.inf).all()
+
+
 def test_streams_at_once():
     """Calls on three streams, each with its own workspace, give what they give alone."""
     cases = [Case([1, 32], [700, 300], 32, 2, 128, seed=20 + i) for i in range(3)]
