@@ -76,7 +76,7 @@ struct Shared {
   uint32_t tmem, abort;
   int poison[16];  // of item k: [k % 16]
   uint32_t there[16];  // of step k: sixteens that have a page (cache)
-  int sums[2][16];
+  int sums[3][16];
   Item items[kItems];  // this CTA's first
 };
 
@@ -173,24 +173,15 @@ __device__ __forceinline__ bool locate(const AttendArgs& p, const Cut& cut, int 
   return false;
 }
 
-// Sum over the CTA's threads.
-__device__ __forceinline__ int cta_sum(int v, int* scratch) {
-  v = warp_sum_i(v);
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int all = 0;
-  for (int w = 0; w < blockDim.x / 32; ++w) all += scratch[w];
-  return all;
-}
-
-// How the call is cut, by all threads of a CTA; the same in every CTA. Pieces of
-// steps / (SMs - items) steps are at most as many as SMs. (Of more items than half
-// the SMs, none is cut: 126 items of 98 steps in two rounds of pieces took 324 us,
-// whole 165.)
-__device__ Cut cut_call(const AttendArgs& p, int (&sums)[2][16]) {
+// How the call is cut, by all threads of a CTA; the same in every CTA. The pieces are
+// at most as many as SMs, and as short as that allows: of a chunk between steps / SMs
+// and steps / (SMs - items), where it is certain, each warp tries one length. (Of
+// more items than half the SMs, none is cut: 126 items of 98 steps in two rounds of
+// pieces took 324 us, whole 165.)
+__device__ Cut cut_call(const AttendArgs& p, int (&sums)[3][16]) {
   const Cut whole = {0, p.n_slots * p.a.c.heads};
   if (!p.may_cut) return whole;
-  const int pair = 2 * p.tokens, ctas = gridDim.x;
+  const int pair = 2 * p.tokens, ctas = gridDim.x, warps = blockDim.x / 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int items = 0;
   uint32_t own = 0;  // steps (what overflows belongs to too many items)
   for (int i = threadIdx.x; i < p.a.s.n; i += blockDim.x) {
@@ -200,18 +191,26 @@ __device__ Cut cut_call(const AttendArgs& p, int (&sums)[2][16]) {
     if (tiles < ctas)
       for (int t = 0; t < tiles; ++t) own += steps_of_tile(p, sp, t) * p.a.c.heads;
   }
-  items = cta_sum(items, sums[0]);
+  items = warp_sum_i(items);
+  int steps = warp_sum_i(static_cast<int>(own));
+  if (lane == 0) sums[0][warp] = items, sums[1][warp] = steps;
+  __syncthreads();
+  items = steps = 0;
+  for (int w = 0; w < warps; ++w) items += sums[0][w], steps += sums[1][w];
   if (2 * items > ctas) return whole;
-  const int steps = cta_sum(static_cast<int>(own), sums[1]);
-  Cut cut;
-  cut.chunk = max(kMinSteps, (steps + ctas - items - 1) / (ctas - items));
+  const int lo = max(kMinSteps, (steps + ctas - 1) / ctas), hi = max(kMinSteps, (steps + ctas - items - 1) / (ctas - items));
+  auto chunk = [&](int w) { return lo + (hi - lo) * w / (warps - 1); };
   int pieces = 0;
-  for (int i = threadIdx.x; i < p.a.s.n; i += blockDim.x) {
+  for (int i = lane; i < p.a.s.n; i += 32) {
     const SeqSpan sp = seq_span(p.a.s, i);
-    for (int t = 0; t * pair < sp.rows; ++t) pieces += pieces_of(steps_of_tile(p, sp, t), cut.chunk) * p.a.c.heads;
+    for (int t = 0; t * pair < sp.rows; ++t) pieces += pieces_of(steps_of_tile(p, sp, t), chunk(warp)) * p.a.c.heads;
   }
-  cut.pieces = cta_sum(pieces, sums[0]);  // (all have read it: there was a barrier between)
-  return cut;
+  pieces = warp_sum_i(pieces);
+  if (lane == 0) sums[2][warp] = pieces;
+  __syncthreads();
+  int w = 0;
+  while (w < warps - 1 && sums[2][w] > ctas) ++w;
+  return {chunk(w), sums[2][w]};
 }
 
 // This CTA's i-th piece: forth and back over the CTAs, so that no CTA always has the
@@ -643,14 +642,18 @@ __device__ void expand_role(const AttendArgs& p, Shared* sh, const Cut& cut, uin
 }
 
 // The row of Q that a thread of the softmax owns to fp16, scaled by a power of two;
-// returns the factor's inverse exponent.
+// returns the factor's inverse exponent. Neighbouring threads begin at different
+// pieces of 16 bytes: rows are 128 bytes apart, where the same piece of eight rows lies
+// in the same banks (6.5 us a tile of 128 elements, of which 32 rows over 131,072
+// cached then took 55).
 template <int kDim>
 __device__ __forceinline__ int convert_row(uint8_t* q, int r) {
   using L = Layout<kDim, true>;
+  uint8_t* row = q + r * 128;
   uint32_t top = 0;  // the largest finite magnitude, as bits
 #pragma unroll 4
   for (int c = 0; c < kDim / 8; ++c) {
-    const uint4 x = *reinterpret_cast<const uint4*>(q + (c / 8) * L::kSlab + r * 128 + (c % 8) * 16);
+    const uint4 x = *reinterpret_cast<const uint4*>(row + (c / 8) * L::kSlab + ((c ^ r) % 8) * 16);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -662,7 +665,7 @@ __device__ __forceinline__ int convert_row(uint8_t* q, int r) {
   const float f0 = scalbnf(1.f, -e / 2), f1 = scalbnf(1.f, -e - -e / 2);  // (2^-e itself may leave fp32's range)
 #pragma unroll 4
   for (int c = 0; c < kDim / 8; ++c) {
-    uint4* at = reinterpret_cast<uint4*>(q + (c / 8) * L::kSlab + r * 128 + (c % 8) * 16);
+    uint4* at = reinterpret_cast<uint4*>(row + (c / 8) * L::kSlab + ((c ^ r) % 8) * 16);
     const uint4 x = *at;
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t o[4];
@@ -718,27 +721,38 @@ __device__ __forceinline__ float largest(const uint32_t (&s)[2][32]) {
   return fmaxf(max3(top[0], top[1], top[2]), top[3]);
 }
 
-// What look_after (expand_tile) has taken out of V, added to elements 32 i .. of the
-// rows that see it: infinities and NaN. By a whole warp.
+// What look_after (expand_tile) has taken out of V, added to the sums of the rows that
+// see it: infinities and NaN. By a whole warp, each lane for its row, whose sums
+// begin at o_at. (They stay in tensor memory: an array that a call changes would lie
+// in memory for every item, which took 3 us of each.)
 template <int kDim, bool kCached>
-__device__ __noinline__ void add_odd_values(const AttendArgs& p, const Cut& cut, int k, int lim, int i, uint32_t (&o)[32]) {
-  using L = Layout<kDim, kCached>;
+__device__ __noinline__ void add_odd_values(const AttendArgs& p, const Cut& cut, int k, int lim, uint32_t o_at) {
   Item it;
   locate(p, cut, k, &it);
-  for (int j = max(it.all, it.j0 * kKeys); j < min(lim, it.j1 * kKeys); ++j) {
-    if (kCached) {
-      const uint8_t* six = kv_sixteen(p.a.c, p.a.s, it.seq, it.head, j);
-      for (int x = 0; x < 32; ++x)
-        if (six != nullptr && (six[17 * kDim + j % 16 * (kDim / 16) + (i * 32 + x) / 16] & 0x7F) == 0x7F) o[x] = 0x7FC00000u;
-    } else {
-      const uint16_t* v = reinterpret_cast<const uint16_t*>(p.a.v.data + (it.sp.key0 + j) * p.a.v.row + it.head * p.a.v.head);
-      for (int x = 0; x < 32; ++x) {
-        const uint32_t b = v[i * 32 + x];
-        if ((b & 0x7F80u) == 0x7F80u) o[x] = __float_as_uint(__uint_as_float(o[x]) + __uint_as_float(b << 16));
+#pragma unroll 1
+  for (int i = 0; i < kDim / 32; ++i) {
+    uint32_t o[1][32];
+    tmem_ld32_async(o_at + i * 32, o[0]);
+    tmem_wait_ld(o);
+    for (int j = max(it.all, it.j0 * kKeys); j < min(lim, it.j1 * kKeys); ++j) {
+      if (kCached) {
+        const uint8_t* six = kv_sixteen(p.a.c, p.a.s, it.seq, it.head, j);
+#pragma unroll
+        for (int x = 0; x < 32; ++x)
+          if (six != nullptr && (six[17 * kDim + j % 16 * (kDim / 16) + (i * 32 + x) / 16] & 0x7F) == 0x7F) o[0][x] = 0x7FC00000u;
+      } else {
+        const uint16_t* v = reinterpret_cast<const uint16_t*>(p.a.v.data + (it.sp.key0 + j) * p.a.v.row + it.head * p.a.v.head);
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+          const uint32_t b = v[i * 32 + x];
+          if ((b & 0x7F80u) == 0x7F80u) o[0][x] = __float_as_uint(__uint_as_float(o[0][x]) + __uint_as_float(b << 16));
+        }
       }
     }
+    __syncwarp();
+    tmem_st32(o_at + i * 32, o[0]);
   }
-  __syncwarp();
+  tmem_wait_st();
 }
 
 template <int kDim, bool kCached>
@@ -806,14 +820,16 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
         m = up;
         l *= f;
         if (i > 0) {
+          // (16 columns at a time: 32 beside all the scores leave the registers, cached
+          // steps took 3 us instead of 1.7)
 #pragma unroll 1
-          for (int d = 0; d < kDim / 32; ++d) {
-            uint32_t o[1][32];
-            tmem_ld32_async(o_at + d * 32, o[0]);
-            tmem_wait_ld(o);
+          for (int d = 0; d < kDim / 16; ++d) {
+            float o[16];
+            uint32_t w[16];
+            tmem_ld16(o_at + d * 16, o);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[0][x] = __float_as_uint(__uint_as_float(o[0][x]) * f);
-            tmem_st32(o_at + d * 32, o[0]);
+            for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(o[x] * f);
+            tmem_st16(o_at + d * 16, w);
           }
         }
       }
@@ -836,8 +852,11 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
     }
     tc_fence_after();
     const float f = part ? 1.f : (l == 0.f ? 0.f : p.a.c.v_mul / l);
-    const bool poison = steps > 0 && *reinterpret_cast<volatile int*>(&sh->poison[item & 15]) != 0;
     const int k = piece_at(work.i);
+    if (n > 0 && *reinterpret_cast<volatile int*>(&sh->poison[item & 15]) != 0) {
+      __syncwarp();
+      add_odd_values<kDim, kCached>(p, cut, k, lim, o_at);
+    }
     // (a piece's sums: four columns of all rows next to one another, as the lanes have them)
     float4* to_part = reinterpret_cast<float4*>(p.part + (static_cast<int64_t>(k) * 2 + t) * 128 * kDim) + r;
 #pragma unroll 1
@@ -849,8 +868,7 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
         tmem_wait_ld(o);
       }
 #pragma unroll
-      for (int x = 0; x < 32; ++x) o[0][x] = n > 0 ? __float_as_uint(__uint_as_float(o[0][x]) * f) : 0u;
-      if (poison) add_odd_values<kDim, kCached>(p, cut, k, lim, i, o[0]);
+      for (int x = 0; x < 32; ++x) o[0][x] = n > 0 && f != 0.f ? __float_as_uint(__uint_as_float(o[0][x]) * f) : 0u;
       if (!mine) continue;
       if (part) {
 #pragma unroll
@@ -952,10 +970,10 @@ __global__ void __launch_bounds__(Layout<kDim, kCached>::kThreads, 1) k_attend(c
   __syncthreads();
   tc_fence_after();
   if (warp < 8) {
-    regs_inc<kCached ? 184 : 216>();  // (a warpgroup's share; 8 x 184 + 8 x 72 and 8 x 216 + 4 x 72 are what a CTA has)
+    regs_inc<kCached ? 192 : 216>();  // (a warpgroup's share; 8 x 192 + 8 x 64 and 8 x 216 + 4 x 72 are what a CTA has)
     softmax_role<kDim, kCached>(p, sh, cut, warp >> 2, q);
   } else {
-    regs_dec<kCached ? 72 : 72>();
+    regs_dec<kCached ? 64 : 72>();
     if (warp == 8)
       load_role<kDim, kCached>(p, sh, cut, smem_u32(q), smem_u32(ring), smem_u32(raw));
     else if (warp == 9)
@@ -975,72 +993,86 @@ __global__ void __launch_bounds__(Layout<kDim, kCached>::kThreads, 1) k_attend(c
 }
 
 // The pieces' sums of cut items, joined. Each piece has kJoinCtas CTAs, which with
-// those of the item's other pieces share its outputs: four columns of 32 rows to two
-// warps, a row to a lane; the warps take 16 pieces each in turn, whose loads are in
-// flight together.
-constexpr int kJoinCtas = 4;
+// those of the item's other pieces share its outputs: four columns of 32 rows to a
+// unit of one to eight warps, a row to a lane. The more pieces, the more warps to a
+// unit: at most 16 pieces to a warp as a rule, eight of whose loads are in flight
+// together; then there are hardly more units than warps for them. (74 pieces of 256
+// rows of 128, two items: 20 MB in 5.5 us. Two warps for every unit, 16 loads at a
+// time, left most warps without one: 6.8 us.)
+constexpr int kJoinCtas = 4, kJoinBatch = 8;
 
 template <int kDim>
-__global__ void __launch_bounds__(256) k_attend_join(const __grid_constant__ AttendArgs p) {
-  __shared__ float4 s_o[4][32];
-  __shared__ float2 s_ml[4][32];
+__global__ void __launch_bounds__(256, 4) k_attend_join(const __grid_constant__ AttendArgs p) {
+  __shared__ float4 s_o[8][32];
+  __shared__ float2 s_ml[8][32];
   pdl_wait();
   pdl_trigger();
   const int k = blockIdx.x / kJoinCtas;
   const AttendJoin it = p.joins[k];
   if (it.parts <= 1) return;
-  const int lane = threadIdx.x & 31, k0 = k - it.part, pair = threadIdx.x >> 6, second = threadIdx.x >> 5 & 1;
-  const int first = (it.part * kJoinCtas + blockIdx.x % kJoinCtas) * 4 + pair;
-  for (int u = first; u < 8 * (kDim / 4); u += it.parts * kJoinCtas * 4) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k0 = k - it.part;
+  const int wide = it.parts <= 16 ? 1 : it.parts <= 32 ? 2 : it.parts <= 64 ? 4 : 8;
+  const int own = warp & (wide - 1), per = 8 / wide, b0 = it.parts * own / wide, b1 = it.parts * (own + 1) / wide;
+  constexpr int kUnits = 8 * (kDim / 4);
+  for (int u0 = (it.part * kJoinCtas + blockIdx.x % kJoinCtas) * per; u0 < kUnits; u0 += it.parts * kJoinCtas * per) {
+    const int u = u0 + warp / wide;  // (the same number of rounds for all warps of the CTA)
     const int r = (u & 7) * 32 + lane, t = r >> 7, tok_in = (r & 127) / p.a.group, tok = t * p.tokens + tok_in, d4 = u >> 3;
-    const bool mine = tok_in < p.tokens && tok < it.tokens;
+    const bool mine = u < kUnits && tok_in < p.tokens && tok < it.tokens;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kBatch = 16;
-    for (int b = second * kBatch; b < it.parts && mine; b += 2 * kBatch) {
-      float2 ml[kBatch];
-      float4 v[kBatch];
+    for (int b = b0; b < b1 && mine; b += kJoinBatch) {
+      float2 ml[kJoinBatch];
+      float4 v[kJoinBatch];
       float top = m;
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        const int64_t at = k0 + min(b + x, it.parts - 1);
+      for (int x = 0; x < kJoinBatch; ++x) {
+        if (b + x >= b1) {
+          ml[x] = make_float2(-INFINITY, 0.f);
+          v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+          continue;
+        }
+        const int64_t at = k0 + b + x;
         ml[x] = __ldcg(&p.part_ml[at * 256 + r]);
         v[x] = __ldcg(reinterpret_cast<const float4*>(p.part + (at * 2 + t) * 128 * kDim) + d4 * 128 + (r & 127));
       }
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) top = fmaxf(top, ml[x].x);
+      for (int x = 0; x < kJoinBatch; ++x) top = fmaxf(top, ml[x].x);
       const float f = m == top ? 1.f : exp2_fast(m - top);
       m = top;
       l *= f;
       o.x *= f, o.y *= f, o.z *= f, o.w *= f;
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        if (b + x >= it.parts) continue;
+      for (int x = 0; x < kJoinBatch; ++x) {
         const float w = ml[x].x == m ? 1.f : exp2_fast(ml[x].x - m);
         l += w * ml[x].y;
         o.x += w * v[x].x, o.y += w * v[x].y, o.z += w * v[x].z, o.w += w * v[x].w;
       }
     }
-    __syncwarp();
-    if (second) {
-      s_o[pair][lane] = o;
-      s_ml[pair][lane] = make_float2(m, l);
+    if (wide > 1) {
+      s_o[warp][lane] = o;
+      s_ml[warp][lane] = make_float2(m, l);
+      __syncthreads();
+      if (own == 0) {
+        for (int x = 1; x < wide; ++x) {
+          const float2 other = s_ml[warp + x][lane];
+          const float4 v = s_o[warp + x][lane];
+          const float top = fmaxf(m, other.x), f = m == top ? 1.f : exp2_fast(m - top), w = other.x == top ? 1.f : exp2_fast(other.x - top);
+          m = top;
+          l = l * f + other.y * w;
+          o = make_float4(o.x * f + v.x * w, o.y * f + v.y * w, o.z * f + v.z * w, o.w * f + v.w * w);
+        }
+      }
+      __syncthreads();
     }
-    named_bar_sync(1 + pair, 64);
-    if (!second && mine) {
-      const float2 other = s_ml[pair][lane];
-      const float4 v = s_o[pair][lane];
-      const float top = fmaxf(m, other.x), f = m == top ? 1.f : exp2_fast(m - top), w = other.x == top ? 1.f : exp2_fast(other.x - top);
-      l = l * f + other.y * w;
-      o = make_float4(o.x * f + v.x * w, o.y * f + v.y * w, o.z * f + v.z * w, o.w * f + v.w * w);
+    if (own == 0 && mine) {
       const int64_t at = static_cast<int64_t>(it.row0 + tok) * p.a.q_heads + it.head * p.a.group + (r & 127) - tok_in * p.a.group;
+      if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
       const float inv = l == 0.f ? 0.f : p.a.c.v_mul / l;
       const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), c = __floats2bfloat162_rn(o.z * inv, o.w * inv);
       *reinterpret_cast<uint2*>(p.a.out + at * kDim + d4 * 4) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
-      if (d4 == 0 && p.a.lse != nullptr) p.a.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+      if (d4 == 0 && p.a.lse != nullptr) p.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
-    named_bar_sync(1 + pair, 64);
   }
 }
 

@@ -395,6 +395,7 @@ __device__ __forceinline__ bool arrive_last(const AttendFewArgs& p, int c0, int 
 
 // A row's result from its sum, maximum and weight.
 __device__ __forceinline__ void write_row(const AttendFewArgs& p, int64_t at, int dim, int d, float4 o, float inv) {
+  if (inv == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);  // (nothing seen: not even 0 times a NaN)
   const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
   *reinterpret_cast<uint2*>(p.a.out + at * dim + d) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
@@ -646,7 +647,7 @@ __device__ void finish_warp(const AttendFewArgs& p, const Cursor& c, const Line&
 #pragma unroll
       for (int j = 0; j < kDim / 16; ++j) {
         const __nv_bfloat162 x = __floats2bfloat162_rn(st->o[h][j][i] * inv, st->o[h][j][i + 2] * inv);
-        w[j] = *reinterpret_cast<const uint32_t*>(&x);
+        w[j] = inv == 0.f ? 0u : *reinterpret_cast<const uint32_t*>(&x);
       }
       uint4* to = reinterpret_cast<uint4*>(p.a.out + at * kDim + g * (kDim / 8));
 #pragma unroll
