@@ -198,7 +198,7 @@ size_t cached_bytes(const clover_kv_cache& c, int32_t n_rows, int32_t q_heads, i
   const bool alone = plan::attend_few_alone(n_seqs, c.kv_heads);
   size_t most = kFreeBytes;
   if (group <= 8) most = std::max(most, few_layout(8, alone, c.head_dim).bytes);
-  if (group <= 16 && plan::attend_few_rows(n_rows, group, n_seqs) == 16)
+  if (group <= 16 && plan::attend_few_rows(n_rows, group, n_seqs, c.kv_heads) == 16)
     most = std::max(most, few_layout(16, alone, c.head_dim).bytes);
   if (!plan::attend_few(n_rows, group, n_seqs)) most = std::max(most, tile_bytes(c.head_dim));
   return most;
@@ -287,7 +287,7 @@ int clover_kv_attention(const clover_kv_cache* cache, const clover_kv_seqs* seqs
     if ((rc = device_sms(&sms))) return rc;
     AttendFewArgs f;
     f.a = a;
-    const int rows = plan::attend_few_rows(n_rows, a.group, seqs->n_seqs);
+    const int rows = plan::attend_few_rows(n_rows, a.group, seqs->n_seqs, cache->kv_heads);
     const bool alone = plan::attend_few_alone(seqs->n_seqs, cache->kv_heads);
     const FewLayout l = few_layout(rows, alone, cache->head_dim);
     uint8_t* at = static_cast<uint8_t*>(workspace);

@@ -88,15 +88,25 @@ inline RouteShape route_shape(int tokens) {
 }
 
 // Attention over a cache: CTAs of the kernel for few rows, and whether it takes a
-// call: sequences of at most 16 rows (tokens x heads of a group) on average.
+// call: sequences of at most 32 rows (tokens x heads of a group) on average. (Groups
+// of 8, 4 heads; this kernel or the one on tiles with 16, 32 and 64 rows. Heads of 128:
+// 64 sequences of 16,384 keys 195 or 428 us, 342 or 428, 645 or 610; 8 of them 51 or 72,
+// 75 or 73, 121 or 74; 8 of 1,024 keys 17 or 23, 32 or 24, 33 or 24. Heads of 64: 8 of
+// 16,384 keys 33 or 57, 46 or 57, 71 or 57.)
 constexpr int kAttendSms = 152;
-inline bool attend_few(long long rows, int group, int seqs) { return group <= 16 && rows * group <= 16LL * seqs; }
+inline bool attend_few(long long rows, int group, int seqs) { return group <= 16 && rows * group <= 32LL * seqs; }
 // Rows of its tiles, at most: 8 where the group has no more heads and the call
-// about one token for each sequence.
-inline int attend_few_rows(long long rows, int group, int seqs) { return group <= 8 && rows * group <= 8LL * seqs ? 8 : 16; }
+// about one token for each sequence, or as few as 8 tiles of 8. (Two tokens of groups
+// of 8, 4 heads of 128, tiles of 8 or 16: one sequence of 16,384 19 or 26 us, 8 of them
+// 56 or 51, 64 of them 224 or 195.)
+inline int attend_few_rows(long long rows, int group, int seqs, int heads) {
+  return group <= 8 && (rows * group <= 8LL * seqs || rows * group * heads <= 64) ? 8 : 16;
+}
 // Whether each warp takes a piece of the work for itself (16, or with tiles of 16
-// rows 12, on an SM), or each SM: with many tiles.
-inline bool attend_few_alone(int seqs, int heads) { return static_cast<long long>(seqs) * heads >= 2 * kAttendSms; }
+// rows 12, on an SM), or each SM: with many tiles. (8,191 keys of 128 elements, groups
+// of 4, warps or SMs: 256 tiles 77 or 96 us, 128 tiles 57 or 57, 64 tiles 66 or 41;
+// 1,023 keys: 32 or 39, 33 or 26, 38 or 14.)
+inline bool attend_few_alone(int seqs, int heads) { return 4LL * seqs * heads >= 5 * kAttendSms; }
 constexpr int attend_few_pieces(int rows, bool alone) { return kAttendSms * (alone ? (rows == 8 ? 16 : 12) : 1); }
 
 // The kernel on tensor-core tiles: items (pairs of tiles of 128 rows) that are at most

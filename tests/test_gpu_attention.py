@@ -516,6 +516,39 @@ def test_cached_queries_that_are_not_numbers(new, group):
     assert torch.isnan(out[0, 1]).all() and torch.isfinite(out[0, 0]).all()
 
 
+@pytest.mark.parametrize("new,length,group", [(1, 70, 8), (1, 900, 8), (40, 200, 8), (40, 1500, 8)])
+def test_cached_scores_of_minus_infinity(new, length, group):
+    """A row whose scores are all -inf is empty, even where a value that it sees is NaN."""
+    c = Case([new, 1], [length, 60], 16, 1, 64, seed=45)
+    c.pages[:, :, :, 0:512:32] = c.pages[:, :, :, 0:512:32] & 0xF0 | 2  # element 0 of every key: 1 times its scale
+    c.pages[c.table[0, 1], 0, 0, 17 * 64] = 0x7F
+    q = c.q(group)
+    q[0, 1] = 0.0
+    q[0, 1, 0] = float("-inf")
+    want = R.kv_attention(q.double().numpy(), c.pages, c.off, c.lens, c.table, 1, 0.125)
+    assert not want[0][0, 1].any() and np.isnan(want[0][0, 0]).any()
+    out, lse = C.kv_attention(q.to(DEV), c.cache(), *c.args(), lse=True)
+    _close(out, want, c.rows, lse, cached=True)
+
+
+def test_prompt_scores_of_minus_infinity_and_values_of_infinity():
+    def poke(q, k, v):
+        q[:, :, 0] = 1.0
+        k[:150, 0, 0] = float("-inf")
+        v[3, 0, 5], v[140, 0, 9] = float("inf"), float("nan")
+    assert not _prompt([200], [200], 1, 4, 64, 1, seed=2, poke=poke)[:150].any()
+
+
+@pytest.mark.parametrize("new,lens,heads,group,dim", [
+    ([2], [500], 2, 8, 128), ([2], [70], 4, 8, 64), ([3], [300], 1, 5, 128),                   # tiles of 8 rows, few of them
+    ([4, 4], [100, 333], 4, 8, 128), ([2, 2], [90, 40], 1, 16, 64), ([31, 1], [31, 64], 1, 2, 128),  # 32 rows each on average
+    ([1] * 95, [40] * 95, 2, 4, 64), ([1] * 64, [33] * 64, 3, 16, 128), ([2] * 48, [60] * 48, 4, 8, 64),  # a piece for each warp
+    ([1] * 94, [50] * 94, 2, 1, 128),
+])
+def test_cached_attention_where_kernels_meet(new, lens, heads, group, dim):
+    Case(new, lens, 16, heads, dim, seed=len(new)).check(heads * group, 1)
+
+
 def test_no_pages_and_no_keys():
     """A table of no pages, keys and values without rows: every query sees nothing."""
     c = Case([3, 1], [3, 1], 16, 2, 64, seed=45)
