@@ -7,8 +7,9 @@
 // keys and values on its side of 16 and queries on that of 8: the tensor core is
 // not what bounds this, and no operand passes through shared memory a second time.
 // Scores come out transposed (a lane holds keys g and g + 8 of rows 2t and 2t + 1),
-// and so do the sums; movmatrix turns the numerators between. Queries are scaled to fp16 by a power of two per row (the largest element to 2^14, so that
-// what falls below fp16's range is 2^-38 of it).
+// and so do the sums; movmatrix turns the numerators between. Queries are scaled to
+// fp16 by a power of two per row (the largest element to 2^14, so that what falls
+// below fp16's range is 2^-38 of it).
 //
 // The call's work is one line of units of keys of one tile; every team of warps
 // takes an equal piece of it, whatever the lengths are. A team is one warp (units of
@@ -19,6 +20,13 @@
 // them up, in the order of the keys. Each warp streams its own keys through its own
 // ring (one copy per 16 tokens, of codes and scales together), on past the ends of
 // tiles.
+//
+// Measured on a GB300 (the kernel alone, in a graph): 64 sequences of 8,192 keys, 32
+// heads over 8 of 128: 123 us, 4.9 TB/s of 6.7; of up to 16,384: 125 us. What bounds it
+// is the issue of instructions, 324 to a warp for 16 tokens, of which expansion takes
+// about half (issue slots 60% busy, ALU 51%, tensor pipe 23%). One token over 1,021 keys
+// of 2 heads: 13 us: 2 to place the work, 2 for the queries and the first keys, 1.5 for
+// the step, 6 for the sums of 16 warps and 4 pieces, most of it code that runs once.
 #include <math.h>
 
 #include "attn_ops.cuh"

@@ -483,7 +483,11 @@ int clover_moe_combine(const uint16_t* y, int32_t n_rows, const int32_t* pos, co
  * A query that sees nothing, or whose z are all -inf, gets out 0 and lse -inf.
  * Scores, softmax statistics and sums are fp32; the softmax's numerators are
  * rounded to the products' 16-bit type. What a query does not see does not
- * change its results, whatever it holds. */
+ * change its results, whatever it holds. Outputs must not overlap inputs, nor
+ * each other. The results of a call do not change from run to run.
+ *
+ * One workspace may serve calls of both attention operations, of different
+ * shapes, one after the other, if it is large enough for each. */
 
 /* Strided rows of heads (bf16 unless a call says otherwise): row i, head h at
  * element i * row_stride + h * head_stride, head_dim contiguous elements. data
