@@ -544,6 +544,7 @@ def test_prompt_scores_of_minus_infinity_and_values_of_infinity():
     ([4, 4], [100, 333], 4, 8, 128), ([2, 2], [90, 40], 1, 16, 64), ([31, 1], [31, 64], 1, 2, 128),  # 32 rows each on average
     ([1] * 95, [40] * 95, 2, 4, 64), ([1] * 64, [33] * 64, 3, 16, 128), ([2] * 48, [60] * 48, 4, 8, 64),  # a piece for each warp
     ([1] * 94, [50] * 94, 2, 1, 128),
+    ([0] * 90 + [250], [0] * 90 + [260], 1, 8, 64), ([1] * 60 + [130, 1], [20] * 60 + [400, 7], 2, 16, 64),  # one has most rows
 ])
 def test_cached_attention_where_kernels_meet(new, lens, heads, group, dim):
     Case(new, lens, 16, heads, dim, seed=len(new)).check(heads * group, 1)
