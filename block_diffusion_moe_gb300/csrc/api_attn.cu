@@ -172,12 +172,12 @@ FewLayout few_layout(int32_t rows, bool alone, int32_t head_dim) {
   return l;
 }
 
-// The kernel on tiles, where a call may be cut: what the pieces are, their maxima and
-// sums of weights, their sums.
+// The kernel on tiles, where a call may be cut: what the pieces are, their maxima,
+// sums of weights and exponents, their sums.
 constexpr size_t kJoinBytes = (plan::kAttendMaxPieces * sizeof(AttendJoin) + 255) / 256 * 256;
 
 size_t tile_bytes(int32_t head_dim) {
-  return kFreeBytes + kJoinBytes + static_cast<size_t>(plan::kAttendMaxPieces) * 256 * (8 + head_dim * 4);
+  return kFreeBytes + kJoinBytes + static_cast<size_t>(plan::kAttendMaxPieces) * 256 * (12 + head_dim * 4);
 }
 
 // Fills in what the kernel on tiles needs besides a.
@@ -188,7 +188,8 @@ int fill_tiles(AttendArgs* t, int32_t n_rows, int32_t n_seqs, int32_t head_dim, 
   t->may_cut = plan::attend_may_cut(n_rows, a.group, a.c.heads);
   t->joins = reinterpret_cast<AttendJoin*>(static_cast<uint8_t*>(workspace) + kFreeBytes);
   t->part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + kFreeBytes + kJoinBytes);
-  t->part = reinterpret_cast<float*>(t->part_ml + plan::kAttendMaxPieces * 256);
+  t->part_c = reinterpret_cast<float*>(t->part_ml + plan::kAttendMaxPieces * 256);
+  t->part = t->part_c + plan::kAttendMaxPieces * 256;
   return encode_head_boxes(&t->tm_q, a.q.data, n_rows, a.q_heads, head_dim, a.q.row, a.q.head, a.group, t->tokens, "q");
 }
 

@@ -4,7 +4,7 @@
 // An item is two tiles of 128 query rows (the group's heads of consecutive tokens
 // of one sequence) over the keys they see, 128 at a time:
 //   S = Q K^T          tcgen05.mma, both operands from shared memory
-//   P = 2^(c S - m)    one thread per row: m a running maximum, l the sum of P
+//   P = 2^(c (S - m))  one thread per row: m a running maximum, l the sum of P
 //   O = O + P V        tcgen05.mma, P (16 bits) from tensor memory
 // and in the end O / l. m moves only where the row's maximum has grown by more
 // than a limit (O and l are scaled then): numerators and sums are floating point,
@@ -61,10 +61,19 @@ struct Layout {
   static constexpr int kHalf = 9 * kDim;      // of their keys, or of their values: codes, then scales
   static constexpr int kRawBytes = 8 * kHalf;  // a tile's
   static constexpr int kRaw = kCached ? 3 * (128 / kDim) : 0;
-  // Cache: numerators are 2^(c S - m + 11), m up to 2^4 behind: at most 2^15, and what
-  // fp16 rounds by more than half a step, or to 0, is 2^-36 of the largest.
+  // Numerators are about 2^(c (S - m) + kLift), m up to 2^kGrowth behind. Cache: at most
+  // 2^15, and what fp16 rounds by more than half a step, or to 0, is 2^-36 of the largest.
   static constexpr float kGrowth = kCached ? 4.f : 8.f, kLift = kCached ? 11.f : 0.f;
 };
+
+// A row's numerators are 2^(c (S - base) + lift): base 0 and lift kLift - c m, rounded once,
+// which all of them share, where c m is at most this. Where it is larger that rounding
+// would be as large as the room above the lift in fp16 (from scores of 9e7 on; in fp32
+// from 2e9 on): then base is m, and the difference, exact near the maximum, comes before
+// the factor. (4 prompts in blocks of 32, heads of 64: 148 us without, 150 so, 153 to 162 with
+// the difference for every row.)
+constexpr float kFar = 1048576.f;
+__device__ __forceinline__ float base_of(float m, float c) { return m == -INFINITY || fabsf(m * c) <= kFar ? 0.f : m; }
 
 constexpr int kItems = 16;  // of a CTA that are worked out at its beginning
 
@@ -728,6 +737,13 @@ __device__ __forceinline__ void mask(uint32_t (&s)[2][32], int at, int left, uin
     if (at + i >= left || !(there >> ((at + i) / 16) & 1u)) s[i / 32][i % 32] = 0xFF800000u;
 }
 
+// The same less the row's base.
+__device__ __forceinline__ void rebase(uint32_t (&s)[2][32], float base) {
+  asm volatile("");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) s[i / 32][i % 32] = __float_as_uint(__uint_as_float(s[i / 32][i % 32]) - base);
+}
+
 __device__ __forceinline__ float largest(const uint32_t (&s)[2][32]) {
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -800,7 +816,8 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) whole = min(whole, __shfl_xor_sync(0xffffffffu, whole, o));
     float c = p.a.scale_log2;
-    float m = -INFINITY, l = 0.f;  // m: of c S
+    float m = -INFINITY, l = 0.f;  // m: of S
+    float lift = L::kLift, gate = L::kGrowth;  // (gate: rows with a base go through the branch in every step)
     item += steps > 0;
     if (kCached && n > 0) {
       if (!warp_wait(p, sh, &sh->q_full[t], q_count & 1)) return;
@@ -827,12 +844,19 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
       float top = largest(lo);
       tmem_wait_ld(hi);
       if (masked) mask(hi, 64, left, there);
-      top = fmaxf(top, largest(hi)) * c;
-      if (__any_sync(0xffffffffu, top - m > L::kGrowth)) {
+      top = fmaxf(top, largest(hi));
+      if (__any_sync(0xffffffffu, (top - m) * c > gate)) {
         const float up = fmaxf(m, top);
-        const float f = m == up ? 1.f : exp2_fast(m - up);
+        const float base = base_of(up, c), lift_to = base != 0.f || up == -INFINITY ? L::kLift : fmaf(-up, c, L::kLift);
+        const float f = m == up ? 1.f : m == -INFINITY ? 0.f : exp2_fast(fmaf(base_of(m, c) - base, c, lift_to - lift));
         m = up;
+        lift = lift_to;
+        gate = base != 0.f ? -INFINITY : L::kGrowth;
         l *= f;
+        if (__any_sync(0xffffffffu, base != 0.f)) {
+          rebase(lo, base);
+          rebase(hi, base);
+        }
         if (i > 0) {
           // (16 columns at a time: 32 beside all the scores leave the registers, cached
           // steps took 3 us instead of 1.7)
@@ -847,7 +871,6 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
           }
         }
       }
-      const float lift = L::kLift - (m == -INFINITY ? 0.f : m);
       l += numerators<kCached>(hi, c, lift, s_at + 32);
       tmem_wait_st();
       tc_fence_before();
@@ -865,7 +888,9 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
       ++q_count;
     }
     tc_fence_after();
-    const float f = part ? 1.f : (l == 0.f ? 0.f : p.a.c.v_mul / l);
+    const float base = base_of(m, c);
+    // (pieces are joined by their m: as if numerators were 2^(c (S - m)))
+    const float f = l == 0.f ? 0.f : part ? exp2_fast(fmaf(base - m, c, -lift)) : p.a.c.v_mul / l;
     const int k = piece_at(work.i);
     if (n > 0 && *reinterpret_cast<volatile int*>(&sh->poison[item & 15]) != 0) {
       __syncwarp();
@@ -906,11 +931,11 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->o_empty[t]);
     }
-    m -= L::kLift;
     if (part) {
-      __stcg(&p.part_ml[(static_cast<int64_t>(k) * 2 + t) * 128 + r], make_float2(m, l));
+      __stcg(&p.part_ml[(static_cast<int64_t>(k) * 2 + t) * 128 + r], make_float2(m, l * f));
+      __stcg(&p.part_c[(static_cast<int64_t>(k) * 2 + t) * 128 + r], c);
     } else if (mine && p.a.lse != nullptr) {
-      p.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      p.a.lse[at] = l == 0.f ? -INFINITY : fmaf(base, c, log2f(l) - lift) * 0.6931471805599453f;
     }
     __syncwarp();
   }
@@ -1033,6 +1058,7 @@ __global__ void __launch_bounds__(256, 4) k_attend_join(const __grid_constant__ 
     const int r = (u & 7) * 32 + lane, t = r >> 7, tok_in = (r & 127) / p.a.group, tok = t * p.tokens + tok_in, d4 = u >> 3;
     const bool mine = u < kUnits && tok_in < p.tokens && tok < it.tokens;
     float m = -INFINITY, l = 0.f;
+    const float c = mine ? __ldcg(&p.part_c[static_cast<int64_t>(k0) * 256 + r]) : 0.f;  // (of any of them)
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int b = b0; b < b1 && mine; b += kJoinBatch) {
       float2 ml[kJoinBatch];
@@ -1051,13 +1077,13 @@ __global__ void __launch_bounds__(256, 4) k_attend_join(const __grid_constant__ 
       }
 #pragma unroll
       for (int x = 0; x < kJoinBatch; ++x) top = fmaxf(top, ml[x].x);
-      const float f = m == top ? 1.f : exp2_fast(m - top);
+      const float f = m == top ? 1.f : exp2_fast((m - top) * c);
       m = top;
       l *= f;
       o.x *= f, o.y *= f, o.z *= f, o.w *= f;
 #pragma unroll
       for (int x = 0; x < kJoinBatch; ++x) {
-        const float w = ml[x].x == m ? 1.f : exp2_fast(ml[x].x - m);
+        const float w = ml[x].x == m ? 1.f : exp2_fast((ml[x].x - m) * c);
         l += w * ml[x].y;
         o.x += w * v[x].x, o.y += w * v[x].y, o.z += w * v[x].z, o.w += w * v[x].w;
       }
@@ -1070,7 +1096,8 @@ __global__ void __launch_bounds__(256, 4) k_attend_join(const __grid_constant__ 
         for (int x = 1; x < wide; ++x) {
           const float2 other = s_ml[warp + x][lane];
           const float4 v = s_o[warp + x][lane];
-          const float top = fmaxf(m, other.x), f = m == top ? 1.f : exp2_fast(m - top), w = other.x == top ? 1.f : exp2_fast(other.x - top);
+          const float top = fmaxf(m, other.x);
+          const float f = m == top ? 1.f : exp2_fast((m - top) * c), w = other.x == top ? 1.f : exp2_fast((other.x - top) * c);
           m = top;
           l = l * f + other.y * w;
           o = make_float4(o.x * f + v.x * w, o.y * f + v.y * w, o.z * f + v.z * w, o.w * f + v.w * w);
@@ -1082,10 +1109,10 @@ __global__ void __launch_bounds__(256, 4) k_attend_join(const __grid_constant__ 
       const int64_t at = static_cast<int64_t>(it.row0 + tok) * p.a.q_heads + it.head * p.a.group + (r & 127) - tok_in * p.a.group;
       if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
       const float inv = l == 0.f ? 0.f : p.a.c.v_mul / l;
-      const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), c = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
       *reinterpret_cast<uint2*>(p.a.out + at * kDim + d4 * 4) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
-      if (d4 == 0 && p.a.lse != nullptr) p.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      if (d4 == 0 && p.a.lse != nullptr) p.a.lse[at] = l == 0.f ? -INFINITY : fmaf(m, c, log2f(l)) * 0.6931471805599453f;
     }
   }
 }

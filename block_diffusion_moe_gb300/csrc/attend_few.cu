@@ -42,9 +42,11 @@ constexpr int kWarpKeys = 32;  // of a unit: two sixteens
 // alone, as many on an SM: the later ones are served last and end 20 us after the
 // first; 64 sequences of 8,192 keys, 8 heads, took 129 us instead of 123.)
 constexpr int few_warps(int cols) { return cols == 1 ? 16 : 12; }
-// Numerators are 2^(c S - m + 11), m the row's maximum or up to 2^4 below it: at most
-// 2^15, and what fp16 cannot tell from 0 or rounds by more than half a step is
-// 2^-36 of the largest.
+// Numerators are 2^(c (S - m) + 11), m the row's largest S or one that is up to 2^4 less in
+// weight: at most 2^15, and what fp16 cannot tell from 0 or rounds by more than half a step
+// is 2^-36 of the largest. (The difference comes before the factor: it is exact near the
+// maximum however large the scores are. c S - c m is off by the roundings of c m, which
+// from scores of 9e7 on are more than fp16 has room for.)
 constexpr float kGrowth = 4.f, kLift = 11.f;
 
 // kCols: groups of 8 rows.
@@ -65,6 +67,7 @@ struct Shared {
   float sums[kTeam > 1 ? kTeam / 2 : 1][kTeam > 1 ? Layout<kDim, kCols>::kFrag * 32 : 1];
   float2 ml[kWarps][kFewRows];
   float2 row_ml[kFewRows];
+  float row_c[kFewRows];
   int64_t scan[kWarps];
   uint64_t full[kWarps][Layout<kDim, kCols>::kStages];
   int poison, last;
@@ -207,7 +210,7 @@ __device__ __forceinline__ void load_rows(const AttendFewArgs& p, const Cursor& 
   }
 }
 
-// Softmax state of a lane's rows, and its share of their sums: accumulator j holds
+// Softmax state of a lane's rows (m: of S), and its share of their sums: accumulator j holds
 // elements kDim / 8 * g + 2 j (registers 0 and 1) and the next (2 and 3).
 template <int kDim, int kCols>
 struct State {
@@ -283,14 +286,14 @@ __device__ __forceinline__ bool step(const uint8_t* stage, const Rows<kDim, kCol
   }
   // each lane's own keys say whether a row's maximum may have grown; only then is
   // it worked out
-  float top[kCols][2], lift[kCols][2];
+  float top[kCols][2], base[kCols][2];
   bool grown = false;
 #pragma unroll
   for (int c = 0; c < kCols; ++c)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      top[c][i] = fmaxf(fmaxf(s[0][c][i], s[0][c][i + 2]), fmaxf(s[1][c][i], s[1][c][i + 2])) * r.c[c][i];
-      grown |= top[c][i] - st->m[c][i] > kGrowth;
+      top[c][i] = fmaxf(fmaxf(s[0][c][i], s[0][c][i + 2]), fmaxf(s[1][c][i], s[1][c][i + 2]));
+      grown |= (top[c][i] - st->m[c][i]) * r.c[c][i] > kGrowth;
     }
   if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
@@ -300,7 +303,7 @@ __device__ __forceinline__ bool step(const uint8_t* stage, const Rows<kDim, kCol
         float up = fmaxf(top[c][i], st->m[c][i]);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
-        const float f = st->m[c][i] == up ? 1.f : exp2_fast(st->m[c][i] - up);
+        const float f = st->m[c][i] == up ? 1.f : exp2_fast((st->m[c][i] - up) * r.c[c][i]);
         st->m[c][i] = up;
         st->l[c][i] *= f;
 #pragma unroll
@@ -310,7 +313,7 @@ __device__ __forceinline__ bool step(const uint8_t* stage, const Rows<kDim, kCol
 #pragma unroll
   for (int c = 0; c < kCols; ++c)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) lift[c][i] = kLift - (st->m[c][i] == -INFINITY ? 0.f : st->m[c][i]);
+    for (int i = 0; i < 2; ++i) base[c][i] = st->m[c][i] == -INFINITY ? 0.f : st->m[c][i];
   bool poison = false;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
@@ -320,7 +323,7 @@ __device__ __forceinline__ bool step(const uint8_t* stage, const Rows<kDim, kCol
       float e[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        e[i] = exp2_fast(fmaf(s[x][c][i], r.c[c][i & 1], lift[c][i & 1]));
+        e[i] = exp2_fast(fmaf(s[x][c][i] - base[c][i & 1], r.c[c][i & 1], kLift));
         st->l[c][i & 1] += e[i];
       }
       b[c][0] = transposed(half2_bits(e[0], e[1]));
@@ -410,8 +413,8 @@ __device__ __forceinline__ void write_row(const AttendFewArgs& p, int64_t at, in
   *reinterpret_cast<uint2*>(p.a.out + at * dim + d) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
-__device__ __forceinline__ void write_lse(const AttendFewArgs& p, int64_t at, float m, float l) {
-  if (p.a.lse != nullptr) p.a.lse[at] = l == 0.f ? -INFINITY : (m - kLift + log2f(l)) * 0.6931471805599453f;
+__device__ __forceinline__ void write_lse(const AttendFewArgs& p, int64_t at, float m, float l, float c) {
+  if (p.a.lse != nullptr) p.a.lse[at] = l == 0.f ? -INFINITY : fmaf(m, c, log2f(l) - kLift) * 0.6931471805599453f;
 }
 
 // The end of a tile's keys in this CTA, by all its threads: the warps' sums
@@ -421,7 +424,7 @@ __device__ __forceinline__ void write_lse(const AttendFewArgs& p, int64_t at, fl
 // one over 1,021 13.1 -> 13.0.)
 template <int kDim, int kCols, int kWarps>
 __device__ void finish_team(const AttendFewArgs& p, Shared<kDim, kCols, kWarps, kWarps>* sh, const Cursor& c, const Line& line,
-                            int u0, int u1, State<kDim, kCols>* st) {
+                            int u0, int u1, const Rows<kDim, kCols>& rw, State<kDim, kCols>* st) {
   using L = Layout<kDim, kCols>;
   constexpr int kThreads = kWarps * 32, kUnit = kWarps * kWarpKeys;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -443,13 +446,14 @@ __device__ void finish_team(const AttendFewArgs& p, Shared<kDim, kCols, kWarps, 
       float m = -INFINITY, l = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sh->ml[w][row].x);
-      const float f = st->m[h][i] == m ? 1.f : exp2_fast(st->m[h][i] - m);
+      const float f = st->m[h][i] == m ? 1.f : exp2_fast((st->m[h][i] - m) * rw.c[h][i]);
       if (warp == 0 && g == 0) {
         for (int w = 0; w < kWarps; ++w) {
           const float2 v = sh->ml[w][row];
-          l += v.y * (v.x == m ? 1.f : exp2_fast(v.x - m));
+          l += v.y * (v.x == m ? 1.f : exp2_fast((v.x - m) * rw.c[h][i]));
         }
         sh->row_ml[row] = make_float2(m, l);
+        sh->row_c[row] = rw.c[h][i];
       }
 #pragma unroll
       for (int j = 0; j < kDim / 16; ++j) st->o[h][j][i] *= f, st->o[h][j][i + 2] *= f;
@@ -510,7 +514,7 @@ __device__ void finish_team(const AttendFewArgs& p, Shared<kDim, kCols, kWarps, 
     }
     if (whole) {
       write_row(p, row_at(r), kDim, d, o, ml.y == 0.f ? 0.f : p.a.c.v_mul / ml.y);
-      if (d == 0) write_lse(p, row_at(r), ml.x, ml.y);
+      if (d == 0) write_lse(p, row_at(r), ml.x, ml.y, sh->row_c[r]);
     } else {
       *reinterpret_cast<float4*>(p.part + (static_cast<int64_t>(place0) * kFewRows + r) * kDim + d) = o;
       if (d == 0) p.part_ml[place0 * kFewRows + r] = ml;
@@ -528,6 +532,7 @@ __device__ void finish_team(const AttendFewArgs& p, Shared<kDim, kCols, kWarps, 
       for (int i = threadIdx.x; i < n_rows * (kDim / 4); i += kThreads) {
         const int r = i / (kDim / 4), d = i % (kDim / 4) * 4;
         float m = -INFINITY, l = 0.f;
+        const float c = sh->row_c[r];
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         // kBatch parts at a time, so that their loads are in flight together
         constexpr int kBatch = 8;
@@ -543,20 +548,20 @@ __device__ void finish_team(const AttendFewArgs& p, Shared<kDim, kCols, kWarps, 
           }
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);
-          const float f = m == top ? 1.f : exp2_fast(m - top);
+          const float f = m == top ? 1.f : exp2_fast((m - top) * c);
           m = top;
           l *= f;
           o.x *= f, o.y *= f, o.z *= f, o.w *= f;
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
             if (k0 + k > c1) continue;
-            const float w = ml[k].x == m ? 1.f : exp2_fast(ml[k].x - m);
+            const float w = ml[k].x == m ? 1.f : exp2_fast((ml[k].x - m) * c);
             l += w * ml[k].y;
             o.x += w * v[k].x, o.y += w * v[k].y, o.z += w * v[k].z, o.w += w * v[k].w;
           }
         }
         write_row(p, row_at(r), kDim, d, o, l == 0.f ? 0.f : p.a.c.v_mul / l);
-        if (d == 0) write_lse(p, row_at(r), m, l);
+        if (d == 0) write_lse(p, row_at(r), m, l, c);
       }
     }
   }
@@ -567,7 +572,7 @@ __device__ void finish_team(const AttendFewArgs& p, Shared<kDim, kCols, kWarps, 
 // in the workspace a part lies as the lanes hold it.
 template <int kDim, int kCols>
 __device__ void finish_warp(const AttendFewArgs& p, const Cursor& c, const Line& line, int piece, int u0, int u1, bool poison,
-                            State<kDim, kCols>* st) {
+                            const Rows<kDim, kCols>& rw, State<kDim, kCols>* st) {
   constexpr int kFrag = Layout<kDim, kCols>::kFrag;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const SeqSpan& sp = c.sp;
@@ -635,7 +640,8 @@ __device__ void finish_warp(const AttendFewArgs& p, const Cursor& c, const Line&
         for (int i = 0; i < 2; ++i) {
           const float2 ml = __ldcg(&p.part_ml[at * kFewRows + 8 * h + 2 * t + i]);
           const float m = fmaxf(st->m[h][i], ml.x);
-          const float f = st->m[h][i] == m ? 1.f : exp2_fast(st->m[h][i] - m), w = ml.x == m ? 1.f : exp2_fast(ml.x - m);
+          const float f = st->m[h][i] == m ? 1.f : exp2_fast((st->m[h][i] - m) * rw.c[h][i]);
+          const float w = ml.x == m ? 1.f : exp2_fast((ml.x - m) * rw.c[h][i]);
           st->m[h][i] = m;
           st->l[h][i] = st->l[h][i] * f + ml.y * w;
 #pragma unroll
@@ -664,7 +670,7 @@ __device__ void finish_warp(const AttendFewArgs& p, const Cursor& c, const Line&
       uint4* to = reinterpret_cast<uint4*>(p.a.out + at * kDim + g * (kDim / 8));
 #pragma unroll
       for (int j = 0; j < kDim / 64; ++j) to[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-      if (g == 0) write_lse(p, at, st->m[h][i], l);
+      if (g == 0) write_lse(p, at, st->m[h][i], l, rw.c[h][i]);
     }
   __syncwarp();
 }
@@ -804,10 +810,10 @@ __global__ void __launch_bounds__(few_warps(kCols) * 32, 1) k_attend_few(const _
     const bool end = c.u + 1 == u_end;
     if (end || c.unit + 1 == c.units) {
       if constexpr (kTeam == 1) {
-        finish_warp<kDim, kCols>(p, c, line, piece, u0, c.unit + 1, poison, &st);
+        finish_warp<kDim, kCols>(p, c, line, piece, u0, c.unit + 1, poison, rows, &st);
       } else {
         if (poison) *reinterpret_cast<volatile int*>(&sh->poison) = 1;
-        finish_team<kDim, kCols, kWarps>(p, sh, c, line, u0, c.unit + 1, &st);
+        finish_team<kDim, kCols, kWarps>(p, sh, c, line, u0, c.unit + 1, rows, &st);
         if (threadIdx.x == 0) sh->poison = 0;
         __syncthreads();
       }

@@ -80,7 +80,8 @@ struct AttendArgs {
   int n_slots;         // pairs of tiles: n_rows / (2 tokens) + the number of sequences
   int may_cut;         // few items are cut into pieces
   float* part;         // [pieces][2][dim / 4][128][4] sums of pieces (workspace)
-  float2* part_ml;     // [pieces][256] their maxima and sums of weights
+  float2* part_ml;     // [pieces][256] their maxima (of S) and sums of weights
+  float* part_c;       // [pieces][256] exponent of 2 per unit of their scores
   AttendJoin* joins;   // [pieces]
   uint32_t per_magic;  // set by the launch: 2^32 / sixteens of a page, rounded up (0: one)
 };
