@@ -817,7 +817,10 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
     for (int o = 16; o > 0; o >>= 1) whole = min(whole, __shfl_xor_sync(0xffffffffu, whole, o));
     float c = p.a.scale_log2;
     float m = -INFINITY, l = 0.f;  // m: of S
-    float lift = L::kLift, gate = L::kGrowth;  // (gate: rows with a base go through the branch in every step)
+    // A row's maximum moves by what that row sees alone: a warp scales its rows together, by 1
+    // where it does not. (Lanes without a query never ask for it, rows with a base in
+    // every step.)
+    float lift = L::kLift, gate = mine ? L::kGrowth : INFINITY;
     item += steps > 0;
     if (kCached && n > 0) {
       if (!warp_wait(p, sh, &sh->q_full[t], q_count & 1)) return;
@@ -845,13 +848,14 @@ __device__ void softmax_role(const AttendArgs& p, Shared* sh, const Cut& cut, in
       tmem_wait_ld(hi);
       if (masked) mask(hi, 64, left, there);
       top = fmaxf(top, largest(hi));
-      if (__any_sync(0xffffffffu, (top - m) * c > gate)) {
-        const float up = fmaxf(m, top);
+      const bool grown = (top - m) * c > gate;
+      if (__any_sync(0xffffffffu, grown)) {
+        const float up = grown ? fmaxf(m, top) : m;
         const float base = base_of(up, c), lift_to = base != 0.f || up == -INFINITY ? L::kLift : fmaf(-up, c, L::kLift);
         const float f = m == up ? 1.f : m == -INFINITY ? 0.f : exp2_fast(fmaf(base_of(m, c) - base, c, lift_to - lift));
         m = up;
         lift = lift_to;
-        gate = base != 0.f ? -INFINITY : L::kGrowth;
+        if (base != 0.f) gate = -INFINITY;
         l *= f;
         if (__any_sync(0xffffffffu, base != 0.f)) {
           rebase(lo, base);

@@ -284,8 +284,8 @@ __device__ __forceinline__ bool step(const uint8_t* stage, const Rows<kDim, kCol
           if (at >= r.lim[c][i & 1] || !(there >> x & 1u)) s[x][c][i] = -INFINITY;
         }
   }
-  // each lane's own keys say whether a row's maximum may have grown; only then is
-  // it worked out
+  // each lane's own keys say whether a row's maximum may have grown; only then is it worked
+  // out, and moves where it has (what a row gets depends on nothing that other rows see)
   float top[kCols][2], base[kCols][2];
   bool grown = false;
 #pragma unroll
@@ -303,6 +303,7 @@ __device__ __forceinline__ bool step(const uint8_t* stage, const Rows<kDim, kCol
         float up = fmaxf(top[c][i], st->m[c][i]);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
+        if (!((up - st->m[c][i]) * r.c[c][i] > kGrowth)) up = st->m[c][i];
         const float f = st->m[c][i] == up ? 1.f : exp2_fast((st->m[c][i] - up) * r.c[c][i]);
         st->m[c][i] = up;
         st->l[c][i] *= f;

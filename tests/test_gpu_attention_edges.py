@@ -1,4 +1,5 @@
-"""The attention operations at their edges, on the GPU: scores of any size."""
+"""The attention operations at their edges, on the GPU: scores of any size, results that depend on nothing but what a
+row sees."""
 import numpy as np
 import pytest
 import torch
@@ -78,3 +79,106 @@ def test_prompt_scores_of_any_size(new, lens, heads, group, dim):
     for scale in SCALES:
         want = R.prompt_attention(q.double().numpy(), k.double().numpy(), v.double().numpy(), off, koff, 1, scale)
         _near(*C.prompt_attention(q.to(DEV), k.to(DEV), v.to(DEV), _ints(off), _ints(koff), scale=scale, lse=True), want, False)
+
+
+# ------------------------------------------- what a result may not depend on
+#
+# Compared bit for bit: out and lse.
+
+
+def _equal(a, b, rows):
+    for x, y in zip(a, b):
+        assert torch.equal(x[rows].view(torch.uint8), y[rows].view(torch.uint8)), (x[rows] != y[rows]).float().mean()
+
+
+def _cached_and_prompt(c, group):
+    """Two calls of the same queries of one sequence: over its cache, and over 300 keys."""
+    k, v = (torch.from_numpy(c.g.standard_normal((300, c.heads, c.dim))).bfloat16().to(DEV) for _ in range(2))
+    off, ln, table = c.args()
+    cache, koff = c.cache(), _ints([0, 300])
+    return [lambda q: C.kv_attention(q, cache, off, ln, table, lse=True), lambda q: C.prompt_attention(q, k, v, off, koff, lse=True)]
+
+
+@pytest.mark.parametrize("group,new", [(3, 40), (7, 40), (4, 50), (33, 5), (48, 5), (8, 1), (3, 4)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_rows_of_no_sequence_change_nothing(group, new, dim):
+    c = Case([new], [300], 16, 2, dim, seed=group, extra_rows=64)
+    q = c.q(2 * group)
+    for call in _cached_and_prompt(c, group):
+        first = call(q.to(DEV))
+        for f in (0.0, 5.0, 100.0, float("nan")):
+            x = q.clone()
+            x[new:] *= f
+            _equal(first, call(x.to(DEV)), slice(0, new))
+
+
+@pytest.mark.parametrize("group,new", [(3, 40), (6, 40), (7, 40), (33, 5), (48, 5), (3, 4), (7, 2)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_calls_before_change_nothing(group, new, dim):
+    """Groups that leave rows of a tile to what the kernel before had there."""
+    c = Case([new], [300], 16, 2, dim, seed=group)
+    q, other = c.q(2 * group).to(DEV), c.q(128)
+    for call in _cached_and_prompt(c, group):
+        got = []
+        for f in (1e-3, 1.0, 5.0, 100.0):
+            call((other * f).to(DEV))
+            got.append(call(q))
+        for x in got[1:]:
+            _equal(got[0], x, slice(0, new))
+
+
+@pytest.mark.parametrize("new,lens,heads,group,dim", [
+    ([4] * 8, [12000 + i for i in range(8)], 2, 2, 64), ([5] * 8, [11000] * 8, 2, 3, 128),  # a few rows, a team per SM
+    ([4] * 100, [1300 + i for i in range(100)], 2, 2, 64), ([2] * 100, [1300] * 100, 2, 6, 128),  # a piece per warp
+    ([40], [900], 2, 8, 64), ([40], [1900], 1, 8, 128),  # tiles, cut
+    ([40] * 40, [140] * 40, 4, 4, 64), ([40] * 40, [300] * 40, 4, 4, 128),  # whole
+])
+def test_cached_positions_behind_change_nothing(new, lens, heads, group, dim):
+    """The last position's key, which only the last row of a sequence sees."""
+    c = Case(new, lens, 16, heads, dim, seed=dim + len(new), written=False)
+    c.pages[...] = c.g.integers(0, 256, c.pages.shape)
+    for base in (0, 9 * dim):
+        c.pages[..., base + 8 * dim:base + 9 * dim] = c.g.integers(28, 52, c.pages.shape[:3] + (dim,))
+    q = c.q(heads * group).to(DEV)
+    rows = torch.from_numpy(np.setdiff1d(np.arange(c.rows), c.off[1:] - 1)).to(DEV)
+    first = C.kv_attention(q, c.cache(), *c.args(), lse=True)
+    for byte in (0, 60, 70, 0x7F):
+        for s, L in enumerate(lens):
+            r = (L - 1) % 16
+            c.pages[c.table[s, (L - 1) // 16], :, 0, 8 * dim + r * (dim // 16):8 * dim + (r + 1) * (dim // 16)] = byte
+        _equal(first, C.kv_attention(q, c.cache(), *c.args(), lse=True), rows)
+
+
+@pytest.mark.parametrize("new,lens,heads,group,dim", [([200], [200], 2, 4, 128), ([200], [200], 2, 8, 64), ([50], [2000], 1, 8, 64),
+                                                      ([40] * 90, [140] * 90, 2, 8, 64), ([40] * 90, [300] * 90, 2, 8, 128)])
+def test_prompt_positions_behind_change_nothing(new, lens, heads, group, dim):
+    g = torch.Generator().manual_seed(dim)
+    off, koff = (np.concatenate([[0], np.cumsum(x)]).astype(np.int32) for x in (new, lens))
+    q = torch.randn((int(off[-1]), heads * group, dim), generator=g).bfloat16().to(DEV)
+    k, v = (torch.randn((int(koff[-1]), heads, dim), generator=g).bfloat16().to(DEV) for _ in range(2))
+    rows = torch.from_numpy(np.setdiff1d(np.arange(off[-1]), off[1:] - 1)).to(DEV)
+    first = C.prompt_attention(q, k, v, _ints(off), _ints(koff), lse=True)
+    last = torch.from_numpy(koff[1:] - 1).long().to(DEV)
+    keys = k[last].clone()
+    for f in (0.0, 10.0, 100.0, float("nan")):
+        k[last] = keys * f
+        _equal(first, C.prompt_attention(q, k, v, _ints(off), _ints(koff), lse=True), rows)
+
+
+@pytest.mark.parametrize("group,dim", [(3, 64), (5, 128), (7, 64), (8, 128), (33, 64)])
+def test_run_to_run(group, dim):
+    """Every form of both operations, with calls of the others between two of a kind."""
+    shapes = [([1], [1900]), ([1, 2, 1], [3000, 70, 900]), ([1] * 100, list(range(30, 330, 3))), ([40], [1500]), ([40] * 30, [90] * 30)]
+    calls = []
+    for i, (new, lens) in enumerate(shapes):
+        c = Case(new, lens, 16, 4, dim, seed=i, written=False)
+        c.pages[...] = c.g.integers(0, 0x38, c.pages.shape)  # (no NaN among the scales)
+        q, cache, args = c.q(4 * group, 0.3).to(DEV), c.cache(), c.args()
+        k = torch.from_numpy(c.g.standard_normal((sum(lens), 4, dim))).bfloat16().to(DEV)
+        koff = _ints(np.concatenate([[0], np.cumsum(lens)]))
+        calls.append(lambda q=q, cache=cache, args=args: C.kv_attention(q, cache, *args, lse=True))
+        calls.append(lambda q=q, k=k, off=args[0], koff=koff: C.prompt_attention(q, k, k, off, koff, lse=True))
+    first = [f() for f in calls]
+    for i in range(4):
+        for j in np.random.default_rng(i).permutation(len(calls)):
+            _equal(first[j], calls[j](), slice(None))
