@@ -48,6 +48,11 @@ constexpr int few_warps(int cols) { return cols == 1 ? 16 : 12; }
 // maximum however large the scores are. c S - c m is off by the roundings of c m, which
 // from scores of 9e7 on are more than fp16 has room for.)
 constexpr float kGrowth = 4.f, kLift = 11.f;
+// Units of a tile after which its sums go to the workspace, where they are added in fp32, and
+// begin again: the tensor core cuts off what its accumulators do not hold, each time it
+// adds 16 keys, which after so many (32,768 keys of a warp) has taken 2^-14 of a sum of values
+// of one sign, and without an end several % of 2^24.
+constexpr int kFlush = 1024;
 
 // kCols: groups of 8 rows.
 template <int kDim, int kCols>
@@ -68,6 +73,7 @@ struct Shared {
   float2 ml[kWarps][kFewRows];
   float2 row_ml[kFewRows];
   float row_c[kFewRows];
+  float2 row_f[kFewRows];
   int64_t scan[kWarps];
   uint64_t full[kWarps][Layout<kDim, kCols>::kStages];
   int poison, last;
@@ -419,13 +425,13 @@ __device__ __forceinline__ void write_lse(const AttendFewArgs& p, int64_t at, fl
 }
 
 // The end of a tile's keys in this CTA, by all its threads: the warps' sums
-// become one, which is the result or goes to the workspace. units u0 .. u1 - 1 of
-// the tile lie here. (All sums added up in one step, with two barriers instead of a dozen,
+// become one, which is the result or goes to the workspace. Units u0 .. u1 - 1 of
+// the tile lie here, those before v0 in the workspace already; done: it does not go on here. (All sums added up in one step, with two barriers instead of a dozen,
 // spilled registers of the loop: one token over 131,072 keys, 8 heads, 50 -> 56 us,
 // one over 1,021 13.1 -> 13.0.)
 template <int kDim, int kCols, int kWarps>
 __device__ void finish_team(const AttendFewArgs& p, Shared<kDim, kCols, kWarps, kWarps>* sh, const Cursor& c, const Line& line,
-                            int u0, int u1, const Rows<kDim, kCols>& rw, State<kDim, kCols>* st) {
+                            int u0, int v0, int u1, bool done, const Rows<kDim, kCols>& rw, State<kDim, kCols>* st) {
   using L = Layout<kDim, kCols>;
   constexpr int kThreads = kWarps * 32, kUnit = kWarps * kWarpKeys;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -491,13 +497,24 @@ __device__ void finish_team(const AttendFewArgs& p, Shared<kDim, kCols, kWarps, 
   __syncthreads();
   const SeqSpan& sp = c.sp;
   const int n_rows = min(p.tokens, sp.rows - c.tile * p.tokens) * p.a.group;
-  const bool whole = u0 == 0 && u1 == c.units, poison = sh->poison != 0;
+  const bool whole = done && u0 == 0 && u1 == c.units, poison = sh->poison != 0;
   const int64_t first = c.u - c.unit;  // unit 0 of the tile
   const int place0 = place_of(line, blockIdx.x, first);
   auto row_at = [&](int r) {
     const int tok = r / p.a.group;
     return (static_cast<int64_t>(sp.row0) + c.tile * p.tokens + tok) * p.a.q_heads + c.head * p.a.group + (r - tok * p.a.group);
   };
+  if (v0 != u0) {
+    if (threadIdx.x < n_rows) {
+      const int r = threadIdx.x;
+      const float2 a = sh->row_ml[r], b = __ldcg(&p.part_ml[place0 * kFewRows + r]);
+      const float m = fmaxf(a.x, b.x), c = sh->row_c[r];
+      const float f = a.x == m ? 1.f : exp2_fast((a.x - m) * c), w = b.x == m ? 1.f : exp2_fast((b.x - m) * c);
+      sh->row_ml[r] = make_float2(m, a.y * f + b.y * w);
+      sh->row_f[r] = make_float2(f, w);
+    }
+    __syncthreads();
+  }
   for (int i = threadIdx.x; i < n_rows * (kDim / 4); i += kThreads) {
     const int r = i / (kDim / 4), d = i % (kDim / 4) * 4;
     const float* s = rows + r * L::kPitch + d + d / (kDim / 8);
@@ -505,13 +522,18 @@ __device__ void finish_team(const AttendFewArgs& p, Shared<kDim, kCols, kWarps, 
     const float2 ml = sh->row_ml[r];
     if (poison) {
       const int tok = c.tile * p.tokens + r / p.a.group, p0 = sp.len - sp.rows;
-      const int lo = max(seen(p0 + c.tile * p.tokens, sp.len, p.a.block), u0 * kUnit);
+      const int lo = max(seen(p0 + c.tile * p.tokens, sp.len, p.a.block), v0 * kUnit);
       const int hi = min(seen(p0 + tok, sp.len, p.a.block), u1 * kUnit);
       for (int j = lo; j < hi; ++j) {
         const uint8_t* six = kv_sixteen(p.a.c, p.a.s, c.seq, c.head, j);
         if (six != nullptr && (six[L::kVs + j % 16 * (kDim / 16) + d / 16] & 0x7F) == 0x7F)
           o = make_float4(NAN, NAN, NAN, NAN);
       }
+    }
+    if (v0 != u0) {
+      const float2 f = sh->row_f[r];
+      const float4 b = __ldcg(reinterpret_cast<const float4*>(p.part + (static_cast<int64_t>(place0) * kFewRows + r) * kDim + d));
+      o = make_float4(o.x * f.x + b.x * f.y, o.y * f.x + b.y * f.y, o.z * f.x + b.z * f.y, o.w * f.x + b.w * f.y);
     }
     if (whole) {
       write_row(p, row_at(r), kDim, d, o, ml.y == 0.f ? 0.f : p.a.c.v_mul / ml.y);
@@ -521,7 +543,7 @@ __device__ void finish_team(const AttendFewArgs& p, Shared<kDim, kCols, kWarps, 
       if (d == 0) p.part_ml[place0 * kFewRows + r] = ml;
     }
   }
-  if (!whole) {
+  if (done && !whole) {
     const int c0 = line.piece_of(first), c1 = line.piece_of(first + c.units - 1);
     __threadfence();
     __syncthreads();
@@ -572,7 +594,7 @@ __device__ void finish_team(const AttendFewArgs& p, Shared<kDim, kCols, kWarps, 
 // The same for a team of one warp, whose lanes keep their own elements throughout:
 // in the workspace a part lies as the lanes hold it.
 template <int kDim, int kCols>
-__device__ void finish_warp(const AttendFewArgs& p, const Cursor& c, const Line& line, int piece, int u0, int u1, bool poison,
+__device__ void finish_warp(const AttendFewArgs& p, const Cursor& c, const Line& line, int piece, int u0, int v0, int u1, bool done, bool poison,
                             const Rows<kDim, kCols>& rw, State<kDim, kCols>* st) {
   constexpr int kFrag = Layout<kDim, kCols>::kFrag;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -585,7 +607,7 @@ __device__ void finish_warp(const AttendFewArgs& p, const Cursor& c, const Line&
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) st->l[h][i] += __shfl_xor_sync(0xffffffffu, st->l[h][i], o);
   if (__any_sync(0xffffffffu, poison)) {
-    const int p0 = sp.len - sp.rows, at0 = max(seen(p0 + c.tile * p.tokens, sp.len, p.a.block), u0 * kWarpKeys);
+    const int p0 = sp.len - sp.rows, at0 = max(seen(p0 + c.tile * p.tokens, sp.len, p.a.block), v0 * kWarpKeys);
 #pragma unroll
     for (int h = 0; h < kCols; ++h)
 #pragma unroll
@@ -602,10 +624,34 @@ __device__ void finish_warp(const AttendFewArgs& p, const Cursor& c, const Line&
     __syncwarp();
   }
   float (&acc)[kFrag] = *reinterpret_cast<float(*)[kFrag]>(&st->o[0][0][0]);
-  if (u0 != 0 || u1 != c.units) {
-    const int64_t first = c.u - c.unit;
-    const int c0 = line.piece_of(first), c1 = line.piece_of(first + c.units - 1);
-    const int mine = place_of(line, piece, first);
+  auto add_part = [&](int at) {
+    const float* from = p.part + static_cast<int64_t>(at) * (kFrag * 32) + lane;
+    float v[kFrag];
+#pragma unroll
+    for (int i = 0; i < kFrag; ++i) v[i] = __ldcg(from + i * 32);
+#pragma unroll
+    for (int h = 0; h < kCols; ++h)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 ml = __ldcg(&p.part_ml[at * kFewRows + 8 * h + 2 * t + i]);
+        const float m = fmaxf(st->m[h][i], ml.x);
+        const float f = st->m[h][i] == m ? 1.f : exp2_fast((st->m[h][i] - m) * rw.c[h][i]);
+        const float w = ml.x == m ? 1.f : exp2_fast((ml.x - m) * rw.c[h][i]);
+        st->m[h][i] = m;
+        st->l[h][i] = st->l[h][i] * f + ml.y * w;
+#pragma unroll
+        for (int j = 0; j < kDim / 16; ++j)
+#pragma unroll
+          for (int e = i; e < 4; e += 2) st->o[h][j][e] = st->o[h][j][e] * f + v[(h * (kDim / 16) + j) * 4 + e] * w;
+      }
+  };
+  const int64_t first = c.u - c.unit;
+  const int mine = place_of(line, piece, first);
+  int at0 = mine, parts = v0 != u0, skip = 0;  // what is to be added: its own sums before, then those of all pieces
+  for (bool join = false;; join = true) {
+#pragma unroll 1
+    for (int k = 0; k < parts; ++k) add_part(at0 + 2 * k + (k == 0 ? skip : 0));
+    if (join || (done && u0 == 0 && u1 == c.units)) break;
     float* part = p.part + static_cast<int64_t>(mine) * (kFrag * 32) + lane;
 #pragma unroll
     for (int i = 0; i < kFrag; ++i) __stcg(part + i * 32, acc[i]);
@@ -615,42 +661,26 @@ __device__ void finish_warp(const AttendFewArgs& p, const Cursor& c, const Line&
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           __stcg(&p.part_ml[mine * kFewRows + 8 * h + 2 * t + i], make_float2(st->m[h][i], st->l[h][i]));
+    if (!done) {
+      __syncwarp();
+      return;
+    }
+    const int c0 = line.piece_of(first), c1 = line.piece_of(first + c.units - 1);
     __threadfence();
     __syncwarp();
     int last = 0;
     if (lane == 0) last = arrive_last(p, c0, c1);
     if (!__shfl_sync(0xffffffffu, last, 0)) return;
     __threadfence();
-    const int skip = place_of(line, c0, first) - 2 * c0;
+    at0 = 2 * c0;
+    parts = c1 - c0 + 1;
+    skip = place_of(line, c0, first) - at0;
 #pragma unroll
     for (int h = 0; h < kCols; ++h)
 #pragma unroll
       for (int i = 0; i < 2; ++i) st->m[h][i] = -INFINITY, st->l[h][i] = 0.f;
 #pragma unroll
     for (int i = 0; i < kFrag; ++i) acc[i] = 0.f;
-#pragma unroll 1
-    for (int k = c0; k <= c1; ++k) {
-      const int at = 2 * k + (k == c0 ? skip : 0);
-      const float* from = p.part + static_cast<int64_t>(at) * (kFrag * 32) + lane;
-      float v[kFrag];
-#pragma unroll
-      for (int i = 0; i < kFrag; ++i) v[i] = __ldcg(from + i * 32);
-#pragma unroll
-      for (int h = 0; h < kCols; ++h)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float2 ml = __ldcg(&p.part_ml[at * kFewRows + 8 * h + 2 * t + i]);
-          const float m = fmaxf(st->m[h][i], ml.x);
-          const float f = st->m[h][i] == m ? 1.f : exp2_fast((st->m[h][i] - m) * rw.c[h][i]);
-          const float w = ml.x == m ? 1.f : exp2_fast((ml.x - m) * rw.c[h][i]);
-          st->m[h][i] = m;
-          st->l[h][i] = st->l[h][i] * f + ml.y * w;
-#pragma unroll
-          for (int j = 0; j < kDim / 16; ++j)
-#pragma unroll
-            for (int e = i; e < 4; e += 2) st->o[h][j][e] = st->o[h][j][e] * f + v[(h * (kDim / 16) + j) * 4 + e] * w;
-        }
-    }
   }
 #pragma unroll
   for (int h = 0; h < kCols; ++h)
@@ -738,10 +768,11 @@ __global__ void __launch_bounds__(few_warps(kCols) * 32, 1) k_attend_few(const _
   uint32_t there = 0;  // two bits per stage: sixteens that have a page
   int fs = 0, s = 0;
   uint32_t fph = 0, ph = 0;  // parity of each stage's last fetch; of the stages worked on
-  bool dead = false, begin = true, poison = false;
+  bool dead = false, poison = false;
   State<kDim, kCols> st;
   Rows<kDim, kCols> rows;
-  int u0 = 0;
+  // the tile's first unit here (-1: its rows are not loaded), that of the sums so far, and where those end (0: they have not begun)
+  int u0 = -1, v0 = 0, v1 = 0;
   for (int warm = L::kStages;;) {
     if (f.u < u_end && !dead) {
       if (ahead == 16) {
@@ -772,11 +803,14 @@ __global__ void __launch_bounds__(few_warps(kCols) * 32, 1) k_attend_few(const _
       }
     }
     if (warm > 0 && --warm > 0) continue;  // fill the ring first
-    if (begin) {
-      begin = false;
-      u0 = c.unit;
+    if (v1 == 0) {
+      if (u0 < 0) {
+        u0 = c.unit;
+        load_rows<kDim, kCols>(p, c, &rows);
+      }
+      v0 = c.unit;
+      v1 = static_cast<int>(min(static_cast<int64_t>(min(c.units - v0, kFlush)), u_end - c.u)) + v0;
       poison = false;
-      load_rows<kDim, kCols>(p, c, &rows);
 #pragma unroll
       for (int h = 0; h < kCols; ++h) {
 #pragma unroll
@@ -808,19 +842,20 @@ __global__ void __launch_bounds__(few_warps(kCols) * 32, 1) k_attend_few(const _
       s = 0;
       ph ^= 1u;
     }
-    const bool end = c.u + 1 == u_end;
-    if (end || c.unit + 1 == c.units) {
+    if (c.unit + 1 == v1) {
+      const bool end = c.u + 1 == u_end, done = end || v1 == c.units;
       if constexpr (kTeam == 1) {
-        finish_warp<kDim, kCols>(p, c, line, piece, u0, c.unit + 1, poison, rows, &st);
+        finish_warp<kDim, kCols>(p, c, line, piece, u0, v0, v1, done, poison, rows, &st);
       } else {
         if (poison) *reinterpret_cast<volatile int*>(&sh->poison) = 1;
-        finish_team<kDim, kCols, kWarps>(p, sh, c, line, u0, c.unit + 1, rows, &st);
+        finish_team<kDim, kCols, kWarps>(p, sh, c, line, u0, v0, v1, done, rows, &st);
         if (threadIdx.x == 0) sh->poison = 0;
         __syncthreads();
       }
-      begin = true;
+      if (end) break;
+      if (done) u0 = -1;
+      v1 = 0;
     }
-    if (end) break;
     ++c.u;
     if (++c.unit == c.units) place<kTeam>(p, sh->before, &c);
   }

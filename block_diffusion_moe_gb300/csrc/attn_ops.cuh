@@ -79,7 +79,7 @@ struct AttendArgs {
   int tokens;
   int n_slots;         // pairs of tiles: n_rows / (2 tokens) + the number of sequences
   int may_cut;         // few items are cut into pieces
-  float* part;         // [pieces][2][dim / 4][128][4] sums of pieces (workspace)
+  float* part;         // [CTAs][2][dim / 4][128][4] sums of pieces, or flushed (workspace)
   float2* part_ml;     // [pieces][256] their maxima (of S) and sums of weights
   float* part_c;       // [pieces][256] exponent of 2 per unit of their scores
   AttendJoin* joins;   // [pieces]
