@@ -760,28 +760,55 @@ __device__ __forceinline__ float largest(const uint32_t (&s)[2][32]) {
 // What look_after (expand_tile) has taken out of V, added to the sums of the rows that
 // see it: infinities and NaN. By a whole warp, each lane for its row, whose sums
 // begin at o_at. (They stay in tensor memory: an array that a call changes would lie
-// in memory for every item, which took 3 us of each.)
+// in memory for every item, which took 3 us of each.) 32 positions at a time, which the
+// lanes share: large blocks leave as many positions as a block has to be gone through, and
+// the roles that wait meanwhile give up after two seconds.
 template <int kDim, bool kCached>
 __device__ __noinline__ void add_odd_values(const AttendArgs& p, const Cut& cut, int k, int lim, uint32_t o_at) {
+  const int lane = threadIdx.x & 31;
   Item it;
   locate(p, cut, k, &it);
+  const int mine = min(lim, it.j1 * kKeys), begin = max(it.all, it.j0 * kKeys), end = warp_uniform(mine);
 #pragma unroll 1
   for (int i = 0; i < kDim / 32; ++i) {
     uint32_t o[1][32];
     tmem_ld32_async(o_at + i * 32, o[0]);
     tmem_wait_ld(o);
-    for (int j = max(it.all, it.j0 * kKeys); j < min(lim, it.j1 * kKeys); ++j) {
+    for (int j = begin; j < end; j += 32) {
+      const int n = min(32, end - j);
       if (kCached) {
-        const uint8_t* six = kv_sixteen(p.a.c, p.a.s, it.seq, it.head, j);
+        // a lane looks at a position's scales: which positions have a NaN among these 32 elements
+        const uint8_t* six = lane < n ? kv_sixteen(p.a.c, p.a.s, it.seq, it.head, j + lane) : nullptr;
+        uint32_t two = 0;
+        if (six != nullptr) two = *reinterpret_cast<const uint16_t*>(six + 17 * kDim + (j + lane) % 16 * (kDim / 16) + i * 2);
+        const uint32_t see = mine - j >= 32 ? 0xffffffffu : (1u << max(mine - j, 0)) - 1u;
 #pragma unroll
-        for (int x = 0; x < 32; ++x)
-          if (six != nullptr && (six[17 * kDim + j % 16 * (kDim / 16) + (i * 32 + x) / 16] & 0x7F) == 0x7F) o[0][x] = 0x7FC00000u;
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t odd = __ballot_sync(0xffffffffu, (two >> (8 * h) & 0x7F) == 0x7F) & see;
+#pragma unroll
+          for (int x = 0; x < 16; ++x)
+            if (odd != 0) o[0][16 * h + x] = 0x7FC00000u;
+        }
       } else {
-        const uint16_t* v = reinterpret_cast<const uint16_t*>(p.a.v.data + (it.sp.key0 + j) * p.a.v.row + it.head * p.a.v.head);
+        // a lane adds up an element's of all these positions, or of those that its row sees
+        const uint16_t* v = reinterpret_cast<const uint16_t*>(p.a.v.data + (it.sp.key0 + j) * p.a.v.row + it.head * p.a.v.head) + i * 32;
+        auto odd = [&](int y, int x) {
+          const uint32_t b = *reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(v + x) + y * p.a.v.row);
+          return (b & 0x7F80u) == 0x7F80u ? __uint_as_float(b << 16) : 0.f;
+        };
+        float sum = 0.f;
+#pragma unroll 8
+        for (int y = 0; y < n; ++y) sum += odd(y, lane);
+        if (!__any_sync(0xffffffffu, sum != 0.f)) continue;
+        const bool some = mine > j && mine < j + n, all = mine >= j + n;
 #pragma unroll
         for (int x = 0; x < 32; ++x) {
-          const uint32_t b = v[i * 32 + x];
-          if ((b & 0x7F80u) == 0x7F80u) o[0][x] = __float_as_uint(__uint_as_float(o[0][x]) + __uint_as_float(b << 16));
+          float add = __shfl_sync(0xffffffffu, sum, x);
+          if (some) {
+            add = 0.f;
+            for (int y = 0; y < mine - j; ++y) add += odd(y, x);
+          }
+          if (all || some) o[0][x] = __float_as_uint(__uint_as_float(o[0][x]) + add);
         }
       }
     }

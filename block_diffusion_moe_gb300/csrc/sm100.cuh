@@ -417,7 +417,7 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// x, which is the same in every lane, in a uniform register: what loops and
+// x, which is the same in every lane (else the largest), in a uniform register: what loops and
 // addresses that depend on it need to be uniform themselves.
 __device__ __forceinline__ int warp_uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
 

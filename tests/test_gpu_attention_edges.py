@@ -182,3 +182,51 @@ def test_run_to_run(group, dim):
     for i in range(4):
         for j in np.random.default_rng(i).permutation(len(calls)):
             _equal(first[j], calls[j](), slice(None))
+
+
+# ---------------------------------- values that are not numbers, in large blocks
+
+
+@pytest.mark.parametrize("block", [700, 333])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prompt_odd_values_of_a_later_block(block, dim):
+    """Tiles whose rows are of two blocks: the first rows must not get what the others see. Infinities of both signs and NaN,
+    more than 32 positions apart and next to one another, at the ends of what is seen."""
+    c = Case([1100], [1100], 16, 2, dim, seed=block, written=False)
+    q = c.q(8)
+    k, v = (torch.from_numpy(c.g.standard_normal((1100, 2, dim))).bfloat16() for _ in range(2))
+    for p, d, x in ((block, 0, np.inf), (block + 40, 1, -np.inf), (block + 41, 1, -np.inf), (2 * block - 1, 33, np.nan),
+                    (1099, dim - 1, np.inf), (1098, dim - 1, -np.inf), (block - 1, 20, np.inf)):
+        if p < 1100:
+            v[p, 1, d] = x
+    off = _ints([0, 1100])
+    out, lse = C.prompt_attention(q.to(DEV), k.to(DEV), v.to(DEV), off, block=block, lse=True)
+    want = R.prompt_attention(q.double().numpy(), k.double().numpy(), v.double().numpy(), np.array([0, 1100]), np.array([0, 1100]),
+                              block, dim ** -0.5)
+    o, g = want[0], out.double().cpu().numpy()
+    assert not np.isfinite(o).all()
+    for same in (np.isnan, lambda x: x == np.inf, lambda x: x == -np.inf):
+        assert np.array_equal(same(g), same(o))
+    fine = np.isfinite(o)
+    # the shorter tests' bound (scores below 64 here: d = 2^-13)
+    assert (np.abs(g - o)[fine] <= (2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2.0 ** -13 + 2.0 ** -11) * want[2])[fine]).all()
+
+
+@pytest.mark.parametrize("block", [700, 333])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_cached_odd_values_of_a_later_block(block, dim):
+    c = Case([1100], [1100], 16, 2, dim, seed=block + 1, written=False)
+    c.pages[...] = c.g.integers(0, 256, c.pages.shape)
+    for base in (0, 9 * dim):
+        c.pages[..., base + 8 * dim:base + 9 * dim] = c.g.integers(28, 52, c.pages.shape[:3] + (dim,))
+    for p, d in ((block, 0), (block + 40, 1), (block + 41, 1), (2 * block - 1, 2), (1099, dim // 16 - 1), (block - 1, 3)):
+        if p < 1100:
+            c.pages[c.table[0, p // 16], 1, 0, 17 * dim + p % 16 * (dim // 16) + d] = 0x7F
+    q = c.q(8)
+    out, lse = C.kv_attention(q.to(DEV), c.cache(), *c.args(), block=block, lse=True)
+    want = R.kv_attention(q.double().numpy(), c.pages, c.off, c.lens, c.table, block, dim ** -0.5)
+    o, g = want[0], out.double().cpu().numpy()
+    fine = ~np.isnan(o)
+    assert not fine.all() and np.array_equal(np.isnan(g), ~fine)
+    # (scores below 64: d = 2^-13)
+    assert (np.abs(g - o)[fine] <= (2.0 ** -8 * np.abs(o) + (2.0 ** -12 + 2.0 ** -13 + 2.0 ** -11) * want[2] + 2.0 ** -36 * want[4])[fine]).all()
