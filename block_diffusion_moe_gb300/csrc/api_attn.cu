@@ -35,7 +35,7 @@ int launched(cudaError_t e, const char* where) {
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 constexpr int kMaxRows = 1 << 24;  // rows, key rows and positions of a call
-constexpr int kMaxSeqs = 1024;
+constexpr int kMaxSeqs = plan::kMaxSeqs;
 constexpr int kMaxKvHeads = 256;
 constexpr int kMaxGroup = 64;
 constexpr size_t kCtrlBytes = 256;  // the status word that clover_workspace_status reads

@@ -867,8 +867,12 @@ __global__ void __launch_bounds__(few_warps(kCols) * 32, 1) k_attend_few(const _
 template <int kDim, int kCols, int kTeam>
 static cudaError_t launch(const AttendFewArgs& a, int sms, cudaStream_t s) {
   void (*k)(const AttendFewArgs) = k_attend_few<kDim, kCols, kTeam>;
-  const size_t smem = sizeof(Shared<kDim, kCols, few_warps(kCols), kTeam>) + static_cast<size_t>(a.a.s.n) * 8;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // (the most a call can ask for, in every call: the attribute is the device's, and other host
+  // threads may be between theirs and their launch)
+  constexpr size_t kBytes = sizeof(Shared<kDim, kCols, few_warps(kCols), kTeam>), kMost = kBytes + 8 * plan::kMaxSeqs;
+  static_assert(kMost <= 227 * 1024, "shared memory of a CTA");
+  const size_t smem = kBytes + 8 * static_cast<size_t>(a.a.s.n);
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMost));
   if (e != cudaSuccess) return e;
   return launch_kernel(k, dim3(sms), dim3(few_warps(kCols) * 32), smem, s, true, a);
 }

@@ -87,6 +87,9 @@ inline RouteShape route_shape(int tokens) {
   return s;
 }
 
+// Sequences of an attention call, at most.
+constexpr int kMaxSeqs = 1024;
+
 // Attention over a cache: CTAs of the kernel for few rows, and whether it takes a
 // call: sequences of at most 32 rows (tokens x heads of a group) on average. (Groups
 // of 8, 4 heads; this kernel or the one on tiles with 16, 32 and 64 rows. Heads of 128:
