@@ -135,6 +135,7 @@ EXPORTS = {
                                           ctypes.c_float, _ptr_t, _i32, _ptr_t, _ptr_t, _size, _ptr_t]),
     "clover_moe_combine": (ctypes.c_int, [_ptr_t, _i32, _ptr_t, _ptr_t, _ptr_t, _ptr_t, _ptr_t, _i32, _i32, _i32,
                                           _ptr_t]),
+    "clover_attention_shared_status": (ctypes.c_int, [ctypes.POINTER(_ptr_t)]),
     "clover_kv_page_bytes": (_size, [_i32, _i32, _i32]),
     "clover_kv_write": (ctypes.c_int, [ctypes.POINTER(KvCacheArgs), ctypes.POINTER(KvSeqs), ctypes.POINTER(Rows),
                                        ctypes.POINTER(Rows), _i32, _i32, _ptr_t]),
@@ -896,13 +897,27 @@ def _attention_out(out, lse, shape, dev: int, device):
     return out, p_out, lse, _tensor("lse", lse, _F32, shape[:2], dev)
 
 
+def _attention_status():
+    """(pointer, bytes) of the library's status block for attention on the current device."""
+    p = ctypes.c_void_p()
+    _check(lib().clover_attention_shared_status(ctypes.byref(p)))
+    return p.value, 256
+
+
+def attention_status(stream=None):
+    """Synchronises the stream, then raises CloverError if a wait ran out in a `kv_attention` or `prompt_attention` on the
+    current device since the last look (rows of its result are then missing), whether it was given a ws or not."""
+    _check(lib().clover_workspace_status(*_attention_status(), _stream(stream)))
+
+
 def kv_attention(q, cache: KvCache, offsets, lens, table, block: int = 1, scale: float | None = None, lse=False, ws=None,
                  out=None, stream=None):
     """Attention of queries (bf16 [rows][q_heads][head_dim], rows and heads may be strided) over the cache: bf16
     [rows][q_heads][head_dim]. offsets, lens and table as for `kv_write`, which writes the rows' own keys and values first.
     The query at position p of a sequence sees positions below (p // block + 1) * block (1: causal; 0: all of them). scale:
     of the scores, head_dim ** -0.5 by default. With lse (True, or fp32 [rows][q_heads] to fill) the result is a pair with
-    the logarithms of the softmax's sums; a query that sees nothing has 0 and -inf."""
+    the logarithms of the softmax's sums; a query that sees nothing has 0 and -inf. ws (kv_attention_workspace_bytes(...))
+    holds the status that workspace_status reads; attention_status reads that of all calls, those without one among them."""
     if stream is not None:
         with _as_current(stream, cache):
             return kv_attention(q, cache, offsets, lens, table, block, scale, lse, ws, out)
@@ -932,7 +947,8 @@ def prompt_attention(q, k, v, offsets, k_offsets=None, block: int = 1, scale: fl
     """Attention over packed prompts: q bf16 [rows][q_heads][head_dim], k and v bf16 [keys][kv_heads][head_dim] (rows and
     heads may be strided) -> bf16 [rows][q_heads][head_dim]. Rows offsets[s] .. offsets[s + 1] - 1 (int32 [sequences + 1])
     are the last positions of sequence s, whose keys are rows k_offsets[s] .. k_offsets[s + 1] - 1 of k and v (by default
-    the same rows: every position has a query). block, scale and lse as for `kv_attention`."""
+    the same rows: every position has a query). block, scale, lse, ws (prompt_attention_workspace_bytes(...)) and status as
+    for `kv_attention`."""
     if stream is not None:
         with _as_current(stream, q):
             return prompt_attention(q, k, v, offsets, k_offsets, block, scale, lse, ws, out)

@@ -152,6 +152,15 @@ float exponent_scale(float scale, float k_mul) {
   return c > FLT_MAX ? FLT_MAX : (c < FLT_TRUE_MIN ? FLT_TRUE_MIN : static_cast<float>(c));
 }
 
+// The status words that a call's kernels set.
+int fill_status(AttnArgs* a, void* workspace) {
+  void* shared = nullptr;
+  const int rc = launched(attention_shared_status(&shared), "looking up the attention status");
+  a->err = static_cast<int*>(workspace);
+  a->shared_err = static_cast<int*>(shared);
+  return rc;
+}
+
 // A workspace: the control block, arrival counters that are zero between calls, and
 // behind them what needs no value before a call. The counters have this place in a
 // workspace of either kernel, whichever was the last to use it.
@@ -210,6 +219,11 @@ size_t prompt_bytes(int32_t head_dim) { return tile_bytes(head_dim); }
 }  // namespace
 
 extern "C" {
+
+int clover_attention_shared_status(void** status) {
+  if (status == nullptr) return fail(CLOVER_ERR_INVALID_ARG, "status is NULL");
+  return launched(attention_shared_status(status), "looking up the attention status");
+}
 
 size_t clover_kv_page_bytes(int32_t page_tokens, int32_t kv_heads, int32_t head_dim) {
   if (check_page(page_tokens) || check_heads(kv_heads, head_dim)) return 0;
@@ -282,7 +296,7 @@ int clover_kv_attention(const clover_kv_cache* cache, const clover_kv_seqs* seqs
   a.scale_log2 = exponent_scale(scale, a.c.k_mul);
   a.out = reinterpret_cast<__nv_bfloat16*>(out);
   a.lse = lse;
-  a.err = static_cast<int*>(workspace);
+  if ((rc = fill_status(&a, workspace))) return rc;
   if (plan::attend_few(n_rows, a.group, seqs->n_seqs)) {
     int sms = 0;
     if ((rc = device_sms(&sms))) return rc;
@@ -350,7 +364,7 @@ int clover_prompt_attention(const clover_prompt_seqs* seqs, const clover_rows* q
   a.scale_log2 = exponent_scale(scale, 1.f);
   a.out = reinterpret_cast<__nv_bfloat16*>(out);
   a.lse = lse;
-  a.err = static_cast<int*>(workspace);
+  if ((rc = fill_status(&a, workspace))) return rc;
   AttendArgs t;
   memset(&t, 0, sizeof(t));
   t.a = a;

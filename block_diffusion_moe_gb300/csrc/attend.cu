@@ -38,7 +38,6 @@
 
 #include "attn_ops.cuh"
 #include "launch.cuh"
-#include "sm100.cuh"
 
 namespace clover {
 
@@ -269,7 +268,7 @@ struct Work {
 __device__ __forceinline__ bool warp_wait(const AttendArgs& p, Shared* sh, uint64_t* bar, uint32_t parity) {
   if (__all_sync(0xffffffffu, mbar_wait(bar, parity, &sh->abort))) return true;
   if (elect_one()) {
-    atomicOr(p.a.err, kErrMbarTimeout);
+    record_timeout(p.a);
     *reinterpret_cast<volatile uint32_t*>(&sh->abort) = 1u;
   }
   __syncwarp();
@@ -1232,6 +1231,11 @@ __global__ void __launch_bounds__(256, 4) k_attend_join(const __grid_constant__ 
     }
   }
 }
+
+// Looked up on every call: the address belongs to the current context.
+static __device__ __align__(256) uint32_t g_attention_status[64];
+
+cudaError_t attention_shared_status(void** p) { return cudaGetSymbolAddress(p, g_attention_status); }
 
 template <int kDim, bool kCached>
 static cudaError_t launch(const AttendArgs& a, int grid, cudaStream_t s) {

@@ -31,7 +31,6 @@
 
 #include "attn_ops.cuh"
 #include "launch.cuh"
-#include "sm100.cuh"
 
 namespace clover {
 
@@ -826,7 +825,7 @@ __global__ void __launch_bounds__(few_warps(kCols) * 32, 1) k_attend_few(const _
     if (!dead && !__all_sync(0xffffffffu, mbar_wait(&sh->full[warp][s], ph, &sh->abort))) {
       dead = true;
       if (lane == 0) {
-        atomicOr(p.a.err, kErrMbarTimeout);
+        record_timeout(p.a);
         *reinterpret_cast<volatile uint32_t*>(&sh->abort) = 1u;
       }
     }

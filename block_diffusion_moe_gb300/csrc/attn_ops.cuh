@@ -10,6 +10,7 @@
 
 #include "fp4.cuh"
 #include "plan.h"
+#include "sm100.cuh"
 
 namespace clover {
 
@@ -59,7 +60,8 @@ struct AttnArgs {
   __nv_bfloat16* out;
   float* lse;  // or null
   int wide_out;  // set by the launch: 32-byte stores to out are aligned
-  int* err;
+  int* err;         // status words of the workspace
+  int* shared_err;  // and of the library
 };
 
 // A piece of a cut item: which of how many (at most one: nothing to join), and the
@@ -88,6 +90,9 @@ struct AttendArgs {
 
 cudaError_t launch_attend(const AttendArgs& a, bool cached, int sms, cudaStream_t s);
 
+// The library's own status block on the current device.
+cudaError_t attention_shared_status(void** p);
+
 // Attention of few query rows over a cache (csrc/attend_few.cu): tiles of at most
 // 8 or 16 rows, the group's query heads of `tokens` tokens.
 constexpr int kFewRows = 16;
@@ -105,6 +110,12 @@ struct AttendFewArgs {
 cudaError_t launch_attend_few(const AttendFewArgs& a, int sms, bool alone, cudaStream_t s);
 
 // ------------------------------------------------------------ device helpers
+
+// A wait ran out.
+__device__ __forceinline__ void record_timeout(const AttnArgs& a) {
+  atomicOr(a.err, kErrMbarTimeout);
+  atomicOr(a.shared_err, kErrMbarTimeout);
+}
 
 // One sequence of a call: its rows, and how many positions it has.
 struct SeqSpan {

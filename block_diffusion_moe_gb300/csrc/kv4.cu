@@ -2,7 +2,6 @@
 // back (clover_kv_write, clover_kv_read).
 #include "attn_ops.cuh"
 #include "launch.cuh"
-#include "sm100.cuh"
 
 namespace clover {
 

@@ -562,6 +562,13 @@ int clover_kv_attention(const clover_kv_cache* cache, const clover_kv_seqs* seqs
                         int32_t q_heads, float scale, int32_t block, uint16_t* out, float* lse, void* workspace,
                         size_t workspace_bytes, clover_stream_t stream);
 
+/* *status receives the device address, on the current device, of 256 bytes in
+ * the library, zeroed when it is loaded, in which calls of both attention
+ * operations record a wait that ran out beside their workspace's status word.
+ * For callers whose workspaces do not outlive the call: clover_workspace_status
+ * (with 256 bytes) reads and clears it. Enqueues nothing. */
+int clover_attention_shared_status(void** status);
+
 /* Packed prompts: query rows by offsets, keys and values by k_offsets (int32
  * [n_seqs + 1]; a sequence's len is its number of keys; the same array as
  * offsets where every position has a query). */

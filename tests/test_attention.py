@@ -256,3 +256,7 @@ def test_oracle_visibility(block):
 def test_struct_sizes():
     assert ctypes.sizeof(C.KvCacheArgs) == 32 and ctypes.sizeof(C.KvSeqs) == 32
     assert ctypes.sizeof(C.PromptSeqs) == 24 and ctypes.sizeof(C.Rows) == 24
+
+
+def test_shared_status_arguments(lib):
+    assert lib.clover_attention_shared_status(None) == C.ERR_INVALID_ARG

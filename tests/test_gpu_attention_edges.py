@@ -209,7 +209,7 @@ def test_prompt_odd_values_of_a_later_block(block, dim):
         assert np.array_equal(same(g), same(o))
     fine = np.isfinite(o)
     # the shorter tests' bound (scores below 64 here: d = 2^-13)
-    assert (np.abs(g - o)[fine] <= (2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2.0 ** -13 + 2.0 ** -11) * want[2])[fine]).all()
+    assert (np.abs(g[fine] - o[fine]) <= 2.0 ** -8 * np.abs(o[fine]) + (2.0 ** -8 + 2.0 ** -13 + 2.0 ** -11) * want[2][fine]).all()
 
 
 @pytest.mark.parametrize("block", [700, 333])
@@ -230,3 +230,38 @@ def test_cached_odd_values_of_a_later_block(block, dim):
     assert not fine.all() and np.array_equal(np.isnan(g), ~fine)
     # (scores below 64: d = 2^-13)
     assert (np.abs(g - o)[fine] <= (2.0 ** -8 * np.abs(o) + (2.0 ** -12 + 2.0 ** -13 + 2.0 ** -11) * want[2] + 2.0 ** -36 * want[4])[fine]).all()
+
+
+# ------------------------------------------------------------------- status
+
+
+class _Words:
+    def __init__(self, p):
+        self.__cuda_array_interface__ = dict(shape=(64,), typestr="<i4", data=(p, False), version=2)
+
+
+def test_status_without_a_workspace():
+    """A set status word is reported once and cleared, whichever calls come between."""
+    c = Case([1, 40], [70, 90], 16, 2, 64, seed=71)
+    q, cache, args = c.q(8).to(DEV), c.cache(), c.args()
+    k = torch.zeros((41, 2, 64), dtype=torch.bfloat16, device=DEV)
+    p, n = C._attention_status()
+    assert n == 256 and p % 256 == 0 and C._attention_status() == (p, n)
+    want = C.kv_attention(q, cache, *args)
+    C.prompt_attention(q, k, k, args[0])
+    C.attention_status()
+    word = torch.as_tensor(_Words(p), device=DEV)
+    assert word.tolist() == [0] * 64
+    word[0] = 1  # what a wait that ran out records
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert torch.equal(C.kv_attention(q, cache, *args), want)
+    ws = C.workspace(C.kv_attention_workspace_bytes(cache, c.rows, 8, *args[2].shape))
+    C.kv_attention(q, cache, *args, ws=ws)
+    C.workspace_status(ws)
+    C.prompt_attention(q, k, k, args[0], stream=side)
+    with pytest.raises(C.CloverError) as e:
+        C.attention_status(stream=side)
+    assert e.value.code == C.ERR_DEVICE_TIMEOUT
+    C.attention_status()
+    assert word.tolist() == [0] * 64
