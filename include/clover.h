@@ -471,8 +471,10 @@ int clover_moe_combine(const uint16_t* y, int32_t n_rows, const int32_t* pos, co
  * [n_seqs + 1] on the device, ascending from 0) belong to sequence s, whose
  * length is len: they are its LAST positions, row offsets[s] + i position
  * p = len - n + i of n rows. Offsets outside [0, rows] count as the nearer end.
- * Rows from offsets[n_seqs] on belong to no sequence: nothing of them is read
- * or written.
+ * Rows from offsets[n_seqs] on belong to no sequence: nothing of theirs is
+ * written, and what they hold changes no result. (It may be read, so all rows
+ * of q, k and v must be memory that a kernel can read, as must rows at negative
+ * positions and keys past k_offsets[n_seqs].)
  *
  * Visibility. The query at position p sees positions below
  *   block 0:      len                    (all of them)
