@@ -8,7 +8,8 @@
 //   O = O + P V        tcgen05.mma, P (16 bits) from tensor memory
 // and in the end O / l. m moves only where the row's maximum has grown by more
 // than a limit (O and l are scaled then): numerators and sums are floating point,
-// so a P above 1 costs no precision.
+// and a P above 1 is rounded like any other. (Were m always the maximum itself, the largest P
+// would be 1 and lose nothing, for a rescaling in most steps.)
 //
 // Roles: warps 0-3 and 4-7 the softmax of tile 0 and 1, warp 8 loads, warp 9
 // issues the MMAs, warp 10 watches the ring for it. While one tile's softmax runs,
@@ -25,13 +26,13 @@
 // an item's keys are cut into pieces, whose sums a second kernel joins.
 //
 // Measured on a GB300 (kernels alone, in a graph): one prompt of 16,384 tokens, causal,
-// 16 heads of 128: 671 to 703 us, 1.6 PFLOP/s; 2 x 1,000 rows over 13,000 keys: 151 us, 1.36
-// PFLOP/s; 4 prompts of up to 6,000 tokens in blocks of 32, 32 heads of 64: 148 us, 0.81
+// 16 heads of 128: 669 to 700 us, 1.6 PFLOP/s; 2 x 1,000 rows over 13,000 keys: 150 us, 1.37
+// PFLOP/s; 4 prompts of up to 6,000 tokens in blocks of 32, 32 heads of 64: 152 us, 0.79
 // PFLOP/s. With 128 elements a tile's chain of scores, softmax and products bounds it:
-// the tensor pipe is 70 to 80% busy. With 64 there are half the products to the same
-// exponentials, and the softmax's chain is what is left (tensor pipe 33%,
-// exponentials 33%, no instruction unit above a third). 32 rows of 16 heads over 131,072
-// cached: 48 us, 14 steps of 1.7 us on each SM (the warps that expand share the issue
+// the tensor pipe is busy 69% of the second of these. With 64 there are half the products
+// to the same exponentials, and the softmax's chain is what is left (tensor pipe 36%,
+// exponentials 36%, issue slots 44%). 32 rows of 16 heads over 131,072
+// cached: 50 us, 14 steps of 1.7 us on each SM (the warps that expand share the issue
 // slots with the softmax; a prompt's step takes 1.4), 9 us before the first and 9 for
 // writing and joining the pieces' sums, 20 MB.
 #include <math.h>
@@ -70,7 +71,7 @@ struct Layout {
 // would be as large as the room above the lift in fp16 (from scores of 9e7 on; in fp32
 // from 2e9 on): then base is m, and the difference, exact near the maximum, comes before
 // the factor. (4 prompts in blocks of 32, heads of 64: 148 us without, 150 so, 153 to 162 with
-// the difference for every row.)
+// the difference for every row; what was added since makes them 152.)
 constexpr float kFar = 1048576.f;
 __device__ __forceinline__ float base_of(float m, float c) { return m == -INFINITY || fabsf(m * c) <= kFar ? 0.f : m; }
 

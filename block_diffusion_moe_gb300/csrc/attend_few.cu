@@ -22,10 +22,11 @@
 // tiles.
 //
 // Measured on a GB300 (the kernel alone, in a graph): 64 sequences of 8,192 keys, 32
-// heads over 8 of 128: 123 us, 4.9 TB/s of 6.7; of up to 16,384: 125 us. What bounds it
-// is the issue of instructions, 324 to a warp for 16 tokens, of which expansion takes
-// about half (issue slots 60% busy, ALU 51%, tensor pipe 23%). One token over 1,021 keys
-// of 2 heads: 13 us: 2 to place the work, 2 for the queries and the first keys, 1.5 for
+// heads over 8 of 128: 122 us, 4.9 TB/s of 6.7; of up to 16,384: 123 us. No unit is
+// saturated (issue slots 61% busy, ALU 51%, tensor pipe 23%; 315 instructions to a warp for
+// 16 tokens, of which expansion takes about half), and warps do not end together: at 107 us
+// on average, the last of an SM at 113 and the last of all at 125, when the whole took that.
+// One token over 1,021 keys of 2 heads: 13.4 us: 2 to place the work, 2 for the queries and the first keys, 1.5 for
 // the step, 6 for the sums of 16 warps and 4 pieces, most of it code that runs once.
 #include <math.h>
 

@@ -93,9 +93,10 @@ constexpr int kMaxSeqs = 1024;
 // Attention over a cache: CTAs of the kernel for few rows, and whether it takes a
 // call: sequences of at most 32 rows (tokens x heads of a group) on average. (Groups
 // of 8, 4 heads; this kernel or the one on tiles with 16, 32 and 64 rows. Heads of 128:
-// 64 sequences of 16,384 keys 195 or 428 us, 342 or 428, 645 or 610; 8 of them 51 or 72,
-// 75 or 73, 121 or 74; 8 of 1,024 keys 17 or 23, 32 or 24, 33 or 24. Heads of 64: 8 of
-// 16,384 keys 33 or 57, 46 or 57, 71 or 57.)
+// 64 sequences of 16,384 keys 187 or 470 us, 326 or 468, 611 or 644; 8 of them 50 or 75,
+// 77 or 75, 128 or 76; 8 of 1,024 keys 18 or 26, 33 or 26, 35 or 27. Heads of 64: 8 of
+// 16,384 keys 31 or 58, 43 or 59, 68 or 60. So at 32 rows the rule is right for many
+// sequences or heads of 64, and up to 27% off for few of 128: their number is not in it.)
 constexpr int kAttendSms = 152;
 inline bool attend_few(long long rows, int group, int seqs) { return group <= 16 && rows * group <= 32LL * seqs; }
 // Rows of its tiles, at most: 8 where the group has no more heads and the call
